@@ -461,6 +461,146 @@ pgd_status pgd_append_decode_attention_fp8(void *out, const void *q, const void 
                                            void *workspace, size_t workspace_bytes, void *stream);
 
 /* ---------------------------------------------------------------------- */
+/* block-scaled 8-bit KV cache: FP8 E4M3 codes, one fp32 scale per         */
+/* (block of tokens, head)                                                 */
+/* ---------------------------------------------------------------------- */
+/* A second 8-bit cache beside the per-token one above ("Module 10", section
+ * "Quantize the cache, evaluate the final artifact"; "The math of Transformer
+ * inference", section 11): 1.004 bytes per value instead of 1.03, written for
+ * any number of tokens at a time, read back as bf16, and attended without
+ * dequantising: its codes go to the tensor cores as they lie.
+ *
+ * Layout: k_cache, v_cache uint8 [NB][n_kv][bs/8][8][8][16] -- a tile's codes
+ * as 8 x 16 core matrices, code of slot s, dim i at (s/8)*1024 + (i/16)*128 +
+ * (s%8)*16 + i%16; k_scales, v_scales fp32 [NB][n_kv], positive.  The value is
+ * E4M3(code) * scale.  Pools 16-byte aligned, scales 4-byte aligned.
+ *
+ * pgd_kv_append_fp8b writes new tokens: sequence b's are rows token_starts[b]
+ * .. token_starts[b + 1] - 1 of k_new and v_new (bf16 [N][n_kv][d]; device
+ * int32 [B + 1], non-decreasing, within [0, N], at most T apart), written at
+ * positions[b] on; a sequence may have none.  token_starts NULL: T tokens
+ * each, N = B * T, so that [B][n_kv][d] with T = 1 is a decode step.  For each
+ * block and head, with m = the largest finite |x| of the rows written into it:
+ *     need  = 2^e, e the smallest integer >= -100 with m <= 448 * 2^e
+ *     scale = need, or the larger of need and the block's scale where slots
+ *             before the first new one hold tokens (the first new slot is not
+ *             slot 0); those slots' codes become E4M3(value(code) * old/scale)
+ *     code  = E4M3(x / scale), rounding to nearest even, saturating to +-448;
+ *             a NaN is stored as NaN
+ * The slots behind the last new token keep their codes and hold no token.  A
+ * block of several sequences must not be appended to (copy on write first).
+ * A range outside [0, MB*bs) or starts that break the rules above set
+ * PGD_DEVERR_BAD_POSITION and write nothing for that sequence; a bad block id
+ * skips its block.
+ *
+ * pgd_kv_read_fp8b is the way back: rows token_starts[b] .. of k_out and v_out
+ * (bf16 [N][n_kv][d]) become the values at positions[b] on, rounded to bf16
+ * (exact for the scales the writer makes).  Same arguments, rules and errors;
+ * rows that belong to no sequence are left as they were.
+ *
+ * pgd_paged_decode_attention_fp8b, pgd_append_decode_attention_fp8b: the calls
+ * of those names over this cache -- same definition on the dequantised K and
+ * V, same arguments (and the scales), checks, errors and workspace
+ * (pgd_attention_workspace_size).  The append is pgd_kv_append_fp8b of one
+ * token at context_lens[b] - 1.  The query must be finite. */
+pgd_status pgd_kv_append_fp8b(const void *k_new, const void *v_new, void *k_cache, void *v_cache,
+                              float *k_scales, float *v_scales, const int32_t *block_tables,
+                              const int32_t *positions, const int32_t *token_starts, int32_t B,
+                              int32_t T, int32_t N, int32_t n_kv, int32_t d, int32_t bs,
+                              int32_t MB, int32_t NB, void *stream);
+pgd_status pgd_kv_read_fp8b(void *k_out, void *v_out, const void *k_cache, const void *v_cache,
+                            const float *k_scales, const float *v_scales,
+                            const int32_t *block_tables, const int32_t *positions,
+                            const int32_t *token_starts, int32_t B, int32_t T, int32_t N,
+                            int32_t n_kv, int32_t d, int32_t bs, int32_t MB, int32_t NB,
+                            void *stream);
+pgd_status pgd_paged_decode_attention_fp8b(void *out, const void *q, const void *k_cache,
+                                           const void *v_cache, const float *k_scales,
+                                           const float *v_scales, const int32_t *block_tables,
+                                           const int32_t *context_lens, int32_t B, int32_t n_q,
+                                           int32_t n_kv, int32_t d, int32_t bs, int32_t MB,
+                                           int32_t NB, float scale, int32_t num_splits,
+                                           void *workspace, size_t workspace_bytes, void *stream);
+pgd_status pgd_append_decode_attention_fp8b(
+    void *out, const void *q, const void *k_new, const void *v_new, void *k_cache, void *v_cache,
+    float *k_scales, float *v_scales, const int32_t *block_tables, const int32_t *context_lens,
+    int32_t B, int32_t n_q, int32_t n_kv, int32_t d, int32_t bs, int32_t MB, int32_t NB,
+    float scale, int32_t num_splits, void *workspace, size_t workspace_bytes, void *stream);
+
+/* ---------------------------------------------------------------------- */
+/* block-sparse decode attention                                           */
+/* ---------------------------------------------------------------------- */
+/* Decode attention that reads W blocks of each context instead of all of it:
+ * the bytes of a decode step are the cache it reads ("The math of Transformer
+ * inference", section 4), and most of a long context takes next to no weight.
+ * A tile is one (block, KV head), numbered block * n_kv + head; each KV head
+ * selects its own tiles for the query heads that share it.
+ *
+ * pgd_block_bounds keeps, per tile, bounds of every key dim over the block's
+ * tokens: bounds int8 [NB][n_kv][2][128] (lower, then upper) and bound_scales
+ * fp32 [NB][n_kv] = s, the smallest 2^e (integer e >= -100) with max |k| <=
+ * 127 s: lower_i = floor(min_t k_ti / s), upper_i = ceil(max_t k_ti / s).
+ * It recomputes the blocks of sequence b that hold positions[b] ..
+ * context_lens[b] - 1 (positions NULL: from 0) over all their tokens before
+ * context_lens[b], from the cache as it stands (after the append): k_cache is
+ * a block-scaled pool with k_scales, or a bf16 pool with k_scales NULL.  T: at
+ * least the largest context_lens[b] - positions[b]; equal ones are a no-op.
+ * Keys must be finite.  PGD_DEVERR_BAD_CONTEXT for a context outside
+ * [0, MB*bs], PGD_DEVERR_BAD_POSITION for positions[b] outside [0,
+ * context_lens[b]] or a range of over T tokens; neither writes anything.
+ *
+ * pgd_select_blocks: for every sequence and KV head, all its blocks if they
+ * are at most W, else its first keep_first, its last keep_last (>= 1) and, of
+ * the others, those of the largest score, W in all, ties to the lower block:
+ *     score = s * max_h f_h * sum_i (max(r_hi, 0) upper_i + min(r_hi, 0) lower_i)
+ * over the KV head's query heads h, with r_h = q[b][h] / f_h rounded to the
+ * nearest integer (even on ties) and f_h the smallest 2^e (e >= -100) with
+ * max |q[b][h]| <= 127 f_h.  No key of a block that is left out has a larger
+ * product with a rounded query than the smallest score selected.  tiles int32
+ * [B][n_kv][W]: the selected tiles in the order of the sequence, then -1;
+ * tile_tokens int32 [B][n_kv]: the tokens they hold.  The scores are exact in
+ * fp32.  A bad context is flagged (PGD_DEVERR_BAD_CONTEXT) and selects
+ * nothing (tile_tokens 0); a block with a bad id counts as the lowest score.
+ * MB at most 49152.
+ *
+ * pgd_selected_decode_attention: decode attention of q over the tokens of the
+ * tiles, the last tile holding tile_tokens - (tiles - 1) * bs of them -- from
+ * pgd_select_blocks or from the caller.  Over a bf16 cache (k_scales and
+ * v_scales NULL) the definition, arithmetic and errors of
+ * pgd_paged_decode_attention, over a block-scaled one those of
+ * pgd_paged_decode_attention_fp8b, with tile ids checked against NB * n_kv and
+ * tile_tokens against [1, W * bs].  pgd_sparse_decode_attention is both calls
+ * in one, every argument checked before the first launch; tiles and
+ * tile_tokens are outputs too.  workspace as for pgd_paged_decode_attention
+ * (pgd_attention_workspace_size(B, n_q, n_kv, d, num_splits) bytes).
+ * B * n_kv at most PGD_MAX_BATCH. */
+pgd_status pgd_block_bounds(int8_t *bounds, float *bound_scales, const void *k_cache,
+                            const float *k_scales, const int32_t *block_tables,
+                            const int32_t *positions, const int32_t *context_lens, int32_t B,
+                            int32_t T, int32_t n_kv, int32_t d, int32_t bs, int32_t MB, int32_t NB,
+                            void *stream);
+pgd_status pgd_select_blocks(int32_t *tiles, int32_t *tile_tokens, const void *q,
+                             const int8_t *bounds, const float *bound_scales,
+                             const int32_t *block_tables, const int32_t *context_lens, int32_t B,
+                             int32_t n_q, int32_t n_kv, int32_t d, int32_t bs, int32_t MB,
+                             int32_t NB, int32_t W, int32_t keep_first, int32_t keep_last,
+                             void *stream);
+pgd_status pgd_selected_decode_attention(void *out, const void *q, const void *k_cache,
+                                         const void *v_cache, const float *k_scales,
+                                         const float *v_scales, const int32_t *tiles,
+                                         const int32_t *tile_tokens, int32_t B, int32_t n_q,
+                                         int32_t n_kv, int32_t d, int32_t bs, int32_t NB,
+                                         int32_t W, float scale, int32_t num_splits,
+                                         void *workspace, size_t workspace_bytes, void *stream);
+pgd_status pgd_sparse_decode_attention(
+    void *out, const void *q, const void *k_cache, const void *v_cache, const float *k_scales,
+    const float *v_scales, const int8_t *bounds, const float *bound_scales,
+    const int32_t *block_tables, const int32_t *context_lens, int32_t *tiles,
+    int32_t *tile_tokens, int32_t B, int32_t n_q, int32_t n_kv, int32_t d, int32_t bs, int32_t MB,
+    int32_t NB, int32_t W, int32_t keep_first, int32_t keep_last, float scale, int32_t num_splits,
+    void *workspace, size_t workspace_bytes, void *stream);
+
+/* ---------------------------------------------------------------------- */
 /* one decode step with host inputs and outputs                            */
 /* ---------------------------------------------------------------------- */
 /* One decode step of one layer for a caller whose per-step tensors live in

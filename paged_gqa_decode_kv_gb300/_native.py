@@ -66,6 +66,14 @@ SIGNATURES = {
                          _I, _I, _F, _I, _P, _Z, _P], _I),
     "pgd_decode_step_fp8": ([_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I,
                              _I, _I, _I, _F, _I, _P, _Z, _P], _I),
+    "pgd_kv_append_fp8b": ([_P] * 9 + [_I] * 8 + [_P], _I),
+    "pgd_kv_read_fp8b": ([_P] * 9 + [_I] * 8 + [_P], _I),
+    "pgd_paged_decode_attention_fp8b": ([_P] * 8 + [_I] * 7 + [_F, _I, _P, _Z, _P], _I),
+    "pgd_append_decode_attention_fp8b": ([_P] * 10 + [_I] * 7 + [_F, _I, _P, _Z, _P], _I),
+    "pgd_block_bounds": ([_P] * 7 + [_I] * 7 + [_P], _I),
+    "pgd_select_blocks": ([_P] * 7 + [_I] * 10 + [_P], _I),
+    "pgd_selected_decode_attention": ([_P] * 8 + [_I] * 7 + [_F, _I, _P, _Z, _P], _I),
+    "pgd_sparse_decode_attention": ([_P] * 12 + [_I] * 10 + [_F, _I, _P, _Z, _P], _I),
     "pgd_copy_blocks": ([_P, _P, _P, _P, _I, _I, _I, _I, _I, _P], _I),
     "pgd_device_errors": ([_P, _I, _P], _I),
     "pgd_read_stream": ([_P, _Z, _I, _P], _I),
@@ -330,7 +338,8 @@ def prepare(op: str, *args, **kwargs) -> PreparedCall:
     """A PreparedCall of one of the step calls, with the arguments that call
     takes: "paged_decode_attention", "paged_decode_attention_fp8",
     "append_decode_attention", "append_decode_attention_fp8", "decode_step",
-    "append_verify_attention" or "verify_step"."""
+    "append_verify_attention", "verify_step", "paged_decode_attention_fp8b",
+    "append_decode_attention_fp8b" or "sparse_decode_attention"."""
     if op == "paged_decode_attention":
         return PreparedCall(*_attention_call(False, *args, **kwargs))
     if op == "paged_decode_attention_fp8":
@@ -345,6 +354,12 @@ def prepare(op: str, *args, **kwargs) -> PreparedCall:
         return PreparedCall(*_append_verify_call(*args, **kwargs))
     if op == "verify_step":
         return PreparedCall(*_verify_step_call(*args, **kwargs))
+    if op == "paged_decode_attention_fp8b":
+        return PreparedCall(*_attention8b_call(*args, **kwargs))
+    if op == "append_decode_attention_fp8b":
+        return PreparedCall(*_append_attention8b_call(*args, **kwargs))
+    if op == "sparse_decode_attention":
+        return PreparedCall(*_sparse_call(*args, **kwargs))
     raise ValueError("no prepared form of %r" % op)
 
 
@@ -646,6 +661,299 @@ def append_decode_attention_fp8(out, q, k_new, v_new, k_cache, v_cache, block_ta
     name, args, out = _append_attention_call(True, out, q, k_new, v_new, k_cache, v_cache,
                                              block_tables, context_lens, scale, num_splits,
                                              workspace, stream)
+    _check(getattr(lib(), name)(*args))
+    return out
+
+
+# ------------------------------------------------- block-scaled 8-bit KV cache
+def _here(**tensors) -> None:
+    """Every given tensor on the current CUDA device (whose stream the call
+    is enqueued on)."""
+    dev = torch.cuda.current_device()
+    for name, t in tensors.items():
+        if t is not None and t.device.index != dev:
+            raise ValueError("%s is on %s, the current device is cuda:%d" % (name, t.device, dev))
+
+
+def _shape(t: torch.Tensor, shape: tuple, name: str) -> None:
+    if tuple(t.shape) != shape:
+        raise ValueError("%s must be %s, got %s" % (name, list(shape), list(t.shape)))
+
+
+def _cache8b_dims(k_cache, v_cache, k_scales, v_scales) -> Tuple[int, int, int]:
+    """(NB, n_kv, bs) of block-scaled pools uint8 [NB][n_kv][bs/8][8][8][16]
+    and their scales fp32 [NB][n_kv]."""
+    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        if t is not None:
+            _need(t, torch.uint8, n)
+            if t.dim() != 6 or tuple(t.shape[3:]) != (8, 8, 16):
+                raise ValueError("%s must be uint8 [NB][n_kv][bs/8][8][8][16]" % n)
+            _shape(t, tuple(k_cache.shape), n)
+    for t, n in ((k_scales, "k_scales"), (v_scales, "v_scales")):
+        if t is not None:
+            _need(t, torch.float32, n)
+            _shape(t, tuple(k_cache.shape[:2]), n)
+    return k_cache.shape[0], k_cache.shape[1], k_cache.shape[2] * 8
+
+
+def _range_call(name, k_rows, v_rows, k_cache, v_cache, k_scales, v_scales, block_tables,
+                positions, token_starts, max_tokens, stream):
+    for t, n in ((k_rows, "k rows"), (v_rows, "v rows")):
+        _need(t, torch.bfloat16, n)
+    NB, n_kv, bs = _cache8b_dims(k_cache, v_cache, k_scales, v_scales)
+    _need(block_tables, torch.int32, "block_tables")
+    _need(positions, torch.int32, "positions")
+    B, MB = block_tables.shape
+    _shape(positions, (B,), "positions")
+    if k_rows.dim() < 3 or tuple(k_rows.shape[-2:]) != (n_kv, HEAD_DIM):
+        raise ValueError("rows must end in [n_kv][%d], got %s" % (HEAD_DIM, list(k_rows.shape)))
+    _shape(v_rows, tuple(k_rows.shape), "v rows")
+    N = k_rows.numel() // (n_kv * HEAD_DIM)
+    if token_starts is None:
+        if (N and not B) or (B and N % B):
+            raise ValueError("%d rows for %d sequences" % (N, B))
+        T = N // B if B else 0
+        if max_tokens is not None and max_tokens != T:
+            raise ValueError("max_tokens = %d, but every sequence has %d" % (max_tokens, T))
+    else:
+        _need(token_starts, torch.int32, "token_starts")
+        _shape(token_starts, (B + 1,), "token_starts")
+        if max_tokens is None:
+            raise ValueError("token_starts needs max_tokens, the most tokens of a sequence")
+        T = int(max_tokens)
+    _here(k_rows=k_rows, v_rows=v_rows, k_cache=k_cache, v_cache=v_cache, k_scales=k_scales,
+          v_scales=v_scales, block_tables=block_tables, positions=positions,
+          token_starts=token_starts)
+    _check(getattr(lib(), name)(
+        _ptr(k_rows), _ptr(v_rows), _ptr(k_cache), _ptr(v_cache), _ptr(k_scales), _ptr(v_scales),
+        _ptr(block_tables), _ptr(positions), _ptr(token_starts), B, T, N, n_kv, HEAD_DIM, bs, MB,
+        NB, _stream(stream)))
+
+
+def kv_append_fp8b(k_new, v_new, k_cache, v_cache, k_scales, v_scales, block_tables, positions,
+                   token_starts=None, max_tokens: Optional[int] = None, stream=None) -> None:
+    """Quantise new tokens into the block-scaled pools at positions[b] on:
+    rows token_starts[b] .. token_starts[b + 1] - 1 of k_new/v_new
+    ([N][n_kv][d] bf16; at most max_tokens each), or without token_starts the
+    same number of tokens for every sequence ([B][n_kv][d] or
+    [B][T][n_kv][d])."""
+    _range_call("pgd_kv_append_fp8b", k_new, v_new, k_cache, v_cache, k_scales, v_scales,
+                block_tables, positions, token_starts, max_tokens, stream)
+
+
+def kv_read_fp8b(k_out, v_out, k_cache, v_cache, k_scales, v_scales, block_tables, positions,
+                 token_starts=None, max_tokens: Optional[int] = None, stream=None) -> None:
+    """Read ranges of positions back into rows of k_out/v_out (bf16): the
+    arguments of kv_append_fp8b, the other way."""
+    _range_call("pgd_kv_read_fp8b", k_out, v_out, k_cache, v_cache, k_scales, v_scales,
+                block_tables, positions, token_starts, max_tokens, stream)
+
+
+def _query(out, q, n_kv):
+    """(B, n_q, out) of a decode call's query [B][n_q][d]; out made if None."""
+    _need(q, torch.bfloat16, "q")
+    if q.dim() != 3:
+        raise ValueError("q must be [B][n_q][d], got %s" % list(q.shape))
+    B, n_q, _ = q.shape
+    if out is None:
+        out = torch.empty_like(q)
+    _need(out, torch.bfloat16, "out")
+    _shape(out, tuple(q.shape), "out")
+    return B, n_q, out
+
+
+def _scratch(workspace, B, n_q, n_kv, num_splits, device):
+    return make_workspace(B, n_q, n_kv, num_splits, device) if workspace is None else workspace
+
+
+def _attention8b_call(out, q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
+                      scale, num_splits=0, workspace=None, stream=None, new=()):
+    NB, n_kv, bs = _cache8b_dims(k_cache, v_cache, k_scales, v_scales)
+    B, n_q, out = _query(out, q, n_kv)
+    _need(block_tables, torch.int32, "block_tables")
+    _need(context_lens, torch.int32, "context_lens")
+    MB = block_tables.shape[1]
+    _shape(block_tables, (B, MB), "block_tables")
+    _shape(context_lens, (B,), "context_lens")
+    for t, n in zip(new, ("k_new", "v_new")):
+        _need(t, torch.bfloat16, n)
+        _shape(t, (B, n_kv, HEAD_DIM), n)
+        _here(**{n: t})
+    workspace = _scratch(workspace, B, n_q, n_kv, num_splits, q.device)
+    _here(out=out, q=q, k_cache=k_cache, v_cache=v_cache, k_scales=k_scales, v_scales=v_scales,
+          block_tables=block_tables, context_lens=context_lens, workspace=workspace)
+    name = "pgd_append_decode_attention_fp8b" if new else "pgd_paged_decode_attention_fp8b"
+    return name, (_ptr(out), _ptr(q), *(_ptr(t) for t in new), _ptr(k_cache), _ptr(v_cache),
+                  _ptr(k_scales), _ptr(v_scales), _ptr(block_tables), _ptr(context_lens), B, n_q,
+                  n_kv, q.shape[2], bs, MB, NB, float(scale), int(num_splits), _ptr(workspace),
+                  workspace.numel() * workspace.element_size(), _stream(stream)), out
+
+
+def _append_attention8b_call(out, q, k_new, v_new, *args, **kwargs):
+    return _attention8b_call(out, q, *args, new=(k_new, v_new), **kwargs)
+
+
+def paged_decode_attention_fp8b(out, q, k_cache, v_cache, k_scales, v_scales, block_tables,
+                                context_lens, scale: float, num_splits: int = 0,
+                                workspace: Optional[torch.Tensor] = None,
+                                stream=None) -> torch.Tensor:
+    """out[B][n_q][d] (bf16) = paged decode attention of q over the
+    block-scaled 8-bit cache."""
+    name, args, out = _attention8b_call(out, q, k_cache, v_cache, k_scales, v_scales,
+                                        block_tables, context_lens, scale, num_splits, workspace,
+                                        stream)
+    _check(getattr(lib(), name)(*args))
+    return out
+
+
+def append_decode_attention_fp8b(out, q, k_new, v_new, k_cache, v_cache, k_scales, v_scales,
+                                 block_tables, context_lens, scale: float, num_splits: int = 0,
+                                 workspace: Optional[torch.Tensor] = None,
+                                 stream=None) -> torch.Tensor:
+    """kv_append_fp8b of one token per sequence at context_lens - 1, then
+    attention over the block-scaled cache."""
+    name, args, out = _append_attention8b_call(out, q, k_new, v_new, k_cache, v_cache, k_scales,
+                                               v_scales, block_tables, context_lens, scale,
+                                               num_splits, workspace, stream)
+    _check(getattr(lib(), name)(*args))
+    return out
+
+
+# ------------------------------------------------------ block-sparse attention
+def _kv_dims(k_cache, v_cache, k_scales, v_scales) -> Tuple[int, int, int]:
+    """(NB, n_kv, bs) of a bf16 cache, or of a block-scaled one (with scales)."""
+    if k_scales is not None or v_scales is not None:
+        if k_scales is None or (v_cache is not None and v_scales is None):
+            raise ValueError("a block-scaled cache needs both scales")
+        return _cache8b_dims(k_cache, v_cache, k_scales, v_scales)
+    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        if t is not None:
+            _need(t, torch.bfloat16, n)
+            _shape(t, tuple(k_cache.shape), n)
+    return _cache_dims(k_cache)[:3]
+
+
+def _bounds_dims(bounds, bound_scales, NB, n_kv) -> None:
+    _need(bounds, torch.int8, "bounds")
+    _shape(bounds, (NB, n_kv, 2, HEAD_DIM), "bounds")
+    _need(bound_scales, torch.float32, "bound_scales")
+    _shape(bound_scales, (NB, n_kv), "bound_scales")
+
+
+def block_bounds(bounds, bound_scales, k_cache, block_tables, context_lens, positions=None,
+                 max_tokens: Optional[int] = None, k_scales=None, stream=None) -> None:
+    """Recompute the key bounds (int8 [NB][n_kv][2][d], fp32 [NB][n_kv]) of
+    the blocks that hold positions[b] .. context_lens[b] - 1 (positions None:
+    the whole contexts) of a bf16 cache, or of a block-scaled one with its
+    k_scales.  max_tokens: the most tokens of a sequence (default: the table
+    width)."""
+    NB, n_kv, bs = _kv_dims(k_cache, None, k_scales, None)
+    _bounds_dims(bounds, bound_scales, NB, n_kv)
+    _need(block_tables, torch.int32, "block_tables")
+    _need(context_lens, torch.int32, "context_lens")
+    B, MB = block_tables.shape
+    _shape(context_lens, (B,), "context_lens")
+    if positions is not None:
+        _need(positions, torch.int32, "positions")
+        _shape(positions, (B,), "positions")
+    _here(bounds=bounds, bound_scales=bound_scales, k_cache=k_cache, block_tables=block_tables,
+          context_lens=context_lens, positions=positions, k_scales=k_scales)
+    T = MB * bs if max_tokens is None else int(max_tokens)
+    _check(lib().pgd_block_bounds(_ptr(bounds), _ptr(bound_scales), _ptr(k_cache), _ptr(k_scales),
+                                  _ptr(block_tables), _ptr(positions), _ptr(context_lens), B, T,
+                                  n_kv, HEAD_DIM, bs, MB, NB, _stream(stream)))
+
+
+def _selection(tiles, tile_tokens, B, n_kv) -> int:
+    _need(tiles, torch.int32, "tiles")
+    _need(tile_tokens, torch.int32, "tile_tokens")
+    if tiles.dim() != 3:
+        raise ValueError("tiles must be [B][n_kv][W]")
+    W = tiles.shape[2]
+    _shape(tiles, (B, n_kv, W), "tiles")
+    _shape(tile_tokens, (B, n_kv), "tile_tokens")
+    return W
+
+
+def select_blocks(tiles, tile_tokens, q, bounds, bound_scales, block_tables, context_lens,
+                  keep_first: int, keep_last: int, block_size: int, stream=None) -> None:
+    """tiles [B][n_kv][W] and tile_tokens [B][n_kv] (int32): for every
+    sequence and KV head the first keep_first blocks, the last keep_last and
+    the others of the largest score, W in all."""
+    _need(bounds, torch.int8, "bounds")
+    NB, n_kv = bounds.shape[:2]
+    _bounds_dims(bounds, bound_scales, NB, n_kv)
+    _need(q, torch.bfloat16, "q")
+    _need(block_tables, torch.int32, "block_tables")
+    _need(context_lens, torch.int32, "context_lens")
+    B, n_q, d = q.shape
+    W = _selection(tiles, tile_tokens, B, n_kv)
+    MB = block_tables.shape[1]
+    _shape(block_tables, (B, MB), "block_tables")
+    _shape(context_lens, (B,), "context_lens")
+    _here(tiles=tiles, tile_tokens=tile_tokens, q=q, bounds=bounds, bound_scales=bound_scales,
+          block_tables=block_tables, context_lens=context_lens)
+    _check(lib().pgd_select_blocks(_ptr(tiles), _ptr(tile_tokens), _ptr(q), _ptr(bounds),
+                                   _ptr(bound_scales), _ptr(block_tables), _ptr(context_lens), B,
+                                   n_q, n_kv, d, int(block_size), MB, NB, W, int(keep_first),
+                                   int(keep_last), _stream(stream)))
+
+
+def selected_decode_attention(out, q, k_cache, v_cache, tiles, tile_tokens, scale: float,
+                              k_scales=None, v_scales=None, num_splits: int = 0,
+                              workspace: Optional[torch.Tensor] = None,
+                              stream=None) -> torch.Tensor:
+    """out[B][n_q][d] (bf16) = decode attention of q over the tiles (block *
+    n_kv + head, [B][n_kv][W]) of a bf16 cache, or of a block-scaled one with
+    its scales."""
+    NB, n_kv, bs = _kv_dims(k_cache, v_cache, k_scales, v_scales)
+    B, n_q, out = _query(out, q, n_kv)
+    W = _selection(tiles, tile_tokens, B, n_kv)
+    workspace = _scratch(workspace, B, n_q, n_kv, num_splits, q.device)
+    _here(out=out, q=q, k_cache=k_cache, v_cache=v_cache, k_scales=k_scales, v_scales=v_scales,
+          tiles=tiles, tile_tokens=tile_tokens, workspace=workspace)
+    _check(lib().pgd_selected_decode_attention(
+        _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scales), _ptr(v_scales),
+        _ptr(tiles), _ptr(tile_tokens), B, n_q, n_kv, q.shape[2], bs, NB, W, float(scale),
+        int(num_splits), _ptr(workspace), workspace.numel() * workspace.element_size(),
+        _stream(stream)))
+    return out
+
+
+def _sparse_call(out, q, k_cache, v_cache, bounds, bound_scales, block_tables, context_lens,
+                 tiles, tile_tokens, keep_first, keep_last, scale, k_scales=None, v_scales=None,
+                 num_splits=0, workspace=None, stream=None):
+    NB, n_kv, bs = _kv_dims(k_cache, v_cache, k_scales, v_scales)
+    _bounds_dims(bounds, bound_scales, NB, n_kv)
+    B, n_q, out = _query(out, q, n_kv)
+    W = _selection(tiles, tile_tokens, B, n_kv)
+    _need(block_tables, torch.int32, "block_tables")
+    _need(context_lens, torch.int32, "context_lens")
+    MB = block_tables.shape[1]
+    _shape(block_tables, (B, MB), "block_tables")
+    _shape(context_lens, (B,), "context_lens")
+    workspace = _scratch(workspace, B, n_q, n_kv, num_splits, q.device)
+    _here(out=out, q=q, k_cache=k_cache, v_cache=v_cache, k_scales=k_scales, v_scales=v_scales,
+          bounds=bounds, bound_scales=bound_scales, block_tables=block_tables,
+          context_lens=context_lens, tiles=tiles, tile_tokens=tile_tokens, workspace=workspace)
+    return "pgd_sparse_decode_attention", (
+        _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scales), _ptr(v_scales),
+        _ptr(bounds), _ptr(bound_scales), _ptr(block_tables), _ptr(context_lens), _ptr(tiles),
+        _ptr(tile_tokens), B, n_q, n_kv, q.shape[2], bs, MB, NB, W, int(keep_first),
+        int(keep_last), float(scale), int(num_splits), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _stream(stream)), out
+
+
+def sparse_decode_attention(out, q, k_cache, v_cache, bounds, bound_scales, block_tables,
+                            context_lens, tiles, tile_tokens, keep_first: int, keep_last: int,
+                            scale: float, k_scales=None, v_scales=None, num_splits: int = 0,
+                            workspace: Optional[torch.Tensor] = None,
+                            stream=None) -> torch.Tensor:
+    """select_blocks into tiles and tile_tokens, then
+    selected_decode_attention over them, in one call."""
+    name, args, out = _sparse_call(out, q, k_cache, v_cache, bounds, bound_scales, block_tables,
+                                   context_lens, tiles, tile_tokens, keep_first, keep_last, scale,
+                                   k_scales, v_scales, num_splits, workspace, stream)
     _check(getattr(lib(), name)(*args))
     return out
 

@@ -14,6 +14,7 @@
 #include <tuple>
 #include <atomic>
 
+#include "kv_fp8b.cuh"
 #include "pgd_device.cuh"
 #include "short_attention.cuh"
 
@@ -1266,6 +1267,361 @@ pgd_status pgd_device_errors(int32_t *flags, int32_t clear, void *stream) {
     if (e != cudaSuccess) return cuda_fail(e, "clear error word");
   }
   return ok();
+}
+
+// ------------------------------------------------ block-scaled 8-bit cache
+// Checks shared by the write, the read-back and the key bounds: sizes, the
+// packed rows and the largest grid (one warp per block, head and pool).
+static pgd_status check_ranges(int32_t B, int32_t T, int32_t n_kv, int32_t d, int32_t bs,
+                               int32_t MB, int32_t NB) {
+  if (B < 0 || T < 0) return fail(PGD_ERR_INVALID_ARG, "B = %d, T = %d", B, T);
+  pgd_status s = check_cache_shape(n_kv, d, bs, MB, NB);
+  if (s != PGD_OK) return s;
+  if ((long long)NB * n_kv > 0x7fffffffLL)
+    return fail(PGD_ERR_INVALID_ARG, "NB * n_kv = %lld overflows int32", (long long)NB * n_kv);
+  if ((long long)B * (1 + ((long long)T + bs - 1) / bs) * n_kv > 0x7fffffffLL)
+    return fail(PGD_ERR_INVALID_ARG, "B * T * n_kv too large");
+  return PGD_OK;
+}
+
+static pgd_status check_scales(const float *k_scales, const float *v_scales) {
+  if (!k_scales || !v_scales) return fail(PGD_ERR_INVALID_ARG, "null scales");
+  if (!aligned(k_scales, 4) || !aligned(v_scales, 4))
+    return fail(PGD_ERR_INVALID_ARG, "scales must be 4-byte aligned");
+  return PGD_OK;
+}
+
+static pgd_status kv8b_range_call(bool write, const void *k_rows, const void *v_rows,
+                                  const void *k_cache, const void *v_cache, const float *k_scales,
+                                  const float *v_scales, const int32_t *tables,
+                                  const int32_t *positions, const int32_t *starts, int32_t B,
+                                  int32_t T, int32_t N, int32_t n_kv, int32_t d, int32_t bs,
+                                  int32_t MB, int32_t NB, void *stream) {
+  pgd_status s = check_ranges(B, T, n_kv, d, bs, MB, NB);
+  if (s != PGD_OK) return s;
+  if (N < 0 || (!starts && (long long)B * T != N))
+    return fail(PGD_ERR_INVALID_ARG, "N = %d rows (B * T = %lld)", N, (long long)B * T);
+  if (B == 0 || T == 0 || N == 0) return ok();
+  if (!k_rows || !v_rows || !k_cache || !v_cache || !tables || !positions)
+    return fail(PGD_ERR_INVALID_ARG, "null pointer");
+  if (!aligned(k_rows, 16) || !aligned(v_rows, 16) || !aligned(k_cache, 16) ||
+      !aligned(v_cache, 16))
+    return fail(PGD_ERR_INVALID_ARG, "rows and pools must be 16-byte aligned");
+  if ((s = check_scales(k_scales, v_scales)) != PGD_OK) return s;
+  Kv8bParams p = {};
+  p.k_cache = static_cast<unsigned char *>(const_cast<void *>(k_cache));
+  p.v_cache = static_cast<unsigned char *>(const_cast<void *>(v_cache));
+  p.k_scales = const_cast<float *>(k_scales);
+  p.v_scales = const_cast<float *>(v_scales);
+  p.tables = tables;
+  p.pos = positions;
+  p.starts = starts;
+  p.B = B;
+  p.T = T;
+  p.N = N;
+  p.n_kv = n_kv;
+  p.bs = bs;
+  p.MB = MB;
+  p.NB = NB;
+  if ((s = error_word(&p.err)) != PGD_OK) return s;
+  cudaError_t e;
+  if (write) {
+    p.k_new = static_cast<const __nv_bfloat16 *>(k_rows);
+    p.v_new = static_cast<const __nv_bfloat16 *>(v_rows);
+    e = kv_append_fp8b_launch(p, static_cast<cudaStream_t>(stream));
+  } else {
+    p.k_out = static_cast<__nv_bfloat16 *>(const_cast<void *>(k_rows));
+    p.v_out = static_cast<__nv_bfloat16 *>(const_cast<void *>(v_rows));
+    e = kv_read_fp8b_launch(p, static_cast<cudaStream_t>(stream));
+  }
+  if (e != cudaSuccess) return cuda_fail(e, write ? "kv_append_fp8b launch" : "kv_read_fp8b launch");
+  return ok();
+}
+
+pgd_status pgd_kv_append_fp8b(const void *k_new, const void *v_new, void *k_cache, void *v_cache,
+                              float *k_scales, float *v_scales, const int32_t *block_tables,
+                              const int32_t *positions, const int32_t *token_starts, int32_t B,
+                              int32_t T, int32_t N, int32_t n_kv, int32_t d, int32_t bs,
+                              int32_t MB, int32_t NB, void *stream) {
+  return kv8b_range_call(true, k_new, v_new, k_cache, v_cache, k_scales, v_scales, block_tables,
+                         positions, token_starts, B, T, N, n_kv, d, bs, MB, NB, stream);
+}
+
+pgd_status pgd_kv_read_fp8b(void *k_out, void *v_out, const void *k_cache, const void *v_cache,
+                            const float *k_scales, const float *v_scales,
+                            const int32_t *block_tables, const int32_t *positions,
+                            const int32_t *token_starts, int32_t B, int32_t T, int32_t N,
+                            int32_t n_kv, int32_t d, int32_t bs, int32_t MB, int32_t NB,
+                            void *stream) {
+  return kv8b_range_call(false, k_out, v_out, k_cache, v_cache, k_scales, v_scales, block_tables,
+                         positions, token_starts, B, T, N, n_kv, d, bs, MB, NB, stream);
+}
+
+// Attention over the block-scaled cache on checked arguments.
+static pgd_status launch_attention_fp8b(void *out, const void *q, const void *k_cache,
+                                        const void *v_cache, const float *k_scales,
+                                        const float *v_scales, const int32_t *tables,
+                                        const int32_t *ctx, int32_t B, int32_t n_q, int32_t n_kv,
+                                        int32_t bs, int32_t MB, int32_t NB, float scale,
+                                        int32_t num_splits, void *workspace,
+                                        size_t workspace_bytes, const Kv8bParams *append,
+                                        cudaStream_t stream) {
+  pgd_status s = check_scales(k_scales, v_scales);
+  if (s != PGD_OK) return s;
+  PreparedAttention pa;
+  s = prepare_attention(out, q, k_cache, v_cache, tables, ctx, B, n_q, n_kv, bs, MB, NB, scale,
+                        num_splits, workspace, workspace_bytes, &pa, true);
+  if (s != PGD_OK) return s;
+  if (append) {
+    Kv8bParams ap = *append;
+    ap.err = pa.p.err;
+    const cudaError_t e = kv_append_fp8b_launch(ap, stream);
+    if (e != cudaSuccess) return cuda_fail(e, "kv_append_fp8b launch");
+  }
+  Attn8bParams p;
+  p.a = pa.p;
+  p.k_scales = k_scales;
+  p.v_scales = v_scales;
+  const cudaError_t e = cluster_attention_fp8b_launch(p, pa.G, bs, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "block-scaled attention launch");
+  return PGD_OK;
+}
+
+pgd_status pgd_paged_decode_attention_fp8b(void *out, const void *q, const void *k_cache,
+                                           const void *v_cache, const float *k_scales,
+                                           const float *v_scales, const int32_t *block_tables,
+                                           const int32_t *context_lens, int32_t B, int32_t n_q,
+                                           int32_t n_kv, int32_t d, int32_t bs, int32_t MB,
+                                           int32_t NB, float scale, int32_t num_splits,
+                                           void *workspace, size_t workspace_bytes,
+                                           void *stream) {
+  pgd_status s = check_attention_args(out, q, k_cache, v_cache, block_tables, context_lens, B,
+                                      n_q, n_kv, d, bs, MB, NB, scale, num_splits);
+  if (s != PGD_OK) return s;
+  if (B == 0) return ok();
+  s = launch_attention_fp8b(out, q, k_cache, v_cache, k_scales, v_scales, block_tables,
+                            context_lens, B, n_q, n_kv, bs, MB, NB, scale, num_splits, workspace,
+                            workspace_bytes, nullptr, static_cast<cudaStream_t>(stream));
+  return s == PGD_OK ? ok() : s;
+}
+
+pgd_status pgd_append_decode_attention_fp8b(
+    void *out, const void *q, const void *k_new, const void *v_new, void *k_cache, void *v_cache,
+    float *k_scales, float *v_scales, const int32_t *block_tables, const int32_t *context_lens,
+    int32_t B, int32_t n_q, int32_t n_kv, int32_t d, int32_t bs, int32_t MB, int32_t NB,
+    float scale, int32_t num_splits, void *workspace, size_t workspace_bytes, void *stream) {
+  pgd_status s = check_attention_args(out, q, k_cache, v_cache, block_tables, context_lens, B,
+                                      n_q, n_kv, d, bs, MB, NB, scale, num_splits);
+  if (s != PGD_OK) return s;
+  if (B == 0) return ok();
+  if (!k_new || !v_new) return fail(PGD_ERR_INVALID_ARG, "null pointer");
+  if (!aligned(k_new, 16) || !aligned(v_new, 16))
+    return fail(PGD_ERR_INVALID_ARG, "bf16 arrays must be 16-byte aligned");
+  if ((s = check_ranges(B, 1, n_kv, d, bs, MB, NB)) != PGD_OK) return s;
+  Kv8bParams ap = {};
+  ap.k_new = static_cast<const __nv_bfloat16 *>(k_new);
+  ap.v_new = static_cast<const __nv_bfloat16 *>(v_new);
+  ap.k_cache = static_cast<unsigned char *>(k_cache);
+  ap.v_cache = static_cast<unsigned char *>(v_cache);
+  ap.k_scales = k_scales;
+  ap.v_scales = v_scales;
+  ap.tables = block_tables;
+  ap.pos = context_lens;
+  ap.pos_offset = -1;
+  ap.B = B;
+  ap.T = 1;
+  ap.N = B;
+  ap.n_kv = n_kv;
+  ap.bs = bs;
+  ap.MB = MB;
+  ap.NB = NB;
+  s = launch_attention_fp8b(out, q, k_cache, v_cache, k_scales, v_scales, block_tables,
+                            context_lens, B, n_q, n_kv, bs, MB, NB, scale, num_splits, workspace,
+                            workspace_bytes, &ap, static_cast<cudaStream_t>(stream));
+  return s == PGD_OK ? ok() : s;
+}
+
+// -------------------------------------------------- block-sparse attention
+pgd_status pgd_block_bounds(int8_t *bounds, float *bound_scales, const void *k_cache,
+                            const float *k_scales, const int32_t *block_tables,
+                            const int32_t *positions, const int32_t *context_lens, int32_t B,
+                            int32_t T, int32_t n_kv, int32_t d, int32_t bs, int32_t MB, int32_t NB,
+                            void *stream) {
+  pgd_status s = check_ranges(B, T, n_kv, d, bs, MB, NB);
+  if (s != PGD_OK) return s;
+  if (B == 0 || T == 0) return ok();
+  if (!bounds || !bound_scales || !k_cache || !block_tables || !context_lens)
+    return fail(PGD_ERR_INVALID_ARG, "null pointer");
+  if (!aligned(bounds, 16) || !aligned(k_cache, 16))
+    return fail(PGD_ERR_INVALID_ARG, "bounds and pool must be 16-byte aligned");
+  if (!aligned(bound_scales, 4) || (k_scales && !aligned(k_scales, 4)))
+    return fail(PGD_ERR_INVALID_ARG, "scales must be 4-byte aligned");
+  BoundsParams p = {};
+  p.bounds = reinterpret_cast<signed char *>(bounds);
+  p.bound_scales = bound_scales;
+  p.k_cache = static_cast<const unsigned char *>(k_cache);
+  p.k_scales = k_scales;
+  p.tables = block_tables;
+  p.pos = positions;
+  p.ctx = context_lens;
+  p.B = B;
+  p.T = T;
+  p.n_kv = n_kv;
+  p.bs = bs;
+  p.MB = MB;
+  p.NB = NB;
+  if ((s = error_word(&p.err)) != PGD_OK) return s;
+  const cudaError_t e = block_bounds_launch(p, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "block bounds launch");
+  return ok();
+}
+
+// Checks of a selection (W tiles per sequence and KV head) and of attention
+// over one: the shapes, and the virtual batch of B * n_kv one-head rows.
+static pgd_status check_selection(int32_t B, int32_t n_q, int32_t n_kv, int32_t d, int32_t bs,
+                                  int32_t NB, int32_t W) {
+  if (B < 0) return fail(PGD_ERR_INVALID_ARG, "B = %d", B);
+  if (W < 1) return fail(PGD_ERR_INVALID_ARG, "W = %d", W);
+  pgd_status s = check_cache_shape(n_kv, d, bs, W, NB);
+  if (s != PGD_OK) return s;
+  if (n_q <= 0 || n_q % n_kv) return fail(PGD_ERR_INVALID_ARG, "n_q %% n_kv != 0");
+  if (!supported_group(n_q / n_kv))
+    return fail(PGD_ERR_UNSUPPORTED, "group size G = %d (1, 2, 4 or 8)", n_q / n_kv);
+  if ((long long)B * n_kv > PGD_MAX_BATCH)
+    return fail(PGD_ERR_UNSUPPORTED, "B * n_kv = %lld > %d", (long long)B * n_kv, PGD_MAX_BATCH);
+  if ((long long)NB * n_kv > 0x7fffffffLL)
+    return fail(PGD_ERR_INVALID_ARG, "NB * n_kv = %lld overflows int32", (long long)NB * n_kv);
+  if ((long long)B * n_kv * W >= 0x7fffffffLL)
+    return fail(PGD_ERR_INVALID_ARG, "B * n_kv * W >= 2^31");
+  return PGD_OK;
+}
+
+static pgd_status prepare_select(int32_t *tiles, int32_t *tile_tokens, const void *q,
+                                 const int8_t *bounds, const float *bound_scales,
+                                 const int32_t *tables, const int32_t *ctx, int32_t B, int32_t n_q,
+                                 int32_t n_kv, int32_t d, int32_t bs, int32_t MB, int32_t NB,
+                                 int32_t W, int32_t keep_first, int32_t keep_last,
+                                 SelectParams *sp) {
+  pgd_status s = check_selection(B, n_q, n_kv, d, bs, NB, W);
+  if (s != PGD_OK) return s;
+  if ((s = check_cache_shape(n_kv, d, bs, MB, NB)) != PGD_OK) return s;
+  if (MB > select_max_blocks())
+    return fail(PGD_ERR_UNSUPPORTED, "MB = %d > %d blocks", MB, select_max_blocks());
+  if ((long long)B * MB >= 0x7fffffffLL) return fail(PGD_ERR_INVALID_ARG, "B * MB >= 2^31");
+  if (keep_first < 0 || keep_last < 1 || (long long)keep_first + keep_last > W)
+    return fail(PGD_ERR_INVALID_ARG, "keep_first = %d, keep_last = %d of W = %d", keep_first,
+                keep_last, W);
+  if (B == 0) return PGD_OK;
+  if (!tiles || !tile_tokens || !q || !bounds || !bound_scales || !tables || !ctx)
+    return fail(PGD_ERR_INVALID_ARG, "null pointer");
+  if (!aligned(q, 16) || !aligned(bounds, 16))
+    return fail(PGD_ERR_INVALID_ARG, "q and bounds must be 16-byte aligned");
+  if (!aligned(bound_scales, 4) || !aligned(tiles, 4) || !aligned(tile_tokens, 4) ||
+      !aligned(tables, 4) || !aligned(ctx, 4))
+    return fail(PGD_ERR_INVALID_ARG, "int32 and fp32 arrays must be 4-byte aligned");
+  sp->tiles = tiles;
+  sp->lens = tile_tokens;
+  sp->q = static_cast<const __nv_bfloat16 *>(q);
+  sp->bounds = reinterpret_cast<const signed char *>(bounds);
+  sp->bound_scales = bound_scales;
+  sp->tables = tables;
+  sp->ctx = ctx;
+  sp->B = B;
+  sp->n_q = n_q;
+  sp->n_kv = n_kv;
+  sp->bs = bs;
+  sp->MB = MB;
+  sp->NB = NB;
+  sp->W = W;
+  sp->keep_first = keep_first;
+  sp->keep_last = keep_last;
+  return PGD_OK;
+}
+
+pgd_status pgd_select_blocks(int32_t *tiles, int32_t *tile_tokens, const void *q,
+                             const int8_t *bounds, const float *bound_scales,
+                             const int32_t *block_tables, const int32_t *context_lens, int32_t B,
+                             int32_t n_q, int32_t n_kv, int32_t d, int32_t bs, int32_t MB,
+                             int32_t NB, int32_t W, int32_t keep_first, int32_t keep_last,
+                             void *stream) {
+  SelectParams sp = {};
+  pgd_status s = prepare_select(tiles, tile_tokens, q, bounds, bound_scales, block_tables,
+                                context_lens, B, n_q, n_kv, d, bs, MB, NB, W, keep_first,
+                                keep_last, &sp);
+  if (s != PGD_OK) return s;
+  if (B == 0) return ok();
+  if ((s = error_word(&sp.err)) != PGD_OK) return s;
+  const cudaError_t e = select_blocks_launch(sp, n_q / n_kv, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "block selection launch");
+  return ok();
+}
+
+// Attention over W tiles per (sequence, KV head): a batch of B * n_kv rows of
+// one KV head each over a pool of NB * n_kv one-head blocks.  `select`, if
+// given, runs first, after every check of both.
+static pgd_status selected_attention(void *out, const void *q, const void *k_cache,
+                                     const void *v_cache, const float *k_scales,
+                                     const float *v_scales, const int32_t *tiles,
+                                     const int32_t *tile_tokens, int32_t B, int32_t n_q,
+                                     int32_t n_kv, int32_t d, int32_t bs, int32_t NB, int32_t W,
+                                     float scale, int32_t num_splits, void *workspace,
+                                     size_t workspace_bytes, SelectParams *select,
+                                     cudaStream_t stream) {
+  pgd_status s = check_selection(B, n_q, n_kv, d, bs, NB, W);
+  if (s != PGD_OK) return s;
+  const int32_t U = B * n_kv, G = n_q / n_kv;
+  s = check_attention_args(out, q, k_cache, v_cache, tiles, tile_tokens, U, G, 1, d, bs, W,
+                           NB * n_kv, scale, num_splits);
+  if (s != PGD_OK) return s;
+  const bool fp8b = k_scales != nullptr || v_scales != nullptr;
+  if (fp8b && (s = check_scales(k_scales, v_scales)) != PGD_OK) return s;
+  if (B == 0) return ok();
+  PreparedAttention pa;  // (checks the workspace; nothing is enqueued)
+  s = prepare_attention(out, q, k_cache, v_cache, tiles, tile_tokens, U, G, 1, bs, W, NB * n_kv,
+                        scale, num_splits, workspace, workspace_bytes, &pa, fp8b);
+  if (s != PGD_OK) return s;
+  if (select) {
+    select->err = pa.p.err;
+    const cudaError_t e = select_blocks_launch(*select, G, stream);
+    if (e != cudaSuccess) return cuda_fail(e, "block selection launch");
+  }
+  if (fp8b)
+    s = launch_attention_fp8b(out, q, k_cache, v_cache, k_scales, v_scales, tiles, tile_tokens, U,
+                              G, 1, bs, W, NB * n_kv, scale, num_splits, workspace,
+                              workspace_bytes, nullptr, stream);
+  else
+    s = launch_attention(out, q, k_cache, v_cache, tiles, tile_tokens, U, G, 1, bs, W, NB * n_kv,
+                         scale, num_splits, workspace, workspace_bytes, stream);
+  return s == PGD_OK ? ok() : s;
+}
+
+pgd_status pgd_selected_decode_attention(void *out, const void *q, const void *k_cache,
+                                         const void *v_cache, const float *k_scales,
+                                         const float *v_scales, const int32_t *tiles,
+                                         const int32_t *tile_tokens, int32_t B, int32_t n_q,
+                                         int32_t n_kv, int32_t d, int32_t bs, int32_t NB,
+                                         int32_t W, float scale, int32_t num_splits,
+                                         void *workspace, size_t workspace_bytes, void *stream) {
+  return selected_attention(out, q, k_cache, v_cache, k_scales, v_scales, tiles, tile_tokens, B,
+                            n_q, n_kv, d, bs, NB, W, scale, num_splits, workspace,
+                            workspace_bytes, nullptr, static_cast<cudaStream_t>(stream));
+}
+
+pgd_status pgd_sparse_decode_attention(
+    void *out, const void *q, const void *k_cache, const void *v_cache, const float *k_scales,
+    const float *v_scales, const int8_t *bounds, const float *bound_scales,
+    const int32_t *block_tables, const int32_t *context_lens, int32_t *tiles,
+    int32_t *tile_tokens, int32_t B, int32_t n_q, int32_t n_kv, int32_t d, int32_t bs, int32_t MB,
+    int32_t NB, int32_t W, int32_t keep_first, int32_t keep_last, float scale, int32_t num_splits,
+    void *workspace, size_t workspace_bytes, void *stream) {
+  SelectParams sp = {};
+  pgd_status s = prepare_select(tiles, tile_tokens, q, bounds, bound_scales, block_tables,
+                                context_lens, B, n_q, n_kv, d, bs, MB, NB, W, keep_first,
+                                keep_last, &sp);
+  if (s != PGD_OK) return s;
+  return selected_attention(out, q, k_cache, v_cache, k_scales, v_scales, tiles, tile_tokens, B,
+                            n_q, n_kv, d, bs, NB, W, scale, num_splits, workspace,
+                            workspace_bytes, B ? &sp : nullptr, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"
