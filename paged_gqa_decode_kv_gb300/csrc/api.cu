@@ -1382,7 +1382,12 @@ static pgd_status launch_attention_fp8b(void *out, const void *q, const void *k_
   p.a = pa.p;
   p.k_scales = k_scales;
   p.v_scales = v_scales;
-  const cudaError_t e = cluster_attention_fp8b_launch(p, pa.G, bs, stream);
+  // The append writes only the cache: the attention's prologue overlaps it.
+  p.a.wait_late = append ? 1 : 0;
+  const cudaError_t e =
+      short_rule(B, n_kv, MB, bs, num_splits, 1)
+          ? cluster_attention_fp8b_launch(p, pa.G, bs, stream)
+          : attention_fp8b_launch(p, pa.G, bs, pa.grid, stream);
   if (e != cudaSuccess) return cuda_fail(e, "block-scaled attention launch");
   return PGD_OK;
 }

@@ -1,0 +1,850 @@
+// attention_fp8b.cu -- paged GQA decode attention over the block-scaled 8-bit
+// cache (kv_fp8b.cuh) on the fifth-generation tensor cores, reading the codes
+// as they lie: nothing is dequantised.
+//
+//   out[b][h] = sum_t softmax_t(scale * q[b][h] . k_t) v_t,  t < ctx[b],
+//   k_t = sk[tile] * E4M3(code), v_t = sv[tile] * E4M3(code)
+//
+// The schedule (units, cost-balanced cuts over CTAs, last-arriver merge), the
+// roles and the bounded waits are those of attention_kernel.cuh, whose
+// helpers this kernel uses; what differs is the arithmetic of a stage of 128
+// tokens, two E4M3 contractions with tokens on the M side (A) resp. the K
+// side, fp32 accumulators in tensor memory:
+//   S^T[128 tok][16]   = Kc[128 tok][128 d]    . Q^T[128 d][16]
+//   O^T[128 d][NP]    += Vc^T[128 d][128 tok]  . P^T[128 tok][NP]
+//
+// Scores.  Q carries each head as a high and a low E4M3 part (columns h and
+// 8 + h), the bf16 query itself within 2^-17 of its largest element; the
+// softmax adds the two columns and applies the query's and the block's scale.
+//
+// Probabilities.  An E4M3 number has four significant bits and no value
+// between 0 and 2^-9, too few of either for a softmax weight.  But M = 128 by
+// N = 16 leaves columns free, so a weight goes in as three E4M3 terms in three
+// columns: x = hi + 2^-5 lo + 2^-10 lo2, each the rounding of what the terms
+// before it leave, scaled up by 2^5.  A residual is at most 2^-4 of its term's
+// binade, so three terms hold a weight to 2^-12 of itself, and to 2^-24 of
+// the head's largest weight however small it is (hi alone ends at 2^-13).
+// The epilogue adds the three columns.  (Two terms would hold 2^-8, but a
+// context of 2^17 light tokens beside a heavy one needs the range: its weights
+// are 2^-17 of the largest.)
+//
+// V's scale goes into the weight: x = 16 p sv.  So that x keeps its range
+// whatever the blocks' scales, the running reference of a head is the maximum
+// of log2(p sv) rather than of log2(p); the sum of p takes the same reference
+// and stays exact in fp32, so outputs, partial states and their merge need no
+// second one.  The reference moves when exceeded by 2^4: x <= 2^8, and 2^5
+// times a residual of x stays within E4M3's 448.
+//
+// Roles (384 threads): warps 0-3 softmax (thread t = token row t), 4 / 5 K / V
+// producers, 6 q.k^T issuer, 7 p.v issuer, 8-11 epilogue.  The K producer also
+// fetches both scales of every block of a stage into a 16-stage ring by
+// 4-byte asynchronous copies that count on the stage's own barrier, so no warp
+// waits for a dependent load.
+#include "attention_kernel.cuh"
+#include "kv_fp8b.cuh"
+
+namespace pgd {
+namespace tc8b {
+
+using namespace tc;
+
+constexpr int NTHREADS = 384;
+constexpr int GROUP = kGroupBytes8b;   // bytes of 8 tokens
+constexpr int STAGE = TOK * kHeadDim;  // K (or V) codes of a stage
+constexpr int NSK = 6, NSV = 6;        // ring depths
+constexpr int NSR = 16;                // stages of scales
+constexpr int Q_BYTES = NPAD * 128;    // 16 E4M3 rows as 8 x 16-byte core matrices
+constexpr float kMoveLog2 = 4.f;       // move the reference when exceeded by 2^4
+constexpr float kWeightUnit = 16.f;    // x = 16 p sv
+constexpr float kTerm = 32.f;          // a term's residual is scaled by 2^5
+
+// Columns of P and O: term i of head h in column i * TS + h.
+template <int G> constexpr int TS = G <= 4 ? 4 : 8;
+template <int G> constexpr int NP = G <= 4 ? 16 : 32;
+constexpr int P_BYTES8 = TOK * 32;     // a P buffer (NP = 32; NP = 16 uses half)
+
+constexpr int OFF_K = 0;
+constexpr int OFF_V = OFF_K + NSK * STAGE;
+constexpr int OFF_Q = OFF_V + NSV * STAGE;  // double buffered by segment parity
+constexpr int OFF_P = OFF_Q + 2 * Q_BYTES;  // double buffered by stage parity
+constexpr int OFF_SC = OFF_P + 2 * P_BYTES8;           // f32 [NSR][2][8] (K, V) scales
+constexpr int OFF_BAR = OFF_SC + NSR * 2 * 8 * 4;
+constexpr int OFF_RED = OFF_BAR + 512;                 // f32 [2][4][8] warp maxima
+constexpr int OFF_LRED = OFF_RED + 2 * 4 * 8 * 4;      // f32 [2][4][8] warp sums
+constexpr int OFF_MREF = OFF_LRED + 2 * 4 * 8 * 4;     // f32 [2][8] references
+constexpr int OFF_QS = OFF_MREF + 2 * 8 * 4;           // f32 [2][8] query scales
+constexpr int OFF_MERGE = OFF_QS + 64;                 // float2 [MERGE_PAIRS]
+constexpr int OFF_MISC = OFF_MERGE + MERGE_PAIRS * 8;
+constexpr int OFF_PRE = OFF_MISC + 192;                // int [B + 1]
+
+constexpr size_t smem_size(int B) { return (size_t)SMEM_SLACK + OFF_PRE + (size_t)(B + 1) * 4; }
+static_assert(smem_size(PGD_MAX_BATCH) <= 232448, "layout exceeds 227 KB");
+static_assert((OFF_MISC + 24) % 8 == 0, "WaitCtl alignment");
+// The scales and the invalid-block mask of stage s are written when it is
+// armed, after the q.k^T of stage s - NSK has completed and so (S buffers)
+// after the softmax has read those of stage s - NSK - NSB.
+static_assert(NSR >= NSK + NSB && (NSR & (NSR - 1)) == 0, "scale and mask rings");
+static_assert(40 + 4 * NSR <= 112 && OFF_MISC % 16 == 0, "misc layout");
+
+// One CTA streams at most about 1/kShare of the HBM rate.
+constexpr long long kShare = 104;
+
+// kind::f8f6f4, D f32, A and B E4M3, both MN-major, M = 128.
+__host__ __device__ constexpr uint32_t idesc_pv(int n) {
+  return (1u << 4) | (1u << 15) | (1u << 16) | ((uint32_t)(n >> 3) << 17) |
+         ((uint32_t)(TOK >> 4) << 24);
+}
+
+// 4 bytes from global to shared memory, asynchronously.
+__device__ __forceinline__ void copy4_async(uint32_t dst, const void *src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+// Arrive on `bar` (one of its expected arrivals) once this thread's earlier
+// asynchronous copies have landed.
+__device__ __forceinline__ void arrive_after_copies(uint64_t *bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar))
+               : "memory");
+}
+
+// One producer warp: walks the CTA's stages and copies one tile per lane.
+// The K producer also copies the blocks' scales, records which blocks of a
+// stage had an invalid id and writes each segment's query (high parts in rows
+// 0-7, low parts in rows 8-15, one power-of-two scale per head).  Table
+// entries and queries are loaded one step ahead.
+template <int G, int BS, bool IS_K>
+__device__ __forceinline__ void produce(const Attn8bParams &pp, const Schedule &sc,
+                                        unsigned char *smem, uint64_t *full, uint64_t *empty,
+                                        volatile int *stage_mask, float *qscale,
+                                        uint64_t *q_ready, uint64_t *q_free,
+                                        volatile int *abort_flag, int lane) {
+  const AttnParams &p = pp.a;
+  constexpr int SB = TOK / BS;
+  constexpr uint32_t TILE = BS * kHeadDim;
+  constexpr int NS = IS_K ? NSK : NSV;
+  constexpr int QPL = (16 * G + 31) / 32;  // 16-byte pieces of q per lane
+  const unsigned char *cache = IS_K ? p.k_cache : p.v_cache;
+  unsigned char *ring = smem + (IS_K ? OFF_K : OFF_V);
+  const uint32_t sring = smem_addr(smem + OFF_SC);
+  const uint64_t policy = l2_policy_evict_first();
+
+  struct Ahead {
+    uint4 q[QPL];
+    int tab, tab_next;
+  };
+  auto load_ahead = [&](const Segment &g, Ahead &a) {
+    if (IS_K) {
+#pragma unroll
+      for (int i = 0; i < QPL; ++i) {
+        const int j = lane + 32 * i, r = j >> 4, c = j & 15;
+        a.q[i] = j < 16 * G ? __ldg(reinterpret_cast<const uint4 *>(
+                                  p.q + q_index(p, g.b, g.g, r) * kHeadDim + c * 8))
+                            : make_uint4(0, 0, 0, 0);
+      }
+    }
+    const int32_t *trow = p.tables + (size_t)g.b * p.MB + g.j0;
+    a.tab = (lane < g.n) ? __ldg(trow + lane) : 0;
+    a.tab_next = (32 + lane < g.n) ? __ldg(trow + 32 + lane) : 0;
+  };
+
+  SegCursor cur(sc);
+  Segment sg, nsg;
+  Ahead cur_a{}, next_a{};
+  bool have = cur.next(sc, p.B, sg);
+  if (have) load_ahead(sg, cur_a);
+  if (p.wait_late == 1) pdl_wait();  // the append has written the cache
+  int s = 0, k = 0;
+  bool stop = false;
+  while (have && !stop) {
+    const bool have_next = cur.next(sc, p.B, nsg);
+    if (have_next) load_ahead(nsg, next_a);
+    if (IS_K) {
+      const int qb = k & 1;
+      if (lane == 0)
+        wait_or_abort(&q_free[qb], ((uint32_t)(k >> 1) & 1u) ^ 1u, abort_flag, p.err);
+      __syncwarp();
+      unsigned char *qdst = smem + OFF_Q + qb * Q_BYTES;
+#pragma unroll
+      for (int i = 0; i < QPL; ++i) {
+        const int j = lane + 32 * i, r = j >> 4, c = j & 15;
+        float f[8];
+        unpack8(cur_a.q[i], f);
+        float a = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) a = fmaxf(a, fabsf(f[e]));
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(kFullMask, a, o));
+        // the query's scale 2^(e - 7), e its largest element's exponent: the
+        // elements keep their bits and the largest lands in [128, 256)
+        const int e = max((int)((__float_as_uint(a) >> 23) & 0xffu) - 127, -119);
+        if (j < 16 * G) {
+          uint2 hi, lo;
+          q_hi_lo(cur_a.q[i], pow2f(7 - e), hi, lo);
+          const int off = (c >> 1) * 128 + (c & 1) * 8;
+          *reinterpret_cast<uint2 *>(qdst + r * 16 + off) = hi;
+          *reinterpret_cast<uint2 *>(qdst + 8 * 128 + r * 16 + off) = lo;
+          if (c == 0) qscale[qb * 8 + r] = pow2f(e - 7);
+        }
+      }
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_ready[qb]);
+    }
+    ++k;
+    const int32_t *trow = p.tables + (size_t)sg.b * p.MB + sg.j0;
+    int tab = cur_a.tab, tab_next = cur_a.tab_next;
+    int tchunk = 0;
+    const int nstages = (sg.n + SB - 1) / SB;
+    for (int st = 0; st < nstages; ++st, ++s) {
+      const int first = st * SB;
+      if ((first >> 5) != tchunk) {
+        tchunk = first >> 5;
+        tab = tab_next;
+        const int j = (tchunk + 1) * 32 + lane;
+        tab_next = (j < sg.n) ? __ldg(trow + j) : 0;
+      }
+      const int nb = min(SB, sg.n - first);
+      const int blk = __shfl_sync(kFullMask, tab, (first & 31) + (lane & (SB - 1)));
+      const bool ok = lane < nb && (unsigned)blk < (unsigned)p.NB;
+      const unsigned okmask = __ballot_sync(kFullMask, ok);
+      const unsigned want = (1u << nb) - 1u;
+      const int slot = s % NS;
+      int go = 1;
+      if (lane == 0) {
+        wait_or_abort(&empty[slot], ((uint32_t)(s / NS) & 1u) ^ 1u, abort_flag, p.err);
+        go = *abort_flag ? 0 : 1;
+      }
+      // (one decision for the warp: after a timeout nothing more is armed)
+      if (!__shfl_sync(kFullMask, go, 0)) {
+        stop = true;
+        break;
+      }
+      if (lane == 0) {
+        if (IS_K) {
+          stage_mask[s & (NSR - 1)] = (int)(want & ~okmask);
+          if (want & ~okmask) atomicOr(p.err, PGD_DEVERR_BAD_BLOCK_ID);
+        }
+        const uint32_t bytes = (uint32_t)__popc(okmask) * TILE;
+        if (bytes == 0)
+          mbar_arrive(&full[slot]);
+        else
+          mbar_arrive_expect_tx(&full[slot], bytes);
+      }
+      __syncwarp();
+      if (ok) {
+        const size_t tile = (size_t)blk * p.n_kv + sg.g;
+        bulk_copy_g2s(ring + (size_t)slot * STAGE + (size_t)lane * TILE, cache + tile * TILE, TILE,
+                      &full[slot], policy);
+        if (IS_K) {
+          const uint32_t dst = sring + (uint32_t)(((s & (NSR - 1)) * 16 + lane) * 4);
+          copy4_async(dst, pp.k_scales + tile);
+          copy4_async(dst + 32, pp.v_scales + tile);
+        }
+      }
+      if (IS_K) arrive_after_copies(&full[slot]);
+    }
+    sg = nsg;
+    cur_a = next_a;
+    have = have_next;
+  }
+  // no copy may still be landing when the CTA exits
+  if (lane == 0) {
+    for (int i = 1; i <= NS && i <= s; ++i) {
+      const int last = s - i;
+      if (!mbar_wait_bounded(&full[last % NS], (uint32_t)(last / NS) & 1u))
+        atomicOr(p.err, PGD_DEVERR_TIMEOUT);
+    }
+  }
+}
+
+template <int G, int BS>
+__global__ void __launch_bounds__(NTHREADS, 1) attention_fp8b_kernel(const Attn8bParams pp) {
+  const AttnParams &p = pp.a;
+  constexpr int SB = TOK / BS;
+  constexpr int NCOL = NP<G>, TSTEP = TS<G>;
+  constexpr int PROW = NCOL;             // bytes of a token's weights
+  constexpr uint32_t PGRP = 8 * PROW;    // bytes of 8 tokens' weights
+  constexpr uint32_t IDESC_QK = instr_desc_e4m3();
+  constexpr uint32_t IDESC_PV = idesc_pv(NCOL);
+
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char *smem = reinterpret_cast<unsigned char *>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + OFF_BAR);
+  uint64_t *full_k = bars;              // [NSK]
+  uint64_t *empty_k = full_k + NSK;     // [NSK]
+  uint64_t *full_v = empty_k + NSK;     // [NSV]
+  uint64_t *empty_v = full_v + NSV;     // [NSV]
+  uint64_t *s_full = empty_v + NSV;     // [NSB]
+  uint64_t *s_free = s_full + NSB;      // [NSB]
+  uint64_t *m_ready = s_free + NSB;     // [NSB]
+  uint64_t *p_full = m_ready + NSB;     // [2]
+  uint64_t *p_free = p_full + 2;        // [2]
+  uint64_t *o_full = p_free + 2;        // [2]
+  uint64_t *o_free = o_full + 2;        // [2]
+  uint64_t *q_ready = o_free + 2;       // [2]
+  uint64_t *q_free = q_ready + 2;       // [2]
+  uint64_t *done = q_free + 2;          // [2]
+  uint64_t *seg_done = done + 2;        // [2]
+  float *red = reinterpret_cast<float *>(smem + OFF_RED);
+  float *lred = reinterpret_cast<float *>(smem + OFF_LRED);
+  float *mref = reinterpret_cast<float *>(smem + OFF_MREF);
+  float *qscale = reinterpret_cast<float *>(smem + OFF_QS);
+  const float *scl = reinterpret_cast<const float *>(smem + OFF_SC);
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + OFF_MISC);
+  volatile int *flag = reinterpret_cast<volatile int *>(smem + OFF_MISC + 8);  // [3]
+  int *nmax_slot = reinterpret_cast<int *>(smem + OFF_MISC + 20);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + OFF_MISC + 24);  // WaitCtl
+  volatile int *stage_mask = reinterpret_cast<volatile int *>(smem + OFF_MISC + 40);  // [NSR]
+  int *over_flag = reinterpret_cast<int *>(smem + OFF_MISC + 112);  // [2][4] softmax votes
+  int *pre = reinterpret_cast<int *>(smem + OFF_PRE);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (!p.wait_late) pdl_wait();
+  // As in attention_kernel.cuh: with no more units than CTAs, CTA c most
+  // likely streams unit c, whose first stages L2 is asked for meanwhile.
+  const bool pf_unit = p.prefetch_units && warp == WARP_KP && (int)blockIdx.x < p.B * p.n_kv;
+  int pf_ctx = 0, pf_blk = -1;
+  if (pf_unit) {
+    const int b = (int)blockIdx.x / p.n_kv;
+    pf_ctx = __ldg(p.ctx + b);
+    if (lane < kPrefetchBlocks<BS> && lane < p.MB) pf_blk = __ldg(p.tables + (size_t)b * p.MB + lane);
+  }
+  if (tid == 0) {
+    for (int i = 0; i < NSK; ++i) {
+      mbar_init(&full_k[i], 1 + 32);  // the producer's arrival and each lane's scale copies
+      mbar_init(&empty_k[i], 1);
+    }
+    for (int i = 0; i < NSV; ++i) {
+      mbar_init(&full_v[i], 1);
+      mbar_init(&empty_v[i], 1);
+    }
+    for (int i = 0; i < NSB; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&s_free[i], 4);
+      mbar_init(&m_ready[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&p_full[i], 4);
+      mbar_init(&p_free[i], 1);
+      mbar_init(&o_full[i], 1);
+      mbar_init(&o_free[i], 4);
+      mbar_init(&done[i], 1);
+      mbar_init(&seg_done[i], 4);
+      mbar_init(&q_ready[i], 1);
+      mbar_init(&q_free[i], 1 + 4);
+    }
+    mbar_init_fence();
+    init_wait_ctl(smem + OFF_MISC + 24, p.wait_limit_ns);
+  }
+  // Query rows and weight columns that belong to no head stay zero.
+  {
+    uint4 *z = reinterpret_cast<uint4 *>(smem + OFF_Q);
+    for (int i = tid; i < (2 * Q_BYTES + 2 * P_BYTES8) / 16; i += NTHREADS)
+      z[i] = make_uint4(0, 0, 0, 0);
+  }
+  const int max_tokens = p.MB * BS;
+  bool bad_ctx = false;
+  for (int b = tid; b < p.B; b += NTHREADS) {
+    const int c = p.ctx[b];
+    int nb = 0;
+    if (c >= 1 && c <= max_tokens) nb = (c + BS - 1) / BS; else bad_ctx = true;
+    pre[b + 1] = nb > 0 ? nb + kSegCost<BS> : 0;
+  }
+  if (bad_ctx && blockIdx.x == 0) atomicOr(p.err, PGD_DEVERR_BAD_CONTEXT);
+  if (warp == WARP_QK) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_addr(tmem_slot)),
+                 "r"(TMEM_COLS)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  fence_proxy_async();
+  __syncthreads();
+  if (pf_unit) {
+    const int g = (int)blockIdx.x % p.n_kv;
+    const int nb = (pf_ctx >= 1 && pf_ctx <= max_tokens) ? (pf_ctx + BS - 1) / BS : 0;
+    if (nb >= 4 * kPrefetchBlocks<BS> && lane < kPrefetchBlocks<BS> &&
+        (unsigned)pf_blk < (unsigned)p.NB) {
+      const size_t off = ((size_t)pf_blk * p.n_kv + g) * (BS * kHeadDim);
+      bulk_prefetch_l2(p.k_cache + off, BS * kHeadDim);
+      bulk_prefetch_l2(p.v_cache + off, BS * kHeadDim);
+    }
+  }
+  if (warp == 0) {
+    int carry = 0, longest = 0;
+    for (int base = 0; base < p.B; base += 32) {
+      const int i = base + lane;
+      int v = (i < p.B) ? pre[i + 1] : 0;
+      longest = max(longest, v);
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int n = __shfl_up_sync(kFullMask, v, o);
+        if (lane >= o) v += n;
+      }
+      if (i < p.B) pre[i + 1] = v + carry;
+      carry += __shfl_sync(kFullMask, v, 31);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) longest = max(longest, __shfl_xor_sync(kFullMask, longest, o));
+    if (lane == 0) {
+      pre[0] = 0;
+      *nmax_slot = longest;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  auto col_o = [&](int ob) { return tmem + 64u + (uint32_t)ob * 32u; };
+
+  // The split: whole units, or balanced cuts (the cost model of
+  // attention_kernel.cuh with this cache's bytes per block).
+  Schedule sc;
+  sc.X = (long long)p.n_kv * pre[p.B];
+  sc.pre = pre;
+  sc.n_kv = p.n_kv;
+  sc.ov = kSegCost<BS>;
+  sc.P = sc.X < (long long)gridDim.x ? sc.X : (long long)gridDim.x;
+  sc.units = false;
+  if (p.auto_split && sc.X > 0) {
+    const long long U = (long long)p.B * p.n_kv, nmax = *nmax_slot;
+    constexpr long long kBlockBytes = 2ll * BS * kHeadDim;
+    constexpr long long m0 = kMergeFixedBytes / kBlockBytes, m1 = kMergePartBytes / kBlockBytes;
+    const long long grid = (long long)gridDim.x;
+    long long P = (long long)sqrtf((float)kShare * (float)sc.X * (float)U / (float)m1);
+    P = max(1ll, min(P, sc.P));
+    const long long cost_cut = max((sc.X + P - 1) / P * kShare, sc.X) + m0 + m1 * ((P + U - 1) / U);
+    sc.P = P;
+    if (U <= grid && max(nmax * kShare, sc.X) <= cost_cut) {
+      sc.units = true;
+      sc.P = U;
+    }
+  }
+
+  if (warp == WARP_KP) {
+    produce<G, BS, true>(pp, sc, smem, full_k, empty_k, stage_mask, qscale, q_ready, q_free,
+                         abort_flag, lane);
+  } else if (warp == WARP_VP) {
+    produce<G, BS, false>(pp, sc, smem, full_v, empty_v, nullptr, nullptr, nullptr, nullptr,
+                          abort_flag, lane);
+  } else if (warp == WARP_QK) {
+    // ---------------------------------------------------- q.k^T issuer
+    if (lane == 0) {
+      const uint32_t q_base = smem_addr(smem + OFF_Q);
+      SegCursor cur(sc);
+      Segment sg;
+      int s = 0, k = 0;
+      while (cur.next(sc, p.B, sg)) {
+        const int nstages = (sg.n + SB - 1) / SB;
+        wait_or_abort(&q_ready[k & 1], (uint32_t)(k >> 1) & 1u, abort_flag, p.err);
+        const uint64_t qd = smem_desc(q_base + (uint32_t)((k & 1) * Q_BYTES), 128, 1024, 0);
+        for (int st = 0; st < nstages; ++st, ++s) {
+          const int slot = s % NSK, sb = s % NSB;
+          wait_or_abort(&full_k[slot], (uint32_t)(s / NSK) & 1u, abort_flag, p.err);
+          wait_or_abort(&s_free[sb], ((uint32_t)(s / NSB) & 1u) ^ 1u, abort_flag, p.err);
+          tc_fence_after();
+          if (!*abort_flag) {
+            // K core matrices 128 B apart along d, token groups 1024 B apart;
+            // a k-step of 32 dims moves K and Q by two core matrices
+            const uint64_t kd = smem_desc(smem_addr(smem + OFF_K + slot * STAGE), 128, GROUP, 0);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              umma_e4m3(tmem + col_s(sb), kd + (uint64_t)(kk * 16), qd + (uint64_t)(kk * 16),
+                        IDESC_QK, kk > 0 ? 1u : 0u);
+          }
+          umma_commit(&s_full[sb]);
+          umma_commit(&empty_k[slot]);
+          // the stage's invalid-block mask and scales, which full_k ordered
+          // before this, for the softmax
+          mbar_arrive(&m_ready[sb]);
+        }
+        umma_commit(&q_free[k & 1]);
+        ++k;
+      }
+      if (s > 0) {
+        umma_commit(&done[0]);
+        mbar_wait_bounded(&done[0], 0);
+      }
+    }
+  } else if (warp == WARP_PV) {
+    // ------------------------------------------------------- p.v issuer
+    if (lane == 0) {
+      SegCursor cur(sc);
+      Segment sg;
+      int s = 0, k = 0;
+      while (cur.next(sc, p.B, sg)) {
+        const int ctx_b = __ldg(p.ctx + sg.b);
+        const int nstages = (sg.n + SB - 1) / SB;
+        const int ob = k & 1;
+        for (int st = 0; st < nstages; ++st, ++s) {
+          const int slot = s % NSV, sb = s & 1;
+          // k-steps of 32 tokens; those past the last token are not issued
+          // (their rows hold no token and were not zeroed)
+          const int nb = min(SB, sg.n - st * SB);
+          int nvalid = nb * BS;
+          if (sg.j0 + st * SB + nb == sg.nblk) nvalid -= sg.nblk * BS - ctx_b;
+          const int nkt = min(4, max(1, (nvalid + 31) >> 5));
+          wait_or_abort(&p_full[sb], (uint32_t)(s >> 1) & 1u, abort_flag, p.err);
+          wait_or_abort(&full_v[slot], (uint32_t)(s / NSV) & 1u, abort_flag, p.err);
+          if (st == 0)
+            wait_or_abort(&o_free[ob], ((uint32_t)(k >> 1) & 1u) ^ 1u, abort_flag, p.err);
+          tc_fence_after();
+          if (!*abort_flag) {
+            // V: dims (M) 128 B apart in chunks of 16, token groups (K)
+            // 1024 B apart; P: columns (N) 128 B apart in chunks of 16, token
+            // groups PGRP apart
+            const uint64_t vd = smem_desc(smem_addr(smem + OFF_V + slot * STAGE), GROUP, 128, 0);
+            const uint64_t pd = smem_desc(smem_addr(smem + OFF_P + sb * P_BYTES8), PGRP, 128, 0);
+#pragma unroll
+            for (int kt = 0; kt < 4; ++kt)
+              if (kt < nkt)
+                umma_e4m3(col_o(ob), vd + (uint64_t)(kt * (4 * GROUP / 16)),
+                          pd + (uint64_t)(kt * (4 * PGRP / 16)), IDESC_PV,
+                          (kt > 0 || st > 0) ? 1u : 0u);
+          }
+          umma_commit(&empty_v[slot]);
+          umma_commit(&p_free[sb]);
+          if (st + 1 == nstages) umma_commit(&o_full[ob]);
+        }
+        ++k;
+      }
+      if (s > 0) {
+        umma_commit(&done[1]);
+        mbar_wait_bounded(&done[1], 0);
+      }
+    }
+  } else if (warp < 4) {
+    // ----------------------------------------------------------- softmax
+    // Two stages an iteration: one maximum, one barrier and one decision to
+    // move the reference for 256 tokens.
+    const int t = tid;
+    const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
+    constexpr int SPI = 2, NCT = 128;
+    SegCursor cur(sc);
+    Segment sg, nsg;
+    int s = 0, k = 0, it = 0;
+    bool have = cur.next(sc, p.B, sg);
+    int ctx_b = have ? __ldg(p.ctx + sg.b) : 0;
+    while (have) {
+      const bool have_next = cur.next(sc, p.B, nsg);
+      const int ctx_n = have_next ? __ldg(p.ctx + nsg.b) : 0;
+      const int nstages = (sg.n + SB - 1) / SB;
+      const int ob = k & 1;
+      float m_ref[G], l_part[G], qsc[G];
+#pragma unroll
+      for (int h = 0; h < G; ++h) { m_ref[h] = -INFINITY; l_part[h] = 0.f; qsc[h] = 0.f; }
+      for (int st = 0; st < nstages; st += SPI, ++it) {
+        const int n2 = min(SPI, nstages - st);
+        bool valid[SPI] = {};
+        int lim[SPI] = {};  // rows p.v reads: the valid length rounded up to 32
+        float ks[SPI] = {}, vs[SPI] = {};
+#pragma unroll
+        for (int u = 0; u < SPI; ++u) {
+          if (u < n2) {
+            const int su = s + u, sbu = su % NSB;
+            wait_or_abort(&s_full[sbu], (uint32_t)(su / NSB) & 1u, abort_flag, p.err);
+            wait_or_abort(&m_ready[sbu], (uint32_t)(su / NSB) & 1u, abort_flag, p.err);
+            const int msk = stage_mask[su & (NSR - 1)];
+            const int nb = min(SB, sg.n - (st + u) * SB);
+            int nvalid = nb * BS;
+            if (sg.j0 + (st + u) * SB + nb == sg.nblk) nvalid -= sg.nblk * BS - ctx_b;
+            valid[u] = (t < nvalid) && !((msk >> (t / BS)) & 1);
+            lim[u] = (nvalid + 31) & ~31;
+            ks[u] = scl[(su & (NSR - 1)) * 16 + t / BS];
+            vs[u] = scl[(su & (NSR - 1)) * 16 + 8 + t / BS];
+          }
+        }
+        tc_fence_after();
+        uint32_t sv[SPI][16];
+#pragma unroll
+        for (int u = 0; u < SPI; ++u)
+          if (u < n2) {
+            const uint32_t a0 = tmem + lane_base + col_s((s + u) % NSB);
+            tmem_ld8_async(a0, sv[u]);
+            tmem_ld8_async(a0 + 8, sv[u] + 8);
+          }
+#pragma unroll
+        for (int u = 0; u < SPI; ++u)
+          if (u < n2) {
+            tmem_wait8(sv[u]);
+            tmem_wait8(sv[u] + 8);
+          }
+        if (st == 0) {
+#pragma unroll
+          for (int h = 0; h < G; ++h) qsc[h] = qscale[(k & 1) * 8 + h] * p.qk_scale_log2;
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&s_free[s % NSB]);
+          if (n2 > 1) mbar_arrive(&s_free[(s + 1) % NSB]);
+          if (st == 0) mbar_arrive(&q_free[k & 1]);
+        }
+        // scores in log2 units, and with the V scale's logarithm the weights
+        // that the reference bounds
+        float w[SPI][G], lv[SPI];
+#pragma unroll
+        for (int u = 0; u < SPI; ++u) {
+          lv[u] = __log2f(fmaxf(vs[u], 7.5e-37f));  // (2^-120: finite whatever the ring holds)
+#pragma unroll
+          for (int h = 0; h < G; ++h)
+            w[u][h] = valid[u] ? (__uint_as_float(sv[u][h]) + __uint_as_float(sv[u][8 + h])) *
+                                     (qsc[h] * ks[u])
+                               : -INFINITY;
+        }
+        // (a row that is not valid has w = -inf)
+        auto top = [&](int h) { return fmaxf(w[0][h] + lv[0], w[1][h] + lv[1]); };
+        const int rb = it & 1;
+        bool move = true;  // (a segment's first iteration always sets it)
+        if (st > 0) {
+          bool over = false;
+#pragma unroll
+          for (int h = 0; h < G; ++h) over |= top(h) > m_ref[h] + kMoveLog2;
+          const bool wover = __any_sync(kFullMask, over);
+          if (lane == 0) over_flag[rb * 4 + warp] = wover ? 1 : 0;
+          named_barrier_sync(1, NCT);
+          const int4 votes = *reinterpret_cast<const int4 *>(over_flag + rb * 4);
+          move = (votes.x | votes.y | votes.z | votes.w) != 0;
+        }
+        if (move) {
+          float v2[G];
+#pragma unroll
+          for (int h = 0; h < G; ++h) v2[h] = top(h);
+          const float wm = warp_reduce_heads<G, true>(v2, lane);
+          constexpr int SH = 5 - kLog2<G>;
+          if ((lane & ((1 << SH) - 1)) == 0) red[(rb * 4 + warp) * 8 + (lane >> SH)] = wm;
+          named_barrier_sync(1, NCT);
+          float alpha[TSTEP];
+#pragma unroll
+          for (int h = 0; h < TSTEP; ++h) alpha[h] = 1.f;
+#pragma unroll
+          for (int h = 0; h < G; ++h) {
+            const float tm = fmaxf(fmaxf(red[(rb * 4 + 0) * 8 + h], red[(rb * 4 + 1) * 8 + h]),
+                                   fmaxf(red[(rb * 4 + 2) * 8 + h], red[(rb * 4 + 3) * 8 + h]));
+            const float mn = fmaxf(m_ref[h], tm);
+            alpha[h] = (m_ref[h] == -INFINITY) ? 0.f : exp2f(m_ref[h] - mn);
+            m_ref[h] = mn;
+            l_part[h] *= alpha[h];
+          }
+          if (st > 0) {
+            wait_or_abort(&p_free[(s - 1) & 1], (uint32_t)((s - 1) >> 1) & 1u, abort_flag, p.err);
+            tc_fence_after();
+#pragma unroll
+            for (int c8 = 0; c8 < NCOL / 8; ++c8) {
+              float ov[8];
+              tmem_ld8(col_o(ob) + lane_base + 8 * c8, ov);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) ov[i] *= alpha[(8 * c8 + i) % TSTEP];
+              tmem_st8(col_o(ob) + lane_base + 8 * c8, ov);
+            }
+            tc_fence_before();
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < SPI; ++u) {
+          if (u < n2) {
+            const int su = s + u, pbuf = su & 1;
+            // A weight's three terms: hi, lo, lo2 (bytes h of three words
+            // groups).  Two heads a conversion.
+            constexpr int HP = G == 1 ? 2 : G;
+            uint32_t word[3][(TSTEP + 3) / 4];
+#pragma unroll
+            for (int i = 0; i < 3; ++i)
+#pragma unroll
+              for (int j = 0; j < (TSTEP + 3) / 4; ++j) word[i][j] = 0;
+            const float unit = valid[u] ? vs[u] * kWeightUnit : 0.f;
+#pragma unroll
+            for (int h = 0; h < HP; h += 2) {
+              float x0 = 0.f, x1 = 0.f;
+              if (valid[u]) {
+                const float p0 = exp2_approx(w[u][h] - m_ref[h]);
+                l_part[h] += p0;
+                x0 = p0 * unit;
+                if (h + 1 < G) {
+                  const float p1 = exp2_approx(w[u][h + 1 < G ? h + 1 : h] -
+                                               m_ref[h + 1 < G ? h + 1 : h]);
+                  l_part[h + 1 < G ? h + 1 : h] += p1;
+                  x1 = p1 * unit;
+                }
+              }
+#pragma unroll
+              for (int i = 0; i < 3; ++i) {
+                const uint16_t c = e4m3x2(x0, x1);
+                word[i][h >> 2] |= (uint32_t)c << ((h & 2) * 8);
+                if (i < 2) {
+                  const float2 back = e4m3x2_to_float2(c);
+                  x0 = (x0 - back.x) * kTerm;
+                  x1 = (x1 - back.y) * kTerm;
+                }
+              }
+            }
+            wait_or_abort(&p_free[pbuf], ((uint32_t)(su >> 1) & 1u) ^ 1u, abort_flag, p.err);
+            unsigned char *dst = smem + OFF_P + pbuf * P_BYTES8 + (t >> 3) * PGRP + (t & 7) * 16;
+            if constexpr (TSTEP == 4) {
+              *reinterpret_cast<uint4 *>(dst) = make_uint4(word[0][0], word[1][0], word[2][0], 0);
+            } else {
+              *reinterpret_cast<uint4 *>(dst) =
+                  make_uint4(word[0][0], word[0][1], word[1][0], word[1][1]);
+              *reinterpret_cast<uint4 *>(dst + 128) = make_uint4(word[2][0], word[2][1], 0, 0);
+            }
+            if (!valid[u] && t < lim[u]) {
+              // rows that p.v reads but that hold no token (the tail of the
+              // last block, a block whose id was bad): their codes may be NaN
+              const int vslot = su % NSV;
+              wait_or_abort(&full_v[vslot], (uint32_t)(su / NSV) & 1u, abort_flag, p.err);
+              uint4 *vrow = reinterpret_cast<uint4 *>(smem + OFF_V + vslot * STAGE +
+                                                      (t >> 3) * GROUP + (t & 7) * 16);
+#pragma unroll
+              for (int c = 0; c < 8; ++c) vrow[c * 8] = make_uint4(0, 0, 0, 0);
+            }
+          }
+        }
+        fence_proxy_async();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&p_full[s & 1]);
+          if (n2 > 1) mbar_arrive(&p_full[(s + 1) & 1]);
+        }
+        s += n2;
+      }
+      // the segment's references and per-warp sums, for the epilogue
+      wait_or_abort(&o_free[ob], ((uint32_t)(k >> 1) & 1u) ^ 1u, abort_flag, p.err);
+      {
+        const float ws = warp_reduce_heads<G, false>(l_part, lane);
+        constexpr int SH = 5 - kLog2<G>;
+        if ((lane & ((1 << SH) - 1)) == 0) lred[(ob * 4 + warp) * 8 + (lane >> SH)] = ws;
+      }
+      if (t == 0) {
+#pragma unroll
+        for (int h = 0; h < G; ++h) mref[ob * 8 + h] = m_ref[h];
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&seg_done[ob]);
+      ++k;
+      sg = nsg;
+      ctx_b = ctx_n;
+      have = have_next;
+    }
+  } else if (warp >= WARP_EPI) {
+    // ---------------------------------------------------------- epilogue
+    const int e = tid - 32 * WARP_EPI;  // head-dim row of O
+    const int ew = warp - WARP_EPI;
+    const uint32_t lane_base = (uint32_t)(ew * 32) << 16;
+    constexpr int NET = 128;
+    SegCursor cur(sc);
+    Segment sg;
+    const int part = (int)blockIdx.x;
+    int k = 0;
+    while (cur.next(sc, p.B, sg)) {
+      const int ob = k & 1;
+      const int unit = sg.b * p.n_kv + sg.g;
+      wait_or_abort(&seg_done[ob], (uint32_t)(k >> 1) & 1u, abort_flag, p.err);
+      float Lsum[G], M[G];
+#pragma unroll
+      for (int h = 0; h < G; ++h) {
+        Lsum[h] = (lred[(ob * 4 + 0) * 8 + h] + lred[(ob * 4 + 1) * 8 + h]) +
+                  (lred[(ob * 4 + 2) * 8 + h] + lred[(ob * 4 + 3) * 8 + h]);
+        M[h] = mref[ob * 8 + h];
+      }
+      wait_or_abort(&o_full[ob], (uint32_t)(k >> 1) & 1u, abort_flag, p.err);
+      tc_fence_after();
+      float o[NCOL];
+#pragma unroll
+      for (int c8 = 0; c8 < 3 * TSTEP / 8 + (TSTEP == 4 ? 1 : 0); ++c8)
+        tmem_ld8(col_o(ob) + lane_base + 8 * c8, *reinterpret_cast<float(*)[8]>(o + 8 * c8));
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&o_free[ob]);
+      float ov[G];
+#pragma unroll
+      for (int h = 0; h < G; ++h)
+        ov[h] = fmaf(fmaf(o[2 * TSTEP + h], 1.f / kTerm, o[TSTEP + h]), 1.f / kTerm, o[h]) *
+                (1.f / kWeightUnit);
+
+      const bool whole = sg.j0 == 0 && sg.n == sg.nblk;
+      const long long c_first = sc.units ? (long long)part : sc.part_of(sg.ucs + sc.ov);
+      const long long c_last = sc.units ? (long long)part : sc.part_of(sg.uce - 1);
+      const size_t obase = q_index(p, sg.b, sg.g, 0);
+      if (whole) {
+#pragma unroll
+        for (int h = 0; h < G; ++h)
+          p.out[(obase + h) * kHeadDim + e] = __float2bfloat16_rn(ov[h] / Lsum[h]);
+      } else {
+        const size_t srow = ((size_t)unit + (size_t)part) * G;
+#pragma unroll
+        for (int h = 0; h < G; ++h) p.part_o[(srow + h) * kHeadDim + e] = ov[h];
+#pragma unroll
+        for (int h = 0; h < G; ++h)
+          if (e == h)
+            *reinterpret_cast<float2 *>(p.part_ml + (srow + h) * 2) = make_float2(M[h], Lsum[h]);
+        // publish this part; the last of the unit's parts to arrive merges
+        named_barrier_sync(2, NET);
+        if (e == 0) {
+          const int n_parts = (int)(c_last - c_first + 1);
+          const int before = atomic_add_acq_rel_gpu(p.counters + unit, 1);
+          const int last = (before == n_parts - 1);
+          if (last) atomicExch(p.counters + unit, 0);
+          flag[0] = last;
+          flag[1] = (int)c_first;
+          flag[2] = n_parts;
+        }
+        named_barrier_sync(2, NET);
+        if (flag[0])
+          merge_parts<G, false>(p.part_o, p.part_ml, p.out, unit, flag[1], flag[2], obase, p.lg_gh,
+                                p.n_q, G, e, reinterpret_cast<float2 *>(smem + OFF_MERGE));
+        named_barrier_sync(2, NET);
+      }
+      ++k;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == WARP_QK) {
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                 "r"(TMEM_COLS)
+                 : "memory");
+  }
+}
+
+template <int G, int BS>
+cudaError_t launch_cfg(const Attn8bParams &p, int grid, cudaStream_t stream) {
+  static volatile int done[64] = {0};  // shared-memory limit raised, per device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64 || !done[dev]) {
+    e = cudaFuncSetAttribute(attention_fp8b_kernel<G, BS>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)smem_size(PGD_MAX_BATCH));
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) done[dev] = 1;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(NTHREADS);
+  cfg.dynamicSmemBytes = smem_size(p.a.B);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attention_fp8b_kernel<G, BS>, p);
+}
+
+}  // namespace tc8b
+
+cudaError_t attention_fp8b_launch(const Attn8bParams &p, int G, int bs, int grid,
+                                  cudaStream_t stream) {
+#define PGD_CASE(G_, BS_) \
+  if (G == G_ && bs == BS_) return tc8b::launch_cfg<G_, BS_>(p, grid, stream);
+  PGD_CASE(1, 16) PGD_CASE(2, 16) PGD_CASE(4, 16) PGD_CASE(8, 16)
+  PGD_CASE(1, 32) PGD_CASE(2, 32) PGD_CASE(4, 32) PGD_CASE(8, 32)
+#undef PGD_CASE
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace pgd

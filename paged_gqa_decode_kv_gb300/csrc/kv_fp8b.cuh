@@ -101,6 +101,8 @@ struct Attn8bParams {
   const float *k_scales;
   const float *v_scales;
 };
+cudaError_t attention_fp8b_launch(const Attn8bParams &p, int G, int bs, int grid,
+                                  cudaStream_t stream);
 cudaError_t cluster_attention_fp8b_launch(const Attn8bParams &p, int G, int bs,
                                           cudaStream_t stream);
 
