@@ -194,8 +194,11 @@ cudaError_t launch_pdl(K kernel, dim3 grid, int threads, size_t smem, cudaStream
 }
 
 // ------------------------------------------------------------------ selection
-constexpr int kSelThreads = 256;
+constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kMaxCluster = 16;
+constexpr int kSliceKeys = 10240;  // keys of a CTA's slice (40 KiB)
+constexpr int kUnroll = 4;  // blocks that a group of eight lanes has in flight
 
 // A float's bits as an unsigned integer of the same order.
 __device__ __forceinline__ uint32_t order_key(float f) {
@@ -203,49 +206,89 @@ __device__ __forceinline__ uint32_t order_key(float f) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// One CTA per (sequence, KV head).  Eight lanes score a block: lane i holds
-// dims 16 i .. + 15 of both bounds (two 16-byte loads) and of the G rounded
-// queries (positive and negative parts), four products of int8 per
-// instruction.  The keys of the scores stay in shared memory; the W-th
-// largest is found digit by digit (8 bits a pass, histogram of the keys that
-// share the digits so far), then the selected blocks are written in order.
+// Barrier over the cluster's CTAs (shared-memory writes before it are visible
+// to the peers' reads behind it), or over the one CTA.
+__device__ __forceinline__ void sync_all(int C) {
+  if (C > 1)
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
+                 "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  else
+    __syncthreads();
+}
+// A word of CTA `rank`'s shared memory, at the place `local` has in ours.
+__device__ __forceinline__ uint32_t ld_peer(const uint32_t *local, int rank, int C) {
+  if (C == 1) return *local;
+  uint32_t remote, v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+               : "=r"(remote)
+               : "r"(smem_addr(local)), "r"(rank));
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(remote) : "memory");
+  return v;
+}
+
+// One cluster of C CTAs per (sequence, KV head), each CTA a contiguous slice
+// of the blocks.
+// 1. Scores.  Eight lanes take a block: lane i holds dims 16 i .. + 15 of both
+//    bounds (two 16-byte loads; a block's 256 bytes are two full lines) and of
+//    the rounded queries' positive and negative parts, four int8 products an
+//    instruction; a group has kUnroll blocks in flight.  The heads' sums are
+//    reduced over the eight lanes by halves (a lane keeps one half of the
+//    heads and sends the other).
+// 2. The least selected score, by 256-way refinement of the range [least,
+//    largest] of the unforced keys: every CTA histograms its keys in the
+//    range, adds up all CTAs' histograms through distributed shared memory and
+//    keeps the bin that holds the wanted rank, until the bin is one value or
+//    all its keys are wanted.  (Starting from the range rather than from the
+//    keys' top byte, which is all but constant for scores of one query, saves
+//    a pass and the contention on one bin.)
+// 3. Every warp counts, then writes, its own part of the slice in order.
 template <int G>
-__global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams p) {
-  extern __shared__ uint32_t keys[];  // [MB]
-  __shared__ uint32_t hist[256];
-  __shared__ int warp_sum[2][kSelWarps];
-  __shared__ int digit_out[2];
+__global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams p, int C) {
+  extern __shared__ uint32_t keys[];  // a slice: block ids, then keys
+  __shared__ uint32_t hist[3][256];   // a pass adds in one, zeroes the next's and leaves the
+                                      // last's to peers that may still be reading it
+  __shared__ uint32_t range[2];       // largest of ~key, largest key: unforced ones
+  __shared__ uint32_t counts[2];      // this CTA's keys above the least, and equal to it
+  __shared__ int warp_cnt[2][kSelWarps];
+  __shared__ int found[3];
   __shared__ __align__(16) signed char qpos[G][kHeadDim], qneg[G][kHeadDim];
   __shared__ float qf[G];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int b = blockIdx.x / p.n_kv, g = blockIdx.x % p.n_kv;
+  const int unit = (int)blockIdx.x / C, rank = (int)blockIdx.x % C;
+  const int b = unit / p.n_kv, g = unit % p.n_kv;
   pdl_wait();
   pdl_launch_dependents();
   const int ctx = __ldg(p.ctx + b);
+  uint2 raw = make_uint2(0, 0);
+  if (warp < G)
+    raw = __ldg(reinterpret_cast<const uint2 *>(
+                    p.q + ((size_t)b * p.n_q + g * G + warp) * kHeadDim) + lane);
   const int W = p.W;
-  int32_t *tiles = p.tiles + (size_t)blockIdx.x * W;
+  int32_t *tiles = p.tiles + (size_t)unit * W;
   const int32_t *row = p.tables + (size_t)b * p.MB;
+  const int nthr = C * kSelThreads, me = rank * kSelThreads + tid;
   if (ctx < 1 || ctx > p.MB * p.bs) {
-    if (tid == 0 && g == 0) atomicOr(p.err, PGD_DEVERR_BAD_CONTEXT);
-    for (int i = tid; i < W; i += kSelThreads) tiles[i] = -1;
-    if (tid == 0) p.lens[blockIdx.x] = 0;
+    if (me == 0) {
+      if (g == 0) atomicOr(p.err, PGD_DEVERR_BAD_CONTEXT);
+      p.lens[unit] = 0;
+    }
+    for (int i = me; i < W; i += nthr) tiles[i] = -1;
     return;
   }
   const int nblk = (ctx + p.bs - 1) / p.bs;
-  const int tail = ctx - (nblk - 1) * p.bs;
-  if (tid == 0) p.lens[blockIdx.x] = (min(nblk, W) - 1) * p.bs + tail;
-  auto tile_of = [&](int j) {
-    const int blk = __ldg(row + j);
-    return (unsigned)blk < (unsigned)p.NB ? blk * p.n_kv + g : -1;
-  };
+  if (me == 0) p.lens[unit] = (min(nblk, W) - 1) * p.bs + ctx - (nblk - 1) * p.bs;
+  auto tile_of = [&](int blk) { return (unsigned)blk < (unsigned)p.NB ? blk * p.n_kv + g : -1; };
   if (nblk <= W) {  // everything is selected
-    for (int i = tid; i < W; i += kSelThreads) tiles[i] = i < nblk ? tile_of(i) : -1;
+    for (int i = me; i < W; i += nthr) tiles[i] = i < nblk ? tile_of(__ldg(row + i)) : -1;
     return;
   }
-  // The rounded queries: warp h takes head h (8 heads at most).
+  const int per = (nblk + C - 1) / C;
+  const int jlo = min(nblk, rank * per), n = min(nblk, jlo + per) - jlo;
+  for (int i = tid; i < n; i += kSelThreads) keys[i] = (uint32_t)__ldg(row + jlo + i);
+  if (tid < 256) hist[0][tid] = 0;
+  if (tid < 2) range[tid] = 0;
+  // The rounded queries: warp h takes head h.
   if (warp < G) {
-    const uint2 raw = __ldg(reinterpret_cast<const uint2 *>(
-        p.q + ((size_t)b * p.n_q + g * G + warp) * kHeadDim) + lane);
     float f[4];
     unpack4(raw, f);
     float a = fmaxf(fmaxf(fabsf(f[0]), fabsf(f[1])), fmaxf(fabsf(f[2]), fabsf(f[3])));
@@ -256,9 +299,9 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
     uint32_t wp = 0, wn = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int n = max(-127, min(127, __float2int_rn(f[i] * inv)));
-      wp |= (uint32_t)(max(n, 0) & 0xff) << (8 * i);
-      wn |= (uint32_t)(min(n, 0) & 0xff) << (8 * i);
+      const int v = max(-127, min(127, __float2int_rn(f[i] * inv)));
+      wp |= (uint32_t)(max(v, 0) & 0xff) << (8 * i);
+      wn |= (uint32_t)(min(v, 0) & 0xff) << (8 * i);
     }
     reinterpret_cast<uint32_t *>(qpos[warp])[lane] = wp;
     reinterpret_cast<uint32_t *>(qneg[warp])[lane] = wn;
@@ -268,109 +311,198 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
   {
     const int i8 = lane & 7;
     uint4 qp[G], qn[G];
-    float f[G];
 #pragma unroll
     for (int h = 0; h < G; ++h) {
       qp[h] = *reinterpret_cast<const uint4 *>(&qpos[h][16 * i8]);
       qn[h] = *reinterpret_cast<const uint4 *>(&qneg[h][16 * i8]);
-      f[h] = qf[h];
     }
-    for (int j0 = 0; j0 < nblk; j0 += kSelThreads / 8) {
-      const int j = j0 + (tid >> 3);
-      int blk = -1;
-      if (j < nblk) blk = __ldg(row + j);
-      const bool there = (unsigned)blk < (unsigned)p.NB;
-      const size_t tile = there ? (size_t)blk * p.n_kv + g : 0;
-      uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
-      float s = 0.f;
-      if (there) {
-        const uint4 *src = reinterpret_cast<const uint4 *>(p.bounds + tile * (2 * kHeadDim));
-        lo = __ldg(src + i8);
-        hi = __ldg(src + 8 + i8);
-        s = __ldg(p.bound_scales + tile);
-      }
-      float best = -__int_as_float(0x7f800000);
+    // after the reduction by halves lane i8 holds head i8 / (8 / G)
+    const float f = qf[i8 / (8 / G)];
+    uint32_t kmin = 0xffffffffu, kmax = 0;
+    constexpr int kGroups = kSelThreads / 8;
+    for (int i0 = 0; i0 < n; i0 += kGroups * kUnroll) {
+      uint4 lo[kUnroll], hi[kUnroll];
+      float s[kUnroll];
+      bool there[kUnroll];
 #pragma unroll
-      for (int h = 0; h < G; ++h) {
-        int d = 0;
-        d = __dp4a((int)hi.x, (int)qp[h].x, d); d = __dp4a((int)hi.y, (int)qp[h].y, d);
-        d = __dp4a((int)hi.z, (int)qp[h].z, d); d = __dp4a((int)hi.w, (int)qp[h].w, d);
-        d = __dp4a((int)lo.x, (int)qn[h].x, d); d = __dp4a((int)lo.y, (int)qn[h].y, d);
-        d = __dp4a((int)lo.z, (int)qn[h].z, d); d = __dp4a((int)lo.w, (int)qn[h].w, d);
-        d += __shfl_xor_sync(kFullMask, d, 1);
-        d += __shfl_xor_sync(kFullMask, d, 2);
-        d += __shfl_xor_sync(kFullMask, d, 4);
-        best = fmaxf(best, (float)d * f[h]);
+      for (int u = 0; u < kUnroll; ++u) {
+        const int i = i0 + u * kGroups + (tid >> 3);
+        const uint32_t blk = i < n ? keys[i] : 0xffffffffu;
+        there[u] = blk < (uint32_t)p.NB;
+        lo[u] = hi[u] = make_uint4(0, 0, 0, 0);
+        s[u] = 0.f;
+        if (there[u]) {
+          const size_t tile = (size_t)blk * p.n_kv + g;
+          const uint4 *src = reinterpret_cast<const uint4 *>(p.bounds + tile * (2 * kHeadDim));
+          lo[u] = __ldg(src + i8);
+          hi[u] = __ldg(src + 8 + i8);
+          s[u] = __ldg(p.bound_scales + tile);
+        }
       }
-      if (i8 == 0 && j < nblk) {
-        const bool kept = j < p.keep_first || j >= nblk - p.keep_last;
-        keys[j] = kept ? 0xffffffffu : there ? order_key(best * s) : 0u;
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        int d[G];
+#pragma unroll
+        for (int h = 0; h < G; ++h) {
+          int x = 0;
+          x = __dp4a((int)hi[u].x, (int)qp[h].x, x); x = __dp4a((int)hi[u].y, (int)qp[h].y, x);
+          x = __dp4a((int)hi[u].z, (int)qp[h].z, x); x = __dp4a((int)hi[u].w, (int)qp[h].w, x);
+          x = __dp4a((int)lo[u].x, (int)qn[h].x, x); x = __dp4a((int)lo[u].y, (int)qn[h].y, x);
+          x = __dp4a((int)lo[u].z, (int)qn[h].z, x); x = __dp4a((int)lo[u].w, (int)qn[h].w, x);
+          d[h] = x;
+        }
+        int off = 4;
+#pragma unroll
+        for (int m = G; m > 1; m >>= 1, off >>= 1) {
+          const bool up = (i8 & off) != 0;
+#pragma unroll
+          for (int h = 0; h < m / 2; ++h) {
+            const int keep = up ? d[h + m / 2] : d[h], send = up ? d[h] : d[h + m / 2];
+            d[h] = keep + __shfl_xor_sync(kFullMask, send, off);
+          }
+        }
+#pragma unroll
+        for (int o = 4 / G; o > 0; o >>= 1) d[0] += __shfl_xor_sync(kFullMask, d[0], o);
+        float best = (float)d[0] * f;
+#pragma unroll
+        for (int o = 4; o > 4 / G && o > 0; o >>= 1)
+          best = fmaxf(best, __shfl_xor_sync(kFullMask, best, o));
+        const int i = i0 + u * kGroups + (tid >> 3);
+        if (i < n) {
+          const int j = jlo + i;
+          const bool forced = j < p.keep_first || j >= nblk - p.keep_last;
+          const uint32_t key = forced ? 0xffffffffu : there[u] ? order_key(best * s[u]) : 0u;
+          if (!forced) {
+            kmin = min(kmin, key);
+            kmax = max(kmax, key);
+          }
+          if (i8 == 0) keys[i] = key;
+        }
       }
+    }
+    kmin = __reduce_min_sync(kFullMask, kmin);
+    kmax = __reduce_max_sync(kFullMask, kmax);
+    if (lane == 0) {
+      atomicMax(&range[0], ~kmin);
+      atomicMax(&range[1], kmax);
     }
   }
-  // The W-th largest key, 8 bits at a time from the top; `need` of the keys
-  // equal to the prefix so far remain to be taken.
-  uint32_t prefix = 0;
-  int need = W;
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    __syncthreads();
-    hist[tid] = 0;  // (256 threads, 256 bins)
-    __syncthreads();
-    for (int j = tid; j < nblk; j += kSelThreads) {
-      const uint32_t k = keys[j];
-      if (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8)))
-        atomicAdd(&hist[(k >> shift) & 255u], 1u);
+  sync_all(C);
+  // `need` of the unforced keys in [lo, hi] remain to be taken, largest first
+  // (there are more unforced blocks than that).
+  uint32_t lo = 0, hi = 0;
+  for (int r = 0; r < C; ++r) {
+    lo = max(lo, ld_peer(&range[0], r, C));
+    hi = max(hi, ld_peer(&range[1], r, C));
+  }
+  lo = ~lo;
+  int need = W - p.keep_first - p.keep_last;
+  bool all = false;  // every key of [lo, hi] is wanted
+  for (int pass = 0; need > 0 && !all && lo != hi; ++pass) {
+    uint32_t *h = hist[pass % 3];
+    const int shift = max(0, 24 - __clz(hi - lo));
+    for (int i = tid; i < n; i += kSelThreads) {
+      const uint32_t k = keys[i];
+      const int j = jlo + i;
+      if (k >= lo && k <= hi && j >= p.keep_first && j < nblk - p.keep_last)
+        atomicAdd(&h[(k - lo) >> shift], 1u);
     }
-    __syncthreads();
-    // count of keys in bins above this thread's: suffix sums
+    if (tid < 256) hist[(pass + 1) % 3][tid] = 0;
+    sync_all(C);
     const int bin = 255 - tid;
-    int n = (int)hist[bin], sum = n;
+    int cnt = 0, sum = 0;
+    if (tid < 256) {
+      for (int r = 0; r < C; ++r) cnt += (int)ld_peer(&h[bin], r, C);
+      sum = cnt;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(kFullMask, sum, o);
-      if (lane >= o) sum += v;
-    }
-    if (lane == 31) warp_sum[0][warp] = sum;
-    __syncthreads();
-    for (int w = 0; w < warp; ++w) sum += warp_sum[0][w];
-    if (sum >= need && sum - n < need) {
-      digit_out[0] = bin;
-      digit_out[1] = need - (sum - n);
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(kFullMask, sum, o);
+        if (lane >= o) sum += v;
+      }
+      if (lane == 31) warp_cnt[0][warp] = sum;
     }
     __syncthreads();
-    prefix |= (uint32_t)digit_out[0] << shift;
-    need = digit_out[1];
+    if (tid < 256) {
+      for (int w = 0; w < warp; ++w) sum += warp_cnt[0][w];
+      if (sum >= need && sum - cnt < need) {  // this bin holds the need-th largest
+        found[0] = bin;
+        found[1] = need - (sum - cnt);
+        found[2] = cnt;
+      }
+    }
+    __syncthreads();
+    need = found[1];
+    all = found[2] == need;
+    lo += (uint32_t)found[0] << shift;
+    hi = min(hi, lo + ((1u << shift) - 1u));
   }
-  // All keys above the prefix, and the first `need` equal to it, in order.
-  int taken = 0, ties = 0;
-  for (int j0 = 0; j0 < nblk; j0 += kSelThreads) {
-    const int j = j0 + tid;
-    const uint32_t k = j < nblk ? keys[j] : 0u;
-    const bool tie = j < nblk && k == prefix;
-    const unsigned tb = __ballot_sync(kFullMask, tie);
-    __syncthreads();
-    if (lane == 0) warp_sum[0][warp] = __popc(tb);
-    __syncthreads();
-    int tpos = ties + __popc(tb & ((1u << lane) - 1u));
-    int all = 0;
+  // Above: forced, or a key above hi, or in [lo, hi] where all are wanted.
+  // Equal: the rest of [lo, hi], one value, the first `need` of which are taken.
+  if (need == 0) {
+    hi = 0xffffffffu;  // (nothing but the forced blocks)
+    lo = 0xffffffffu;
+  }
+  if (all) need = 0;
+  auto above = [&](int i) {
+    const int j = jlo + i;
+    if (j < p.keep_first || j >= nblk - p.keep_last) return true;
+    return all ? keys[i] >= lo : keys[i] > hi;
+  };
+  auto equal = [&](int i) {
+    const int j = jlo + i;
+    return !all && need > 0 && j >= p.keep_first && j < nblk - p.keep_last && keys[i] >= lo &&
+           keys[i] <= hi;
+  };
+  const int pw = (n + kSelWarps - 1) / kSelWarps;
+  const int w0 = min(n, warp * pw), w1 = min(n, w0 + pw);
+  int n_above = 0, n_equal = 0;
+  for (int i0 = w0; i0 < w1; i0 += 32) {
+    const int i = i0 + lane;
+    const bool in = i < w1;
+    n_above += __popc(__ballot_sync(kFullMask, in && above(i)));
+    n_equal += __popc(__ballot_sync(kFullMask, in && equal(i)));
+  }
+  __syncthreads();  // (warp_cnt was read by the last pass)
+  if (lane == 0) {
+    warp_cnt[0][warp] = n_above;
+    warp_cnt[1][warp] = n_equal;
+  }
+  __syncthreads();
+  if (tid == 0) {
+    int a = 0, e = 0;
     for (int w = 0; w < kSelWarps; ++w) {
-      if (w < warp) tpos += warp_sum[0][w];
-      all += warp_sum[0][w];
+      a += warp_cnt[0][w];
+      e += warp_cnt[1][w];
     }
-    ties += all;
-    const bool sel = j < nblk && (k > prefix || (tie && tpos < need));
+    counts[0] = (uint32_t)a;
+    counts[1] = (uint32_t)e;
+  }
+  sync_all(C);
+  int at = 0, left = need;  // next output place, equal keys still to be taken
+  for (int r = 0; r < rank; ++r) {
+    const int a = (int)ld_peer(&counts[0], r, C), e = (int)ld_peer(&counts[1], r, C);
+    const int take = min(e, left);
+    at += a + take;
+    left -= take;
+  }
+  for (int w = 0; w < warp; ++w) {
+    const int take = min(warp_cnt[1][w], left);
+    at += warp_cnt[0][w] + take;
+    left -= take;
+  }
+  for (int i0 = w0; i0 < w1; i0 += 32) {
+    const int i = i0 + lane;
+    const bool in = i < w1;
+    const bool a = in && above(i), e = in && equal(i);
+    const unsigned below = (1u << lane) - 1u;
+    const unsigned eb = __ballot_sync(kFullMask, e);
+    const bool sel = a || (e && __popc(eb & below) < left);
     const unsigned sb = __ballot_sync(kFullMask, sel);
-    if (lane == 0) warp_sum[1][warp] = __popc(sb);
-    __syncthreads();
-    int spos = taken + __popc(sb & ((1u << lane) - 1u));
-    all = 0;
-    for (int w = 0; w < kSelWarps; ++w) {
-      if (w < warp) spos += warp_sum[1][w];
-      all += warp_sum[1][w];
-    }
-    taken += all;
-    if (sel) tiles[spos] = tile_of(j);
+    if (sel) tiles[at + __popc(sb & below)] = tile_of(__ldg(row + jlo + i));
+    at += __popc(sb);
+    left -= min(left, __popc(eb));
   }
+  if (C > 1) sync_all(C);  // peers may still be reading this CTA's counts
 }
 
 }  // namespace
@@ -390,20 +522,42 @@ cudaError_t block_bounds_launch(const BoundsParams &p, cudaStream_t stream) {
                     : launch_pdl(bounds_kernel<32, false>, gd, nt, 0, stream, p, JM);
 }
 
-// Blocks of a sequence that the selection holds keys for (192 KiB of them).
-int select_max_blocks() { return 49152; }
+// Blocks of a sequence that the selection holds keys for.
+int select_max_blocks() { return kMaxCluster * kSliceKeys; }
+
+// CTAs per (sequence, KV head): as many as fill the GPU once, but no more than
+// leave each 128 blocks (fewer are not worth the cluster barriers), and at
+// least as many as hold the keys.
+static int select_cluster(int units, int MB) {
+  int C = 1;
+  while (C < kMaxCluster && ((units * C * 2 <= 152 && MB >= C * 2 * 128) || MB > C * kSliceKeys)) C *= 2;
+  return C;
+}
 
 cudaError_t select_blocks_launch(const SelectParams &p, int G, cudaStream_t stream) {
   if (p.B == 0) return cudaSuccess;
-  const dim3 grid((unsigned)(p.B * p.n_kv));
-  const size_t smem = (size_t)p.MB * 4;
+  const int units = p.B * p.n_kv, C = select_cluster(units, p.MB);
   auto go = [&](auto kernel) {
-    if (smem > 40 * 1024) {
-      const cudaError_t e = cudaFuncSetAttribute(
-          kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, select_max_blocks() * 4);
+    if (C > 8) {
+      const cudaError_t e =
+          cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
       if (e != cudaSuccess) return e;
     }
-    return launch_pdl(kernel, grid, kSelThreads, smem, stream, p);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(units * C));
+    cfg.blockDim = dim3(kSelThreads);
+    cfg.dynamicSmemBytes = (size_t)((p.MB + C - 1) / C) * 4;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)C;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, p, C);
   };
   switch (G) {
     case 1: return go(select_kernel<1>);
