@@ -666,48 +666,84 @@ def append_decode_attention_fp8(out, q, k_new, v_new, k_cache, v_cache, block_ta
 
 
 # ------------------------------------------------- block-scaled 8-bit KV cache
-def _here(**tensors) -> None:
-    """Every given tensor on the current CUDA device (whose stream the call
-    is enqueued on)."""
-    dev = torch.cuda.current_device()
-    for name, t in tensors.items():
-        if t is not None and t.device.index != dev:
-            raise ValueError("%s is on %s, the current device is cuda:%d" % (name, t.device, dev))
+# A decode step's calls take a few microseconds on the GPU, so their
+# marshalling is kept to one pass over the tensors: each is checked against
+# its type, shape and device in one expression and only a mismatch is looked
+# at closer.
+_U8, _I8, _I32, _F32, _BF16 = (torch.uint8, torch.int8, torch.int32, torch.float32,
+                               torch.bfloat16)
+_fns = {}
 
 
-def _shape(t: torch.Tensor, shape: tuple, name: str) -> None:
-    if tuple(t.shape) != shape:
+def _fn(name: str):
+    f = _fns.get(name)
+    if f is None:
+        f = _fns[name] = getattr(lib(), name)
+    return f
+
+
+def _refuse(t, dtype, shape, name, dev) -> None:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a tensor, got %s" % (name, type(t).__name__))
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if tuple(t.shape) != tuple(shape):
         raise ValueError("%s must be %s, got %s" % (name, list(shape), list(t.shape)))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    if not t.is_cuda:
+        raise ValueError("%s must be on a CUDA device" % name)
+    raise ValueError("%s is on %s, the call on cuda:%d" % (name, t.device, dev))
 
 
-def _cache8b_dims(k_cache, v_cache, k_scales, v_scales) -> Tuple[int, int, int]:
-    """(NB, n_kv, bs) of block-scaled pools uint8 [NB][n_kv][bs/8][8][8][16]
-    and their scales fp32 [NB][n_kv]."""
-    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        if t is not None:
-            _need(t, torch.uint8, n)
-            if t.dim() != 6 or tuple(t.shape[3:]) != (8, 8, 16):
-                raise ValueError("%s must be uint8 [NB][n_kv][bs/8][8][8][16]" % n)
-            _shape(t, tuple(k_cache.shape), n)
-    for t, n in ((k_scales, "k_scales"), (v_scales, "v_scales")):
-        if t is not None:
-            _need(t, torch.float32, n)
-            _shape(t, tuple(k_cache.shape[:2]), n)
-    return k_cache.shape[0], k_cache.shape[1], k_cache.shape[2] * 8
+def _take(dev: int, *specs) -> list:
+    """Device addresses of tensors given as (tensor, dtype, shape, name), each
+    contiguous and on device `dev`; None (an optional tensor left out) stays
+    None."""
+    ptrs = []
+    for t, dtype, shape, name in specs:
+        if t is None:
+            ptrs.append(None)
+            continue
+        try:
+            fine = (t.dtype is dtype and t.shape == shape and t.is_contiguous()
+                    and t.get_device() == dev and dev >= 0)
+        except AttributeError:
+            fine = False
+        if not fine:
+            _refuse(t, dtype, shape, name, dev)
+        ptrs.append(t.data_ptr())
+    return ptrs
+
+
+def _raw_stream(stream, dev: int) -> int:
+    """The given stream, or the current one of `dev`, which must be the
+    current device: the library launches there."""
+    if torch._C._cuda_getDevice() != dev:
+        raise ValueError("the tensors are on cuda:%d, the current device is cuda:%d"
+                         % (dev, torch._C._cuda_getDevice()))
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _sizes(t, n: int, name: str, dtype=None):
+    """The n sizes of a tensor's shape (of the given type, if any)."""
+    if dtype is not None and isinstance(t, torch.Tensor) and t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if not isinstance(t, torch.Tensor) or t.dim() != n:
+        raise ValueError("%s must be a tensor of %d dims, got %s" % (
+            name, n, list(t.shape) if isinstance(t, torch.Tensor) else type(t).__name__))
+    return t.shape
 
 
 def _range_call(name, k_rows, v_rows, k_cache, v_cache, k_scales, v_scales, block_tables,
                 positions, token_starts, max_tokens, stream):
-    for t, n in ((k_rows, "k rows"), (v_rows, "v rows")):
-        _need(t, torch.bfloat16, n)
-    NB, n_kv, bs = _cache8b_dims(k_cache, v_cache, k_scales, v_scales)
-    _need(block_tables, torch.int32, "block_tables")
-    _need(positions, torch.int32, "positions")
-    B, MB = block_tables.shape
-    _shape(positions, (B,), "positions")
-    if k_rows.dim() < 3 or tuple(k_rows.shape[-2:]) != (n_kv, HEAD_DIM):
-        raise ValueError("rows must end in [n_kv][%d], got %s" % (HEAD_DIM, list(k_rows.shape)))
-    _shape(v_rows, tuple(k_rows.shape), "v rows")
+    pool = _sizes(k_cache, 6, "k_cache")
+    NB, n_kv, rg = pool[:3]
+    B, MB = _sizes(block_tables, 2, "block_tables")
+    dev, rows = k_cache.get_device(), k_rows.shape
+    row_ptrs = _take(dev, (k_rows, _BF16, rows, "k rows"), (v_rows, _BF16, rows, "v rows"))
+    if len(rows) < 3 or rows[-2] != n_kv or rows[-1] != HEAD_DIM:
+        raise ValueError("rows must end in [%d][%d], got %s" % (n_kv, HEAD_DIM, list(rows)))
     N = k_rows.numel() // (n_kv * HEAD_DIM)
     if token_starts is None:
         if (N and not B) or (B and N % B):
@@ -715,24 +751,26 @@ def _range_call(name, k_rows, v_rows, k_cache, v_cache, k_scales, v_scales, bloc
         T = N // B if B else 0
         if max_tokens is not None and max_tokens != T:
             raise ValueError("max_tokens = %d, but every sequence has %d" % (max_tokens, T))
+    elif max_tokens is None:
+        raise ValueError("token_starts needs max_tokens, the most tokens of a sequence")
     else:
-        _need(token_starts, torch.int32, "token_starts")
-        _shape(token_starts, (B + 1,), "token_starts")
-        if max_tokens is None:
-            raise ValueError("token_starts needs max_tokens, the most tokens of a sequence")
         T = int(max_tokens)
-    _here(k_rows=k_rows, v_rows=v_rows, k_cache=k_cache, v_cache=v_cache, k_scales=k_scales,
-          v_scales=v_scales, block_tables=block_tables, positions=positions,
-          token_starts=token_starts)
-    _check(getattr(lib(), name)(
-        _ptr(k_rows), _ptr(v_rows), _ptr(k_cache), _ptr(v_cache), _ptr(k_scales), _ptr(v_scales),
-        _ptr(block_tables), _ptr(positions), _ptr(token_starts), B, T, N, n_kv, HEAD_DIM, bs, MB,
-        NB, _stream(stream)))
+    pool, scales = (NB, n_kv, rg, 8, 8, 16), (NB, n_kv)
+    ptrs = _take(dev, (k_cache, _U8, pool, "k_cache"), (v_cache, _U8, pool, "v_cache"),
+                 (k_scales, _F32, scales, "k_scales"), (v_scales, _F32, scales, "v_scales"),
+                 (block_tables, _I32, (B, MB), "block_tables"),
+                 (positions, _I32, (B,), "positions"),
+                 (token_starts, _I32, (B + 1,), "token_starts"))
+    s = _fn(name)(*row_ptrs, *ptrs, B, T, N, n_kv, HEAD_DIM, rg * 8, MB, NB,
+                  _raw_stream(stream, dev))
+    if s:
+        _check(s)
 
 
 def kv_append_fp8b(k_new, v_new, k_cache, v_cache, k_scales, v_scales, block_tables, positions,
                    token_starts=None, max_tokens: Optional[int] = None, stream=None) -> None:
-    """Quantise new tokens into the block-scaled pools at positions[b] on:
+    """Quantise new tokens into the block-scaled pools (uint8
+    [NB][n_kv][bs/8][8][8][16], scales fp32 [NB][n_kv]) at positions[b] on:
     rows token_starts[b] .. token_starts[b + 1] - 1 of k_new/v_new
     ([N][n_kv][d] bf16; at most max_tokens each), or without token_starts the
     same number of tokens for every sequence ([B][n_kv][d] or
@@ -749,44 +787,29 @@ def kv_read_fp8b(k_out, v_out, k_cache, v_cache, k_scales, v_scales, block_table
                 block_tables, positions, token_starts, max_tokens, stream)
 
 
-def _query(out, q, n_kv):
-    """(B, n_q, out) of a decode call's query [B][n_q][d]; out made if None."""
-    _need(q, torch.bfloat16, "q")
-    if q.dim() != 3:
-        raise ValueError("q must be [B][n_q][d], got %s" % list(q.shape))
-    B, n_q, _ = q.shape
-    if out is None:
-        out = torch.empty_like(q)
-    _need(out, torch.bfloat16, "out")
-    _shape(out, tuple(q.shape), "out")
-    return B, n_q, out
-
-
-def _scratch(workspace, B, n_q, n_kv, num_splits, device):
-    return make_workspace(B, n_q, n_kv, num_splits, device) if workspace is None else workspace
-
-
 def _attention8b_call(out, q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
                       scale, num_splits=0, workspace=None, stream=None, new=()):
-    NB, n_kv, bs = _cache8b_dims(k_cache, v_cache, k_scales, v_scales)
-    B, n_q, out = _query(out, q, n_kv)
-    _need(block_tables, torch.int32, "block_tables")
-    _need(context_lens, torch.int32, "context_lens")
-    MB = block_tables.shape[1]
-    _shape(block_tables, (B, MB), "block_tables")
-    _shape(context_lens, (B,), "context_lens")
-    for t, n in zip(new, ("k_new", "v_new")):
-        _need(t, torch.bfloat16, n)
-        _shape(t, (B, n_kv, HEAD_DIM), n)
-        _here(**{n: t})
-    workspace = _scratch(workspace, B, n_q, n_kv, num_splits, q.device)
-    _here(out=out, q=q, k_cache=k_cache, v_cache=v_cache, k_scales=k_scales, v_scales=v_scales,
-          block_tables=block_tables, context_lens=context_lens, workspace=workspace)
+    NB, n_kv, rg = _sizes(k_cache, 6, "k_cache", _U8)[:3]
+    B, n_q, d = _sizes(q, 3, "q")
+    MB = _sizes(block_tables, 2, "block_tables")[1]
+    dev = q.get_device()
+    pool, scales, rows = (NB, n_kv, rg, 8, 8, 16), (NB, n_kv), (B, n_kv, d)
+    ptrs = _take(dev, (q, _BF16, (B, n_q, d), "q"), (k_cache, _U8, pool, "k_cache"),
+                 (v_cache, _U8, pool, "v_cache"), (k_scales, _F32, scales, "k_scales"),
+                 (v_scales, _F32, scales, "v_scales"),
+                 (block_tables, _I32, (B, MB), "block_tables"),
+                 (context_lens, _I32, (B,), "context_lens"))
+    if new:
+        ptrs[1:1] = _take(dev, (new[0], _BF16, rows, "k_new"), (new[1], _BF16, rows, "v_new"))
+    if out is None:
+        out = torch.empty_like(q)
+    if workspace is None:
+        workspace = make_workspace(B, n_q, n_kv, num_splits, q.device)
+    po, = _take(dev, (out, _BF16, (B, n_q, d), "out"))
+    pw, = _take(dev, (workspace, workspace.dtype, workspace.shape, "workspace"))
     name = "pgd_append_decode_attention_fp8b" if new else "pgd_paged_decode_attention_fp8b"
-    return name, (_ptr(out), _ptr(q), *(_ptr(t) for t in new), _ptr(k_cache), _ptr(v_cache),
-                  _ptr(k_scales), _ptr(v_scales), _ptr(block_tables), _ptr(context_lens), B, n_q,
-                  n_kv, q.shape[2], bs, MB, NB, float(scale), int(num_splits), _ptr(workspace),
-                  workspace.numel() * workspace.element_size(), _stream(stream)), out
+    return name, (po, *ptrs, B, n_q, n_kv, d, rg * 8, MB, NB, float(scale), int(num_splits), pw,
+                  workspace.nbytes, _raw_stream(stream, dev)), out
 
 
 def _append_attention8b_call(out, q, k_new, v_new, *args, **kwargs):
@@ -802,7 +825,9 @@ def paged_decode_attention_fp8b(out, q, k_cache, v_cache, k_scales, v_scales, bl
     name, args, out = _attention8b_call(out, q, k_cache, v_cache, k_scales, v_scales,
                                         block_tables, context_lens, scale, num_splits, workspace,
                                         stream)
-    _check(getattr(lib(), name)(*args))
+    s = _fn(name)(*args)
+    if s:
+        _check(s)
     return out
 
 
@@ -815,29 +840,27 @@ def append_decode_attention_fp8b(out, q, k_new, v_new, k_cache, v_cache, k_scale
     name, args, out = _append_attention8b_call(out, q, k_new, v_new, k_cache, v_cache, k_scales,
                                                v_scales, block_tables, context_lens, scale,
                                                num_splits, workspace, stream)
-    _check(getattr(lib(), name)(*args))
+    s = _fn(name)(*args)
+    if s:
+        _check(s)
     return out
 
 
 # ------------------------------------------------------ block-sparse attention
-def _kv_dims(k_cache, v_cache, k_scales, v_scales) -> Tuple[int, int, int]:
-    """(NB, n_kv, bs) of a bf16 cache, or of a block-scaled one (with scales)."""
-    if k_scales is not None or v_scales is not None:
-        if k_scales is None or (v_cache is not None and v_scales is None):
-            raise ValueError("a block-scaled cache needs both scales")
-        return _cache8b_dims(k_cache, v_cache, k_scales, v_scales)
-    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        if t is not None:
-            _need(t, torch.bfloat16, n)
-            _shape(t, tuple(k_cache.shape), n)
-    return _cache_dims(k_cache)[:3]
-
-
-def _bounds_dims(bounds, bound_scales, NB, n_kv) -> None:
-    _need(bounds, torch.int8, "bounds")
-    _shape(bounds, (NB, n_kv, 2, HEAD_DIM), "bounds")
-    _need(bound_scales, torch.float32, "bound_scales")
-    _shape(bound_scales, (NB, n_kv), "bound_scales")
+def _kv_specs(k_cache, v_cache, k_scales, v_scales, with_v=True):
+    """(NB, n_kv, bs, specs of the pools and scales) of a bf16 cache, or of a
+    block-scaled one (with scales)."""
+    if (k_scales is None) != (v_scales is None) and with_v:
+        raise ValueError("a block-scaled cache needs both scales")
+    if k_scales is not None:
+        NB, n_kv, rg = _sizes(k_cache, 6, "k_cache")[:3]
+        pool, dtype = (NB, n_kv, rg, 8, 8, 16), _U8
+    else:
+        NB, n_kv, rg = _sizes(k_cache, 6, "k_cache")[:3]
+        pool, dtype = (NB, n_kv, rg, 16, 8, 8), _BF16
+    return NB, n_kv, rg * 8, ((k_cache, dtype, pool, "k_cache"), (v_cache, dtype, pool, "v_cache"),
+                              (k_scales, _F32, (NB, n_kv), "k_scales"),
+                              (v_scales, _F32, (NB, n_kv), "v_scales"))
 
 
 def block_bounds(bounds, bound_scales, k_cache, block_tables, context_lens, positions=None,
@@ -847,32 +870,17 @@ def block_bounds(bounds, bound_scales, k_cache, block_tables, context_lens, posi
     the whole contexts) of a bf16 cache, or of a block-scaled one with its
     k_scales.  max_tokens: the most tokens of a sequence (default: the table
     width)."""
-    NB, n_kv, bs = _kv_dims(k_cache, None, k_scales, None)
-    _bounds_dims(bounds, bound_scales, NB, n_kv)
-    _need(block_tables, torch.int32, "block_tables")
-    _need(context_lens, torch.int32, "context_lens")
-    B, MB = block_tables.shape
-    _shape(context_lens, (B,), "context_lens")
-    if positions is not None:
-        _need(positions, torch.int32, "positions")
-        _shape(positions, (B,), "positions")
-    _here(bounds=bounds, bound_scales=bound_scales, k_cache=k_cache, block_tables=block_tables,
-          context_lens=context_lens, positions=positions, k_scales=k_scales)
+    NB, n_kv, bs, (k_spec, _, scale_spec, _) = _kv_specs(k_cache, None, k_scales, None, False)
+    B, MB = _sizes(block_tables, 2, "block_tables")
+    dev = k_cache.get_device()
+    ptrs = _take(dev, (bounds, _I8, (NB, n_kv, 2, HEAD_DIM), "bounds"),
+                 (bound_scales, _F32, (NB, n_kv), "bound_scales"), k_spec, scale_spec,
+                 (block_tables, _I32, (B, MB), "block_tables"),
+                 (positions, _I32, (B,), "positions"), (context_lens, _I32, (B,), "context_lens"))
     T = MB * bs if max_tokens is None else int(max_tokens)
-    _check(lib().pgd_block_bounds(_ptr(bounds), _ptr(bound_scales), _ptr(k_cache), _ptr(k_scales),
-                                  _ptr(block_tables), _ptr(positions), _ptr(context_lens), B, T,
-                                  n_kv, HEAD_DIM, bs, MB, NB, _stream(stream)))
-
-
-def _selection(tiles, tile_tokens, B, n_kv) -> int:
-    _need(tiles, torch.int32, "tiles")
-    _need(tile_tokens, torch.int32, "tile_tokens")
-    if tiles.dim() != 3:
-        raise ValueError("tiles must be [B][n_kv][W]")
-    W = tiles.shape[2]
-    _shape(tiles, (B, n_kv, W), "tiles")
-    _shape(tile_tokens, (B, n_kv), "tile_tokens")
-    return W
+    s = _fn("pgd_block_bounds")(*ptrs, B, T, n_kv, HEAD_DIM, bs, MB, NB, _raw_stream(stream, dev))
+    if s:
+        _check(s)
 
 
 def select_blocks(tiles, tile_tokens, q, bounds, bound_scales, block_tables, context_lens,
@@ -880,23 +888,51 @@ def select_blocks(tiles, tile_tokens, q, bounds, bound_scales, block_tables, con
     """tiles [B][n_kv][W] and tile_tokens [B][n_kv] (int32): for every
     sequence and KV head the first keep_first blocks, the last keep_last and
     the others of the largest score, W in all."""
-    _need(bounds, torch.int8, "bounds")
-    NB, n_kv = bounds.shape[:2]
-    _bounds_dims(bounds, bound_scales, NB, n_kv)
-    _need(q, torch.bfloat16, "q")
-    _need(block_tables, torch.int32, "block_tables")
-    _need(context_lens, torch.int32, "context_lens")
-    B, n_q, d = q.shape
-    W = _selection(tiles, tile_tokens, B, n_kv)
-    MB = block_tables.shape[1]
-    _shape(block_tables, (B, MB), "block_tables")
-    _shape(context_lens, (B,), "context_lens")
-    _here(tiles=tiles, tile_tokens=tile_tokens, q=q, bounds=bounds, bound_scales=bound_scales,
-          block_tables=block_tables, context_lens=context_lens)
-    _check(lib().pgd_select_blocks(_ptr(tiles), _ptr(tile_tokens), _ptr(q), _ptr(bounds),
-                                   _ptr(bound_scales), _ptr(block_tables), _ptr(context_lens), B,
-                                   n_q, n_kv, d, int(block_size), MB, NB, W, int(keep_first),
-                                   int(keep_last), _stream(stream)))
+    NB, n_kv = _sizes(bounds, 4, "bounds", _I8)[:2]
+    B, n_q, d = _sizes(q, 3, "q")
+    W = _sizes(tiles, 3, "tiles")[2]
+    MB = _sizes(block_tables, 2, "block_tables")[1]
+    dev = q.get_device()
+    ptrs = _take(dev, (tiles, _I32, (B, n_kv, W), "tiles"),
+                 (tile_tokens, _I32, (B, n_kv), "tile_tokens"), (q, _BF16, (B, n_q, d), "q"),
+                 (bounds, _I8, (NB, n_kv, 2, HEAD_DIM), "bounds"),
+                 (bound_scales, _F32, (NB, n_kv), "bound_scales"),
+                 (block_tables, _I32, (B, MB), "block_tables"),
+                 (context_lens, _I32, (B,), "context_lens"))
+    s = _fn("pgd_select_blocks")(*ptrs, B, n_q, n_kv, d, int(block_size), MB, NB, W,
+                                 int(keep_first), int(keep_last), _raw_stream(stream, dev))
+    if s:
+        _check(s)
+
+
+def _tiles_call(name, out, q, k_cache, v_cache, k_scales, v_scales, middle, tiles, tile_tokens,
+                keep, scale, num_splits, workspace, stream):
+    """A call over W tiles per (sequence, KV head); `middle` (the selection's
+    inputs: bounds, bound_scales, block_tables, context_lens) and `keep` are
+    empty where the tiles are given."""
+    NB, n_kv, bs, specs = _kv_specs(k_cache, v_cache, k_scales, v_scales)
+    B, n_q, d = _sizes(q, 3, "q")
+    W = _sizes(tiles, 3, "tiles")[2]
+    dev = q.get_device()
+    ints = [B, n_q, n_kv, d, bs, NB, W]
+    if middle:
+        MB = _sizes(middle[2], 2, "block_tables")[1]
+        ints.insert(5, MB)
+        specs += ((middle[0], _I8, (NB, n_kv, 2, HEAD_DIM), "bounds"),
+                  (middle[1], _F32, (NB, n_kv), "bound_scales"),
+                  (middle[2], _I32, (B, MB), "block_tables"),
+                  (middle[3], _I32, (B,), "context_lens"))
+    ptrs = _take(dev, (q, _BF16, (B, n_q, d), "q"), *specs,
+                 (tiles, _I32, (B, n_kv, W), "tiles"),
+                 (tile_tokens, _I32, (B, n_kv), "tile_tokens"))
+    if out is None:
+        out = torch.empty_like(q)
+    if workspace is None:
+        workspace = make_workspace(B, n_q, n_kv, num_splits, q.device)
+    po, = _take(dev, (out, _BF16, (B, n_q, d), "out"))
+    pw, = _take(dev, (workspace, workspace.dtype, workspace.shape, "workspace"))
+    return name, (po, *ptrs, *ints, *keep, float(scale), int(num_splits), pw, workspace.nbytes,
+                  _raw_stream(stream, dev)), out
 
 
 def selected_decode_attention(out, q, k_cache, v_cache, tiles, tile_tokens, scale: float,
@@ -906,42 +942,21 @@ def selected_decode_attention(out, q, k_cache, v_cache, tiles, tile_tokens, scal
     """out[B][n_q][d] (bf16) = decode attention of q over the tiles (block *
     n_kv + head, [B][n_kv][W]) of a bf16 cache, or of a block-scaled one with
     its scales."""
-    NB, n_kv, bs = _kv_dims(k_cache, v_cache, k_scales, v_scales)
-    B, n_q, out = _query(out, q, n_kv)
-    W = _selection(tiles, tile_tokens, B, n_kv)
-    workspace = _scratch(workspace, B, n_q, n_kv, num_splits, q.device)
-    _here(out=out, q=q, k_cache=k_cache, v_cache=v_cache, k_scales=k_scales, v_scales=v_scales,
-          tiles=tiles, tile_tokens=tile_tokens, workspace=workspace)
-    _check(lib().pgd_selected_decode_attention(
-        _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scales), _ptr(v_scales),
-        _ptr(tiles), _ptr(tile_tokens), B, n_q, n_kv, q.shape[2], bs, NB, W, float(scale),
-        int(num_splits), _ptr(workspace), workspace.numel() * workspace.element_size(),
-        _stream(stream)))
+    name, args, out = _tiles_call("pgd_selected_decode_attention", out, q, k_cache, v_cache,
+                                  k_scales, v_scales, (), tiles, tile_tokens, (), scale,
+                                  num_splits, workspace, stream)
+    s = _fn(name)(*args)
+    if s:
+        _check(s)
     return out
 
 
 def _sparse_call(out, q, k_cache, v_cache, bounds, bound_scales, block_tables, context_lens,
                  tiles, tile_tokens, keep_first, keep_last, scale, k_scales=None, v_scales=None,
                  num_splits=0, workspace=None, stream=None):
-    NB, n_kv, bs = _kv_dims(k_cache, v_cache, k_scales, v_scales)
-    _bounds_dims(bounds, bound_scales, NB, n_kv)
-    B, n_q, out = _query(out, q, n_kv)
-    W = _selection(tiles, tile_tokens, B, n_kv)
-    _need(block_tables, torch.int32, "block_tables")
-    _need(context_lens, torch.int32, "context_lens")
-    MB = block_tables.shape[1]
-    _shape(block_tables, (B, MB), "block_tables")
-    _shape(context_lens, (B,), "context_lens")
-    workspace = _scratch(workspace, B, n_q, n_kv, num_splits, q.device)
-    _here(out=out, q=q, k_cache=k_cache, v_cache=v_cache, k_scales=k_scales, v_scales=v_scales,
-          bounds=bounds, bound_scales=bound_scales, block_tables=block_tables,
-          context_lens=context_lens, tiles=tiles, tile_tokens=tile_tokens, workspace=workspace)
-    return "pgd_sparse_decode_attention", (
-        _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scales), _ptr(v_scales),
-        _ptr(bounds), _ptr(bound_scales), _ptr(block_tables), _ptr(context_lens), _ptr(tiles),
-        _ptr(tile_tokens), B, n_q, n_kv, q.shape[2], bs, MB, NB, W, int(keep_first),
-        int(keep_last), float(scale), int(num_splits), _ptr(workspace),
-        workspace.numel() * workspace.element_size(), _stream(stream)), out
+    return _tiles_call("pgd_sparse_decode_attention", out, q, k_cache, v_cache, k_scales, v_scales,
+                       (bounds, bound_scales, block_tables, context_lens), tiles, tile_tokens,
+                       (int(keep_first), int(keep_last)), scale, num_splits, workspace, stream)
 
 
 def sparse_decode_attention(out, q, k_cache, v_cache, bounds, bound_scales, block_tables,
@@ -954,7 +969,9 @@ def sparse_decode_attention(out, q, k_cache, v_cache, bounds, bound_scales, bloc
     name, args, out = _sparse_call(out, q, k_cache, v_cache, bounds, bound_scales, block_tables,
                                    context_lens, tiles, tile_tokens, keep_first, keep_last, scale,
                                    k_scales, v_scales, num_splits, workspace, stream)
-    _check(getattr(lib(), name)(*args))
+    s = _fn(name)(*args)
+    if s:
+        _check(s)
     return out
 
 
