@@ -1,20 +1,27 @@
 // kv_fp8b.cu -- writing tokens into the block-scaled 8-bit cache and reading
 // ranges of it back (layout and scale rule: kv_fp8b.cuh).
 //
-// One warp per (sequence, block, KV head, K or V).  Lane l holds dims
-// 16 (l % 8) .. + 15 of slots l / 8, l / 8 + 4, ...: a row is 8 lanes x 32 B
-// of bf16 and 8 x 16 B of codes, so both sides move in whole 16-byte vectors.
+// One warp per (sequence, block, KV head, K or V), holding slots l / 8,
+// l / 8 + 4, ... in lane l.
 //
-// Write: the rows are loaded into registers (all loads in flight together),
-// their largest finite |x| gives the least power-of-two scale that holds
-// them, and each value becomes E4M3(x / scale).  A block that a sequence has
-// begun before (its first new slot is not slot 0) keeps the larger of its
-// scale and that; where it grows, the earlier slots' codes are encoded again
-// for the new scale.  The slots behind the last new token are not touched:
-// they hold no token.  NaN is stored as NaN; an infinity saturates.
-// Read: bf16(E4M3(code) * scale), one rounding (none for power-of-two scales).
+// Write: lane l has dims 8 c .. + 7 and 64 + 8 c .. + 7 (c = l % 8) of its
+// slots, so that every load instruction reads four rows' halves of 128
+// contiguous bytes.  The rows are loaded into registers (all loads in flight
+// together), their largest finite |x| gives the least power-of-two scale that
+// holds them, and each value becomes E4M3(x / scale): a product with the
+// inverse, exact, in packed bf16.  A block that a sequence has begun before
+// (its first new slot is not slot 0) keeps the larger of its scale and that;
+// where it grows, the earlier slots' codes are encoded again for the new
+// scale.  The slots behind the last new token are not touched: they hold no
+// token.  NaN is stored as NaN; an infinity saturates.
+// Read: lane l has dims 16 c .. + 15; bf16(E4M3(code) * scale), one rounding
+// (none for power-of-two scales).
 //
-// Both are bound by memory: 2 + 1 bytes per value.
+// Both are bound by memory: 2 + 1 bytes per value.  What is rare (values that
+// are not finite, growing a begun block, a caller's scale that is no power of
+// two) is out of line and works from memory, so that the common path stays
+// short: with it inlined and unrolled the write stalled on instruction
+// fetches.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -70,13 +77,61 @@ __device__ __forceinline__ bool find_item(const Kv8bParams &p, int bs, int JM, I
   return true;
 }
 
-// The largest finite |x| of two bf16 pairs' worth of bits, as bf16 bits (a
-// non-finite value counts as 0).
-__device__ __forceinline__ uint32_t finite_abs(uint32_t w) {
-  w &= 0x7fff7fffu;
-  if ((w & 0xffffu) >= 0x7f80u) w &= 0xffff0000u;
-  if ((w >> 16) >= 0x7f80u) w &= 0xffffu;
-  return w;
+// The 16 values of a lane (dims 16 c .. + 15 of a slot) as codes.
+__device__ __forceinline__ void put16(unsigned char *at, const float (&f)[16]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    w[k] = (uint32_t)f32x2_to_e4m3x2(f[4 * k], f[4 * k + 1]) |
+           ((uint32_t)f32x2_to_e4m3x2(f[4 * k + 2], f[4 * k + 3]) << 16);
+  *reinterpret_cast<uint4 *>(at) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// The warp's largest finite |x| over rows [row, row + n), as bf16 bits.
+__device__ __noinline__ uint32_t finite_max(const __nv_bfloat16 *row, size_t stride, int n) {
+  uint32_t top = 0;
+  for (int i = threadIdx.x & 31; i < n * kHeadDim; i += 32) {
+    const uint32_t a =
+        __bfloat16_as_ushort(row[(size_t)(i / kHeadDim) * stride + i % kHeadDim]) & 0x7fffu;
+    if (a < 0x7f80u) top = max(top, a);
+  }
+  return __reduce_max_sync(kFullMask, top);
+}
+
+// The codes of slots [0, s0) encoded again for a scale `ratio` times smaller
+// relative to their values.
+__device__ __noinline__ void rescale_codes(unsigned char *tile, int s0, float ratio) {
+  const int lane = threadIdx.x & 31, c = lane & 7;
+  for (int s = lane >> 3; s < s0; s += 4) {
+    const uint4 v = *reinterpret_cast<const uint4 *>(tile + code_offset8b(s, c));
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    float f[16];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float2 y = __half22float2(e4m3x2_to_half2((uint16_t)(w[k >> 1] >> ((k & 1) * 16))));
+      f[2 * k] = y.x * ratio;
+      f[2 * k + 1] = y.y * ratio;
+    }
+    put16(tile + code_offset8b(s, c), f);
+  }
+}
+
+// Rows [row, row + s1 - s0) into slots [s0, s1), divided by any scale.
+__device__ __noinline__ void write_divided(unsigned char *tile, const __nv_bfloat16 *row,
+                                           size_t stride, int s0, int s1, float scale) {
+  const int lane = threadIdx.x & 31, c = lane & 7;
+  for (int s = s0 + (lane >> 3); s < s1; s += 4) {
+    float f[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k)
+      f[k] = __fdiv_rn(__bfloat162float(row[(size_t)(s - s0) * stride + 16 * c + k]), scale);
+    put16(tile + code_offset8b(s, c), f);
+  }
+}
+
+__device__ __forceinline__ uint32_t bf16x2_mul(uint32_t w, __nv_bfloat162 m) {
+  const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&w), m);
+  return *reinterpret_cast<const uint32_t *>(&r);
 }
 
 template <int BS>
@@ -87,7 +142,9 @@ __global__ void __launch_bounds__(kWarps * 32) append_kernel(const Kv8bParams p,
   Item it;
   if (!find_item(p, BS, JM, it)) return;
   const int lane = threadIdx.x & 31, c = lane & 7, r = lane >> 3;
-  const uint4 *src = reinterpret_cast<const uint4 *>(it.is_v ? p.v_new : p.k_new) + c * 2;
+  const size_t stride = (size_t)p.n_kv * kHeadDim;  // a packed row's
+  const __nv_bfloat16 *rows = (it.is_v ? p.v_new : p.k_new) +
+                              ((size_t)it.row0 * p.n_kv + it.g) * kHeadDim;  // slot s0's
   unsigned char *tile = (it.is_v ? p.v_cache : p.k_cache) + it.tile * (size_t)(BS * kHeadDim);
   float *scale_at = (it.is_v ? p.v_scales : p.k_scales) + it.tile;
   uint4 x[NI][2];
@@ -96,9 +153,9 @@ __global__ void __launch_bounds__(kWarps * 32) append_kernel(const Kv8bParams p,
     const int s = 4 * i + r;
     x[i][0] = x[i][1] = make_uint4(0, 0, 0, 0);
     if (s >= it.s0 && s < it.s1) {
-      const uint4 *row = src + ((it.row0 + (s - it.s0)) * p.n_kv + it.g) * (kHeadDim / 8);
-      x[i][0] = __ldg(row);
-      x[i][1] = __ldg(row + 1);
+      const uint4 *at = reinterpret_cast<const uint4 *>(rows + (size_t)(s - it.s0) * stride) + c;
+      x[i][0] = __ldg(at);
+      x[i][1] = __ldg(at + 8);
     }
   }
   const float old = it.s0 > 0 ? *scale_at : 0.f;
@@ -107,56 +164,44 @@ __global__ void __launch_bounds__(kWarps * 32) append_kernel(const Kv8bParams p,
   for (int i = 0; i < NI; ++i)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      top = __vmaxu2(top, finite_abs(x[i][h].x));
-      top = __vmaxu2(top, finite_abs(x[i][h].y));
-      top = __vmaxu2(top, finite_abs(x[i][h].z));
-      top = __vmaxu2(top, finite_abs(x[i][h].w));
+      top = __vmaxu2(top, x[i][h].x & 0x7fff7fffu);
+      top = __vmaxu2(top, x[i][h].y & 0x7fff7fffu);
+      top = __vmaxu2(top, x[i][h].z & 0x7fff7fffu);
+      top = __vmaxu2(top, x[i][h].w & 0x7fff7fffu);
     }
-  const uint32_t amax = __reduce_max_sync(kFullMask, max(top & 0xffffu, top >> 16));
+  uint32_t amax = __reduce_max_sync(kFullMask, max(top & 0xffffu, top >> 16));
+  if (amax >= 0x7f80u) amax = finite_max(rows, stride, it.s1 - it.s0);
   const float need = pow2f(scale_exponent_e4m3(__uint_as_float(amax << 16)));
   const float scale = it.s0 > 0 ? fmaxf(old, need) : need;
-  // x / scale: exact as a product with the inverse where the scale is a power
-  // of two (always, unless the caller filled in another one)
-  const bool pow2 = (__float_as_uint(scale) & 0x7fffffu) == 0;
-  const float inv = pow2 ? __uint_as_float(0x7f000000u - __float_as_uint(scale)) : 1.f;
-  auto put = [&](int s, const float (&f)[16]) {
-    uint32_t w[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      w[k] = (uint32_t)f32x2_to_e4m3x2(f[4 * k], f[4 * k + 1]) |
-             ((uint32_t)f32x2_to_e4m3x2(f[4 * k + 2], f[4 * k + 3]) << 16);
-    *reinterpret_cast<uint4 *>(tile + code_offset8b(s, c)) = make_uint4(w[0], w[1], w[2], w[3]);
-  };
+  if (it.s0 > 0 && scale != old) rescale_codes(tile, it.s0, __fdiv_rn(old, scale));
+  __syncwarp();
+  if (lane == 0) *scale_at = scale;
+  // a power of two in the range of the writer's own: its inverse is a bf16
+  // number and the products are exact (or so small that they are 0 in E4M3)
+  const uint32_t bits = __float_as_uint(scale);
+  if ((bits & 0x7fffffu) != 0 || scale < 0x1p-100f || scale > 0x1p120f) {
+    write_divided(tile, rows, stride, it.s0, it.s1, scale);
+    return;
+  }
+  const __nv_bfloat162 inv = __float2bfloat162_rn(__uint_as_float(0x7f000000u - bits));
+  unsigned char *dst = tile + (c >> 1) * 128 + (c & 1) * 8;  // dims 8 c of slot 0
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
     const int s = 4 * i + r;
     if (s < it.s0 || s >= it.s1) continue;
-    float a[8], b[8], f[16];
-    unpack8(x[i][0], a);
-    unpack8(x[i][1], b);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      f[k] = pow2 ? a[k] * inv : __fdiv_rn(a[k], scale);
-      f[8 + k] = pow2 ? b[k] * inv : __fdiv_rn(b[k], scale);
-    }
-    put(s, f);
-  }
-  if (it.s0 > 0 && scale != old) {
-    const float ratio = __fdiv_rn(old, scale);
-    for (int s = r; s < it.s0; s += 4) {
-      const uint4 v = *reinterpret_cast<const uint4 *>(tile + code_offset8b(s, c));
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-      float f[16];
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t v[4] = {x[i][h].x, x[i][h].y, x[i][h].z, x[i][h].w};
+      uint32_t q[4];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float2 y = __half22float2(e4m3x2_to_half2((uint16_t)(w[k >> 1] >> ((k & 1) * 16))));
-        f[2 * k] = y.x * ratio;
-        f[2 * k + 1] = y.y * ratio;
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t y = bf16x2_mul(v[k], inv);
+        q[k] = f32x2_to_e4m3x2(bf16lo(y), bf16hi(y));
       }
-      put(s, f);
+      *reinterpret_cast<uint2 *>(dst + (s >> 3) * kGroupBytes8b + (s & 7) * 16 + h * 512) =
+          make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
     }
   }
-  if (lane == 0) *scale_at = scale;
 }
 
 template <int BS>
