@@ -26,12 +26,34 @@ namespace {
 
 constexpr int kBoundWarps = 4;
 
-// One warp per tile to be updated.  bf16: lane = (16-byte chunk of 8 dims,
-// half of each 8-token group); 8-bit: lane = (16-byte chunk of 16 dims,
-// quarter).  Minimum and maximum over the lane's tokens in the storage's own
-// precision (bf16, or f16 for widened codes: exact), then over the lanes that
-// share the dims; fminf/fmaxf semantics, so a NaN among numbers is passed
-// over.  Bound by the read of the keys.
+// Least of each of two packed numbers, passing over a NaN beside a number:
+// f16 (widened 8-bit codes) or bf16.
+template <bool FP8>
+__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
+  if constexpr (FP8) {
+    const __half2 r = __hmin2(*reinterpret_cast<const __half2 *>(&a),
+                              *reinterpret_cast<const __half2 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&r);
+  } else {
+    const __nv_bfloat162 r = __hmin2(*reinterpret_cast<const __nv_bfloat162 *>(&a),
+                                     *reinterpret_cast<const __nv_bfloat162 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&r);
+  }
+}
+template <bool FP8>
+__device__ __forceinline__ float2 widen2(uint32_t a) {
+  if constexpr (FP8) return __half22float2(*reinterpret_cast<const __half2 *>(&a));
+  return make_float2(bf16lo(a), bf16hi(a));
+}
+
+// One warp per tile to be updated.  Lane l takes slot l % 8 of every 8-token
+// group and the 16-byte chunks l / 8, l / 8 + 4, ..., so that a load
+// instruction reads 512 contiguous bytes.  Per chunk it keeps the least k and
+// the least -k of each dim in the storage's own precision (bf16, or f16 for
+// widened codes: exact); the eight lanes of a chunk then reduce them by
+// halves: a lane keeps one half of the values and sends the other, and ends
+// with the lower bounds (l % 8 < 4) or the negated upper bounds (l % 8 >= 4)
+// of a few dims over all tokens.  Bound by the read of the keys.
 template <int BS, bool FP8>
 __global__ void __launch_bounds__(kBoundWarps * 32) bounds_kernel(const BoundsParams p, int JM) {
   pdl_wait();
@@ -61,118 +83,94 @@ __global__ void __launch_bounds__(kBoundWarps * 32) bounds_kernel(const BoundsPa
   }
   const int valid = min(BS, ctx - j * BS);
   const size_t tile = (size_t)blk * p.n_kv + g;
-  constexpr int ND = FP8 ? 16 : 8;  // dims of a lane
-  float lo[ND], hi[ND];
-  const float inf = __int_as_float(0x7f800000);
-  if constexpr (FP8) {
-    const int c = lane & 7, qt = lane >> 3;
-    const unsigned char *base = p.k_cache + tile * (size_t)(BS * kHeadDim);
-    uint4 x[BS / 4];
+  constexpr int NG = BS / 8;             // 8-token groups
+  constexpr int NC = FP8 ? 2 : 4;        // chunks of a lane
+  constexpr int ND2 = FP8 ? 8 : 4;       // pairs of dims in a chunk
+  constexpr int NW = ND2 / 4;            // pairs of a chunk that a lane ends with
+  constexpr uint32_t kSign = 0x80008000u, kInf = FP8 ? 0x7c007c00u : 0x7f807f80u;
+  const int slot = lane & 7, cl = lane >> 3;
+  // (chunks of a group are 8 slots x 16 bytes apart, groups follow each other)
+  const uint4 *base = reinterpret_cast<const uint4 *>(p.k_cache) +
+                      tile * (size_t)(BS * (FP8 ? 8 : 16)) + cl * 8 + slot;
+  uint4 x[NG][NC];
 #pragma unroll
-    for (int i = 0; i < BS / 4; ++i) {
-      const int s = (i >> 1) * 8 + qt * 2 + (i & 1);
-      x[i] = make_uint4(0, 0, 0, 0);
-      if (s < valid) x[i] = __ldg(reinterpret_cast<const uint4 *>(base + code_offset8b(s, c)));
+  for (int i = 0; i < NG; ++i)
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      x[i][c] = make_uint4(0, 0, 0, 0);
+      if (8 * i + slot < valid) x[i][c] = __ldg(base + i * (NC * 32) + c * 32);
     }
-    const float scale = __ldg(p.k_scales + tile);
-    __half2 l[8], h[8];
+  float scale = 1.f;
+  if constexpr (FP8) scale = __ldg(p.k_scales + tile);
+  uint32_t out[NC][NW];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      l[k] = __half2half2(__ushort_as_half(0x7c00));
-      h[k] = __half2half2(__ushort_as_half(0xfc00));
-    }
+  for (int c = 0; c < NC; ++c) {
+    uint32_t v[2 * ND2];  // least k of the chunk's pairs, then least -k
 #pragma unroll
-    for (int i = 0; i < BS / 4; ++i) {
-      const int s = (i >> 1) * 8 + qt * 2 + (i & 1);
-      if (s < valid) {
-        const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+    for (int k = 0; k < 2 * ND2; ++k) v[k] = kInf;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const __half2 v = e4m3x2_to_half2((uint16_t)(w[k >> 1] >> ((k & 1) * 16)));
-          l[k] = __hmin2(l[k], v);
-          h[k] = __hmax2(h[k], v);
+    for (int i = 0; i < NG; ++i)
+      if (8 * i + slot < valid) {
+        const uint32_t w[4] = {x[i][c].x, x[i][c].y, x[i][c].z, x[i][c].w};
+#pragma unroll
+        for (int k = 0; k < ND2; ++k) {
+          uint32_t y = w[FP8 ? k >> 1 : k];
+          if constexpr (FP8) {
+            const __half2 h = e4m3x2_to_half2((uint16_t)(y >> ((k & 1) * 16)));
+            y = *reinterpret_cast<const uint32_t *>(&h);
+          }
+          v[k] = min2<FP8>(v[k], y);
+          v[ND2 + k] = min2<FP8>(v[ND2 + k], y ^ kSign);
         }
       }
-    }
 #pragma unroll
-    for (int o = 8; o < 32; o <<= 1)
+    for (int m = 2 * ND2, off = 4; off > 0; m >>= 1, off >>= 1) {
+      const bool up = (slot & off) != 0;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        l[k] = __hmin2(l[k], __shfl_xor_sync(kFullMask, l[k], o));
-        h[k] = __hmax2(h[k], __shfl_xor_sync(kFullMask, h[k], o));
-      }
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float2 a = __half22float2(l[k]), bb = __half22float2(h[k]);
-      lo[2 * k] = a.x * scale; lo[2 * k + 1] = a.y * scale;
-      hi[2 * k] = bb.x * scale; hi[2 * k + 1] = bb.y * scale;
-    }
-  } else {
-    const int c = lane & 15, half = lane >> 4;
-    const uint4 *base = reinterpret_cast<const uint4 *>(p.k_cache) + tile * (size_t)(BS * 16);
-    uint4 x[BS / 2];
-#pragma unroll
-    for (int i = 0; i < BS / 2; ++i) {
-      const int s = (i >> 2) * 8 + half * 4 + (i & 3);
-      x[i] = make_uint4(0, 0, 0, 0);
-      if (s < valid) x[i] = __ldg(base + (s >> 3) * 128 + c * 8 + (s & 7));
-    }
-    __nv_bfloat162 l[4], h[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      l[k] = __bfloat162bfloat162(__ushort_as_bfloat16(0x7f80));
-      h[k] = __bfloat162bfloat162(__ushort_as_bfloat16(0xff80));
-    }
-#pragma unroll
-    for (int i = 0; i < BS / 2; ++i) {
-      const int s = (i >> 2) * 8 + half * 4 + (i & 3);
-      if (s < valid) {
-        const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const __nv_bfloat162 v = *reinterpret_cast<const __nv_bfloat162 *>(&w[k]);
-          l[k] = __hmin2(l[k], v);
-          h[k] = __hmax2(h[k], v);
-        }
+      for (int k = 0; k < m / 2; ++k) {
+        const uint32_t keep = up ? v[k + m / 2] : v[k], send = up ? v[k] : v[k + m / 2];
+        v[k] = min2<FP8>(keep, __shfl_xor_sync(kFullMask, send, off));
       }
     }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      l[k] = __hmin2(l[k], __shfl_xor_sync(kFullMask, l[k], 16));
-      h[k] = __hmax2(h[k], __shfl_xor_sync(kFullMask, h[k], 16));
-      const float2 a = __bfloat1622float2(l[k]), bb = __bfloat1622float2(h[k]);
-      lo[2 * k] = a.x; lo[2 * k + 1] = a.y;
-      hi[2 * k] = bb.x; hi[2 * k + 1] = bb.y;
-    }
+    for (int k = 0; k < NW; ++k) out[c][k] = v[k];
   }
+  // Largest finite bound, the scale, and this lane's bounds: dims
+  // chunk * 2 ND2 + (slot % 4) * 2 NW .. of the lower or upper ones.
+  const bool upper = slot >= 4;
   float amax = 0.f;
 #pragma unroll
-  for (int k = 0; k < ND; ++k) {
-    const float m = fmaxf(fabsf(lo[k]), fabsf(hi[k]));
-    amax = fmaxf(amax, m < inf ? m : 0.f);
-  }
+  for (int c = 0; c < NC; ++c)
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFullMask, amax, o));
+    for (int k = 0; k < NW; ++k) {
+      const float2 y = widen2<FP8>(out[c][k]);
+      const float a0 = fabsf(y.x * scale), a1 = fabsf(y.y * scale);
+      amax = fmaxf(amax, fmaxf(a0 < INFINITY ? a0 : 0.f, a1 < INFINITY ? a1 : 0.f));
+    }
+  amax = __uint_as_float(__reduce_max_sync(kFullMask, __float_as_uint(amax)));
   const int e = scale_exponent_int8(amax);
   const float inv = pow2f(-e);
-  const int part = FP8 ? lane >> 3 : lane >> 4;  // 0 writes the lower bounds, 1 the upper
-  if (part < 2) {
-    uint32_t w[ND / 4];
+  signed char *dst = p.bounds + tile * (2 * kHeadDim) + (upper ? kHeadDim : 0) +
+                     cl * 2 * ND2 + (slot & 3) * 2 * NW;
 #pragma unroll
-    for (int k = 0; k < ND / 4; ++k) {
-      w[k] = 0;
+  for (int c = 0; c < NC; ++c) {
+    uint32_t w = 0;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float v = part ? ceilf(hi[4 * k + i] * inv) : floorf(lo[4 * k + i] * inv);
-        const int n = (int)fminf(fmaxf(v, -127.f), 127.f);
-        w[k] |= (uint32_t)(n & 0xff) << (8 * i);
+    for (int k = 0; k < NW; ++k) {
+      const float2 y = widen2<FP8>(out[c][k]);
+      float f[2] = {y.x * scale, y.y * scale};
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        // (floor of -max is -ceil(max))
+        int n = (int)fminf(fmaxf(floorf(f[i] * inv), -127.f), 127.f);
+        if (upper) n = -n;
+        w |= (uint32_t)(n & 0xff) << (16 * k + 8 * i);
       }
     }
-    signed char *dst = p.bounds + tile * (2 * kHeadDim) + part * kHeadDim;
     if constexpr (FP8)
-      *reinterpret_cast<uint4 *>(dst + (lane & 7) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+      *reinterpret_cast<uint32_t *>(dst + c * 8 * ND2) = w;
     else
-      *reinterpret_cast<uint2 *>(dst + (lane & 15) * 8) = make_uint2(w[0], w[1]);
+      *reinterpret_cast<uint16_t *>(dst + c * 8 * ND2) = (uint16_t)w;
   }
   if (lane == 0) p.bound_scales[tile] = pow2f(e);
 }
@@ -525,12 +523,15 @@ cudaError_t block_bounds_launch(const BoundsParams &p, cudaStream_t stream) {
 // Blocks of a sequence that the selection holds keys for.
 int select_max_blocks() { return kMaxCluster * kSliceKeys; }
 
-// CTAs per (sequence, KV head): as many as fill the GPU once, but no more than
-// leave each 128 blocks (fewer are not worth the cluster barriers), and at
-// least as many as hold the keys.
+// CTAs per (sequence, KV head): as many as fill the GPU once, up to 8, but no
+// more than leave each 128 blocks (fewer are not worth the cluster barriers),
+// and at least as many as hold the keys.  (Clusters of 16 do not all find
+// their place at once: 8 heads of 8192 blocks take 29.8 us in clusters of 16,
+// 16.5 in 8, 21.5 in 4, 34.5 in 2.)
 static int select_cluster(int units, int MB) {
   int C = 1;
-  while (C < kMaxCluster && ((units * C * 2 <= 152 && MB >= C * 2 * 128) || MB > C * kSliceKeys)) C *= 2;
+  while (C < 8 && units * C * 2 <= 152 && MB >= C * 2 * 128) C *= 2;
+  while (MB > C * kSliceKeys) C *= 2;
   return C;
 }
 
