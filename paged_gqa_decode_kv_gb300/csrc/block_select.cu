@@ -46,7 +46,7 @@ __device__ __forceinline__ float2 widen2(uint32_t a) {
   return make_float2(bf16lo(a), bf16hi(a));
 }
 
-// One warp per tile to be updated.  Lane l takes slot l % 8 of every 8-token
+// The bounds of one tile by one warp.  Lane l takes slot l % 8 of every 8-token
 // group and the 16-byte chunks l / 8, l / 8 + 4, ..., so that a load
 // instruction reads 512 contiguous bytes.  Per chunk it keeps the least k and
 // the least -k of each dim in the storage's own precision (bf16, or f16 for
@@ -55,34 +55,8 @@ __device__ __forceinline__ float2 widen2(uint32_t a) {
 // with the lower bounds (l % 8 < 4) or the negated upper bounds (l % 8 >= 4)
 // of a few dims over all tokens.  Bound by the read of the keys.
 template <int BS, bool FP8>
-__global__ void __launch_bounds__(kBoundWarps * 32) bounds_kernel(const BoundsParams p, int JM) {
-  pdl_wait();
-  pdl_launch_dependents();
-  const long long id = (long long)blockIdx.x * kBoundWarps + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  const long long per_b = (long long)JM * p.n_kv;
-  if (id >= per_b * p.B) return;
-  const int b = (int)(id / per_b), r = (int)(id % per_b);
-  const int jrel = r / p.n_kv, g = r % p.n_kv;
-  const int ctx = __ldg(p.ctx + b), p0 = p.pos ? __ldg(p.pos + b) : 0;
-  const bool first = jrel == 0 && g == 0 && lane == 0;
-  if (ctx < 0 || ctx > p.MB * BS) {
-    if (first) atomicOr(p.err, PGD_DEVERR_BAD_CONTEXT);
-    return;
-  }
-  if (p0 < 0 || p0 > ctx || ctx - p0 > p.T) {
-    if (first) atomicOr(p.err, PGD_DEVERR_BAD_POSITION);
-    return;
-  }
-  const int j = p0 / BS + jrel;
-  if (p0 == ctx || j * BS >= ctx) return;
-  const int blk = __ldg(p.tables + (size_t)b * p.MB + j);
-  if ((unsigned)blk >= (unsigned)p.NB) {
-    if (g == 0 && lane == 0) atomicOr(p.err, PGD_DEVERR_BAD_BLOCK_ID);
-    return;
-  }
-  const int valid = min(BS, ctx - j * BS);
-  const size_t tile = (size_t)blk * p.n_kv + g;
+__device__ __forceinline__ void tile_bounds(const BoundsParams &p, size_t tile, int valid,
+                                            int lane) {
   constexpr int NG = BS / 8;             // 8-token groups
   constexpr int NC = FP8 ? 2 : 4;        // chunks of a lane
   constexpr int ND2 = FP8 ? 8 : 4;       // pairs of dims in a chunk
@@ -175,6 +149,40 @@ __global__ void __launch_bounds__(kBoundWarps * 32) bounds_kernel(const BoundsPa
   if (lane == 0) p.bound_scales[tile] = pow2f(e);
 }
 
+// One warp per run of up to 32 blocks of a (sequence, KV head).
+template <int BS, bool FP8>
+__global__ void __launch_bounds__(kBoundWarps * 32)
+bounds_kernel(const BoundsParams p, int runs, int run) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const long long id = (long long)blockIdx.x * kBoundWarps + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  const long long per_b = (long long)runs * p.n_kv;
+  if (id >= per_b * p.B) return;
+  const int b = (int)(id / per_b), r = (int)(id % per_b);
+  const int jrel = r / p.n_kv * run, g = r % p.n_kv;
+  const int ctx = __ldg(p.ctx + b), p0 = p.pos ? __ldg(p.pos + b) : 0;
+  const bool first = jrel == 0 && g == 0 && lane == 0;
+  if (ctx < 0 || ctx > p.MB * BS) {
+    if (first) atomicOr(p.err, PGD_DEVERR_BAD_CONTEXT);
+    return;
+  }
+  if (p0 < 0 || p0 > ctx || ctx - p0 > p.T) {
+    if (first) atomicOr(p.err, PGD_DEVERR_BAD_POSITION);
+    return;
+  }
+  const int j0 = p0 / BS + jrel, jend = p0 == ctx ? 0 : (ctx + BS - 1) / BS;
+  const int n = min(run, jend - j0);
+  const int mine = lane < n ? __ldg(p.tables + (size_t)b * p.MB + j0 + lane) : 0;
+#pragma unroll 1
+  for (int i = 0; i < n; ++i) {
+    const int blk = __shfl_sync(kFullMask, mine, i);
+    if ((unsigned)blk < (unsigned)p.NB)
+      tile_bounds<BS, FP8>(p, (size_t)blk * p.n_kv + g, min(BS, ctx - (j0 + i) * BS), lane);
+    else if (g == 0 && lane == 0)
+      atomicOr(p.err, PGD_DEVERR_BAD_BLOCK_ID);
+  }
+}
 template <typename K, typename P, typename... A>
 cudaError_t launch_pdl(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t stream,
                        const P &p, A... more) {
@@ -507,17 +515,21 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
 
 cudaError_t block_bounds_launch(const BoundsParams &p, cudaStream_t stream) {
   if (p.B == 0 || p.T == 0) return cudaSuccess;
+  // Blocks a warp takes one after another: one for a few (latency), four for
+  // many, so that the chain of a warp's first loads (lengths, then block ids)
+  // is paid once for four tiles.
   const int JM = 1 + (p.T - 1 + p.bs - 1) / p.bs;
-  const long long items = (long long)p.B * JM * p.n_kv;
+  const int run = (long long)p.B * JM * p.n_kv > 16384 ? 4 : 1, runs = (JM + run - 1) / run;
+  const long long items = (long long)p.B * runs * p.n_kv;
   const long long grid = (items + kBoundWarps - 1) / kBoundWarps;
   if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
   const dim3 gd((unsigned)grid);
   const int nt = kBoundWarps * 32;
   if (p.k_scales)
-    return p.bs == 16 ? launch_pdl(bounds_kernel<16, true>, gd, nt, 0, stream, p, JM)
-                      : launch_pdl(bounds_kernel<32, true>, gd, nt, 0, stream, p, JM);
-  return p.bs == 16 ? launch_pdl(bounds_kernel<16, false>, gd, nt, 0, stream, p, JM)
-                    : launch_pdl(bounds_kernel<32, false>, gd, nt, 0, stream, p, JM);
+    return p.bs == 16 ? launch_pdl(bounds_kernel<16, true>, gd, nt, 0, stream, p, runs, run)
+                      : launch_pdl(bounds_kernel<32, true>, gd, nt, 0, stream, p, runs, run);
+  return p.bs == 16 ? launch_pdl(bounds_kernel<16, false>, gd, nt, 0, stream, p, runs, run)
+                    : launch_pdl(bounds_kernel<32, false>, gd, nt, 0, stream, p, runs, run);
 }
 
 // Blocks of a sequence that the selection holds keys for.

@@ -360,8 +360,10 @@ def _want_bounds(c, got, gs, blocks):
 
 @pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("n_kv,bs", [(1, 32), (5, 16)])
-@pytest.mark.parametrize("first", [None, [0, 0, 31, 16, 200, 33]], ids=["all", "from"])
-def test_bounds(fp8, n_kv, bs, first):
+@pytest.mark.parametrize("first,most", [(None, None), ([0, 0, 31, 16, 200, 33], 315),
+                                        ([0, 0, 31, 16, 200, 33], 1 << 17)],
+                         ids=["all", "from", "from_runs"])
+def test_bounds(fp8, n_kv, bs, first, most):
     ctx = [1, 16, 33, 17, 515, 33]
     c = bsc.make_cache(ctx, n_kv, bs, fp8=fp8, seed=bs + n_kv, scale_spread=6)
     if not fp8:  # zeros, tiny and huge keys
@@ -375,7 +377,7 @@ def test_bounds(fp8, n_kv, bs, first):
                                                             else first[b] // bs, -(-n // bs))
         if first is None or first[b] < n])
     pgd.block_bounds(got, gs, k, tables, lens, positions=None if first is None else _i32(first),
-                     max_tokens=None if first is None else 315, k_scales=ks)
+                     max_tokens=most, k_scales=ks)
     assert torch.equal(got.cpu(), want) and torch.equal(gs.cpu(), ws)
 
 
