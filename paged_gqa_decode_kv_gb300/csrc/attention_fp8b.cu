@@ -35,11 +35,15 @@
 // second one.  The reference moves when exceeded by 2^4: x <= 2^8, and 2^5
 // times a residual of x stays within E4M3's 448.
 //
-// Roles (384 threads): warps 0-3 softmax (thread t = token row t), 4 / 5 K / V
-// producers, 6 q.k^T issuer, 7 p.v issuer, 8-11 epilogue.  The K producer also
-// fetches both scales of every block of a stage into a 16-stage ring by
-// 4-byte asynchronous copies that count on the stage's own barrier, so no warp
-// waits for a dependent load.
+// Roles (512 threads): warps 0-3 and 12-15 softmax (thread t = token row t),
+// 4 / 5 K / V producers, 6 q.k^T issuer, 7 p.v issuer, 8-11 epilogue.  The two
+// softmax groups take alternate stages, each with a reference, sums and an
+// accumulator of its own that the epilogue merges: a stage's chain (barrier,
+// tensor-memory load, vote, exponentials, conversions) is longer than the time
+// HBM takes to deliver a stage, so one group alone sets the pace.  The K
+// producer also fetches both scales of every block of a stage into a 16-stage
+// ring by 4-byte asynchronous copies that count on the stage's own barrier, so
+// no warp waits for a dependent load.
 #include "attention_kernel.cuh"
 #include "kv_fp8b.cuh"
 
@@ -48,7 +52,9 @@ namespace tc8b {
 
 using namespace tc;
 
-constexpr int NTHREADS = 384;
+constexpr int NTHREADS = 512;
+constexpr int WARP_SM1 = 12;            // warps of the second softmax group
+constexpr uint32_t TMEM_COLS8 = 256;   // S 4 x 16; O 2 x 2 x 32 from column 64
 constexpr int GROUP = kGroupBytes8b;   // bytes of 8 tokens
 constexpr int STAGE = TOK * kHeadDim;  // K (or V) codes of a stage
 constexpr int NSK = 6, NSV = 6;        // ring depths
@@ -69,13 +75,13 @@ constexpr int OFF_Q = OFF_V + NSV * STAGE;  // double buffered by segment parity
 constexpr int OFF_P = OFF_Q + 2 * Q_BYTES;  // double buffered by stage parity
 constexpr int OFF_SC = OFF_P + 2 * P_BYTES8;           // f32 [NSR][2][8] (K, V) scales
 constexpr int OFF_BAR = OFF_SC + NSR * 2 * 8 * 4;
-constexpr int OFF_RED = OFF_BAR + 512;                 // f32 [2][4][8] warp maxima
-constexpr int OFF_LRED = OFF_RED + 2 * 4 * 8 * 4;      // f32 [2][4][8] warp sums
-constexpr int OFF_MREF = OFF_LRED + 2 * 4 * 8 * 4;     // f32 [2][8] references
-constexpr int OFF_QS = OFF_MREF + 2 * 8 * 4;           // f32 [2][8] query scales
+constexpr int OFF_RED = OFF_BAR + 512;                 // f32 [group][2][4][8] warp maxima
+constexpr int OFF_LRED = OFF_RED + 2 * 2 * 4 * 8 * 4;  // f32 [2][group][4][8] warp sums
+constexpr int OFF_MREF = OFF_LRED + 2 * 2 * 4 * 8 * 4;  // f32 [2][group][8] references
+constexpr int OFF_QS = OFF_MREF + 2 * 2 * 8 * 4;           // f32 [2][8] query scales
 constexpr int OFF_MERGE = OFF_QS + 64;                 // float2 [MERGE_PAIRS]
 constexpr int OFF_MISC = OFF_MERGE + MERGE_PAIRS * 8;
-constexpr int OFF_PRE = OFF_MISC + 192;                // int [B + 1]
+constexpr int OFF_PRE = OFF_MISC + 256;                // int [B + 1]
 
 constexpr size_t smem_size(int B) { return (size_t)SMEM_SLACK + OFF_PRE + (size_t)(B + 1) * 4; }
 static_assert(smem_size(PGD_MAX_BATCH) <= 232448, "layout exceeds 227 KB");
@@ -295,20 +301,13 @@ __global__ void __launch_bounds__(NTHREADS, 1) attention_fp8b_kernel(const Attn8
   int *nmax_slot = reinterpret_cast<int *>(smem + OFF_MISC + 20);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + OFF_MISC + 24);  // WaitCtl
   volatile int *stage_mask = reinterpret_cast<volatile int *>(smem + OFF_MISC + 40);  // [NSR]
-  int *over_flag = reinterpret_cast<int *>(smem + OFF_MISC + 112);  // [2][4] softmax votes
+  int *over_flag = reinterpret_cast<int *>(smem + OFF_MISC + 112);  // [group][2][4] votes
   int *pre = reinterpret_cast<int *>(smem + OFF_PRE);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (!p.wait_late) pdl_wait();
-  // As in attention_kernel.cuh: with no more units than CTAs, CTA c most
-  // likely streams unit c, whose first stages L2 is asked for meanwhile.
-  const bool pf_unit = p.prefetch_units && warp == WARP_KP && (int)blockIdx.x < p.B * p.n_kv;
-  int pf_ctx = 0, pf_blk = -1;
-  if (pf_unit) {
-    const int b = (int)blockIdx.x / p.n_kv;
-    pf_ctx = __ldg(p.ctx + b);
-    if (lane < kPrefetchBlocks<BS> && lane < p.MB) pf_blk = __ldg(p.tables + (size_t)b * p.MB + lane);
-  }
+  // The next kernel of the stream may take this one's place CTA by CTA; like
+  // this one it waits for its predecessor before it reads memory.
+  pdl_launch_dependents();
   if (tid == 0) {
     for (int i = 0; i < NSK; ++i) {
       mbar_init(&full_k[i], 1 + 32);  // the producer's arrival and each lane's scale copies
@@ -329,9 +328,9 @@ __global__ void __launch_bounds__(NTHREADS, 1) attention_fp8b_kernel(const Attn8
       mbar_init(&o_full[i], 1);
       mbar_init(&o_free[i], 4);
       mbar_init(&done[i], 1);
-      mbar_init(&seg_done[i], 4);
+      mbar_init(&seg_done[i], 8);
       mbar_init(&q_ready[i], 1);
-      mbar_init(&q_free[i], 1 + 4);
+      mbar_init(&q_free[i], 1 + 8);
     }
     mbar_init_fence();
     init_wait_ctl(smem + OFF_MISC + 24, p.wait_limit_ns);
@@ -342,6 +341,25 @@ __global__ void __launch_bounds__(NTHREADS, 1) attention_fp8b_kernel(const Attn8
     for (int i = tid; i < (2 * Q_BYTES + 2 * P_BYTES8) / 16; i += NTHREADS)
       z[i] = make_uint4(0, 0, 0, 0);
   }
+  if (warp == WARP_QK) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_addr(tmem_slot)),
+                 "r"(TMEM_COLS8)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  // Everything above touches only this CTA's own memory; what follows reads
+  // the caller's.
+  if (!p.wait_late) pdl_wait();
+  // As in attention_kernel.cuh: with no more units than CTAs, CTA c most
+  // likely streams unit c, whose first stages L2 is asked for meanwhile.
+  const bool pf_unit = p.prefetch_units && warp == WARP_KP && (int)blockIdx.x < p.B * p.n_kv;
+  int pf_ctx = 0, pf_blk = -1;
+  if (pf_unit) {
+    const int b = (int)blockIdx.x / p.n_kv;
+    pf_ctx = __ldg(p.ctx + b);
+    if (lane < kPrefetchBlocks<BS> && lane < p.MB) pf_blk = __ldg(p.tables + (size_t)b * p.MB + lane);
+  }
   const int max_tokens = p.MB * BS;
   bool bad_ctx = false;
   for (int b = tid; b < p.B; b += NTHREADS) {
@@ -351,13 +369,6 @@ __global__ void __launch_bounds__(NTHREADS, 1) attention_fp8b_kernel(const Attn8
     pre[b + 1] = nb > 0 ? nb + kSegCost<BS> : 0;
   }
   if (bad_ctx && blockIdx.x == 0) atomicOr(p.err, PGD_DEVERR_BAD_CONTEXT);
-  if (warp == WARP_QK) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                     smem_addr(tmem_slot)),
-                 "r"(TMEM_COLS)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-  }
   fence_proxy_async();
   __syncthreads();
   if (pf_unit) {
@@ -395,7 +406,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) attention_fp8b_kernel(const Attn8
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  auto col_o = [&](int ob) { return tmem + 64u + (uint32_t)ob * 32u; };
+  auto col_o = [&](int ob, int grp) { return tmem + 64u + (uint32_t)(ob * 2 + grp) * 32u; };
 
   // The split: whole units, or balanced cuts (the cost model of
   // attention_kernel.cuh with this cache's bytes per block).
@@ -498,9 +509,9 @@ __global__ void __launch_bounds__(NTHREADS, 1) attention_fp8b_kernel(const Attn8
 #pragma unroll
             for (int kt = 0; kt < 4; ++kt)
               if (kt < nkt)
-                umma_e4m3(col_o(ob), vd + (uint64_t)(kt * (4 * GROUP / 16)),
+                umma_e4m3(col_o(ob, sb), vd + (uint64_t)(kt * (4 * GROUP / 16)),
                           pd + (uint64_t)(kt * (4 * PGRP / 16)), IDESC_PV,
-                          (kt > 0 || st > 0) ? 1u : 0u);
+                          (kt > 0 || st > 1) ? 1u : 0u);
           }
           umma_commit(&empty_v[slot]);
           umma_commit(&p_free[sb]);
@@ -513,16 +524,18 @@ __global__ void __launch_bounds__(NTHREADS, 1) attention_fp8b_kernel(const Attn8
         mbar_wait_bounded(&done[1], 0);
       }
     }
-  } else if (warp < 4) {
+  } else if (warp < 4 || warp >= WARP_SM1) {
     // ----------------------------------------------------------- softmax
-    // Two stages an iteration: one maximum, one barrier and one decision to
-    // move the reference for 256 tokens.
-    const int t = tid;
-    const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
-    constexpr int SPI = 2, NCT = 128;
+    // Group grp takes the stages s with s % 2 == grp.
+    const int grp = warp < 4 ? 0 : 1;
+    const int t = tid & 127, gw = warp & 3;
+    const uint32_t lane_base = (uint32_t)(gw * 32) << 16;
+    constexpr int NCT = 128;
+    float *gred = red + grp * 2 * 4 * 8;
+    int *gvote = over_flag + grp * 2 * 4;
     SegCursor cur(sc);
     Segment sg, nsg;
-    int s = 0, k = 0, it = 0;
+    int s = 0, k = 0, it = 0;  // s: the segment's first stage
     bool have = cur.next(sc, p.B, sg);
     int ctx_b = have ? __ldg(p.ctx + sg.b) : 0;
     while (have) {
@@ -530,194 +543,162 @@ __global__ void __launch_bounds__(NTHREADS, 1) attention_fp8b_kernel(const Attn8
       const int ctx_n = have_next ? __ldg(p.ctx + nsg.b) : 0;
       const int nstages = (sg.n + SB - 1) / SB;
       const int ob = k & 1;
+      const int st0 = (s & 1) == grp ? 0 : 1;  // this group's first stage
       float m_ref[G], l_part[G], qsc[G];
+      wait_or_abort(&q_ready[k & 1], (uint32_t)(k >> 1) & 1u, abort_flag, p.err);
 #pragma unroll
-      for (int h = 0; h < G; ++h) { m_ref[h] = -INFINITY; l_part[h] = 0.f; qsc[h] = 0.f; }
-      for (int st = 0; st < nstages; st += SPI, ++it) {
-        const int n2 = min(SPI, nstages - st);
-        bool valid[SPI] = {};
-        int lim[SPI] = {};  // rows p.v reads: the valid length rounded up to 32
-        float ks[SPI] = {}, vs[SPI] = {};
-#pragma unroll
-        for (int u = 0; u < SPI; ++u) {
-          if (u < n2) {
-            const int su = s + u, sbu = su % NSB;
-            wait_or_abort(&s_full[sbu], (uint32_t)(su / NSB) & 1u, abort_flag, p.err);
-            wait_or_abort(&m_ready[sbu], (uint32_t)(su / NSB) & 1u, abort_flag, p.err);
-            const int msk = stage_mask[su & (NSR - 1)];
-            const int nb = min(SB, sg.n - (st + u) * SB);
-            int nvalid = nb * BS;
-            if (sg.j0 + (st + u) * SB + nb == sg.nblk) nvalid -= sg.nblk * BS - ctx_b;
-            valid[u] = (t < nvalid) && !((msk >> (t / BS)) & 1);
-            lim[u] = (nvalid + 31) & ~31;
-            ks[u] = scl[(su & (NSR - 1)) * 16 + t / BS];
-            vs[u] = scl[(su & (NSR - 1)) * 16 + 8 + t / BS];
-          }
-        }
+      for (int h = 0; h < G; ++h) {
+        m_ref[h] = -INFINITY;
+        l_part[h] = 0.f;
+        qsc[h] = qscale[(k & 1) * 8 + h] * p.qk_scale_log2;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_free[k & 1]);
+      for (int st = st0; st < nstages; st += 2, ++it) {
+        const int su = s + st, sbu = su % NSB;
+        wait_or_abort(&s_full[sbu], (uint32_t)(su / NSB) & 1u, abort_flag, p.err);
+        wait_or_abort(&m_ready[sbu], (uint32_t)(su / NSB) & 1u, abort_flag, p.err);
+        const int msk = stage_mask[su & (NSR - 1)];
+        const int nb = min(SB, sg.n - st * SB);
+        int nvalid = nb * BS;
+        if (sg.j0 + st * SB + nb == sg.nblk) nvalid -= sg.nblk * BS - ctx_b;
+        const bool valid = (t < nvalid) && !((msk >> (t / BS)) & 1);
+        const int lim = (nvalid + 31) & ~31;  // rows p.v reads
+        const float ks = scl[(su & (NSR - 1)) * 16 + t / BS];
+        const float vs = scl[(su & (NSR - 1)) * 16 + 8 + t / BS];
         tc_fence_after();
-        uint32_t sv[SPI][16];
-#pragma unroll
-        for (int u = 0; u < SPI; ++u)
-          if (u < n2) {
-            const uint32_t a0 = tmem + lane_base + col_s((s + u) % NSB);
-            tmem_ld8_async(a0, sv[u]);
-            tmem_ld8_async(a0 + 8, sv[u] + 8);
-          }
-#pragma unroll
-        for (int u = 0; u < SPI; ++u)
-          if (u < n2) {
-            tmem_wait8(sv[u]);
-            tmem_wait8(sv[u] + 8);
-          }
-        if (st == 0) {
-#pragma unroll
-          for (int h = 0; h < G; ++h) qsc[h] = qscale[(k & 1) * 8 + h] * p.qk_scale_log2;
-        }
+        uint32_t sv[16];
+        tmem_ld8_async(tmem + lane_base + col_s(sbu), sv);
+        tmem_ld8_async(tmem + lane_base + col_s(sbu) + 8, sv + 8);
+        tmem_wait8(sv);
+        tmem_wait8(sv + 8);
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&s_free[s % NSB]);
-          if (n2 > 1) mbar_arrive(&s_free[(s + 1) % NSB]);
-          if (st == 0) mbar_arrive(&q_free[k & 1]);
-        }
+        if (lane == 0) mbar_arrive(&s_free[sbu]);
         // scores in log2 units, and with the V scale's logarithm the weights
-        // that the reference bounds
-        float w[SPI][G], lv[SPI];
+        // that the reference bounds (a row that is not valid has w = -inf;
+        // 2^-120 keeps the logarithm finite whatever the ring holds)
+        const float lv = __log2f(fmaxf(vs, 0x1p-120f));
+        float w[G];
 #pragma unroll
-        for (int u = 0; u < SPI; ++u) {
-          lv[u] = __log2f(fmaxf(vs[u], 7.5e-37f));  // (2^-120: finite whatever the ring holds)
-#pragma unroll
-          for (int h = 0; h < G; ++h)
-            w[u][h] = valid[u] ? (__uint_as_float(sv[u][h]) + __uint_as_float(sv[u][8 + h])) *
-                                     (qsc[h] * ks[u])
-                               : -INFINITY;
-        }
-        // (a row that is not valid has w = -inf)
-        auto top = [&](int h) { return fmaxf(w[0][h] + lv[0], w[1][h] + lv[1]); };
+        for (int h = 0; h < G; ++h)
+          w[h] = valid ? (__uint_as_float(sv[h]) + __uint_as_float(sv[8 + h])) * (qsc[h] * ks)
+                       : -INFINITY;
         const int rb = it & 1;
-        bool move = true;  // (a segment's first iteration always sets it)
-        if (st > 0) {
+        bool move = true;  // (a segment's first stage always sets it)
+        if (st > st0) {
           bool over = false;
 #pragma unroll
-          for (int h = 0; h < G; ++h) over |= top(h) > m_ref[h] + kMoveLog2;
+          for (int h = 0; h < G; ++h) over |= w[h] + lv > m_ref[h] + kMoveLog2;
           const bool wover = __any_sync(kFullMask, over);
-          if (lane == 0) over_flag[rb * 4 + warp] = wover ? 1 : 0;
-          named_barrier_sync(1, NCT);
-          const int4 votes = *reinterpret_cast<const int4 *>(over_flag + rb * 4);
+          if (lane == 0) gvote[rb * 4 + gw] = wover ? 1 : 0;
+          named_barrier_sync(1 + 2 * grp, NCT);
+          const int4 votes = *reinterpret_cast<const int4 *>(gvote + rb * 4);
           move = (votes.x | votes.y | votes.z | votes.w) != 0;
         }
         if (move) {
           float v2[G];
 #pragma unroll
-          for (int h = 0; h < G; ++h) v2[h] = top(h);
+          for (int h = 0; h < G; ++h) v2[h] = w[h] + lv;
           const float wm = warp_reduce_heads<G, true>(v2, lane);
           constexpr int SH = 5 - kLog2<G>;
-          if ((lane & ((1 << SH) - 1)) == 0) red[(rb * 4 + warp) * 8 + (lane >> SH)] = wm;
-          named_barrier_sync(1, NCT);
+          if ((lane & ((1 << SH) - 1)) == 0) gred[(rb * 4 + gw) * 8 + (lane >> SH)] = wm;
+          named_barrier_sync(1 + 2 * grp, NCT);
           float alpha[TSTEP];
 #pragma unroll
           for (int h = 0; h < TSTEP; ++h) alpha[h] = 1.f;
 #pragma unroll
           for (int h = 0; h < G; ++h) {
-            const float tm = fmaxf(fmaxf(red[(rb * 4 + 0) * 8 + h], red[(rb * 4 + 1) * 8 + h]),
-                                   fmaxf(red[(rb * 4 + 2) * 8 + h], red[(rb * 4 + 3) * 8 + h]));
+            const float tm = fmaxf(fmaxf(gred[(rb * 4 + 0) * 8 + h], gred[(rb * 4 + 1) * 8 + h]),
+                                   fmaxf(gred[(rb * 4 + 2) * 8 + h], gred[(rb * 4 + 3) * 8 + h]));
             const float mn = fmaxf(m_ref[h], tm);
             alpha[h] = (m_ref[h] == -INFINITY) ? 0.f : exp2f(m_ref[h] - mn);
             m_ref[h] = mn;
             l_part[h] *= alpha[h];
           }
-          if (st > 0) {
-            wait_or_abort(&p_free[(s - 1) & 1], (uint32_t)((s - 1) >> 1) & 1u, abort_flag, p.err);
+          if (st > st0) {
+            // (the group's last p.v was that of stage su - 2)
+            wait_or_abort(&p_free[grp], (uint32_t)((su - 2) >> 1) & 1u, abort_flag, p.err);
             tc_fence_after();
 #pragma unroll
             for (int c8 = 0; c8 < NCOL / 8; ++c8) {
               float ov[8];
-              tmem_ld8(col_o(ob) + lane_base + 8 * c8, ov);
+              tmem_ld8(col_o(ob, grp) + lane_base + 8 * c8, ov);
 #pragma unroll
               for (int i = 0; i < 8; ++i) ov[i] *= alpha[(8 * c8 + i) % TSTEP];
-              tmem_st8(col_o(ob) + lane_base + 8 * c8, ov);
+              tmem_st8(col_o(ob, grp) + lane_base + 8 * c8, ov);
             }
             tc_fence_before();
           }
         }
+        // A weight's three terms, two heads a conversion.
+        constexpr int HP = G == 1 ? 2 : G;
+        uint32_t word[3][(TSTEP + 3) / 4];
 #pragma unroll
-        for (int u = 0; u < SPI; ++u) {
-          if (u < n2) {
-            const int su = s + u, pbuf = su & 1;
-            // A weight's three terms: hi, lo, lo2 (bytes h of three words
-            // groups).  Two heads a conversion.
-            constexpr int HP = G == 1 ? 2 : G;
-            uint32_t word[3][(TSTEP + 3) / 4];
+        for (int i = 0; i < 3; ++i)
 #pragma unroll
-            for (int i = 0; i < 3; ++i)
+          for (int j = 0; j < (TSTEP + 3) / 4; ++j) word[i][j] = 0;
+        const float unit = vs * kWeightUnit;
 #pragma unroll
-              for (int j = 0; j < (TSTEP + 3) / 4; ++j) word[i][j] = 0;
-            const float unit = valid[u] ? vs[u] * kWeightUnit : 0.f;
-#pragma unroll
-            for (int h = 0; h < HP; h += 2) {
-              float x0 = 0.f, x1 = 0.f;
-              if (valid[u]) {
-                const float p0 = exp2_approx(w[u][h] - m_ref[h]);
-                l_part[h] += p0;
-                x0 = p0 * unit;
-                if (h + 1 < G) {
-                  const float p1 = exp2_approx(w[u][h + 1 < G ? h + 1 : h] -
-                                               m_ref[h + 1 < G ? h + 1 : h]);
-                  l_part[h + 1 < G ? h + 1 : h] += p1;
-                  x1 = p1 * unit;
-                }
-              }
-#pragma unroll
-              for (int i = 0; i < 3; ++i) {
-                const uint16_t c = e4m3x2(x0, x1);
-                word[i][h >> 2] |= (uint32_t)c << ((h & 2) * 8);
-                if (i < 2) {
-                  const float2 back = e4m3x2_to_float2(c);
-                  x0 = (x0 - back.x) * kTerm;
-                  x1 = (x1 - back.y) * kTerm;
-                }
-              }
-            }
-            wait_or_abort(&p_free[pbuf], ((uint32_t)(su >> 1) & 1u) ^ 1u, abort_flag, p.err);
-            unsigned char *dst = smem + OFF_P + pbuf * P_BYTES8 + (t >> 3) * PGRP + (t & 7) * 16;
-            if constexpr (TSTEP == 4) {
-              *reinterpret_cast<uint4 *>(dst) = make_uint4(word[0][0], word[1][0], word[2][0], 0);
-            } else {
-              *reinterpret_cast<uint4 *>(dst) =
-                  make_uint4(word[0][0], word[0][1], word[1][0], word[1][1]);
-              *reinterpret_cast<uint4 *>(dst + 128) = make_uint4(word[2][0], word[2][1], 0, 0);
-            }
-            if (!valid[u] && t < lim[u]) {
-              // rows that p.v reads but that hold no token (the tail of the
-              // last block, a block whose id was bad): their codes may be NaN
-              const int vslot = su % NSV;
-              wait_or_abort(&full_v[vslot], (uint32_t)(su / NSV) & 1u, abort_flag, p.err);
-              uint4 *vrow = reinterpret_cast<uint4 *>(smem + OFF_V + vslot * STAGE +
-                                                      (t >> 3) * GROUP + (t & 7) * 16);
-#pragma unroll
-              for (int c = 0; c < 8; ++c) vrow[c * 8] = make_uint4(0, 0, 0, 0);
+        for (int h = 0; h < HP; h += 2) {
+          float x0 = 0.f, x1 = 0.f;
+          if (valid) {
+            const float p0 = exp2_approx(w[h] - m_ref[h]);
+            l_part[h] += p0;
+            x0 = p0 * unit;
+            if (h + 1 < G) {
+              const float p1 = exp2_approx(w[h + 1 < G ? h + 1 : h] - m_ref[h + 1 < G ? h + 1 : h]);
+              l_part[h + 1 < G ? h + 1 : h] += p1;
+              x1 = p1 * unit;
             }
           }
+#pragma unroll
+          for (int i = 0; i < 3; ++i) {
+            const uint16_t c = e4m3x2(x0, x1);
+            word[i][h >> 2] |= (uint32_t)c << ((h & 2) * 8);
+            if (i < 2) {
+              const float2 back = e4m3x2_to_float2(c);
+              x0 = (x0 - back.x) * kTerm;
+              x1 = (x1 - back.y) * kTerm;
+            }
+          }
+        }
+        wait_or_abort(&p_free[grp], ((uint32_t)(su >> 1) & 1u) ^ 1u, abort_flag, p.err);
+        unsigned char *dst = smem + OFF_P + grp * P_BYTES8 + (t >> 3) * PGRP + (t & 7) * 16;
+        if constexpr (TSTEP == 4) {
+          *reinterpret_cast<uint4 *>(dst) = make_uint4(word[0][0], word[1][0], word[2][0], 0);
+        } else {
+          *reinterpret_cast<uint4 *>(dst) =
+              make_uint4(word[0][0], word[0][1], word[1][0], word[1][1]);
+          *reinterpret_cast<uint4 *>(dst + 128) = make_uint4(word[2][0], word[2][1], 0, 0);
+        }
+        if (!valid && t < lim) {
+          // rows that p.v reads but that hold no token (the tail of the last
+          // block, a block whose id was bad): their codes may be NaN
+          const int vslot = su % NSV;
+          wait_or_abort(&full_v[vslot], (uint32_t)(su / NSV) & 1u, abort_flag, p.err);
+          uint4 *vrow = reinterpret_cast<uint4 *>(smem + OFF_V + vslot * STAGE +
+                                                  (t >> 3) * GROUP + (t & 7) * 16);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) vrow[c * 8] = make_uint4(0, 0, 0, 0);
         }
         fence_proxy_async();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&p_full[s & 1]);
-          if (n2 > 1) mbar_arrive(&p_full[(s + 1) & 1]);
-        }
-        s += n2;
+        if (lane == 0) mbar_arrive(&p_full[grp]);
       }
-      // the segment's references and per-warp sums, for the epilogue
+      s += nstages;
+      // the group's references and per-warp sums, for the epilogue
       wait_or_abort(&o_free[ob], ((uint32_t)(k >> 1) & 1u) ^ 1u, abort_flag, p.err);
       {
         const float ws = warp_reduce_heads<G, false>(l_part, lane);
         constexpr int SH = 5 - kLog2<G>;
-        if ((lane & ((1 << SH) - 1)) == 0) lred[(ob * 4 + warp) * 8 + (lane >> SH)] = ws;
+        if ((lane & ((1 << SH) - 1)) == 0)
+          lred[((ob * 2 + grp) * 4 + gw) * 8 + (lane >> SH)] = ws;
       }
       if (t == 0) {
 #pragma unroll
-        for (int h = 0; h < G; ++h) mref[ob * 8 + h] = m_ref[h];
+        for (int h = 0; h < G; ++h) mref[(ob * 2 + grp) * 8 + h] = m_ref[h];
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&seg_done[ob]);
@@ -726,7 +707,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) attention_fp8b_kernel(const Attn8
       ctx_b = ctx_n;
       have = have_next;
     }
-  } else if (warp >= WARP_EPI) {
+  } else {
     // ---------------------------------------------------------- epilogue
     const int e = tid - 32 * WARP_EPI;  // head-dim row of O
     const int ew = warp - WARP_EPI;
@@ -740,27 +721,41 @@ __global__ void __launch_bounds__(NTHREADS, 1) attention_fp8b_kernel(const Attn8
       const int ob = k & 1;
       const int unit = sg.b * p.n_kv + sg.g;
       wait_or_abort(&seg_done[ob], (uint32_t)(k >> 1) & 1u, abort_flag, p.err);
-      float Lsum[G], M[G];
+      // the two softmax groups' states merged (a group without stages, or
+      // with none of its rows valid, has the reference -inf and no weight; its
+      // accumulator was perhaps never written)
+      float Lsum[G], M[G], f0[G], f1[G];
 #pragma unroll
       for (int h = 0; h < G; ++h) {
-        Lsum[h] = (lred[(ob * 4 + 0) * 8 + h] + lred[(ob * 4 + 1) * 8 + h]) +
-                  (lred[(ob * 4 + 2) * 8 + h] + lred[(ob * 4 + 3) * 8 + h]);
-        M[h] = mref[ob * 8 + h];
+        const float m0 = mref[ob * 16 + h], m1 = mref[ob * 16 + 8 + h];
+        M[h] = fmaxf(m0, m1);
+        f0[h] = m0 == -INFINITY ? 0.f : exp2f(m0 - M[h]);
+        f1[h] = m1 == -INFINITY ? 0.f : exp2f(m1 - M[h]);
+        const float *l0 = lred + ob * 64 + h, *l1 = l0 + 32;
+        Lsum[h] = f0[h] * ((l0[0] + l0[8]) + (l0[16] + l0[24])) +
+                  f1[h] * ((l1[0] + l1[8]) + (l1[16] + l1[24]));
       }
       wait_or_abort(&o_full[ob], (uint32_t)(k >> 1) & 1u, abort_flag, p.err);
       tc_fence_after();
-      float o[NCOL];
+      float ov[G];
 #pragma unroll
-      for (int c8 = 0; c8 < 3 * TSTEP / 8 + (TSTEP == 4 ? 1 : 0); ++c8)
-        tmem_ld8(col_o(ob) + lane_base + 8 * c8, *reinterpret_cast<float(*)[8]>(o + 8 * c8));
+      for (int grp = 0; grp < 2; ++grp) {
+        float o[NCOL];
+#pragma unroll
+        for (int c8 = 0; c8 < (3 * TSTEP + 7) / 8; ++c8)
+          tmem_ld8(col_o(ob, grp) + lane_base + 8 * c8,
+                   *reinterpret_cast<float(*)[8]>(o + 8 * c8));
+#pragma unroll
+        for (int h = 0; h < G; ++h) {
+          const float f = grp ? f1[h] : f0[h];
+          const float x = fmaf(fmaf(o[2 * TSTEP + h], 1.f / kTerm, o[TSTEP + h]), 1.f / kTerm, o[h]);
+          const float y = f != 0.f ? x * (f * (1.f / kWeightUnit)) : 0.f;
+          ov[h] = grp ? ov[h] + y : y;
+        }
+      }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&o_free[ob]);
-      float ov[G];
-#pragma unroll
-      for (int h = 0; h < G; ++h)
-        ov[h] = fmaf(fmaf(o[2 * TSTEP + h], 1.f / kTerm, o[TSTEP + h]), 1.f / kTerm, o[h]) *
-                (1.f / kWeightUnit);
 
       const bool whole = sg.j0 == 0 && sg.n == sg.nblk;
       const long long c_first = sc.units ? (long long)part : sc.part_of(sg.ucs + sc.ov);
@@ -791,7 +786,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) attention_fp8b_kernel(const Attn8
         }
         named_barrier_sync(2, NET);
         if (flag[0])
-          merge_parts<G, false>(p.part_o, p.part_ml, p.out, unit, flag[1], flag[2], obase, p.lg_gh,
+          merge_parts<G, true>(p.part_o, p.part_ml, p.out, unit, flag[1], flag[2], obase, p.lg_gh,
                                 p.n_q, G, e, reinterpret_cast<float2 *>(smem + OFF_MERGE));
         named_barrier_sync(2, NET);
       }
@@ -804,7 +799,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) attention_fp8b_kernel(const Attn8
   tc_fence_after();
   if (warp == WARP_QK) {
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
-                 "r"(TMEM_COLS)
+                 "r"(TMEM_COLS8)
                  : "memory");
   }
 }
