@@ -79,8 +79,7 @@ constexpr int OFF_RED = OFF_BAR + 512;                 // f32 [group][2][4][8] w
 constexpr int OFF_LRED = OFF_RED + 2 * 2 * 4 * 8 * 4;  // f32 [2][group][4][8] warp sums
 constexpr int OFF_MREF = OFF_LRED + 2 * 2 * 4 * 8 * 4;  // f32 [2][group][8] references
 constexpr int OFF_QS = OFF_MREF + 2 * 2 * 8 * 4;           // f32 [2][8] query scales
-constexpr int OFF_MERGE = OFF_QS + 64;                 // float2 [MERGE_PAIRS]
-constexpr int OFF_MISC = OFF_MERGE + MERGE_PAIRS * 8;
+constexpr int OFF_MISC = OFF_QS + 64;
 constexpr int OFF_PRE = OFF_MISC + 256;                // int [B + 1]
 
 constexpr size_t smem_size(int B) { return (size_t)SMEM_SLACK + OFF_PRE + (size_t)(B + 1) * 4; }
@@ -92,8 +91,10 @@ static_assert((OFF_MISC + 24) % 8 == 0, "WaitCtl alignment");
 static_assert(NSR >= NSK + NSB && (NSR & (NSR - 1)) == 0, "scale and mask rings");
 static_assert(40 + 4 * NSR <= 112 && OFF_MISC % 16 == 0, "misc layout");
 
-// One CTA streams at most about 1/kShare of the HBM rate.
-constexpr long long kShare = 104;
+// One CTA streams at most about 1/kShare of the HBM rate: 0.58 us a stage with
+// 32-token tiles, 0.65 with 16-token ones (twice the bulk copies).
+template <int BS> constexpr long long kShare = BS == 16 ? 145 : 129;
+constexpr int MERGE_U = 20;  // parts of a unit that a merging thread has in flight
 
 // kind::f8f6f4, D f32, A and B E4M3, both MN-major, M = 128.
 __host__ __device__ constexpr uint32_t idesc_pv(int n) {
@@ -262,6 +263,49 @@ __device__ __forceinline__ void produce(const Attn8bParams &pp, const Schedule &
   }
 }
 
+// A unit's partial states (unit, first part, parts) merged by log-sum-exp into
+// its output rows by the whole CTA: a quarter of it takes every fourth head,
+// thread e dim e, the loads of MERGE_U parts in flight together.
+template <int G>
+__device__ __forceinline__ void merge_unit(const AttnParams &p, const int4 &m, int tid) {
+  const int e = tid & 127;
+  const size_t row0 = ((size_t)m.x + (size_t)m.y) * G;
+  const size_t obase = q_index(p, m.x / p.n_kv, m.x % p.n_kv, 0);
+#pragma unroll 1
+  for (int h = tid >> 7; h < G; h += NTHREADS / 128) {
+    float M = -INFINITY, L = 0.f, O = 0.f;
+#pragma unroll 1
+    for (int i0 = 0; i0 < m.z; i0 += MERGE_U) {
+      float2 ml[MERGE_U];
+      float o[MERGE_U];
+#pragma unroll
+      for (int i = 0; i < MERGE_U; ++i) {
+        ml[i] = make_float2(-INFINITY, 0.f);
+        o[i] = 0.f;
+        if (i0 + i < m.z) {
+          const size_t row = row0 + (size_t)(i0 + i) * G + h;
+          ml[i] = __ldcg(reinterpret_cast<const float2 *>(p.part_ml) + row);
+          o[i] = __ldcg(p.part_o + row * kHeadDim + e);
+        }
+      }
+      float mx = M;
+#pragma unroll
+      for (int i = 0; i < MERGE_U; ++i) mx = fmaxf(mx, ml[i].x);
+      const float c = M == -INFINITY ? 0.f : exp2f(M - mx);
+      L *= c;
+      O *= c;
+      M = mx;
+#pragma unroll
+      for (int i = 0; i < MERGE_U; ++i) {
+        const float f = ml[i].x == -INFINITY ? 0.f : exp2f(ml[i].x - mx);
+        L = fmaf(f, ml[i].y, L);
+        O = fmaf(f, o[i], O);
+      }
+    }
+    p.out[(obase + h) * kHeadDim + e] = __float2bfloat16_rn(O / L);
+  }
+}
+
 template <int G, int BS>
 __global__ void __launch_bounds__(NTHREADS, 1) attention_fp8b_kernel(const Attn8bParams pp) {
   const AttnParams &p = pp.a;
@@ -297,43 +341,40 @@ __global__ void __launch_bounds__(NTHREADS, 1) attention_fp8b_kernel(const Attn8
   float *qscale = reinterpret_cast<float *>(smem + OFF_QS);
   const float *scl = reinterpret_cast<const float *>(smem + OFF_SC);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + OFF_MISC);
-  volatile int *flag = reinterpret_cast<volatile int *>(smem + OFF_MISC + 8);  // [3]
+  int *n_merges = reinterpret_cast<int *>(smem + OFF_MISC + 8);
   int *nmax_slot = reinterpret_cast<int *>(smem + OFF_MISC + 20);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + OFF_MISC + 24);  // WaitCtl
   volatile int *stage_mask = reinterpret_cast<volatile int *>(smem + OFF_MISC + 40);  // [NSR]
   int *over_flag = reinterpret_cast<int *>(smem + OFF_MISC + 112);  // [group][2][4] votes
+  int4 *merges = reinterpret_cast<int4 *>(smem + OFF_MISC + 176);  // [2] unit, first part, parts
   int *pre = reinterpret_cast<int *>(smem + OFF_PRE);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // The next kernel of the stream may take this one's place CTA by CTA; like
   // this one it waits for its predecessor before it reads memory.
   pdl_launch_dependents();
-  if (tid == 0) {
-    for (int i = 0; i < NSK; ++i) {
-      mbar_init(&full_k[i], 1 + 32);  // the producer's arrival and each lane's scale copies
-      mbar_init(&empty_k[i], 1);
-    }
-    for (int i = 0; i < NSV; ++i) {
-      mbar_init(&full_v[i], 1);
-      mbar_init(&empty_v[i], 1);
-    }
-    for (int i = 0; i < NSB; ++i) {
-      mbar_init(&s_full[i], 1);
-      mbar_init(&s_free[i], 4);
-      mbar_init(&m_ready[i], 1);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&p_full[i], 4);
-      mbar_init(&p_free[i], 1);
-      mbar_init(&o_full[i], 1);
-      mbar_init(&o_free[i], 4);
-      mbar_init(&done[i], 1);
-      mbar_init(&seg_done[i], 8);
-      mbar_init(&q_ready[i], 1);
-      mbar_init(&q_free[i], 1 + 8);
+  if (warp == 0) {
+    // Arrivals a barrier expects, in the order of the arrays above: 33 = the
+    // producer's and each lane's scale copies, 4 and 8 = softmax warps, 9 =
+    // those and the q.k^T issuer.
+    constexpr int N_BARS = 2 * NSK + 2 * NSV + 3 * NSB + 8 * 2;
+    static_assert(N_BARS * 8 <= 512, "barriers");
+    for (int i = lane; i < N_BARS; i += 32) {
+      constexpr int S0 = 2 * NSK + 2 * NSV, P0 = S0 + 3 * NSB;
+      uint32_t n = 1;
+      if (i < NSK) n = 1 + 32;                          // full_k
+      else if (i >= S0 + NSB && i < S0 + 2 * NSB) n = 4;  // s_free
+      else if (i >= P0 && i < P0 + 2) n = 4;            // p_full
+      else if (i >= P0 + 6 && i < P0 + 8) n = 4;        // o_free
+      else if (i >= P0 + 10 && i < P0 + 12) n = 1 + 8;  // q_free
+      else if (i >= P0 + 14) n = 8;                     // seg_done
+      mbar_init(&bars[i], n);
     }
     mbar_init_fence();
-    init_wait_ctl(smem + OFF_MISC + 24, p.wait_limit_ns);
+    if (lane == 0) {
+      *n_merges = 0;
+      init_wait_ctl(smem + OFF_MISC + 24, p.wait_limit_ns);
+    }
   }
   // Query rows and weight columns that belong to no head stay zero.
   {
@@ -422,11 +463,11 @@ __global__ void __launch_bounds__(NTHREADS, 1) attention_fp8b_kernel(const Attn8
     constexpr long long kBlockBytes = 2ll * BS * kHeadDim;
     constexpr long long m0 = kMergeFixedBytes / kBlockBytes, m1 = kMergePartBytes / kBlockBytes;
     const long long grid = (long long)gridDim.x;
-    long long P = (long long)sqrtf((float)kShare * (float)sc.X * (float)U / (float)m1);
+    long long P = (long long)sqrtf((float)kShare<BS> * (float)sc.X * (float)U / (float)m1);
     P = max(1ll, min(P, sc.P));
-    const long long cost_cut = max((sc.X + P - 1) / P * kShare, sc.X) + m0 + m1 * ((P + U - 1) / U);
+    const long long cost_cut = max((sc.X + P - 1) / P * kShare<BS>, sc.X) + m0 + m1 * ((P + U - 1) / U);
     sc.P = P;
-    if (U <= grid && max(nmax * kShare, sc.X) <= cost_cut) {
+    if (U <= grid && max(nmax * kShare<BS>, sc.X) <= cost_cut) {
       sc.units = true;
       sc.P = U;
     }
@@ -773,22 +814,20 @@ __global__ void __launch_bounds__(NTHREADS, 1) attention_fp8b_kernel(const Attn8
         for (int h = 0; h < G; ++h)
           if (e == h)
             *reinterpret_cast<float2 *>(p.part_ml + (srow + h) * 2) = make_float2(M[h], Lsum[h]);
-        // publish this part; the last of the unit's parts to arrive merges
+        // Publish this part; the CTA of the unit's last part to arrive merges
+        // them, once all its warps are done (a CTA's part holds at most two
+        // cut units: its first and its last).  The barrier orders the 128
+        // threads' stores before the atomic, whose release makes them visible
+        // and whose acquire, in the last arriver, the other parts'.
         named_barrier_sync(2, NET);
         if (e == 0) {
           const int n_parts = (int)(c_last - c_first + 1);
-          const int before = atomic_add_acq_rel_gpu(p.counters + unit, 1);
-          const int last = (before == n_parts - 1);
-          if (last) atomicExch(p.counters + unit, 0);
-          flag[0] = last;
-          flag[1] = (int)c_first;
-          flag[2] = n_parts;
+          if (atomic_add_acq_rel_gpu(p.counters + unit, 1) == n_parts - 1) {
+            atomicExch(p.counters + unit, 0);  // ready for the next call
+            merges[*n_merges] = make_int4(unit, (int)c_first, n_parts, 0);
+            ++*n_merges;
+          }
         }
-        named_barrier_sync(2, NET);
-        if (flag[0])
-          merge_parts<G, true>(p.part_o, p.part_ml, p.out, unit, flag[1], flag[2], obase, p.lg_gh,
-                                p.n_q, G, e, reinterpret_cast<float2 *>(smem + OFF_MERGE));
-        named_barrier_sync(2, NET);
       }
       ++k;
     }
@@ -797,6 +836,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) attention_fp8b_kernel(const Attn8
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  for (int i = 0; i < *n_merges; ++i) merge_unit<G>(p, merges[i], tid);
   if (warp == WARP_QK) {
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
                  "r"(TMEM_COLS8)
