@@ -502,7 +502,8 @@ pgd_status pgd_append_decode_attention_fp8(void *out, const void *q, const void 
  * of those names over this cache -- same definition on the dequantised K and
  * V, same arguments (and the scales), checks, errors and workspace
  * (pgd_attention_workspace_size).  The append is pgd_kv_append_fp8b of one
- * token at context_lens[b] - 1.  The query must be finite. */
+ * token at context_lens[b] - 1.  The query must be finite.  B * n_kv *
+ * (MB + 24) must be below 2^31. */
 pgd_status pgd_kv_append_fp8b(const void *k_new, const void *v_new, void *k_cache, void *v_cache,
                               float *k_scales, float *v_scales, const int32_t *block_tables,
                               const int32_t *positions, const int32_t *token_starts, int32_t B,

@@ -1291,6 +1291,14 @@ static pgd_status check_scales(const float *k_scales, const float *v_scales) {
   return PGD_OK;
 }
 
+// The block-scaled attention's cost space (blocks, and up to 24 for each unit)
+// is 32 bits wide.
+static pgd_status check_cost_space(int32_t B, int32_t n_kv, int32_t MB) {
+  if ((long long)B * n_kv * ((long long)MB + 24) > 0x7fffffffLL)
+    return fail(PGD_ERR_UNSUPPORTED, "B * n_kv * (MB + 24) >= 2^31");
+  return PGD_OK;
+}
+
 static pgd_status kv8b_range_call(bool write, const void *k_rows, const void *v_rows,
                                   const void *k_cache, const void *v_cache, const float *k_scales,
                                   const float *v_scales, const int32_t *tables,
@@ -1368,6 +1376,7 @@ static pgd_status launch_attention_fp8b(void *out, const void *q, const void *k_
                                         cudaStream_t stream) {
   pgd_status s = check_scales(k_scales, v_scales);
   if (s != PGD_OK) return s;
+  if ((s = check_cost_space(B, n_kv, MB)) != PGD_OK) return s;
   PreparedAttention pa;
   s = prepare_attention(out, q, k_cache, v_cache, tables, ctx, B, n_q, n_kv, bs, MB, NB, scale,
                         num_splits, workspace, workspace_bytes, &pa, true);
@@ -1579,7 +1588,9 @@ static pgd_status selected_attention(void *out, const void *q, const void *k_cac
                            NB * n_kv, scale, num_splits);
   if (s != PGD_OK) return s;
   const bool fp8b = k_scales != nullptr || v_scales != nullptr;
-  if (fp8b && (s = check_scales(k_scales, v_scales)) != PGD_OK) return s;
+  if (fp8b && ((s = check_scales(k_scales, v_scales)) != PGD_OK ||
+               (s = check_cost_space(U, 1, W)) != PGD_OK))
+    return s;
   if (B == 0) return ok();
   PreparedAttention pa;  // (checks the workspace; nothing is enqueued)
   s = prepare_attention(out, q, k_cache, v_cache, tiles, tile_tokens, U, G, 1, bs, W, NB * n_kv,

@@ -5,11 +5,11 @@
 //   out[b][h] = sum_t softmax_t(scale * q[b][h] . k_t) v_t,  t < ctx[b],
 //   k_t = sk[tile] * E4M3(code), v_t = sv[tile] * E4M3(code)
 //
-// The schedule (units, cost-balanced cuts over CTAs, last-arriver merge), the
-// roles and the bounded waits are those of attention_kernel.cuh, whose
-// helpers this kernel uses; what differs is the arithmetic of a stage of 128
-// tokens, two E4M3 contractions with tokens on the M side (A) resp. the K
-// side, fp32 accumulators in tensor memory:
+// The schedule (units, cost-balanced cuts over CTAs, last-arriver merge) and
+// the bounded waits are those of attention_kernel.cuh, whose helpers this
+// kernel uses; what differs is the arithmetic of a stage of 128 tokens, two
+// E4M3 contractions with tokens on the M side (A) resp. the K side, fp32
+// accumulators in tensor memory:
 //   S^T[128 tok][16]   = Kc[128 tok][128 d]    . Q^T[128 d][16]
 //   O^T[128 d][NP]    += Vc^T[128 d][128 tok]  . P^T[128 tok][NP]
 //
@@ -36,7 +36,8 @@
 // times a residual of x stays within E4M3's 448.
 //
 // Roles (512 threads): warps 0-3 and 12-15 softmax (thread t = token row t),
-// 4 / 5 K / V producers, 6 q.k^T issuer, 7 p.v issuer, 8-11 epilogue.  The two
+// 4 / 5 K / V producers, 6 query conversion and q.k^T issuer, 7 p.v issuer,
+// 8-11 epilogue.  The two
 // softmax groups take alternate stages, each with a reference, sums and an
 // accumulator of its own that the epilogue merges: a stage's chain (barrier,
 // tensor-memory load, vote, exponentials, conversions) is longer than the time
@@ -44,6 +45,12 @@
 // producer also fetches both scales of every block of a stage into a 16-stage
 // ring by 4-byte asynchronous copies that count on the stage's own barrier, so
 // no warp waits for a dependent load.
+//
+// Start.  What lies between the wait for the previous kernel and the first
+// copy is on the path of every call (6 us of it at first), so it is kept to
+// the context lengths, one scan, 32-bit arithmetic and the block ids, which
+// are guessed and loaded beside the lengths; the query is converted beside the
+// first copies, by the warp that needs it.
 #include "attention_kernel.cuh"
 #include "kv_fp8b.cuh"
 
@@ -78,8 +85,9 @@ constexpr int OFF_BAR = OFF_SC + NSR * 2 * 8 * 4;
 constexpr int OFF_RED = OFF_BAR + 512;                 // f32 [group][2][4][8] warp maxima
 constexpr int OFF_LRED = OFF_RED + 2 * 2 * 4 * 8 * 4;  // f32 [2][group][4][8] warp sums
 constexpr int OFF_MREF = OFF_LRED + 2 * 2 * 4 * 8 * 4;  // f32 [2][group][8] references
-constexpr int OFF_QS = OFF_MREF + 2 * 2 * 8 * 4;           // f32 [2][8] query scales
-constexpr int OFF_MISC = OFF_QS + 64;
+constexpr int OFF_QS = OFF_MREF + 2 * 2 * 8 * 4;           // f32 [NQS][8] query scales
+constexpr int NQS = 8;  // (the issuer is at most NSB + 1 segments ahead of the softmax)
+constexpr int OFF_MISC = OFF_QS + NQS * 8 * 4;
 constexpr int OFF_PRE = OFF_MISC + 256;                // int [B + 1]
 
 constexpr size_t smem_size(int B) { return (size_t)SMEM_SLACK + OFF_PRE + (size_t)(B + 1) * 4; }
@@ -113,92 +121,122 @@ __device__ __forceinline__ void arrive_after_copies(uint64_t *bar) {
                : "memory");
 }
 
+// The CTAs' parts of the cost space: Schedule and SegCursor of
+// attention_kernel.cuh in 32 bits (the host refuses calls whose cost space
+// does not fit).
+struct Cuts {
+  int X, P;        // cost of all units, parts
+  int q, r;        // X / P, X % P
+  bool units;      // part c = unit c
+  const int *pre;  // cost of one head of the sequences before b
+  int n_kv, ov;
+  __device__ __forceinline__ int cut(int i) const {  // X * i / P
+    return q * i + (P <= 65535 ? (int)(((unsigned)r * (unsigned)i) / (unsigned)P)
+                               : (int)(((unsigned long long)r * (unsigned)i) / (unsigned)P));
+  }
+  // the part that holds cost position x (for units that are cut)
+  __device__ __forceinline__ int part_of(int x) const {
+    return (int)(((unsigned long long)P * ((unsigned)x + 1u) - 1u) / (unsigned)X);
+  }
+};
+
+struct Piece {  // blocks j0 .. j0 + n - 1 of the nblk of unit (b, g), at cost [ucs, uce)
+  int b, g, j0, nblk, n, ucs, uce;
+};
+
+struct Walk {
+  int x, end, b, g;
+  __device__ __forceinline__ Walk(const Cuts &sc) {
+    x = end = 0;
+    b = -1;
+    g = 0;
+    const int c = (int)blockIdx.x;
+    if (c >= sc.P) return;
+    if (sc.units) {
+      const int sb = c / sc.n_kv, sg = c - sb * sc.n_kv;
+      const int cost = sc.pre[sb + 1] - sc.pre[sb];
+      x = sc.n_kv * sc.pre[sb] + sg * cost;
+      end = x + cost;
+    } else {
+      x = sc.cut(c);
+      end = sc.cut(c + 1);
+    }
+  }
+  __device__ __forceinline__ bool next(const Cuts &sc, int B, Piece &sg) {
+    const int *pre = sc.pre;
+    while (x < end) {
+      if (b < 0) {
+        int lo = 0, hi = B - 1;  // largest b with n_kv * pre[b] <= x
+        while (lo < hi) {
+          const int mid = (lo + hi + 1) >> 1;
+          if (sc.n_kv * pre[mid] <= x) lo = mid; else hi = mid - 1;
+        }
+        b = lo;
+        g = (x - sc.n_kv * pre[b]) / (pre[b + 1] - pre[b]);
+      } else if (++g == sc.n_kv) {
+        g = 0;
+        do { ++b; } while (b < B - 1 && pre[b + 1] == pre[b]);
+      }
+      const int cost = pre[b + 1] - pre[b];
+      const int ucs = sc.n_kv * pre[b] + g * cost, uce = ucs + cost;
+      const int e = min(end, uce);
+      const int j0 = max(0, x - ucs - sc.ov), j1 = max(0, e - ucs - sc.ov);
+      x = e;
+      if (j1 > j0) {
+        sg.b = b;
+        sg.g = g;
+        sg.j0 = j0;
+        sg.nblk = cost - sc.ov;
+        sg.n = j1 - j0;
+        sg.ucs = ucs;
+        sg.uce = uce;
+        return true;
+      }
+    }
+    return false;
+  }
+};
+
+// Block ids of a segment: entries lane and 32 + lane of what is left of it.
+struct Ids {
+  int tab, tab_next;
+};
+
 // One producer warp: walks the CTA's stages and copies one tile per lane.
-// The K producer also copies the blocks' scales, records which blocks of a
-// stage had an invalid id and writes each segment's query (high parts in rows
-// 0-7, low parts in rows 8-15, one power-of-two scale per head).  Table
-// entries and queries are loaded one step ahead.
-template <int G, int BS, bool IS_K>
-__device__ __forceinline__ void produce(const Attn8bParams &pp, const Schedule &sc,
+// The K producer also copies the blocks' scales and records which blocks of a
+// stage had an invalid id.  Block ids are loaded one step ahead; `guess` has
+// those of the start of sequence guess_b.
+template <int BS, bool IS_K>
+__device__ __forceinline__ void produce(const Attn8bParams &pp, const Cuts &sc,
                                         unsigned char *smem, uint64_t *full, uint64_t *empty,
-                                        volatile int *stage_mask, float *qscale,
-                                        uint64_t *q_ready, uint64_t *q_free,
-                                        volatile int *abort_flag, int lane) {
+                                        volatile int *stage_mask, volatile int *abort_flag,
+                                        int guess_b, const Ids &guess, int lane) {
   const AttnParams &p = pp.a;
   constexpr int SB = TOK / BS;
   constexpr uint32_t TILE = BS * kHeadDim;
   constexpr int NS = IS_K ? NSK : NSV;
-  constexpr int QPL = (16 * G + 31) / 32;  // 16-byte pieces of q per lane
   const unsigned char *cache = IS_K ? p.k_cache : p.v_cache;
   unsigned char *ring = smem + (IS_K ? OFF_K : OFF_V);
   const uint32_t sring = smem_addr(smem + OFF_SC);
   const uint64_t policy = l2_policy_evict_first();
-
-  struct Ahead {
-    uint4 q[QPL];
-    int tab, tab_next;
-  };
-  auto load_ahead = [&](const Segment &g, Ahead &a) {
-    if (IS_K) {
-#pragma unroll
-      for (int i = 0; i < QPL; ++i) {
-        const int j = lane + 32 * i, r = j >> 4, c = j & 15;
-        a.q[i] = j < 16 * G ? __ldg(reinterpret_cast<const uint4 *>(
-                                  p.q + q_index(p, g.b, g.g, r) * kHeadDim + c * 8))
-                            : make_uint4(0, 0, 0, 0);
-      }
-    }
+  auto load_ids = [&](const Piece &g, Ids &a) {
     const int32_t *trow = p.tables + (size_t)g.b * p.MB + g.j0;
     a.tab = (lane < g.n) ? __ldg(trow + lane) : 0;
     a.tab_next = (32 + lane < g.n) ? __ldg(trow + 32 + lane) : 0;
   };
-
-  SegCursor cur(sc);
-  Segment sg, nsg;
-  Ahead cur_a{}, next_a{};
+  Walk cur(sc);
+  Piece sg, nsg;
+  Ids ids = guess, next_ids{};
   bool have = cur.next(sc, p.B, sg);
-  if (have) load_ahead(sg, cur_a);
+  if (have && !(sg.b == guess_b && sg.j0 == 0)) load_ids(sg, ids);
   if (p.wait_late == 1) pdl_wait();  // the append has written the cache
-  int s = 0, k = 0;
+  int s = 0;
   bool stop = false;
   while (have && !stop) {
     const bool have_next = cur.next(sc, p.B, nsg);
-    if (have_next) load_ahead(nsg, next_a);
-    if (IS_K) {
-      const int qb = k & 1;
-      if (lane == 0)
-        wait_or_abort(&q_free[qb], ((uint32_t)(k >> 1) & 1u) ^ 1u, abort_flag, p.err);
-      __syncwarp();
-      unsigned char *qdst = smem + OFF_Q + qb * Q_BYTES;
-#pragma unroll
-      for (int i = 0; i < QPL; ++i) {
-        const int j = lane + 32 * i, r = j >> 4, c = j & 15;
-        float f[8];
-        unpack8(cur_a.q[i], f);
-        float a = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) a = fmaxf(a, fabsf(f[e]));
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(kFullMask, a, o));
-        // the query's scale 2^(e - 7), e its largest element's exponent: the
-        // elements keep their bits and the largest lands in [128, 256)
-        const int e = max((int)((__float_as_uint(a) >> 23) & 0xffu) - 127, -119);
-        if (j < 16 * G) {
-          uint2 hi, lo;
-          q_hi_lo(cur_a.q[i], pow2f(7 - e), hi, lo);
-          const int off = (c >> 1) * 128 + (c & 1) * 8;
-          *reinterpret_cast<uint2 *>(qdst + r * 16 + off) = hi;
-          *reinterpret_cast<uint2 *>(qdst + 8 * 128 + r * 16 + off) = lo;
-          if (c == 0) qscale[qb * 8 + r] = pow2f(e - 7);
-        }
-      }
-      fence_proxy_async();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&q_ready[qb]);
-    }
-    ++k;
+    if (have_next) load_ids(nsg, next_ids);
     const int32_t *trow = p.tables + (size_t)sg.b * p.MB + sg.j0;
-    int tab = cur_a.tab, tab_next = cur_a.tab_next;
+    int tab = ids.tab, tab_next = ids.tab_next;
     int tchunk = 0;
     const int nstages = (sg.n + SB - 1) / SB;
     for (int st = 0; st < nstages; ++st, ++s) {
@@ -250,7 +288,7 @@ __device__ __forceinline__ void produce(const Attn8bParams &pp, const Schedule &
       if (IS_K) arrive_after_copies(&full[slot]);
     }
     sg = nsg;
-    cur_a = next_a;
+    ids = next_ids;
     have = have_next;
   }
   // no copy may still be landing when the CTA exits
@@ -261,6 +299,50 @@ __device__ __forceinline__ void produce(const Attn8bParams &pp, const Schedule &
         atomicOr(p.err, PGD_DEVERR_TIMEOUT);
     }
   }
+}
+
+// A segment's query rows by one warp: 16-byte pieces lane + 32 i, piece c of
+// row r; then as E4M3 high parts in rows 0-7 and low parts in rows 8-15 of
+// the B operand, with one power-of-two scale a head.
+template <int G> constexpr int kPieces = (16 * G + 31) / 32;
+template <int G>
+__device__ __forceinline__ void load_query(const AttnParams &p, const Piece &g, int lane,
+                                           uint4 (&q)[kPieces<G>]) {
+#pragma unroll
+  for (int i = 0; i < kPieces<G>; ++i) {
+    const int j = lane + 32 * i, r = j >> 4, c = j & 15;
+    q[i] = j < 16 * G ? __ldg(reinterpret_cast<const uint4 *>(
+                            p.q + q_index(p, g.b, g.g, r) * kHeadDim + c * 8))
+                      : make_uint4(0, 0, 0, 0);
+  }
+}
+template <int G>
+__device__ __forceinline__ void write_query(const uint4 (&q)[kPieces<G>], unsigned char *qdst,
+                                            float *qscale, int lane) {
+#pragma unroll
+  for (int i = 0; i < kPieces<G>; ++i) {
+    const int j = lane + 32 * i, r = j >> 4, c = j & 15;
+    float f[8];
+    unpack8(q[i], f);
+    float a = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) a = fmaxf(a, fabsf(f[e]));
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(kFullMask, a, o));
+    // the scale 2^(e - 7), e the largest element's exponent: the elements
+    // keep their bits and the largest lands in [128, 256)
+    const int e = max((int)((__float_as_uint(a) >> 23) & 0xffu) - 127, -119);
+    if (j < 16 * G) {
+      uint2 hi, lo;
+      q_hi_lo(q[i], pow2f(7 - e), hi, lo);
+      const int off = (c >> 1) * 128 + (c & 1) * 8;
+      *reinterpret_cast<uint2 *>(qdst + r * 16 + off) = hi;
+      *reinterpret_cast<uint2 *>(qdst + 8 * 128 + r * 16 + off) = lo;
+      if (c == 0) qscale[r] = pow2f(e - 7);
+    }
+  }
+  fence_proxy_async();
+  __syncwarp();
 }
 
 // A unit's partial states (unit, first part, parts) merged by log-sum-exp into
@@ -331,9 +413,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) attention_fp8b_kernel(const Attn8
   uint64_t *p_free = p_full + 2;        // [2]
   uint64_t *o_full = p_free + 2;        // [2]
   uint64_t *o_free = o_full + 2;        // [2]
-  uint64_t *q_ready = o_free + 2;       // [2]
-  uint64_t *q_free = q_ready + 2;       // [2]
-  uint64_t *done = q_free + 2;          // [2]
+  uint64_t *done = o_free + 2;          // [2]
   uint64_t *seg_done = done + 2;        // [2]
   float *red = reinterpret_cast<float *>(smem + OFF_RED);
   float *lred = reinterpret_cast<float *>(smem + OFF_LRED);
@@ -342,11 +422,11 @@ __global__ void __launch_bounds__(NTHREADS, 1) attention_fp8b_kernel(const Attn8
   const float *scl = reinterpret_cast<const float *>(smem + OFF_SC);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + OFF_MISC);
   int *n_merges = reinterpret_cast<int *>(smem + OFF_MISC + 8);
-  int *nmax_slot = reinterpret_cast<int *>(smem + OFF_MISC + 20);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + OFF_MISC + 24);  // WaitCtl
   volatile int *stage_mask = reinterpret_cast<volatile int *>(smem + OFF_MISC + 40);  // [NSR]
   int *over_flag = reinterpret_cast<int *>(smem + OFF_MISC + 112);  // [group][2][4] votes
   int4 *merges = reinterpret_cast<int4 *>(smem + OFF_MISC + 176);  // [2] unit, first part, parts
+  int2 *warp_sum = reinterpret_cast<int2 *>(smem + OFF_RED);  // (before the softmax)
   int *pre = reinterpret_cast<int *>(smem + OFF_PRE);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -355,9 +435,9 @@ __global__ void __launch_bounds__(NTHREADS, 1) attention_fp8b_kernel(const Attn8
   pdl_launch_dependents();
   if (warp == 0) {
     // Arrivals a barrier expects, in the order of the arrays above: 33 = the
-    // producer's and each lane's scale copies, 4 and 8 = softmax warps, 9 =
-    // those and the q.k^T issuer.
-    constexpr int N_BARS = 2 * NSK + 2 * NSV + 3 * NSB + 8 * 2;
+    // producer's and each lane's scale copies, 4 and 8 = softmax or epilogue
+    // warps.
+    constexpr int N_BARS = 2 * NSK + 2 * NSV + 3 * NSB + 6 * 2;
     static_assert(N_BARS * 8 <= 512, "barriers");
     for (int i = lane; i < N_BARS; i += 32) {
       constexpr int S0 = 2 * NSK + 2 * NSV, P0 = S0 + 3 * NSB;
@@ -366,8 +446,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) attention_fp8b_kernel(const Attn8
       else if (i >= S0 + NSB && i < S0 + 2 * NSB) n = 4;  // s_free
       else if (i >= P0 && i < P0 + 2) n = 4;            // p_full
       else if (i >= P0 + 6 && i < P0 + 8) n = 4;        // o_free
-      else if (i >= P0 + 10 && i < P0 + 12) n = 1 + 8;  // q_free
-      else if (i >= P0 + 14) n = 8;                     // seg_done
+      else if (i >= P0 + 10) n = 8;                     // seg_done
       mbar_init(&bars[i], n);
     }
     mbar_init_fence();
@@ -392,55 +471,59 @@ __global__ void __launch_bounds__(NTHREADS, 1) attention_fp8b_kernel(const Attn8
   // Everything above touches only this CTA's own memory; what follows reads
   // the caller's.
   if (!p.wait_late) pdl_wait();
-  // As in attention_kernel.cuh: with no more units than CTAs, CTA c most
-  // likely streams unit c, whose first stages L2 is asked for meanwhile.
-  const bool pf_unit = p.prefetch_units && warp == WARP_KP && (int)blockIdx.x < p.B * p.n_kv;
-  int pf_ctx = 0, pf_blk = -1;
-  if (pf_unit) {
-    const int b = (int)blockIdx.x / p.n_kv;
-    pf_ctx = __ldg(p.ctx + b);
-    if (lane < kPrefetchBlocks<BS> && lane < p.MB) pf_blk = __ldg(p.tables + (size_t)b * p.MB + lane);
+  // The producers' guess: CTA c streams unit c from its first block (so it
+  // does with no more units than CTAs, unless the units are cut).
+  int guess_b = -1;
+  Ids guess{};
+  if ((warp == WARP_KP || warp == WARP_VP) && (int)blockIdx.x < p.B * p.n_kv) {
+    guess_b = (int)blockIdx.x / p.n_kv;
+    const int32_t *trow = p.tables + (size_t)guess_b * p.MB;
+    if (lane < p.MB) guess.tab = __ldg(trow + lane);
+    if (32 + lane < p.MB) guess.tab_next = __ldg(trow + 32 + lane);
   }
+  // Blocks of every sequence (thread t takes `per` of them from t * per), and
+  // their exclusive prefix over the batch.
   const int max_tokens = p.MB * BS;
+  const int per = (p.B + NTHREADS - 1) / NTHREADS;
+  int cost[PGD_MAX_BATCH / NTHREADS];
+  int sum = 0, longest = 0;
   bool bad_ctx = false;
-  for (int b = tid; b < p.B; b += NTHREADS) {
-    const int c = p.ctx[b];
-    int nb = 0;
-    if (c >= 1 && c <= max_tokens) nb = (c + BS - 1) / BS; else bad_ctx = true;
-    pre[b + 1] = nb > 0 ? nb + kSegCost<BS> : 0;
+#pragma unroll
+  for (int i = 0; i < PGD_MAX_BATCH / NTHREADS; ++i) {
+    const int b = tid * per + i;
+    cost[i] = 0;
+    if (i < per && b < p.B) {
+      const int c = __ldg(p.ctx + b);
+      if (c >= 1 && c <= max_tokens) cost[i] = (c + BS - 1) / BS + kSegCost<BS>; else bad_ctx = true;
+    }
+    sum += cost[i];
+    longest = max(longest, cost[i]);
   }
   if (bad_ctx && blockIdx.x == 0) atomicOr(p.err, PGD_DEVERR_BAD_CONTEXT);
+  int upto = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(kFullMask, upto, o);
+    if (lane >= o) upto += v;
+  }
+  longest = __reduce_max_sync(kFullMask, longest);
+  if (lane == 31) warp_sum[warp] = make_int2(upto, longest);
   fence_proxy_async();
   __syncthreads();
-  if (pf_unit) {
-    const int g = (int)blockIdx.x % p.n_kv;
-    const int nb = (pf_ctx >= 1 && pf_ctx <= max_tokens) ? (pf_ctx + BS - 1) / BS : 0;
-    if (nb >= 4 * kPrefetchBlocks<BS> && lane < kPrefetchBlocks<BS> &&
-        (unsigned)pf_blk < (unsigned)p.NB) {
-      const size_t off = ((size_t)pf_blk * p.n_kv + g) * (BS * kHeadDim);
-      bulk_prefetch_l2(p.k_cache + off, BS * kHeadDim);
-      bulk_prefetch_l2(p.v_cache + off, BS * kHeadDim);
-    }
+  int before = upto - sum;
+#pragma unroll
+  for (int w = 0; w < NTHREADS / 32; ++w) {
+    const int2 v = warp_sum[w];
+    if (w < warp) before += v.x;
+    longest = max(longest, v.y);
   }
-  if (warp == 0) {
-    int carry = 0, longest = 0;
-    for (int base = 0; base < p.B; base += 32) {
-      const int i = base + lane;
-      int v = (i < p.B) ? pre[i + 1] : 0;
-      longest = max(longest, v);
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int n = __shfl_up_sync(kFullMask, v, o);
-        if (lane >= o) v += n;
-      }
-      if (i < p.B) pre[i + 1] = v + carry;
-      carry += __shfl_sync(kFullMask, v, 31);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) longest = max(longest, __shfl_xor_sync(kFullMask, longest, o));
-    if (lane == 0) {
-      pre[0] = 0;
-      *nmax_slot = longest;
+  for (int i = 0; i < PGD_MAX_BATCH / NTHREADS; ++i) {
+    const int b = tid * per + i;
+    if (i < per && b < p.B) {
+      pre[b] = before;
+      before += cost[i];
+      if (b == p.B - 1) pre[p.B] = before;
     }
   }
   tc_fence_before();
@@ -451,49 +534,59 @@ __global__ void __launch_bounds__(NTHREADS, 1) attention_fp8b_kernel(const Attn8
 
   // The split: whole units, or balanced cuts (the cost model of
   // attention_kernel.cuh with this cache's bytes per block).
-  Schedule sc;
-  sc.X = (long long)p.n_kv * pre[p.B];
+  Cuts sc;
+  sc.X = p.n_kv * pre[p.B];
   sc.pre = pre;
   sc.n_kv = p.n_kv;
   sc.ov = kSegCost<BS>;
-  sc.P = sc.X < (long long)gridDim.x ? sc.X : (long long)gridDim.x;
+  sc.P = min(sc.X, (int)gridDim.x);
   sc.units = false;
   if (p.auto_split && sc.X > 0) {
-    const long long U = (long long)p.B * p.n_kv, nmax = *nmax_slot;
-    constexpr long long kBlockBytes = 2ll * BS * kHeadDim;
-    constexpr long long m0 = kMergeFixedBytes / kBlockBytes, m1 = kMergePartBytes / kBlockBytes;
-    const long long grid = (long long)gridDim.x;
-    long long P = (long long)sqrtf((float)kShare<BS> * (float)sc.X * (float)U / (float)m1);
-    P = max(1ll, min(P, sc.P));
-    const long long cost_cut = max((sc.X + P - 1) / P * kShare<BS>, sc.X) + m0 + m1 * ((P + U - 1) / U);
+    const int U = p.B * p.n_kv;
+    constexpr float kBlockBytes = 2.f * BS * kHeadDim;
+    constexpr float m0 = (float)kMergeFixedBytes / kBlockBytes;
+    constexpr float m1 = (float)kMergePartBytes / kBlockBytes;
+    const float X = (float)sc.X;
+    const int P = max(1, min(sc.P, (int)sqrtf(kShare<BS> * X * (float)U / m1)));
+    const float cost_cut = fmaxf(X / (float)P * kShare<BS>, X) + m0 + m1 * (float)((P + U - 1) / U);
     sc.P = P;
-    if (U <= grid && max(nmax * kShare<BS>, sc.X) <= cost_cut) {
+    if (U <= (int)gridDim.x && fmaxf((float)longest * kShare<BS>, X) <= cost_cut) {
       sc.units = true;
       sc.P = U;
     }
   }
+  sc.q = sc.P > 0 ? sc.X / sc.P : 0;
+  sc.r = sc.X - sc.q * sc.P;
 
   if (warp == WARP_KP) {
-    produce<G, BS, true>(pp, sc, smem, full_k, empty_k, stage_mask, qscale, q_ready, q_free,
-                         abort_flag, lane);
+    produce<BS, true>(pp, sc, smem, full_k, empty_k, stage_mask, abort_flag, guess_b, guess, lane);
   } else if (warp == WARP_VP) {
-    produce<G, BS, false>(pp, sc, smem, full_v, empty_v, nullptr, nullptr, nullptr, nullptr,
-                          abort_flag, lane);
+    produce<BS, false>(pp, sc, smem, full_v, empty_v, nullptr, abort_flag, guess_b, guess, lane);
   } else if (warp == WARP_QK) {
-    // ---------------------------------------------------- q.k^T issuer
-    if (lane == 0) {
-      const uint32_t q_base = smem_addr(smem + OFF_Q);
-      SegCursor cur(sc);
-      Segment sg;
-      int s = 0, k = 0;
-      while (cur.next(sc, p.B, sg)) {
-        const int nstages = (sg.n + SB - 1) / SB;
-        wait_or_abort(&q_ready[k & 1], (uint32_t)(k >> 1) & 1u, abort_flag, p.err);
-        const uint64_t qd = smem_desc(q_base + (uint32_t)((k & 1) * Q_BYTES), 128, 1024, 0);
-        for (int st = 0; st < nstages; ++st, ++s) {
-          const int slot = s % NSK, sb = s % NSB;
-          wait_or_abort(&full_k[slot], (uint32_t)(s / NSK) & 1u, abort_flag, p.err);
-          wait_or_abort(&s_free[sb], ((uint32_t)(s / NSB) & 1u) ^ 1u, abort_flag, p.err);
+    // ------------------------------ query conversion, then q.k^T (one lane)
+    Walk cur(sc);
+    Piece sg, nsg;
+    bool have = cur.next(sc, p.B, sg);
+    uint4 q[kPieces<G>];
+    if (have) load_query<G>(p, sg, lane, q);
+    int s = 0, k = 0, last1 = -1, last2 = -1;  // last stages of segments k - 1, k - 2
+    while (have) {
+      const int nstages = (sg.n + SB - 1) / SB;
+      // Query buffer k % 2 was read by the MMAs of segment k - 2: they are done
+      // if the softmax has freed their last S buffer for a stage since, else
+      // that buffer's barrier is still in their phase.
+      if (last2 >= 0 && last1 - last2 < NSB)
+        wait_or_abort(&s_full[last2 % NSB], (uint32_t)(last2 / NSB) & 1u, abort_flag, p.err);
+      unsigned char *qbuf = smem + OFF_Q + (k & 1) * Q_BYTES;
+      write_query<G>(q, qbuf, qscale + (k & (NQS - 1)) * 8, lane);
+      const bool have_next = cur.next(sc, p.B, nsg);
+      if (have_next) load_query<G>(p, nsg, lane, q);
+      if (lane == 0) {
+        const uint64_t qd = smem_desc(smem_addr(qbuf), 128, 1024, 0);
+        for (int st = 0; st < nstages; ++st) {
+          const int su = s + st, slot = su % NSK, sb = su % NSB;
+          wait_or_abort(&full_k[slot], (uint32_t)(su / NSK) & 1u, abort_flag, p.err);
+          wait_or_abort(&s_free[sb], ((uint32_t)(su / NSB) & 1u) ^ 1u, abort_flag, p.err);
           tc_fence_after();
           if (!*abort_flag) {
             // K core matrices 128 B apart along d, token groups 1024 B apart;
@@ -507,22 +600,27 @@ __global__ void __launch_bounds__(NTHREADS, 1) attention_fp8b_kernel(const Attn8
           umma_commit(&s_full[sb]);
           umma_commit(&empty_k[slot]);
           // the stage's invalid-block mask and scales, which full_k ordered
-          // before this, for the softmax
+          // before this, and the query's scales, for the softmax
           mbar_arrive(&m_ready[sb]);
         }
-        umma_commit(&q_free[k & 1]);
-        ++k;
       }
-      if (s > 0) {
-        umma_commit(&done[0]);
-        mbar_wait_bounded(&done[0], 0);
-      }
+      __syncwarp();
+      s += nstages;
+      last2 = last1;
+      last1 = s - 1;
+      ++k;
+      sg = nsg;
+      have = have_next;
+    }
+    if (lane == 0 && s > 0) {
+      umma_commit(&done[0]);
+      mbar_wait_bounded(&done[0], 0);
     }
   } else if (warp == WARP_PV) {
     // ------------------------------------------------------- p.v issuer
     if (lane == 0) {
-      SegCursor cur(sc);
-      Segment sg;
+      Walk cur(sc);
+      Piece sg;
       int s = 0, k = 0;
       while (cur.next(sc, p.B, sg)) {
         const int ctx_b = __ldg(p.ctx + sg.b);
@@ -574,8 +672,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) attention_fp8b_kernel(const Attn8
     constexpr int NCT = 128;
     float *gred = red + grp * 2 * 4 * 8;
     int *gvote = over_flag + grp * 2 * 4;
-    SegCursor cur(sc);
-    Segment sg, nsg;
+    Walk cur(sc);
+    Piece sg, nsg;
     int s = 0, k = 0, it = 0;  // s: the segment's first stage
     bool have = cur.next(sc, p.B, sg);
     int ctx_b = have ? __ldg(p.ctx + sg.b) : 0;
@@ -586,15 +684,12 @@ __global__ void __launch_bounds__(NTHREADS, 1) attention_fp8b_kernel(const Attn8
       const int ob = k & 1;
       const int st0 = (s & 1) == grp ? 0 : 1;  // this group's first stage
       float m_ref[G], l_part[G], qsc[G];
-      wait_or_abort(&q_ready[k & 1], (uint32_t)(k >> 1) & 1u, abort_flag, p.err);
 #pragma unroll
       for (int h = 0; h < G; ++h) {
         m_ref[h] = -INFINITY;
         l_part[h] = 0.f;
-        qsc[h] = qscale[(k & 1) * 8 + h] * p.qk_scale_log2;
+        qsc[h] = 0.f;
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&q_free[k & 1]);
       for (int st = st0; st < nstages; st += 2, ++it) {
         const int su = s + st, sbu = su % NSB;
         wait_or_abort(&s_full[sbu], (uint32_t)(su / NSB) & 1u, abort_flag, p.err);
@@ -607,6 +702,10 @@ __global__ void __launch_bounds__(NTHREADS, 1) attention_fp8b_kernel(const Attn8
         const int lim = (nvalid + 31) & ~31;  // rows p.v reads
         const float ks = scl[(su & (NSR - 1)) * 16 + t / BS];
         const float vs = scl[(su & (NSR - 1)) * 16 + 8 + t / BS];
+        if (st == st0) {
+#pragma unroll
+          for (int h = 0; h < G; ++h) qsc[h] = qscale[(k & (NQS - 1)) * 8 + h] * p.qk_scale_log2;
+        }
         tc_fence_after();
         uint32_t sv[16];
         tmem_ld8_async(tmem + lane_base + col_s(sbu), sv);
@@ -754,8 +853,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) attention_fp8b_kernel(const Attn8
     const int ew = warp - WARP_EPI;
     const uint32_t lane_base = (uint32_t)(ew * 32) << 16;
     constexpr int NET = 128;
-    SegCursor cur(sc);
-    Segment sg;
+    Walk cur(sc);
+    Piece sg;
     const int part = (int)blockIdx.x;
     int k = 0;
     while (cur.next(sc, p.B, sg)) {
@@ -799,8 +898,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) attention_fp8b_kernel(const Attn8
       if (lane == 0) mbar_arrive(&o_free[ob]);
 
       const bool whole = sg.j0 == 0 && sg.n == sg.nblk;
-      const long long c_first = sc.units ? (long long)part : sc.part_of(sg.ucs + sc.ov);
-      const long long c_last = sc.units ? (long long)part : sc.part_of(sg.uce - 1);
+      const int c_first = sc.units ? part : sc.part_of(sg.ucs + sc.ov);
+      const int c_last = sc.units ? part : sc.part_of(sg.uce - 1);
       const size_t obase = q_index(p, sg.b, sg.g, 0);
       if (whole) {
 #pragma unroll
@@ -821,10 +920,10 @@ __global__ void __launch_bounds__(NTHREADS, 1) attention_fp8b_kernel(const Attn8
         // and whose acquire, in the last arriver, the other parts'.
         named_barrier_sync(2, NET);
         if (e == 0) {
-          const int n_parts = (int)(c_last - c_first + 1);
+          const int n_parts = c_last - c_first + 1;
           if (atomic_add_acq_rel_gpu(p.counters + unit, 1) == n_parts - 1) {
             atomicExch(p.counters + unit, 0);  // ready for the next call
-            merges[*n_merges] = make_int4(unit, (int)c_first, n_parts, 0);
+            merges[*n_merges] = make_int4(unit, c_first, n_parts, 0);
             ++*n_merges;
           }
         }

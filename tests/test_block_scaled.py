@@ -134,6 +134,7 @@ def _attend(L, append=False, **kw):
     (dict(scale=float("nan")), _native.ERR_INVALID_ARG), (dict(q=None), _native.ERR_INVALID_ARG),
     (dict(k=24), _native.ERR_INVALID_ARG), (dict(splits=-1), _native.ERR_INVALID_ARG),
     (dict(ks=None), _native.ERR_INVALID_ARG), (dict(vs=2), _native.ERR_INVALID_ARG),
+    (dict(B=2048, n_kv=8, MB=(1 << 17) - 23), _native.ERR_UNSUPPORTED),
     (dict(ws=None), _native.ERR_WORKSPACE), (dict(ws=256, wsb=16), _native.ERR_WORKSPACE),
     (dict(ws=264, wsb=1 << 30), _native.ERR_WORKSPACE),
 ], ids=lambda x: str(x))
