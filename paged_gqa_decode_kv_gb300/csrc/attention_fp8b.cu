@@ -37,8 +37,7 @@
 //
 // Roles (512 threads): warps 0-3 and 12-15 softmax (thread t = token row t),
 // 4 / 5 K / V producers, 6 query conversion and q.k^T issuer, 7 p.v issuer,
-// 8-11 epilogue.  The two
-// softmax groups take alternate stages, each with a reference, sums and an
+// 8-11 epilogue.  The two softmax groups take alternate stages, each with a reference, sums and an
 // accumulator of its own that the epilogue merges: a stage's chain (barrier,
 // tensor-memory load, vote, exponentials, conversions) is longer than the time
 // HBM takes to deliver a stage, so one group alone sets the pace.  The K
@@ -51,6 +50,10 @@
 // the context lengths, one scan, 32-bit arithmetic and the block ids, which
 // are guessed and loaded beside the lengths; the query is converted beside the
 // first copies, by the warp that needs it.
+#include <cuda.h>
+
+#include <atomic>
+
 #include "attention_kernel.cuh"
 #include "kv_fp8b.cuh"
 
@@ -58,6 +61,13 @@ namespace pgd {
 namespace tc8b {
 
 using namespace tc;
+
+// The launch's parameters: K and V pools as tensors of NB * n_kv rows (tiles)
+// of bs * 16 8-byte elements, read in boxes of one row by 256.
+struct Params {
+  Attn8bParams q8;
+  CUtensorMap k_map, v_map;
+};
 
 constexpr int NTHREADS = 512;
 constexpr int WARP_SM1 = 12;            // warps of the second softmax group
@@ -99,9 +109,9 @@ static_assert((OFF_MISC + 24) % 8 == 0, "WaitCtl alignment");
 static_assert(NSR >= NSK + NSB && (NSR & (NSR - 1)) == 0, "scale and mask rings");
 static_assert(40 + 4 * NSR <= 112 && OFF_MISC % 16 == 0, "misc layout");
 
-// One CTA streams at most about 1/kShare of the HBM rate: 0.58 us a stage with
-// 32-token tiles, 0.65 with 16-token ones (twice the bulk copies).
-template <int BS> constexpr long long kShare = BS == 16 ? 145 : 129;
+// One CTA streams at most about 1/kShare of the HBM rate (128 of 152 CTAs take
+// the whole of it: 0.58 us a stage).
+constexpr float kShare = 126.f;
 constexpr int MERGE_U = 20;  // parts of a unit that a merging thread has in flight
 
 // kind::f8f6f4, D f32, A and B E4M3, both MN-major, M = 128.
@@ -113,6 +123,18 @@ __host__ __device__ constexpr uint32_t idesc_pv(int n) {
 // 4 bytes from global to shared memory, asynchronously.
 __device__ __forceinline__ void copy4_async(uint32_t dst, const void *src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+// Four tiles' 2 KiB runs at element x (of 8 bytes) into `dst`, one behind the
+// other: rows t0 .. t3 of the pool as a two-dimensional tensor.  A row outside
+// the pool arrives as zeros.
+__device__ __forceinline__ void gather_tiles(void *dst, const CUtensorMap *map, int x, int t0,
+                                             int t1, int t2, int t3, uint64_t *bar,
+                                             uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8;" ::"r"(smem_addr(dst)),
+      "l"(map), "r"(x), "r"(t0), "r"(t1), "r"(t2), "r"(t3), "r"(smem_addr(bar)), "l"(policy)
+      : "memory");
 }
 // Arrive on `bar` (one of its expected arrivals) once this thread's earlier
 // asynchronous copies have landed.
@@ -146,95 +168,102 @@ struct Piece {  // blocks j0 .. j0 + n - 1 of the nblk of unit (b, g), at cost [
 
 struct Walk {
   int x, end, b, g;
-  __device__ __forceinline__ Walk(const Cuts &sc) {
-    x = end = 0;
-    b = -1;
-    g = 0;
-    const int c = (int)blockIdx.x;
-    if (c >= sc.P) return;
-    if (sc.units) {
-      const int sb = c / sc.n_kv, sg = c - sb * sc.n_kv;
-      const int cost = sc.pre[sb + 1] - sc.pre[sb];
-      x = sc.n_kv * sc.pre[sb] + sg * cost;
-      end = x + cost;
-    } else {
-      x = sc.cut(c);
-      end = sc.cut(c + 1);
-    }
-  }
-  __device__ __forceinline__ bool next(const Cuts &sc, int B, Piece &sg) {
-    const int *pre = sc.pre;
-    while (x < end) {
-      if (b < 0) {
-        int lo = 0, hi = B - 1;  // largest b with n_kv * pre[b] <= x
-        while (lo < hi) {
-          const int mid = (lo + hi + 1) >> 1;
-          if (sc.n_kv * pre[mid] <= x) lo = mid; else hi = mid - 1;
-        }
-        b = lo;
-        g = (x - sc.n_kv * pre[b]) / (pre[b + 1] - pre[b]);
-      } else if (++g == sc.n_kv) {
-        g = 0;
-        do { ++b; } while (b < B - 1 && pre[b + 1] == pre[b]);
-      }
-      const int cost = pre[b + 1] - pre[b];
-      const int ucs = sc.n_kv * pre[b] + g * cost, uce = ucs + cost;
-      const int e = min(end, uce);
-      const int j0 = max(0, x - ucs - sc.ov), j1 = max(0, e - ucs - sc.ov);
-      x = e;
-      if (j1 > j0) {
-        sg.b = b;
-        sg.g = g;
-        sg.j0 = j0;
-        sg.nblk = cost - sc.ov;
-        sg.n = j1 - j0;
-        sg.ucs = ucs;
-        sg.uce = uce;
-        return true;
-      }
-    }
-    return false;
-  }
 };
+__device__ __forceinline__ void walk_start(const Cuts &sc, Walk &w) {
+  w.x = w.end = 0;
+  w.b = -1;
+  w.g = 0;
+  const int c = (int)blockIdx.x;
+  if (c >= sc.P) return;
+  if (sc.units) {
+    const int sb = c / sc.n_kv, sg = c - sb * sc.n_kv;
+    const int cost = sc.pre[sb + 1] - sc.pre[sb];
+    w.x = sc.n_kv * sc.pre[sb] + sg * cost;
+    w.end = w.x + cost;
+  } else {
+    w.x = sc.cut(c);
+    w.end = sc.cut(c + 1);
+  }
+}
+__device__ __forceinline__ bool walk_step(const int *pre, int n_kv, int ov, int B, Walk &w,
+                                          Piece &sg) {
+  while (w.x < w.end) {
+    if (w.b < 0) {
+      int lo = 0, hi = B - 1;  // largest b with n_kv * pre[b] <= x
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (n_kv * pre[mid] <= w.x) lo = mid; else hi = mid - 1;
+      }
+      w.b = lo;
+      w.g = (w.x - n_kv * pre[lo]) / (pre[lo + 1] - pre[lo]);
+    } else if (++w.g == n_kv) {
+      w.g = 0;
+      do { ++w.b; } while (w.b < B - 1 && pre[w.b + 1] == pre[w.b]);
+    }
+    const int cost = pre[w.b + 1] - pre[w.b];
+    const int ucs = n_kv * pre[w.b] + w.g * cost, uce = ucs + cost;
+    const int e = min(w.end, uce);
+    const int j0 = max(0, w.x - ucs - ov), j1 = max(0, e - ucs - ov);
+    w.x = e;
+    if (j1 > j0) {
+      sg.b = w.b;
+      sg.g = w.g;
+      sg.j0 = j0;
+      sg.nblk = cost - ov;
+      sg.n = j1 - j0;
+      sg.ucs = ucs;
+      sg.uce = uce;
+      return true;
+    }
+  }
+  return false;
+}
+// The steps after the first, out of line: one copy for all roles instead of
+// one for each, whose first instructions every call would fetch anew.
+__device__ __noinline__ bool walk_next(const int *pre, int n_kv, int ov, int B, Walk &w, Piece &sg) {
+  return walk_step(pre, n_kv, ov, B, w, sg);
+}
 
 // Block ids of a segment: entries lane and 32 + lane of what is left of it.
 struct Ids {
   int tab, tab_next;
 };
+__device__ __forceinline__ Ids load_ids(const AttnParams &p, const Piece &g, int lane) {
+  const int32_t *trow = p.tables + (size_t)g.b * p.MB + g.j0;
+  Ids a;
+  a.tab = (lane < g.n) ? __ldg(trow + lane) : 0;
+  a.tab_next = (32 + lane < g.n) ? __ldg(trow + 32 + lane) : 0;
+  return a;
+}
 
-// One producer warp: walks the CTA's stages and copies one tile per lane.
-// The K producer also copies the blocks' scales and records which blocks of a
-// stage had an invalid id.  Block ids are loaded one step ahead; `guess` has
-// those of the start of sequence guess_b.
+// One producer warp: walks the CTA's stages, two gathers of four tiles (16
+// tokens) or of four tiles' halves (32 tokens) each.  (A bulk copy a tile, one
+// lane each, cost the warp about 100 cycles a copy: 1200 a stage of 16-token
+// tiles, as long as HBM takes to deliver it.)  In the place of absent blocks
+// of a last stage and of blocks whose id is bad, tile 0 is read, and its rows
+// take no weight.  The K producer also copies the blocks' scales and records which blocks of a
+// stage had an invalid id.  Block ids are loaded one step ahead; `ids` has
+// those of the first segment.
 template <int BS, bool IS_K>
-__device__ __forceinline__ void produce(const Attn8bParams &pp, const Cuts &sc,
-                                        unsigned char *smem, uint64_t *full, uint64_t *empty,
-                                        volatile int *stage_mask, volatile int *abort_flag,
-                                        int guess_b, const Ids &guess, int lane) {
+__device__ __forceinline__ void produce(const Params &pr, const Cuts &sc, Walk w, Piece sg,
+                                        bool have, Ids ids, unsigned char *smem, uint64_t *full,
+                                        uint64_t *empty, volatile int *stage_mask,
+                                        volatile int *abort_flag, int lane) {
+  const Attn8bParams &pp = pr.q8;
   const AttnParams &p = pp.a;
   constexpr int SB = TOK / BS;
-  constexpr uint32_t TILE = BS * kHeadDim;
   constexpr int NS = IS_K ? NSK : NSV;
-  const unsigned char *cache = IS_K ? p.k_cache : p.v_cache;
+  const CUtensorMap *map = IS_K ? &pr.k_map : &pr.v_map;
   unsigned char *ring = smem + (IS_K ? OFF_K : OFF_V);
   const uint32_t sring = smem_addr(smem + OFF_SC);
   const uint64_t policy = l2_policy_evict_first();
-  auto load_ids = [&](const Piece &g, Ids &a) {
-    const int32_t *trow = p.tables + (size_t)g.b * p.MB + g.j0;
-    a.tab = (lane < g.n) ? __ldg(trow + lane) : 0;
-    a.tab_next = (32 + lane < g.n) ? __ldg(trow + 32 + lane) : 0;
-  };
-  Walk cur(sc);
-  Piece sg, nsg;
-  Ids ids = guess, next_ids{};
-  bool have = cur.next(sc, p.B, sg);
-  if (have && !(sg.b == guess_b && sg.j0 == 0)) load_ids(sg, ids);
   if (p.wait_late == 1) pdl_wait();  // the append has written the cache
   int s = 0;
   bool stop = false;
   while (have && !stop) {
-    const bool have_next = cur.next(sc, p.B, nsg);
-    if (have_next) load_ids(nsg, next_ids);
+    bool have_next = false;
+    Piece nsg{};
+    Ids next_ids{};
     const int32_t *trow = p.tables + (size_t)sg.b * p.MB + sg.j0;
     int tab = ids.tab, tab_next = ids.tab_next;
     int tchunk = 0;
@@ -251,41 +280,49 @@ __device__ __forceinline__ void produce(const Attn8bParams &pp, const Cuts &sc,
       const int blk = __shfl_sync(kFullMask, tab, (first & 31) + (lane & (SB - 1)));
       const bool ok = lane < nb && (unsigned)blk < (unsigned)p.NB;
       const unsigned okmask = __ballot_sync(kFullMask, ok);
-      const unsigned want = (1u << nb) - 1u;
+      const int tile = ok ? blk * p.n_kv + sg.g : 0;
+      int rows[SB];
+#pragma unroll
+      for (int i = 0; i < SB; ++i) rows[i] = __shfl_sync(kFullMask, tile, i);
       const int slot = s % NS;
       int go = 1;
       if (lane == 0) {
         wait_or_abort(&empty[slot], ((uint32_t)(s / NS) & 1u) ^ 1u, abort_flag, p.err);
         go = *abort_flag ? 0 : 1;
+        if (go) {
+          if (IS_K) {
+            const unsigned bad = ((1u << nb) - 1u) & ~okmask;
+            stage_mask[s & (NSR - 1)] = (int)bad;
+            if (bad) atomicOr(p.err, PGD_DEVERR_BAD_BLOCK_ID);
+          }
+          mbar_arrive_expect_tx(&full[slot], STAGE);
+          unsigned char *dst = ring + (size_t)slot * STAGE;
+          gather_tiles(dst, map, 0, rows[0], rows[1], rows[2], rows[3], &full[slot], policy);
+          if constexpr (SB == 8)
+            gather_tiles(dst + STAGE / 2, map, 0, rows[4], rows[5], rows[6], rows[7], &full[slot],
+                         policy);
+          else
+            gather_tiles(dst + STAGE / 2, map, 256, rows[0], rows[1], rows[2], rows[3],
+                         &full[slot], policy);
+        }
       }
       // (one decision for the warp: after a timeout nothing more is armed)
       if (!__shfl_sync(kFullMask, go, 0)) {
         stop = true;
         break;
       }
-      if (lane == 0) {
-        if (IS_K) {
-          stage_mask[s & (NSR - 1)] = (int)(want & ~okmask);
-          if (want & ~okmask) atomicOr(p.err, PGD_DEVERR_BAD_BLOCK_ID);
-        }
-        const uint32_t bytes = (uint32_t)__popc(okmask) * TILE;
-        if (bytes == 0)
-          mbar_arrive(&full[slot]);
-        else
-          mbar_arrive_expect_tx(&full[slot], bytes);
-      }
-      __syncwarp();
-      if (ok) {
-        const size_t tile = (size_t)blk * p.n_kv + sg.g;
-        bulk_copy_g2s(ring + (size_t)slot * STAGE + (size_t)lane * TILE, cache + tile * TILE, TILE,
-                      &full[slot], policy);
-        if (IS_K) {
+      if (IS_K) {
+        if (ok) {
           const uint32_t dst = sring + (uint32_t)(((s & (NSR - 1)) * 16 + lane) * 4);
           copy4_async(dst, pp.k_scales + tile);
           copy4_async(dst + 32, pp.v_scales + tile);
         }
+        arrive_after_copies(&full[slot]);
       }
-      if (IS_K) arrive_after_copies(&full[slot]);
+      if (st == 0) {  // the next segment's ids, once this one's copies have begun
+        have_next = walk_next(sc.pre, sc.n_kv, sc.ov, p.B, w, nsg);
+        if (have_next) next_ids = load_ids(p, nsg, lane);
+      }
     }
     sg = nsg;
     ids = next_ids;
@@ -389,8 +426,9 @@ __device__ __forceinline__ void merge_unit(const AttnParams &p, const int4 &m, i
 }
 
 template <int G, int BS>
-__global__ void __launch_bounds__(NTHREADS, 1) attention_fp8b_kernel(const Attn8bParams pp) {
-  const AttnParams &p = pp.a;
+__global__ void __launch_bounds__(NTHREADS, 1)
+attention_fp8b_kernel(const __grid_constant__ Params pr) {
+  const AttnParams &p = pr.q8.a;
   constexpr int SB = TOK / BS;
   constexpr int NCOL = NP<G>, TSTEP = TS<G>;
   constexpr int PROW = NCOL;             // bytes of a token's weights
@@ -547,10 +585,10 @@ __global__ void __launch_bounds__(NTHREADS, 1) attention_fp8b_kernel(const Attn8
     constexpr float m0 = (float)kMergeFixedBytes / kBlockBytes;
     constexpr float m1 = (float)kMergePartBytes / kBlockBytes;
     const float X = (float)sc.X;
-    const int P = max(1, min(sc.P, (int)sqrtf(kShare<BS> * X * (float)U / m1)));
-    const float cost_cut = fmaxf(X / (float)P * kShare<BS>, X) + m0 + m1 * (float)((P + U - 1) / U);
+    const int P = max(1, min(sc.P, (int)sqrtf(kShare * X * (float)U / m1)));
+    const float cost_cut = fmaxf(X / (float)P * kShare, X) + m0 + m1 * (float)((P + U - 1) / U);
     sc.P = P;
-    if (U <= (int)gridDim.x && fmaxf((float)longest * kShare<BS>, X) <= cost_cut) {
+    if (U <= (int)gridDim.x && fmaxf((float)longest * kShare, X) <= cost_cut) {
       sc.units = true;
       sc.P = U;
     }
@@ -558,15 +596,24 @@ __global__ void __launch_bounds__(NTHREADS, 1) attention_fp8b_kernel(const Attn8
   sc.q = sc.P > 0 ? sc.X / sc.P : 0;
   sc.r = sc.X - sc.q * sc.P;
 
+  // Every role walks the same segments; the first is found once.
+  Walk walk;
+  Piece sg;
+  walk_start(sc, walk);
+  bool have = walk_step(pre, sc.n_kv, sc.ov, p.B, walk, sg);
+  if ((warp == WARP_KP || warp == WARP_VP) && have && !(sg.b == guess_b && sg.j0 == 0))
+    guess = load_ids(p, sg, lane);
+  auto next = [&](Piece &g) { return walk_next(pre, sc.n_kv, sc.ov, p.B, walk, g); };
+
   if (warp == WARP_KP) {
-    produce<BS, true>(pp, sc, smem, full_k, empty_k, stage_mask, abort_flag, guess_b, guess, lane);
+    produce<BS, true>(pr, sc, walk, sg, have, guess, smem, full_k, empty_k, stage_mask,
+                      abort_flag, lane);
   } else if (warp == WARP_VP) {
-    produce<BS, false>(pp, sc, smem, full_v, empty_v, nullptr, abort_flag, guess_b, guess, lane);
+    produce<BS, false>(pr, sc, walk, sg, have, guess, smem, full_v, empty_v, nullptr, abort_flag,
+                       lane);
   } else if (warp == WARP_QK) {
     // ------------------------------ query conversion, then q.k^T (one lane)
-    Walk cur(sc);
-    Piece sg, nsg;
-    bool have = cur.next(sc, p.B, sg);
+    Piece nsg;
     uint4 q[kPieces<G>];
     if (have) load_query<G>(p, sg, lane, q);
     int s = 0, k = 0, last1 = -1, last2 = -1;  // last stages of segments k - 1, k - 2
@@ -579,7 +626,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) attention_fp8b_kernel(const Attn8
         wait_or_abort(&s_full[last2 % NSB], (uint32_t)(last2 / NSB) & 1u, abort_flag, p.err);
       unsigned char *qbuf = smem + OFF_Q + (k & 1) * Q_BYTES;
       write_query<G>(q, qbuf, qscale + (k & (NQS - 1)) * 8, lane);
-      const bool have_next = cur.next(sc, p.B, nsg);
+      const bool have_next = next(nsg);
       if (have_next) load_query<G>(p, nsg, lane, q);
       if (lane == 0) {
         const uint64_t qd = smem_desc(smem_addr(qbuf), 128, 1024, 0);
@@ -619,21 +666,12 @@ __global__ void __launch_bounds__(NTHREADS, 1) attention_fp8b_kernel(const Attn8
   } else if (warp == WARP_PV) {
     // ------------------------------------------------------- p.v issuer
     if (lane == 0) {
-      Walk cur(sc);
-      Piece sg;
       int s = 0, k = 0;
-      while (cur.next(sc, p.B, sg)) {
-        const int ctx_b = __ldg(p.ctx + sg.b);
+      while (have) {
         const int nstages = (sg.n + SB - 1) / SB;
         const int ob = k & 1;
         for (int st = 0; st < nstages; ++st, ++s) {
           const int slot = s % NSV, sb = s & 1;
-          // k-steps of 32 tokens; those past the last token are not issued
-          // (their rows hold no token and were not zeroed)
-          const int nb = min(SB, sg.n - st * SB);
-          int nvalid = nb * BS;
-          if (sg.j0 + st * SB + nb == sg.nblk) nvalid -= sg.nblk * BS - ctx_b;
-          const int nkt = min(4, max(1, (nvalid + 31) >> 5));
           wait_or_abort(&p_full[sb], (uint32_t)(s >> 1) & 1u, abort_flag, p.err);
           wait_or_abort(&full_v[slot], (uint32_t)(s / NSV) & 1u, abort_flag, p.err);
           if (st == 0)
@@ -642,21 +680,21 @@ __global__ void __launch_bounds__(NTHREADS, 1) attention_fp8b_kernel(const Attn8
           if (!*abort_flag) {
             // V: dims (M) 128 B apart in chunks of 16, token groups (K)
             // 1024 B apart; P: columns (N) 128 B apart in chunks of 16, token
-            // groups PGRP apart
+            // groups PGRP apart; a k-step is 32 token rows
             const uint64_t vd = smem_desc(smem_addr(smem + OFF_V + slot * STAGE), GROUP, 128, 0);
             const uint64_t pd = smem_desc(smem_addr(smem + OFF_P + sb * P_BYTES8), PGRP, 128, 0);
 #pragma unroll
             for (int kt = 0; kt < 4; ++kt)
-              if (kt < nkt)
-                umma_e4m3(col_o(ob, sb), vd + (uint64_t)(kt * (4 * GROUP / 16)),
-                          pd + (uint64_t)(kt * (4 * PGRP / 16)), IDESC_PV,
-                          (kt > 0 || st > 1) ? 1u : 0u);
+              umma_e4m3(col_o(ob, sb), vd + (uint64_t)(kt * (4 * GROUP / 16)),
+                        pd + (uint64_t)(kt * (4 * PGRP / 16)), IDESC_PV,
+                        (kt > 0 || st > 1) ? 1u : 0u);
           }
           umma_commit(&empty_v[slot]);
           umma_commit(&p_free[sb]);
           if (st + 1 == nstages) umma_commit(&o_full[ob]);
         }
         ++k;
+        have = next(sg);
       }
       if (s > 0) {
         umma_commit(&done[1]);
@@ -672,13 +710,15 @@ __global__ void __launch_bounds__(NTHREADS, 1) attention_fp8b_kernel(const Attn8
     constexpr int NCT = 128;
     float *gred = red + grp * 2 * 4 * 8;
     int *gvote = over_flag + grp * 2 * 4;
-    Walk cur(sc);
-    Piece sg, nsg;
+    // Row t of a stage: which of the stage's blocks, and which token of the
+    // stage (32-token tiles land as their first halves, then their second).
+    const int tblk = BS == 16 ? t >> 4 : (t >> 4) & 3;
+    const int ttok = BS == 16 ? t : tblk * 32 + (t >> 6) * 16 + (t & 15);
+    Piece nsg;
     int s = 0, k = 0, it = 0;  // s: the segment's first stage
-    bool have = cur.next(sc, p.B, sg);
     int ctx_b = have ? __ldg(p.ctx + sg.b) : 0;
     while (have) {
-      const bool have_next = cur.next(sc, p.B, nsg);
+      const bool have_next = next(nsg);
       const int ctx_n = have_next ? __ldg(p.ctx + nsg.b) : 0;
       const int nstages = (sg.n + SB - 1) / SB;
       const int ob = k & 1;
@@ -698,10 +738,9 @@ __global__ void __launch_bounds__(NTHREADS, 1) attention_fp8b_kernel(const Attn8
         const int nb = min(SB, sg.n - st * SB);
         int nvalid = nb * BS;
         if (sg.j0 + st * SB + nb == sg.nblk) nvalid -= sg.nblk * BS - ctx_b;
-        const bool valid = (t < nvalid) && !((msk >> (t / BS)) & 1);
-        const int lim = (nvalid + 31) & ~31;  // rows p.v reads
-        const float ks = scl[(su & (NSR - 1)) * 16 + t / BS];
-        const float vs = scl[(su & (NSR - 1)) * 16 + 8 + t / BS];
+        const bool valid = (ttok < nvalid) && !((msk >> tblk) & 1);
+        const float ks = scl[(su & (NSR - 1)) * 16 + tblk];
+        const float vs = scl[(su & (NSR - 1)) * 16 + 8 + tblk];
         if (st == st0) {
 #pragma unroll
           for (int h = 0; h < G; ++h) qsc[h] = qscale[(k & (NQS - 1)) * 8 + h] * p.qk_scale_log2;
@@ -812,9 +851,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) attention_fp8b_kernel(const Attn8
               make_uint4(word[0][0], word[0][1], word[1][0], word[1][1]);
           *reinterpret_cast<uint4 *>(dst + 128) = make_uint4(word[2][0], word[2][1], 0, 0);
         }
-        if (!valid && t < lim) {
-          // rows that p.v reads but that hold no token (the tail of the last
-          // block, a block whose id was bad): their codes may be NaN
+        if (!valid) {
+          // rows that hold no token: their codes may be NaN
           const int vslot = su % NSV;
           wait_or_abort(&full_v[vslot], (uint32_t)(su / NSV) & 1u, abort_flag, p.err);
           uint4 *vrow = reinterpret_cast<uint4 *>(smem + OFF_V + vslot * STAGE +
@@ -853,11 +891,9 @@ __global__ void __launch_bounds__(NTHREADS, 1) attention_fp8b_kernel(const Attn8
     const int ew = warp - WARP_EPI;
     const uint32_t lane_base = (uint32_t)(ew * 32) << 16;
     constexpr int NET = 128;
-    Walk cur(sc);
-    Piece sg;
     const int part = (int)blockIdx.x;
     int k = 0;
-    while (cur.next(sc, p.B, sg)) {
+    for (; have; have = next(sg)) {
       const int ob = k & 1;
       const int unit = sg.b * p.n_kv + sg.g;
       wait_or_abort(&seg_done[ob], (uint32_t)(k >> 1) & 1u, abort_flag, p.err);
@@ -943,8 +979,37 @@ __global__ void __launch_bounds__(NTHREADS, 1) attention_fp8b_kernel(const Attn8
   }
 }
 
+// A pool as a tensor of tiles (see Params).
+cudaError_t encode_map(CUtensorMap *map, const void *pool, long long tiles, int bs) {
+  using Encode = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                              const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                              const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+  static std::atomic<Encode> encode{nullptr};
+  Encode fn = encode.load();
+  if (!fn) {
+    void *f = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    const cudaError_t e =
+        cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
+                                         &found);
+    if (e != cudaSuccess) return e;
+    if (!f || found != cudaDriverEntryPointSuccess) return cudaErrorNotSupported;
+    fn = reinterpret_cast<Encode>(f);
+    encode.store(fn);
+  }
+  const cuuint64_t dims[2] = {(cuuint64_t)bs * 16, (cuuint64_t)tiles};
+  const cuuint64_t strides[1] = {(cuuint64_t)bs * kHeadDim};
+  const cuuint32_t box[2] = {256, 1}, steps[2] = {1, 1};
+  const CUresult r =
+      fn(map, CU_TENSOR_MAP_DATA_TYPE_INT64, 2, const_cast<void *>(pool), dims, strides, box, steps,
+         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 template <int G, int BS>
-cudaError_t launch_cfg(const Attn8bParams &p, int grid, cudaStream_t stream) {
+cudaError_t launch_cfg(const Params &p, int grid, cudaStream_t stream) {
   static volatile int done[64] = {0};  // shared-memory limit raised, per device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -959,7 +1024,7 @@ cudaError_t launch_cfg(const Attn8bParams &p, int grid, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(NTHREADS);
-  cfg.dynamicSmemBytes = smem_size(p.a.B);
+  cfg.dynamicSmemBytes = smem_size(p.q8.a.B);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -971,8 +1036,14 @@ cudaError_t launch_cfg(const Attn8bParams &p, int grid, cudaStream_t stream) {
 
 }  // namespace tc8b
 
-cudaError_t attention_fp8b_launch(const Attn8bParams &p, int G, int bs, int grid,
+cudaError_t attention_fp8b_launch(const Attn8bParams &q8, int G, int bs, int grid,
                                   cudaStream_t stream) {
+  tc8b::Params p;
+  p.q8 = q8;
+  const long long tiles = (long long)q8.a.NB * q8.a.n_kv;
+  cudaError_t e = tc8b::encode_map(&p.k_map, q8.a.k_cache, tiles, bs);
+  if (e == cudaSuccess) e = tc8b::encode_map(&p.v_map, q8.a.v_cache, tiles, bs);
+  if (e != cudaSuccess) return e;
 #define PGD_CASE(G_, BS_) \
   if (G == G_ && bs == BS_) return tc8b::launch_cfg<G_, BS_>(p, grid, stream);
   PGD_CASE(1, 16) PGD_CASE(2, 16) PGD_CASE(4, 16) PGD_CASE(8, 16)
