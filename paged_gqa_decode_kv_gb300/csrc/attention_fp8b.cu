@@ -62,8 +62,8 @@ namespace tc8b {
 
 using namespace tc;
 
-// The launch's parameters: K and V pools as tensors of NB * n_kv rows (tiles)
-// of bs * 16 8-byte elements, read in boxes of one row by 256.
+// The launch's parameters: pools of 16-token tiles also as tensors of NB * n_kv
+// rows (tiles) of 256 8-byte elements, read in boxes of one row.
 struct Params {
   Attn8bParams q8;
   CUtensorMap k_map, v_map;
@@ -74,7 +74,8 @@ constexpr int WARP_SM1 = 12;            // warps of the second softmax group
 constexpr uint32_t TMEM_COLS8 = 256;   // S 4 x 16; O 2 x 2 x 32 from column 64
 constexpr int GROUP = kGroupBytes8b;   // bytes of 8 tokens
 constexpr int STAGE = TOK * kHeadDim;  // K (or V) codes of a stage
-constexpr int NSK = 6, NSV = 6;        // ring depths
+constexpr int NSK = 5, NSV = 5;        // ring depths (3, 4 and 6 stages: 350, 342, 351 us where 5
+                                       // take 344 on 64 ragged contexts)
 constexpr int NSR = 16;                // stages of scales
 constexpr int Q_BYTES = NPAD * 128;    // 16 E4M3 rows as 8 x 16-byte core matrices
 constexpr float kMoveLog2 = 4.f;       // move the reference when exceeded by 2^4
@@ -124,16 +125,14 @@ __host__ __device__ constexpr uint32_t idesc_pv(int n) {
 __device__ __forceinline__ void copy4_async(uint32_t dst, const void *src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
-// Four tiles' 2 KiB runs at element x (of 8 bytes) into `dst`, one behind the
-// other: rows t0 .. t3 of the pool as a two-dimensional tensor.  A row outside
+// Four 2 KiB tiles into `dst`, one behind the other: rows t0 .. t3 of the pool as a two-dimensional tensor.  A row outside
 // the pool arrives as zeros.
-__device__ __forceinline__ void gather_tiles(void *dst, const CUtensorMap *map, int x, int t0,
-                                             int t1, int t2, int t3, uint64_t *bar,
-                                             uint64_t policy) {
+__device__ __forceinline__ void gather_tiles(void *dst, const CUtensorMap *map, int t0, int t1,
+                                             int t2, int t3, uint64_t *bar, uint64_t policy) {
   asm volatile(
       "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
       ".L2::cache_hint [%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8;" ::"r"(smem_addr(dst)),
-      "l"(map), "r"(x), "r"(t0), "r"(t1), "r"(t2), "r"(t3), "r"(smem_addr(bar)), "l"(policy)
+      "l"(map), "r"(0), "r"(t0), "r"(t1), "r"(t2), "r"(t3), "r"(smem_addr(bar)), "l"(policy)
       : "memory");
 }
 // Arrive on `bar` (one of its expected arrivals) once this thread's earlier
@@ -169,23 +168,33 @@ struct Piece {  // blocks j0 .. j0 + n - 1 of the nblk of unit (b, g), at cost [
 struct Walk {
   int x, end, b, g;
 };
-__device__ __forceinline__ void walk_start(const Cuts &sc, Walk &w) {
+__device__ __forceinline__ void walk_start(Cuts &sc, Walk &w) {
   w.x = w.end = 0;
   w.b = -1;
   w.g = 0;
   const int c = (int)blockIdx.x;
   if (c >= sc.P) return;
-  if (sc.units) {
-    const int sb = c / sc.n_kv, sg = c - sb * sc.n_kv;
-    const int cost = sc.pre[sb + 1] - sc.pre[sb];
-    w.x = sc.n_kv * sc.pre[sb] + sg * cost;
-    w.end = w.x + cost;
-  } else {
-    w.x = sc.cut(c);
-    w.end = sc.cut(c + 1);
-  }
+  sc.q = sc.X / sc.P;
+  sc.r = sc.X - sc.q * sc.P;
+  w.x = sc.cut(c);
+  w.end = sc.cut(c + 1);
 }
-__device__ __forceinline__ bool walk_step(const int *pre, int n_kv, int ov, int B, Walk &w,
+// Part c of a split into whole units: unit c, if it has blocks.
+__device__ __forceinline__ bool whole_unit(const Cuts &sc, Piece &sg) {
+  const int c = (int)blockIdx.x;
+  if (c >= sc.P) return false;
+  sg.b = c / sc.n_kv;
+  sg.g = c - sg.b * sc.n_kv;
+  const int cost = sc.pre[sg.b + 1] - sc.pre[sg.b];
+  sg.j0 = 0;
+  sg.nblk = sg.n = cost - sc.ov;
+  sg.ucs = sc.n_kv * sc.pre[sg.b] + sg.g * cost;
+  sg.uce = sg.ucs + cost;
+  return cost > 0;
+}
+// The next segment.  Out of line: one copy for all roles instead of one for
+// each, whose first instructions every call would fetch anew.
+__device__ __noinline__ bool walk_next(const int *pre, int n_kv, int ov, int B, Walk &w,
                                           Piece &sg) {
   while (w.x < w.end) {
     if (w.b < 0) {
@@ -218,12 +227,6 @@ __device__ __forceinline__ bool walk_step(const int *pre, int n_kv, int ov, int 
   }
   return false;
 }
-// The steps after the first, out of line: one copy for all roles instead of
-// one for each, whose first instructions every call would fetch anew.
-__device__ __noinline__ bool walk_next(const int *pre, int n_kv, int ov, int B, Walk &w, Piece &sg) {
-  return walk_step(pre, n_kv, ov, B, w, sg);
-}
-
 // Block ids of a segment: entries lane and 32 + lane of what is left of it.
 struct Ids {
   int tab, tab_next;
@@ -236,12 +239,14 @@ __device__ __forceinline__ Ids load_ids(const AttnParams &p, const Piece &g, int
   return a;
 }
 
-// One producer warp: walks the CTA's stages, two gathers of four tiles (16
-// tokens) or of four tiles' halves (32 tokens) each.  (A bulk copy a tile, one
-// lane each, cost the warp about 100 cycles a copy: 1200 a stage of 16-token
-// tiles, as long as HBM takes to deliver it.)  In the place of absent blocks
-// of a last stage and of blocks whose id is bad, tile 0 is read, and its rows
-// take no weight.  The K producer also copies the blocks' scales and records which blocks of a
+// One producer warp: walks the CTA's stages.  Tiles of 16 tokens come four at
+// a time by two gathers a stage (a bulk copy a tile, one lane each, costs the
+// warp about 100 cycles a copy: 1200 a stage of eight, as long as HBM takes to
+// deliver it); in the place of absent blocks of a last stage and of blocks
+// whose id is bad, tile 0 is read, and its rows take no weight.  Tiles of 32
+// tokens come by a bulk copy each (a gather's rows end at 2 KiB: 4 KiB tiles
+// in two halves took 343 us where whole ones take 335 on 64 ragged contexts).
+// The K producer also copies the blocks' scales and records which blocks of a
 // stage had an invalid id.  Block ids are loaded one step ahead; `ids` has
 // those of the first segment.
 template <int BS, bool IS_K>
@@ -253,7 +258,10 @@ __device__ __forceinline__ void produce(const Params &pr, const Cuts &sc, Walk w
   const AttnParams &p = pp.a;
   constexpr int SB = TOK / BS;
   constexpr int NS = IS_K ? NSK : NSV;
+  constexpr bool GATHER = BS == 16;
+  constexpr uint32_t TILE = BS * kHeadDim;
   const CUtensorMap *map = IS_K ? &pr.k_map : &pr.v_map;
+  const unsigned char *cache = IS_K ? p.k_cache : p.v_cache;
   unsigned char *ring = smem + (IS_K ? OFF_K : OFF_V);
   const uint32_t sring = smem_addr(smem + OFF_SC);
   const uint64_t policy = l2_policy_evict_first();
@@ -281,10 +289,13 @@ __device__ __forceinline__ void produce(const Params &pr, const Cuts &sc, Walk w
       const bool ok = lane < nb && (unsigned)blk < (unsigned)p.NB;
       const unsigned okmask = __ballot_sync(kFullMask, ok);
       const int tile = ok ? blk * p.n_kv + sg.g : 0;
-      int rows[SB];
-#pragma unroll
-      for (int i = 0; i < SB; ++i) rows[i] = __shfl_sync(kFullMask, tile, i);
       const int slot = s % NS;
+      unsigned char *dst = ring + (size_t)slot * STAGE;
+      int rows[SB];
+      if constexpr (GATHER) {
+#pragma unroll
+        for (int i = 0; i < SB; ++i) rows[i] = __shfl_sync(kFullMask, tile, i);
+      }
       int go = 1;
       if (lane == 0) {
         wait_or_abort(&empty[slot], ((uint32_t)(s / NS) & 1u) ^ 1u, abort_flag, p.err);
@@ -295,15 +306,16 @@ __device__ __forceinline__ void produce(const Params &pr, const Cuts &sc, Walk w
             stage_mask[s & (NSR - 1)] = (int)bad;
             if (bad) atomicOr(p.err, PGD_DEVERR_BAD_BLOCK_ID);
           }
-          mbar_arrive_expect_tx(&full[slot], STAGE);
-          unsigned char *dst = ring + (size_t)slot * STAGE;
-          gather_tiles(dst, map, 0, rows[0], rows[1], rows[2], rows[3], &full[slot], policy);
-          if constexpr (SB == 8)
-            gather_tiles(dst + STAGE / 2, map, 0, rows[4], rows[5], rows[6], rows[7], &full[slot],
-                         policy);
-          else
-            gather_tiles(dst + STAGE / 2, map, 256, rows[0], rows[1], rows[2], rows[3],
-                         &full[slot], policy);
+          if constexpr (GATHER) {
+            mbar_arrive_expect_tx(&full[slot], STAGE);
+            gather_tiles(dst, map, rows[0], rows[1], rows[2], rows[3], &full[slot], policy);
+            gather_tiles(dst + STAGE / 2, map, rows[SB - 4], rows[SB - 3], rows[SB - 2],
+                         rows[SB - 1], &full[slot], policy);
+          } else if (okmask) {
+            mbar_arrive_expect_tx(&full[slot], (uint32_t)__popc(okmask) * TILE);
+          } else {
+            mbar_arrive(&full[slot]);
+          }
         }
       }
       // (one decision for the warp: after a timeout nothing more is armed)
@@ -311,11 +323,14 @@ __device__ __forceinline__ void produce(const Params &pr, const Cuts &sc, Walk w
         stop = true;
         break;
       }
+      if (!GATHER && ok)
+        bulk_copy_g2s(dst + (size_t)lane * TILE, cache + (size_t)tile * TILE, TILE, &full[slot],
+                      policy);
       if (IS_K) {
         if (ok) {
-          const uint32_t dst = sring + (uint32_t)(((s & (NSR - 1)) * 16 + lane) * 4);
-          copy4_async(dst, pp.k_scales + tile);
-          copy4_async(dst + 32, pp.v_scales + tile);
+          const uint32_t at = sring + (uint32_t)(((s & (NSR - 1)) * 16 + lane) * 4);
+          copy4_async(at, pp.k_scales + tile);
+          copy4_async(at + 32, pp.v_scales + tile);
         }
         arrive_after_copies(&full[slot]);
       }
@@ -593,14 +608,17 @@ attention_fp8b_kernel(const __grid_constant__ Params pr) {
       sc.P = U;
     }
   }
-  sc.q = sc.P > 0 ? sc.X / sc.P : 0;
-  sc.r = sc.X - sc.q * sc.P;
 
   // Every role walks the same segments; the first is found once.
-  Walk walk;
-  Piece sg;
-  walk_start(sc, walk);
-  bool have = walk_step(pre, sc.n_kv, sc.ov, p.B, walk, sg);
+  Walk walk{};
+  Piece sg{};
+  bool have;
+  if (sc.units) {
+    have = whole_unit(sc, sg);
+  } else {
+    walk_start(sc, walk);
+    have = walk_next(pre, sc.n_kv, sc.ov, p.B, walk, sg);
+  }
   if ((warp == WARP_KP || warp == WARP_VP) && have && !(sg.b == guess_b && sg.j0 == 0))
     guess = load_ids(p, sg, lane);
   auto next = [&](Piece &g) { return walk_next(pre, sc.n_kv, sc.ov, p.B, walk, g); };
@@ -710,10 +728,7 @@ attention_fp8b_kernel(const __grid_constant__ Params pr) {
     constexpr int NCT = 128;
     float *gred = red + grp * 2 * 4 * 8;
     int *gvote = over_flag + grp * 2 * 4;
-    // Row t of a stage: which of the stage's blocks, and which token of the
-    // stage (32-token tiles land as their first halves, then their second).
-    const int tblk = BS == 16 ? t >> 4 : (t >> 4) & 3;
-    const int ttok = BS == 16 ? t : tblk * 32 + (t >> 6) * 16 + (t & 15);
+    const int tblk = t / BS;  // the stage's block of row t
     Piece nsg;
     int s = 0, k = 0, it = 0;  // s: the segment's first stage
     int ctx_b = have ? __ldg(p.ctx + sg.b) : 0;
@@ -738,7 +753,7 @@ attention_fp8b_kernel(const __grid_constant__ Params pr) {
         const int nb = min(SB, sg.n - st * SB);
         int nvalid = nb * BS;
         if (sg.j0 + st * SB + nb == sg.nblk) nvalid -= sg.nblk * BS - ctx_b;
-        const bool valid = (ttok < nvalid) && !((msk >> tblk) & 1);
+        const bool valid = (t < nvalid) && !((msk >> tblk) & 1);
         const float ks = scl[(su & (NSR - 1)) * 16 + tblk];
         const float vs = scl[(su & (NSR - 1)) * 16 + 8 + tblk];
         if (st == st0) {
@@ -980,7 +995,7 @@ attention_fp8b_kernel(const __grid_constant__ Params pr) {
 }
 
 // A pool as a tensor of tiles (see Params).
-cudaError_t encode_map(CUtensorMap *map, const void *pool, long long tiles, int bs) {
+cudaError_t encode_map(CUtensorMap *map, const void *pool, long long tiles) {
   using Encode = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
                               const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
                               const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
@@ -998,8 +1013,8 @@ cudaError_t encode_map(CUtensorMap *map, const void *pool, long long tiles, int 
     fn = reinterpret_cast<Encode>(f);
     encode.store(fn);
   }
-  const cuuint64_t dims[2] = {(cuuint64_t)bs * 16, (cuuint64_t)tiles};
-  const cuuint64_t strides[1] = {(cuuint64_t)bs * kHeadDim};
+  const cuuint64_t dims[2] = {256, (cuuint64_t)tiles};
+  const cuuint64_t strides[1] = {16 * kHeadDim};
   const cuuint32_t box[2] = {256, 1}, steps[2] = {1, 1};
   const CUresult r =
       fn(map, CU_TENSOR_MAP_DATA_TYPE_INT64, 2, const_cast<void *>(pool), dims, strides, box, steps,
@@ -1038,12 +1053,14 @@ cudaError_t launch_cfg(const Params &p, int grid, cudaStream_t stream) {
 
 cudaError_t attention_fp8b_launch(const Attn8bParams &q8, int G, int bs, int grid,
                                   cudaStream_t stream) {
-  tc8b::Params p;
+  tc8b::Params p = {};
   p.q8 = q8;
-  const long long tiles = (long long)q8.a.NB * q8.a.n_kv;
-  cudaError_t e = tc8b::encode_map(&p.k_map, q8.a.k_cache, tiles, bs);
-  if (e == cudaSuccess) e = tc8b::encode_map(&p.v_map, q8.a.v_cache, tiles, bs);
-  if (e != cudaSuccess) return e;
+  if (bs == 16) {
+    const long long tiles = (long long)q8.a.NB * q8.a.n_kv;
+    cudaError_t e = tc8b::encode_map(&p.k_map, q8.a.k_cache, tiles);
+    if (e == cudaSuccess) e = tc8b::encode_map(&p.v_map, q8.a.v_cache, tiles);
+    if (e != cudaSuccess) return e;
+  }
 #define PGD_CASE(G_, BS_) \
   if (G == G_ && bs == BS_) return tc8b::launch_cfg<G_, BS_>(p, grid, stream);
   PGD_CASE(1, 16) PGD_CASE(2, 16) PGD_CASE(4, 16) PGD_CASE(8, 16)
