@@ -562,7 +562,7 @@ pgd_status pgd_append_decode_attention_fp8b(
  * tile_tokens int32 [B][n_kv]: the tokens they hold.  The scores are exact in
  * fp32.  A bad context is flagged (PGD_DEVERR_BAD_CONTEXT) and selects
  * nothing (tile_tokens 0); a block with a bad id counts as the lowest score.
- * MB at most 163840.
+ * MB at most 49152.
  *
  * pgd_selected_decode_attention: decode attention of q over the tokens of the
  * tiles, the last tile holding tile_tokens - (tiles - 1) * bs of them -- from

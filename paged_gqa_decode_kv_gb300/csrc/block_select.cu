@@ -202,9 +202,9 @@ cudaError_t launch_pdl(K kernel, dim3 grid, int threads, size_t smem, cudaStream
 // ------------------------------------------------------------------ selection
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kMaxCluster = 16;
-constexpr int kSliceKeys = 10240;  // keys of a CTA's slice (40 KiB)
-constexpr int kUnroll = 4;  // blocks that a group of eight lanes has in flight
+constexpr int kMaxCluster = 8;
+constexpr int kSliceKeys = 6144;   // keys of a CTA's slice at most (24 KiB)
+constexpr int kBins = 256;
 
 // A float's bits as an unsigned integer of the same order.
 __device__ __forceinline__ uint32_t order_key(float f) {
@@ -212,8 +212,8 @@ __device__ __forceinline__ uint32_t order_key(float f) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// Barrier over the cluster's CTAs (shared-memory writes before it are visible
-// to the peers' reads behind it), or over the one CTA.
+// Barrier over the cluster's CTAs (shared-memory writes before it, into any
+// CTA's, are visible behind it), or over the one CTA.
 __device__ __forceinline__ void sync_all(int C) {
   if (C > 1)
     asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
@@ -221,44 +221,67 @@ __device__ __forceinline__ void sync_all(int C) {
   else
     __syncthreads();
 }
-// A word of CTA `rank`'s shared memory, at the place `local` has in ours.
-__device__ __forceinline__ uint32_t ld_peer(const uint32_t *local, int rank, int C) {
-  if (C == 1) return *local;
-  uint32_t remote, v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
-               : "=r"(remote)
-               : "r"(smem_addr(local)), "r"(rank));
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(remote) : "memory");
-  return v;
+// Store into every CTA's shared memory at the place `local` has in ours.
+__device__ __forceinline__ void push_all(uint32_t *local, uint32_t v, int C) {
+  if (C == 1) {
+    *local = v;
+    return;
+  }
+  for (int r = 0; r < C; ++r) {
+    uint32_t remote;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                 : "=r"(remote)
+                 : "r"(smem_addr(local)), "r"(r));
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(remote), "r"(v) : "memory");
+  }
+}
+
+// D += A B, m16n8k16, f16 operands, fp32 accumulation.
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 // One cluster of C CTAs per (sequence, KV head), each CTA a contiguous slice
 // of the blocks.
-// 1. Scores.  Eight lanes take a block: lane i holds dims 16 i .. + 15 of both
-//    bounds (two 16-byte loads; a block's 256 bytes are two full lines) and of
-//    the rounded queries' positive and negative parts, four int8 products an
-//    instruction; a group has kUnroll blocks in flight.  The heads' sums are
-//    reduced over the eight lanes by halves (a lane keeps one half of the
-//    heads and sends the other).
+//
+// 1. Scores: a [blocks][256] by [256][heads] product of integers.  A warp takes
+//    16 blocks: lane (r, t) = (l / 4, l % 4) reads the 16-byte pieces t, t + 4,
+//    ... of the bounds of blocks r and r + 8, all eight loads in flight.  The
+//    product runs on the warp-level tensor instruction in f16: the byte b + 128
+//    zero-extended to 16 bits is the f16 subnormal (b + 128) 2^-24, one byte
+//    permutation for two values, and the query's integers are f16 numbers, so
+//    each product and each sum (below 2^23, times 2^-24) is exact in fp32; the
+//    accumulator starts at -128 sum_i r_hi to take the 128 off.  (Four int8
+//    products an instruction on the CUDA cores took 12.8k cycles for 1024
+//    blocks, three times the loads.  The operands come from registers, 16 rows
+//    at a time from scattered blocks: the shared-memory operands of the
+//    fifth-generation instruction would cost a pass through shared memory for
+//    an eighth of its N.)
 // 2. The least selected score, by 256-way refinement of the range [least,
 //    largest] of the unforced keys: every CTA histograms its keys in the
-//    range, adds up all CTAs' histograms through distributed shared memory and
-//    keeps the bin that holds the wanted rank, until the bin is one value or
-//    all its keys are wanted.  (Starting from the range rather than from the
-//    keys' top byte, which is all but constant for scores of one query, saves
-//    a pass and the contention on one bin.)
+//    range, stores the counts in every CTA's shared memory and after a cluster
+//    barrier adds them up and keeps the bin that holds the wanted rank, until
+//    the bin is one value or all its keys are wanted.  (Starting from the
+//    range rather than from the keys' top byte, which is all but constant for
+//    scores of one query, saves a pass and the contention on one bin.)
 // 3. Every warp counts, then writes, its own part of the slice in order.
 template <int G>
 __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams p, int C) {
   extern __shared__ uint32_t keys[];  // a slice: block ids, then keys
-  __shared__ uint32_t hist[3][256];   // a pass adds in one, zeroes the next's and leaves the
-                                      // last's to peers that may still be reading it
-  __shared__ uint32_t range[2];       // largest of ~key, largest key: unforced ones
-  __shared__ uint32_t counts[2];      // this CTA's keys above the least, and equal to it
+  __shared__ uint32_t hist[kBins];
+  __shared__ uint32_t all_hist[2][kMaxCluster][kBins];  // by pass parity, every CTA's
+  __shared__ uint32_t all_range[kMaxCluster][2];   // largest ~key, largest key: unforced ones
+  __shared__ uint32_t all_counts[kMaxCluster][2];  // keys above the least, and equal to it
+  __shared__ uint32_t range[2];
   __shared__ int warp_cnt[2][kSelWarps];
   __shared__ int found[3];
-  __shared__ __align__(16) signed char qpos[G][kHeadDim], qneg[G][kHeadDim];
-  __shared__ float qf[G];
+  __shared__ __align__(16) uint32_t qh[8][kHeadDim / 2];  // rounded queries, f16 pairs
+  __shared__ float qf[8], qbias[8];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int unit = (int)blockIdx.x / C, rank = (int)blockIdx.x % C;
   const int b = unit / p.n_kv, g = unit % p.n_kv;
@@ -288,13 +311,16 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
     for (int i = me; i < W; i += nthr) tiles[i] = i < nblk ? tile_of(__ldg(row + i)) : -1;
     return;
   }
+  // (every CTA of the cluster has started: waited for before the first store
+  // into another's shared memory)
+  if (C > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   const int per = (nblk + C - 1) / C;
   const int jlo = min(nblk, rank * per), n = min(nblk, jlo + per) - jlo;
   for (int i = tid; i < n; i += kSelThreads) keys[i] = (uint32_t)__ldg(row + jlo + i);
-  if (tid < 256) hist[0][tid] = 0;
+  if (tid < kBins) hist[tid] = 0;
   if (tid < 2) range[tid] = 0;
-  // The rounded queries: warp h takes head h.
-  if (warp < G) {
+  // The rounded queries: warp h takes head h (heads past G are zero).
+  if (warp < 8) {
     float f[4];
     unpack4(raw, f);
     float a = fmaxf(fmaxf(fabsf(f[0]), fabsf(f[1])), fmaxf(fabsf(f[2]), fabsf(f[3])));
@@ -302,87 +328,94 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
     for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(kFullMask, a, o));
     const int e = scale_exponent_int8(fminf(a, 3.3895314e38f));
     const float inv = pow2f(-e);
-    uint32_t wp = 0, wn = 0;
+    int v[4], sum = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int v = max(-127, min(127, __float2int_rn(f[i] * inv)));
-      wp |= (uint32_t)(max(v, 0) & 0xff) << (8 * i);
-      wn |= (uint32_t)(min(v, 0) & 0xff) << (8 * i);
+      v[i] = max(-127, min(127, __float2int_rn(f[i] * inv)));
+      sum += v[i];
     }
-    reinterpret_cast<uint32_t *>(qpos[warp])[lane] = wp;
-    reinterpret_cast<uint32_t *>(qneg[warp])[lane] = wn;
-    if (lane == 0) qf[warp] = pow2f(e);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const __half2 h = __floats2half2_rn((float)v[2 * i], (float)v[2 * i + 1]);
+      qh[warp][2 * lane + i] = *reinterpret_cast<const uint32_t *>(&h);
+    }
+    sum = __reduce_add_sync(kFullMask, sum);
+    if (lane == 0) {
+      qf[warp] = warp < G ? pow2f(e) : 0.f;
+      qbias[warp] = (float)(-128 * sum) * 0x1p-24f;
+    }
   }
   __syncthreads();
   {
-    const int i8 = lane & 7;
-    uint4 qp[G], qn[G];
+    // B fragments of all 16 k-steps (piece c, word w): head l / 4, the four
+    // dims of bytes 64 c + 16 t + 4 w of a block's bounds; the lower bounds
+    // (c < 2) take the query's negative part, the upper its positive part.
+    const int r = lane >> 2, t = lane & 3;
+    uint32_t bq[4][4][2];
+    const __half2 zero = __float2half2_rn(0.f);
 #pragma unroll
-    for (int h = 0; h < G; ++h) {
-      qp[h] = *reinterpret_cast<const uint4 *>(&qpos[h][16 * i8]);
-      qn[h] = *reinterpret_cast<const uint4 *>(&qneg[h][16 * i8]);
-    }
-    // after the reduction by halves lane i8 holds head i8 / (8 / G)
-    const float f = qf[i8 / (8 / G)];
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+      for (int w = 0; w < 4; ++w)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t x = qh[r][((c & 1) * 64 + 16 * t + 4 * w) / 2 + i];
+          const __half2 h = *reinterpret_cast<const __half2 *>(&x);
+          const __half2 y = c < 2 ? __hmin2(h, zero) : __hmax2(h, zero);
+          bq[c][w][i] = *reinterpret_cast<const uint32_t *>(&y);
+        }
+    const float f0 = qf[2 * t], f1 = qf[2 * t + 1];
+    const float b0 = qbias[2 * t], b1 = qbias[2 * t + 1];
     uint32_t kmin = 0xffffffffu, kmax = 0;
-    constexpr int kGroups = kSelThreads / 8;
-    for (int i0 = 0; i0 < n; i0 += kGroups * kUnroll) {
-      uint4 lo[kUnroll], hi[kUnroll];
-      float s[kUnroll];
-      bool there[kUnroll];
+    for (int i0 = warp * 16; i0 < n; i0 += kSelWarps * 16) {
+      uint4 x[2][4];
+      float s[2];
+      bool there[2];
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        const int i = i0 + u * kGroups + (tid >> 3);
+      for (int h = 0; h < 2; ++h) {
+        const int i = i0 + r + 8 * h;
         const uint32_t blk = i < n ? keys[i] : 0xffffffffu;
-        there[u] = blk < (uint32_t)p.NB;
-        lo[u] = hi[u] = make_uint4(0, 0, 0, 0);
-        s[u] = 0.f;
-        if (there[u]) {
+        there[h] = blk < (uint32_t)p.NB;
+        s[h] = 0.f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) x[h][c] = make_uint4(0, 0, 0, 0);
+        if (there[h]) {
           const size_t tile = (size_t)blk * p.n_kv + g;
-          const uint4 *src = reinterpret_cast<const uint4 *>(p.bounds + tile * (2 * kHeadDim));
-          lo[u] = __ldg(src + i8);
-          hi[u] = __ldg(src + 8 + i8);
-          s[u] = __ldg(p.bound_scales + tile);
+          const uint4 *src = reinterpret_cast<const uint4 *>(p.bounds + tile * (2 * kHeadDim)) + t;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) x[h][c] = __ldg(src + 4 * c);
+          s[h] = __ldg(p.bound_scales + tile);
+        }
+      }
+      float d[4] = {b0, b1, b0, b1};
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const uint32_t u[2][4] = {{x[0][c].x, x[0][c].y, x[0][c].z, x[0][c].w},
+                                  {x[1][c].x, x[1][c].y, x[1][c].z, x[1][c].w}};
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const uint32_t y0 = u[0][w] ^ 0x80808080u, y1 = u[1][w] ^ 0x80808080u;
+          mma16816(d, __byte_perm(y0, 0, 0x4140), __byte_perm(y1, 0, 0x4140),
+                   __byte_perm(y0, 0, 0x4342), __byte_perm(y1, 0, 0x4342), bq[c][w][0],
+                   bq[c][w][1]);
         }
       }
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        int d[G];
-#pragma unroll
-        for (int h = 0; h < G; ++h) {
-          int x = 0;
-          x = __dp4a((int)hi[u].x, (int)qp[h].x, x); x = __dp4a((int)hi[u].y, (int)qp[h].y, x);
-          x = __dp4a((int)hi[u].z, (int)qp[h].z, x); x = __dp4a((int)hi[u].w, (int)qp[h].w, x);
-          x = __dp4a((int)lo[u].x, (int)qn[h].x, x); x = __dp4a((int)lo[u].y, (int)qn[h].y, x);
-          x = __dp4a((int)lo[u].z, (int)qn[h].z, x); x = __dp4a((int)lo[u].w, (int)qn[h].w, x);
-          d[h] = x;
-        }
-        int off = 4;
-#pragma unroll
-        for (int m = G; m > 1; m >>= 1, off >>= 1) {
-          const bool up = (i8 & off) != 0;
-#pragma unroll
-          for (int h = 0; h < m / 2; ++h) {
-            const int keep = up ? d[h + m / 2] : d[h], send = up ? d[h] : d[h + m / 2];
-            d[h] = keep + __shfl_xor_sync(kFullMask, send, off);
-          }
-        }
-#pragma unroll
-        for (int o = 4 / G; o > 0; o >>= 1) d[0] += __shfl_xor_sync(kFullMask, d[0], o);
-        float best = (float)d[0] * f;
-#pragma unroll
-        for (int o = 4; o > 4 / G && o > 0; o >>= 1)
-          best = fmaxf(best, __shfl_xor_sync(kFullMask, best, o));
-        const int i = i0 + u * kGroups + (tid >> 3);
-        if (i < n) {
-          const int j = jlo + i;
+      for (int h = 0; h < 2; ++h) {
+        const float inf = __int_as_float(0x7f800000);
+        float best = fmaxf(2 * t < G ? d[2 * h] * 0x1p24f * f0 : -inf,
+                           2 * t + 1 < G ? d[2 * h + 1] * 0x1p24f * f1 : -inf);
+        best = fmaxf(best, __shfl_xor_sync(kFullMask, best, 1));
+        best = fmaxf(best, __shfl_xor_sync(kFullMask, best, 2));
+        const int i = i0 + r + 8 * h, j = jlo + i;
+        if (i < n && t == 0) {
           const bool forced = j < p.keep_first || j >= nblk - p.keep_last;
-          const uint32_t key = forced ? 0xffffffffu : there[u] ? order_key(best * s[u]) : 0u;
+          const uint32_t key = forced ? 0xffffffffu : there[h] ? order_key(best * s[h]) : 0u;
           if (!forced) {
             kmin = min(kmin, key);
             kmax = max(kmax, key);
           }
-          if (i8 == 0) keys[i] = key;
+          keys[i] = key;
         }
       }
     }
@@ -393,32 +426,40 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
       atomicMax(&range[1], kmax);
     }
   }
+  __syncthreads();
+  if (C > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  if (tid < 2) push_all(&all_range[rank][tid], range[tid], C);
   sync_all(C);
   // `need` of the unforced keys in [lo, hi] remain to be taken, largest first
   // (there are more unforced blocks than that).
   uint32_t lo = 0, hi = 0;
   for (int r = 0; r < C; ++r) {
-    lo = max(lo, ld_peer(&range[0], r, C));
-    hi = max(hi, ld_peer(&range[1], r, C));
+    lo = max(lo, all_range[r][0]);
+    hi = max(hi, all_range[r][1]);
   }
   lo = ~lo;
   int need = W - p.keep_first - p.keep_last;
   bool all = false;  // every key of [lo, hi] is wanted
   for (int pass = 0; need > 0 && !all && lo != hi; ++pass) {
-    uint32_t *h = hist[pass % 3];
     const int shift = max(0, 24 - __clz(hi - lo));
     for (int i = tid; i < n; i += kSelThreads) {
       const uint32_t k = keys[i];
       const int j = jlo + i;
       if (k >= lo && k <= hi && j >= p.keep_first && j < nblk - p.keep_last)
-        atomicAdd(&h[(k - lo) >> shift], 1u);
+        atomicAdd(&hist[(k - lo) >> shift], 1u);
     }
-    if (tid < 256) hist[(pass + 1) % 3][tid] = 0;
+    __syncthreads();
+    if (tid < kBins) {
+      // (this pass's half of all_hist was last read two passes ago, before the
+      // barrier that every CTA has passed since)
+      push_all(&all_hist[pass & 1][rank][tid], hist[tid], C);
+      hist[tid] = 0;
+    }
     sync_all(C);
-    const int bin = 255 - tid;
+    const int bin = kBins - 1 - tid;
     int cnt = 0, sum = 0;
-    if (tid < 256) {
-      for (int r = 0; r < C; ++r) cnt += (int)ld_peer(&h[bin], r, C);
+    if (tid < kBins) {
+      for (int r = 0; r < C; ++r) cnt += (int)all_hist[pass & 1][r][bin];
       sum = cnt;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -428,7 +469,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
       if (lane == 31) warp_cnt[0][warp] = sum;
     }
     __syncthreads();
-    if (tid < 256) {
+    if (tid < kBins) {
       for (int w = 0; w < warp; ++w) sum += warp_cnt[0][w];
       if (sum >= need && sum - cnt < need) {  // this bin holds the need-th largest
         found[0] = bin;
@@ -474,21 +515,16 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
     warp_cnt[1][warp] = n_equal;
   }
   __syncthreads();
-  if (tid == 0) {
-    int a = 0, e = 0;
-    for (int w = 0; w < kSelWarps; ++w) {
-      a += warp_cnt[0][w];
-      e += warp_cnt[1][w];
-    }
-    counts[0] = (uint32_t)a;
-    counts[1] = (uint32_t)e;
+  if (tid < 2) {
+    int a = 0;
+    for (int w = 0; w < kSelWarps; ++w) a += warp_cnt[tid][w];
+    push_all(&all_counts[rank][tid], (uint32_t)a, C);
   }
-  sync_all(C);
+  sync_all(C);  // (nobody writes into another CTA's memory after this)
   int at = 0, left = need;  // next output place, equal keys still to be taken
   for (int r = 0; r < rank; ++r) {
-    const int a = (int)ld_peer(&counts[0], r, C), e = (int)ld_peer(&counts[1], r, C);
-    const int take = min(e, left);
-    at += a + take;
+    const int take = min((int)all_counts[r][1], left);
+    at += (int)all_counts[r][0] + take;
     left -= take;
   }
   for (int w = 0; w < warp; ++w) {
@@ -508,7 +544,6 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
     at += __popc(sb);
     left -= min(left, __popc(eb));
   }
-  if (C > 1) sync_all(C);  // peers may still be reading this CTA's counts
 }
 
 }  // namespace
@@ -535,14 +570,14 @@ cudaError_t block_bounds_launch(const BoundsParams &p, cudaStream_t stream) {
 // Blocks of a sequence that the selection holds keys for.
 int select_max_blocks() { return kMaxCluster * kSliceKeys; }
 
-// CTAs per (sequence, KV head): as many as fill the GPU once, up to 8, but no
-// more than leave each 128 blocks (fewer are not worth the cluster barriers),
-// and at least as many as hold the keys.  (Clusters of 16 do not all find
-// their place at once: 8 heads of 8192 blocks take 29.8 us in clusters of 16,
-// 16.5 in 8, 21.5 in 4, 34.5 in 2.)
+// CTAs per (sequence, KV head): as many as fill the GPU once, but no more than
+// leave each 128 blocks (fewer are not worth the cluster barriers), and at
+// least as many as hold the keys.  At most 8: clusters of 16 do not all find
+// their place at once (8 heads of 8192 blocks took 29.8 us in clusters of 16,
+// 16.5 in 8, 21.5 in 4, 34.5 in 2).
 static int select_cluster(int units, int MB) {
   int C = 1;
-  while (C < 8 && units * C * 2 <= 152 && MB >= C * 2 * 128) C *= 2;
+  while (C < kMaxCluster && units * C * 2 <= 152 && MB >= C * 2 * 128) C *= 2;
   while (MB > C * kSliceKeys) C *= 2;
   return C;
 }
@@ -551,11 +586,6 @@ cudaError_t select_blocks_launch(const SelectParams &p, int G, cudaStream_t stre
   if (p.B == 0) return cudaSuccess;
   const int units = p.B * p.n_kv, C = select_cluster(units, p.MB);
   auto go = [&](auto kernel) {
-    if (C > 8) {
-      const cudaError_t e =
-          cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-      if (e != cudaSuccess) return e;
-    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(units * C));
     cfg.blockDim = dim3(kSelThreads);

@@ -189,7 +189,7 @@ SELECT_REFUSALS = [
     (dict(n_q=32), _native.ERR_UNSUPPORTED), (dict(n_q=9), _native.ERR_INVALID_ARG),
     (dict(W=0), _native.ERR_INVALID_ARG), (dict(first=-1), _native.ERR_INVALID_ARG),
     (dict(last=0), _native.ERR_INVALID_ARG), (dict(first=5, last=5), _native.ERR_INVALID_ARG),
-    (dict(MB=163841), _native.ERR_UNSUPPORTED), (dict(B=1025), _native.ERR_UNSUPPORTED),
+    (dict(MB=49153), _native.ERR_UNSUPPORTED), (dict(B=1025), _native.ERR_UNSUPPORTED),
     (dict(NB=1 << 30, n_kv=4), _native.ERR_INVALID_ARG), (dict(q=None), _native.ERR_INVALID_ARG),
     (dict(b=24), _native.ERR_INVALID_ARG), (dict(s=None), _native.ERR_INVALID_ARG),
     (dict(ti=None), _native.ERR_INVALID_ARG), (dict(tt=2), _native.ERR_INVALID_ARG),
