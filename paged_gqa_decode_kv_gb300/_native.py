@@ -4,6 +4,8 @@ The library is loaded on first use and a missing build is an error."""
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import threading
 from typing import Optional, Sequence, Tuple
@@ -355,11 +357,11 @@ def prepare(op: str, *args, **kwargs) -> PreparedCall:
     if op == "verify_step":
         return PreparedCall(*_verify_step_call(*args, **kwargs))
     if op == "paged_decode_attention_fp8b":
-        return PreparedCall(*_attention8b_call(*args, **kwargs))
+        return PreparedCall(*_prepared8b(*args, **kwargs))
     if op == "append_decode_attention_fp8b":
-        return PreparedCall(*_append_attention8b_call(*args, **kwargs))
+        return PreparedCall(*_prepared_append8b(*args, **kwargs))
     if op == "sparse_decode_attention":
-        return PreparedCall(*_sparse_call(*args, **kwargs))
+        return PreparedCall(*_prepared_sparse(*args, **kwargs))
     raise ValueError("no prepared form of %r" % op)
 
 
@@ -666,105 +668,26 @@ def append_decode_attention_fp8(out, q, k_new, v_new, k_cache, v_cache, block_ta
 
 
 # ------------------------------------------------- block-scaled 8-bit KV cache
-# A decode step's calls take a few microseconds on the GPU, so their
-# marshalling is kept to one pass over the tensors: each is checked against
-# its type, shape and device in one expression and only a mismatch is looked
-# at closer.
-_U8, _I8, _I32, _F32, _BF16 = (torch.uint8, torch.int8, torch.int32, torch.float32,
-                               torch.bfloat16)
-_fns = {}
+# The calls of this section and the next check and convert their tensors in
+# binding/tensors.cpp: they run for a few microseconds on the GPU, and a dozen
+# tensors took longer than that in Python.
+_tensor_side = None
 
 
-def _fn(name: str):
-    f = _fns.get(name)
-    if f is None:
-        f = _fns[name] = getattr(lib(), name)
-    return f
-
-
-def _refuse(t, dtype, shape, name, dev) -> None:
-    if not isinstance(t, torch.Tensor):
-        raise TypeError("%s must be a tensor, got %s" % (name, type(t).__name__))
-    if t.dtype != dtype:
-        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError("%s must be %s, got %s" % (name, list(shape), list(t.shape)))
-    if not t.is_contiguous():
-        raise ValueError("%s must be contiguous" % name)
-    if not t.is_cuda:
-        raise ValueError("%s must be on a CUDA device" % name)
-    raise ValueError("%s is on %s, the call on cuda:%d" % (name, t.device, dev))
-
-
-def _take(dev: int, *specs) -> list:
-    """Device addresses of tensors given as (tensor, dtype, shape, name), each
-    contiguous and on device `dev`; None (an optional tensor left out) stays
-    None."""
-    ptrs = []
-    for t, dtype, shape, name in specs:
-        if t is None:
-            ptrs.append(None)
-            continue
-        try:
-            fine = (t.dtype is dtype and t.shape == shape and t.is_contiguous()
-                    and t.get_device() == dev and dev >= 0)
-        except AttributeError:
-            fine = False
-        if not fine:
-            _refuse(t, dtype, shape, name, dev)
-        ptrs.append(t.data_ptr())
-    return ptrs
-
-
-def _raw_stream(stream, dev: int) -> int:
-    """The given stream, or the current one of `dev`, which must be the
-    current device: the library launches there."""
-    if torch._C._cuda_getDevice() != dev:
-        raise ValueError("the tensors are on cuda:%d, the current device is cuda:%d"
-                         % (dev, torch._C._cuda_getDevice()))
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
-
-
-def _sizes(t, n: int, name: str, dtype=None):
-    """The n sizes of a tensor's shape (of the given type, if any)."""
-    if dtype is not None and isinstance(t, torch.Tensor) and t.dtype != dtype:
-        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if not isinstance(t, torch.Tensor) or t.dim() != n:
-        raise ValueError("%s must be a tensor of %d dims, got %s" % (
-            name, n, list(t.shape) if isinstance(t, torch.Tensor) else type(t).__name__))
-    return t.shape
-
-
-def _range_call(name, k_rows, v_rows, k_cache, v_cache, k_scales, v_scales, block_tables,
-                positions, token_starts, max_tokens, stream):
-    pool = _sizes(k_cache, 6, "k_cache")
-    NB, n_kv, rg = pool[:3]
-    B, MB = _sizes(block_tables, 2, "block_tables")
-    dev, rows = k_cache.get_device(), k_rows.shape
-    row_ptrs = _take(dev, (k_rows, _BF16, rows, "k rows"), (v_rows, _BF16, rows, "v rows"))
-    if len(rows) < 3 or rows[-2] != n_kv or rows[-1] != HEAD_DIM:
-        raise ValueError("rows must end in [%d][%d], got %s" % (n_kv, HEAD_DIM, list(rows)))
-    N = k_rows.numel() // (n_kv * HEAD_DIM)
-    if token_starts is None:
-        if (N and not B) or (B and N % B):
-            raise ValueError("%d rows for %d sequences" % (N, B))
-        T = N // B if B else 0
-        if max_tokens is not None and max_tokens != T:
-            raise ValueError("max_tokens = %d, but every sequence has %d" % (max_tokens, T))
-    elif max_tokens is None:
-        raise ValueError("token_starts needs max_tokens, the most tokens of a sequence")
-    else:
-        T = int(max_tokens)
-    pool, scales = (NB, n_kv, rg, 8, 8, 16), (NB, n_kv)
-    ptrs = _take(dev, (k_cache, _U8, pool, "k_cache"), (v_cache, _U8, pool, "v_cache"),
-                 (k_scales, _F32, scales, "k_scales"), (v_scales, _F32, scales, "v_scales"),
-                 (block_tables, _I32, (B, MB), "block_tables"),
-                 (positions, _I32, (B,), "positions"),
-                 (token_starts, _I32, (B + 1,), "token_starts"))
-    s = _fn(name)(*row_ptrs, *ptrs, B, T, N, n_kv, HEAD_DIM, rg * 8, MB, NB,
-                  _raw_stream(stream, dev))
-    if s:
-        _check(s)
+def _tensors():
+    """The binding's tensor extension.  Raises if it has not been built."""
+    global _tensor_side
+    if _tensor_side is None:
+        lib()  # (a missing build says so)
+        path = _build.tensors_path()
+        if not os.path.exists(path):
+            raise RuntimeError("%s is not built; run paged_gqa_decode_kv_gb300.build.build()" % path)
+        loader = importlib.machinery.ExtensionFileLoader("_pgd_tensors", path)
+        spec = importlib.util.spec_from_file_location("_pgd_tensors", path, loader=loader)
+        module = importlib.util.module_from_spec(spec)
+        loader.exec_module(module)
+        _tensor_side = module
+    return _tensor_side
 
 
 def kv_append_fp8b(k_new, v_new, k_cache, v_cache, k_scales, v_scales, block_tables, positions,
@@ -775,45 +698,52 @@ def kv_append_fp8b(k_new, v_new, k_cache, v_cache, k_scales, v_scales, block_tab
     ([N][n_kv][d] bf16; at most max_tokens each), or without token_starts the
     same number of tokens for every sequence ([B][n_kv][d] or
     [B][T][n_kv][d])."""
-    _range_call("pgd_kv_append_fp8b", k_new, v_new, k_cache, v_cache, k_scales, v_scales,
-                block_tables, positions, token_starts, max_tokens, stream)
+    s = (_tensor_side or _tensors()).range(
+        False, k_new, v_new, k_cache, v_cache, k_scales, v_scales, block_tables, positions,
+        token_starts, max_tokens, stream)
+    if s:
+        _check(s)
 
 
 def kv_read_fp8b(k_out, v_out, k_cache, v_cache, k_scales, v_scales, block_tables, positions,
                  token_starts=None, max_tokens: Optional[int] = None, stream=None) -> None:
     """Read ranges of positions back into rows of k_out/v_out (bf16): the
     arguments of kv_append_fp8b, the other way."""
-    _range_call("pgd_kv_read_fp8b", k_out, v_out, k_cache, v_cache, k_scales, v_scales,
-                block_tables, positions, token_starts, max_tokens, stream)
+    s = (_tensor_side or _tensors()).range(
+        True, k_out, v_out, k_cache, v_cache, k_scales, v_scales, block_tables, positions,
+        token_starts, max_tokens, stream)
+    if s:
+        _check(s)
 
 
-def _attention8b_call(out, q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
-                      scale, num_splits=0, workspace=None, stream=None, new=()):
-    NB, n_kv, rg = _sizes(k_cache, 6, "k_cache", _U8)[:3]
-    B, n_q, d = _sizes(q, 3, "q")
-    MB = _sizes(block_tables, 2, "block_tables")[1]
-    dev = q.get_device()
-    pool, scales, rows = (NB, n_kv, rg, 8, 8, 16), (NB, n_kv), (B, n_kv, d)
-    ptrs = _take(dev, (q, _BF16, (B, n_q, d), "q"), (k_cache, _U8, pool, "k_cache"),
-                 (v_cache, _U8, pool, "v_cache"), (k_scales, _F32, scales, "k_scales"),
-                 (v_scales, _F32, scales, "v_scales"),
-                 (block_tables, _I32, (B, MB), "block_tables"),
-                 (context_lens, _I32, (B,), "context_lens"))
-    if new:
-        ptrs[1:1] = _take(dev, (new[0], _BF16, rows, "k_new"), (new[1], _BF16, rows, "v_new"))
+def _out_and_scratch(out, q, n_kv, num_splits, workspace):
+    """The output and the workspace of a decode call, made where not given."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be [B][n_q][d]")
     if out is None:
         out = torch.empty_like(q)
     if workspace is None:
-        workspace = make_workspace(B, n_q, n_kv, num_splits, q.device)
-    po, = _take(dev, (out, _BF16, (B, n_q, d), "out"))
-    pw, = _take(dev, (workspace, workspace.dtype, workspace.shape, "workspace"))
-    name = "pgd_append_decode_attention_fp8b" if new else "pgd_paged_decode_attention_fp8b"
-    return name, (po, *ptrs, B, n_q, n_kv, d, rg * 8, MB, NB, float(scale), int(num_splits), pw,
-                  workspace.nbytes, _raw_stream(stream, dev)), out
+        if not q.is_cuda:
+            raise ValueError("q must be on a CUDA device")
+        workspace = make_workspace(q.shape[0], q.shape[1], max(1, n_kv), num_splits, q.device)
+    return out, workspace
 
 
-def _append_attention8b_call(out, q, k_new, v_new, *args, **kwargs):
-    return _attention8b_call(out, q, *args, new=(k_new, v_new), **kwargs)
+def _pool_heads(k_cache) -> int:
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 6:
+        raise ValueError("k_cache must be a pool of 6 dims")
+    return k_cache.shape[1]
+
+
+def _attention8b(pack, out, q, k_new, v_new, k_cache, v_cache, k_scales, v_scales, block_tables,
+                 context_lens, scale, num_splits, workspace, stream):
+    if out is None or workspace is None:
+        if isinstance(k_cache, torch.Tensor) and k_cache.dtype != torch.uint8:
+            raise TypeError("k_cache must be torch.uint8, got %s" % k_cache.dtype)
+        out, workspace = _out_and_scratch(out, q, _pool_heads(k_cache), num_splits, workspace)
+    return out, (_tensor_side or _tensors()).attention(
+        out, q, k_new, v_new, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
+        scale, num_splits, workspace, stream, pack)
 
 
 def paged_decode_attention_fp8b(out, q, k_cache, v_cache, k_scales, v_scales, block_tables,
@@ -822,10 +752,8 @@ def paged_decode_attention_fp8b(out, q, k_cache, v_cache, k_scales, v_scales, bl
                                 stream=None) -> torch.Tensor:
     """out[B][n_q][d] (bf16) = paged decode attention of q over the
     block-scaled 8-bit cache."""
-    name, args, out = _attention8b_call(out, q, k_cache, v_cache, k_scales, v_scales,
-                                        block_tables, context_lens, scale, num_splits, workspace,
-                                        stream)
-    s = _fn(name)(*args)
+    out, s = _attention8b(False, out, q, None, None, k_cache, v_cache, k_scales, v_scales,
+                          block_tables, context_lens, scale, num_splits, workspace, stream)
     if s:
         _check(s)
     return out
@@ -837,32 +765,14 @@ def append_decode_attention_fp8b(out, q, k_new, v_new, k_cache, v_cache, k_scale
                                  stream=None) -> torch.Tensor:
     """kv_append_fp8b of one token per sequence at context_lens - 1, then
     attention over the block-scaled cache."""
-    name, args, out = _append_attention8b_call(out, q, k_new, v_new, k_cache, v_cache, k_scales,
-                                               v_scales, block_tables, context_lens, scale,
-                                               num_splits, workspace, stream)
-    s = _fn(name)(*args)
+    out, s = _attention8b(False, out, q, k_new, v_new, k_cache, v_cache, k_scales, v_scales,
+                          block_tables, context_lens, scale, num_splits, workspace, stream)
     if s:
         _check(s)
     return out
 
 
 # ------------------------------------------------------ block-sparse attention
-def _kv_specs(k_cache, v_cache, k_scales, v_scales, with_v=True):
-    """(NB, n_kv, bs, specs of the pools and scales) of a bf16 cache, or of a
-    block-scaled one (with scales)."""
-    if (k_scales is None) != (v_scales is None) and with_v:
-        raise ValueError("a block-scaled cache needs both scales")
-    if k_scales is not None:
-        NB, n_kv, rg = _sizes(k_cache, 6, "k_cache")[:3]
-        pool, dtype = (NB, n_kv, rg, 8, 8, 16), _U8
-    else:
-        NB, n_kv, rg = _sizes(k_cache, 6, "k_cache")[:3]
-        pool, dtype = (NB, n_kv, rg, 16, 8, 8), _BF16
-    return NB, n_kv, rg * 8, ((k_cache, dtype, pool, "k_cache"), (v_cache, dtype, pool, "v_cache"),
-                              (k_scales, _F32, (NB, n_kv), "k_scales"),
-                              (v_scales, _F32, (NB, n_kv), "v_scales"))
-
-
 def block_bounds(bounds, bound_scales, k_cache, block_tables, context_lens, positions=None,
                  max_tokens: Optional[int] = None, k_scales=None, stream=None) -> None:
     """Recompute the key bounds (int8 [NB][n_kv][2][d], fp32 [NB][n_kv]) of
@@ -870,15 +780,8 @@ def block_bounds(bounds, bound_scales, k_cache, block_tables, context_lens, posi
     the whole contexts) of a bf16 cache, or of a block-scaled one with its
     k_scales.  max_tokens: the most tokens of a sequence (default: the table
     width)."""
-    NB, n_kv, bs, (k_spec, _, scale_spec, _) = _kv_specs(k_cache, None, k_scales, None, False)
-    B, MB = _sizes(block_tables, 2, "block_tables")
-    dev = k_cache.get_device()
-    ptrs = _take(dev, (bounds, _I8, (NB, n_kv, 2, HEAD_DIM), "bounds"),
-                 (bound_scales, _F32, (NB, n_kv), "bound_scales"), k_spec, scale_spec,
-                 (block_tables, _I32, (B, MB), "block_tables"),
-                 (positions, _I32, (B,), "positions"), (context_lens, _I32, (B,), "context_lens"))
-    T = MB * bs if max_tokens is None else int(max_tokens)
-    s = _fn("pgd_block_bounds")(*ptrs, B, T, n_kv, HEAD_DIM, bs, MB, NB, _raw_stream(stream, dev))
+    s = (_tensor_side or _tensors()).bounds(bounds, bound_scales, k_cache, block_tables,
+                                            context_lens, positions, max_tokens, k_scales, stream)
     if s:
         _check(s)
 
@@ -888,51 +791,24 @@ def select_blocks(tiles, tile_tokens, q, bounds, bound_scales, block_tables, con
     """tiles [B][n_kv][W] and tile_tokens [B][n_kv] (int32): for every
     sequence and KV head the first keep_first blocks, the last keep_last and
     the others of the largest score, W in all."""
-    NB, n_kv = _sizes(bounds, 4, "bounds", _I8)[:2]
-    B, n_q, d = _sizes(q, 3, "q")
-    W = _sizes(tiles, 3, "tiles")[2]
-    MB = _sizes(block_tables, 2, "block_tables")[1]
-    dev = q.get_device()
-    ptrs = _take(dev, (tiles, _I32, (B, n_kv, W), "tiles"),
-                 (tile_tokens, _I32, (B, n_kv), "tile_tokens"), (q, _BF16, (B, n_q, d), "q"),
-                 (bounds, _I8, (NB, n_kv, 2, HEAD_DIM), "bounds"),
-                 (bound_scales, _F32, (NB, n_kv), "bound_scales"),
-                 (block_tables, _I32, (B, MB), "block_tables"),
-                 (context_lens, _I32, (B,), "context_lens"))
-    s = _fn("pgd_select_blocks")(*ptrs, B, n_q, n_kv, d, int(block_size), MB, NB, W,
-                                 int(keep_first), int(keep_last), _raw_stream(stream, dev))
+    s = (_tensor_side or _tensors()).select(tiles, tile_tokens, q, bounds, bound_scales,
+                                            block_tables, context_lens, keep_first, keep_last,
+                                            block_size, stream)
     if s:
         _check(s)
 
 
-def _tiles_call(name, out, q, k_cache, v_cache, k_scales, v_scales, middle, tiles, tile_tokens,
-                keep, scale, num_splits, workspace, stream):
-    """A call over W tiles per (sequence, KV head); `middle` (the selection's
-    inputs: bounds, bound_scales, block_tables, context_lens) and `keep` are
-    empty where the tiles are given."""
-    NB, n_kv, bs, specs = _kv_specs(k_cache, v_cache, k_scales, v_scales)
-    B, n_q, d = _sizes(q, 3, "q")
-    W = _sizes(tiles, 3, "tiles")[2]
-    dev = q.get_device()
-    ints = [B, n_q, n_kv, d, bs, NB, W]
-    if middle:
-        MB = _sizes(middle[2], 2, "block_tables")[1]
-        ints.insert(5, MB)
-        specs += ((middle[0], _I8, (NB, n_kv, 2, HEAD_DIM), "bounds"),
-                  (middle[1], _F32, (NB, n_kv), "bound_scales"),
-                  (middle[2], _I32, (B, MB), "block_tables"),
-                  (middle[3], _I32, (B,), "context_lens"))
-    ptrs = _take(dev, (q, _BF16, (B, n_q, d), "q"), *specs,
-                 (tiles, _I32, (B, n_kv, W), "tiles"),
-                 (tile_tokens, _I32, (B, n_kv), "tile_tokens"))
-    if out is None:
-        out = torch.empty_like(q)
-    if workspace is None:
-        workspace = make_workspace(B, n_q, n_kv, num_splits, q.device)
-    po, = _take(dev, (out, _BF16, (B, n_q, d), "out"))
-    pw, = _take(dev, (workspace, workspace.dtype, workspace.shape, "workspace"))
-    return name, (po, *ptrs, *ints, *keep, float(scale), int(num_splits), pw, workspace.nbytes,
-                  _raw_stream(stream, dev)), out
+def _tiles_attention(pack, out, q, k_cache, v_cache, k_scales, v_scales, bounds, bound_scales,
+                     block_tables, context_lens, tiles, tile_tokens, keep_first, keep_last, scale,
+                     num_splits, workspace, stream):
+    if out is None or workspace is None:
+        if (k_scales is None) != (v_scales is None):
+            raise ValueError("a block-scaled cache needs both scales")
+        out, workspace = _out_and_scratch(out, q, _pool_heads(k_cache), num_splits, workspace)
+    return out, (_tensor_side or _tensors()).tiles(
+        out, q, k_cache, v_cache, k_scales, v_scales, bounds, bound_scales, block_tables,
+        context_lens, tiles, tile_tokens, keep_first, keep_last, scale, num_splits, workspace,
+        stream, pack)
 
 
 def selected_decode_attention(out, q, k_cache, v_cache, tiles, tile_tokens, scale: float,
@@ -942,21 +818,12 @@ def selected_decode_attention(out, q, k_cache, v_cache, tiles, tile_tokens, scal
     """out[B][n_q][d] (bf16) = decode attention of q over the tiles (block *
     n_kv + head, [B][n_kv][W]) of a bf16 cache, or of a block-scaled one with
     its scales."""
-    name, args, out = _tiles_call("pgd_selected_decode_attention", out, q, k_cache, v_cache,
-                                  k_scales, v_scales, (), tiles, tile_tokens, (), scale,
-                                  num_splits, workspace, stream)
-    s = _fn(name)(*args)
+    out, s = _tiles_attention(False, out, q, k_cache, v_cache, k_scales, v_scales, None, None,
+                              None, None, tiles, tile_tokens, 0, 0, scale, num_splits, workspace,
+                              stream)
     if s:
         _check(s)
     return out
-
-
-def _sparse_call(out, q, k_cache, v_cache, bounds, bound_scales, block_tables, context_lens,
-                 tiles, tile_tokens, keep_first, keep_last, scale, k_scales=None, v_scales=None,
-                 num_splits=0, workspace=None, stream=None):
-    return _tiles_call("pgd_sparse_decode_attention", out, q, k_cache, v_cache, k_scales, v_scales,
-                       (bounds, bound_scales, block_tables, context_lens), tiles, tile_tokens,
-                       (int(keep_first), int(keep_last)), scale, num_splits, workspace, stream)
 
 
 def sparse_decode_attention(out, q, k_cache, v_cache, bounds, bound_scales, block_tables,
@@ -966,13 +833,37 @@ def sparse_decode_attention(out, q, k_cache, v_cache, bounds, bound_scales, bloc
                             stream=None) -> torch.Tensor:
     """select_blocks into tiles and tile_tokens, then
     selected_decode_attention over them, in one call."""
-    name, args, out = _sparse_call(out, q, k_cache, v_cache, bounds, bound_scales, block_tables,
-                                   context_lens, tiles, tile_tokens, keep_first, keep_last, scale,
-                                   k_scales, v_scales, num_splits, workspace, stream)
-    s = _fn(name)(*args)
+    if bounds is None:
+        raise TypeError("bounds must be a tensor")
+    out, s = _tiles_attention(False, out, q, k_cache, v_cache, k_scales, v_scales, bounds,
+                              bound_scales, block_tables, context_lens, tiles, tile_tokens,
+                              keep_first, keep_last, scale, num_splits, workspace, stream)
     if s:
         _check(s)
     return out
+
+
+def _prepared8b(out, q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, scale,
+                num_splits=0, workspace=None, stream=None):
+    out, args = _attention8b(True, out, q, None, None, k_cache, v_cache, k_scales, v_scales,
+                             block_tables, context_lens, scale, num_splits, workspace, stream)
+    return "pgd_paged_decode_attention_fp8b", args, out
+
+
+def _prepared_append8b(out, q, k_new, v_new, k_cache, v_cache, k_scales, v_scales, block_tables,
+                       context_lens, scale, num_splits=0, workspace=None, stream=None):
+    out, args = _attention8b(True, out, q, k_new, v_new, k_cache, v_cache, k_scales, v_scales,
+                             block_tables, context_lens, scale, num_splits, workspace, stream)
+    return "pgd_append_decode_attention_fp8b", args, out
+
+
+def _prepared_sparse(out, q, k_cache, v_cache, bounds, bound_scales, block_tables, context_lens,
+                     tiles, tile_tokens, keep_first, keep_last, scale, k_scales=None,
+                     v_scales=None, num_splits=0, workspace=None, stream=None):
+    out, args = _tiles_attention(True, out, q, k_cache, v_cache, k_scales, v_scales, bounds,
+                                 bound_scales, block_tables, context_lens, tiles, tile_tokens,
+                                 keep_first, keep_last, scale, num_splits, workspace, stream)
+    return "pgd_sparse_decode_attention", args, out
 
 
 def copy_blocks(k_cache, v_cache, src_ids, dst_ids, stream=None) -> None:

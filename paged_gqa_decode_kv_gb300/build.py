@@ -3,17 +3,21 @@
 Each CUDA translation unit is compiled by nvcc with one -gencode
 (compute_103a -> sm_103a), in parallel, and the objects are linked into
 ``paged_gqa_decode_kv_gb300/_build/libpgd.so`` (CUDA runtime linked
-statically).  Rebuilds only when a source or header is newer than the
-library.
+statically).  Beside it, ``_pgd_tensors``: the part of the binding that reads
+torch tensors, a CPython extension built against the installed torch (whose
+version is part of its file name).  Rebuilds only when a source or header is
+newer than the library.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
 import os
+import re
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -21,6 +25,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libpgd.so")
 HEADER = os.path.join(ROOT, "include", "pgd.h")
+TENSORS_SRC = os.path.join(HERE, "binding", "tensors.cpp")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-Wall",
@@ -39,17 +44,43 @@ def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "*.cpp")))
 
 
+def tensors_path() -> str:
+    """The binding's tensor extension for the installed torch."""
+    import torch
+
+    tag = re.sub(r"[^0-9a-zA-Z]+", "_", torch.__version__)
+    return os.path.join(BUILD, "_pgd_tensors_torch_%s.so" % tag)
+
+
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(tensors_path()):
         return True
-    t = os.path.getmtime(LIB)
-    deps = sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + [HEADER, __file__]
+    t = min(os.path.getmtime(LIB), os.path.getmtime(tensors_path()))
+    deps = sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + [HEADER, TENSORS_SRC, __file__]
     return any(os.path.getmtime(p) > t for p in deps)
+
+
+def _torch_flags():
+    """Compile and link flags of an extension against the installed torch."""
+    import torch
+
+    at = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    inc = [os.path.join(at, "include"), os.path.join(at, "include", "torch", "csrc", "api",
+                                                     "include"),
+           os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    abi = int(torch._C._GLIBCXX_USE_CXX11_ABI)
+    lib = os.path.join(at, "lib")
+    return (["-D_GLIBCXX_USE_CXX11_ABI=%d" % abi] + [x for p in inc for x in ("-isystem", p)],
+            ["-L" + lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python",
+             "-Wl,-rpath," + lib])
 
 
 def _compile(src: str, verbose_ptxas: bool) -> str:
     obj = os.path.join(BUILD, os.path.basename(src) + ".o")
-    if src.endswith(".cu"):
+    if src == TENSORS_SRC:
+        cmd = [os.environ.get("CXX", "g++")] + CXX_FLAGS + _torch_flags()[0] + ["-c", src, "-o", obj]
+    elif src.endswith(".cu"):
         cmd = [_nvcc()] + ARCH + NVCC_FLAGS + (["-Xptxas", "-v"] if verbose_ptxas else []) + \
             ["-c", src, "-o", obj]
     else:
@@ -67,16 +98,22 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     if not force and not verbose_ptxas and not _stale():
         return LIB
     os.makedirs(BUILD, exist_ok=True)
-    srcs = sources()
+    srcs = [TENSORS_SRC] + sources()
     with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 1))) as ex:
         objs = list(ex.map(lambda s: _compile(s, verbose_ptxas), srcs))
-    tmp = LIB + ".tmp.%d" % os.getpid()
-    cmd = [_nvcc()] + ARCH + ["-shared", "-Xcompiler", "-fPIC", "-o", tmp] + objs
+    _link([_nvcc()] + ARCH + ["-shared", "-Xcompiler", "-fPIC"] + objs[1:], LIB)
+    _link([os.environ.get("CXX", "g++"), "-shared", objs[0], "-L" + BUILD, "-lpgd",
+           "-Wl,-rpath,$ORIGIN"] + _torch_flags()[1], tensors_path())
+    return LIB
+
+
+def _link(cmd, path: str) -> None:
+    tmp = path + ".tmp.%d" % os.getpid()
+    cmd = cmd + ["-o", tmp]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("link failed: %s\n%s\n%s" % (" ".join(cmd), r.stdout, r.stderr))
-    os.replace(tmp, LIB)
-    return LIB
+    os.replace(tmp, path)
 
 
 if __name__ == "__main__":
