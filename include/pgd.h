@@ -500,10 +500,22 @@ pgd_status pgd_append_decode_attention_fp8(void *out, const void *q, const void 
  *
  * pgd_paged_decode_attention_fp8b, pgd_append_decode_attention_fp8b: the calls
  * of those names over this cache -- same definition on the dequantised K and
- * V, same arguments (and the scales), checks, errors and workspace
- * (pgd_attention_workspace_size).  The append is pgd_kv_append_fp8b of one
- * token at context_lens[b] - 1.  The query must be finite.  B * n_kv *
- * (MB + 24) must be below 2^31. */
+ * V, same arguments (and the scales), checks and errors.  The append is
+ * pgd_kv_append_fp8b of one token at context_lens[b] - 1.  The query must be
+ * finite.  B * n_kv at most 65536, B * n_kv * (MB + 24) below 2^31.  Arithmetic:
+ * q.k^T and p.v on the tensor cores on the codes themselves, the query as two
+ * E4M3 terms, a probability (times V's scale) as three, to 2^-12 of itself and
+ * 2^-24 of the largest; scales, softmax and accumulation in fp32; bf16 output.
+ * An automatic call (num_splits = 0) of few heads and at most 1024 tokens (the
+ * limit of pgd_set_short_context_tokens) runs on the CUDA cores in fp32.
+ *
+ * workspace: device scratch of pgd_block_workspace_size(...) bytes (0 for
+ * arguments outside the limits), 256-byte aligned, zero-filled before its first
+ * use.  Completed calls leave it ready for the next of any sizes: one serves
+ * every call of this section and the next in stream order.  Concurrent calls
+ * need separate ones, and so do the calls of other sections. */
+size_t pgd_block_workspace_size(int32_t B, int32_t n_q, int32_t n_kv, int32_t d,
+                                int32_t num_splits);
 pgd_status pgd_kv_append_fp8b(const void *k_new, const void *v_new, void *k_cache, void *v_cache,
                               float *k_scales, float *v_scales, const int32_t *block_tables,
                               const int32_t *positions, const int32_t *token_starts, int32_t B,
@@ -572,9 +584,8 @@ pgd_status pgd_append_decode_attention_fp8b(
  * pgd_paged_decode_attention_fp8b, with tile ids checked against NB * n_kv and
  * tile_tokens against [1, W * bs].  pgd_sparse_decode_attention is both calls
  * in one, every argument checked before the first launch; tiles and
- * tile_tokens are outputs too.  workspace as for pgd_paged_decode_attention
- * (pgd_attention_workspace_size(B, n_q, n_kv, d, num_splits) bytes).
- * B * n_kv at most PGD_MAX_BATCH. */
+ * tile_tokens are outputs too.  workspace: pgd_block_workspace_size(B, n_q,
+ * n_kv, d, num_splits) bytes, as above.  B * n_kv at most PGD_MAX_BATCH. */
 pgd_status pgd_block_bounds(int8_t *bounds, float *bound_scales, const void *k_cache,
                             const float *k_scales, const int32_t *block_tables,
                             const int32_t *positions, const int32_t *context_lens, int32_t B,

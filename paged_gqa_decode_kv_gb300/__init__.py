@@ -13,7 +13,7 @@ from ._native import (  # noqa: F401
     kv_append_fp8, paged_decode_attention_fp8, append_decode_attention_fp8,
     cascade_decode_attention, cascade_workspace_size, kv_append_tokens, paged_verify_attention,
     kv_append_fp8b, kv_read_fp8b, paged_decode_attention_fp8b, append_decode_attention_fp8b,
-    block_bounds, select_blocks, selected_decode_attention, sparse_decode_attention,
+    block_workspace_size, make_block_workspace, block_bounds, select_blocks, selected_decode_attention, sparse_decode_attention,
     append_verify_attention, verify_step, verify_workspace_size, mla_append, mla_decode_attention,
     mla_append_decode_attention, mla_step, mla_workspace_size, device_errors,
     workspace_size, make_workspace, attention_grid, validate_tables, read_stream, set_wait_limit_ns,
@@ -26,7 +26,8 @@ __all__ = ["WORKLOADS", "Workload", "PagedBatch", "make_batch", "make_workload",
            "paged_decode_attention_noalloc", "append_decode_attention", "decode_step",
            "copy_blocks", "kv_append_fp8", "paged_decode_attention_fp8",
            "append_decode_attention_fp8", "kv_append_fp8b", "kv_read_fp8b",
-           "paged_decode_attention_fp8b", "append_decode_attention_fp8b", "block_bounds",
+           "paged_decode_attention_fp8b", "append_decode_attention_fp8b", "block_workspace_size",
+           "make_block_workspace", "block_bounds",
            "select_blocks", "selected_decode_attention", "sparse_decode_attention", "cascade_decode_attention", "cascade_workspace_size",
            "kv_append_tokens", "paged_verify_attention", "append_verify_attention",
            "verify_step", "verify_workspace_size",

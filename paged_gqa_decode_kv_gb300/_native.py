@@ -68,6 +68,7 @@ SIGNATURES = {
                          _I, _I, _F, _I, _P, _Z, _P], _I),
     "pgd_decode_step_fp8": ([_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I,
                              _I, _I, _I, _F, _I, _P, _Z, _P], _I),
+    "pgd_block_workspace_size": ([_I, _I, _I, _I, _I], _Z),
     "pgd_kv_append_fp8b": ([_P] * 9 + [_I] * 8 + [_P], _I),
     "pgd_kv_read_fp8b": ([_P] * 9 + [_I] * 8 + [_P], _I),
     "pgd_paged_decode_attention_fp8b": ([_P] * 8 + [_I] * 7 + [_F, _I, _P, _Z, _P], _I),
@@ -690,6 +691,19 @@ def _tensors():
     return _tensor_side
 
 
+def block_workspace_size(B: int, n_q: int, n_kv: int, num_splits: int = 0,
+                         d: int = HEAD_DIM) -> int:
+    return int(lib().pgd_block_workspace_size(B, n_q, n_kv, d, num_splits))
+
+
+def make_block_workspace(B: int, n_q: int, n_kv: int, num_splits: int = 0,
+                         device=None) -> torch.Tensor:
+    """A zero-filled workspace of the block-scaled and selected attention
+    calls; one serves calls of any sizes up to these, in stream order."""
+    n = max(1, block_workspace_size(B, n_q, n_kv, num_splits))
+    return torch.zeros(n, dtype=torch.uint8, device=device or torch.device("cuda"))
+
+
 def kv_append_fp8b(k_new, v_new, k_cache, v_cache, k_scales, v_scales, block_tables, positions,
                    token_starts=None, max_tokens: Optional[int] = None, stream=None) -> None:
     """Quantise new tokens into the block-scaled pools (uint8
@@ -725,7 +739,7 @@ def _out_and_scratch(out, q, n_kv, num_splits, workspace):
     if workspace is None:
         if not q.is_cuda:
             raise ValueError("q must be on a CUDA device")
-        workspace = make_workspace(q.shape[0], q.shape[1], max(1, n_kv), num_splits, q.device)
+        workspace = make_block_workspace(q.shape[0], q.shape[1], n_kv, num_splits, q.device)
     return out, workspace
 
 

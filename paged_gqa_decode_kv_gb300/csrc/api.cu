@@ -144,13 +144,18 @@ int unit_rows(int T, int Gh) {
   return g;
 }
 
-WsLayout ws_layout(int32_t B, int32_t n_q, int32_t n_kv, long long grid) {
+// Block-scaled and selected attention (`blocks`) give the counters a region of
+// one size whatever the call's, so that no call's partial states lie where
+// another's counters must be zero: one workspace serves calls of any sizes.
+constexpr long long kMaxBlockUnits = 65536;
+
+WsLayout ws_layout(int32_t B, int32_t n_q, int32_t n_kv, long long grid, bool blocks = false) {
   WsLayout L;
   const int G = n_q / n_kv;
   const long long units = (long long)B * n_kv;
   L.slots = units + grid;
   L.counters = 0;
-  L.part_ml = round_up((size_t)units * 4, kWsAlign);
+  L.part_ml = round_up((size_t)(blocks ? kMaxBlockUnits : units) * 4, kWsAlign);
   L.part_o = L.part_ml + round_up((size_t)L.slots * G * 2 * 4, kWsAlign);
   L.total = L.part_o + (size_t)L.slots * G * kHeadDim * 4;
   return L;
@@ -219,7 +224,8 @@ pgd_status prepare_attention(void *out, const void *q, const void *k_cache, cons
                              const int32_t *tables, const int32_t *ctx, int32_t B, int32_t n_q,
                              int32_t n_kv, int32_t bs, int32_t MB, int32_t NB, float scale,
                              int32_t num_splits, void *workspace, size_t workspace_bytes,
-                             PreparedAttention *pa, bool fp8 = false, int32_t T = 1) {
+                             PreparedAttention *pa, bool fp8 = false, int32_t T = 1,
+                             bool blocks = false) {
   if (!workspace) return fail(PGD_ERR_WORKSPACE, "workspace is NULL");
   if (!aligned(workspace, kWsAlign)) return fail(PGD_ERR_WORKSPACE, "workspace not 256-aligned");
   // query rows per unit: T tokens x the KV head's query heads, padded to a
@@ -229,7 +235,7 @@ pgd_status prepare_attention(void *out, const void *q, const void *k_cache, cons
   if (G == 0 || (fp8 && T != 1))
     return fail(PGD_ERR_UNSUPPORTED, "T = %d x %d heads per KV head (at most 16 rows)", T, Gh);
   const int32_t n_rows = G * n_kv;
-  if (workspace_bytes < ws_layout(B, n_rows, n_kv, 1).total)
+  if (workspace_bytes < ws_layout(B, n_rows, n_kv, 1, blocks).total)
     return fail(PGD_ERR_WORKSPACE, "workspace %zu bytes is too small", workspace_bytes);
   int grid = 0;
   if (num_splits > 0) {
@@ -238,7 +244,7 @@ pgd_status prepare_attention(void *out, const void *q, const void *k_cache, cons
     pgd_status s = auto_grid(G, bs, B, &grid, fp8);
     if (s != PGD_OK) return s;
   }
-  const WsLayout L = ws_layout(B, n_rows, n_kv, grid);
+  const WsLayout L = ws_layout(B, n_rows, n_kv, grid, blocks);
   if (workspace_bytes < L.total)
     return fail(PGD_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, L.total);
   int32_t *err = nullptr;
@@ -1269,6 +1275,14 @@ pgd_status pgd_device_errors(int32_t *flags, int32_t clear, void *stream) {
   return ok();
 }
 
+size_t pgd_block_workspace_size(int32_t B, int32_t n_q, int32_t n_kv, int32_t d,
+                                int32_t num_splits) {
+  const size_t n = pgd_attention_workspace_size(B, n_q, n_kv, d, num_splits);
+  const long long units = (long long)B * n_kv;
+  if (n == 0 || units > kMaxBlockUnits) return 0;
+  return n - round_up((size_t)units * 4, kWsAlign) + (size_t)kMaxBlockUnits * 4;
+}
+
 // ------------------------------------------------ block-scaled 8-bit cache
 // Checks shared by the write, the read-back and the key bounds: sizes, the
 // packed rows and the largest grid (one warp per block, head and pool).
@@ -1292,8 +1306,10 @@ static pgd_status check_scales(const float *k_scales, const float *v_scales) {
 }
 
 // The block-scaled attention's cost space (blocks, and up to 24 for each unit)
-// is 32 bits wide.
+// is 32 bits wide, its workspace has kMaxBlockUnits counters.
 static pgd_status check_cost_space(int32_t B, int32_t n_kv, int32_t MB) {
+  if ((long long)B * n_kv > kMaxBlockUnits)
+    return fail(PGD_ERR_UNSUPPORTED, "B * n_kv = %lld > %lld", (long long)B * n_kv, kMaxBlockUnits);
   if ((long long)B * n_kv * ((long long)MB + 24) > 0x7fffffffLL)
     return fail(PGD_ERR_UNSUPPORTED, "B * n_kv * (MB + 24) >= 2^31");
   return PGD_OK;
@@ -1365,6 +1381,17 @@ pgd_status pgd_kv_read_fp8b(void *k_out, void *v_out, const void *k_cache, const
                          positions, token_starts, B, T, N, n_kv, d, bs, MB, NB, stream);
 }
 
+// Whether an automatic call goes to the cluster kernel instead of the
+// tensor-core one: few units, whose eight CTAs each find a place at once (with
+// more query heads a unit each takes longer), and short contexts.  Device time
+// of the two in us, 16-token blocks: 8 units x 512 tokens, G = 4: 5.2 / 7.0; 8 x
+// 1024: 7.9 / 10.9; 32 x 512, G = 4: 6.8 / 7.3; 32 x 512, G = 8: 9.1 / 8.5; 64 x
+// 256, G = 1: 5.0 / 5.9; 64 x 256, G = 4: 10.4 / 6.5; 64 x 640, G = 1: 7.9 / 7.4.
+static bool cluster_rule(long long units, int G, long long tokens, int32_t num_splits) {
+  return num_splits == 0 && units <= 64 && units * G <= 128 && units * tokens <= 32768 &&
+         tokens <= std::min(g_short_tokens.load(), 1024);
+}
+
 // Attention over the block-scaled cache on checked arguments.
 static pgd_status launch_attention_fp8b(void *out, const void *q, const void *k_cache,
                                         const void *v_cache, const float *k_scales,
@@ -1379,7 +1406,7 @@ static pgd_status launch_attention_fp8b(void *out, const void *q, const void *k_
   if ((s = check_cost_space(B, n_kv, MB)) != PGD_OK) return s;
   PreparedAttention pa;
   s = prepare_attention(out, q, k_cache, v_cache, tables, ctx, B, n_q, n_kv, bs, MB, NB, scale,
-                        num_splits, workspace, workspace_bytes, &pa, true);
+                        num_splits, workspace, workspace_bytes, &pa, true, 1, true);
   if (s != PGD_OK) return s;
   if (append) {
     Kv8bParams ap = *append;
@@ -1394,7 +1421,7 @@ static pgd_status launch_attention_fp8b(void *out, const void *q, const void *k_
   // The append writes only the cache: the attention's prologue overlaps it.
   p.a.wait_late = append ? 1 : 0;
   const cudaError_t e =
-      short_rule(B, n_kv, MB, bs, num_splits, 1)
+      cluster_rule((long long)B * n_kv, pa.G, (long long)MB * bs, num_splits)
           ? cluster_attention_fp8b_launch(p, pa.G, bs, stream)
           : attention_fp8b_launch(p, pa.G, bs, pa.grid, stream);
   if (e != cudaSuccess) return cuda_fail(e, "block-scaled attention launch");
@@ -1594,7 +1621,7 @@ static pgd_status selected_attention(void *out, const void *q, const void *k_cac
   if (B == 0) return ok();
   PreparedAttention pa;  // (checks the workspace; nothing is enqueued)
   s = prepare_attention(out, q, k_cache, v_cache, tiles, tile_tokens, U, G, 1, bs, W, NB * n_kv,
-                        scale, num_splits, workspace, workspace_bytes, &pa, fp8b);
+                        scale, num_splits, workspace, workspace_bytes, &pa, fp8b, 1, true);
   if (s != PGD_OK) return s;
   if (select) {
     select->err = pa.p.err;
@@ -1605,9 +1632,11 @@ static pgd_status selected_attention(void *out, const void *q, const void *k_cac
     s = launch_attention_fp8b(out, q, k_cache, v_cache, k_scales, v_scales, tiles, tile_tokens, U,
                               G, 1, bs, W, NB * n_kv, scale, num_splits, workspace,
                               workspace_bytes, nullptr, stream);
+  else if (short_path(pa, num_splits, W, bs))
+    s = launch_short(pa, nullptr, nullptr, const_cast<void *>(k_cache),
+                     const_cast<void *>(v_cache), stream);
   else
-    s = launch_attention(out, q, k_cache, v_cache, tiles, tile_tokens, U, G, 1, bs, W, NB * n_kv,
-                         scale, num_splits, workspace, workspace_bytes, stream);
+    s = launch_prepared(pa, stream);
   return s == PGD_OK ? ok() : s;
 }
 

@@ -504,7 +504,7 @@ def test_sparse_attention(fp8, G, n_kv, bs, W):
     ref = bsc.selected(c, q, chosen, SCALE)
     bsc.close(got, *ref)
     # the two calls, and a workspace of the documented size
-    ws = pgd.make_workspace(5, n_kv * G, n_kv)
+    ws = pgd.make_block_workspace(5, n_kv * G, n_kv)
     again = pgd.selected_decode_attention(None, q.cuda(), k, v, tiles, tokens, SCALE, k_scales=ks,
                                           v_scales=vs, workspace=ws)
     assert torch.equal(again, got)
@@ -564,7 +564,7 @@ def _serving_state(n_kv=4, G=4, bs=16, W=10):
              out=torch.zeros(3, n_kv * G, 128, dtype=torch.bfloat16, device="cuda"),
              tiles=torch.zeros(3, n_kv, W, dtype=torch.int32, device="cuda"),
              tokens=torch.zeros(3, n_kv, dtype=torch.int32, device="cuda"),
-             ws=pgd.make_workspace(3, n_kv * G, n_kv))
+             ws=pgd.make_block_workspace(3, n_kv * G, n_kv))
     return s
 
 
@@ -644,7 +644,7 @@ def test_two_streams_at_once():
     q = [bsc.make_query(3, 16, seed=i).cuda() for i in range(2)]
     ref = [pgd.paged_decode_attention_fp8b(None, x, s["k"], s["v"], s["ks"], s["vs"], s["tables"],
                                            s["ctx"], SCALE, num_splits=3) for x in q]
-    ws = [pgd.make_workspace(3, 16, 4, 3) for _ in q]
+    ws = [pgd.make_block_workspace(3, 16, 4, 3) for _ in q]
     out = [torch.zeros_like(x) for x in q]
     streams = [torch.cuda.Stream() for _ in q]
     torch.cuda.synchronize()
@@ -655,6 +655,49 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for o, r in zip(out, ref):
         assert torch.equal(o, r)
+
+
+def test_one_workspace_for_calls_of_different_sizes():
+    """Two captured graphs and eager calls of other sizes share a workspace, every call split so
+    that partial states lie in it: each gives what it gives with one of its own."""
+    cases = []
+    for i, (ctx, n_kv, G, bs, fp8) in enumerate([([900, 40], 2, 4, 16, True),
+                                                 ([700] * 9, 8, 8, 32, True),
+                                                 ([1500, 33, 64], 5, 1, 16, False)]):
+        c = bsc.make_cache(ctx, n_kv, bs, fp8=fp8, seed=i)
+        q = bsc.make_query(len(ctx), n_kv * G, seed=i).cuda()
+        k, v, ks, vs, tables, lens = c.cuda()
+        W = 20
+        tiles = torch.zeros(len(ctx), n_kv, W, dtype=torch.int32, device="cuda")
+        tiles += torch.arange(W, device="cuda", dtype=torch.int32)
+        tokens = torch.full((len(ctx), n_kv), W * bs, dtype=torch.int32, device="cuda")
+        k.copy_(torch.where(torch.isnan(k), 0, k) if not fp8 else torch.where(k == 0x7F, 0, k))
+        v.copy_(torch.where(torch.isnan(v), 0, v) if not fp8 else torch.where(v == 0x7F, 0, v))
+
+        def call(ws, q=q, k=k, v=v, ks=ks, vs=vs, tiles=tiles, tokens=tokens, tables=tables,
+                 lens=lens, fp8=fp8):
+            a = pgd.selected_decode_attention(None, q, k, v, tiles, tokens, SCALE, k_scales=ks,
+                                              v_scales=vs, num_splits=5, workspace=ws)
+            if not fp8:
+                return a, a
+            return a, pgd.paged_decode_attention_fp8b(None, q, k, v, ks, vs, tables, lens, SCALE,
+                                                      num_splits=3, workspace=ws)
+
+        cases.append((call, call(None)))
+    ws = pgd.make_block_workspace(9, 64, 8, 5)
+    graphs = []
+    for call, _ in cases[:2]:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got = call(ws)
+        graphs.append((g, got))
+    for _ in range(3):
+        for (g, got), (_, want) in zip(graphs, cases):
+            g.replay()
+            again = cases[2][0](ws)
+            torch.cuda.synchronize()
+            for x, y in zip(got + again, want + cases[2][1]):
+                assert torch.equal(x, y)
 
 
 def test_binding_refuses_shapes_and_devices():
