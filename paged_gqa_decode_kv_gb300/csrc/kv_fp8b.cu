@@ -1,8 +1,8 @@
 // kv_fp8b.cu -- writing tokens into the block-scaled 8-bit cache and reading
 // ranges of it back (layout and scale rule: kv_fp8b.cuh).
 //
-// One warp per (sequence, block, KV head, K or V), holding slots l / 8,
-// l / 8 + 4, ... in lane l.
+// One warp per (sequence, run of blocks, KV head, K or V), block by block,
+// holding slots l / 8, l / 8 + 4, ... in lane l.
 //
 // Write: lane l has dims 8 c .. + 7 and 64 + 8 c .. + 7 (c = l % 8) of its
 // slots, so that every load instruction reads four rows' halves of 128
@@ -32,22 +32,25 @@ namespace {
 
 constexpr int kWarps = 4;
 
-// The item of this warp: sequence, block of the sequence and the slots
-// [s0, s1) of it that the call's tokens fill.  False: nothing to do.
-struct Item {
-  int b, g, is_v;
-  int s0, s1;
-  long long row0;  // packed row of slot s0
-  size_t tile;
+// The tokens of this warp: those of sequence b that fall into blocks j0 ..
+// j0 + n - 1, KV head g, K or V.  n = 0: nothing to do.
+struct Items {
+  int b, g, is_v, n;
+  long long j0;
+  long long p0, p1;   // the sequence's positions [p0, p1)
+  long long row0;     // packed row of position p0
+  int ids;            // lane i: the id of block j0 + i
 };
-__device__ __forceinline__ bool find_item(const Kv8bParams &p, int bs, int JM, Item &it) {
+__device__ __forceinline__ Items find_items(const Kv8bParams &p, int bs, int runs, int run) {
+  Items it;
+  it.n = 0;
   const long long id = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
-  const long long per_b = (long long)JM * 2 * p.n_kv;
-  if (id >= per_b * p.B) return false;
+  const long long per_b = (long long)runs * 2 * p.n_kv;
+  if (id >= per_b * p.B) return it;
   it.b = (int)(id / per_b);
   int r = (int)(id % per_b);
-  const int jrel = r / (2 * p.n_kv);
+  const int jrel = r / (2 * p.n_kv) * run;
   r %= 2 * p.n_kv;
   it.is_v = r / p.n_kv;
   it.g = r % p.n_kv;
@@ -55,25 +58,42 @@ __device__ __forceinline__ bool find_item(const Kv8bParams &p, int bs, int JM, I
   const bool first = jrel == 0 && it.g == 0 && it.is_v == 0 && lane == 0;
   if (t.bad) {
     if (first) atomicOr(p.err, PGD_DEVERR_BAD_POSITION);
-    return false;
+    return it;
   }
-  if (t.count == 0) return false;
-  const long long p0 = (long long)__ldg(p.pos + it.b) + p.pos_offset, p1 = p0 + t.count;
-  if (p0 < 0 || p1 > (long long)p.MB * bs) {
+  if (t.count == 0) return it;
+  it.p0 = (long long)__ldg(p.pos + it.b) + p.pos_offset;
+  it.p1 = it.p0 + t.count;
+  if (it.p0 < 0 || it.p1 > (long long)p.MB * bs) {
     if (first) atomicOr(p.err, PGD_DEVERR_BAD_POSITION);
-    return false;
+    return it;
   }
-  const long long j = p0 / bs + jrel;
-  if (j * bs >= p1) return false;
-  const int blk = __ldg(p.tables + (size_t)it.b * p.MB + j);
+  it.row0 = t.row;
+  it.j0 = it.p0 / bs + jrel;
+  it.n = (int)max(0ll, min((long long)run, (it.p1 + bs - 1) / bs - it.j0));
+  it.ids = lane < it.n ? __ldg(p.tables + (size_t)it.b * p.MB + it.j0 + lane) : 0;
+  return it;
+}
+
+// Block i of the warp's: its tile, the slots [s0, s1) and the packed row of s0.
+// False (and flagged): its id is bad.
+struct Item {
+  int s0, s1;
+  long long row0;
+  size_t tile;
+};
+__device__ __forceinline__ bool find_item(const Kv8bParams &p, int bs, const Items &its, int i,
+                                          Item &it) {
+  const int blk = __shfl_sync(kFullMask, its.ids, i);
   if ((unsigned)blk >= (unsigned)p.NB) {
-    if (it.g == 0 && it.is_v == 0 && lane == 0) atomicOr(p.err, PGD_DEVERR_BAD_BLOCK_ID);
+    if (its.g == 0 && its.is_v == 0 && (threadIdx.x & 31) == 0)
+      atomicOr(p.err, PGD_DEVERR_BAD_BLOCK_ID);
     return false;
   }
-  it.s0 = (int)max(0ll, p0 - j * bs);
-  it.s1 = (int)min((long long)bs, p1 - j * bs);
-  it.row0 = t.row + (j * bs + it.s0 - p0);
-  it.tile = (size_t)blk * p.n_kv + it.g;
+  const long long at = (its.j0 + i) * bs;
+  it.s0 = (int)max(0ll, its.p0 - at);
+  it.s1 = (int)min((long long)bs, its.p1 - at);
+  it.row0 = its.row0 + (at + it.s0 - its.p0);
+  it.tile = (size_t)blk * p.n_kv + its.g;
   return true;
 }
 
@@ -135,18 +155,15 @@ __device__ __forceinline__ uint32_t bf16x2_mul(uint32_t w, __nv_bfloat162 m) {
 }
 
 template <int BS>
-__global__ void __launch_bounds__(kWarps * 32) append_kernel(const Kv8bParams p, int JM) {
+__device__ __forceinline__ void append_tile(const Kv8bParams &p, const Items &its,
+                                            const Item &it) {
   constexpr int NI = BS / 4;
-  pdl_wait();
-  pdl_launch_dependents();
-  Item it;
-  if (!find_item(p, BS, JM, it)) return;
   const int lane = threadIdx.x & 31, c = lane & 7, r = lane >> 3;
   const size_t stride = (size_t)p.n_kv * kHeadDim;  // a packed row's
-  const __nv_bfloat16 *rows = (it.is_v ? p.v_new : p.k_new) +
-                              ((size_t)it.row0 * p.n_kv + it.g) * kHeadDim;  // slot s0's
-  unsigned char *tile = (it.is_v ? p.v_cache : p.k_cache) + it.tile * (size_t)(BS * kHeadDim);
-  float *scale_at = (it.is_v ? p.v_scales : p.k_scales) + it.tile;
+  const __nv_bfloat16 *rows = (its.is_v ? p.v_new : p.k_new) +
+                              ((size_t)it.row0 * p.n_kv + its.g) * kHeadDim;  // slot s0's
+  unsigned char *tile = (its.is_v ? p.v_cache : p.k_cache) + it.tile * (size_t)(BS * kHeadDim);
+  float *scale_at = (its.is_v ? p.v_scales : p.k_scales) + it.tile;
   uint4 x[NI][2];
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
@@ -205,14 +222,10 @@ __global__ void __launch_bounds__(kWarps * 32) append_kernel(const Kv8bParams p,
 }
 
 template <int BS>
-__global__ void __launch_bounds__(kWarps * 32) read_kernel(const Kv8bParams p, int JM) {
+__device__ __forceinline__ void read_tile(const Kv8bParams &p, const Items &its, const Item &it) {
   constexpr int NI = BS / 4;
-  pdl_wait();
-  pdl_launch_dependents();
-  Item it;
-  if (!find_item(p, BS, JM, it)) return;
   const int lane = threadIdx.x & 31, c = lane & 7, r = lane >> 3;
-  const unsigned char *tile = (it.is_v ? p.v_cache : p.k_cache) + it.tile * (size_t)(BS * kHeadDim);
+  const unsigned char *tile = (its.is_v ? p.v_cache : p.k_cache) + it.tile * (size_t)(BS * kHeadDim);
   uint4 x[NI];
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
@@ -221,8 +234,8 @@ __global__ void __launch_bounds__(kWarps * 32) read_kernel(const Kv8bParams p, i
     if (s >= it.s0 && s < it.s1)
       x[i] = __ldg(reinterpret_cast<const uint4 *>(tile + code_offset8b(s, c)));
   }
-  const float scale = __ldg((it.is_v ? p.v_scales : p.k_scales) + it.tile);
-  uint4 *dst = reinterpret_cast<uint4 *>(it.is_v ? p.v_out : p.k_out) + c * 2;
+  const float scale = __ldg((its.is_v ? p.v_scales : p.k_scales) + it.tile);
+  uint4 *dst = reinterpret_cast<uint4 *>(its.is_v ? p.v_out : p.k_out) + c * 2;
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
     const int s = 4 * i + r;
@@ -235,17 +248,40 @@ __global__ void __launch_bounds__(kWarps * 32) read_kernel(const Kv8bParams p, i
       const __nv_bfloat162 z = __floats2bfloat162_rn(y.x * scale, y.y * scale);
       o[k] = *reinterpret_cast<const uint32_t *>(&z);
     }
-    uint4 *row = dst + ((it.row0 + (s - it.s0)) * p.n_kv + it.g) * (kHeadDim / 8);
+    uint4 *row = dst + ((it.row0 + (s - it.s0)) * p.n_kv + its.g) * (kHeadDim / 8);
     row[0] = make_uint4(o[0], o[1], o[2], o[3]);
     row[1] = make_uint4(o[4], o[5], o[6], o[7]);
   }
 }
 
-// Most blocks that T tokens of a sequence can touch, and the launch over them.
+template <int BS, bool WRITE>
+__global__ void __launch_bounds__(kWarps * 32) ranges_kernel(const Kv8bParams p, int runs, int run) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const Items its = find_items(p, BS, runs, run);
+#pragma unroll 1
+  for (int i = 0; i < its.n; ++i) {
+    Item it;
+    if (!find_item(p, BS, its, i, it)) continue;
+    if constexpr (WRITE)
+      append_tile<BS>(p, its, it);
+    else
+      read_tile<BS>(p, its, it);
+  }
+}
+
+// The launch over the most blocks that T tokens of a sequence can touch.  A
+// writing warp takes one block of few (latency), four of many one after
+// another, so that the chain of its first loads (range, position, block ids)
+// is paid once for four tiles (56k tokens: 55.7 us, one by one 58.5).  Reading
+// back is bound by the stores of twice the bytes it loads, and one block a
+// warp spreads those best (16 x 8192 tokens: 130 us, four 137).
 template <typename K>
-cudaError_t launch(K kernel, const Kv8bParams &p, cudaStream_t stream) {
+cudaError_t launch(K kernel, const Kv8bParams &p, bool write, cudaStream_t stream) {
   const int JM = 1 + (p.T - 1 + p.bs - 1) / p.bs;
-  const long long items = (long long)p.B * JM * p.n_kv * 2;
+  const int run = write && (long long)p.B * JM * p.n_kv * 2 > 16384 ? 4 : 1,
+            runs = (JM + run - 1) / run;
+  const long long items = (long long)p.B * runs * p.n_kv * 2;
   const long long grid = (items + kWarps - 1) / kWarps;
   if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
@@ -257,19 +293,21 @@ cudaError_t launch(K kernel, const Kv8bParams &p, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p, JM);
+  return cudaLaunchKernelEx(&cfg, kernel, p, runs, run);
 }
 
 }  // namespace
 
 cudaError_t kv_append_fp8b_launch(const Kv8bParams &p, cudaStream_t stream) {
   if (p.B == 0 || p.T == 0) return cudaSuccess;
-  return p.bs == 16 ? launch(append_kernel<16>, p, stream) : launch(append_kernel<32>, p, stream);
+  return p.bs == 16 ? launch(ranges_kernel<16, true>, p, true, stream)
+                    : launch(ranges_kernel<32, true>, p, true, stream);
 }
 
 cudaError_t kv_read_fp8b_launch(const Kv8bParams &p, cudaStream_t stream) {
   if (p.B == 0 || p.T == 0) return cudaSuccess;
-  return p.bs == 16 ? launch(read_kernel<16>, p, stream) : launch(read_kernel<32>, p, stream);
+  return p.bs == 16 ? launch(ranges_kernel<16, false>, p, false, stream)
+                    : launch(ranges_kernel<32, false>, p, false, stream);
 }
 
 }  // namespace pgd

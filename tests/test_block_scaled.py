@@ -135,6 +135,7 @@ def _attend(L, append=False, **kw):
     (dict(k=24), _native.ERR_INVALID_ARG), (dict(splits=-1), _native.ERR_INVALID_ARG),
     (dict(ks=None), _native.ERR_INVALID_ARG), (dict(vs=2), _native.ERR_INVALID_ARG),
     (dict(B=2048, n_kv=8, MB=(1 << 17) - 23), _native.ERR_UNSUPPORTED),
+    (dict(B=2048, n_kv=40, n_q=40), _native.ERR_UNSUPPORTED),
     (dict(ws=None), _native.ERR_WORKSPACE), (dict(ws=256, wsb=16), _native.ERR_WORKSPACE),
     (dict(ws=264, wsb=1 << 30), _native.ERR_WORKSPACE),
 ], ids=lambda x: str(x))
@@ -146,6 +147,14 @@ def test_attention_refuses(L, append, kw, status):
     (dict(kn=None), _native.ERR_INVALID_ARG), (dict(vn=8), _native.ERR_INVALID_ARG)], ids=str)
 def test_append_attention_refuses_its_rows(L, kw, status):
     assert _attend(L, True, **kw) == status
+
+
+def test_workspace_size(L):
+    """Grows with the batch from one counter region for all sizes; 0 where no call would do."""
+    size = pgd.block_workspace_size
+    assert 65536 * 4 < size(1, 8, 8) <= size(4, 32, 8) <= size(64, 32, 8)
+    assert size(64, 32, 8, 4) - size(64, 32, 8, 2) == 2 * 64 * 8 * 4 * (128 + 2) * 4
+    assert size(2048, 2048 * 40, 40) == size(3, 7, 2) == size(2, 8, 2, d=64) == 0
 
 
 def test_attention_of_nothing(L):

@@ -48,8 +48,10 @@ RANGES = [
 
 
 @pytest.mark.parametrize("ranges", RANGES, ids=str)
-@pytest.mark.parametrize("n_kv,bs", [(1, 16), (3, 32), (8, 16)])
-def test_append_ranges(ranges, n_kv, bs):
+@pytest.mark.parametrize("n_kv,bs,more", [(1, 16, 0), (3, 32, 0), (8, 16, 0), (2, 16, 1 << 17),
+                                          (4, 32, 1 << 17)])
+def test_append_ranges(ranges, n_kv, bs, more):
+    """`more`: max_tokens far above the ranges (warps then take runs of blocks)."""
     past, lens = [p for p, _ in ranges], [n for _, n in ranges]
     c = bsc.make_cache(past, n_kv, bs, seed=sum(lens) + bs, room=max(lens) + 1)
     st = _starts(lens)
@@ -60,7 +62,7 @@ def test_append_ranges(ranges, n_kv, bs):
         vn[-1] *= 1000
     k, v, ks, vs, tables, _ = c.cuda()
     pgd.kv_append_fp8b(kn.cuda(), vn.cuda(), k, v, ks, vs, tables, _i32(past),
-                       token_starts=_i32(st), max_tokens=max(lens))
+                       token_starts=_i32(st), max_tokens=max(lens) + more)
     bsc.append(c, kn, vn, past, st)
     _same_pools(c, k, v, ks, vs)
 
@@ -128,8 +130,8 @@ def test_append_keeps_scales_that_are_no_powers_of_two():
 
 
 @pytest.mark.parametrize("ranges", RANGES, ids=str)
-@pytest.mark.parametrize("n_kv,bs", [(1, 16), (3, 32), (8, 16)])
-def test_read_ranges(ranges, n_kv, bs):
+@pytest.mark.parametrize("n_kv,bs,more", [(1, 16, 0), (3, 32, 0), (8, 16, 0), (2, 16, 1 << 17)])
+def test_read_ranges(ranges, n_kv, bs, more):
     """Every row bit for bit; rows that belong to no sequence stay as they were."""
     past, lens = [p for p, _ in ranges], [n for _, n in ranges]
     c = bsc.make_cache([p + n for p, n in ranges], n_kv, bs, seed=bs)
@@ -138,7 +140,7 @@ def test_read_ranges(ranges, n_kv, bs):
            for _ in range(2)]
     k, v, ks, vs, tables, _ = c.cuda()
     pgd.kv_read_fp8b(*out, k, v, ks, vs, tables, _i32(past), token_starts=_i32(st),
-                     max_tokens=max(lens))
+                     max_tokens=max(lens) + more)
     for which, got in zip("kv", out):
         want = np.full((st[-1] + 3, n_kv, 128), 7.0)
         for b, (p, n) in enumerate(ranges):
