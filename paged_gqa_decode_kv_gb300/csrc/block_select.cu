@@ -200,7 +200,8 @@ cudaError_t launch_pdl(K kernel, dim3 grid, int threads, size_t smem, cudaStream
 }
 
 // ------------------------------------------------------------------ selection
-constexpr int kSelThreads = 512;
+// (two CTAs an SM: 256 heads of 256 blocks take 8.5 us, with 512 threads 15.0)
+constexpr int kSelThreads = 256;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kSliceKeys = 6144;   // keys of a CTA's slice at most (24 KiB)
@@ -347,57 +348,68 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
   }
   __syncthreads();
   {
-    // B fragments of all 16 k-steps (piece c, word w): head l / 4, the four
-    // dims of bytes 64 c + 16 t + 4 w of a block's bounds; the lower bounds
-    // (c < 2) take the query's negative part, the upper its positive part.
+    // B fragments: head l / 4, the query's dims that meet bytes 64 c + 16 t +
+    // 4 w of a block's bounds; the lower bounds (c < 2) take the negative part,
+    // the upper the positive part.
     const int r = lane >> 2, t = lane & 3;
-    uint32_t bq[4][4][2];
-    const __half2 zero = __float2half2_rn(0.f);
+    uint32_t bq[2][4][2];
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
+    for (int c = 0; c < 2; ++c)
 #pragma unroll
       for (int w = 0; w < 4; ++w)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint32_t x = qh[r][((c & 1) * 64 + 16 * t + 4 * w) / 2 + i];
-          const __half2 h = *reinterpret_cast<const __half2 *>(&x);
-          const __half2 y = c < 2 ? __hmin2(h, zero) : __hmax2(h, zero);
-          bq[c][w][i] = *reinterpret_cast<const uint32_t *>(&y);
-        }
+        for (int i = 0; i < 2; ++i) bq[c][w][i] = qh[r][(c * 64 + 16 * t + 4 * w) / 2 + i];
+    auto part = [](uint32_t x, bool upper) {
+      const __half2 h = *reinterpret_cast<const __half2 *>(&x), zero = __float2half2_rn(0.f);
+      const __half2 y = upper ? __hmax2(h, zero) : __hmin2(h, zero);
+      return *reinterpret_cast<const uint32_t *>(&y);
+    };
     const float f0 = qf[2 * t], f1 = qf[2 * t + 1];
     const float b0 = qbias[2 * t], b1 = qbias[2 * t + 1];
     uint32_t kmin = 0xffffffffu, kmax = 0;
-    for (int i0 = warp * 16; i0 < n; i0 += kSelWarps * 16) {
+    // 16 blocks' bounds and scales; the next ones are loaded before the last
+    // ones are used
+    struct Rows {
       uint4 x[2][4];
       float s[2];
       bool there[2];
+    };
+    auto load = [&](int i0, Rows &v) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int i = i0 + r + 8 * h;
         const uint32_t blk = i < n ? keys[i] : 0xffffffffu;
-        there[h] = blk < (uint32_t)p.NB;
-        s[h] = 0.f;
+        v.there[h] = blk < (uint32_t)p.NB;
+        v.s[h] = 0.f;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) x[h][c] = make_uint4(0, 0, 0, 0);
-        if (there[h]) {
+        for (int c = 0; c < 4; ++c) v.x[h][c] = make_uint4(0, 0, 0, 0);
+        if (v.there[h]) {
           const size_t tile = (size_t)blk * p.n_kv + g;
           const uint4 *src = reinterpret_cast<const uint4 *>(p.bounds + tile * (2 * kHeadDim)) + t;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) x[h][c] = __ldg(src + 4 * c);
-          s[h] = __ldg(p.bound_scales + tile);
+          for (int c = 0; c < 4; ++c) v.x[h][c] = __ldg(src + 4 * c);
+          v.s[h] = __ldg(p.bound_scales + tile);
         }
       }
+    };
+    constexpr int kStep = kSelWarps * 16;
+    Rows v, next;
+    load(warp * 16, next);
+#pragma unroll 1
+    for (int i0 = warp * 16; i0 < n; i0 += kStep) {
+      v = next;
+      load(i0 + kStep, next);
       float d[4] = {b0, b1, b0, b1};
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        const uint32_t u[2][4] = {{x[0][c].x, x[0][c].y, x[0][c].z, x[0][c].w},
-                                  {x[1][c].x, x[1][c].y, x[1][c].z, x[1][c].w}};
+        const uint32_t u[2][4] = {{v.x[0][c].x, v.x[0][c].y, v.x[0][c].z, v.x[0][c].w},
+                                  {v.x[1][c].x, v.x[1][c].y, v.x[1][c].z, v.x[1][c].w}};
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
           const uint32_t y0 = u[0][w] ^ 0x80808080u, y1 = u[1][w] ^ 0x80808080u;
           mma16816(d, __byte_perm(y0, 0, 0x4140), __byte_perm(y1, 0, 0x4140),
-                   __byte_perm(y0, 0, 0x4342), __byte_perm(y1, 0, 0x4342), bq[c][w][0],
-                   bq[c][w][1]);
+                   __byte_perm(y0, 0, 0x4342), __byte_perm(y1, 0, 0x4342),
+                   part(bq[c & 1][w][0], c >= 2), part(bq[c & 1][w][1], c >= 2));
         }
       }
 #pragma unroll
@@ -410,7 +422,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
         const int i = i0 + r + 8 * h, j = jlo + i;
         if (i < n && t == 0) {
           const bool forced = j < p.keep_first || j >= nblk - p.keep_last;
-          const uint32_t key = forced ? 0xffffffffu : there[h] ? order_key(best * s[h]) : 0u;
+          const uint32_t key = forced ? 0xffffffffu : v.there[h] ? order_key(best * v.s[h]) : 0u;
           if (!forced) {
             kmin = min(kmin, key);
             kmax = max(kmax, key);
