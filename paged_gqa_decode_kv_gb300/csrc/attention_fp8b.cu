@@ -142,23 +142,14 @@ __device__ __forceinline__ void arrive_after_copies(uint64_t *bar) {
                : "memory");
 }
 
-// The CTAs' parts of the cost space: Schedule and SegCursor of
-// attention_kernel.cuh in 32 bits (the host refuses calls whose cost space
-// does not fit).
+// The CTAs' parts of the cost space of attention_kernel.cuh, in 32 bits (the
+// host refuses calls whose cost space does not fit): whole units, or parts of
+// one size.
 struct Cuts {
-  int X, P;        // cost of all units, parts
-  int q, r;        // X / P, X % P
+  int X, P, S;     // cost of all units, parts, cost of a part (but the last)
   bool units;      // part c = unit c
   const int *pre;  // cost of one head of the sequences before b
   int n_kv, ov;
-  __device__ __forceinline__ int cut(int i) const {  // X * i / P
-    return q * i + (P <= 65535 ? (int)(((unsigned)r * (unsigned)i) / (unsigned)P)
-                               : (int)(((unsigned long long)r * (unsigned)i) / (unsigned)P));
-  }
-  // the part that holds cost position x (for units that are cut)
-  __device__ __forceinline__ int part_of(int x) const {
-    return (int)(((unsigned long long)P * ((unsigned)x + 1u) - 1u) / (unsigned)X);
-  }
 };
 
 struct Piece {  // blocks j0 .. j0 + n - 1 of the nblk of unit (b, g), at cost [ucs, uce)
@@ -168,16 +159,11 @@ struct Piece {  // blocks j0 .. j0 + n - 1 of the nblk of unit (b, g), at cost [
 struct Walk {
   int x, end, b, g;
 };
-__device__ __forceinline__ void walk_start(Cuts &sc, Walk &w) {
-  w.x = w.end = 0;
+__device__ __forceinline__ void walk_start(const Cuts &sc, Walk &w) {
   w.b = -1;
   w.g = 0;
-  const int c = (int)blockIdx.x;
-  if (c >= sc.P) return;
-  sc.q = sc.X / sc.P;
-  sc.r = sc.X - sc.q * sc.P;
-  w.x = sc.cut(c);
-  w.end = sc.cut(c + 1);
+  w.x = (int)min((long long)sc.X, (long long)blockIdx.x * sc.S);
+  w.end = (int)min((long long)sc.X, (long long)w.x + sc.S);
 }
 // Part c of a split into whole units: unit c, if it has blocks.
 __device__ __forceinline__ bool whole_unit(const Cuts &sc, Piece &sg) {
@@ -616,6 +602,7 @@ attention_fp8b_kernel(const __grid_constant__ Params pr) {
   if (sc.units) {
     have = whole_unit(sc, sg);
   } else {
+    sc.S = sc.P > 0 ? (sc.X + sc.P - 1) / sc.P : 1;
     walk_start(sc, walk);
     have = walk_next(pre, sc.n_kv, sc.ov, p.B, walk, sg);
   }
@@ -949,8 +936,8 @@ attention_fp8b_kernel(const __grid_constant__ Params pr) {
       if (lane == 0) mbar_arrive(&o_free[ob]);
 
       const bool whole = sg.j0 == 0 && sg.n == sg.nblk;
-      const int c_first = sc.units ? part : sc.part_of(sg.ucs + sc.ov);
-      const int c_last = sc.units ? part : sc.part_of(sg.uce - 1);
+      const int c_first = sc.units ? part : (sg.ucs + sc.ov) / sc.S;
+      const int c_last = sc.units ? part : (sg.uce - 1) / sc.S;
       const size_t obase = q_index(p, sg.b, sg.g, 0);
       if (whole) {
 #pragma unroll

@@ -204,6 +204,9 @@ cudaError_t launch_pdl(K kernel, dim3 grid, int threads, size_t smem, cudaStream
 constexpr int kSelThreads = 256;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kMaxCluster = 8;
+constexpr int kSMs = 152;          // of a GB300
+// Dynamic shared memory that leaves an SM room for one CTA.
+constexpr size_t kAloneBytes = 120 * 1024;
 constexpr int kSliceKeys = 6144;   // keys of a CTA's slice at most (24 KiB)
 constexpr int kBins = 256;
 
@@ -586,39 +589,54 @@ int select_max_blocks() { return kMaxCluster * kSliceKeys; }
 // leave each 128 blocks (fewer are not worth the cluster barriers), and at
 // least as many as hold the keys.  At most 8: clusters of 16 do not all find
 // their place at once (8 heads of 8192 blocks took 29.8 us in clusters of 16,
-// 16.5 in 8, 21.5 in 4, 34.5 in 2).
+// 16.5 in 8, 21.5 in 4, 34.5 in 2, in an earlier form of this kernel).
 static int select_cluster(int units, int MB) {
   int C = 1;
-  while (C < kMaxCluster && units * C * 2 <= 152 && MB >= C * 2 * 128) C *= 2;
+  while (C < kMaxCluster && units * C * 2 <= kSMs && MB >= C * 2 * 128) C *= 2;
   while (MB > C * kSliceKeys) C *= 2;
   return C;
 }
 
+template <int G>
+static cudaError_t launch_select(const SelectParams &p, cudaStream_t stream) {
+  static volatile int done[64] = {0};  // shared-memory limit raised, per device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64 || !done[dev]) {
+    e = cudaFuncSetAttribute(select_kernel<G>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)kAloneBytes);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) done[dev] = 1;
+  }
+  const int units = p.B * p.n_kv, C = select_cluster(units, p.MB);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(units * C));
+  cfg.blockDim = dim3(kSelThreads);
+  // With no more CTAs than SMs each gets an SM to itself: behind an attention
+  // call, whose CTAs leave one by one, two would crowd the first SMs to be free
+  // (a sparse step of one 131072-token context: 31.5 us crowded, 27.3 apart).
+  cfg.dynamicSmemBytes = units * C <= kSMs ? kAloneBytes : (size_t)((p.MB + C - 1) / C) * 4;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)C;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, select_kernel<G>, p, C);
+}
+
 cudaError_t select_blocks_launch(const SelectParams &p, int G, cudaStream_t stream) {
   if (p.B == 0) return cudaSuccess;
-  const int units = p.B * p.n_kv, C = select_cluster(units, p.MB);
-  auto go = [&](auto kernel) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(units * C));
-    cfg.blockDim = dim3(kSelThreads);
-    cfg.dynamicSmemBytes = (size_t)((p.MB + C - 1) / C) * 4;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = (unsigned)C;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kernel, p, C);
-  };
   switch (G) {
-    case 1: return go(select_kernel<1>);
-    case 2: return go(select_kernel<2>);
-    case 4: return go(select_kernel<4>);
-    case 8: return go(select_kernel<8>);
+    case 1: return launch_select<1>(p, stream);
+    case 2: return launch_select<2>(p, stream);
+    case 4: return launch_select<4>(p, stream);
+    case 8: return launch_select<8>(p, stream);
   }
   return cudaErrorInvalidValue;
 }
