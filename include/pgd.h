@@ -558,7 +558,9 @@ pgd_status pgd_append_decode_attention_fp8b(
  * context_lens[b], from the cache as it stands (after the append): k_cache is
  * a block-scaled pool with k_scales, or a bf16 pool with k_scales NULL.  T: at
  * least the largest context_lens[b] - positions[b]; equal ones are a no-op.
- * Keys must be finite.  PGD_DEVERR_BAD_CONTEXT for a context outside
+ * Keys must be finite.  A block that several sequences hold has one pair of
+ * bounds: update it through the sequence that holds most of its tokens.
+ * PGD_DEVERR_BAD_CONTEXT for a context outside
  * [0, MB*bs], PGD_DEVERR_BAD_POSITION for positions[b] outside [0,
  * context_lens[b]] or a range of over T tokens; neither writes anything.
  *

@@ -1293,7 +1293,7 @@ static pgd_status check_ranges(int32_t B, int32_t T, int32_t n_kv, int32_t d, in
   if (s != PGD_OK) return s;
   if ((long long)NB * n_kv > 0x7fffffffLL)
     return fail(PGD_ERR_INVALID_ARG, "NB * n_kv = %lld overflows int32", (long long)NB * n_kv);
-  if ((long long)B * (1 + ((long long)T + bs - 1) / bs) * n_kv > 0x7fffffffLL)
+  if ((long long)B * most_blocks(std::max(T, 1), bs, MB) * n_kv > 0x7fffffffLL)
     return fail(PGD_ERR_INVALID_ARG, "B * T * n_kv too large");
   return PGD_OK;
 }

@@ -568,7 +568,7 @@ cudaError_t block_bounds_launch(const BoundsParams &p, cudaStream_t stream) {
   // Blocks a warp takes one after another: one for a few (latency), four for
   // many, so that the chain of a warp's first loads (lengths, then block ids)
   // is paid once for four tiles.
-  const int JM = 1 + (p.T - 1 + p.bs - 1) / p.bs;
+  const int JM = most_blocks(p.T, p.bs, p.MB);
   const int run = (long long)p.B * JM * p.n_kv > 16384 ? 4 : 1, runs = (JM + run - 1) / run;
   const long long items = (long long)p.B * runs * p.n_kv;
   const long long grid = (items + kBoundWarps - 1) / kBoundWarps;

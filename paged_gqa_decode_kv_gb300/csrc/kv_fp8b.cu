@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(kWarps * 32) ranges_kernel(const Kv8bParams p,
 // warp spreads those best (16 x 8192 tokens: 130 us, four 137).
 template <typename K>
 cudaError_t launch(K kernel, const Kv8bParams &p, bool write, cudaStream_t stream) {
-  const int JM = 1 + (p.T - 1 + p.bs - 1) / p.bs;
+  const int JM = most_blocks(p.T, p.bs, p.MB);
   const int run = write && (long long)p.B * JM * p.n_kv * 2 > 16384 ? 4 : 1,
             runs = (JM + run - 1) / run;
   const long long items = (long long)p.B * runs * p.n_kv * 2;

@@ -78,6 +78,12 @@ __device__ __forceinline__ TokenRange token_range(const int32_t *starts, int b, 
   return r;
 }
 
+// The most blocks of a table row (MB of them) that T > 0 tokens in a row touch.
+inline int most_blocks(int T, int bs, int MB) {
+  const long long n = 1 + ((long long)T - 1 + bs - 1) / bs;
+  return n < MB ? (int)n : MB;
+}
+
 // Write and read-back of ranges of positions (kv_fp8b.cu).
 struct Kv8bParams {
   const __nv_bfloat16 *k_new, *v_new;  // packed rows [N][n_kv][D] (write)

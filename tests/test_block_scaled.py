@@ -94,7 +94,7 @@ RANGE_REFUSALS = [
     (dict(B=-1), _native.ERR_INVALID_ARG), (dict(T=-1), _native.ERR_INVALID_ARG),
     (dict(N=-1), _native.ERR_INVALID_ARG), (dict(st=None, N=7), _native.ERR_INVALID_ARG),
     (dict(n_kv=0), _native.ERR_INVALID_ARG), (dict(NB=1 << 30, n_kv=4), _native.ERR_INVALID_ARG),
-    (dict(B=1 << 20, T=1 << 20), _native.ERR_INVALID_ARG),
+    (dict(B=1 << 20, T=1 << 20, MB=1 << 20), _native.ERR_INVALID_ARG),
     (dict(k=None), _native.ERR_INVALID_ARG), (dict(v=24), _native.ERR_INVALID_ARG),
     (dict(kc=8), _native.ERR_INVALID_ARG), (dict(vc=None), _native.ERR_INVALID_ARG),
     (dict(ks=None), _native.ERR_INVALID_ARG), (dict(vs=18), _native.ERR_INVALID_ARG),

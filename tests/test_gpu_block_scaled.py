@@ -67,6 +67,26 @@ def test_append_ranges(ranges, n_kv, bs, more):
     _same_pools(c, k, v, ks, vs)
 
 
+def test_any_max_tokens():
+    """max_tokens is a bound: the largest number does."""
+    c = bsc.make_cache([20, 3], 2, 16, seed=5, room=30)
+    kn, vn = _rows(31, 2, 1), _rows(31, 2, 2)
+    k, v, ks, vs, tables, lens = c.cuda()
+    st, most = [0, 30, 31], (1 << 31) - 1
+    pgd.kv_append_fp8b(kn.cuda(), vn.cuda(), k, v, ks, vs, tables, lens, token_starts=_i32(st),
+                       max_tokens=most)
+    bsc.append(c, kn, vn, [20, 3], st)
+    _same_pools(c, k, v, ks, vs)
+    out = [torch.zeros_like(kn, device="cuda") for _ in range(2)]
+    pgd.kv_read_fp8b(*out, k, v, ks, vs, tables, lens, token_starts=_i32(st), max_tokens=most)
+    assert np.array_equal(bsc.f64(out[0][:30]), c.rows("k", 0, 50)[20:])
+    bounds, scales = _empty_bounds(c)
+    want, ws = _want_bounds(c, bounds.cpu(), scales.cpu(), [(0, j, 50) for j in range(4)] +
+                            [(1, 0, 4)])
+    pgd.block_bounds(bounds, scales, k, tables, _i32([50, 4]), max_tokens=most, k_scales=ks)
+    assert torch.equal(bounds.cpu(), want) and torch.equal(scales.cpu(), ws)
+
+
 def test_append_one_token_each_without_starts():
     past = [0, 4, 15, 16, 33]
     c = bsc.make_cache(past, 4, 16, seed=9, room=1)
@@ -340,6 +360,28 @@ def test_attention_flags_contexts_and_ids():
     pgd.paged_decode_attention_fp8b(None, q, k, v, ks, vs, c.tables.cuda(),
                                     _i32([40, 65, 40, 40]), SCALE)
     assert pgd.device_errors(clear=True) == _native.DEVERR_BAD_CONTEXT
+
+
+@pytest.mark.parametrize("num_splits", [0, 3])
+@pytest.mark.parametrize("bs", [16, 32])
+def test_attention_timeout_then_normal_call(num_splits, bs):
+    """The kernel's timeout exit, made to happen by a wait limit of 1 ns: the call returns and
+    reports it, and the next one on the same workspace is right."""
+    ctx = [3000, 17, 900, 2048, 1, 5000, 64, 333, 1200, 4096, 700, 16]
+    c = bsc.make_cache(ctx, 2, bs, seed=31)
+    q = bsc.make_query(12, 8)
+    k, v, ks, vs, tables, lens = c.cuda()
+    ws = pgd.make_block_workspace(12, 8, 2, num_splits)
+    call = lambda: pgd.paged_decode_attention_fp8b(None, q.cuda(), k, v, ks, vs, tables, lens,
+                                                   SCALE, num_splits=num_splits, workspace=ws)
+    try:
+        pgd.set_wait_limit_ns(1)
+        call()
+        torch.cuda.synchronize()
+        assert pgd.device_errors(clear=True) & _native.DEVERR_TIMEOUT
+    finally:
+        pgd.set_wait_limit_ns(0)
+    bsc.close(call(), *bsc.paged(c, q, SCALE))
 
 
 # ------------------------------------------------------------------- bounds and selection
