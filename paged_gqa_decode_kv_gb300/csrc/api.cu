@@ -1389,7 +1389,7 @@ pgd_status pgd_kv_read_fp8b(void *k_out, void *v_out, const void *k_cache, const
 // 256, G = 1: 5.0 / 5.9; 64 x 256, G = 4: 10.4 / 6.5; 64 x 640, G = 1: 7.9 / 7.4.
 static bool cluster_rule(long long units, int G, long long tokens, int32_t num_splits) {
   return num_splits == 0 && units <= 64 && units * G <= 128 && units * tokens <= 32768 &&
-         tokens <= std::min(g_short_tokens.load(), 1024);
+         tokens <= std::min(g_short_tokens.load(), cluster_max_tokens());
 }
 
 // Attention over the block-scaled cache on checked arguments.

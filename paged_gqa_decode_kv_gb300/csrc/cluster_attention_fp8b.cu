@@ -1,14 +1,24 @@
 // cluster_attention_fp8b.cu -- decode attention over the block-scaled 8-bit
-// cache on the CUDA cores, one cluster of 8 CTAs per (sequence, KV head).
+// cache for short contexts, on the CUDA cores: one cluster of 8 CTAs per
+// (sequence, KV head).
 //
-//   out[b][h] = sum_t softmax_t(scale * q[b][h] . k_t) v_t,  t < ctx[b],
+//   out[b][h] = sum_t softmax_t(scale * q[b][h] . k_t) v_t,  t < ctx[b] <= 1024,
 //   k_t = sk[tile] * E4M3(code), v_t = sv[tile] * E4M3(code)
 //
-// CTA r of a cluster takes the contiguous tokens [r ctx / 8, (r + 1) ctx / 8)
-// in pieces of 64: two threads per token for q.k (64 dims each), an online
-// softmax over the pieces (fp32, exact exp2), one thread per output dim for
-// p.v from codes staged in shared memory.  The eight (max, sum, output)
-// states are merged by log-sum-exp through distributed shared memory.
+// Such a call is bound by a chain of latencies, so the chain is short:
+// - the context length, the table row (at most 64 blocks) and the query are
+//   loaded side by side; then K and V codes and scales, all in flight together;
+// - CTA r of a cluster takes the contiguous tokens [r ctx / 8, (r + 1) ctx / 8),
+//   at most 128, in one piece: two threads a token for q.k (64 dims each), one
+//   maximum and one sum per head; p.v with two dims a thread and every fourth
+//   token, V's scale folded into the probability; fp32, exact exp2;
+// - every CTA stores its maxima, sums and output dims into the shared memory of
+//   the CTAs that write them, and after one cluster barrier CTA r merges the
+//   eight states of dims [16 r, 16 r + 16) by log-sum-exp from its own memory
+//   (reading the peers' states instead takes a second barrier, before a CTA
+//   may exit, and the latency of the remote loads).
+// 8 heads x 512 tokens, G = 4: 4.2 us (5.1 in pieces of 64 tokens, with a table
+// load behind the length and remote loads).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -17,194 +27,203 @@
 namespace pgd {
 namespace cl8b {
 
-constexpr int CL = 8;         // CTAs per (sequence, KV head): one cluster
-constexpr int CH = 64;        // tokens per piece
-constexpr int THREADS = 128;  // = the head dim
+constexpr int CL = 8;          // CTAs per (sequence, KV head): one cluster
+constexpr int THREADS = 256;
+constexpr int CH = 128;        // tokens of a CTA at most
+constexpr int MAX_TOKENS = CL * CH;
+constexpr int MAXB = 64;       // blocks of a sequence (16 tokens each) at most
+constexpr int NTG = 4;         // token groups of p.v
 
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
-               "barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// A load from CTA `rank`'s shared memory at the offset `local` has in ours.
-__device__ __forceinline__ float ld_peer(const float *local, uint32_t rank) {
+// Store into CTA `rank`'s shared memory at the place `local` has in ours.
+__device__ __forceinline__ void st_peer(float *local, uint32_t rank, float v) {
   uint32_t remote;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_addr(local)), "r"(rank));
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(remote) : "memory");
-  return v;
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(remote), "f"(v) : "memory");
 }
 
 template <int G, int BS>
 __global__ void __launch_bounds__(THREADS) cluster_attention_kernel(const Attn8bParams pp) {
   const AttnParams &p = pp.a;
   constexpr size_t TILE = (size_t)BS * kHeadDim;
-  __shared__ __align__(16) float qs[G][kHeadDim];
-  __shared__ __align__(16) unsigned char vs[CH][kHeadDim];  // V codes of a piece
+  constexpr int NW = THREADS / 32;
+  // (two halves, 4 banks apart: a warp reads the same dims of both at once)
+  __shared__ __align__(16) float qs[G][2][kHeadDim / 2 + 4];
+  __shared__ __align__(16) unsigned char vs[CH][kHeadDim];  // V codes
   __shared__ float vsc[CH];                                 // their scales (0: no weight)
-  __shared__ __align__(16) float ps[CH][G];                 // probabilities
-  __shared__ float red[4][G];
-  __shared__ float st_m[G], st_l[G], st_o[G][kHeadDim];
+  __shared__ __align__(16) float ps[CH][G];                 // probability times V's scale
+  __shared__ float red[2][NW][G];                           // per-warp maxima, sums
+  __shared__ int tbl[MAXB];
+  __shared__ float po[NTG][G][kHeadDim];                    // outputs of the token groups
+  __shared__ float in_m[CL][G], in_l[CL][G], in_o[CL][G][kHeadDim / CL];  // written by the peers
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t rank = cluster_rank();
   const int unit = (int)blockIdx.x / CL;
   const int b = unit / p.n_kv, g = unit % p.n_kv;
+  // (every CTA of the cluster has started: waited for before the first store
+  // into another's shared memory)
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   pdl_wait();
   pdl_launch_dependents();
   const int ctx = __ldg(p.ctx + b);
-  const uint4 *qsrc = reinterpret_cast<const uint4 *>(p.q + ((size_t)b * p.n_q + g * G) * kHeadDim);
-  for (int i = tid; i < G * 16; i += THREADS) {
-    float f[8];
-    unpack8(__ldg(qsrc + i), f);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) qs[i / 16][(i % 16) * 8 + e] = f[e];
-  }
   const int32_t *trow = p.tables + (size_t)b * p.MB;
+  if (tid < p.MB && tid < MAXB) tbl[tid] = __ldg(trow + tid);
+  const uint4 *qsrc = reinterpret_cast<const uint4 *>(p.q + ((size_t)b * p.n_q + g * G) * kHeadDim);
+  if (tid < G * 16) {
+    float f[8];
+    unpack8(__ldg(qsrc + tid), f);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) qs[tid / 16][(tid % 16) / 8][(tid % 8) * 8 + e] = f[e];
+  }
   const bool ctx_ok = ctx >= 1 && ctx <= p.MB * BS;
   if (!ctx_ok && tid == 0 && rank == 0 && g == 0) atomicOr(p.err, PGD_DEVERR_BAD_CONTEXT);
   const int n = ctx_ok ? ctx : 0;
-  const int t_lo = (int)((long long)n * rank / CL), t_hi = (int)((long long)n * (rank + 1) / CL);
+  const int t_lo = n * (int)rank / CL, nt = n * ((int)rank + 1) / CL - t_lo;
   __syncthreads();
 
+  // K of token j (64 dims); V row 32 k + tid / 8, chunk tid % 8
   const int j = tid >> 1, hf = tid & 1;
-  float m_run[G], l_run[G], o_acc[G];
+  uint4 kr[4], vr[4];
+  float ksc = 0.f, vscl = 0.f;
+  const int kblk = j < nt ? tbl[(t_lo + j) / BS] : -1;
+  const bool kval = (unsigned)kblk < (unsigned)p.NB;
+  if (j < nt && !kval) atomicOr(p.err, PGD_DEVERR_BAD_BLOCK_ID);
 #pragma unroll
-  for (int h = 0; h < G; ++h) { m_run[h] = -INFINITY; l_run[h] = 0.f; o_acc[h] = 0.f; }
-  bool bad = false;
-  for (int tb = t_lo; tb < t_hi; tb += CH) {
-    const int nt = min(CH, t_hi - tb);
-    // K of token tb + j (this thread's 64 dims), V row 16 k + tid / 8, chunk tid % 8
-    uint4 kr[4], vr[4];
-    float ksc = 0.f, vscl = 0.f;
-    const int t = tb + j;
-    const int kblk = j < nt ? __ldg(trow + t / BS) : -1;
-    const bool kval = (unsigned)kblk < (unsigned)p.NB;
-    if (j < nt && !kval) bad = true;
+  for (int k = 0; k < 4; ++k) kr[k] = make_uint4(0, 0, 0, 0);
+  if (kval) {
+    const size_t tile = (size_t)kblk * p.n_kv + g;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) kr[k] = make_uint4(0, 0, 0, 0);
-    if (kval) {
-      const size_t tile = (size_t)kblk * p.n_kv + g;
+    for (int k = 0; k < 4; ++k)
+      kr[k] = __ldg(reinterpret_cast<const uint4 *>(
+          p.k_cache + tile * TILE + code_offset8b((t_lo + j) % BS, 4 * hf + k)));
+    ksc = __ldg(pp.k_scales + tile);
+    if (hf == 0) vscl = __ldg(pp.v_scales + tile);
+  }
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        kr[k] = __ldg(reinterpret_cast<const uint4 *>(p.k_cache + tile * TILE +
-                                                      code_offset8b(t % BS, 4 * hf + k)));
-      ksc = __ldg(pp.k_scales + tile);
+  for (int k = 0; k < 4; ++k) {
+    const int jj = 32 * k + (tid >> 3), tv = t_lo + jj;
+    vr[k] = make_uint4(0, 0, 0, 0);
+    if (jj < nt) {
+      const int blk = tbl[tv / BS];
+      if ((unsigned)blk < (unsigned)p.NB)
+        vr[k] = __ldg(reinterpret_cast<const uint4 *>(
+            p.v_cache + ((size_t)blk * p.n_kv + g) * TILE + code_offset8b(tv % BS, tid & 7)));
     }
+  }
+  float s[G];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int jj = 16 * k + (tid >> 3), tv = tb + jj;
-      vr[k] = make_uint4(0, 0, 0, 0);
-      if (jj < nt) {
-        const int blk = __ldg(trow + tv / BS);
-        if ((unsigned)blk < (unsigned)p.NB)
-          vr[k] = __ldg(reinterpret_cast<const uint4 *>(
-              p.v_cache + ((size_t)blk * p.n_kv + g) * TILE + code_offset8b(tv % BS, tid & 7)));
-      }
-    }
-    if (tid < nt) {
-      const int blk = __ldg(trow + (tb + tid) / BS);
-      if ((unsigned)blk < (unsigned)p.NB) vscl = __ldg(pp.v_scales + (size_t)blk * p.n_kv + g);
-    }
-    float s[G];
-#pragma unroll
-    for (int h = 0; h < G; ++h) s[h] = 0.f;
+  for (int h = 0; h < G; ++h) s[h] = 0.f;
+  if (warp * 16 < nt) {  // (the other warps have no token)
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const uint32_t w[4] = {kr[k].x, kr[k].y, kr[k].z, kr[k].w};
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float2 f = __half22float2(e4m3x2_to_half2((uint16_t)(w[e >> 1] >> ((e & 1) * 16))));
-        const int d = 64 * hf + 16 * k + 2 * e;
+      for (int e = 0; e < 4; ++e) {
+        const float2 a = __half22float2(e4m3x2_to_half2((uint16_t)w[e]));
+        const float2 c = __half22float2(e4m3x2_to_half2((uint16_t)(w[e] >> 16)));
 #pragma unroll
         for (int h = 0; h < G; ++h) {
-          const float2 q2 = *reinterpret_cast<const float2 *>(&qs[h][d]);
-          s[h] = fmaf(q2.x, f.x, s[h]);
-          s[h] = fmaf(q2.y, f.y, s[h]);
+          const float4 q4 = *reinterpret_cast<const float4 *>(&qs[h][hf][16 * k + 4 * e]);
+          s[h] = fmaf(q4.x, a.x, s[h]);
+          s[h] = fmaf(q4.y, a.y, s[h]);
+          s[h] = fmaf(q4.z, c.x, s[h]);
+          s[h] = fmaf(q4.w, c.y, s[h]);
         }
       }
     }
+  }
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      *reinterpret_cast<uint4 *>(&vs[16 * k + (tid >> 3)][16 * (tid & 7)]) = vr[k];
-    if (tid < CH) vsc[tid] = vscl;
+  for (int k = 0; k < 4; ++k)
+    *reinterpret_cast<uint4 *>(&vs[32 * k + (tid >> 3)][16 * (tid & 7)]) = vr[k];
+  if (hf == 0) vsc[j] = vscl;
+  // the CTA's maximum of each head, the probabilities, their sums
 #pragma unroll
-    for (int h = 0; h < G; ++h) {
-      s[h] += __shfl_xor_sync(kFullMask, s[h], 1);
-      s[h] = kval ? s[h] * ksc * p.qk_scale_log2 : -INFINITY;
-      float m = s[h];
+  for (int h = 0; h < G; ++h) {
+    s[h] += __shfl_xor_sync(kFullMask, s[h], 1);
+    s[h] = kval ? s[h] * ksc * p.qk_scale_log2 : -INFINITY;
+    float m = s[h];
 #pragma unroll
-      for (int o = 2; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(kFullMask, m, o));
-      if (lane == 0) red[warp][h] = m;
-    }
-    __syncthreads();
-    float alpha[G], m_new[G];
+    for (int o = 2; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(kFullMask, m, o));
+    if (lane == 0) red[0][warp][h] = m;
+  }
+  __syncthreads();
+  float mx[G];
 #pragma unroll
-    for (int h = 0; h < G; ++h) {
-      const float mc = fmaxf(fmaxf(red[0][h], red[1][h]), fmaxf(red[2][h], red[3][h]));
-      m_new[h] = fmaxf(m_run[h], mc);
-      alpha[h] = m_run[h] == -INFINITY ? 0.f : exp2f(m_run[h] - m_new[h]);
-      m_run[h] = m_new[h];
-      if (hf == 0) ps[j][h] = s[h] == -INFINITY ? 0.f : exp2f(s[h] - m_new[h]);
-    }
-    __syncthreads();
-    float acc[G], ls[G];
+  for (int h = 0; h < G; ++h) {
+    mx[h] = red[0][0][h];
 #pragma unroll
-    for (int h = 0; h < G; ++h) { acc[h] = 0.f; ls[h] = 0.f; }
-    for (int jj = 0; jj < nt; ++jj) {
-      const __half hv = __half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)vs[jj][tid], __NV_E4M3));
-      const float v = __half2float(hv) * vsc[jj];
+    for (int w = 1; w < NW; ++w) mx[h] = fmaxf(mx[h], red[0][w][h]);
+    const float e = s[h] == -INFINITY ? 0.f : exp2f(s[h] - mx[h]);
+    if (hf == 0) ps[j][h] = e * vsc[j];
+    float l = e;
+#pragma unroll
+    for (int o = 2; o < 32; o <<= 1) l += __shfl_xor_sync(kFullMask, l, o);
+    if (lane == 0) red[1][warp][h] = l;
+  }
+  __syncthreads();
+  // p.v: dims 2 d and 2 d + 1 over the tokens of group tg
+  {
+    const int d = tid & 63, tg = tid >> 6;
+    float a0[G], a1[G];
+#pragma unroll
+    for (int h = 0; h < G; ++h) { a0[h] = 0.f; a1[h] = 0.f; }
+#pragma unroll 4
+    for (int jj = tg; jj < nt; jj += NTG) {
+      const float2 v = __half22float2(
+          e4m3x2_to_half2(*reinterpret_cast<const uint16_t *>(&vs[jj][2 * d])));
 #pragma unroll
       for (int h = 0; h < G; ++h) {
-        const float pw = ps[jj][h];
-        acc[h] = fmaf(pw, v, acc[h]);
-        ls[h] += pw;
+        const float w = ps[jj][h];
+        a0[h] = fmaf(w, v.x, a0[h]);
+        a1[h] = fmaf(w, v.y, a1[h]);
       }
     }
 #pragma unroll
-    for (int h = 0; h < G; ++h) {
-      o_acc[h] = o_acc[h] * alpha[h] + acc[h];
-      l_run[h] = l_run[h] * alpha[h] + ls[h];
+    for (int h = 0; h < G; ++h)
+      *reinterpret_cast<float2 *>(&po[tg][h][2 * d]) = make_float2(a0[h], a1[h]);
+  }
+  __syncthreads();
+  // This CTA's state to the CTAs that merge it.
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  for (int i = tid; i < G * kHeadDim; i += THREADS) {
+    const int h = i / kHeadDim, d = i % kHeadDim;
+    const float o = (po[0][h][d] + po[1][h][d]) + (po[2][h][d] + po[3][h][d]);
+    st_peer(&in_o[rank][h][d % (kHeadDim / CL)], (uint32_t)(d / (kHeadDim / CL)), o);
+  }
+  if (tid < CL * G) {
+    const int h = tid / CL, r = tid % CL;
+    float l = 0.f, m = red[0][0][h];
+    for (int w = 0; w < NW; ++w) {
+      l += red[1][w][h];
+      m = fmaxf(m, red[0][w][h]);
     }
-    __syncthreads();
+    st_peer(&in_m[rank][h], (uint32_t)r, m);
+    st_peer(&in_l[rank][h], (uint32_t)r, l);
   }
-  if (bad) atomicOr(p.err, PGD_DEVERR_BAD_BLOCK_ID);
-#pragma unroll
-  for (int h = 0; h < G; ++h) st_o[h][tid] = o_acc[h];
-  if (tid == 0) {
-#pragma unroll
-    for (int h = 0; h < G; ++h) { st_m[h] = m_run[h]; st_l[h] = l_run[h]; }
-  }
-  cluster_sync();
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
+               "barrier.cluster.wait.acquire.aligned;" ::: "memory");
   if (tid < 16 * G) {
-    const int h = tid / 16, d = (int)rank * 16 + (tid % 16);
-    float mk[CL], lk[CL], ok[CL];
+    const int h = tid / 16, d = tid % 16;
+    float M = in_m[0][h];
 #pragma unroll
-    for (int k = 0; k < CL; ++k) {
-      mk[k] = ld_peer(&st_m[h], (uint32_t)k);
-      lk[k] = ld_peer(&st_l[h], (uint32_t)k);
-      ok[k] = ld_peer(&st_o[h][d], (uint32_t)k);
-    }
-    float M = mk[0];
-#pragma unroll
-    for (int k = 1; k < CL; ++k) M = fmaxf(M, mk[k]);
+    for (int k = 1; k < CL; ++k) M = fmaxf(M, in_m[k][h]);
     float num = 0.f, den = 0.f;
     if (M != -INFINITY) {
 #pragma unroll
       for (int k = 0; k < CL; ++k) {
-        const float w = mk[k] == -INFINITY ? 0.f : exp2f(mk[k] - M);
-        num = fmaf(w, ok[k], num);
-        den = fmaf(w, lk[k], den);
+        const float w = in_m[k][h] == -INFINITY ? 0.f : exp2f(in_m[k][h] - M);
+        num = fmaf(w, in_o[k][h][d], num);
+        den = fmaf(w, in_l[k][h], den);
       }
     }
-    p.out[((size_t)b * p.n_q + g * G + h) * kHeadDim + d] =
+    p.out[((size_t)b * p.n_q + g * G + h) * kHeadDim + rank * 16 + d] =
         __float2bfloat16_rn(den != 0.f ? num / den : 0.f);
   }
-  cluster_sync();  // peers may still be reading this CTA's state
 }
 
 template <int G, int BS>
@@ -238,9 +257,12 @@ cudaError_t launch_bs(const Attn8bParams &p, int G, cudaStream_t stream) {
 
 }  // namespace cl8b
 
+int cluster_max_tokens() { return cl8b::MAX_TOKENS; }
+
 cudaError_t cluster_attention_fp8b_launch(const Attn8bParams &p, int G, int bs,
                                           cudaStream_t stream) {
   if (p.a.B * p.a.n_kv == 0) return cudaSuccess;
+  if ((long long)p.a.MB * bs > cl8b::MAX_TOKENS) return cudaErrorInvalidValue;
   return bs == 16   ? cl8b::launch_bs<16>(p, G, stream)
          : bs == 32 ? cl8b::launch_bs<32>(p, G, stream)
                     : cudaErrorInvalidValue;

@@ -109,6 +109,7 @@ struct Attn8bParams {
 };
 cudaError_t attention_fp8b_launch(const Attn8bParams &p, int G, int bs, int grid,
                                   cudaStream_t stream);
+int cluster_max_tokens();
 cudaError_t cluster_attention_fp8b_launch(const Attn8bParams &p, int G, int bs,
                                           cudaStream_t stream);
 
