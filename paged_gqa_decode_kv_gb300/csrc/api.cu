@@ -1382,14 +1382,15 @@ pgd_status pgd_kv_read_fp8b(void *k_out, void *v_out, const void *k_cache, const
 }
 
 // Whether an automatic call goes to the cluster kernel instead of the
-// tensor-core one: few units, whose eight CTAs each find a place at once (with
-// more query heads a unit each takes longer), and short contexts.  Device time
-// of the two in us, 16-token blocks: 8 units x 512 tokens, G = 4: 5.2 / 7.0; 8 x
-// 1024: 7.9 / 10.9; 32 x 512, G = 4: 6.8 / 7.3; 32 x 512, G = 8: 9.1 / 8.5; 64 x
-// 256, G = 1: 5.0 / 5.9; 64 x 256, G = 4: 10.4 / 6.5; 64 x 640, G = 1: 7.9 / 7.4.
+// tensor-core one: short contexts and few units, fewer with more query heads to
+// a unit, each of which costs its CTAs time.  Device time of the two in us,
+// 16-token blocks: 8 units x 512 tokens, G = 4: 4.2 / 6.9; 32 x 1024, G = 4: 7.1
+// / 11.6; 48 x 512, G = 4: 8.1 / 7.4; 64 x 512, G = 2: 6.2 / 7.1; 64 x 1024, G =
+// 2: 9.1 / 9.0; 96 x 64, G = 1: 6.4 / 5.9; 24 x 1024, G = 8: 9.9 / 14.6; 32 x 512,
+// G = 8: 9.3 / 8.5.
 static bool cluster_rule(long long units, int G, long long tokens, int32_t num_splits) {
-  return num_splits == 0 && units <= 64 && units * G <= 128 && units * tokens <= 32768 &&
-         tokens <= std::min(g_short_tokens.load(), cluster_max_tokens());
+  return num_splits == 0 && units <= (G <= 2 ? 64 : G == 4 ? 32 : 24) &&
+         units * tokens <= 32768 && tokens <= std::min(g_short_tokens.load(), cluster_max_tokens());
 }
 
 // Attention over the block-scaled cache on checked arguments.

@@ -17,8 +17,9 @@
 //   eight states of dims [16 r, 16 r + 16) by log-sum-exp from its own memory
 //   (reading the peers' states instead takes a second barrier, before a CTA
 //   may exit, and the latency of the remote loads).
-// 8 heads x 512 tokens, G = 4: 4.2 us (5.1 in pieces of 64 tokens, with a table
-// load behind the length and remote loads).
+// 8 heads x 512 tokens, G = 4: 4.2 us (5.1 in pieces of 64 tokens with a table
+// load behind the length and remote loads; 8.0 with eight threads a token, whose
+// reads of the query met in the same banks).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
