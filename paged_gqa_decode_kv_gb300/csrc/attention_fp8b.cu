@@ -66,6 +66,8 @@ using namespace tc;
 // rows (tiles) of 256 8-byte elements, read in boxes of one row.
 struct Params {
   Attn8bParams q8;
+  float split_root;  // parts of a split by its cost X: split_root * sqrt(X)
+  float inv_units;   // 1 / (B * n_kv)
   CUtensorMap k_map, v_map;
 };
 
@@ -113,6 +115,7 @@ static_assert(40 + 4 * NSR <= 112 && OFF_MISC % 16 == 0, "misc layout");
 // One CTA streams at most about 1/kShare of the HBM rate (128 of 152 CTAs take
 // the whole of it: 0.58 us a stage).
 constexpr float kShare = 126.f;
+template <int BS> constexpr float kBlockBytes = 2.f * BS * kHeadDim;
 constexpr int MERGE_U = 20;  // parts of a unit that a merging thread has in flight
 
 // kind::f8f6f4, D f32, A and B E4M3, both MN-major, M = 128.
@@ -166,11 +169,11 @@ __device__ __forceinline__ void walk_start(const Cuts &sc, Walk &w) {
   w.end = (int)min((long long)sc.X, (long long)w.x + sc.S);
 }
 // Part c of a split into whole units: unit c, if it has blocks.
-__device__ __forceinline__ bool whole_unit(const Cuts &sc, Piece &sg) {
+__device__ __forceinline__ bool whole_unit(const Cuts &sc, int b, Piece &sg) {
   const int c = (int)blockIdx.x;
   if (c >= sc.P) return false;
-  sg.b = c / sc.n_kv;
-  sg.g = c - sg.b * sc.n_kv;
+  sg.b = b;
+  sg.g = c - b * sc.n_kv;
   const int cost = sc.pre[sg.b + 1] - sc.pre[sg.b];
   sg.j0 = 0;
   sg.nblk = sg.n = cost - sc.ov;
@@ -239,7 +242,7 @@ template <int BS, bool IS_K>
 __device__ __forceinline__ void produce(const Params &pr, const Cuts &sc, Walk w, Piece sg,
                                         bool have, Ids ids, unsigned char *smem, uint64_t *full,
                                         uint64_t *empty, volatile int *stage_mask,
-                                        volatile int *abort_flag, int lane) {
+                                        volatile int *abort_flag, uint64_t policy, int lane) {
   const Attn8bParams &pp = pr.q8;
   const AttnParams &p = pp.a;
   constexpr int SB = TOK / BS;
@@ -250,9 +253,9 @@ __device__ __forceinline__ void produce(const Params &pr, const Cuts &sc, Walk w
   const unsigned char *cache = IS_K ? p.k_cache : p.v_cache;
   unsigned char *ring = smem + (IS_K ? OFF_K : OFF_V);
   const uint32_t sring = smem_addr(smem + OFF_SC);
-  const uint64_t policy = l2_policy_evict_first();
   if (p.wait_late == 1) pdl_wait();  // the append has written the cache
-  int s = 0;
+  int s = 0, slot = 0;
+  uint32_t phase = 1;  // (the ring starts empty)
   bool stop = false;
   while (have && !stop) {
     bool have_next = false;
@@ -275,7 +278,6 @@ __device__ __forceinline__ void produce(const Params &pr, const Cuts &sc, Walk w
       const bool ok = lane < nb && (unsigned)blk < (unsigned)p.NB;
       const unsigned okmask = __ballot_sync(kFullMask, ok);
       const int tile = ok ? blk * p.n_kv + sg.g : 0;
-      const int slot = s % NS;
       unsigned char *dst = ring + (size_t)slot * STAGE;
       int rows[SB];
       if constexpr (GATHER) {
@@ -284,7 +286,7 @@ __device__ __forceinline__ void produce(const Params &pr, const Cuts &sc, Walk w
       }
       int go = 1;
       if (lane == 0) {
-        wait_or_abort(&empty[slot], ((uint32_t)(s / NS) & 1u) ^ 1u, abort_flag, p.err);
+        wait_or_abort(&empty[slot], phase, abort_flag, p.err);
         go = *abort_flag ? 0 : 1;
         if (go) {
           if (IS_K) {
@@ -323,6 +325,10 @@ __device__ __forceinline__ void produce(const Params &pr, const Cuts &sc, Walk w
       if (st == 0) {  // the next segment's ids, once this one's copies have begun
         have_next = walk_next(sc.pre, sc.n_kv, sc.ov, p.B, w, nsg);
         if (have_next) next_ids = load_ids(p, nsg, lane);
+      }
+      if (++slot == NS) {
+        slot = 0;
+        phase ^= 1u;
       }
     }
     sg = nsg;
@@ -499,6 +505,15 @@ attention_fp8b_kernel(const __grid_constant__ Params pr) {
     uint4 *z = reinterpret_cast<uint4 *>(smem + OFF_Q);
     for (int i = tid; i < (2 * Q_BYTES + 2 * P_BYTES8) / 16; i += NTHREADS)
       z[i] = make_uint4(0, 0, 0, 0);
+    fence_proxy_async();
+  }
+  const int unit_b = (int)blockIdx.x / p.n_kv;  // CTA c's unit in a split into whole units
+  uint64_t policy = 0;
+  if (warp == WARP_KP || warp == WARP_VP) {
+    policy = l2_policy_evict_first();
+    if (BS == 16 && lane == 0)
+      asm volatile("prefetch.tensormap [%0];" ::"l"(warp == WARP_KP ? &pr.k_map : &pr.v_map)
+                   : "memory");
   }
   if (warp == WARP_QK) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -514,31 +529,30 @@ attention_fp8b_kernel(const __grid_constant__ Params pr) {
   // does with no more units than CTAs, unless the units are cut).
   int guess_b = -1;
   Ids guess{};
-  if ((warp == WARP_KP || warp == WARP_VP) && (int)blockIdx.x < p.B * p.n_kv) {
-    guess_b = (int)blockIdx.x / p.n_kv;
+  if ((warp == WARP_KP || warp == WARP_VP) && unit_b < p.B) {
+    guess_b = unit_b;
     const int32_t *trow = p.tables + (size_t)guess_b * p.MB;
     if (lane < p.MB) guess.tab = __ldg(trow + lane);
     if (32 + lane < p.MB) guess.tab_next = __ldg(trow + 32 + lane);
   }
-  // Blocks of every sequence (thread t takes `per` of them from t * per), and
-  // their exclusive prefix over the batch.
+  // Cost of every sequence's blocks (thread t takes `per` of them from t * per)
+  // and its prefix over the batch.
   const int max_tokens = p.MB * BS;
   const int per = (p.B + NTHREADS - 1) / NTHREADS;
-  int cost[PGD_MAX_BATCH / NTHREADS];
+  const int b_end = min(p.B, (tid + 1) * per);
   int sum = 0, longest = 0;
-  bool bad_ctx = false;
-#pragma unroll
-  for (int i = 0; i < PGD_MAX_BATCH / NTHREADS; ++i) {
-    const int b = tid * per + i;
-    cost[i] = 0;
-    if (i < per && b < p.B) {
-      const int c = __ldg(p.ctx + b);
-      if (c >= 1 && c <= max_tokens) cost[i] = (c + BS - 1) / BS + kSegCost<BS>; else bad_ctx = true;
+#pragma unroll 1
+  for (int b = tid * per; b < b_end; ++b) {
+    const int c = __ldg(p.ctx + b);
+    if (c >= 1 && c <= max_tokens) {
+      const int cost = (c + BS - 1) / BS + kSegCost<BS>;
+      sum += cost;
+      longest = max(longest, cost);
+    } else if (blockIdx.x == 0) {
+      atomicOr(p.err, PGD_DEVERR_BAD_CONTEXT);
     }
-    sum += cost[i];
-    longest = max(longest, cost[i]);
+    pre[b + 1] = sum;
   }
-  if (bad_ctx && blockIdx.x == 0) atomicOr(p.err, PGD_DEVERR_BAD_CONTEXT);
   int upto = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -547,7 +561,6 @@ attention_fp8b_kernel(const __grid_constant__ Params pr) {
   }
   longest = __reduce_max_sync(kFullMask, longest);
   if (lane == 31) warp_sum[warp] = make_int2(upto, longest);
-  fence_proxy_async();
   __syncthreads();
   int before = upto - sum;
 #pragma unroll
@@ -556,15 +569,9 @@ attention_fp8b_kernel(const __grid_constant__ Params pr) {
     if (w < warp) before += v.x;
     longest = max(longest, v.y);
   }
-#pragma unroll
-  for (int i = 0; i < PGD_MAX_BATCH / NTHREADS; ++i) {
-    const int b = tid * per + i;
-    if (i < per && b < p.B) {
-      pre[b] = before;
-      before += cost[i];
-      if (b == p.B - 1) pre[p.B] = before;
-    }
-  }
+#pragma unroll 1
+  for (int b = tid * per; b < b_end; ++b) pre[b + 1] += before;
+  if (tid == 0) pre[0] = 0;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -581,13 +588,16 @@ attention_fp8b_kernel(const __grid_constant__ Params pr) {
   sc.P = min(sc.X, (int)gridDim.x);
   sc.units = false;
   if (p.auto_split && sc.X > 0) {
+    // (approximate functions: the same in every thread, which is all it takes)
     const int U = p.B * p.n_kv;
-    constexpr float kBlockBytes = 2.f * BS * kHeadDim;
-    constexpr float m0 = (float)kMergeFixedBytes / kBlockBytes;
-    constexpr float m1 = (float)kMergePartBytes / kBlockBytes;
+    constexpr float m0 = (float)kMergeFixedBytes / kBlockBytes<BS>;
+    constexpr float m1 = (float)kMergePartBytes / kBlockBytes<BS>;
     const float X = (float)sc.X;
-    const int P = max(1, min(sc.P, (int)sqrtf(kShare * X * (float)U / m1)));
-    const float cost_cut = fmaxf(X / (float)P * kShare, X) + m0 + m1 * (float)((P + U - 1) / U);
+    float root;
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(root) : "f"(X));
+    const int P = max(1, min(sc.P, (int)(pr.split_root * root)));
+    const float cost_cut = fmaxf(__fdividef(X, (float)P) * kShare, X) + m0 +
+                           m1 * ceilf((float)P * pr.inv_units);
     sc.P = P;
     if (U <= (int)gridDim.x && fmaxf((float)longest * kShare, X) <= cost_cut) {
       sc.units = true;
@@ -600,7 +610,7 @@ attention_fp8b_kernel(const __grid_constant__ Params pr) {
   Piece sg{};
   bool have;
   if (sc.units) {
-    have = whole_unit(sc, sg);
+    have = whole_unit(sc, unit_b, sg);
   } else {
     sc.S = sc.P > 0 ? (sc.X + sc.P - 1) / sc.P : 1;
     walk_start(sc, walk);
@@ -612,15 +622,17 @@ attention_fp8b_kernel(const __grid_constant__ Params pr) {
 
   if (warp == WARP_KP) {
     produce<BS, true>(pr, sc, walk, sg, have, guess, smem, full_k, empty_k, stage_mask,
-                      abort_flag, lane);
+                      abort_flag, policy, lane);
   } else if (warp == WARP_VP) {
     produce<BS, false>(pr, sc, walk, sg, have, guess, smem, full_v, empty_v, nullptr, abort_flag,
-                       lane);
+                       policy, lane);
   } else if (warp == WARP_QK) {
     // ------------------------------ query conversion, then q.k^T (one lane)
     Piece nsg;
     uint4 q[kPieces<G>];
     if (have) load_query<G>(p, sg, lane, q);
+    int slot = 0;
+    uint32_t phase = 0;
     int s = 0, k = 0, last1 = -1, last2 = -1;  // last stages of segments k - 1, k - 2
     while (have) {
       const int nstages = (sg.n + SB - 1) / SB;
@@ -636,8 +648,8 @@ attention_fp8b_kernel(const __grid_constant__ Params pr) {
       if (lane == 0) {
         const uint64_t qd = smem_desc(smem_addr(qbuf), 128, 1024, 0);
         for (int st = 0; st < nstages; ++st) {
-          const int su = s + st, slot = su % NSK, sb = su % NSB;
-          wait_or_abort(&full_k[slot], (uint32_t)(su / NSK) & 1u, abort_flag, p.err);
+          const int su = s + st, sb = su % NSB;
+          wait_or_abort(&full_k[slot], phase, abort_flag, p.err);
           wait_or_abort(&s_free[sb], ((uint32_t)(su / NSB) & 1u) ^ 1u, abort_flag, p.err);
           tc_fence_after();
           if (!*abort_flag) {
@@ -654,6 +666,10 @@ attention_fp8b_kernel(const __grid_constant__ Params pr) {
           // the stage's invalid-block mask and scales, which full_k ordered
           // before this, and the query's scales, for the softmax
           mbar_arrive(&m_ready[sb]);
+          if (++slot == NSK) {
+            slot = 0;
+            phase ^= 1u;
+          }
         }
       }
       __syncwarp();
@@ -671,14 +687,15 @@ attention_fp8b_kernel(const __grid_constant__ Params pr) {
   } else if (warp == WARP_PV) {
     // ------------------------------------------------------- p.v issuer
     if (lane == 0) {
-      int s = 0, k = 0;
+      int s = 0, k = 0, slot = 0;
+      uint32_t phase = 0;
       while (have) {
         const int nstages = (sg.n + SB - 1) / SB;
         const int ob = k & 1;
         for (int st = 0; st < nstages; ++st, ++s) {
-          const int slot = s % NSV, sb = s & 1;
+          const int sb = s & 1;
           wait_or_abort(&p_full[sb], (uint32_t)(s >> 1) & 1u, abort_flag, p.err);
-          wait_or_abort(&full_v[slot], (uint32_t)(s / NSV) & 1u, abort_flag, p.err);
+          wait_or_abort(&full_v[slot], phase, abort_flag, p.err);
           if (st == 0)
             wait_or_abort(&o_free[ob], ((uint32_t)(k >> 1) & 1u) ^ 1u, abort_flag, p.err);
           tc_fence_after();
@@ -697,6 +714,10 @@ attention_fp8b_kernel(const __grid_constant__ Params pr) {
           umma_commit(&empty_v[slot]);
           umma_commit(&p_free[sb]);
           if (st + 1 == nstages) umma_commit(&o_full[ob]);
+          if (++slot == NSV) {
+            slot = 0;
+            phase ^= 1u;
+          }
         }
         ++k;
         have = next(sg);
@@ -1042,6 +1063,10 @@ cudaError_t attention_fp8b_launch(const Attn8bParams &q8, int G, int bs, int gri
                                   cudaStream_t stream) {
   tc8b::Params p = {};
   p.q8 = q8;
+  const float units = (float)q8.a.B * (float)q8.a.n_kv;
+  const float block = bs == 16 ? tc8b::kBlockBytes<16> : tc8b::kBlockBytes<32>;
+  p.split_root = sqrtf(tc8b::kShare * units * block / (float)tc::kMergePartBytes);
+  p.inv_units = 1.f / units;
   if (bs == 16) {
     const long long tiles = (long long)q8.a.NB * q8.a.n_kv;
     cudaError_t e = tc8b::encode_map(&p.k_map, q8.a.k_cache, tiles);
