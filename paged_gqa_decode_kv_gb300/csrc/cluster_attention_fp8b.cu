@@ -1,23 +1,25 @@
 // cluster_attention_fp8b.cu -- decode attention over the block-scaled 8-bit
-// cache for short contexts, on the CUDA cores: one cluster of 8 CTAs per
-// (sequence, KV head).
+// cache for short contexts, on the CUDA cores: one cluster of CTAs per
+// (sequence, KV head), 8 of them up to 1024 tokens and 16 up to 2048.
 //
-//   out[b][h] = sum_t softmax_t(scale * q[b][h] . k_t) v_t,  t < ctx[b] <= 1024,
+//   out[b][h] = sum_t softmax_t(scale * q[b][h] . k_t) v_t,  t < ctx[b] <= 2048,
 //   k_t = sk[tile] * E4M3(code), v_t = sv[tile] * E4M3(code)
 //
 // Such a call is bound by a chain of latencies, so the chain is short:
-// - the context length, the table row (at most 64 blocks) and the query are
+// - the context length, the table row (at most 128 blocks) and the query are
 //   loaded side by side; then K and V codes and scales, all in flight together;
-// - CTA r of a cluster takes the contiguous tokens [r ctx / 8, (r + 1) ctx / 8),
+// - CTA r of a cluster takes the contiguous tokens [r ctx / C, (r + 1) ctx / C),
 //   at most 128, in one piece: two threads a token for q.k (64 dims each), one
 //   maximum and one sum per head; p.v with two dims a thread and every fourth
 //   token, V's scale folded into the probability; fp32, exact exp2;
 // - every CTA stores its maxima, sums and output dims into the shared memory of
 //   the CTAs that write them, and after one cluster barrier CTA r merges the
-//   eight states of dims [16 r, 16 r + 16) by log-sum-exp from its own memory
+//   C states of its 128 / C dims by log-sum-exp from its own memory
 //   (reading the peers' states instead takes a second barrier, before a CTA
 //   may exit, and the latency of the remote loads).
-// 8 heads x 512 tokens, G = 4: 4.2 us (5.1 in pieces of 64 tokens with a table
+// 8 heads x 2048 tokens, G = 4: 7.3 us (10.5 on the tensor cores; 4096 tokens
+// in 16 CTAs of 512 threads: 13.2 against 11.2).
+// 8 heads x 512 tokens, G = 4: 4.0 us (5.1 in pieces of 64 tokens with a table
 // load behind the length and remote loads; 8.0 with eight threads a token, whose
 // reads of the query met in the same banks).
 #include <cuda_bf16.h>
@@ -28,11 +30,8 @@
 namespace pgd {
 namespace cl8b {
 
-constexpr int CL = 8;          // CTAs per (sequence, KV head): one cluster
 constexpr int THREADS = 256;
 constexpr int CH = 128;        // tokens of a CTA at most
-constexpr int MAX_TOKENS = CL * CH;
-constexpr int MAXB = 64;       // blocks of a sequence (16 tokens each) at most
 constexpr int NTG = 4;         // token groups of p.v
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -47,11 +46,14 @@ __device__ __forceinline__ void st_peer(float *local, uint32_t rank, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(remote), "f"(v) : "memory");
 }
 
-template <int G, int BS>
+// CL: CTAs per (sequence, KV head), one cluster.
+template <int G, int BS, int CL>
 __global__ void __launch_bounds__(THREADS) cluster_attention_kernel(const Attn8bParams pp) {
   const AttnParams &p = pp.a;
   constexpr size_t TILE = (size_t)BS * kHeadDim;
   constexpr int NW = THREADS / 32;
+  constexpr int MAXB = CL * CH / 16;  // blocks of a sequence (16 tokens each) at most
+  constexpr int OD = kHeadDim / CL;   // output dims that a CTA merges
   // (two halves, 4 banks apart: a warp reads the same dims of both at once)
   __shared__ __align__(16) float qs[G][2][kHeadDim / 2 + 4];
   __shared__ __align__(16) unsigned char vs[CH][kHeadDim];  // V codes
@@ -60,7 +62,7 @@ __global__ void __launch_bounds__(THREADS) cluster_attention_kernel(const Attn8b
   __shared__ float red[2][NW][G];                           // per-warp maxima, sums
   __shared__ int tbl[MAXB];
   __shared__ float po[NTG][G][kHeadDim];                    // outputs of the token groups
-  __shared__ float in_m[CL][G], in_l[CL][G], in_o[CL][G][kHeadDim / CL];  // written by the peers
+  __shared__ float in_m[CL][G], in_l[CL][G], in_o[CL][G][OD];  // written by the peers
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t rank = cluster_rank();
@@ -194,7 +196,7 @@ __global__ void __launch_bounds__(THREADS) cluster_attention_kernel(const Attn8b
   for (int i = tid; i < G * kHeadDim; i += THREADS) {
     const int h = i / kHeadDim, d = i % kHeadDim;
     const float o = (po[0][h][d] + po[1][h][d]) + (po[2][h][d] + po[3][h][d]);
-    st_peer(&in_o[rank][h][d % (kHeadDim / CL)], (uint32_t)(d / (kHeadDim / CL)), o);
+    st_peer(&in_o[rank][h][d % OD], (uint32_t)(d / OD), o);
   }
   if (tid < CL * G) {
     const int h = tid / CL, r = tid % CL;
@@ -208,8 +210,8 @@ __global__ void __launch_bounds__(THREADS) cluster_attention_kernel(const Attn8b
   }
   asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
                "barrier.cluster.wait.acquire.aligned;" ::: "memory");
-  if (tid < 16 * G) {
-    const int h = tid / 16, d = tid % 16;
+  if (tid < OD * G) {
+    const int h = tid / OD, d = tid % OD;
     float M = in_m[0][h];
 #pragma unroll
     for (int k = 1; k < CL; ++k) M = fmaxf(M, in_m[k][h]);
@@ -222,27 +224,53 @@ __global__ void __launch_bounds__(THREADS) cluster_attention_kernel(const Attn8b
         den = fmaf(w, in_l[k][h], den);
       }
     }
-    p.out[((size_t)b * p.n_q + g * G + h) * kHeadDim + rank * 16 + d] =
+    p.out[((size_t)b * p.n_q + g * G + h) * kHeadDim + rank * OD + d] =
         __float2bfloat16_rn(den != 0.f ? num / den : 0.f);
   }
 }
 
-template <int G, int BS>
-cudaError_t launch_g(const Attn8bParams &p, cudaStream_t stream) {
+template <class Kernel>
+cudaError_t allow_large_clusters(Kernel kernel, volatile int (&done)[64]) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (dev >= 0 && dev < 64 && done[dev])) return e;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = 1;
+  return e;
+}
+cudaLaunchAttribute cluster_of(int n) {
+  cudaLaunchAttribute a = {};
+  a.id = cudaLaunchAttributeClusterDimension;
+  a.val.clusterDim.x = (unsigned)n;
+  a.val.clusterDim.y = 1;
+  a.val.clusterDim.z = 1;
+  return a;
+}
+
+template <int G, int BS, int CL>
+cudaError_t launch_cl(const Attn8bParams &p, cudaStream_t stream) {
+  auto kernel = cluster_attention_kernel<G, BS, CL>;
+  if (CL > 8) {
+    static volatile int done[64] = {0};  // larger clusters allowed, per device
+    const cudaError_t e = allow_large_clusters(kernel, done);
+    if (e != cudaSuccess) return e;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(p.a.B * p.a.n_kv * CL));
   cfg.blockDim = dim3(THREADS);
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = CL;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
+  attr[0] = cluster_of(CL);
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, cluster_attention_kernel<G, BS>, p);
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+template <int G, int BS>
+cudaError_t launch_g(const Attn8bParams &p, cudaStream_t stream) {
+  return p.a.MB * BS <= 8 * CH ? launch_cl<G, BS, 8>(p, stream) : launch_cl<G, BS, 16>(p, stream);
 }
 
 template <int BS>
@@ -258,12 +286,37 @@ cudaError_t launch_bs(const Attn8bParams &p, int G, cudaStream_t stream) {
 
 }  // namespace cl8b
 
-int cluster_max_tokens() { return cl8b::MAX_TOKENS; }
+// Whether the current device places clusters of 16 (a slice of a GPU may not).
+static bool clusters_of_16() {
+  static volatile int known[64] = {0};  // per device: 1 no, 2 yes
+  static volatile int done[64] = {0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+  if (!known[dev]) {
+    auto kernel = cl8b::cluster_attention_kernel<8, 16, 16>;  // the largest one
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(16);
+    cfg.blockDim = dim3(cl8b::THREADS);
+    cudaLaunchAttribute attr = cl8b::cluster_of(16);
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cl8b::allow_large_clusters(kernel, done) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+      cudaGetLastError();
+      n = 0;
+    }
+    known[dev] = n > 0 ? 2 : 1;
+  }
+  return known[dev] == 2;
+}
+
+int cluster_max_tokens() { return (clusters_of_16() ? 16 : 8) * cl8b::CH; }
 
 cudaError_t cluster_attention_fp8b_launch(const Attn8bParams &p, int G, int bs,
                                           cudaStream_t stream) {
   if (p.a.B * p.a.n_kv == 0) return cudaSuccess;
-  if ((long long)p.a.MB * bs > cl8b::MAX_TOKENS) return cudaErrorInvalidValue;
+  if ((long long)p.a.MB * bs > 16 * cl8b::CH) return cudaErrorInvalidValue;
   return bs == 16   ? cl8b::launch_bs<16>(p, G, stream)
          : bs == 32 ? cl8b::launch_bs<32>(p, G, stream)
                     : cudaErrorInvalidValue;

@@ -256,6 +256,26 @@ def test_attention_ragged(G, bs):
     bsc.close(got, *bsc.paged(c, q, SCALE))
 
 
+@pytest.mark.parametrize("limit", [1024, 600, 0])
+@pytest.mark.parametrize("G", [1, 2, 4, 8])
+@pytest.mark.parametrize("n_kv, bs, ctx", [
+    (4, 16, [2048, 1, 129]), (3, 32, [1025, 2033, 16]), (12, 16, [1023]), (13, 16, [1900]),
+    (16, 32, [1200]), (1, 16, [2049, 700]),
+])
+def test_attention_at_the_limits_of_short_contexts(n_kv, bs, ctx, G, limit):
+    """Sizes on both sides of every bound of the kernel for short contexts, and of each of its
+    two cluster sizes, at any limit."""
+    c = bsc.make_cache(ctx, n_kv, bs, seed=n_kv + G)
+    q = bsc.make_query(len(ctx), n_kv * G)
+    k, v, ks, vs, tables, lens = c.cuda()
+    before = pgd.set_short_context_tokens(limit)
+    try:
+        got = pgd.paged_decode_attention_fp8b(None, q.cuda(), k, v, ks, vs, tables, lens, SCALE)
+    finally:
+        pgd.set_short_context_tokens(before)
+    bsc.close(got, *bsc.paged(c, q, SCALE))
+
+
 @pytest.mark.parametrize("G", [1, 4, 8])
 @pytest.mark.parametrize("num_splits", [0, 1, 3])
 def test_attention_scores_grow_along_the_context(G, num_splits):
