@@ -276,14 +276,13 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
 // 3. Every warp counts, then writes, its own part of the slice in order.
 template <int G>
 __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams p, int C) {
-  extern __shared__ uint32_t keys[];  // a slice: block ids, then keys
+  extern __shared__ uint32_t ids[];  // a slice: block ids, and behind them the keys
   __shared__ uint32_t hist[kBins];
   __shared__ uint32_t all_hist[2][kMaxCluster][kBins];  // by pass parity, every CTA's
   __shared__ uint32_t all_range[kMaxCluster][2];   // largest ~key, largest key: unforced ones
-  __shared__ uint32_t all_counts[kMaxCluster][2];  // keys above the least, and equal to it
   __shared__ uint32_t range[2];
   __shared__ int warp_cnt[2][kSelWarps];
-  __shared__ int found[3];
+  __shared__ int found[5];
   __shared__ __align__(16) uint32_t qh[8][kHeadDim / 2];  // rounded queries, f16 pairs
   __shared__ float qf[8], qbias[8];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -320,7 +319,11 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
   if (C > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   const int per = (nblk + C - 1) / C;
   const int jlo = min(nblk, rank * per), n = min(nblk, jlo + per) - jlo;
-  for (int i = tid; i < n; i += kSelThreads) keys[i] = (uint32_t)__ldg(row + jlo + i);
+  uint32_t *keys = ids + per;
+  for (int i = tid; i < n; i += kSelThreads) {
+    const uint32_t blk = (uint32_t)__ldg(row + jlo + i);
+    ids[i] = blk;
+  }
   if (tid < kBins) hist[tid] = 0;
   if (tid < 2) range[tid] = 0;
   // The rounded queries: warp h takes head h (heads past G are zero).
@@ -381,7 +384,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int i = i0 + r + 8 * h;
-        const uint32_t blk = i < n ? keys[i] : 0xffffffffu;
+        const uint32_t blk = i < n ? ids[i] : 0xffffffffu;
         v.there[h] = blk < (uint32_t)p.NB;
         v.s[h] = 0.f;
 #pragma unroll
@@ -455,6 +458,10 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
   lo = ~lo;
   int need = W - p.keep_first - p.keep_last;
   bool all = false;  // every key of [lo, hi] is wanted
+  // In the slices before ours: forced blocks, unforced keys above hi, and keys
+  // in [lo, hi] (read when this is the last range).
+  const int forced = min(jlo, p.keep_first) + max(0, jlo - (nblk - p.keep_last));
+  int before = forced, inside = jlo - forced;
   for (int pass = 0; need > 0 && !all && lo != hi; ++pass) {
     const int shift = max(0, 24 - __clz(hi - lo));
     for (int i = tid; i < n; i += kSelThreads) {
@@ -472,37 +479,44 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
     }
     sync_all(C);
     const int bin = kBins - 1 - tid;
-    int cnt = 0, sum = 0;
+    // (two counts below 2^16: of all slices, and of the ones before ours)
+    uint32_t cnt = 0, sum = 0;
     if (tid < kBins) {
-      for (int r = 0; r < C; ++r) cnt += (int)all_hist[pass & 1][r][bin];
+      for (int r = 0; r < C; ++r) cnt += all_hist[pass & 1][r][bin] * (r < rank ? 0x10001u : 1u);
       sum = cnt;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(kFullMask, sum, o);
+        const uint32_t v = __shfl_up_sync(kFullMask, sum, o);
         if (lane >= o) sum += v;
       }
-      if (lane == 31) warp_cnt[0][warp] = sum;
+      if (lane == 31) warp_cnt[0][warp] = (int)sum;
     }
     __syncthreads();
     if (tid < kBins) {
-      for (int w = 0; w < warp; ++w) sum += warp_cnt[0][w];
-      if (sum >= need && sum - cnt < need) {  // this bin holds the need-th largest
+      for (int w = 0; w < warp; ++w) sum += (uint32_t)warp_cnt[0][w];
+      const uint32_t over = sum - cnt;  // in higher bins
+      const int n_over = (int)(over & 0xffffu), n_bin = (int)(cnt & 0xffffu);
+      if (n_over < need && n_over + n_bin >= need) {  // this bin holds the need-th largest
         found[0] = bin;
-        found[1] = need - (sum - cnt);
-        found[2] = cnt;
+        found[1] = need - n_over;
+        found[2] = n_bin;
+        found[3] = (int)(over >> 16);
+        found[4] = (int)(cnt >> 16);
       }
     }
     __syncthreads();
     need = found[1];
     all = found[2] == need;
+    before += found[3];
+    inside = found[4];
     lo += (uint32_t)found[0] << shift;
     hi = min(hi, lo + ((1u << shift) - 1u));
   }
   // Above: forced, or a key above hi, or in [lo, hi] where all are wanted.
   // Equal: the rest of [lo, hi], one value, the first `need` of which are taken.
-  if (need == 0) {
-    hi = 0xffffffffu;  // (nothing but the forced blocks)
-    lo = 0xffffffffu;
+  if (need == 0) {  // (nothing but the forced blocks)
+    hi = lo = 0xffffffffu;
+    inside = 0;
   }
   if (all) need = 0;
   auto above = [&](int i) {
@@ -524,24 +538,14 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
     n_above += __popc(__ballot_sync(kFullMask, in && above(i)));
     n_equal += __popc(__ballot_sync(kFullMask, in && equal(i)));
   }
-  __syncthreads();  // (warp_cnt was read by the last pass)
   if (lane == 0) {
     warp_cnt[0][warp] = n_above;
     warp_cnt[1][warp] = n_equal;
   }
   __syncthreads();
-  if (tid < 2) {
-    int a = 0;
-    for (int w = 0; w < kSelWarps; ++w) a += warp_cnt[tid][w];
-    push_all(&all_counts[rank][tid], (uint32_t)a, C);
-  }
-  sync_all(C);  // (nobody writes into another CTA's memory after this)
-  int at = 0, left = need;  // next output place, equal keys still to be taken
-  for (int r = 0; r < rank; ++r) {
-    const int take = min((int)all_counts[r][1], left);
-    at += (int)all_counts[r][0] + take;
-    left -= take;
-  }
+  // Next output place, and equal keys still to be taken.
+  if (!all) inside = min(inside, need);
+  int at = before + inside, left = need - (all ? 0 : inside);
   for (int w = 0; w < warp; ++w) {
     const int take = min(warp_cnt[1][w], left);
     at += warp_cnt[0][w] + take;
@@ -555,7 +559,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
     const unsigned eb = __ballot_sync(kFullMask, e);
     const bool sel = a || (e && __popc(eb & below) < left);
     const unsigned sb = __ballot_sync(kFullMask, sel);
-    if (sel) tiles[at + __popc(sb & below)] = tile_of(__ldg(row + jlo + i));
+    if (sel) tiles[at + __popc(sb & below)] = tile_of((int)ids[i]);
     at += __popc(sb);
     left -= min(left, __popc(eb));
   }
@@ -616,7 +620,7 @@ static cudaError_t launch_select(const SelectParams &p, cudaStream_t stream) {
   // With no more CTAs than SMs each gets an SM to itself: behind an attention
   // call, whose CTAs leave one by one, two would crowd the first SMs to be free
   // (a sparse step of one 131072-token context: 31.5 us crowded, 27.3 apart).
-  cfg.dynamicSmemBytes = units * C <= kSMs ? kAloneBytes : (size_t)((p.MB + C - 1) / C) * 4;
+  cfg.dynamicSmemBytes = units * C <= kSMs ? kAloneBytes : (size_t)((p.MB + C - 1) / C) * 8;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
