@@ -203,12 +203,14 @@ cudaError_t launch_pdl(K kernel, dim3 grid, int threads, size_t smem, cudaStream
 // (two CTAs an SM: 256 heads of 256 blocks take 8.5 us, with 512 threads 15.0)
 constexpr int kSelThreads = 256;
 constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 16;
+constexpr int kLarge[2] = {16, 12};  // clusters past the portable 8
+
 constexpr int kSMs = 152;          // of a GB300
 // Dynamic shared memory that leaves an SM room for one CTA.
 constexpr size_t kAloneBytes = 120 * 1024;
 constexpr int kSliceKeys = 6144;   // keys of a CTA's slice at most (24 KiB)
-constexpr int kBins = 256;
+constexpr int kBins = kSelThreads;  // a thread takes one
 
 // A float's bits as an unsigned integer of the same order.
 __device__ __forceinline__ uint32_t order_key(float f) {
@@ -216,28 +218,19 @@ __device__ __forceinline__ uint32_t order_key(float f) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// Barrier over the cluster's CTAs (shared-memory writes before it, into any
-// CTA's, are visible behind it), or over the one CTA.
-__device__ __forceinline__ void sync_all(int C) {
-  if (C > 1)
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
-                 "barrier.cluster.wait.acquire.aligned;" ::: "memory");
-  else
-    __syncthreads();
+// Barrier over the cluster's CTAs: shared-memory writes before it, into any
+// CTA's, are visible behind it.
+__device__ __forceinline__ void sync_cluster() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
+               "barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// Store into every CTA's shared memory at the place `local` has in ours.
-__device__ __forceinline__ void push_all(uint32_t *local, uint32_t v, int C) {
-  if (C == 1) {
-    *local = v;
-    return;
-  }
-  for (int r = 0; r < C; ++r) {
-    uint32_t remote;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
-                 : "=r"(remote)
-                 : "r"(smem_addr(local)), "r"(r));
-    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(remote), "r"(v) : "memory");
-  }
+// The place in CTA r's shared memory that `local` is in ours.
+__device__ __forceinline__ uint32_t peer_addr(const void *local, int r) {
+  uint32_t remote;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+               : "=r"(remote)
+               : "r"(smem_addr(local)), "r"(r));
+  return remote;
 }
 
 // D += A B, m16n8k16, f16 operands, fp32 accumulation.
@@ -272,13 +265,18 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
 //    barrier adds them up and keeps the bin that holds the wanted rank, until
 //    the bin is one value or all its keys are wanted.  (Starting from the
 //    range rather than from the keys' top byte, which is all but constant for
-//    scores of one query, saves a pass and the contention on one bin.)
+//    scores of one query, saves a pass and the contention on one bin.)  The
+//    same histograms say how many blocks the slices before ours take, so the
+//    places to write need no further exchange.
 // 3. Every warp counts, then writes, its own part of the slice in order.
+// 8 heads of 8192 blocks: 11.9 us, 10.8k of its 22k cycles before clusters of
+// 12 in the scores (8 CTAs a head read 3.6 TB/s; loads further ahead, and
+// prefetches to L2, took longer), a cluster barrier a pass in the rest.
 template <int G>
 __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams p, int C) {
   extern __shared__ uint32_t ids[];  // a slice: block ids, and behind them the keys
-  __shared__ uint32_t hist[kBins];
-  __shared__ uint32_t all_hist[2][kMaxCluster][kBins];  // by pass parity, every CTA's
+  __shared__ __align__(16) uint32_t hist[kBins];
+  __shared__ __align__(16) uint16_t all_hist[2][kMaxCluster][kBins];  // by pass parity, every CTA's
   __shared__ uint32_t all_range[kMaxCluster][2];   // largest ~key, largest key: unforced ones
   __shared__ uint32_t range[2];
   __shared__ int warp_cnt[2][kSelWarps];
@@ -324,7 +322,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
     const uint32_t blk = (uint32_t)__ldg(row + jlo + i);
     ids[i] = blk;
   }
-  if (tid < kBins) hist[tid] = 0;
+  hist[tid] = 0;
   if (tid < 2) range[tid] = 0;
   // The rounded queries: warp h takes head h (heads past G are zero).
   if (warp < 8) {
@@ -445,15 +443,21 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
     }
   }
   __syncthreads();
-  if (C > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-  if (tid < 2) push_all(&all_range[rank][tid], range[tid], C);
-  sync_all(C);
   // `need` of the unforced keys in [lo, hi] remain to be taken, largest first
   // (there are more unforced blocks than that).
-  uint32_t lo = 0, hi = 0;
-  for (int r = 0; r < C; ++r) {
-    lo = max(lo, all_range[r][0]);
-    hi = max(hi, all_range[r][1]);
+  uint32_t lo = range[0], hi = range[1];
+  if (C > 1) {
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (tid < 2 * C)
+      asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(
+                       peer_addr(&all_range[rank][tid & 1], tid >> 1)),
+                   "r"(range[tid & 1])
+                   : "memory");
+    sync_cluster();
+    for (int r = 0; r < C; ++r) {
+      lo = max(lo, all_range[r][0]);
+      hi = max(hi, all_range[r][1]);
+    }
   }
   lo = ~lo;
   int need = W - p.keep_first - p.keep_last;
@@ -471,38 +475,45 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
         atomicAdd(&hist[(k - lo) >> shift], 1u);
     }
     __syncthreads();
-    if (tid < kBins) {
-      // (this pass's half of all_hist was last read two passes ago, before the
-      // barrier that every CTA has passed since)
-      push_all(&all_hist[pass & 1][rank][tid], hist[tid], C);
-      hist[tid] = 0;
+    if (C > 1) {
+      // A warp sends all counts to one CTA, in 16 bits (a slice's fit), eight a
+      // lane.  (This pass's half of all_hist was last read two passes ago,
+      // before the barrier that every CTA has passed since.)
+      for (int r = warp; r < C; r += kSelWarps) {
+        const uint4 x = *reinterpret_cast<const uint4 *>(&hist[8 * lane]);
+        const uint4 y = *reinterpret_cast<const uint4 *>(&hist[8 * lane + 4]);
+        asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                         peer_addr(&all_hist[pass & 1][rank][8 * lane], r)),
+                     "r"(x.x | x.y << 16), "r"(x.z | x.w << 16), "r"(y.x | y.y << 16),
+                     "r"(y.z | y.w << 16)
+                     : "memory");
+      }
+      sync_cluster();
     }
-    sync_all(C);
     const int bin = kBins - 1 - tid;
     // (two counts below 2^16: of all slices, and of the ones before ours)
-    uint32_t cnt = 0, sum = 0;
-    if (tid < kBins) {
-      for (int r = 0; r < C; ++r) cnt += all_hist[pass & 1][r][bin] * (r < rank ? 0x10001u : 1u);
-      sum = cnt;
+    uint32_t cnt = 0;
+    if (C == 1) cnt = hist[bin];
+    for (int r = 0; C > 1 && r < C; ++r)
+      cnt += all_hist[pass & 1][r][bin] * (r < rank ? 0x10001u : 1u);
+    hist[bin] = 0;
+    uint32_t sum = cnt;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t v = __shfl_up_sync(kFullMask, sum, o);
-        if (lane >= o) sum += v;
-      }
-      if (lane == 31) warp_cnt[0][warp] = (int)sum;
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t v = __shfl_up_sync(kFullMask, sum, o);
+      if (lane >= o) sum += v;
     }
+    if (lane == 31) warp_cnt[0][warp] = (int)sum;
     __syncthreads();
-    if (tid < kBins) {
-      for (int w = 0; w < warp; ++w) sum += (uint32_t)warp_cnt[0][w];
-      const uint32_t over = sum - cnt;  // in higher bins
-      const int n_over = (int)(over & 0xffffu), n_bin = (int)(cnt & 0xffffu);
-      if (n_over < need && n_over + n_bin >= need) {  // this bin holds the need-th largest
-        found[0] = bin;
-        found[1] = need - n_over;
-        found[2] = n_bin;
-        found[3] = (int)(over >> 16);
-        found[4] = (int)(cnt >> 16);
-      }
+    for (int w = 0; w < warp; ++w) sum += (uint32_t)warp_cnt[0][w];
+    const uint32_t over = sum - cnt;  // in higher bins
+    const int n_over = (int)(over & 0xffffu), n_bin = (int)(cnt & 0xffffu);
+    if (n_over < need && n_over + n_bin >= need) {  // this bin holds the need-th largest
+      found[0] = bin;
+      found[1] = need - n_over;
+      found[2] = n_bin;
+      found[3] = (int)(over >> 16);
+      found[4] = (int)(cnt >> 16);
     }
     __syncthreads();
     need = found[1];
@@ -587,33 +598,65 @@ cudaError_t block_bounds_launch(const BoundsParams &p, cudaStream_t stream) {
 }
 
 // Blocks of a sequence that the selection holds keys for.
-int select_max_blocks() { return kMaxCluster * kSliceKeys; }
+int select_max_blocks() { return 8 * kSliceKeys; }
 
 // CTAs per (sequence, KV head): as many as fill the GPU once, but no more than
 // leave each 128 blocks (fewer are not worth the cluster barriers), and at
-// least as many as hold the keys.  At most 8: clusters of 16 do not all find
-// their place at once (8 heads of 8192 blocks took 29.8 us in clusters of 16,
-// 16.5 in 8, 21.5 in 4, 34.5 in 2, in an earlier form of this kernel).
-static int select_cluster(int units, int MB) {
+// least as many as hold the keys.  Past the portable 8 a cluster takes most of
+// a GPC, so only as many as are resident at once (`large`, asked for per
+// device) run side by side: 8 heads of 8192 blocks took 13.9 us in clusters of
+// 8, 12.7 in 12 and 20.5 in 16, of which 7 fit; 4 heads 14.8 in 8, 11.8 in 16.
+static int select_cluster(int units, int MB, const int (&large)[2]) {
+  for (int i = 0; i < 2; ++i)
+    if (units <= large[i] && units * kLarge[i] <= kSMs && MB >= kLarge[i] * 128) return kLarge[i];
   int C = 1;
-  while (C < kMaxCluster && units * C * 2 <= kSMs && MB >= C * 2 * 128) C *= 2;
+  while (C < 8 && units * C * 2 <= kSMs && MB >= C * 2 * 128) C *= 2;
   while (MB > C * kSliceKeys) C *= 2;
   return C;
 }
 
 template <int G>
 static cudaError_t launch_select(const SelectParams &p, cudaStream_t stream) {
-  static volatile int done[64] = {0};  // shared-memory limit raised, per device
+  // Per device: limits raised, large clusters that are resident at once.
+  static volatile int done[64] = {0};
+  static int large[64][2];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64 || !done[dev]) {
+  int now[2] = {0, 0};
+  if (dev >= 0 && dev < 64 && done[dev]) {
+    now[0] = large[dev][0];
+    now[1] = large[dev][1];
+  } else {
     e = cudaFuncSetAttribute(select_kernel<G>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)kAloneBytes);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(select_kernel<G>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
-    if (dev >= 0 && dev < 64) done[dev] = 1;
+    for (int i = 0; i < 2; ++i) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3((unsigned)kLarge[i]);
+      cfg.blockDim = dim3(kSelThreads);
+      cfg.dynamicSmemBytes = kAloneBytes;
+      cudaLaunchAttribute attr = {};
+      attr.id = cudaLaunchAttributeClusterDimension;
+      attr.val.clusterDim.x = (unsigned)kLarge[i];
+      attr.val.clusterDim.y = 1;
+      attr.val.clusterDim.z = 1;
+      cfg.attrs = &attr;
+      cfg.numAttrs = 1;
+      if (cudaOccupancyMaxActiveClusters(&now[i], select_kernel<G>, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        now[i] = 0;
+      }
+    }
+    if (dev >= 0 && dev < 64) {
+      large[dev][0] = now[0];
+      large[dev][1] = now[1];
+      done[dev] = 1;
+    }
   }
-  const int units = p.B * p.n_kv, C = select_cluster(units, p.MB);
+  const int units = p.B * p.n_kv, C = select_cluster(units, p.MB, now);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(units * C));
   cfg.blockDim = dim3(kSelThreads);
