@@ -13,18 +13,19 @@
 //   maximum and one sum per head; p.v with two dims a thread and every fourth
 //   token, V's scale folded into the probability; fp32, exact exp2;
 // - every CTA stores its maxima, sums and output dims into the shared memory of
-//   the CTAs that write them, and after one cluster barrier CTA r merges the
-//   C states of its 128 / C dims by log-sum-exp from its own memory
-//   (reading the peers' states instead takes a second barrier, before a CTA
-//   may exit, and the latency of the remote loads).
-// 8 heads x 2048 tokens, G = 4: 7.3 us (10.5 on the tensor cores; 4096 tokens
+//   the CTAs that write them, counted on a barrier of the receiver, and CTA r
+//   merges the C states of its 128 / C dims by log-sum-exp from its own memory
+//   (a cluster barrier instead takes 0.3 us more; reading the peers' states, a
+//   second barrier before a CTA may exit and the latency of the loads).
+// 8 heads x 2048 tokens, G = 4: 7.0 us (10.4 on the tensor cores; 4096 tokens
 // in 16 CTAs of 512 threads: 13.2 against 11.2).
-// 8 heads x 512 tokens, G = 4: 4.0 us (5.1 in pieces of 64 tokens with a table
+// 8 heads x 512 tokens, G = 4: 3.9 us (5.1 in pieces of 64 tokens with a table
 // load behind the length and remote loads; 8.0 with eight threads a token, whose
 // reads of the query met in the same banks).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include "cluster.cuh"
 #include "kv_fp8b.cuh"
 
 namespace pgd {
@@ -38,12 +39,6 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
-}
-// Store into CTA `rank`'s shared memory at the place `local` has in ours.
-__device__ __forceinline__ void st_peer(float *local, uint32_t rank, float v) {
-  uint32_t remote;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_addr(local)), "r"(rank));
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(remote), "f"(v) : "memory");
 }
 
 // CL: CTAs per (sequence, KV head), one cluster.
@@ -62,15 +57,23 @@ __global__ void __launch_bounds__(THREADS) cluster_attention_kernel(const Attn8b
   __shared__ float red[2][NW][G];                           // per-warp maxima, sums
   __shared__ int tbl[MAXB];
   __shared__ float po[NTG][G][kHeadDim];                    // outputs of the token groups
-  __shared__ float in_m[CL][G], in_l[CL][G], in_o[CL][G][OD];  // written by the peers
+  // written by the peers: maxima and sums, outputs
+  __shared__ __align__(16) float2 in_ml[CL][G];
+  __shared__ __align__(16) float in_o[CL][G][OD];
+  __shared__ uint64_t arrived;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t rank = cluster_rank();
   const int unit = (int)blockIdx.x / CL;
   const int b = unit / p.n_kv, g = unit % p.n_kv;
-  // (every CTA of the cluster has started: waited for before the first store
-  // into another's shared memory)
-  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  // (every CTA of the cluster has started and has its barrier: waited for before
+  // the first store into another's shared memory)
+  if (tid == 0) {
+    mbar_init(&arrived, 1);
+    mbar_init_fence();
+    mbar_arrive_expect_tx(&arrived, sizeof(in_ml) + sizeof(in_o));
+  }
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   pdl_wait();
   pdl_launch_dependents();
   const int ctx = __ldg(p.ctx + b);
@@ -193,35 +196,41 @@ __global__ void __launch_bounds__(THREADS) cluster_attention_kernel(const Attn8b
   __syncthreads();
   // This CTA's state to the CTAs that merge it.
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-  for (int i = tid; i < G * kHeadDim; i += THREADS) {
-    const int h = i / kHeadDim, d = i % kHeadDim;
-    const float o = (po[0][h][d] + po[1][h][d]) + (po[2][h][d] + po[3][h][d]);
-    st_peer(&in_o[rank][h][d % OD], (uint32_t)(d / OD), o);
+  for (int i = tid; i < G * (kHeadDim / 4); i += THREADS) {
+    const int h = i / (kHeadDim / 4), d = i % (kHeadDim / 4) * 4;
+    uint32_t o[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      o[k] = __float_as_uint((po[0][h][d + k] + po[1][h][d + k]) +
+                             (po[2][h][d + k] + po[3][h][d + k]));
+    send16(&in_o[rank][h][d % OD], &arrived, (uint32_t)(d / OD), o[0], o[1], o[2], o[3]);
   }
-  if (tid < CL * G) {
-    const int h = tid / CL, r = tid % CL;
+  if (tid >= THREADS - CL * G) {
+    const int i = THREADS - 1 - tid, h = i / CL, r = i % CL;
     float l = 0.f, m = red[0][0][h];
     for (int w = 0; w < NW; ++w) {
       l += red[1][w][h];
       m = fmaxf(m, red[0][w][h]);
     }
-    st_peer(&in_m[rank][h], (uint32_t)r, m);
-    st_peer(&in_l[rank][h], (uint32_t)r, l);
+    send8(&in_ml[rank][h], &arrived, (uint32_t)r, __float_as_uint(m), __float_as_uint(l));
   }
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
-               "barrier.cluster.wait.acquire.aligned;" ::: "memory");
   if (tid < OD * G) {
     const int h = tid / OD, d = tid % OD;
-    float M = in_m[0][h];
+    if (!wait_for_peers(&arrived, 0)) {
+      atomicOr(p.err, PGD_DEVERR_TIMEOUT);
+      wait_to_leave();
+      return;
+    }
+    float M = in_ml[0][h].x;
 #pragma unroll
-    for (int k = 1; k < CL; ++k) M = fmaxf(M, in_m[k][h]);
+    for (int k = 1; k < CL; ++k) M = fmaxf(M, in_ml[k][h].x);
     float num = 0.f, den = 0.f;
     if (M != -INFINITY) {
 #pragma unroll
       for (int k = 0; k < CL; ++k) {
-        const float w = in_m[k][h] == -INFINITY ? 0.f : exp2f(in_m[k][h] - M);
+        const float w = in_ml[k][h].x == -INFINITY ? 0.f : exp2f(in_ml[k][h].x - M);
         num = fmaf(w, in_o[k][h][d], num);
-        den = fmaf(w, in_l[k][h], den);
+        den = fmaf(w, in_ml[k][h].y, den);
       }
     }
     p.out[((size_t)b * p.n_q + g * G + h) * kHeadDim + rank * OD + d] =
