@@ -19,6 +19,9 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
+
+#include "cluster.cuh"
 #include "kv_fp8b.cuh"
 
 namespace pgd {
@@ -218,21 +221,6 @@ __device__ __forceinline__ uint32_t order_key(float f) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// Barrier over the cluster's CTAs: shared-memory writes before it, into any
-// CTA's, are visible behind it.
-__device__ __forceinline__ void sync_cluster() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
-               "barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// The place in CTA r's shared memory that `local` is in ours.
-__device__ __forceinline__ uint32_t peer_addr(const void *local, int r) {
-  uint32_t remote;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
-               : "=r"(remote)
-               : "r"(smem_addr(local)), "r"(r));
-  return remote;
-}
-
 // D += A B, m16n8k16, f16 operands, fp32 accumulation.
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -272,12 +260,15 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
 // 8 heads of 8192 blocks: 11.9 us, 10.8k of its 22k cycles before clusters of
 // 12 in the scores (8 CTAs a head read 3.6 TB/s; loads further ahead, and
 // prefetches to L2, took longer), a cluster barrier a pass in the rest.
-template <int G>
-__global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams p, int C) {
+template <int G, bool CLUSTER>
+__global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams p, int cluster) {
+  const int C = CLUSTER ? cluster : 1;
   extern __shared__ uint32_t ids[];  // a slice: block ids, and behind them the keys
   __shared__ __align__(16) uint32_t hist[kBins];
-  __shared__ __align__(16) uint16_t all_hist[2][kMaxCluster][kBins];  // by pass parity, every CTA's
-  __shared__ uint32_t all_range[kMaxCluster][2];   // largest ~key, largest key: unforced ones
+  // by pass parity, every CTA's
+  __shared__ __align__(16) uint16_t all_hist[2][CLUSTER ? kMaxCluster : 1][kBins];
+  __shared__ __align__(8) uint32_t all_range[CLUSTER ? kMaxCluster : 1][2];  // largest ~key, key: unforced ones
+  __shared__ uint64_t range_bar, hist_bar[2];  // the peers' ranges, counts (by pass parity)
   __shared__ uint32_t range[2];
   __shared__ int warp_cnt[2][kSelWarps];
   __shared__ int found[5];
@@ -312,9 +303,17 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
     for (int i = me; i < W; i += nthr) tiles[i] = i < nblk ? tile_of(__ldg(row + i)) : -1;
     return;
   }
-  // (every CTA of the cluster has started: waited for before the first store
-  // into another's shared memory)
-  if (C > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  // (every CTA of the cluster has started and has its barriers: waited for
+  // before the first store into another's shared memory)
+  if constexpr (CLUSTER) {
+    if (tid == 0) {
+      mbar_init(&range_bar, 1);
+      mbar_init(&hist_bar[0], 1);
+      mbar_init(&hist_bar[1], 1);
+      mbar_init_fence();
+    }
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  }
   const int per = (nblk + C - 1) / C;
   const int jlo = min(nblk, rank * per), n = min(nblk, jlo + per) - jlo;
   uint32_t *keys = ids + per;
@@ -443,17 +442,24 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
     }
   }
   __syncthreads();
+  bool failed = false;  // a wait for the peers gave up: the CTA leaves at its next barrier
+  auto sync_failed = [&] {
+    if constexpr (CLUSTER) return __syncthreads_or(failed) != 0;
+    __syncthreads();
+    return false;
+  };
+  auto gave_up = [&] {
+    if (tid == 0) atomicOr(p.err, PGD_DEVERR_TIMEOUT);
+    wait_to_leave();
+  };
   // `need` of the unforced keys in [lo, hi] remain to be taken, largest first
   // (there are more unforced blocks than that).
   uint32_t lo = range[0], hi = range[1];
-  if (C > 1) {
+  if constexpr (CLUSTER) {
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-    if (tid < 2 * C)
-      asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(
-                       peer_addr(&all_range[rank][tid & 1], tid >> 1)),
-                   "r"(range[tid & 1])
-                   : "memory");
-    sync_cluster();
+    if (tid == 0) mbar_arrive_expect_tx(&range_bar, C * 8);
+    if (tid < C) send8(all_range[rank], &range_bar, tid, lo, hi);
+    failed = !wait_for_peers(&range_bar, 0);
     for (int r = 0; r < C; ++r) {
       lo = max(lo, all_range[r][0]);
       hi = max(hi, all_range[r][1]);
@@ -474,29 +480,29 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
       if (k >= lo && k <= hi && j >= p.keep_first && j < nblk - p.keep_last)
         atomicAdd(&hist[(k - lo) >> shift], 1u);
     }
-    __syncthreads();
-    if (C > 1) {
+    if (sync_failed()) return gave_up();
+    if constexpr (CLUSTER) {
       // A warp sends all counts to one CTA, in 16 bits (a slice's fit), eight a
       // lane.  (This pass's half of all_hist was last read two passes ago,
       // before the barrier that every CTA has passed since.)
       for (int r = warp; r < C; r += kSelWarps) {
         const uint4 x = *reinterpret_cast<const uint4 *>(&hist[8 * lane]);
         const uint4 y = *reinterpret_cast<const uint4 *>(&hist[8 * lane + 4]);
-        asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
-                         peer_addr(&all_hist[pass & 1][rank][8 * lane], r)),
-                     "r"(x.x | x.y << 16), "r"(x.z | x.w << 16), "r"(y.x | y.y << 16),
-                     "r"(y.z | y.w << 16)
-                     : "memory");
+        send16(&all_hist[pass & 1][rank][8 * lane], &hist_bar[pass & 1], r, x.x | x.y << 16,
+               x.z | x.w << 16, y.x | y.y << 16, y.z | y.w << 16);
       }
-      sync_cluster();
+      if (tid == 0) mbar_arrive_expect_tx(&hist_bar[pass & 1], C * (uint32_t)sizeof(all_hist[0][0]));
+      failed = !wait_for_peers(&hist_bar[pass & 1], (uint32_t)(pass >> 1) & 1u);
     }
     const int bin = kBins - 1 - tid;
     // (two counts below 2^16: of all slices, and of the ones before ours)
     uint32_t cnt = 0;
-    if (C == 1) cnt = hist[bin];
-    for (int r = 0; C > 1 && r < C; ++r)
-      cnt += all_hist[pass & 1][r][bin] * (r < rank ? 0x10001u : 1u);
-    hist[bin] = 0;
+    if constexpr (CLUSTER) {
+      for (int r = 0; r < C; ++r)
+        cnt += all_hist[pass & 1][r][bin] * (r < rank ? 0x10001u : 1u);
+    } else {
+      cnt = hist[bin];
+    }
     uint32_t sum = cnt;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -504,7 +510,8 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
       if (lane >= o) sum += v;
     }
     if (lane == 31) warp_cnt[0][warp] = (int)sum;
-    __syncthreads();
+    if (sync_failed()) return gave_up();
+    hist[bin] = 0;  // (every warp has read and sent it)
     for (int w = 0; w < warp; ++w) sum += (uint32_t)warp_cnt[0][w];
     const uint32_t over = sum - cnt;  // in higher bins
     const int n_over = (int)(over & 0xffffu), n_bin = (int)(cnt & 0xffffu);
@@ -553,7 +560,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
     warp_cnt[0][warp] = n_above;
     warp_cnt[1][warp] = n_equal;
   }
-  __syncthreads();
+  if (sync_failed()) return gave_up();
   // Next output place, and equal keys still to be taken.
   if (!all) inside = min(inside, need);
   int at = before + inside, left = need - (all ? 0 : inside);
@@ -615,48 +622,57 @@ static int select_cluster(int units, int MB, const int (&large)[2]) {
   return C;
 }
 
+static cudaLaunchAttribute cluster_of(int n) {
+  cudaLaunchAttribute a = {};
+  a.id = cudaLaunchAttributeClusterDimension;
+  a.val.clusterDim.x = (unsigned)n;
+  a.val.clusterDim.y = 1;
+  a.val.clusterDim.z = 1;
+  return a;
+}
+
+// A kernel's limits raised on the current device.
+template <class Kernel>
+static cudaError_t raise_limits(Kernel kernel) {
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)kAloneBytes);
+  return e != cudaSuccess
+             ? e
+             : cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+}
+
 template <int G>
 static cudaError_t launch_select(const SelectParams &p, cudaStream_t stream) {
-  // Per device: limits raised, large clusters that are resident at once.
-  static volatile int done[64] = {0};
-  static int large[64][2];
+  // Per device, once: both kernels' limits raised (bit 16), and the large
+  // clusters that are resident at once (bits 0-7, 8-15).
+  static std::atomic<int> known[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  int now[2] = {0, 0};
-  if (dev >= 0 && dev < 64 && done[dev]) {
-    now[0] = large[dev][0];
-    now[1] = large[dev][1];
-  } else {
-    e = cudaFuncSetAttribute(select_kernel<G>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)kAloneBytes);
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(select_kernel<G>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return e;
+  int state = dev >= 0 && dev < 64 ? known[dev].load() : 0;
+  if (!state) {
+    if ((e = raise_limits(select_kernel<G, true>)) != cudaSuccess) return e;
+    if ((e = raise_limits(select_kernel<G, false>)) != cudaSuccess) return e;
+    state = 1 << 16;
     for (int i = 0; i < 2; ++i) {
       cudaLaunchConfig_t cfg = {};
       cfg.gridDim = dim3((unsigned)kLarge[i]);
       cfg.blockDim = dim3(kSelThreads);
       cfg.dynamicSmemBytes = kAloneBytes;
-      cudaLaunchAttribute attr = {};
-      attr.id = cudaLaunchAttributeClusterDimension;
-      attr.val.clusterDim.x = (unsigned)kLarge[i];
-      attr.val.clusterDim.y = 1;
-      attr.val.clusterDim.z = 1;
+      cudaLaunchAttribute attr = cluster_of(kLarge[i]);
       cfg.attrs = &attr;
       cfg.numAttrs = 1;
-      if (cudaOccupancyMaxActiveClusters(&now[i], select_kernel<G>, &cfg) != cudaSuccess) {
+      int n = 0;
+      if (cudaOccupancyMaxActiveClusters(&n, select_kernel<G, true>, &cfg) != cudaSuccess) {
         cudaGetLastError();
-        now[i] = 0;
+        n = 0;
       }
+      state |= n << (8 * i);
     }
-    if (dev >= 0 && dev < 64) {
-      large[dev][0] = now[0];
-      large[dev][1] = now[1];
-      done[dev] = 1;
-    }
+    if (dev >= 0 && dev < 64) known[dev].store(state);
   }
-  const int units = p.B * p.n_kv, C = select_cluster(units, p.MB, now);
+  const int large[2] = {state & 255, state >> 8 & 255};
+  const int units = p.B * p.n_kv, C = select_cluster(units, p.MB, large);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(units * C));
   cfg.blockDim = dim3(kSelThreads);
@@ -668,13 +684,11 @@ static cudaError_t launch_select(const SelectParams &p, cudaStream_t stream) {
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = (unsigned)C;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
+  attr[1] = cluster_of(C);
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, select_kernel<G>, p, C);
+  cfg.numAttrs = C > 1 ? 2 : 1;
+  return C > 1 ? cudaLaunchKernelEx(&cfg, select_kernel<G, true>, p, C)
+               : cudaLaunchKernelEx(&cfg, select_kernel<G, false>, p, C);
 }
 
 cudaError_t select_blocks_launch(const SelectParams &p, int G, cudaStream_t stream) {
