@@ -116,7 +116,7 @@ static_assert(40 + 4 * NSR <= 112 && OFF_MISC % 16 == 0, "misc layout");
 // the whole of it: 0.58 us a stage).
 constexpr float kShare = 126.f;
 template <int BS> constexpr float kBlockBytes = 2.f * BS * kHeadDim;
-constexpr int MERGE_U = 20;  // parts of a unit that a merging thread has in flight
+constexpr int MERGE_U = 5;  // parts of a unit that a merging warp has in flight
 
 // kind::f8f6f4, D f32, A and B E4M3, both MN-major, M = 128.
 __host__ __device__ constexpr uint32_t idesc_pv(int n) {
@@ -390,45 +390,90 @@ __device__ __forceinline__ void write_query(const uint4 (&q)[kPieces<G>], unsign
 }
 
 // A unit's partial states (unit, first part, parts) merged by log-sum-exp into
-// its output rows by the whole CTA: a quarter of it takes every fourth head,
-// thread e dim e, the loads of MERGE_U parts in flight together.
+// its output rows by the whole CTA.  Warp w takes head w % G and every
+// (16 / G)-th part: lane i holds the weight of its i-th part, four dims a lane,
+// the loads of MERGE_U parts and of the weights in flight together; the warps'
+// states then meet in shared memory.  (19 parts of 4 heads by a thread for each
+// dim, which computes every weight itself: 4400 cycles.)
 template <int G>
-__device__ __forceinline__ void merge_unit(const AttnParams &p, const int4 &m, int tid) {
-  const int e = tid & 127;
-  const size_t row0 = ((size_t)m.x + (size_t)m.y) * G;
-  const size_t obase = q_index(p, m.x / p.n_kv, m.x % p.n_kv, 0);
+__device__ __forceinline__ void merge_unit(const AttnParams &p, const int4 &m, float *scratch,
+                                           int tid) {
+  constexpr int NG = NTHREADS / 32 / G;  // warps a head
+  constexpr int ROW = kHeadDim + 4;      // a warp's outputs, maximum, sum
+  const int lane = tid & 31, warp = tid >> 5, h = warp % G, first = warp / G;
+  const size_t row0 = ((size_t)m.x + (size_t)m.y) * G + h;
+  float M = -INFINITY, L = 0.f;
+  float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-  for (int h = tid >> 7; h < G; h += NTHREADS / 128) {
-    float M = -INFINITY, L = 0.f, O = 0.f;
+  for (int c0 = first; c0 < m.z; c0 += 32 * NG) {
+    const int cnt = min(32, (m.z - c0 + NG - 1) / NG);
+    float4 o[MERGE_U];
+    auto load = [&](int j0) {
+#pragma unroll
+      for (int k = 0; k < MERGE_U; ++k) {
+        o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (j0 + k < cnt)
+          o[k] = __ldcg(reinterpret_cast<const float4 *>(
+                            p.part_o + (row0 + (size_t)(c0 + NG * (j0 + k)) * G) * kHeadDim) +
+                        lane);
+      }
+    };
+    float2 ml = make_float2(-INFINITY, 0.f);
+    if (lane < cnt)
+      ml = __ldcg(reinterpret_cast<const float2 *>(p.part_ml) + row0 +
+                  (size_t)(c0 + NG * lane) * G);
+    load(0);
+    float mx = ml.x;
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFullMask, mx, x));
+    mx = fmaxf(mx, M);
+    const float c = M == -INFINITY ? 0.f : exp2f(M - mx);
+    const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - mx);
+    float l = f * ml.y;
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) l += __shfl_xor_sync(kFullMask, l, x);
+    L = fmaf(L, c, l);
+    M = mx;
+    O.x *= c, O.y *= c, O.z *= c, O.w *= c;
 #pragma unroll 1
-    for (int i0 = 0; i0 < m.z; i0 += MERGE_U) {
-      float2 ml[MERGE_U];
-      float o[MERGE_U];
+    for (int j0 = 0;;) {
 #pragma unroll
-      for (int i = 0; i < MERGE_U; ++i) {
-        ml[i] = make_float2(-INFINITY, 0.f);
-        o[i] = 0.f;
-        if (i0 + i < m.z) {
-          const size_t row = row0 + (size_t)(i0 + i) * G + h;
-          ml[i] = __ldcg(reinterpret_cast<const float2 *>(p.part_ml) + row);
-          o[i] = __ldcg(p.part_o + row * kHeadDim + e);
-        }
+      for (int k = 0; k < MERGE_U; ++k) {
+        const float fk = __shfl_sync(kFullMask, f, j0 + k);  // (past cnt: o is 0)
+        O.x = fmaf(fk, o[k].x, O.x);
+        O.y = fmaf(fk, o[k].y, O.y);
+        O.z = fmaf(fk, o[k].z, O.z);
+        O.w = fmaf(fk, o[k].w, O.w);
       }
-      float mx = M;
-#pragma unroll
-      for (int i = 0; i < MERGE_U; ++i) mx = fmaxf(mx, ml[i].x);
-      const float c = M == -INFINITY ? 0.f : exp2f(M - mx);
-      L *= c;
-      O *= c;
-      M = mx;
-#pragma unroll
-      for (int i = 0; i < MERGE_U; ++i) {
-        const float f = ml[i].x == -INFINITY ? 0.f : exp2f(ml[i].x - mx);
-        L = fmaf(f, ml[i].y, L);
-        O = fmaf(f, o[i], O);
-      }
+      if ((j0 += MERGE_U) >= cnt) break;
+      load(j0);
     }
-    p.out[(obase + h) * kHeadDim + e] = __float2bfloat16_rn(O / L);
+  }
+  float *mine = scratch + warp * ROW;
+  *reinterpret_cast<float4 *>(mine + 4 * lane) = O;
+  if (lane == 0) {
+    mine[kHeadDim] = M;
+    mine[kHeadDim + 1] = L;
+  }
+  __syncthreads();
+  const size_t obase = q_index(p, m.x / p.n_kv, m.x % p.n_kv, 0) * kHeadDim;
+#pragma unroll
+  for (int i = 0; i < (G * kHeadDim + NTHREADS - 1) / NTHREADS; ++i) {
+    const int at = tid + i * NTHREADS;
+    if (at >= G * kHeadDim) break;
+    const float *s = scratch + at / kHeadDim * ROW;
+    float mx = s[kHeadDim];
+#pragma unroll
+    for (int k = 1; k < NG; ++k) mx = fmaxf(mx, s[k * G * ROW + kHeadDim]);
+    float num = 0.f, den = 0.f;
+#pragma unroll
+    for (int k = 0; k < NG; ++k) {
+      const float *r = s + k * G * ROW;
+      const float f = r[kHeadDim] == -INFINITY ? 0.f : exp2f(r[kHeadDim] - mx);
+      den = fmaf(f, r[kHeadDim + 1], den);
+      num = fmaf(f, r[at % kHeadDim], num);
+    }
+    p.out[obase + at] = __float2bfloat16_rn(num / den);
   }
 }
 
@@ -994,7 +1039,11 @@ attention_fp8b_kernel(const __grid_constant__ Params pr) {
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  for (int i = 0; i < *n_merges; ++i) merge_unit<G>(p, merges[i], tid);
+  // (nothing lands in the K ring any more)
+  for (int i = 0; i < *n_merges; ++i) {
+    if (i) __syncthreads();
+    merge_unit<G>(p, merges[i], reinterpret_cast<float *>(smem + OFF_K), tid);
+  }
   if (warp == WARP_QK) {
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
                  "r"(TMEM_COLS8)
