@@ -49,6 +49,21 @@ __device__ __forceinline__ float2 widen2(uint32_t a) {
   return make_float2(bf16lo(a), bf16hi(a));
 }
 
+// 16 bytes that this SM reads once, or zeros: past L1, whose lines a
+// long stream would only churn.
+// (Predicated in the text: a branch around each load would keep the loads of a
+// sequence from being in flight together.)
+__device__ __forceinline__ uint4 load_once(const uint4 *p, bool there) {
+  uint4 v;
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+      "@q ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+      : "l"(p), "r"((uint32_t)there));
+  return v;
+}
+
 // The bounds of one tile by one warp.  Lane l takes slot l % 8 of every 8-token
 // group and the 16-byte chunks l / 8, l / 8 + 4, ..., so that a load
 // instruction reads 512 contiguous bytes.  Per chunk it keeps the least k and
@@ -57,7 +72,7 @@ __device__ __forceinline__ float2 widen2(uint32_t a) {
 // halves: a lane keeps one half of the values and sends the other, and ends
 // with the lower bounds (l % 8 < 4) or the negated upper bounds (l % 8 >= 4)
 // of a few dims over all tokens.  Bound by the read of the keys.
-template <int BS, bool FP8>
+template <int BS, bool FP8, bool STREAM>
 __device__ __forceinline__ void tile_bounds(const BoundsParams &p, size_t tile, int valid,
                                             int lane) {
   constexpr int NG = BS / 8;             // 8-token groups
@@ -74,8 +89,14 @@ __device__ __forceinline__ void tile_bounds(const BoundsParams &p, size_t tile, 
   for (int i = 0; i < NG; ++i)
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      x[i][c] = make_uint4(0, 0, 0, 0);
-      if (8 * i + slot < valid) x[i][c] = __ldg(base + i * (NC * 32) + c * 32);
+      const uint4 *at = base + i * (NC * 32) + c * 32;
+      const bool there = 8 * i + slot < valid;
+      if constexpr (STREAM) {
+        x[i][c] = load_once(at, there);
+      } else {
+        x[i][c] = make_uint4(0, 0, 0, 0);
+        if (there) x[i][c] = __ldg(at);
+      }
     }
   float scale = 1.f;
   if constexpr (FP8) scale = __ldg(p.k_scales + tile);
@@ -152,17 +173,17 @@ __device__ __forceinline__ void tile_bounds(const BoundsParams &p, size_t tile, 
   if (lane == 0) p.bound_scales[tile] = pow2f(e);
 }
 
-// One warp per run of up to 32 blocks of a (sequence, KV head).
-template <int BS, bool FP8>
+// One warp per run of up to 32 blocks of a (sequence, KV head).  STREAM: many
+// tiles, read past L1 (20 prompts: 25.7 us, 27.5 through it; 48 tiles the other
+// way round: 2.6 and 2.2).
+template <int BS, bool FP8, bool STREAM>
 __global__ void __launch_bounds__(kBoundWarps * 32)
 bounds_kernel(const BoundsParams p, int runs, int run) {
   pdl_wait();
   pdl_launch_dependents();
-  const long long id = (long long)blockIdx.x * kBoundWarps + (threadIdx.x >> 5);
+  const int r = (int)blockIdx.x * kBoundWarps + (int)(threadIdx.x >> 5), b = (int)blockIdx.y;
   const int lane = threadIdx.x & 31;
-  const long long per_b = (long long)runs * p.n_kv;
-  if (id >= per_b * p.B) return;
-  const int b = (int)(id / per_b), r = (int)(id % per_b);
+  if (r >= runs * p.n_kv) return;
   const int jrel = r / p.n_kv * run, g = r % p.n_kv;
   const int ctx = __ldg(p.ctx + b), p0 = p.pos ? __ldg(p.pos + b) : 0;
   const bool first = jrel == 0 && g == 0 && lane == 0;
@@ -181,7 +202,7 @@ bounds_kernel(const BoundsParams p, int runs, int run) {
   for (int i = 0; i < n; ++i) {
     const int blk = __shfl_sync(kFullMask, mine, i);
     if ((unsigned)blk < (unsigned)p.NB)
-      tile_bounds<BS, FP8>(p, (size_t)blk * p.n_kv + g, min(BS, ctx - (j0 + i) * BS), lane);
+      tile_bounds<BS, FP8, STREAM>(p, (size_t)blk * p.n_kv + g, min(BS, ctx - (j0 + i) * BS), lane);
     else if (g == 0 && lane == 0)
       atomicOr(p.err, PGD_DEVERR_BAD_BLOCK_ID);
   }
@@ -585,6 +606,17 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
 
 }  // namespace
 
+template <bool FP8>
+static cudaError_t bounds_form(const BoundsParams &p, dim3 grid, int runs, int run,
+                               cudaStream_t stream) {
+  constexpr int nt = kBoundWarps * 32;
+  if (p.bs == 16)
+    return run > 1 ? launch_pdl(bounds_kernel<16, FP8, true>, grid, nt, 0, stream, p, runs, run)
+                   : launch_pdl(bounds_kernel<16, FP8, false>, grid, nt, 0, stream, p, runs, run);
+  return run > 1 ? launch_pdl(bounds_kernel<32, FP8, true>, grid, nt, 0, stream, p, runs, run)
+                 : launch_pdl(bounds_kernel<32, FP8, false>, grid, nt, 0, stream, p, runs, run);
+}
+
 cudaError_t block_bounds_launch(const BoundsParams &p, cudaStream_t stream) {
   if (p.B == 0 || p.T == 0) return cudaSuccess;
   // Blocks a warp takes one after another: one for a few (latency), four for
@@ -592,16 +624,11 @@ cudaError_t block_bounds_launch(const BoundsParams &p, cudaStream_t stream) {
   // is paid once for four tiles.
   const int JM = most_blocks(p.T, p.bs, p.MB);
   const int run = (long long)p.B * JM * p.n_kv > 16384 ? 4 : 1, runs = (JM + run - 1) / run;
-  const long long items = (long long)p.B * runs * p.n_kv;
-  const long long grid = (items + kBoundWarps - 1) / kBoundWarps;
-  if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
-  const dim3 gd((unsigned)grid);
-  const int nt = kBoundWarps * 32;
-  if (p.k_scales)
-    return p.bs == 16 ? launch_pdl(bounds_kernel<16, true>, gd, nt, 0, stream, p, runs, run)
-                      : launch_pdl(bounds_kernel<32, true>, gd, nt, 0, stream, p, runs, run);
-  return p.bs == 16 ? launch_pdl(bounds_kernel<16, false>, gd, nt, 0, stream, p, runs, run)
-                    : launch_pdl(bounds_kernel<32, false>, gd, nt, 0, stream, p, runs, run);
+  const long long grid = ((long long)runs * p.n_kv + kBoundWarps - 1) / kBoundWarps;
+  if (grid * kBoundWarps > 0x7fffffffLL) return cudaErrorInvalidValue;
+  const dim3 gd((unsigned)grid, (unsigned)p.B);
+  return p.k_scales ? bounds_form<true>(p, gd, runs, run, stream)
+                    : bounds_form<false>(p, gd, runs, run, stream);
 }
 
 // Blocks of a sequence that the selection holds keys for.
