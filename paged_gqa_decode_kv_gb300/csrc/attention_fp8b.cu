@@ -159,14 +159,26 @@ struct Piece {  // blocks j0 .. j0 + n - 1 of the nblk of unit (b, g), at cost [
   int b, g, j0, nblk, n, ucs, uce;
 };
 
+// A CTA's place in its part: what is left of it, and the last unit.
 struct Walk {
   int x, end, b, g;
 };
-__device__ __forceinline__ void walk_start(const Cuts &sc, Walk &w) {
-  w.b = -1;
-  w.g = 0;
+// Largest b with n_kv * pre[b] <= x.  Out of line: one copy for all roles.
+__device__ __noinline__ int find_sequence(const int *pre, int n_kv, int B, int x) {
+  int lo = 0, hi = B - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (n_kv * pre[mid] <= x) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+// (g: one before the first unit)
+__device__ __forceinline__ void walk_start(const Cuts &sc, int B, Walk &w) {
   w.x = (int)min((long long)sc.X, (long long)blockIdx.x * sc.S);
   w.end = (int)min((long long)sc.X, (long long)w.x + sc.S);
+  if (w.x >= w.end) return;
+  w.b = find_sequence(sc.pre, sc.n_kv, B, w.x);
+  w.g = (w.x - sc.n_kv * sc.pre[w.b]) / (sc.pre[w.b + 1] - sc.pre[w.b]) - 1;
 }
 // Part c of a split into whole units: unit c, if it has blocks.
 __device__ __forceinline__ bool whole_unit(const Cuts &sc, int b, Piece &sg) {
@@ -181,21 +193,15 @@ __device__ __forceinline__ bool whole_unit(const Cuts &sc, int b, Piece &sg) {
   sg.uce = sg.ucs + cost;
   return cost > 0;
 }
-// The next segment.  Out of line: one copy for all roles instead of one for
-// each, whose first instructions every call would fetch anew.
-__device__ __noinline__ bool walk_next(const int *pre, int n_kv, int ov, int B, Walk &w,
+// The next segment.  (Inlined into every role, its state in registers: out of
+// line the state went through local memory, 3000 cycles at every change of unit.)
+__device__ __forceinline__ bool walk_next(const int *pre, int n_kv, int ov, int B, Walk &w,
                                           Piece &sg) {
+#pragma unroll 1
   while (w.x < w.end) {
-    if (w.b < 0) {
-      int lo = 0, hi = B - 1;  // largest b with n_kv * pre[b] <= x
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (n_kv * pre[mid] <= w.x) lo = mid; else hi = mid - 1;
-      }
-      w.b = lo;
-      w.g = (w.x - n_kv * pre[lo]) / (pre[lo + 1] - pre[lo]);
-    } else if (++w.g == n_kv) {
+    if (++w.g == n_kv) {
       w.g = 0;
+#pragma unroll 1
       do { ++w.b; } while (w.b < B - 1 && pre[w.b + 1] == pre[w.b]);
     }
     const int cost = pre[w.b + 1] - pre[w.b];
@@ -674,7 +680,7 @@ attention_fp8b_kernel(const __grid_constant__ Params pr) {
     have = whole_unit(sc, unit_b, sg);
   } else {
     sc.S = sc.P > 0 ? (sc.X + sc.P - 1) / sc.P : 1;
-    walk_start(sc, walk);
+    walk_start(sc, p.B, walk);
     have = walk_next(pre, sc.n_kv, sc.ov, p.B, walk, sg);
   }
   if ((warp == WARP_KP || warp == WARP_VP) && have && !(sg.b == guess_b && sg.j0 == 0))
