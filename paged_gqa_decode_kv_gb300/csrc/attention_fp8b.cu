@@ -36,11 +36,14 @@
 // times a residual of x stays within E4M3's 448.
 //
 // Roles (512 threads): warps 0-3 and 12-15 softmax (thread t = token row t),
-// 4 / 5 K / V producers, 6 query conversion and q.k^T issuer, 7 p.v issuer,
-// 8-11 epilogue.  The two softmax groups take alternate stages, each with a reference, sums and an
-// accumulator of its own that the epilogue merges: a stage's chain (barrier,
-// tensor-memory load, vote, exponentials, conversions) is longer than the time
-// HBM takes to deliver a stage, so one group alone sets the pace.  The K
+// 4 / 5 K / V producers, 6 q.k^T issuer, 7 p.v issuer, 8-11 query conversion,
+// a segment ahead, and epilogue.  (The issuer's warp converting a query when its
+// segment began held up the tensor cores: 51 contexts of 1800 tokens, G = 8:
+// 51.8 us, 46.1 so.)  The two softmax groups take alternate stages, each with a
+// reference, sums and an accumulator of its own that the epilogue merges: a
+// stage's chain (barrier, tensor-memory load, vote, exponentials, conversions)
+// is longer than the time HBM takes to deliver a stage, so one group alone sets
+// the pace.  The K
 // producer also fetches both scales of every block of a stage into a 16-stage
 // ring by 4-byte asynchronous copies that count on the stage's own barrier, so
 // no warp waits for a dependent load.
@@ -49,7 +52,7 @@
 // copy is on the path of every call (6 us of it at first), so it is kept to
 // the context lengths, one scan, 32-bit arithmetic and the block ids, which
 // are guessed and loaded beside the lengths; the query is converted beside the
-// first copies, by the warp that needs it.
+// first copies.
 #include <cuda.h>
 
 #include <atomic>
@@ -99,7 +102,7 @@ constexpr int OFF_RED = OFF_BAR + 512;                 // f32 [group][2][4][8] w
 constexpr int OFF_LRED = OFF_RED + 2 * 2 * 4 * 8 * 4;  // f32 [2][group][4][8] warp sums
 constexpr int OFF_MREF = OFF_LRED + 2 * 2 * 4 * 8 * 4;  // f32 [2][group][8] references
 constexpr int OFF_QS = OFF_MREF + 2 * 2 * 8 * 4;           // f32 [NQS][8] query scales
-constexpr int NQS = 8;  // (the issuer is at most NSB + 1 segments ahead of the softmax)
+constexpr int NQS = 2;  // (by segment parity, like the queries)
 constexpr int OFF_MISC = OFF_QS + NQS * 8 * 4;
 constexpr int OFF_PRE = OFF_MISC + 256;                // int [B + 1]
 
@@ -351,45 +354,33 @@ __device__ __forceinline__ void produce(const Params &pr, const Cuts &sc, Walk w
   }
 }
 
-// A segment's query rows by one warp: 16-byte pieces lane + 32 i, piece c of
-// row r; then as E4M3 high parts in rows 0-7 and low parts in rows 8-15 of
-// the B operand, with one power-of-two scale a head.
-template <int G> constexpr int kPieces = (16 * G + 31) / 32;
+// A segment's query rows by the 128 epilogue threads: thread e takes 16 bytes
+// (piece c of row r) and writes them as E4M3, high parts in rows 0-7 and low
+// parts in rows 8-15 of the B operand, with one power-of-two scale a head.
 template <int G>
-__device__ __forceinline__ void load_query(const AttnParams &p, const Piece &g, int lane,
-                                           uint4 (&q)[kPieces<G>]) {
+__device__ __forceinline__ void convert_query(const AttnParams &p, const Piece &g,
+                                              unsigned char *qdst, float *qscale, int e) {
+  const int r = e >> 4, c = e & 15;
+  uint4 q = make_uint4(0, 0, 0, 0);
+  if (r < G)
+    q = __ldg(reinterpret_cast<const uint4 *>(p.q + q_index(p, g.b, g.g, r) * kHeadDim + c * 8));
+  float f[8];
+  unpack8(q, f);
+  float a = 0.f;
 #pragma unroll
-  for (int i = 0; i < kPieces<G>; ++i) {
-    const int j = lane + 32 * i, r = j >> 4, c = j & 15;
-    q[i] = j < 16 * G ? __ldg(reinterpret_cast<const uint4 *>(
-                            p.q + q_index(p, g.b, g.g, r) * kHeadDim + c * 8))
-                      : make_uint4(0, 0, 0, 0);
-  }
-}
-template <int G>
-__device__ __forceinline__ void write_query(const uint4 (&q)[kPieces<G>], unsigned char *qdst,
-                                            float *qscale, int lane) {
+  for (int i = 0; i < 8; ++i) a = fmaxf(a, fabsf(f[i]));
 #pragma unroll
-  for (int i = 0; i < kPieces<G>; ++i) {
-    const int j = lane + 32 * i, r = j >> 4, c = j & 15;
-    float f[8];
-    unpack8(q[i], f);
-    float a = 0.f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) a = fmaxf(a, fabsf(f[e]));
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(kFullMask, a, o));
-    // the scale 2^(e - 7), e the largest element's exponent: the elements
-    // keep their bits and the largest lands in [128, 256)
-    const int e = max((int)((__float_as_uint(a) >> 23) & 0xffu) - 127, -119);
-    if (j < 16 * G) {
-      uint2 hi, lo;
-      q_hi_lo(q[i], pow2f(7 - e), hi, lo);
-      const int off = (c >> 1) * 128 + (c & 1) * 8;
-      *reinterpret_cast<uint2 *>(qdst + r * 16 + off) = hi;
-      *reinterpret_cast<uint2 *>(qdst + 8 * 128 + r * 16 + off) = lo;
-      if (c == 0) qscale[r] = pow2f(e - 7);
-    }
+  for (int o = 8; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(kFullMask, a, o));
+  // the scale 2^(x - 7), x the largest element's exponent: the elements
+  // keep their bits and the largest lands in [128, 256)
+  const int x = max((int)((__float_as_uint(a) >> 23) & 0xffu) - 127, -119);
+  if (r < G) {
+    uint2 hi, lo;
+    q_hi_lo(q, pow2f(7 - x), hi, lo);
+    const int off = (c >> 1) * 128 + (c & 1) * 8;
+    *reinterpret_cast<uint2 *>(qdst + r * 16 + off) = hi;
+    *reinterpret_cast<uint2 *>(qdst + 8 * 128 + r * 16 + off) = lo;
+    if (c == 0) qscale[r] = pow2f(x - 7);
   }
   fence_proxy_async();
   __syncwarp();
@@ -511,6 +502,7 @@ attention_fp8b_kernel(const __grid_constant__ Params pr) {
   uint64_t *o_free = o_full + 2;        // [2]
   uint64_t *done = o_free + 2;          // [2]
   uint64_t *seg_done = done + 2;        // [2]
+  uint64_t *q_ready = seg_done + 2;     // [2]
   float *red = reinterpret_cast<float *>(smem + OFF_RED);
   float *lred = reinterpret_cast<float *>(smem + OFF_LRED);
   float *mref = reinterpret_cast<float *>(smem + OFF_MREF);
@@ -533,7 +525,7 @@ attention_fp8b_kernel(const __grid_constant__ Params pr) {
     // Arrivals a barrier expects, in the order of the arrays above: 33 = the
     // producer's and each lane's scale copies, 4 and 8 = softmax or epilogue
     // warps.
-    constexpr int N_BARS = 2 * NSK + 2 * NSV + 3 * NSB + 6 * 2;
+    constexpr int N_BARS = 2 * NSK + 2 * NSV + 3 * NSB + 7 * 2;
     static_assert(N_BARS * 8 <= 512, "barriers");
     for (int i = lane; i < N_BARS; i += 32) {
       constexpr int S0 = 2 * NSK + 2 * NSV, P0 = S0 + 3 * NSB;
@@ -542,7 +534,8 @@ attention_fp8b_kernel(const __grid_constant__ Params pr) {
       else if (i >= S0 + NSB && i < S0 + 2 * NSB) n = 4;  // s_free
       else if (i >= P0 && i < P0 + 2) n = 4;            // p_full
       else if (i >= P0 + 6 && i < P0 + 8) n = 4;        // o_free
-      else if (i >= P0 + 10) n = 8;                     // seg_done
+      else if (i >= P0 + 10 && i < P0 + 12) n = 8;      // seg_done
+      else if (i >= P0 + 12) n = 4;                     // q_ready
       mbar_init(&bars[i], n);
     }
     mbar_init_fence();
@@ -694,26 +687,15 @@ attention_fp8b_kernel(const __grid_constant__ Params pr) {
     produce<BS, false>(pr, sc, walk, sg, have, guess, smem, full_v, empty_v, nullptr, abort_flag,
                        policy, lane);
   } else if (warp == WARP_QK) {
-    // ------------------------------ query conversion, then q.k^T (one lane)
-    Piece nsg;
-    uint4 q[kPieces<G>];
-    if (have) load_query<G>(p, sg, lane, q);
-    int slot = 0;
-    uint32_t phase = 0;
-    int s = 0, k = 0, last1 = -1, last2 = -1;  // last stages of segments k - 1, k - 2
-    while (have) {
-      const int nstages = (sg.n + SB - 1) / SB;
-      // Query buffer k % 2 was read by the MMAs of segment k - 2: they are done
-      // if the softmax has freed their last S buffer for a stage since, else
-      // that buffer's barrier is still in their phase.
-      if (last2 >= 0 && last1 - last2 < NSB)
-        wait_or_abort(&s_full[last2 % NSB], (uint32_t)(last2 / NSB) & 1u, abort_flag, p.err);
-      unsigned char *qbuf = smem + OFF_Q + (k & 1) * Q_BYTES;
-      write_query<G>(q, qbuf, qscale + (k & (NQS - 1)) * 8, lane);
-      const bool have_next = next(nsg);
-      if (have_next) load_query<G>(p, nsg, lane, q);
-      if (lane == 0) {
-        const uint64_t qd = smem_desc(smem_addr(qbuf), 128, 1024, 0);
+    // ------------------------------------------------------ q.k^T issuer
+    if (lane == 0) {
+      int s = 0, k = 0, slot = 0;
+      uint32_t phase = 0;
+      while (have) {
+        const int nstages = (sg.n + SB - 1) / SB;
+        wait_or_abort(&q_ready[k & 1], (uint32_t)(k >> 1) & 1u, abort_flag, p.err);
+        const uint64_t qd =
+            smem_desc(smem_addr(smem + OFF_Q + (k & 1) * Q_BYTES), 128, 1024, 0);
         for (int st = 0; st < nstages; ++st) {
           const int su = s + st, sb = su % NSB;
           wait_or_abort(&full_k[slot], phase, abort_flag, p.err);
@@ -738,18 +720,14 @@ attention_fp8b_kernel(const __grid_constant__ Params pr) {
             phase ^= 1u;
           }
         }
+        s += nstages;
+        ++k;
+        have = next(sg);
       }
-      __syncwarp();
-      s += nstages;
-      last2 = last1;
-      last1 = s - 1;
-      ++k;
-      sg = nsg;
-      have = have_next;
-    }
-    if (lane == 0 && s > 0) {
-      umma_commit(&done[0]);
-      mbar_wait_bounded(&done[0], 0);
+      if (s > 0) {
+        umma_commit(&done[0]);
+        mbar_wait_bounded(&done[0], 0);
+      }
     }
   } else if (warp == WARP_PV) {
     // ------------------------------------------------------- p.v issuer
@@ -982,8 +960,18 @@ attention_fp8b_kernel(const __grid_constant__ Params pr) {
     const uint32_t lane_base = (uint32_t)(ew * 32) << 16;
     constexpr int NET = 128;
     const int part = (int)blockIdx.x;
+    // Query buffer k % 2 for segment k, one segment ahead: its last readers, the
+    // MMAs of segment k - 2, were done before that segment's epilogue.
+    auto convert = [&](const Piece &g, int k) {
+      convert_query<G>(p, g, smem + OFF_Q + (k & 1) * Q_BYTES, qscale + (k & (NQS - 1)) * 8, e);
+      if (lane == 0) mbar_arrive(&q_ready[k & 1]);
+    };
+    if (have) convert(sg, 0);
     int k = 0;
-    for (; have; have = next(sg)) {
+    while (have) {
+      Piece nsg;
+      const bool have_next = next(nsg);
+      if (have_next) convert(nsg, k + 1);
       const int ob = k & 1;
       const int unit = sg.b * p.n_kv + sg.g;
       wait_or_abort(&seg_done[ob], (uint32_t)(k >> 1) & 1u, abort_flag, p.err);
@@ -1055,6 +1043,8 @@ attention_fp8b_kernel(const __grid_constant__ Params pr) {
         }
       }
       ++k;
+      sg = nsg;
+      have = have_next;
     }
   }
 
