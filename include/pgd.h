@@ -507,9 +507,8 @@ pgd_status pgd_append_decode_attention_fp8(void *out, const void *q, const void 
  * E4M3 terms, a probability (times V's scale) as three, to 2^-12 of itself and
  * 2^-24 of the largest; scales, softmax and accumulation in fp32; bf16 output.
  * An automatic call (num_splits = 0) of few heads and at most 1024 tokens (the
- * limit of pgd_set_short_context_tokens; twice that with at most 12 (sequence,
- * KV head) pairs, 16 with at most two query heads each) runs on the CUDA cores
- * in fp32.
+ * limit of pgd_set_short_context_tokens, or twice that with fewer heads still)
+ * runs on the CUDA cores in fp32.
  *
  * workspace: device scratch of pgd_block_workspace_size(...) bytes (0 for
  * arguments outside the limits), 256-byte aligned, zero-filled before its first

@@ -1384,17 +1384,18 @@ pgd_status pgd_kv_read_fp8b(void *k_out, void *v_out, const void *k_cache, const
 // Whether an automatic call goes to the cluster kernel instead of the
 // tensor-core one: short contexts and few units, fewer with more query heads to
 // a unit, each of which costs its CTAs time.  Device time of the two in us,
-// 16-token blocks: 8 units x 512 tokens, G = 4: 4.2 / 6.9; 32 x 1024, G = 4: 7.1
-// / 11.6; 48 x 512, G = 4: 8.1 / 7.4; 64 x 512, G = 2: 6.2 / 7.1; 64 x 1024, G =
-// 2: 9.1 / 9.0; 96 x 64, G = 1: 6.4 / 5.9; 24 x 1024, G = 8: 9.9 / 14.6; 32 x 512,
-// G = 8: 9.3 / 8.5.  Twice the tokens take clusters of 16, of which fewer are
-// resident at once: 8 x 2048, G = 4: 7.3 / 10.5; 12 x 2048: 7.3 / 10.7 (G = 8:
-// 10.5 / 14.3); 16 x 2048, G = 2: 7.3 / 9.9, G = 4: 12.9 / 11.1; 24 x 2048, G =
-// 1: 11.9 / 9.5.
+// 16-token blocks: 8 units x 512 tokens, G = 4: 3.9 / 5.7; 32 x 1024, G = 4: 6.7
+// / 9.4; 64 x 512, G = 2: 6.0 / 6.2; 24 x 1024, G = 8: 9.5 / 9.8; past the rule
+// 48 x 512, G = 4: 8.1 / 6.4; 64 x 1024, G = 2: 9.1 / 8.3; 96 x 64, G = 1: 6.4 /
+// 4.5; 32 x 512, G = 8: 9.3 / 7.0.  Twice the tokens take clusters of 16, of
+// which fewer are resident at once: 16 x 2048, G = 2: 7.2 / 8.9; 12 x 2048, G =
+// 4: 7.0 / 9.1; 4 x 2048, G = 8: 7.4 / 9.4; past the rule 24 x 2048, G = 1: 11.9
+// / 8.5; 16 x 2048, G = 4: 12.9 / 9.4; 12 x 2048, G = 8: 13.6 / 10.1.
 static bool cluster_rule(long long units, int G, long long tokens, int32_t num_splits) {
   const long long limit = std::min(g_short_tokens.load(), 1024);
   if (num_splits != 0 || tokens > 2 * limit || units > 64) return false;
-  if (tokens > limit) return units <= (G <= 2 ? 16 : 12) && tokens <= cluster_max_tokens();
+  if (tokens > limit)
+    return units <= (G <= 2 ? 16 : G == 4 ? 12 : 4) && tokens <= cluster_max_tokens();
   return units <= (G <= 2 ? 64 : G == 4 ? 32 : 24) && units * tokens <= 32768;
 }
 

@@ -43,10 +43,9 @@
 // reference, sums and an accumulator of its own that the epilogue merges: a
 // stage's chain (barrier, tensor-memory load, vote, exponentials, conversions)
 // is longer than the time HBM takes to deliver a stage, so one group alone sets
-// the pace.  The K
-// producer also fetches both scales of every block of a stage into a 16-stage
-// ring by 4-byte asynchronous copies that count on the stage's own barrier, so
-// no warp waits for a dependent load.
+// the pace.  The K producer also fetches both scales of every block of a stage
+// into a 16-stage ring by 4-byte asynchronous copies that count on the stage's
+// own barrier, so no warp waits for a dependent load.
 //
 // Start.  What lies between the wait for the previous kernel and the first
 // copy is on the path of every call (6 us of it at first), so it is kept to

@@ -260,7 +260,7 @@ def test_attention_ragged(G, bs):
 @pytest.mark.parametrize("G", [1, 2, 4, 8])
 @pytest.mark.parametrize("n_kv, bs, ctx", [
     (4, 16, [2048, 1, 129]), (3, 32, [1025, 2033, 16]), (12, 16, [1023]), (13, 16, [1900]),
-    (16, 32, [1200]), (1, 16, [2049, 700]),
+    (16, 32, [1200]), (1, 16, [2049, 700]), (2, 32, [1999, 1300]),
 ])
 def test_attention_at_the_limits_of_short_contexts(n_kv, bs, ctx, G, limit):
     """Sizes on both sides of every bound of the kernel for short contexts, and of each of its
