@@ -278,9 +278,10 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
 //    same histograms say how many blocks the slices before ours take, so the
 //    places to write need no further exchange.
 // 3. Every warp counts, then writes, its own part of the slice in order.
-// 8 heads of 8192 blocks: 11.9 us, 10.8k of its 22k cycles before clusters of
-// 12 in the scores (8 CTAs a head read 3.6 TB/s; loads further ahead, and
-// prefetches to L2, took longer), a cluster barrier a pass in the rest.
+// 8 heads of 8192 blocks: 11.7 us, in clusters of 12; 7.8k of its 21k cycles go
+// to the scores (29 bytes a cycle and SM; loads further ahead, and prefetches
+// to L2, took longer), about 2k to each of three exchanges.  16 x 8 heads of 512
+// blocks: 7.9 us, the scores at 5 TB/s.
 template <int G, bool CLUSTER>
 __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams p, int cluster) {
   const int C = CLUSTER ? cluster : 1;

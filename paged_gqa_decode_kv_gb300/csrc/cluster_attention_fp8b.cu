@@ -17,7 +17,7 @@
 //   merges the C states of its 128 / C dims by log-sum-exp from its own memory
 //   (a cluster barrier instead takes 0.3 us more; reading the peers' states, a
 //   second barrier before a CTA may exit and the latency of the loads).
-// 8 heads x 2048 tokens, G = 4: 7.0 us (10.4 on the tensor cores; 4096 tokens
+// 8 heads x 2048 tokens, G = 4: 7.0 us (8.7 on the tensor cores; 4096 tokens
 // in 16 CTAs of 512 threads: 13.2 against 11.2).
 // 8 heads x 512 tokens, G = 4: 3.9 us (5.1 in pieces of 64 tokens with a table
 // load behind the length and remote loads; 8.0 with eight threads a token, whose
