@@ -520,6 +520,23 @@ def test_select_of_a_long_context(n):
     assert torch.equal(tokens.cpu(), wn) and torch.equal(tiles.cpu(), want)
 
 
+@pytest.mark.parametrize("n_kv", [1, 2, 4, 8])
+@pytest.mark.parametrize("W, first, last, ties", [(7, 2, 5, False), (37, 0, 1, True),
+                                                 (400, 260, 100, True), (2000, 1, 1, False)])
+def test_select_in_clusters_of_every_size(n_kv, W, first, last, ties):
+    """A wide table (16, 12, 8 and 4 CTAs a head) and contexts that leave slices empty, that end
+    in the first one and that are selected whole; forced blocks over several slices."""
+    ctx = [40000, 300, 640, 16 * 401]
+    c, bounds, scales, q = _select_inputs(ctx, n_kv, 2, 16, seed=W + n_kv, ties=ties)
+    tiles = torch.full((4, n_kv, W), 99, dtype=torch.int32, device="cuda")
+    tokens = torch.full((4, n_kv), 99, dtype=torch.int32, device="cuda")
+    want, wn = _want_tiles(c, _chosen(c, q, bounds, scales, W, first, last), W)
+    args = (q.cuda(), bounds.cuda(), scales.cuda(), c.tables.cuda(), _i32(ctx), first, last, 16)
+    for _ in range(3):
+        pgd.select_blocks(tiles, tokens, *args)
+        assert torch.equal(tokens.cpu(), wn) and torch.equal(tiles.cpu(), want)
+
+
 def test_select_zero_and_extreme_queries():
     """A zero query (every score 0: the first blocks), queries of tiny and of huge values."""
     ctx = [900, 900, 900]
