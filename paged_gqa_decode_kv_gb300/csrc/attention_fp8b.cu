@@ -70,6 +70,7 @@ struct Params {
   Attn8bParams q8;
   float split_root;  // parts of a split by its cost X: split_root * sqrt(X)
   float inv_units;   // 1 / (B * n_kv)
+  float starts;      // B * n_kv * kSegCost
   CUtensorMap k_map, v_map;
 };
 
@@ -655,10 +656,14 @@ attention_fp8b_kernel(const __grid_constant__ Params pr) {
     float root;
     asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(root) : "f"(X));
     const int P = max(1, min(sc.P, (int)(pr.split_root * root)));
-    const float cost_cut = fmaxf(__fdividef(X, (float)P) * kShare, X) + m0 +
+    // (what HBM has to deliver is without the units' starts, and so is a CTA's
+    // only unit, which begins as the call does)
+    const float bytes = X - pr.starts;
+    const float cost_cut = fmaxf(__fdividef(X, (float)P) * kShare, bytes) + m0 +
                            m1 * ceilf((float)P * pr.inv_units);
     sc.P = P;
-    if (U <= (int)gridDim.x && fmaxf((float)longest * kShare, X) <= cost_cut) {
+    if (U <= (int)gridDim.x &&
+        fmaxf(fmaf((float)longest, kShare, -kSegCost<BS> * kShare), bytes) <= cost_cut) {
       sc.units = true;
       sc.P = U;
     }
@@ -1127,6 +1132,7 @@ cudaError_t attention_fp8b_launch(const Attn8bParams &q8, int G, int bs, int gri
   const float block = bs == 16 ? tc8b::kBlockBytes<16> : tc8b::kBlockBytes<32>;
   p.split_root = sqrtf(tc8b::kShare * units * block / (float)tc::kMergePartBytes);
   p.inv_units = 1.f / units;
+  p.starts = units * (float)(bs == 16 ? tc::kSegCost<16> : tc::kSegCost<32>);
   if (bs == 16) {
     const long long tiles = (long long)q8.a.NB * q8.a.n_kv;
     cudaError_t e = tc8b::encode_map(&p.k_map, q8.a.k_cache, tiles);
