@@ -29,8 +29,8 @@ namespace {
 
 constexpr int kBoundWarps = 4;
 
-// Least of each of two packed numbers, passing over a NaN beside a number:
-// f16 (widened 8-bit codes) or bf16.
+// Least (largest) of each of two packed numbers, passing over a NaN beside a
+// number: f16 (widened 8-bit codes) or bf16.
 template <bool FP8>
 __device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
   if constexpr (FP8) {
@@ -44,13 +44,25 @@ __device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
   }
 }
 template <bool FP8>
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+  if constexpr (FP8) {
+    const __half2 r = __hmax2(*reinterpret_cast<const __half2 *>(&a),
+                              *reinterpret_cast<const __half2 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&r);
+  } else {
+    const __nv_bfloat162 r = __hmax2(*reinterpret_cast<const __nv_bfloat162 *>(&a),
+                                     *reinterpret_cast<const __nv_bfloat162 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&r);
+  }
+}
+template <bool FP8>
 __device__ __forceinline__ float2 widen2(uint32_t a) {
   if constexpr (FP8) return __half22float2(*reinterpret_cast<const __half2 *>(&a));
   return make_float2(bf16lo(a), bf16hi(a));
 }
 
-// 16 bytes that this SM reads once, or zeros: past L1, whose lines a
-// long stream would only churn.
+// 16 bytes that this SM reads once, or zeros: past L1, whose lines a long stream
+// would only churn.
 // (Predicated in the text: a branch around each load would keep the loads of a
 // sequence from being in flight together.)
 __device__ __forceinline__ uint4 load_once(const uint4 *p, bool there) {
@@ -64,33 +76,36 @@ __device__ __forceinline__ uint4 load_once(const uint4 *p, bool there) {
   return v;
 }
 
-// The bounds of one tile by one warp.  Lane l takes slot l % 8 of every 8-token
-// group and the 16-byte chunks l / 8, l / 8 + 4, ..., so that a load
-// instruction reads 512 contiguous bytes.  Per chunk it keeps the least k and
-// the least -k of each dim in the storage's own precision (bf16, or f16 for
-// widened codes: exact); the eight lanes of a chunk then reduce them by
-// halves: a lane keeps one half of the values and sends the other, and ends
-// with the lower bounds (l % 8 < 4) or the negated upper bounds (l % 8 >= 4)
-// of a few dims over all tokens.  Bound by the read of the keys.
+// The bounds of one tile by one warp.  Lane l takes slots l % 4 and l % 4 + 4 of
+// every 8-token group and the 16-byte chunks l / 4, l / 4 + 8, so that a load
+// instruction reads whole 64-byte pieces.  Per chunk it keeps the least and the
+// largest k of each dim in the storage's own precision (bf16, or f16 for
+// widened codes: exact); the four lanes of a chunk then reduce the least and
+// the negated largest by halves: a lane keeps one half of the values and sends
+// the other, and ends with the lower bounds (l % 4 < 2) or the negated upper
+// bounds of a few dims over all tokens.  Bound by the read of the keys (bf16)
+// and by issue slots (8-bit): 84k tokens of bf16 23.7 us, 115k of 8 bits and 10
+// heads 34.8.  (One slot a lane, eight lanes a chunk: 25.7 and 43.0, of which
+// the minimum of -k instead of the maximum 0.6 and 2.9.)
 template <int BS, bool FP8, bool STREAM>
 __device__ __forceinline__ void tile_bounds(const BoundsParams &p, size_t tile, int valid,
                                             int lane) {
-  constexpr int NG = BS / 8;             // 8-token groups
-  constexpr int NC = FP8 ? 2 : 4;        // chunks of a lane
+  constexpr int NT = BS / 4;             // tokens of a lane: its slot of every half group
+  constexpr int NC = FP8 ? 1 : 2;        // chunks of a lane
   constexpr int ND2 = FP8 ? 8 : 4;       // pairs of dims in a chunk
-  constexpr int NW = ND2 / 4;            // pairs of a chunk that a lane ends with
+  constexpr int NW = ND2 / 2;            // pairs of a chunk that a lane ends with
   constexpr uint32_t kSign = 0x80008000u, kInf = FP8 ? 0x7c007c00u : 0x7f807f80u;
-  const int slot = lane & 7, cl = lane >> 3;
+  const int slot = lane & 3, cl = lane >> 2;
   // (chunks of a group are 8 slots x 16 bytes apart, groups follow each other)
   const uint4 *base = reinterpret_cast<const uint4 *>(p.k_cache) +
                       tile * (size_t)(BS * (FP8 ? 8 : 16)) + cl * 8 + slot;
-  uint4 x[NG][NC];
+  uint4 x[NT][NC];
 #pragma unroll
-  for (int i = 0; i < NG; ++i)
+  for (int i = 0; i < NT; ++i)
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      const uint4 *at = base + i * (NC * 32) + c * 32;
-      const bool there = 8 * i + slot < valid;
+      const uint4 *at = base + (i >> 1) * (NC * 64) + c * 64 + (i & 1) * 4;
+      const bool there = 4 * i + slot < valid;
       if constexpr (STREAM) {
         x[i][c] = load_once(at, there);
       } else {
@@ -103,12 +118,12 @@ __device__ __forceinline__ void tile_bounds(const BoundsParams &p, size_t tile, 
   uint32_t out[NC][NW];
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
-    uint32_t v[2 * ND2];  // least k of the chunk's pairs, then least -k
+    uint32_t v[2 * ND2];  // least k of the chunk's pairs, then the largest, negated below
 #pragma unroll
-    for (int k = 0; k < 2 * ND2; ++k) v[k] = kInf;
+    for (int k = 0; k < 2 * ND2; ++k) v[k] = k < ND2 ? kInf : kInf | kSign;
 #pragma unroll
-    for (int i = 0; i < NG; ++i)
-      if (8 * i + slot < valid) {
+    for (int i = 0; i < NT; ++i)
+      if (4 * i + slot < valid) {
         const uint32_t w[4] = {x[i][c].x, x[i][c].y, x[i][c].z, x[i][c].w};
 #pragma unroll
         for (int k = 0; k < ND2; ++k) {
@@ -118,11 +133,13 @@ __device__ __forceinline__ void tile_bounds(const BoundsParams &p, size_t tile, 
             y = *reinterpret_cast<const uint32_t *>(&h);
           }
           v[k] = min2<FP8>(v[k], y);
-          v[ND2 + k] = min2<FP8>(v[ND2 + k], y ^ kSign);
+          v[ND2 + k] = max2<FP8>(v[ND2 + k], y);
         }
       }
 #pragma unroll
-    for (int m = 2 * ND2, off = 4; off > 0; m >>= 1, off >>= 1) {
+    for (int k = ND2; k < 2 * ND2; ++k) v[k] ^= kSign;
+#pragma unroll
+    for (int m = 2 * ND2, off = 2; off > 0; m >>= 1, off >>= 1) {
       const bool up = (slot & off) != 0;
 #pragma unroll
       for (int k = 0; k < m / 2; ++k) {
@@ -134,8 +151,8 @@ __device__ __forceinline__ void tile_bounds(const BoundsParams &p, size_t tile, 
     for (int k = 0; k < NW; ++k) out[c][k] = v[k];
   }
   // Largest finite bound, the scale, and this lane's bounds: dims
-  // chunk * 2 ND2 + (slot % 4) * 2 NW .. of the lower or upper ones.
-  const bool upper = slot >= 4;
+  // chunk * 2 ND2 + (slot % 2) * 2 NW .. of the lower or upper ones.
+  const bool upper = slot >= 2;
   float amax = 0.f;
 #pragma unroll
   for (int c = 0; c < NC; ++c)
@@ -149,33 +166,34 @@ __device__ __forceinline__ void tile_bounds(const BoundsParams &p, size_t tile, 
   const int e = scale_exponent_int8(amax);
   const float inv = pow2f(-e);
   signed char *dst = p.bounds + tile * (2 * kHeadDim) + (upper ? kHeadDim : 0) +
-                     cl * 2 * ND2 + (slot & 3) * 2 * NW;
+                     cl * 2 * ND2 + (slot & 1) * 2 * NW;
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
-    uint32_t w = 0;
+    uint32_t w[NW / 2];
 #pragma unroll
     for (int k = 0; k < NW; ++k) {
       const float2 y = widen2<FP8>(out[c][k]);
       float f[2] = {y.x * scale, y.y * scale};
+      if ((k & 1) == 0) w[k / 2] = 0;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         // (floor of -max is -ceil(max))
         int n = (int)fminf(fmaxf(floorf(f[i] * inv), -127.f), 127.f);
         if (upper) n = -n;
-        w |= (uint32_t)(n & 0xff) << (16 * k + 8 * i);
+        w[k / 2] |= (uint32_t)(n & 0xff) << (16 * (k & 1) + 8 * i);
       }
     }
     if constexpr (FP8)
-      *reinterpret_cast<uint32_t *>(dst + c * 8 * ND2) = w;
+      *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
     else
-      *reinterpret_cast<uint16_t *>(dst + c * 8 * ND2) = (uint16_t)w;
+      *reinterpret_cast<uint32_t *>(dst + c * 16 * ND2) = w[0];
   }
   if (lane == 0) p.bound_scales[tile] = pow2f(e);
 }
 
 // One warp per run of up to 32 blocks of a (sequence, KV head).  STREAM: many
-// tiles, read past L1 (20 prompts: 25.7 us, 27.5 through it; 48 tiles the other
-// way round: 2.6 and 2.2).
+// tiles, read past L1 (20 prompts: 7 % faster; 48 x 8 tiles: 2.6 us, 2.2 through
+// it).
 template <int BS, bool FP8, bool STREAM>
 __global__ void __launch_bounds__(kBoundWarps * 32)
 bounds_kernel(const BoundsParams p, int runs, int run) {
