@@ -131,8 +131,8 @@ __host__ __device__ constexpr uint32_t idesc_pv(int n) {
 __device__ __forceinline__ void copy4_async(uint32_t dst, const void *src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
-// Four 2 KiB tiles into `dst`, one behind the other: rows t0 .. t3 of the pool as a two-dimensional tensor.  A row outside
-// the pool arrives as zeros.
+// Four 2 KiB tiles into `dst`, one behind the other: rows t0 .. t3 of the pool
+// as a two-dimensional tensor.  A row outside the pool arrives as zeros.
 __device__ __forceinline__ void gather_tiles(void *dst, const CUtensorMap *map, int t0, int t1,
                                              int t2, int t3, uint64_t *bar, uint64_t policy) {
   asm volatile(
@@ -1006,7 +1006,8 @@ attention_fp8b_kernel(const __grid_constant__ Params pr) {
 #pragma unroll
         for (int h = 0; h < G; ++h) {
           const float f = grp ? f1[h] : f0[h];
-          const float x = fmaf(fmaf(o[2 * TSTEP + h], 1.f / kTerm, o[TSTEP + h]), 1.f / kTerm, o[h]);
+          const float x =
+              fmaf(fmaf(o[2 * TSTEP + h], 1.f / kTerm, o[TSTEP + h]), 1.f / kTerm, o[h]);
           const float y = f != 0.f ? x * (f * (1.f / kWeightUnit)) : 0.f;
           ov[h] = grp ? ov[h] + y : y;
         }

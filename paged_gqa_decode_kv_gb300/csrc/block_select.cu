@@ -307,7 +307,8 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
   __shared__ __align__(16) uint32_t hist[kBins];
   // by pass parity, every CTA's
   __shared__ __align__(16) uint16_t all_hist[2][CLUSTER ? kMaxCluster : 1][kBins];
-  __shared__ __align__(8) uint32_t all_range[CLUSTER ? kMaxCluster : 1][2];  // largest ~key, key: unforced ones
+  // (largest ~key and largest key of the unforced ones)
+  __shared__ __align__(8) uint32_t all_range[CLUSTER ? kMaxCluster : 1][2];
   __shared__ uint64_t range_bar, hist_bar[2];  // the peers' ranges, counts (by pass parity)
   __shared__ uint32_t range[2];
   __shared__ int warp_cnt[2][kSelWarps];
@@ -531,7 +532,8 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
         send16(&all_hist[pass & 1][rank][8 * lane], &hist_bar[pass & 1], r, x.x | x.y << 16,
                x.z | x.w << 16, y.x | y.y << 16, y.z | y.w << 16);
       }
-      if (tid == 0) mbar_arrive_expect_tx(&hist_bar[pass & 1], C * (uint32_t)sizeof(all_hist[0][0]));
+      if (tid == 0)
+        mbar_arrive_expect_tx(&hist_bar[pass & 1], C * (uint32_t)sizeof(all_hist[0][0]));
       failed = !wait_for_peers(&hist_bar[pass & 1], (uint32_t)(pass >> 1) & 1u);
     }
     const int bin = kBins - 1 - tid;
