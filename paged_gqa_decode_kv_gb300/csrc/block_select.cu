@@ -288,8 +288,8 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
 //    an eighth of its N.)
 // 2. The least selected score, by 256-way refinement of the range [least,
 //    largest] of the unforced keys: every CTA histograms its keys in the
-//    range, stores the counts in every CTA's shared memory and after a cluster
-//    barrier adds them up and keeps the bin that holds the wanted rank, until
+//    range, sends the counts into every CTA's shared memory and, once all have
+//    arrived, adds them up and keeps the bin that holds the wanted rank, until
 //    the bin is one value or all its keys are wanted.  (Starting from the
 //    range rather than from the keys' top byte, which is all but constant for
 //    scores of one query, saves a pass and the contention on one bin.)  The
