@@ -23,6 +23,7 @@
 
 #include "cluster.cuh"
 #include "kv_fp8b.cuh"
+#include "select_range.cuh"
 
 namespace pgd {
 namespace {
@@ -252,7 +253,8 @@ constexpr int kSMs = 152;          // of a GB300
 // Dynamic shared memory that leaves an SM room for one CTA.
 constexpr size_t kAloneBytes = 120 * 1024;
 constexpr int kSliceKeys = 6144;   // keys of a CTA's slice at most (24 KiB)
-constexpr int kBins = kSelThreads;  // a thread takes one
+constexpr int kBins = kRangeBins;
+static_assert(kBins == kSelThreads, "a thread takes a bin");
 
 // A float's bits as an unsigned integer of the same order.
 __device__ __forceinline__ uint32_t order_key(float f) {
@@ -513,8 +515,8 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
   // in [lo, hi] (read when this is the last range).
   const int forced = min(jlo, p.keep_first) + max(0, jlo - (nblk - p.keep_last));
   int before = forced, inside = jlo - forced;
-  for (int pass = 0; need > 0 && !all && lo != hi; ++pass) {
-    const int shift = max(0, 24 - __clz(hi - lo));
+  for (int pass = 0; pass < kRangePasses && need > 0 && !all && lo != hi; ++pass) {
+    const int shift = range_shift(lo, hi);
     for (int i = tid; i < n; i += kSelThreads) {
       const uint32_t k = keys[i];
       const int j = jlo + i;
@@ -569,8 +571,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
     all = found[2] == need;
     before += found[3];
     inside = found[4];
-    lo += (uint32_t)found[0] << shift;
-    hi = min(hi, lo + ((1u << shift) - 1u));
+    narrow_range(lo, hi, (uint32_t)found[0], shift);
   }
   // Above: forced, or a key above hi, or in [lo, hi] where all are wanted.
   // Equal: the rest of [lo, hi], one value, the first `need` of which are taken.
@@ -619,7 +620,8 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
     const unsigned eb = __ballot_sync(kFullMask, e);
     const bool sel = a || (e && __popc(eb & below) < left);
     const unsigned sb = __ballot_sync(kFullMask, sel);
-    if (sel) tiles[at + __popc(sb & below)] = tile_of((int)ids[i]);
+    const int place = at + __popc(sb & below);
+    if (sel && place < W) tiles[place] = tile_of((int)ids[i]);
     at += __popc(sb);
     left -= min(left, __popc(eb));
   }

@@ -1,0 +1,83 @@
+"""Block selection with scores at the ends of the range and beyond it."""
+import pytest
+import torch
+
+import block_scaled as bsc
+import paged_gqa_decode_kv_gb300 as pgd
+
+pytestmark = pytest.mark.gpu
+GUARD = 0x5A5A5A5A
+
+
+@pytest.fixture(autouse=True)
+def _clean_errors():
+    pgd.device_errors(clear=True)
+    yield
+    assert pgd.device_errors(clear=True) == 0
+
+
+def _case(ctx, n_kv, G, seed):
+    """Tables, bounds and scales as a cache of the given contexts has them, and a query."""
+    c = bsc.make_cache(ctx, n_kv, 16, fp8=False, seed=seed)
+    g = torch.Generator().manual_seed(seed)
+    lo = torch.randint(-127, 60, (c.k.shape[0], n_kv, 128), generator=g)
+    hi = torch.minimum(lo + torch.randint(0, 150, lo.shape, generator=g), torch.tensor(127))
+    scales = torch.exp2(torch.randint(-3, 2, lo.shape[:2], generator=g).float())
+    return c, torch.stack([lo, hi], 2).to(torch.int8), scales, bsc.make_query(len(ctx), n_kv * G,
+                                                                              seed=seed)
+
+
+def _select(c, q, bounds, scales, W, first, last):
+    """Tiles and tokens of a selection whose outputs lie between guard words."""
+    B, n = len(c.ctx), len(c.ctx) * c.n_kv * W
+    room = torch.full((n + 512,), GUARD, dtype=torch.int32, device="cuda")
+    tiles = room[256:256 + n].view(B, c.n_kv, W)
+    tokens = torch.full((B, c.n_kv), -7, dtype=torch.int32, device="cuda")
+    pgd.select_blocks(tiles, tokens, q.cuda(), bounds.cuda(), scales.cuda(), c.tables.cuda(),
+                      torch.tensor(c.ctx, dtype=torch.int32, device="cuda"), first, last, 16)
+    torch.cuda.synchronize()
+    assert (room[:256] == GUARD).all() and (room[256 + n:] == GUARD).all()
+    return tiles.cpu(), tokens.cpu()
+
+
+def _check_form(c, tiles, tokens, W, first, last):
+    """W different blocks of each context, in its order, the forced ones among them."""
+    for b, n in enumerate(c.ctx):
+        nblk = -(-n // 16)
+        place = {int(t): j for j, t in enumerate(c.tables[b, :nblk])}
+        for g in range(c.n_kv):
+            t = tiles[b, g]
+            assert (t % c.n_kv == g).all()
+            js = [place[int(x)] for x in t // c.n_kv]
+            assert js == sorted(set(js)) and len(js) == W
+            assert js[:first] == list(range(first))
+            assert js[W - last:] == list(range(nblk - last, nblk))
+            assert int(tokens[b, g]) == (W - 1) * 16 + n - (nblk - 1) * 16
+
+
+@pytest.mark.parametrize("G", [1, 2, 8])
+@pytest.mark.parametrize("ctx", [[1600, 1000], [8192, 5000], [40000, 9000]], ids=str)
+@pytest.mark.parametrize("W,first,last", [(20, 0, 1), (62, 2, 8)])
+def test_scores_of_queries_that_are_not_finite(ctx, G, W, first, last):
+    """One, some and all elements of a query infinite: many scores at the ends of the range beside
+    ordinary ones of the other sign.  A selection has its form and stays within its output."""
+    c, bounds, scales, q = _case(ctx, 2, G, seed=W + G)
+    for k, value in [(1, float("inf")), (40, float("-inf")), (128, float("inf")),
+                     (3, float("nan")), (128, 3.3e38)]:
+        x = q.clone()
+        x[0, :, :k] = value
+        x[1, 0, ::max(1, 128 // k)] = value
+        tiles, tokens = _select(c, x, bounds, scales, W, first, last)
+        _check_form(c, tiles, tokens, W, first, last)
+
+
+@pytest.mark.parametrize("value", [float("inf"), float("nan"), 3e38])
+@pytest.mark.parametrize("ctx", [[1600, 1000], [40000, 9000]], ids=str)
+def test_scores_of_bounds_that_were_never_made(ctx, value):
+    """Scales of blocks that hold whatever their memory held."""
+    c, bounds, scales, q = _case(ctx, 2, 2, seed=3)
+    g = torch.Generator().manual_seed(4)
+    for share in (0.02, 0.4, 1.0):
+        s = torch.where(torch.rand(scales.shape, generator=g) < share, torch.tensor(value), scales)
+        tiles, tokens = _select(c, q, bounds, s, 30, 1, 2)
+        _check_form(c, tiles, tokens, 30, 1, 2)
