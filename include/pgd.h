@@ -574,10 +574,14 @@ pgd_status pgd_append_decode_attention_fp8b(
  * max |q[b][h]| <= 127 f_h.  No key of a block that is left out has a larger
  * product with a rounded query than the smallest score selected.  tiles int32
  * [B][n_kv][W]: the selected tiles in the order of the sequence, then -1;
- * tile_tokens int32 [B][n_kv]: the tokens they hold.  The scores are exact in
- * fp32.  A bad context is flagged (PGD_DEVERR_BAD_CONTEXT) and selects
- * nothing (tile_tokens 0); a block with a bad id counts as the lowest score.
- * MB at most 49152.
+ * tile_tokens int32 [B][n_kv]: the tokens they hold.  The scores are compared
+ * exactly for every finite query and the bounds of pgd_block_bounds (heads of
+ * one KV head whose f_h lie more than 2^25 apart are exact while s is above
+ * 2^-100 by what is more).  In a query that is not finite an infinity counts as
+ * 127 f_h, f_h that of the largest bf16, and a NaN as 0.  A bad context is
+ * flagged (PGD_DEVERR_BAD_CONTEXT) and selects nothing (tile_tokens 0); a block
+ * with a bad id, or with a score that is no number (a NaN in bound_scales),
+ * counts as the lowest score.  MB at most 49152.
  *
  * pgd_selected_decode_attention: decode attention of q over the tokens of the
  * tiles, the last tile holding tile_tokens - (tiles - 1) * bs of them -- from

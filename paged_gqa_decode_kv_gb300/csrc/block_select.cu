@@ -15,7 +15,9 @@
 // with the rounded query exceeds the least selected score.  The sums are
 // integers below 2^23 and the factors powers of two: every step is exact in
 // fp32, no order of summation changes a score, and ties are real (the lower
-// block wins).
+// block wins).  Scores of one query and KV head are held as parts of 2^24 times
+// its largest f_h, which keeps them in fp32's range whatever the query's and
+// the keys' magnitude: |sum| 2^-24 < 2^-1, f_h / max f_h <= 1, 2^-100 <= s <= 2^122.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -256,12 +258,6 @@ constexpr int kSliceKeys = 6144;   // keys of a CTA's slice at most (24 KiB)
 constexpr int kBins = kRangeBins;
 static_assert(kBins == kSelThreads, "a thread takes a bin");
 
-// A float's bits as an unsigned integer of the same order.
-__device__ __forceinline__ uint32_t order_key(float f) {
-  const uint32_t u = __float_as_uint(f);
-  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-}
-
 // D += A B, m16n8k16, f16 operands, fp32 accumulation.
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -316,7 +312,8 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
   __shared__ int warp_cnt[2][kSelWarps];
   __shared__ int found[5];
   __shared__ __align__(16) uint32_t qh[8][kHeadDim / 2];  // rounded queries, f16 pairs
-  __shared__ float qf[8], qbias[8];
+  __shared__ int qe[8];  // exponents of the queries' steps
+  __shared__ float qbias[8];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int unit = (int)blockIdx.x / C, rank = (int)blockIdx.x % C;
   const int b = unit / p.n_kv, g = unit % p.n_kv;
@@ -388,7 +385,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
     }
     sum = __reduce_add_sync(kFullMask, sum);
     if (lane == 0) {
-      qf[warp] = warp < G ? pow2f(e) : 0.f;
+      qe[warp] = e;
       qbias[warp] = (float)(-128 * sum) * 0x1p-24f;
     }
   }
@@ -410,7 +407,10 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
       const __half2 y = upper ? __hmax2(h, zero) : __hmin2(h, zero);
       return *reinterpret_cast<const uint32_t *>(&y);
     };
-    const float f0 = qf[2 * t], f1 = qf[2 * t + 1];
+    int top = qe[0];  // heads' steps are relative to the largest
+#pragma unroll
+    for (int h = 1; h < G; ++h) top = max(top, qe[h]);
+    const float f0 = pow2f(max(qe[2 * t] - top, -126)), f1 = pow2f(max(qe[2 * t + 1] - top, -126));
     const float b0 = qbias[2 * t], b1 = qbias[2 * t + 1];
     uint32_t kmin = 0xffffffffu, kmax = 0;
     // 16 blocks' bounds and scales; the next ones are loaded before the last
@@ -461,14 +461,15 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const float inf = __int_as_float(0x7f800000);
-        float best = fmaxf(2 * t < G ? d[2 * h] * 0x1p24f * f0 : -inf,
-                           2 * t + 1 < G ? d[2 * h + 1] * 0x1p24f * f1 : -inf);
+        float best = fmaxf(2 * t < G ? d[2 * h] * f0 : -inf,
+                           2 * t + 1 < G ? d[2 * h + 1] * f1 : -inf);
         best = fmaxf(best, __shfl_xor_sync(kFullMask, best, 1));
         best = fmaxf(best, __shfl_xor_sync(kFullMask, best, 2));
         const int i = i0 + r + 8 * h, j = jlo + i;
         if (i < n && t == 0) {
           const bool forced = j < p.keep_first || j >= nblk - p.keep_last;
-          const uint32_t key = forced ? 0xffffffffu : v.there[h] ? order_key(best * v.s[h]) : 0u;
+          const uint32_t score = v.there[h] ? score_key(__float_as_uint(best * v.s[h])) : 0u;
+          const uint32_t key = forced ? 0xffffffffu : score;
           if (!forced) {
             kmin = min(kmin, key);
             kmax = max(kmax, key);

@@ -1,7 +1,7 @@
-// select_range.cuh -- the block selection's search for its least selected
-// score: a range of unsigned keys narrowed to the one of 256 equal bins that
-// holds a wanted rank, until it is one key or wholly wanted.  On the host too,
-// where its arithmetic is tested over the whole range of keys.
+// select_range.cuh -- the block selection's keys and its search for the least
+// selected one: a range of unsigned keys narrowed to the one of 256 equal bins
+// that holds a wanted rank, until it is one key or wholly wanted.  On the host
+// too, where its arithmetic is tested over the whole range of keys.
 #pragma once
 
 #include <stdint.h>
@@ -17,6 +17,12 @@ namespace pgd {
 constexpr int kRangeBins = 256;
 // 32 bits of keys, 8 taken a pass.
 constexpr int kRangePasses = 4;
+
+// A score's bits as an unsigned integer of the same order; no number: the lowest.
+PGD_HOST_DEVICE uint32_t score_key(uint32_t bits) {
+  if ((bits & 0x7fffffffu) > 0x7f800000u) return 0u;
+  return (bits & 0x80000000u) ? ~bits : (bits | 0x80000000u);
+}
 
 // Key k in [lo, hi] falls into bin (k - lo) >> range_shift(lo, hi) < 256; lo < hi.
 PGD_HOST_DEVICE int range_shift(uint32_t lo, uint32_t hi) {

@@ -81,3 +81,40 @@ def test_scores_of_bounds_that_were_never_made(ctx, value):
         s = torch.where(torch.rand(scales.shape, generator=g) < share, torch.tensor(value), scales)
         tiles, tokens = _select(c, q, bounds, s, 30, 1, 2)
         _check_form(c, tiles, tokens, 30, 1, 2)
+
+
+def _want(c, q, bounds, scales, W, first, last):
+    G = q.shape[1] // c.n_kv
+    tiles = torch.empty(len(c.ctx), c.n_kv, W, dtype=torch.int32)
+    for b, n in enumerate(c.ctx):
+        at = c.tables[b, :-(-n // 16)].long()
+        for g in range(c.n_kv):
+            js = bsc.select(q[b, g * G:(g + 1) * G], bsc.f64(bounds[at, g, 0]),
+                            bsc.f64(bounds[at, g, 1]), bsc.f64(scales[at, g]), W, first, last)
+            tiles[b, g] = c.tables[b, js] * c.n_kv + g
+    return tiles
+
+
+@pytest.mark.parametrize("G", [1, 4, 8])
+@pytest.mark.parametrize("q_exp", [-100, 0, 106, 114, 122])
+@pytest.mark.parametrize("s_exp", [-90, 0, 100])
+def test_scores_of_any_magnitude(G, q_exp, s_exp):
+    """Finite queries and keys from 2^-100 to 2^122, whose scores leave fp32's range at either end;
+    the heads of a KV head 2^0 to 2^-7 of the largest: the selection of the 64-bit definition."""
+    c, bounds, scales, q = _case([1600, 5000], 2, G, seed=G)
+    by_head = torch.arange(2 * G, dtype=torch.float64) % G
+    q = (q.double() * torch.exp2(q_exp - by_head)[:, None]).to(torch.bfloat16)
+    scales = scales * 2.0 ** s_exp
+    tiles, tokens = _select(c, q, bounds, scales, 40, 1, 2)
+    assert torch.equal(tiles, _want(c, q, bounds, scales, 40, 1, 2))
+    _check_form(c, tiles, tokens, 40, 1, 2)
+
+
+def test_a_score_that_is_no_number_is_the_lowest():
+    c, bounds, scales, q = _case([1600], 1, 2, seed=8)
+    scales[c.tables[0, 10:60].long()] = float("nan")
+    tiles, tokens = _select(c, q, bounds, scales, 49, 0, 1)
+    left = [j for j in range(100) if not 10 <= j < 60]
+    assert set(tiles[0, 0].tolist()) <= {int(c.tables[0, j]) for j in left}
+    tiles, _ = _select(c, q, bounds, scales, 55, 0, 1)
+    assert tiles[0, 0].tolist() == [int(c.tables[0, j]) for j in [*range(15), *range(60, 100)]]

@@ -42,11 +42,14 @@ extern "C" int search(const uint32_t *keys, int n, int need, uint32_t *got) {
   got[0] = lo, got[1] = hi, got[2] = (uint32_t)need, got[3] = all, got[4] = (uint32_t)pass;
   return 0;
 }
+extern "C" void keys(uint32_t *bits, int n) {
+  for (int i = 0; i < n; ++i) bits[i] = pgd::score_key(bits[i]);
+}
 """
 
 
 @pytest.fixture(scope="module")
-def search(tmp_path_factory):
+def lib(tmp_path_factory):
     cxx = os.environ.get("CXX") or shutil.which("g++")
     if not cxx:
         pytest.skip("no host compiler")
@@ -55,15 +58,16 @@ def search(tmp_path_factory):
     so = str(at / "search.so")
     subprocess.run([cxx, "-O2", "-std=c++17", "-Wall", "-fPIC", "-shared", "-I" + CSRC,
                     str(at / "search.cpp"), "-o", so], check=True)
-    fn = ctypes.CDLL(so).search
-    fn.argtypes = [ctypes.c_void_p, ctypes.c_int, ctypes.c_int, ctypes.c_void_p]
-    return fn
+    lib = ctypes.CDLL(so)
+    lib.search.argtypes = [ctypes.c_void_p, ctypes.c_int, ctypes.c_int, ctypes.c_void_p]
+    lib.keys.argtypes = [ctypes.c_void_p, ctypes.c_int]
+    return lib
 
 
-def _check(search, keys, need):
+def _check(lib, keys, need):
     keys = np.ascontiguousarray(keys, dtype=np.uint32)
     got = np.zeros(5, dtype=np.uint32)
-    assert search(keys.ctypes.data, len(keys), need, got.ctypes.data) == 0
+    assert lib.search(keys.ctypes.data, len(keys), need, got.ctypes.data) == 0
     lo, hi, left, all_, passes = (int(x) for x in got)
     ordered = np.sort(keys.astype(np.int64))[::-1]
     k = keys.astype(np.int64)
@@ -82,7 +86,7 @@ def _order(f):
 
 @pytest.mark.parametrize("share", [0.0, 0.02, 0.4, 0.98])
 @pytest.mark.parametrize("top", [np.inf, np.nan, 3.4e38, 1.8e38, 1e30, 1.0])
-def test_search_with_keys_at_the_top_of_the_range(search, top, share):
+def test_search_with_keys_at_the_top_of_the_range(lib, top, share):
     """Ordinary scores of both signs, a share of them `top`: the ends of a bin then lie beyond
     2^32."""
     r = np.random.default_rng(int(share * 100) + 1)
@@ -91,10 +95,10 @@ def test_search_with_keys_at_the_top_of_the_range(search, top, share):
         f[r.random(100) < share] = top
         if share:
             f[r.integers(100)] = top
-        _check(search, _order(f), int(r.integers(1, 100)))
+        _check(lib, _order(f), int(r.integers(1, 100)))
 
 
-def test_search_over_every_kind_of_key(search):
+def test_search_over_every_kind_of_key(lib):
     r = np.random.default_rng(5)
     for n in (1, 2, 3, 17, 256, 3000):
         for _ in range(60):
@@ -103,9 +107,23 @@ def test_search_over_every_kind_of_key(search):
             keys = (first + r.integers(0, span, n)).astype(np.uint32)
             if r.random() < 0.5:
                 keys = keys[r.integers(0, n, n)]
-            _check(search, keys, int(r.integers(1, n + 1)))
+            _check(lib, keys, int(r.integers(1, n + 1)))
     ends = np.array([0, 1, 0x7FFFFFFF, 0x80000000, 0xFEFFFFFF, 0xFF000000, 0xFF000001, 0xFFFFFFFE,
                      0xFFFFFFFF], dtype=np.uint32)
     for _ in range(500):
         keys = ends[r.integers(0, len(ends), 12)]
-        _check(search, keys, int(r.integers(1, 13)))
+        _check(lib, keys, int(r.integers(1, 13)))
+
+
+def test_keys_keep_the_order_of_scores(lib):
+    r = np.random.default_rng(9)
+    f = np.concatenate([r.standard_normal(4000) * 2.0 ** r.integers(-140, 127, 4000),
+                        [0.0, np.inf, -np.inf, 3.4e38, -3.4e38, 1e-45, -1e-45]]).astype(np.float32)
+    k = f.copy().view(np.uint32)
+    lib.keys(k.ctypes.data, len(k))
+    o = np.argsort(f, kind="stable")
+    assert (np.diff(k[o].astype(np.int64))[np.diff(f[o]) > 0] > 0).all()
+    assert (k > 0).all()  # the lowest key is left to what is no number
+    nan = np.array([0x7FC00000, 0xFFC00000, 0x7F800001, 0xFFFFFFFF], dtype=np.uint32)
+    lib.keys(nan.ctypes.data, 4)
+    assert (nan == 0).all()
