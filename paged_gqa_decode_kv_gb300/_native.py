@@ -211,15 +211,16 @@ def _attention_call(fp8, out, q, k_cache, v_cache, block_tables, context_lens, s
     return name, (
         _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), _ptr(context_lens),
         B, n_q, n_kv, d, bs, MB, NB, float(scale), int(num_splits), _ptr(workspace),
-        workspace.numel() * workspace.element_size(), _stream(stream)), out
+        workspace.numel() * workspace.element_size(), _stream(stream)), out, workspace
 
 
 def paged_decode_attention(out, q, k_cache, v_cache, block_tables, context_lens, scale: float,
                            num_splits: int = 0, workspace: Optional[torch.Tensor] = None,
                            stream=None) -> torch.Tensor:
     """out[B][n_q][d] (bf16) = paged decode attention of q over the cache."""
-    name, args, out = _attention_call(False, out, q, k_cache, v_cache, block_tables,
-                                      context_lens, scale, num_splits, workspace, stream)
+    name, args, out, workspace = _attention_call(False, out, q, k_cache, v_cache, block_tables,
+                                                 context_lens, scale, num_splits, workspace,
+                                                 stream)
     _check(getattr(lib(), name)(*args))
     return out
 
@@ -264,7 +265,7 @@ def _append_attention_call(fp8, out, q, k_new, v_new, k_cache, v_cache, block_ta
         _ptr(out), _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_cache), _ptr(v_cache),
         _ptr(block_tables), _ptr(context_lens), B, n_q, n_kv, d, bs, MB, NB, float(scale),
         int(num_splits), _ptr(workspace), workspace.numel() * workspace.element_size(),
-        _stream(stream)), out
+        _stream(stream)), out, workspace
 
 
 def append_decode_attention(out, q, k_new, v_new, k_cache, v_cache, block_tables, context_lens,
@@ -274,9 +275,9 @@ def append_decode_attention(out, q, k_new, v_new, k_cache, v_cache, block_tables
     attention over the updated cache (one call; two kernels, the attention
     prologue overlapping the append, or one short-context kernel that
     appends itself)."""
-    name, args, out = _append_attention_call(False, out, q, k_new, v_new, k_cache, v_cache,
-                                             block_tables, context_lens, scale, num_splits,
-                                             workspace, stream)
+    name, args, out, workspace = _append_attention_call(
+        False, out, q, k_new, v_new, k_cache, v_cache, block_tables, context_lens, scale,
+        num_splits, workspace, stream)
     _check(getattr(lib(), name)(*args))
     return out
 
@@ -297,7 +298,7 @@ def _decode_step_call(out_h, q_h, k_new_h, v_new_h, context_lens_h, out_d, q_d, 
         _ptr(q_d), _ptr(k_new_d), _ptr(v_new_d), _ptr(context_lens_d), _ptr(k_cache),
         _ptr(v_cache), _ptr(block_tables), B, n_q, n_kv, d, bs, MB, NB, float(scale),
         int(num_splits), _ptr(workspace), workspace.numel() * workspace.element_size(),
-        _stream(stream)), None
+        _stream(stream)), None, workspace
 
 
 def decode_step(out_h, q_h, k_new_h, v_new_h, context_lens_h, out_d, q_d, k_new_d, v_new_d,
@@ -308,9 +309,9 @@ def decode_step(out_h, q_h, k_new_h, v_new_h, context_lens_h, out_d, q_d, k_new_
     read and written in place by the kernels; pageable ones go through the
     given device tensors and a copy each.  An 8-bit pool (uint8) selects the
     FP8 path."""
-    name, args, _ = _decode_step_call(out_h, q_h, k_new_h, v_new_h, context_lens_h, out_d, q_d,
-                                      k_new_d, v_new_d, context_lens_d, k_cache, v_cache,
-                                      block_tables, scale, num_splits, workspace, stream)
+    name, args, _, _ = _decode_step_call(out_h, q_h, k_new_h, v_new_h, context_lens_h, out_d, q_d,
+                                         k_new_d, v_new_d, context_lens_d, k_cache, v_cache,
+                                         block_tables, scale, num_splits, workspace, stream)
     _check(getattr(lib(), name)(*args))
 
 
@@ -320,15 +321,17 @@ class PreparedCall:
     stream) and returns its output tensor.  The Python side of a regular
     binding call -- a dozen tensor checks and pointer conversions -- takes
     about 10 us, longer than a short-context decode step on the GPU; a
-    prepared call leaves only the C call (a few us).  The buffers must stay
-    alive and unchanged in shape while the object is used."""
-    __slots__ = ("name", "_fn", "_args", "out")
+    prepared call leaves only the C call (a few us).  The caller's buffers must
+    stay alive and unchanged in shape while the object is used; the output and
+    the workspace, which the call may have made itself, are held by it."""
+    __slots__ = ("name", "_fn", "_args", "out", "workspace")
 
-    def __init__(self, name: str, args: tuple, out=None):
+    def __init__(self, name: str, args: tuple, out=None, workspace=None):
         self.name = name
         self._fn = getattr(lib(), name)
         self._args = args
         self.out = out
+        self.workspace = workspace
 
     def __call__(self):
         s = self._fn(*self._args)
@@ -438,7 +441,7 @@ def _append_verify_call(out, q, k_new, v_new, k_cache, v_cache, block_tables, co
         _ptr(out), _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_cache), _ptr(v_cache),
         _ptr(block_tables), _ptr(context_lens), B, T, n_q, n_kv, d, bs, MB, NB, float(scale),
         int(num_splits), _ptr(workspace), workspace.numel() * workspace.element_size(),
-        _stream(stream)), out
+        _stream(stream)), out, workspace
 
 
 def append_verify_attention(out, q, k_new, v_new, k_cache, v_cache, block_tables, context_lens,
@@ -448,8 +451,9 @@ def append_verify_attention(out, q, k_new, v_new, k_cache, v_cache, block_tables
     (k_new/v_new [B][T][n_kv][d]) appended at context_lens - T + j, then
     paged_verify_attention over the updated caches (its prologue overlapping
     the append)."""
-    name, args, out = _append_verify_call(out, q, k_new, v_new, k_cache, v_cache, block_tables,
-                                          context_lens, scale, num_splits, workspace, stream)
+    name, args, out, workspace = _append_verify_call(
+        out, q, k_new, v_new, k_cache, v_cache, block_tables, context_lens, scale, num_splits,
+        workspace, stream)
     _check(getattr(lib(), name)(*args))
     return out
 
@@ -469,7 +473,7 @@ def _verify_step_call(out_h, q_h, k_new_h, v_new_h, context_lens_h, out_d, q_d, 
         _ptr(q_d), _ptr(k_new_d), _ptr(v_new_d), _ptr(context_lens_d), _ptr(k_cache),
         _ptr(v_cache), _ptr(block_tables), B, T, n_q, n_kv, d, bs, MB, NB, float(scale),
         int(num_splits), _ptr(workspace), workspace.numel() * workspace.element_size(),
-        _stream(stream)), None
+        _stream(stream)), None, workspace
 
 
 def verify_step(out_h, q_h, k_new_h, v_new_h, context_lens_h, out_d, q_d, k_new_d, v_new_d,
@@ -480,9 +484,9 @@ def verify_step(out_h, q_h, k_new_h, v_new_h, context_lens_h, out_d, q_d, k_new_
     attention, all on `stream`.  Page-locked (pinned) host tensors are read
     and written in place by the kernels; pageable ones go through the given
     device tensors and a copy each."""
-    name, args, _ = _verify_step_call(out_h, q_h, k_new_h, v_new_h, context_lens_h, out_d, q_d,
-                                      k_new_d, v_new_d, context_lens_d, k_cache, v_cache,
-                                      block_tables, scale, num_splits, workspace, stream)
+    name, args, _, _ = _verify_step_call(out_h, q_h, k_new_h, v_new_h, context_lens_h, out_d, q_d,
+                                         k_new_d, v_new_d, context_lens_d, k_cache, v_cache,
+                                         block_tables, scale, num_splits, workspace, stream)
     _check(getattr(lib(), name)(*args))
 
 
@@ -650,8 +654,9 @@ def paged_decode_attention_fp8(out, q, k_cache, v_cache, block_tables, context_l
                                workspace: Optional[torch.Tensor] = None,
                                stream=None) -> torch.Tensor:
     """out[B][n_q][d] (bf16) = paged decode attention of q over the 8-bit cache."""
-    name, args, out = _attention_call(True, out, q, k_cache, v_cache, block_tables, context_lens,
-                                      scale, num_splits, workspace, stream)
+    name, args, out, workspace = _attention_call(True, out, q, k_cache, v_cache, block_tables,
+                                                 context_lens, scale, num_splits, workspace,
+                                                 stream)
     _check(getattr(lib(), name)(*args))
     return out
 
@@ -661,9 +666,9 @@ def append_decode_attention_fp8(out, q, k_new, v_new, k_cache, v_cache, block_ta
                                 workspace: Optional[torch.Tensor] = None,
                                 stream=None) -> torch.Tensor:
     """kv_append_fp8 at context_lens - 1, then attention over the 8-bit cache."""
-    name, args, out = _append_attention_call(True, out, q, k_new, v_new, k_cache, v_cache,
-                                             block_tables, context_lens, scale, num_splits,
-                                             workspace, stream)
+    name, args, out, workspace = _append_attention_call(
+        True, out, q, k_new, v_new, k_cache, v_cache, block_tables, context_lens, scale,
+        num_splits, workspace, stream)
     _check(getattr(lib(), name)(*args))
     return out
 
@@ -755,7 +760,7 @@ def _attention8b(pack, out, q, k_new, v_new, k_cache, v_cache, k_scales, v_scale
         if isinstance(k_cache, torch.Tensor) and k_cache.dtype != torch.uint8:
             raise TypeError("k_cache must be torch.uint8, got %s" % k_cache.dtype)
         out, workspace = _out_and_scratch(out, q, _pool_heads(k_cache), num_splits, workspace)
-    return out, (_tensor_side or _tensors()).attention(
+    return out, workspace, (_tensor_side or _tensors()).attention(
         out, q, k_new, v_new, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
         scale, num_splits, workspace, stream, pack)
 
@@ -766,8 +771,8 @@ def paged_decode_attention_fp8b(out, q, k_cache, v_cache, k_scales, v_scales, bl
                                 stream=None) -> torch.Tensor:
     """out[B][n_q][d] (bf16) = paged decode attention of q over the
     block-scaled 8-bit cache."""
-    out, s = _attention8b(False, out, q, None, None, k_cache, v_cache, k_scales, v_scales,
-                          block_tables, context_lens, scale, num_splits, workspace, stream)
+    out, _, s = _attention8b(False, out, q, None, None, k_cache, v_cache, k_scales, v_scales,
+                             block_tables, context_lens, scale, num_splits, workspace, stream)
     if s:
         _check(s)
     return out
@@ -779,8 +784,8 @@ def append_decode_attention_fp8b(out, q, k_new, v_new, k_cache, v_cache, k_scale
                                  stream=None) -> torch.Tensor:
     """kv_append_fp8b of one token per sequence at context_lens - 1, then
     attention over the block-scaled cache."""
-    out, s = _attention8b(False, out, q, k_new, v_new, k_cache, v_cache, k_scales, v_scales,
-                          block_tables, context_lens, scale, num_splits, workspace, stream)
+    out, _, s = _attention8b(False, out, q, k_new, v_new, k_cache, v_cache, k_scales, v_scales,
+                             block_tables, context_lens, scale, num_splits, workspace, stream)
     if s:
         _check(s)
     return out
@@ -819,7 +824,7 @@ def _tiles_attention(pack, out, q, k_cache, v_cache, k_scales, v_scales, bounds,
         if (k_scales is None) != (v_scales is None):
             raise ValueError("a block-scaled cache needs both scales")
         out, workspace = _out_and_scratch(out, q, _pool_heads(k_cache), num_splits, workspace)
-    return out, (_tensor_side or _tensors()).tiles(
+    return out, workspace, (_tensor_side or _tensors()).tiles(
         out, q, k_cache, v_cache, k_scales, v_scales, bounds, bound_scales, block_tables,
         context_lens, tiles, tile_tokens, keep_first, keep_last, scale, num_splits, workspace,
         stream, pack)
@@ -832,9 +837,9 @@ def selected_decode_attention(out, q, k_cache, v_cache, tiles, tile_tokens, scal
     """out[B][n_q][d] (bf16) = decode attention of q over the tiles (block *
     n_kv + head, [B][n_kv][W]) of a bf16 cache, or of a block-scaled one with
     its scales."""
-    out, s = _tiles_attention(False, out, q, k_cache, v_cache, k_scales, v_scales, None, None,
-                              None, None, tiles, tile_tokens, 0, 0, scale, num_splits, workspace,
-                              stream)
+    out, _, s = _tiles_attention(False, out, q, k_cache, v_cache, k_scales, v_scales, None, None,
+                                 None, None, tiles, tile_tokens, 0, 0, scale, num_splits,
+                                 workspace, stream)
     if s:
         _check(s)
     return out
@@ -849,9 +854,9 @@ def sparse_decode_attention(out, q, k_cache, v_cache, bounds, bound_scales, bloc
     selected_decode_attention over them, in one call."""
     if bounds is None:
         raise TypeError("bounds must be a tensor")
-    out, s = _tiles_attention(False, out, q, k_cache, v_cache, k_scales, v_scales, bounds,
-                              bound_scales, block_tables, context_lens, tiles, tile_tokens,
-                              keep_first, keep_last, scale, num_splits, workspace, stream)
+    out, _, s = _tiles_attention(False, out, q, k_cache, v_cache, k_scales, v_scales, bounds,
+                                 bound_scales, block_tables, context_lens, tiles, tile_tokens,
+                                 keep_first, keep_last, scale, num_splits, workspace, stream)
     if s:
         _check(s)
     return out
@@ -859,25 +864,28 @@ def sparse_decode_attention(out, q, k_cache, v_cache, bounds, bound_scales, bloc
 
 def _prepared8b(out, q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, scale,
                 num_splits=0, workspace=None, stream=None):
-    out, args = _attention8b(True, out, q, None, None, k_cache, v_cache, k_scales, v_scales,
-                             block_tables, context_lens, scale, num_splits, workspace, stream)
-    return "pgd_paged_decode_attention_fp8b", args, out
+    out, workspace, args = _attention8b(True, out, q, None, None, k_cache, v_cache, k_scales,
+                                        v_scales, block_tables, context_lens, scale, num_splits,
+                                        workspace, stream)
+    return "pgd_paged_decode_attention_fp8b", args, out, workspace
 
 
 def _prepared_append8b(out, q, k_new, v_new, k_cache, v_cache, k_scales, v_scales, block_tables,
                        context_lens, scale, num_splits=0, workspace=None, stream=None):
-    out, args = _attention8b(True, out, q, k_new, v_new, k_cache, v_cache, k_scales, v_scales,
-                             block_tables, context_lens, scale, num_splits, workspace, stream)
-    return "pgd_append_decode_attention_fp8b", args, out
+    out, workspace, args = _attention8b(True, out, q, k_new, v_new, k_cache, v_cache, k_scales,
+                                        v_scales, block_tables, context_lens, scale, num_splits,
+                                        workspace, stream)
+    return "pgd_append_decode_attention_fp8b", args, out, workspace
 
 
 def _prepared_sparse(out, q, k_cache, v_cache, bounds, bound_scales, block_tables, context_lens,
                      tiles, tile_tokens, keep_first, keep_last, scale, k_scales=None,
                      v_scales=None, num_splits=0, workspace=None, stream=None):
-    out, args = _tiles_attention(True, out, q, k_cache, v_cache, k_scales, v_scales, bounds,
-                                 bound_scales, block_tables, context_lens, tiles, tile_tokens,
-                                 keep_first, keep_last, scale, num_splits, workspace, stream)
-    return "pgd_sparse_decode_attention", args, out
+    out, workspace, args = _tiles_attention(True, out, q, k_cache, v_cache, k_scales, v_scales,
+                                            bounds, bound_scales, block_tables, context_lens,
+                                            tiles, tile_tokens, keep_first, keep_last, scale,
+                                            num_splits, workspace, stream)
+    return "pgd_sparse_decode_attention", args, out, workspace
 
 
 def copy_blocks(k_cache, v_cache, src_ids, dst_ids, stream=None) -> None:
