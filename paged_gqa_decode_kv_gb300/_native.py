@@ -145,6 +145,25 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _made_for(stream, make, result: bool = False) -> torch.Tensor:
+    """A buffer that a call on `stream` makes itself: allocated and filled on
+    that stream, so that the call finds it filled and its memory is not given
+    to other work before the call is done.  result: the caller keeps it, and
+    reads it on the current stream."""
+    if stream is None:
+        return make()
+    current = torch.cuda.current_stream()
+    if stream.cuda_stream == current.cuda_stream:
+        return make()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream)
+    with torch.cuda.stream(stream):
+        t = make()
+    if result and t.is_cuda:
+        t.record_stream(current)
+    return t
+
+
 def _need(t: torch.Tensor, dtype: torch.dtype, name: str, cuda: bool = True) -> None:
     if t.dtype != dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
@@ -202,10 +221,10 @@ def _attention_call(fp8, out, q, k_cache, v_cache, block_tables, context_lens, s
     B, n_q, d = q.shape
     NB, n_kv, bs, _ = _cache8_dims(k_cache) if fp8 else _cache_dims(k_cache)
     if out is None:
-        out = torch.empty_like(q)
+        out = _made_for(stream, lambda: torch.empty_like(q), result=True)
     _need(out, torch.bfloat16, "out")
     if workspace is None:
-        workspace = make_workspace(B, n_q, n_kv, num_splits, q.device)
+        workspace = _made_for(stream, lambda: make_workspace(B, n_q, n_kv, num_splits, q.device))
     MB = block_tables.shape[1]
     name = "pgd_paged_decode_attention_fp8" if fp8 else "pgd_paged_decode_attention"
     return name, (
@@ -255,10 +274,10 @@ def _append_attention_call(fp8, out, q, k_new, v_new, k_cache, v_cache, block_ta
     B, n_q, d = q.shape
     NB, n_kv, bs, _ = _cache8_dims(k_cache) if fp8 else _cache_dims(k_cache)
     if out is None:
-        out = torch.empty_like(q)
+        out = _made_for(stream, lambda: torch.empty_like(q), result=True)
     _need(out, torch.bfloat16, "out")
     if workspace is None:
-        workspace = make_workspace(B, n_q, n_kv, num_splits, q.device)
+        workspace = _made_for(stream, lambda: make_workspace(B, n_q, n_kv, num_splits, q.device))
     MB = block_tables.shape[1]
     name = "pgd_append_decode_attention_fp8" if fp8 else "pgd_append_decode_attention"
     return name, (
@@ -403,11 +422,11 @@ def paged_verify_attention(out, q, k_cache, v_cache, block_tables, context_lens,
     B, T, n_q, d = q.shape
     NB, n_kv, bs, d2 = _cache_dims(k_cache)
     if out is None:
-        out = torch.empty_like(q)
+        out = _made_for(stream, lambda: torch.empty_like(q), result=True)
     _need(out, torch.bfloat16, "out")
     if workspace is None:
         n = max(1, verify_workspace_size(B, T, n_q, n_kv, num_splits))
-        workspace = torch.zeros(n, dtype=torch.uint8, device=q.device)
+        workspace = _made_for(stream, lambda: torch.zeros(n, dtype=torch.uint8, device=q.device))
     MB = block_tables.shape[1]
     _check(lib().pgd_paged_verify_attention(
         _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), _ptr(context_lens),
@@ -416,10 +435,10 @@ def paged_verify_attention(out, q, k_cache, v_cache, block_tables, context_lens,
     return out
 
 
-def _verify_workspace(workspace, B, T, n_q, n_kv, num_splits, device):
+def _verify_workspace(workspace, B, T, n_q, n_kv, num_splits, device, stream):
     if workspace is None:
         n = max(1, verify_workspace_size(B, T, n_q, n_kv, num_splits))
-        workspace = torch.zeros(n, dtype=torch.uint8, device=device)
+        workspace = _made_for(stream, lambda: torch.zeros(n, dtype=torch.uint8, device=device))
     return workspace
 
 
@@ -433,9 +452,9 @@ def _append_verify_call(out, q, k_new, v_new, k_cache, v_cache, block_tables, co
     B, T, n_q, d = q.shape
     NB, n_kv, bs, _ = _cache_dims(k_cache)
     if out is None:
-        out = torch.empty_like(q)
+        out = _made_for(stream, lambda: torch.empty_like(q), result=True)
     _need(out, torch.bfloat16, "out")
-    workspace = _verify_workspace(workspace, B, T, n_q, n_kv, num_splits, q.device)
+    workspace = _verify_workspace(workspace, B, T, n_q, n_kv, num_splits, q.device, stream)
     MB = block_tables.shape[1]
     return "pgd_append_verify_attention", (
         _ptr(out), _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_cache), _ptr(v_cache),
@@ -513,6 +532,16 @@ def mla_workspace_size(B: int, H: int, num_splits: int = 0) -> int:
     return int(lib().pgd_mla_workspace_size(B, H, num_splits))
 
 
+def _mla_out(q, stream):
+    make = lambda: torch.empty((*q.shape[:2], 512), dtype=torch.bfloat16, device=q.device)
+    return _made_for(stream, make, result=True)
+
+
+def _mla_workspace(q, num_splits, stream):
+    n = max(256, mla_workspace_size(*q.shape[:2], num_splits))
+    return _made_for(stream, lambda: torch.empty(n, dtype=torch.uint8, device=q.device))
+
+
 def mla_decode_attention(out, q, cache, block_tables, context_lens, scale: float,
                          num_splits: int = 0, workspace: Optional[torch.Tensor] = None,
                          stream=None) -> torch.Tensor:
@@ -525,11 +554,10 @@ def mla_decode_attention(out, q, cache, block_tables, context_lens, scale: float
     B, H, D = q.shape
     NB, bs, D2 = _mla_pool_dims(cache)
     if out is None:
-        out = torch.empty((B, H, 512), dtype=torch.bfloat16, device=q.device)
+        out = _mla_out(q, stream)
     _need(out, torch.bfloat16, "out")
     if workspace is None:
-        workspace = torch.empty(max(256, mla_workspace_size(B, H, num_splits)), dtype=torch.uint8,
-                                device=q.device)
+        workspace = _mla_workspace(q, num_splits, stream)
     MB = block_tables.shape[1]
     _check(lib().pgd_mla_decode_attention(
         _ptr(out), _ptr(q), _ptr(cache), _ptr(block_tables), _ptr(context_lens), B, H, D, 512,
@@ -552,11 +580,10 @@ def mla_append_decode_attention(out, q, c_new, cache, block_tables, context_lens
     B, H, D = q.shape
     NB, bs, D2 = _mla_pool_dims(cache)
     if out is None:
-        out = torch.empty((B, H, 512), dtype=torch.bfloat16, device=q.device)
+        out = _mla_out(q, stream)
     _need(out, torch.bfloat16, "out")
     if workspace is None:
-        workspace = torch.empty(max(256, mla_workspace_size(B, H, num_splits)), dtype=torch.uint8,
-                                device=q.device)
+        workspace = _mla_workspace(q, num_splits, stream)
     MB = block_tables.shape[1]
     _check(lib().pgd_mla_append_decode_attention(
         _ptr(out), _ptr(q), _ptr(c_new), _ptr(cache), _ptr(block_tables), _ptr(context_lens), B,
@@ -609,11 +636,12 @@ def cascade_decode_attention(out, q, k_cache, v_cache, block_tables, context_len
     B, n_q, d = q.shape
     NB, n_kv, bs, _ = _cache_dims(k_cache)
     if out is None:
-        out = torch.empty_like(q)
+        out = _made_for(stream, lambda: torch.empty_like(q), result=True)
     _need(out, torch.bfloat16, "out")
     if workspace is None:
         n = cascade_workspace_size(B, n_q, n_kv, bs, max_group_size, max_group_blocks, num_splits)
-        workspace = torch.zeros(max(1, n), dtype=torch.uint8, device=q.device)
+        n = max(1, n)
+        workspace = _made_for(stream, lambda: torch.zeros(n, dtype=torch.uint8, device=q.device))
     MB = block_tables.shape[1]
     _check(lib().pgd_cascade_decode_attention(
         _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), _ptr(context_lens),
@@ -735,16 +763,17 @@ def kv_read_fp8b(k_out, v_out, k_cache, v_cache, k_scales, v_scales, block_table
         _check(s)
 
 
-def _out_and_scratch(out, q, n_kv, num_splits, workspace):
+def _out_and_scratch(out, q, n_kv, num_splits, workspace, stream):
     """The output and the workspace of a decode call, made where not given."""
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
         raise ValueError("q must be [B][n_q][d]")
     if out is None:
-        out = torch.empty_like(q)
+        out = _made_for(stream, lambda: torch.empty_like(q), result=True)
     if workspace is None:
         if not q.is_cuda:
             raise ValueError("q must be on a CUDA device")
-        workspace = make_block_workspace(q.shape[0], q.shape[1], n_kv, num_splits, q.device)
+        workspace = _made_for(stream, lambda: make_block_workspace(q.shape[0], q.shape[1], n_kv,
+                                                                   num_splits, q.device))
     return out, workspace
 
 
@@ -759,7 +788,8 @@ def _attention8b(pack, out, q, k_new, v_new, k_cache, v_cache, k_scales, v_scale
     if out is None or workspace is None:
         if isinstance(k_cache, torch.Tensor) and k_cache.dtype != torch.uint8:
             raise TypeError("k_cache must be torch.uint8, got %s" % k_cache.dtype)
-        out, workspace = _out_and_scratch(out, q, _pool_heads(k_cache), num_splits, workspace)
+        out, workspace = _out_and_scratch(out, q, _pool_heads(k_cache), num_splits, workspace,
+                                          stream)
     return out, workspace, (_tensor_side or _tensors()).attention(
         out, q, k_new, v_new, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
         scale, num_splits, workspace, stream, pack)
@@ -823,7 +853,8 @@ def _tiles_attention(pack, out, q, k_cache, v_cache, k_scales, v_scales, bounds,
     if out is None or workspace is None:
         if (k_scales is None) != (v_scales is None):
             raise ValueError("a block-scaled cache needs both scales")
-        out, workspace = _out_and_scratch(out, q, _pool_heads(k_cache), num_splits, workspace)
+        out, workspace = _out_and_scratch(out, q, _pool_heads(k_cache), num_splits, workspace,
+                                          stream)
     return out, workspace, (_tensor_side or _tensors()).tiles(
         out, q, k_cache, v_cache, k_scales, v_scales, bounds, bound_scales, block_tables,
         context_lens, tiles, tile_tokens, keep_first, keep_last, scale, num_splits, workspace,

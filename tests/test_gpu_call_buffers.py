@@ -125,3 +125,56 @@ def test_a_prepared_call_keeps_what_it_made(name):
         torch.cuda.synchronize()
         assert torch.equal(got, want)
     assert all(bool((x == 1).all()) for x in later)
+
+
+def _busy(stream):
+    """A few milliseconds of copies on a stream."""
+    with torch.cuda.stream(stream):
+        a = torch.empty(1 << 30, dtype=torch.uint8, device="cuda")
+        b = torch.empty_like(a)
+        for _ in range(24):
+            b.copy_(a)
+
+
+@pytest.mark.parametrize("slow", ["current", "given"])
+@pytest.mark.parametrize("name", CALLS)
+def test_buffers_made_for_a_call_on_another_stream(name, slow):
+    """While the current stream is busy, and while the given one is: the fill of the counters comes
+    before the call, and what the call has given back is not handed out before it is done."""
+    fn, args, kw, want, n = _setup(name)
+    side = torch.cuda.Stream()
+    del _ones(n, 6)[:]  # what the allocator gives out next is not zero
+    torch.cuda.synchronize()
+    _busy(torch.cuda.current_stream() if slow == "current" else side)
+    got = fn(None, *args, stream=side, **kw)
+    later = _ones(n) + _ones(want.numel() * 2)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+    assert all(bool((x == 1).all()) for x in later)
+
+
+def test_a_prepared_call_on_another_stream():
+    fn, args, kw, want, n = _setup("paged_decode_attention_fp8b")
+    side = torch.cuda.Stream()
+    del _ones(n, 6)[:]
+    torch.cuda.synchronize()
+    _busy(torch.cuda.current_stream())
+    call = pgd.prepare("paged_decode_attention_fp8b", None, *args, stream=side, **kw)
+    got = call()
+    later = _ones(n)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and torch.equal(call(), want)
+    assert all(bool((x == 1).all()) for x in later)
+
+
+@pytest.mark.parametrize("name", ["paged_decode_attention", "sparse_decode_attention"])
+def test_a_stream_given_by_its_handle(name):
+    """Any object with a cuda_stream will do, as it does where the caller gives the buffers."""
+    fn, args, kw, want, n = _setup(name)
+
+    class Handle:
+        cuda_stream = torch.cuda.Stream().cuda_stream
+
+    got = fn(None, *args, stream=Handle(), **kw)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
