@@ -3,10 +3,11 @@
 Each CUDA translation unit is compiled by nvcc with one -gencode
 (compute_103a -> sm_103a), in parallel, and the objects are linked into
 ``paged_gqa_decode_kv_gb300/_build/libpgd.so`` (CUDA runtime linked
-statically).  Beside it, ``_pgd_tensors``: the part of the binding that reads
-torch tensors, a CPython extension built against the installed torch (whose
-version is part of its file name).  Rebuilds only when a source or header is
-newer than the library.
+statically); this needs the CUDA toolkit and a C++ compiler alone.  Beside it,
+where torch is installed, ``_pgd_tensors``: the part of the binding that reads
+torch tensors, a CPython extension built against that torch (whose version is
+part of its file name).  Rebuilds only when a source or header is newer than
+what is built.
 """
 from __future__ import annotations
 
@@ -44,6 +45,14 @@ def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "*.cpp")))
 
 
+def _has_torch() -> bool:
+    try:
+        import torch  # noqa: F401
+    except ImportError:
+        return False
+    return True
+
+
 def tensors_path() -> str:
     """The binding's tensor extension for the installed torch."""
     import torch
@@ -52,12 +61,19 @@ def tensors_path() -> str:
     return os.path.join(BUILD, "_pgd_tensors_torch_%s.so" % tag)
 
 
-def _stale() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(tensors_path()):
+def _older(path: str, deps) -> bool:
+    if not os.path.exists(path):
         return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(tensors_path()))
-    deps = sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + [HEADER, TENSORS_SRC, __file__]
+    t = os.path.getmtime(path)
     return any(os.path.getmtime(p) > t for p in deps)
+
+
+def _library_stale() -> bool:
+    return _older(LIB, sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + [HEADER, __file__])
+
+
+def _tensors_stale() -> bool:
+    return _has_torch() and _older(tensors_path(), [TENSORS_SRC, HEADER, __file__])
 
 
 def _torch_flags():
@@ -94,16 +110,24 @@ def _compile(src: str, verbose_ptxas: bool) -> str:
 
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
-    """Compile and link libpgd.so; return its path."""
-    if not force and not verbose_ptxas and not _stale():
+    """Compile and link libpgd.so, and the tensor extension where torch is
+    installed; return the library's path."""
+    force = force or verbose_ptxas
+    library = sources() if force or _library_stale() else []
+    tensors = [TENSORS_SRC] if (force and _has_torch()) or _tensors_stale() else []
+    if not library and not tensors:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
-    srcs = [TENSORS_SRC] + sources()
-    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 1))) as ex:
-        objs = list(ex.map(lambda s: _compile(s, verbose_ptxas), srcs))
-    _link([_nvcc()] + ARCH + ["-shared", "-Xcompiler", "-fPIC"] + objs[1:], LIB)
-    _link([os.environ.get("CXX", "g++"), "-shared", objs[0], "-L" + BUILD, "-lpgd",
-           "-Wl,-rpath,$ORIGIN"] + _torch_flags()[1], tensors_path())
+    jobs = tensors + library
+    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(jobs), os.cpu_count() or 1))) as ex:
+        objs = [ex.submit(_compile, s, verbose_ptxas) for s in jobs]
+    # (the library first: it stands whatever becomes of the extension)
+    if library:
+        _link([_nvcc()] + ARCH + ["-shared", "-Xcompiler", "-fPIC"] +
+              [o.result() for o in objs[len(tensors):]], LIB)
+    if tensors:
+        _link([os.environ.get("CXX", "g++"), "-shared", objs[0].result(), "-L" + BUILD, "-lpgd",
+               "-Wl,-rpath,$ORIGIN"] + _torch_flags()[1], tensors_path())
     return LIB
 
 
