@@ -21,6 +21,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 
 #include "cluster.cuh"
@@ -31,6 +32,7 @@ namespace pgd {
 namespace {
 
 constexpr int kBoundWarps = 4;
+constexpr int kGridRows = 65535;  // of a launch
 
 // Least (largest) of each of two packed numbers, passing over a NaN beside a
 // number: f16 (widened 8-bit codes) or bf16.
@@ -650,9 +652,19 @@ cudaError_t block_bounds_launch(const BoundsParams &p, cudaStream_t stream) {
   const int run = (long long)p.B * JM * p.n_kv > 16384 ? 4 : 1, runs = (JM + run - 1) / run;
   const long long grid = ((long long)runs * p.n_kv + kBoundWarps - 1) / kBoundWarps;
   if (grid * kBoundWarps > 0x7fffffffLL) return cudaErrorInvalidValue;
-  const dim3 gd((unsigned)grid, (unsigned)p.B);
-  return p.k_scales ? bounds_form<true>(p, gd, runs, run, stream)
-                    : bounds_form<false>(p, gd, runs, run, stream);
+  // a grid row a sequence, as many of them as a grid has to a launch
+  for (int b = 0; b < p.B; b += kGridRows) {
+    BoundsParams part = p;
+    part.B = std::min(kGridRows, p.B - b);
+    part.tables += (size_t)b * p.MB;
+    part.ctx += b;
+    if (p.pos) part.pos += b;
+    const dim3 gd((unsigned)grid, (unsigned)part.B);
+    const cudaError_t e = p.k_scales ? bounds_form<true>(part, gd, runs, run, stream)
+                                     : bounds_form<false>(part, gd, runs, run, stream);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 // Blocks of a sequence that the selection holds keys for.

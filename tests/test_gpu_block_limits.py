@@ -1,0 +1,45 @@
+"""The calls on the block-scaled cache and on selections at the ends of the sizes they take."""
+import pytest
+import torch
+
+import block_scaled as bsc
+import paged_gqa_decode_kv_gb300 as pgd
+
+pytestmark = pytest.mark.gpu
+SCALE = 128 ** -0.5
+
+
+@pytest.fixture(autouse=True)
+def _clean_errors():
+    pgd.device_errors(clear=True)
+    yield
+    assert pgd.device_errors(clear=True) == 0
+
+
+def _i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+@pytest.mark.parametrize("B", [65535, 65536, 131071])
+@pytest.mark.parametrize("first", [False, True])
+def test_bounds_of_more_sequences_than_a_grid_has_rows(B, first):
+    """One token a sequence, but for every seventh, which has none: its block keeps its bounds."""
+    g = torch.Generator(device="cuda").manual_seed(B)
+    k = torch.randn(B, 1, 2, 16, 8, 8, generator=g, device="cuda").to(torch.bfloat16)
+    tables = torch.randperm(B, generator=g, device="cuda").to(torch.int32)[:, None].contiguous()
+    ctx = (torch.arange(B, device="cuda") % 7 > 0).to(torch.int32)
+    bounds = torch.full((B, 1, 2, 128), -77, dtype=torch.int8, device="cuda")
+    scales = torch.full((B, 1), -1.0, device="cuda")
+    pos = torch.zeros(B, dtype=torch.int32, device="cuda") if first else None
+    pgd.block_bounds(bounds, scales, k, tables, ctx, positions=pos, max_tokens=1)
+    has = torch.zeros(B, dtype=torch.bool, device="cuda")
+    has[tables[:, 0].long()] = ctx > 0
+    x = k[:, 0, 0, :, 0].reshape(B, 128).double()  # slot 0 of every block
+    m, e = torch.frexp(x.abs().amax(1))  # m in [1/2, 1); 127 * 2^n = (127/128) * 2^(n + 7)
+    e = torch.where(m <= 127 / 128, e - 7, e - 6).double()
+    s = torch.where(has, torch.exp2(e), torch.tensor(-1.0, device="cuda").double())
+    y = x / torch.exp2(e)[:, None]
+    want = torch.stack([torch.floor(y), torch.ceil(y)], 1)
+    want = torch.where(has[:, None, None], want, torch.tensor(-77.0, device="cuda").double())
+    assert torch.equal(scales[:, 0].double(), s)
+    assert torch.equal(bounds[:, 0].double(), want)
