@@ -676,7 +676,7 @@ attention_fp8b_kernel(const __grid_constant__ Params pr) {
   if (sc.units) {
     have = whole_unit(sc, unit_b, sg);
   } else {
-    sc.S = sc.P > 0 ? (sc.X + sc.P - 1) / sc.P : 1;
+    sc.S = sc.P > 0 ? (sc.X - 1) / sc.P + 1 : 1;  // (X + P may not fit 32 bits)
     walk_start(sc, p.B, walk);
     have = walk_next(pre, sc.n_kv, sc.ov, p.B, walk, sg);
   }

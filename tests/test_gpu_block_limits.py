@@ -43,3 +43,26 @@ def test_bounds_of_more_sequences_than_a_grid_has_rows(B, first):
     want = torch.where(has[:, None, None], want, torch.tensor(-77.0, device="cuda").double())
     assert torch.equal(scales[:, 0].double(), s)
     assert torch.equal(bounds[:, 0].double(), want)
+
+
+def test_attention_at_the_end_of_the_cost_space():
+    """B * n_kv * (MB + 24) = 2^31 - 2, every context full: the cuts of the work are computed next to
+    the largest 32-bit number.  The tables repeat 64 blocks, so a softmax over those with their
+    multiplicities is the reference."""
+    B, n_kv, MB, NB = 2046, 21, 49957, 64
+    assert B * n_kv * (MB + 24) == 2 ** 31 - 2
+    c = bsc.make_cache([NB * 16], n_kv, 16, seed=4, spoil=False)
+    k, v, ks, vs, tables, _ = c.cuda()
+    row = tables[0, :NB][torch.arange(MB, device="cuda") % NB]
+    q = bsc.make_query(B, n_kv).cuda()
+    got = pgd.paged_decode_attention_fp8b(None, q, k, v, ks, vs, row.repeat(B, 1),
+                                          _i32([MB * 16]).repeat(B), SCALE)
+    times = torch.full((NB,), MB // NB, dtype=torch.float64)
+    times[:MB % NB] += 1
+    times = times.repeat_interleave(16).cuda()  # of every token
+    kd, vd = (torch.from_numpy(c.rows(x, 0, NB * 16)).cuda() for x in "kv")
+    s = torch.einsum("bhd,thd->bht", q.double(), kd) * SCALE
+    w = torch.exp(s - s.amax(-1, keepdim=True)) * times
+    w /= w.sum(-1, keepdim=True)
+    want, mag = (torch.einsum("bht,thd->bhd", w, x) for x in (vd, vd.abs()))
+    bsc.close(got, want.cpu().numpy(), mag.cpu().numpy())
