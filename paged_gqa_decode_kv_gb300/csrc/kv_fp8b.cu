@@ -49,11 +49,12 @@ __device__ __forceinline__ Items find_items(const Kv8bParams &p, int bs, int run
   const long long per_b = (long long)runs * 2 * p.n_kv;
   if (id >= per_b * p.B) return it;
   it.b = (int)(id / per_b);
-  int r = (int)(id % per_b);
-  const int jrel = r / (2 * p.n_kv) * run;
-  r %= 2 * p.n_kv;
-  it.is_v = r / p.n_kv;
-  it.g = r % p.n_kv;
+  uint32_t r = (uint32_t)(id % per_b);  // (up to 2^32: the host bounds runs * n_kv by 2^31)
+  const uint32_t heads = (uint32_t)p.n_kv;
+  const int jrel = (int)(r / (2 * heads)) * run;
+  r %= 2 * heads;
+  it.is_v = (int)(r / heads);
+  it.g = (int)(r % heads);
   const TokenRange t = token_range(p.starts, it.b, p.T, p.N);
   const bool first = jrel == 0 && it.g == 0 && it.is_v == 0 && lane == 0;
   if (t.bad) {

@@ -66,3 +66,26 @@ def test_attention_at_the_end_of_the_cost_space():
     w /= w.sum(-1, keepdim=True)
     want, mag = (torch.einsum("bht,thd->bhd", w, x) for x in (vd, vd.abs()))
     bsc.close(got, want.cpu().numpy(), mag.cpu().numpy())
+
+
+@pytest.mark.parametrize("call", ["append", "read"])
+def test_ranges_whose_items_pass_32_bits(call):
+    """max_tokens as long as a table of 2^20 blocks, 1100 heads: 2.3e9 (block, head, K or V) items of
+    one sequence, of which three tokens' exist.  (The write takes blocks in fours: a quarter.)"""
+    n_kv, MB = 1100, 1 << 20
+    c = bsc.make_cache([18], n_kv, 16, seed=7, spoil=False)
+    k, v, ks, vs, tables, _ = c.cuda()
+    table = torch.full((1, MB), -1, dtype=torch.int32, device="cuda")
+    table[0, :2] = tables[0, :2]
+    g = torch.Generator().manual_seed(2)
+    rows = [torch.randn(3, n_kv, 128, generator=g).to(torch.bfloat16) for _ in range(2)]
+    up = [x.cuda() for x in rows]
+    fn = pgd.kv_append_fp8b if call == "append" else pgd.kv_read_fp8b
+    fn(*up, k, v, ks, vs, table, _i32([15]), token_starts=_i32([0, 3]), max_tokens=16 * MB)
+    if call == "append":
+        bsc.append(c, *rows, [15], [0, 3])
+        assert torch.equal(bsc.untile8(k.cpu()), c.k) and torch.equal(bsc.untile8(v.cpu()), c.v)
+        assert torch.equal(ks.cpu(), c.k_scales) and torch.equal(vs.cpu(), c.v_scales)
+    else:
+        for which, got in zip("kv", up):
+            assert (bsc.f64(got) == c.rows(which, 0, 18)[15:]).all()
