@@ -506,6 +506,8 @@ pgd_status pgd_append_decode_attention_fp8(void *out, const void *q, const void 
  * q.k^T and p.v on the tensor cores on the codes themselves, the query as two
  * E4M3 terms, a probability (times V's scale) as three, to 2^-12 of itself and
  * 2^-24 of the largest; scales, softmax and accumulation in fp32; bf16 output.
+ * That holds for V scales of 2^-100 (the writer's least) to 2^100 (values of
+ * 10^32); past them small weights are lost first.
  * An automatic call (num_splits = 0) of few heads and at most 1024 tokens (the
  * limit of pgd_set_short_context_tokens, or twice that with fewer heads still)
  * runs on the CUDA cores in fp32.

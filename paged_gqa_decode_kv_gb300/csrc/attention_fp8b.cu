@@ -33,7 +33,11 @@
 // of log2(p sv) rather than of log2(p); the sum of p takes the same reference
 // and stays exact in fp32, so outputs, partial states and their merge need no
 // second one.  The reference moves when exceeded by 2^4: x <= 2^8, and 2^5
-// times a residual of x stays within E4M3's 448.
+// times a residual of x stays within E4M3's 448.  Relative to it a sum of p is
+// as large as 1 / sv: 2^100 for blocks of zeros.  Two references can lie further
+// apart than the exponents of fp32 reach while both sums count alike, so a sum
+// passes to another reference by two factors, each the root of the whole (an
+// output, at most 2^8 times its tokens, has vanished where one factor does).
 //
 // Roles (512 threads): warps 0-3 and 12-15 softmax (thread t = token row t),
 // 4 / 5 K / V producers, 6 q.k^T issuer, 7 p.v issuer, 8-11 query conversion,
@@ -386,6 +390,12 @@ __device__ __forceinline__ void convert_query(const AttnParams &p, const Piece &
   __syncwarp();
 }
 
+// The root of the factor that takes a state from reference m to M >= m (0 for a
+// state without a reference).
+__device__ __forceinline__ float to_reference_root(float m, float M) {
+  return m == -INFINITY ? 0.f : exp2f(0.5f * (m - M));
+}
+
 // A unit's partial states (unit, first part, parts) merged by log-sum-exp into
 // its output rows by the whole CTA.  Warp w takes head w % G and every
 // (16 / G)-th part: lane i holds the weight of its i-th part, four dims a lane,
@@ -424,12 +434,12 @@ __device__ __forceinline__ void merge_unit(const AttnParams &p, const int4 &m, f
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFullMask, mx, x));
     mx = fmaxf(mx, M);
-    const float c = M == -INFINITY ? 0.f : exp2f(M - mx);
-    const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - mx);
-    float l = f * ml.y;
+    const float c_root = to_reference_root(M, mx), c = c_root * c_root;
+    const float f_root = to_reference_root(ml.x, mx), f = f_root * f_root;
+    float l = f_root * ml.y * f_root;
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) l += __shfl_xor_sync(kFullMask, l, x);
-    L = fmaf(L, c, l);
+    L = fmaf(L * c_root, c_root, l);
     M = mx;
     O.x *= c, O.y *= c, O.z *= c, O.w *= c;
 #pragma unroll 1
@@ -466,9 +476,9 @@ __device__ __forceinline__ void merge_unit(const AttnParams &p, const int4 &m, f
 #pragma unroll
     for (int k = 0; k < NG; ++k) {
       const float *r = s + k * G * ROW;
-      const float f = r[kHeadDim] == -INFINITY ? 0.f : exp2f(r[kHeadDim] - mx);
-      den = fmaf(f, r[kHeadDim + 1], den);
-      num = fmaf(f, r[at % kHeadDim], num);
+      const float root = to_reference_root(r[kHeadDim], mx);
+      den = fmaf(root * r[kHeadDim + 1], root, den);
+      num = fmaf(root * root, r[at % kHeadDim], num);
     }
     p.out[obase + at] = __float2bfloat16_rn(num / den);
   }
@@ -863,9 +873,10 @@ attention_fp8b_kernel(const __grid_constant__ Params pr) {
             const float tm = fmaxf(fmaxf(gred[(rb * 4 + 0) * 8 + h], gred[(rb * 4 + 1) * 8 + h]),
                                    fmaxf(gred[(rb * 4 + 2) * 8 + h], gred[(rb * 4 + 3) * 8 + h]));
             const float mn = fmaxf(m_ref[h], tm);
-            alpha[h] = (m_ref[h] == -INFINITY) ? 0.f : exp2f(m_ref[h] - mn);
+            const float root = to_reference_root(m_ref[h], mn);
+            alpha[h] = root * root;
             m_ref[h] = mn;
-            l_part[h] *= alpha[h];
+            l_part[h] = l_part[h] * root * root;
           }
           if (st > st0) {
             // (the group's last p.v was that of stage su - 2)
@@ -987,11 +998,12 @@ attention_fp8b_kernel(const __grid_constant__ Params pr) {
       for (int h = 0; h < G; ++h) {
         const float m0 = mref[ob * 16 + h], m1 = mref[ob * 16 + 8 + h];
         M[h] = fmaxf(m0, m1);
-        f0[h] = m0 == -INFINITY ? 0.f : exp2f(m0 - M[h]);
-        f1[h] = m1 == -INFINITY ? 0.f : exp2f(m1 - M[h]);
+        const float r0 = to_reference_root(m0, M[h]), r1 = to_reference_root(m1, M[h]);
+        f0[h] = r0 * r0;
+        f1[h] = r1 * r1;
         const float *l0 = lred + ob * 64 + h, *l1 = l0 + 32;
-        Lsum[h] = f0[h] * ((l0[0] + l0[8]) + (l0[16] + l0[24])) +
-                  f1[h] * ((l1[0] + l1[8]) + (l1[16] + l1[24]));
+        Lsum[h] = r0 * ((l0[0] + l0[8]) + (l0[16] + l0[24])) * r0 +
+                  r1 * ((l1[0] + l1[8]) + (l1[16] + l1[24])) * r1;
       }
       wait_or_abort(&o_full[ob], (uint32_t)(k >> 1) & 1u, abort_flag, p.err);
       tc_fence_after();
