@@ -393,7 +393,7 @@ __device__ __forceinline__ void convert_query(const AttnParams &p, const Piece &
 // The root of the factor that takes a state from reference m to M >= m (0 for a
 // state without a reference).
 __device__ __forceinline__ float to_reference_root(float m, float M) {
-  return m == -INFINITY ? 0.f : exp2f(0.5f * (m - M));
+  return m == -INFINITY ? 0.f : exp2_approx(0.5f * (m - M));
 }
 
 // A unit's partial states (unit, first part, parts) merged by log-sum-exp into
