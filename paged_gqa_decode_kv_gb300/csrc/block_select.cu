@@ -470,7 +470,9 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
         const int i = i0 + r + 8 * h, j = jlo + i;
         if (i < n && t == 0) {
           const bool forced = j < p.keep_first || j >= nblk - p.keep_last;
-          const uint32_t score = v.there[h] ? score_key(__float_as_uint(best * v.s[h])) : 0u;
+          // (the maximum: a score that is no number becomes the least)
+          const uint32_t score =
+              v.there[h] ? score_key(__float_as_uint(fmaxf(best * v.s[h], -3.4028235e38f))) : 0u;
           const uint32_t key = forced ? 0xffffffffu : score;
           if (!forced) {
             kmin = min(kmin, key);

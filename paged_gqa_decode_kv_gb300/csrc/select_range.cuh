@@ -18,9 +18,8 @@ constexpr int kRangeBins = 256;
 // 32 bits of keys, 8 taken a pass.
 constexpr int kRangePasses = 4;
 
-// A score's bits as an unsigned integer of the same order; no number: the lowest.
+// A score's bits as an unsigned integer of the same order, above 0.
 PGD_HOST_DEVICE uint32_t score_key(uint32_t bits) {
-  if ((bits & 0x7fffffffu) > 0x7f800000u) return 0u;
   return (bits & 0x80000000u) ? ~bits : (bits | 0x80000000u);
 }
 
