@@ -89,3 +89,93 @@ def test_ranges_whose_items_pass_32_bits(call):
     else:
         for which, got in zip("kv", up):
             assert (bsc.f64(got) == c.rows(which, 0, 18)[15:]).all()
+
+
+@pytest.mark.parametrize("B", [1, 40])
+def test_select_from_the_widest_table(B):
+    """49152 blocks a sequence, every context full, in one cluster and in more than fit side by
+    side."""
+    MB, W = 49152, 700
+    g = torch.Generator().manual_seed(B)
+    lo = torch.randint(-127, 60, (MB, 1, 128), generator=g)
+    hi = torch.minimum(lo + torch.randint(0, 150, lo.shape, generator=g), torch.tensor(127))
+    bounds = torch.stack([lo, hi], 2).to(torch.int8)
+    scales = torch.exp2(torch.randint(-3, 2, (MB, 1), generator=g).float())
+    tables = torch.stack([torch.randperm(MB, generator=g) for _ in range(B)]).to(torch.int32)
+    q = bsc.make_query(B, 4, seed=B)
+    tiles = torch.empty(B, 1, W, dtype=torch.int32, device="cuda")
+    tokens = torch.empty(B, 1, dtype=torch.int32, device="cuda")
+    pgd.select_blocks(tiles, tokens, q.cuda(), bounds.cuda(), scales.cuda(), tables.cuda(),
+                      _i32([MB * 16 - 3]).repeat(B), 2, 5, 16)
+    assert (tokens == W * 16 - 3).all()
+    for b in range(0, B, 13):
+        at = tables[b].long()
+        js = bsc.select(q[b], bsc.f64(bounds[at, 0, 0]), bsc.f64(bounds[at, 0, 1]),
+                        bsc.f64(scales[at, 0]), W, 2, 5)
+        assert torch.equal(tiles[b, 0].cpu(), tables[b, js])
+
+
+@pytest.mark.parametrize("fp8", [True, False])
+def test_pools_past_32_bits_of_bytes(fp8):
+    """The last blocks of pools of more than 2^32 bytes: every call gives what it gives on the same
+    blocks at the start of small pools."""
+    n_kv, G, bs, far = 8, 4, 16, 280000
+    lens = [900, 70]
+    c = bsc.make_cache(lens, n_kv, bs, fp8=fp8, seed=9, room=20)
+    k, v, ks, vs, tables, ctx = c.cuda()
+    small = k.shape[0]
+    big = [torch.empty((far + small, *k.shape[1:]), dtype=k.dtype, device="cuda") for _ in "kv"]
+    assert big[0].nbytes > 1 << 32
+    big[0][far:], big[1][far:] = k, v
+    big_scales = [None, None]
+    if fp8:
+        big_scales = [torch.ones(far + small, n_kv, device="cuda") for _ in "kv"]
+        big_scales[0][far:], big_scales[1][far:] = ks, vs
+    q = bsc.make_query(2, n_kv * G).cuda()
+    rows = [torch.randn(2, 9, n_kv, 128, generator=torch.Generator().manual_seed(i)).to(
+        torch.bfloat16).cuda() for i in range(2)]
+    got = []
+    moved = torch.where(tables < 0, tables, tables + far)
+    for pools, scales, t, at in [((k, v), (ks, vs), tables, 0), (big, big_scales, moved, far)]:
+        kw = dict(k_scales=scales[0], v_scales=scales[1])
+        new = ctx.clone()
+        res = []
+        if fp8:
+            pgd.kv_append_fp8b(*rows, *pools, *scales, t, ctx)
+            new += 9
+            back = [torch.empty_like(x) for x in rows]
+            pgd.kv_read_fp8b(*back, *pools, *scales, t, ctx)
+            res += back + [pgd.paged_decode_attention_fp8b(None, q, *pools, *scales, t, new, SCALE,
+                                                           num_splits=n) for n in (0, 2)]
+        NB = pools[0].shape[0]
+        bounds = torch.zeros(NB, n_kv, 2, 128, dtype=torch.int8, device="cuda")
+        bound_scales = torch.ones(NB, n_kv, device="cuda")
+        pgd.block_bounds(bounds, bound_scales, pools[0], t, new, k_scales=scales[0])
+        tiles = torch.empty(2, n_kv, 12, dtype=torch.int32, device="cuda")
+        tokens = torch.empty(2, n_kv, dtype=torch.int32, device="cuda")
+        res.append(pgd.sparse_decode_attention(None, q, *pools, bounds, bound_scales, t, new, tiles,
+                                               tokens, 1, 2, SCALE, **kw))
+        res += [bounds[at:at + small], bound_scales[at:at + small], tokens,
+                torch.where(tiles < 0, tiles, tiles - at * n_kv)]
+        got.append(res)
+    for x, y in zip(*got):
+        assert torch.equal(x, y)
+
+
+def test_calls_of_no_sequences():
+    """B = 0 through the binding."""
+    c = bsc.make_cache([20], 2, 16, seed=9)
+    k, v, ks, vs, tables, ctx = c.cuda()
+    none, q = ctx[:0], bsc.make_query(1, 8).cuda()[:0]
+    rows = torch.empty(0, 2, 128, dtype=torch.bfloat16, device="cuda")
+    pgd.kv_append_fp8b(rows, rows, k, v, ks, vs, tables[:0], none)
+    pgd.kv_read_fp8b(rows, rows, k, v, ks, vs, tables[:0], none, token_starts=ctx * 0, max_tokens=4)
+    out = pgd.paged_decode_attention_fp8b(None, q, k, v, ks, vs, tables[:0], none, SCALE)
+    assert out.shape == q.shape
+    bounds = torch.zeros(k.shape[0], 2, 2, 128, dtype=torch.int8, device="cuda")
+    scales = torch.ones(k.shape[0], 2, device="cuda")
+    pgd.block_bounds(bounds, scales, k, tables[:0], none, k_scales=ks)
+    tiles = torch.empty(0, 2, 4, dtype=torch.int32, device="cuda")
+    tokens = torch.empty(0, 2, dtype=torch.int32, device="cuda")
+    pgd.sparse_decode_attention(None, q, k, v, bounds, scales, tables[:0], none, tiles, tokens, 1, 2,
+                                SCALE, k_scales=ks, v_scales=vs)
