@@ -847,6 +847,12 @@ def select_blocks(tiles, tile_tokens, q, bounds, bound_scales, block_tables, con
         _check(s)
 
 
+def _need_bounds(bounds) -> None:
+    """(None would make the extension take the tiles as given.)"""
+    if bounds is None:
+        raise TypeError("bounds must be a tensor")
+
+
 def _tiles_attention(pack, out, q, k_cache, v_cache, k_scales, v_scales, bounds, bound_scales,
                      block_tables, context_lens, tiles, tile_tokens, keep_first, keep_last, scale,
                      num_splits, workspace, stream):
@@ -883,8 +889,7 @@ def sparse_decode_attention(out, q, k_cache, v_cache, bounds, bound_scales, bloc
                             stream=None) -> torch.Tensor:
     """select_blocks into tiles and tile_tokens, then
     selected_decode_attention over them, in one call."""
-    if bounds is None:
-        raise TypeError("bounds must be a tensor")
+    _need_bounds(bounds)
     out, _, s = _tiles_attention(False, out, q, k_cache, v_cache, k_scales, v_scales, bounds,
                                  bound_scales, block_tables, context_lens, tiles, tile_tokens,
                                  keep_first, keep_last, scale, num_splits, workspace, stream)
@@ -912,6 +917,7 @@ def _prepared_append8b(out, q, k_new, v_new, k_cache, v_cache, k_scales, v_scale
 def _prepared_sparse(out, q, k_cache, v_cache, bounds, bound_scales, block_tables, context_lens,
                      tiles, tile_tokens, keep_first, keep_last, scale, k_scales=None,
                      v_scales=None, num_splits=0, workspace=None, stream=None):
+    _need_bounds(bounds)
     out, workspace, args = _tiles_attention(True, out, q, k_cache, v_cache, k_scales, v_scales,
                                             bounds, bound_scales, block_tables, context_lens,
                                             tiles, tile_tokens, keep_first, keep_last, scale,
