@@ -179,3 +179,39 @@ def test_calls_of_no_sequences():
     tokens = torch.empty(0, 2, dtype=torch.int32, device="cuda")
     pgd.sparse_decode_attention(None, q, k, v, bounds, scales, tables[:0], none, tiles, tokens, 1, 2,
                                 SCALE, k_scales=ks, v_scales=vs)
+
+
+def test_a_shared_block_copied_before_an_append():
+    """Two sequences that share their last, begun block: the second takes a copy of its tiles, scales
+    and bounds and appends large rows; the first keeps its values, both attend to their own."""
+    c = bsc.make_cache([40, 40], 2, 16, seed=12, room=8)
+    shared, own = int(c.tables[0, 2]), int(c.tables[1, 2])
+    c.tables[1, :2] = c.tables[0, :2]
+    k, v, ks, vs, tables, _ = c.cuda()
+    bounds = torch.zeros(k.shape[0], 2, 2, 128, dtype=torch.int8, device="cuda")
+    bound_scales = torch.ones(k.shape[0], 2, device="cuda")
+    pgd.block_bounds(bounds, bound_scales, k, tables[:1], _i32([40]), k_scales=ks)
+    for x in (k, v, ks, vs, bounds, bound_scales):
+        x[own] = x[shared]
+    for x in (c.k, c.v, c.k_scales, c.v_scales):
+        x[own] = x[shared]
+    before = [x[shared].clone() for x in (k, v, ks, vs, bounds, bound_scales)]
+    g = torch.Generator().manual_seed(3)
+    rows = [(torch.randn(2, 2, 128, generator=g) * 50).to(torch.bfloat16) for _ in range(2)]
+    q = bsc.make_query(2, 8)
+    # (the first sequence appends nothing)
+    pgd.kv_append_fp8b(*(x.cuda() for x in rows), k, v, ks, vs, tables, _i32([40, 40]),
+                       token_starts=_i32([0, 0, 2]), max_tokens=2)
+    pgd.block_bounds(bounds, bound_scales, k, tables, _i32([40, 42]), positions=_i32([40, 40]),
+                     max_tokens=2, k_scales=ks)
+    bsc.append(c, *rows, [40, 40], [0, 0, 2])
+    c.ctx = [40, 42]
+    for x, y in zip((k, v, ks, vs, bounds, bound_scales), before):
+        assert torch.equal(x[shared], y)
+    assert torch.equal(bsc.untile8(k.cpu()), c.k) and torch.equal(vs.cpu(), c.v_scales)
+    for g_ in range(2):
+        lo, hi, s = bsc.bounds(c, 1, 2, g_, 42)
+        assert (bounds[own, g_].cpu().numpy() == [lo, hi]).all()
+        assert float(bound_scales[own, g_]) == s
+    got = pgd.paged_decode_attention_fp8b(None, q.cuda(), k, v, ks, vs, tables, _i32([40, 42]), SCALE)
+    bsc.close(got, *bsc.paged(c, q, SCALE))
