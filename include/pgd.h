@@ -126,7 +126,8 @@ pgd_status pgd_kv_append(const void *k_new, const void *v_new, void *k_cache, vo
  * into parts whose (max, sum, weighted-sum) states are merged by log-sum-exp
  * ("The math of Transformer inference", section 8, sharding the KV cache
  * along the sequence; "LLM inference systems engineering", 2.8.3).
- * Arithmetic: bf16 inputs, fp32 accumulation, fp32 softmax, bf16 output
+ * Arithmetic: bf16 inputs, fp32 accumulation, fp32 softmax (its probabilities
+ * rounded to bf16 where the tensor cores take them for p.v), bf16 output
  * rounded to nearest even.
  *
  * num_splits: 0 = automatic: one CTA per SM; the kernel reads the context
@@ -488,15 +489,19 @@ pgd_status pgd_append_decode_attention_fp8(void *out, const void *q, const void 
  *     code  = E4M3(x / scale), rounding to nearest even, saturating to +-448;
  *             a NaN is stored as NaN
  * The slots behind the last new token keep their codes and hold no token.  A
- * block of several sequences must not be appended to (copy on write first).
+ * block of several sequences must not be appended to: copy it first.  That copy
+ * is the caller's, as pgd_copy_blocks copies bf16 pools: the n_kv tiles and
+ * scales of both pools, each contiguous at its block, and where key bounds are
+ * kept (below) the block's bounds and bound scales.
  * A range outside [0, MB*bs) or starts that break the rules above set
  * PGD_DEVERR_BAD_POSITION and write nothing for that sequence; a bad block id
  * skips its block.
  *
  * pgd_kv_read_fp8b is the way back: rows token_starts[b] .. of k_out and v_out
  * (bf16 [N][n_kv][d]) become the values at positions[b] on, rounded to bf16
- * (exact for the scales the writer makes).  Same arguments, rules and errors;
- * rows that belong to no sequence are left as they were.
+ * (exact for the scales the writer makes; for other scales the fp32 product is
+ * what is rounded, as the fp32 quotient is in a write).  Same arguments, rules
+ * and errors; rows that belong to no sequence are left as they were.
  *
  * pgd_paged_decode_attention_fp8b, pgd_append_decode_attention_fp8b: the calls
  * of those names over this cache -- same definition on the dequantised K and

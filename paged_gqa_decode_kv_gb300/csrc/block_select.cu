@@ -89,8 +89,8 @@ __device__ __forceinline__ uint4 load_once(const uint4 *p, bool there) {
 // the negated largest by halves: a lane keeps one half of the values and sends
 // the other, and ends with the lower bounds (l % 4 < 2) or the negated upper
 // bounds of a few dims over all tokens.  Bound by the read of the keys (bf16)
-// and by issue slots (8-bit): 84k tokens of bf16 23.7 us, 115k of 8 bits and 10
-// heads 34.8.  (One slot a lane, eight lanes a chunk: 25.7 and 43.0, of which
+// and by the ALU pipe (8-bit: 80 % busy with conversions and minima): 84k tokens
+// of bf16 24.2 us, 115k of 8 bits and 10 heads 34.6.  (One slot a lane, eight lanes a chunk: 25.7 and 43.0, of which
 // the minimum of -k instead of the maximum 0.6 and 2.9.)
 template <int BS, bool FP8, bool STREAM>
 __device__ __forceinline__ void tile_bounds(const BoundsParams &p, size_t tile, int valid,
@@ -296,10 +296,10 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
 //    same histograms say how many blocks the slices before ours take, so the
 //    places to write need no further exchange.
 // 3. Every warp counts, then writes, its own part of the slice in order.
-// 8 heads of 8192 blocks: 11.7 us, in clusters of 12; 7.8k of its 21k cycles go
+// 8 heads of 8192 blocks: 11.6 us, in clusters of 12; 7.8k of its 21k cycles go
 // to the scores (29 bytes a cycle and SM; loads further ahead, and prefetches
 // to L2, took longer), about 2k to each of three exchanges.  16 x 8 heads of 512
-// blocks: 7.9 us, the scores at 5 TB/s.
+// blocks: 7.8 us, the scores at 5 TB/s.
 template <int G, bool CLUSTER>
 __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams p, int cluster) {
   const int C = CLUSTER ? cluster : 1;

@@ -14,8 +14,9 @@
 // where it grows, the earlier slots' codes are encoded again for the new
 // scale.  The slots behind the last new token are not touched: they hold no
 // token.  NaN is stored as NaN; an infinity saturates.
-// Read: lane l has dims 16 c .. + 15; bf16(E4M3(code) * scale), one rounding
-// (none for power-of-two scales).
+// Read: lane l has dims 16 c .. + 15; bf16(E4M3(code) * scale): exact for
+// power-of-two scales, else an fp32 product rounded to bf16 (two roundings, as
+// a write with such a scale rounds an fp32 quotient to E4M3).
 //
 // Both are bound by memory: 2 + 1 bytes per value.  What is rare (values that
 // are not finite, growing a begun block, a caller's scale that is no power of
