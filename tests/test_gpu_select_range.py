@@ -118,3 +118,31 @@ def test_a_score_that_is_no_number_is_the_lowest():
     assert set(tiles[0, 0].tolist()) <= {int(c.tables[0, j]) for j in left}
     tiles, _ = _select(c, q, bounds, scales, 55, 0, 1)
     assert tiles[0, 0].tolist() == [int(c.tables[0, j]) for j in [*range(15), *range(60, 100)]]
+
+
+@pytest.mark.parametrize("G", [1, 4, 8])
+@pytest.mark.parametrize("ctx", [[1600, 900], [20000, 5000]], ids=str)
+def test_scores_that_are_zero_in_many_ways(ctx, G):
+    """Blocks of zero bounds, and small bounds that meet few query elements: sums that cancel to 0,
+    which tie with those that are 0 throughout."""
+    c, bounds, scales, q = _case(ctx, 2, G, seed=20 + G)
+    g = torch.Generator().manual_seed(G)
+    lo = torch.randint(-1, 2, bounds[:, :, 0].shape, generator=g)
+    hi = torch.maximum(lo, torch.randint(-1, 2, lo.shape, generator=g))
+    bounds = torch.stack([lo, hi], 2).to(torch.int8)
+    bounds[torch.rand(bounds.shape[0], generator=g) < 0.3] = 0
+    few = torch.zeros_like(q)
+    few[..., 5], few[..., 70], few[..., 71] = 1.0, -1.0, 0.5
+    tiles, tokens = _select(c, few, bounds, scales, 40, 1, 2)
+    assert torch.equal(tiles, _want(c, few, bounds, scales, 40, 1, 2))
+    _check_form(c, tiles, tokens, 40, 1, 2)
+
+
+def test_heads_far_apart():
+    """Eight heads 2^3 apart, the largest with no positive score anywhere: the others decide."""
+    c, bounds, scales, q = _case([1600, 5000], 2, 8, seed=33)
+    q = (q.double() * torch.exp2(-3.0 * (torch.arange(16) % 8).double())[:, None]).to(torch.bfloat16)
+    q[:, ::8] = q[:, ::8].abs()
+    bounds = torch.minimum(bounds, torch.tensor(0, dtype=torch.int8))
+    tiles, _ = _select(c, q, bounds, scales, 40, 1, 2)
+    assert torch.equal(tiles, _want(c, q, bounds, scales, 40, 1, 2))
