@@ -549,6 +549,190 @@ pgd_status pgd_append_decode_attention_fp8b(
     float scale, int32_t num_splits, void *workspace, size_t workspace_bytes, void *stream);
 
 /* ---------------------------------------------------------------------- */
+/* 4-bit KV cache: E2M1 codes, one E4M3 scale per token, head and 16 dims  */
+/* ---------------------------------------------------------------------- */
+/* 0.5625 bytes per value where the 8-bit caches above take 1.03 and 1.004
+ * ("Module 10", section "Quantize the cache, evaluate the final artifact";
+ * "The math of Transformer inference", section 11: the bytes of the cache set
+ * the decode step's time).
+ *
+ * Layout: k_cache, v_cache uint8 [NB][n_kv][bs/16][1152], 16-byte aligned: per
+ * 16 tokens of a tile 1024 bytes of codes, then 128 of scales.  K: dims 2 j
+ * (low nibble) and 2 j + 1 of token t at t * 64 + j, the scale of dims 16 g ..
+ * 16 g + 15 at 1024 + t * 8 + g.  V: dim i of token t in the byte (i/64) * 512 +
+ * (i%8) * 64 + (t/4) * 16 + (i/8%8) * 2 + (t%4)/2, the even token in the low
+ * nibble, the scale at 1024 + (t/4) * 32 + g * 4 + t%4.  A code's low three bits
+ * stand for 0, 0.5, 1, 1.5, 2, 3, 4, 6, its fourth for the sign; the value is
+ * E2M1(code) * E4M3(scale) * S, S being the call's k_scale or v_scale: a power
+ * of two from 2^-32 to 2^32, the same for every call on a cache (1 covers
+ * groups whose largest value lies between 0.012 and 2688; another moves that
+ * range).
+ *
+ * pgd_kv_append_fp4 writes new tokens: the arguments and rules of
+ * pgd_kv_append_fp8b (ranges of positions, token_starts, T, N).  For 16 dims of
+ * a token with m = max |x|:
+ *     scale = E4M3(m / 6 / S)             both roundings to nearest, ties to
+ *     code  = E2M1(x / (scale * S))       the even code, saturating (448, 6)
+ * A scale of 0 has codes of 0; an infinity saturates; a NaN makes the scale, and
+ * so the 16 values, NaN.  No other token's values change.  A block of several
+ * sequences must not be appended to: copy it first (pgd_copy_blocks_fp4).
+ *
+ * pgd_kv_read_fp4 is the way back: rows token_starts[b] .. of k_out and v_out
+ * (bf16 [N][n_kv][d]) become the values at positions[b] on (exact in bf16 but
+ * below its normal range).  Rows that belong to no sequence are left as they
+ * were.
+ *
+ * pgd_paged_decode_attention_fp4, pgd_append_decode_attention_fp4: the calls of
+ * those names over this cache -- same definition on the values that it stands
+ * for, same arguments, checks and errors.  The append is pgd_kv_append_fp4 of
+ * one token at context_lens[b] - 1.  The query must be finite.  B * n_kv at most
+ * 65536, B * n_kv * MB * bs below 2^35.  Arithmetic: q.k^T and p.v on f16
+ * operands with fp32 accumulation -- K, V and the query exact (a query's element
+ * to 2^-39 of its largest), a probability to 2^-11 of itself and 2^-32 of the
+ * largest; softmax and sums in fp32; bf16 output.
+ *
+ * workspace: device scratch of pgd_fp4_workspace_size(...) bytes (0 for
+ * arguments outside the limits), 256-byte aligned, zero-filled before its first
+ * use.  Completed calls leave it ready for the next of any sizes up to those it
+ * was made for, in stream order; a workspace of the block-scaled calls that is
+ * large enough serves too.  Concurrent calls need separate ones. */
+size_t pgd_fp4_workspace_size(int32_t B, int32_t n_q, int32_t n_kv, int32_t d,
+                              int32_t num_splits);
+pgd_status pgd_kv_append_fp4(const void *k_new, const void *v_new, void *k_cache, void *v_cache,
+                             const int32_t *block_tables, const int32_t *positions,
+                             const int32_t *token_starts, int32_t B, int32_t T, int32_t N,
+                             int32_t n_kv, int32_t d, int32_t bs, int32_t MB, int32_t NB,
+                             float k_scale, float v_scale, void *stream);
+pgd_status pgd_kv_read_fp4(void *k_out, void *v_out, const void *k_cache, const void *v_cache,
+                           const int32_t *block_tables, const int32_t *positions,
+                           const int32_t *token_starts, int32_t B, int32_t T, int32_t N,
+                           int32_t n_kv, int32_t d, int32_t bs, int32_t MB, int32_t NB,
+                           float k_scale, float v_scale, void *stream);
+pgd_status pgd_paged_decode_attention_fp4(void *out, const void *q, const void *k_cache,
+                                          const void *v_cache, const int32_t *block_tables,
+                                          const int32_t *context_lens, int32_t B, int32_t n_q,
+                                          int32_t n_kv, int32_t d, int32_t bs, int32_t MB,
+                                          int32_t NB, float scale, float k_scale, float v_scale,
+                                          int32_t num_splits, void *workspace,
+                                          size_t workspace_bytes, void *stream);
+pgd_status pgd_append_decode_attention_fp4(
+    void *out, const void *q, const void *k_new, const void *v_new, void *k_cache, void *v_cache,
+    const int32_t *block_tables, const int32_t *context_lens, int32_t B, int32_t n_q,
+    int32_t n_kv, int32_t d, int32_t bs, int32_t MB, int32_t NB, float scale, float k_scale,
+    float v_scale, int32_t num_splits, void *workspace, size_t workspace_bytes, void *stream);
+
+/* ---------------------------------------------------------------------- */
+/* rotary positions                                                        */
+/* ---------------------------------------------------------------------- */
+/* Queries and keys turned by their positions before the keys are cached ("The
+ * math of Transformer inference", section 1: what a cached key holds; the MLA
+ * section: 64 of the 576 cached values are a rotated key).  The pairs i <
+ * rotary / 2 of dims first .. first + rotary - 1 of every head, (i, i + rotary/2)
+ * or with `interleaved` (2 i, 2 i + 1), become
+ *     (x1, x2) -> factor * (x1 cos a - x2 sin a, x2 cos a + x1 sin a),
+ *     a = position * f_i
+ * computed in fp32 and rounded once to bf16; the other dims are copied.
+ *
+ * frequencies: device int64 [rotary / 2], f_i as turns per position in units of
+ * 2^-64 (radians / 2 pi * 2^64, modulo 2^64): the product with any int32
+ * position wraps to the exact fraction of a turn, however far the position.
+ * pgd_rope_frequencies fills a host array: f_i = base^(-2 i / rotary), scaled for
+ * contexts longer than the model was trained on:
+ *   PGD_ROPE_PLAIN            as it is
+ *   PGD_ROPE_LINEAR           f_i / factor
+ *   PGD_ROPE_BASE             base * factor^(rotary / (rotary - 2))
+ *   PGD_ROPE_RAMP_DIM         f_i for pairs below the one that makes fast_turns
+ *                             turns in original_context positions (rounded
+ *                             down), f_i / factor above the one that makes
+ *                             slow_turns (rounded up), a line in i between
+ *   PGD_ROPE_RAMP_WAVELENGTH  f_i for pairs that make fast_turns or more,
+ *                             f_i / factor for slow_turns or fewer, a line in
+ *                             the number of turns between
+ * (original_context, slow_turns and fast_turns are read by the ramps alone.)
+ *
+ * pgd_rope: T tokens' rows, q [T][n_q][d] to q_out and k [T][n_kv][d] to k_out
+ * (bf16; n_q or n_kv 0: none); positions device int32 [T].  strides NULL: dense;
+ * else host int64 [8], elements between tokens and between heads of q_out, k_out,
+ * q, k in that order (heads of one projection's output lie side by side).  An
+ * output may be its input (same address and strides); no other overlap.
+ * d a multiple of 16 up to 2048, first of 8, rotary of 16, strides of 8, rows
+ * 16-byte aligned.
+ *
+ * pgd_rope_append: the same with K written into the paged bf16 cache and V copied
+ * beside it (d = 128): token t at slots[t] = block * bs + slot (device int64 [T],
+ * as pgd_grow_tables gives them).  A token whose slot is negative is left out
+ * altogether (the padding of a captured batch), one past the pool too, and sets
+ * PGD_DEVERR_BAD_POSITION.  strides: of q_out, q, k, v.  Slots must differ. */
+#define PGD_ROPE_PLAIN 0
+#define PGD_ROPE_LINEAR 1
+#define PGD_ROPE_BASE 2
+#define PGD_ROPE_RAMP_DIM 3
+#define PGD_ROPE_RAMP_WAVELENGTH 4
+pgd_status pgd_rope_frequencies(int64_t *freq_h, int32_t rotary, double base, int32_t scaling,
+                                double factor, double original_context, double slow_turns,
+                                double fast_turns);
+pgd_status pgd_rope(void *q_out, void *k_out, const void *q, const void *k,
+                    const int32_t *positions, const int64_t *frequencies, int32_t T, int32_t n_q,
+                    int32_t n_kv, int32_t d, int32_t first, int32_t rotary, int32_t interleaved,
+                    float factor, const int64_t *strides, void *stream);
+pgd_status pgd_rope_append(void *q_out, const void *q, const void *k, const void *v, void *k_cache,
+                           void *v_cache, const int64_t *slots, const int32_t *positions,
+                           const int64_t *frequencies, int32_t T, int32_t n_q, int32_t n_kv,
+                           int32_t d, int32_t bs, int32_t NB, int32_t first, int32_t rotary,
+                           int32_t interleaved, float factor, const int64_t *strides,
+                           void *stream);
+
+/* ---------------------------------------------------------------------- */
+/* block tables grown and cut on the GPU                                   */
+/* ---------------------------------------------------------------------- */
+/* The host allocator's work (below) for a batch at once, on device state, so
+ * that a captured step can grow its own tables ("Module 10", sections "Mapping
+ * logical positions to physical blocks" and "Share only identical state"; "Ch.
+ * 6", 6.4).  State, all device memory: block_tables int32 [B][MB], context_lens
+ * int32 [B] (tokens cached), refs int32 [NB] (references of every block) and
+ * free_bits int32 [(NB + 31) / 32] (bit id % 32 of word id / 32: block id is
+ * free, which it is exactly where refs[id] is 0).  To share a block, put its id
+ * in another row and add to its refs.
+ *
+ * pgd_grow_tables adds new_tokens[b] (>= 0) tokens to every row.  A row takes
+ * the blocks that its new tokens reach; a row whose last block is partly filled
+ * and has refs above 1 takes one more in its place and drops its reference
+ * (copy_src[b], copy_dst[b]: the pair to copy before anything is written,
+ * pgd_copy_blocks or pgd_copy_blocks_fp4 with n = B; -1, -1 where there is
+ * none).  Rows that share such a block each take a copy, the last of them too;
+ * a block that loses its last reference so is free for later calls.  Blocks are
+ * given out in the order of the rows, the lowest free ids first.  Outputs:
+ *   positions[b]        the row's length before (int32 [B])
+ *   context_lens[b]     its new length
+ *   token_starts[b]     new tokens of the rows before (int32 [B + 1])
+ *   slots[n], token_positions[n]   block * bs + slot (int64) and position (int32)
+ *                       of new token n, rows in order; -1 and 0 from the last
+ *                       new token to N
+ *   result[0..3]        0 done, 1 too few free blocks, 2 more than N new
+ *                       tokens; blocks taken; blocks that were missing; tokens
+ * Where result[0] is not 0 nothing changes: token_starts are 0, slots -1,
+ * copies -1, so that the step's appends write nothing.  (2 also sets
+ * PGD_DEVERR_BAD_POSITION.)  A row with a negative length or count, or more than
+ * MB * bs tokens, sets PGD_DEVERR_BAD_CONTEXT, one whose last block's id is bad
+ * PGD_DEVERR_BAD_BLOCK_ID; it gets no tokens.  B at most 16384.
+ *
+ * pgd_trim_tables cuts row b to keep_lens[b] tokens (no change where it has no
+ * more; 0 releases the request): entries behind them become -1, their blocks
+ * lose a reference and are free where it was the last ("Module 10", "Verify a
+ * chain, then roll back uncommitted state").  A negative keep_lens[b] or a bad
+ * length changes nothing and sets PGD_DEVERR_BAD_CONTEXT; a bad id, or one
+ * without references, sets PGD_DEVERR_BAD_BLOCK_ID. */
+pgd_status pgd_grow_tables(int32_t *block_tables, int32_t *context_lens,
+                           const int32_t *new_tokens, int32_t *refs, int32_t *free_bits,
+                           int32_t *positions, int32_t *token_starts, int64_t *slots,
+                           int32_t *token_positions, int32_t *copy_src, int32_t *copy_dst,
+                           int32_t *result, int32_t B, int32_t N, int32_t bs, int32_t MB,
+                           int32_t NB, void *stream);
+pgd_status pgd_trim_tables(int32_t *block_tables, int32_t *context_lens,
+                           const int32_t *keep_lens, int32_t *refs, int32_t *free_bits, int32_t B,
+                           int32_t bs, int32_t MB, int32_t NB, void *stream);
+
+/* ---------------------------------------------------------------------- */
 /* block-sparse decode attention                                           */
 /* ---------------------------------------------------------------------- */
 /* Decode attention that reads W blocks of each context instead of all of it:
@@ -671,11 +855,16 @@ pgd_status pgd_decode_step_fp8(void *out_h, const void *q_h, const void *k_new_h
  * bs slots, K and V).  The device half of copy-on-write: a sequence that must
  * write into a block other sequences share first gets a private copy ("Module
  * 10", section "Share only identical state"; "Ch. 6", 6.4).  src_ids and
- * dst_ids are device arrays; a pair with an id outside [0, NB) is skipped and
- * flagged.  Source and destination blocks must not overlap. */
+ * dst_ids are device arrays; a pair (-1, -1) is a place without one, another
+ * pair with an id outside [0, NB) is skipped and flagged.  Source and
+ * destination blocks must not overlap.  pgd_copy_blocks_fp4: the same on pools of
+ * the 4-bit cache. */
 pgd_status pgd_copy_blocks(void *k_cache, void *v_cache, const int32_t *src_ids,
                            const int32_t *dst_ids, int32_t n, int32_t n_kv, int32_t d,
                            int32_t bs, int32_t NB, void *stream);
+pgd_status pgd_copy_blocks_fp4(void *k_cache, void *v_cache, const int32_t *src_ids,
+                               const int32_t *dst_ids, int32_t n, int32_t n_kv, int32_t d,
+                               int32_t bs, int32_t NB, void *stream);
 
 /* ---------------------------------------------------------------------- */
 /* measurement: read-only streaming bandwidth                              */

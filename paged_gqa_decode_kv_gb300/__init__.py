@@ -14,6 +14,9 @@ from ._native import (  # noqa: F401
     cascade_decode_attention, cascade_workspace_size, kv_append_tokens, paged_verify_attention,
     kv_append_fp8b, kv_read_fp8b, paged_decode_attention_fp8b, append_decode_attention_fp8b,
     block_workspace_size, make_block_workspace, block_bounds, select_blocks, selected_decode_attention, sparse_decode_attention,
+    kv_append_fp4, kv_read_fp4, paged_decode_attention_fp4, append_decode_attention_fp4,
+    fp4_workspace_size, make_fp4_workspace, pool_shape4, rope, rope_append, rope_frequencies,
+    grow_tables, trim_tables, make_block_pool,
     append_verify_attention, verify_step, verify_workspace_size, mla_append, mla_decode_attention,
     mla_append_decode_attention, mla_step, mla_workspace_size, device_errors,
     workspace_size, make_workspace, attention_grid, validate_tables, read_stream, set_wait_limit_ns,
@@ -29,6 +32,10 @@ __all__ = ["WORKLOADS", "Workload", "PagedBatch", "make_batch", "make_workload",
            "paged_decode_attention_fp8b", "append_decode_attention_fp8b", "block_workspace_size",
            "make_block_workspace", "block_bounds",
            "select_blocks", "selected_decode_attention", "sparse_decode_attention", "cascade_decode_attention", "cascade_workspace_size",
+           "kv_append_fp4", "kv_read_fp4", "paged_decode_attention_fp4",
+           "append_decode_attention_fp4", "fp4_workspace_size", "make_fp4_workspace",
+           "pool_shape4", "rope", "rope_append", "rope_frequencies", "grow_tables",
+           "trim_tables", "make_block_pool",
            "kv_append_tokens", "paged_verify_attention", "append_verify_attention",
            "verify_step", "verify_workspace_size",
            "mla_append", "mla_decode_attention", "mla_append_decode_attention", "mla_step",

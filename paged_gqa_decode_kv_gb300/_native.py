@@ -27,6 +27,7 @@ DEVERR_BAD_BLOCK_ID, DEVERR_BAD_CONTEXT, DEVERR_BAD_POSITION, DEVERR_TIMEOUT = 1
 
 #: every symbol include/pgd.h declares, with (argtypes, restype)
 _P, _I, _F, _Z = ctypes.c_void_p, ctypes.c_int32, ctypes.c_float, ctypes.c_size_t
+_D = ctypes.c_double
 SIGNATURES = {
     "pgd_status_string": ([_I], ctypes.c_char_p),
     "pgd_last_error_detail": ([], ctypes.c_char_p),
@@ -77,6 +78,17 @@ SIGNATURES = {
     "pgd_select_blocks": ([_P] * 7 + [_I] * 10 + [_P], _I),
     "pgd_selected_decode_attention": ([_P] * 8 + [_I] * 7 + [_F, _I, _P, _Z, _P], _I),
     "pgd_sparse_decode_attention": ([_P] * 12 + [_I] * 10 + [_F, _I, _P, _Z, _P], _I),
+    "pgd_fp4_workspace_size": ([_I, _I, _I, _I, _I], _Z),
+    "pgd_kv_append_fp4": ([_P] * 7 + [_I] * 8 + [_F, _F, _P], _I),
+    "pgd_kv_read_fp4": ([_P] * 7 + [_I] * 8 + [_F, _F, _P], _I),
+    "pgd_paged_decode_attention_fp4": ([_P] * 6 + [_I] * 7 + [_F, _F, _F, _I, _P, _Z, _P], _I),
+    "pgd_append_decode_attention_fp4": ([_P] * 8 + [_I] * 7 + [_F, _F, _F, _I, _P, _Z, _P], _I),
+    "pgd_rope_frequencies": ([_P, _I, _D, _I, _D, _D, _D, _D], _I),
+    "pgd_rope": ([_P] * 6 + [_I] * 7 + [_F, _P, _P], _I),
+    "pgd_rope_append": ([_P] * 9 + [_I] * 9 + [_F, _P, _P], _I),
+    "pgd_grow_tables": ([_P] * 12 + [_I] * 5 + [_P], _I),
+    "pgd_trim_tables": ([_P] * 5 + [_I] * 4 + [_P], _I),
+    "pgd_copy_blocks_fp4": ([_P, _P, _P, _P, _I, _I, _I, _I, _I, _P], _I),
     "pgd_copy_blocks": ([_P, _P, _P, _P, _I, _I, _I, _I, _I, _P], _I),
     "pgd_device_errors": ([_P, _I, _P], _I),
     "pgd_read_stream": ([_P, _Z, _I, _P], _I),
@@ -364,7 +376,8 @@ def prepare(op: str, *args, **kwargs) -> PreparedCall:
     takes: "paged_decode_attention", "paged_decode_attention_fp8",
     "append_decode_attention", "append_decode_attention_fp8", "decode_step",
     "append_verify_attention", "verify_step", "paged_decode_attention_fp8b",
-    "append_decode_attention_fp8b" or "sparse_decode_attention"."""
+    "append_decode_attention_fp8b", "sparse_decode_attention",
+    "paged_decode_attention_fp4" or "append_decode_attention_fp4"."""
     if op == "paged_decode_attention":
         return PreparedCall(*_attention_call(False, *args, **kwargs))
     if op == "paged_decode_attention_fp8":
@@ -385,6 +398,10 @@ def prepare(op: str, *args, **kwargs) -> PreparedCall:
         return PreparedCall(*_prepared_append8b(*args, **kwargs))
     if op == "sparse_decode_attention":
         return PreparedCall(*_prepared_sparse(*args, **kwargs))
+    if op == "paged_decode_attention_fp4":
+        return PreparedCall(*_prepared4(*args, **kwargs))
+    if op == "append_decode_attention_fp4":
+        return PreparedCall(*_prepared_append4(*args, **kwargs))
     raise ValueError("no prepared form of %r" % op)
 
 
@@ -821,6 +838,224 @@ def append_decode_attention_fp8b(out, q, k_new, v_new, k_cache, v_cache, k_scale
     return out
 
 
+# ------------------------------------------------------------- 4-bit KV cache
+GROUP_BYTES4 = 1152  # 16 tokens of a tile: 1024 of codes, 128 of scales
+
+
+def pool_shape4(num_blocks: int, n_kv: int, block_size: int) -> Tuple[int, int, int, int]:
+    """Shape of a 4-bit pool (uint8)."""
+    return num_blocks, n_kv, block_size // 16, GROUP_BYTES4
+
+
+def _cache4_dims(pool: torch.Tensor) -> Tuple[int, int, int, int]:
+    """(NB, n_kv, bs, d) of a 4-bit pool uint8 [NB][n_kv][bs/16][1152]."""
+    if pool.dim() != 4 or pool.shape[3] != GROUP_BYTES4:
+        raise ValueError("4-bit cache must be uint8 [NB][n_kv][bs/16][%d]" % GROUP_BYTES4)
+    NB, n_kv, ng, _ = pool.shape
+    return NB, n_kv, ng * 16, HEAD_DIM
+
+
+def fp4_workspace_size(B: int, n_q: int, n_kv: int, num_splits: int = 0,
+                       d: int = HEAD_DIM) -> int:
+    return int(lib().pgd_fp4_workspace_size(B, n_q, n_kv, d, num_splits))
+
+
+def make_fp4_workspace(B: int, n_q: int, n_kv: int, num_splits: int = 0,
+                       device=None) -> torch.Tensor:
+    """A zero-filled workspace of the 4-bit attention calls; one serves calls of
+    any sizes up to these, in stream order."""
+    n = max(1, fp4_workspace_size(B, n_q, n_kv, num_splits))
+    return torch.zeros(n, dtype=torch.uint8, device=device or torch.device("cuda"))
+
+
+def kv_append_fp4(k_new, v_new, k_cache, v_cache, block_tables, positions, token_starts=None,
+                  max_tokens: Optional[int] = None, k_scale: float = 1.0, v_scale: float = 1.0,
+                  stream=None) -> None:
+    """Quantise new tokens into the 4-bit pools (uint8 [NB][n_kv][bs/16][1152])
+    at positions[b] on: rows token_starts[b] .. token_starts[b + 1] - 1 of
+    k_new/v_new ([N][n_kv][d] bf16; at most max_tokens each), or without
+    token_starts the same number of tokens for every sequence ([B][n_kv][d] or
+    [B][T][n_kv][d]).  k_scale, v_scale: powers of two, the cache's own."""
+    s = (_tensor_side or _tensors()).range4(False, k_new, v_new, k_cache, v_cache, block_tables,
+                                            positions, token_starts, max_tokens, k_scale, v_scale,
+                                            stream)
+    if s:
+        _check(s)
+
+
+def kv_read_fp4(k_out, v_out, k_cache, v_cache, block_tables, positions, token_starts=None,
+                max_tokens: Optional[int] = None, k_scale: float = 1.0, v_scale: float = 1.0,
+                stream=None) -> None:
+    """Read ranges of positions back into rows of k_out/v_out (bf16): the
+    arguments of kv_append_fp4, the other way."""
+    s = (_tensor_side or _tensors()).range4(True, k_out, v_out, k_cache, v_cache, block_tables,
+                                            positions, token_starts, max_tokens, k_scale, v_scale,
+                                            stream)
+    if s:
+        _check(s)
+
+
+def _attention4(pack, out, q, k_new, v_new, k_cache, v_cache, block_tables, context_lens, scale,
+                k_scale, v_scale, num_splits, workspace, stream):
+    if out is None or workspace is None:
+        if not isinstance(q, torch.Tensor) or q.dim() != 3:
+            raise ValueError("q must be [B][n_q][d]")
+        if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
+            raise ValueError("k_cache must be a 4-bit pool")
+        if not q.is_cuda:
+            raise ValueError("q must be on a CUDA device")
+        if out is None:
+            out = _made_for(stream, lambda: torch.empty_like(q), result=True)
+        if workspace is None:
+            workspace = _made_for(stream, lambda: make_fp4_workspace(
+                q.shape[0], q.shape[1], k_cache.shape[1], num_splits, q.device))
+    return out, workspace, (_tensor_side or _tensors()).attention4(
+        out, q, k_new, v_new, k_cache, v_cache, block_tables, context_lens, scale, k_scale,
+        v_scale, num_splits, workspace, stream, pack)
+
+
+def paged_decode_attention_fp4(out, q, k_cache, v_cache, block_tables, context_lens, scale: float,
+                               k_scale: float = 1.0, v_scale: float = 1.0, num_splits: int = 0,
+                               workspace: Optional[torch.Tensor] = None,
+                               stream=None) -> torch.Tensor:
+    """out[B][n_q][d] (bf16) = paged decode attention of q over the 4-bit
+    cache."""
+    out, _, s = _attention4(False, out, q, None, None, k_cache, v_cache, block_tables,
+                            context_lens, scale, k_scale, v_scale, num_splits, workspace, stream)
+    if s:
+        _check(s)
+    return out
+
+
+def append_decode_attention_fp4(out, q, k_new, v_new, k_cache, v_cache, block_tables,
+                                context_lens, scale: float, k_scale: float = 1.0,
+                                v_scale: float = 1.0, num_splits: int = 0,
+                                workspace: Optional[torch.Tensor] = None,
+                                stream=None) -> torch.Tensor:
+    """kv_append_fp4 of one token per sequence at context_lens - 1, then
+    attention over the 4-bit cache."""
+    if k_new is None or v_new is None:
+        raise TypeError("k_new and v_new must be tensors")
+    out, _, s = _attention4(False, out, q, k_new, v_new, k_cache, v_cache, block_tables,
+                            context_lens, scale, k_scale, v_scale, num_splits, workspace, stream)
+    if s:
+        _check(s)
+    return out
+
+
+def _prepared4(out, q, k_cache, v_cache, block_tables, context_lens, scale, k_scale=1.0,
+               v_scale=1.0, num_splits=0, workspace=None, stream=None):
+    out, workspace, args = _attention4(True, out, q, None, None, k_cache, v_cache, block_tables,
+                                       context_lens, scale, k_scale, v_scale, num_splits,
+                                       workspace, stream)
+    return "pgd_paged_decode_attention_fp4", args, out, workspace
+
+
+def _prepared_append4(out, q, k_new, v_new, k_cache, v_cache, block_tables, context_lens, scale,
+                      k_scale=1.0, v_scale=1.0, num_splits=0, workspace=None, stream=None):
+    if k_new is None or v_new is None:
+        raise TypeError("k_new and v_new must be tensors")
+    out, workspace, args = _attention4(True, out, q, k_new, v_new, k_cache, v_cache, block_tables,
+                                       context_lens, scale, k_scale, v_scale, num_splits,
+                                       workspace, stream)
+    return "pgd_append_decode_attention_fp4", args, out, workspace
+
+
+# ------------------------------------------------------------ rotary positions
+ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "ramp_dim": 3, "ramp_wavelength": 4}
+
+
+def rope_frequencies(rotary: int, base: float = 10000.0, scaling: str = "none",
+                     factor: float = 1.0, original_context: float = 0.0, slow_turns: float = 1.0,
+                     fast_turns: float = 32.0, device=None) -> torch.Tensor:
+    """The frequencies of `rotary` rotated dims as rope and rope_append take
+    them (int64 [rotary / 2], turns a position in units of 2^-64), scaled for
+    long contexts by "linear", "base", "ramp_dim" or "ramp_wavelength" (see
+    pgd_rope_frequencies).  device None: the current CUDA device."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError("scaling must be one of %s, got %r" % (sorted(ROPE_SCALINGS), scaling))
+    buf = (ctypes.c_int64 * max(1, int(rotary) // 2))()
+    _check(lib().pgd_rope_frequencies(ctypes.addressof(buf), int(rotary), float(base),
+                                      ROPE_SCALINGS[scaling], float(factor),
+                                      float(original_context), float(slow_turns),
+                                      float(fast_turns)))
+    t = torch.tensor(list(buf), dtype=torch.int64)
+    return t.to(device if device is not None else torch.device("cuda"))
+
+
+def rope(q_out, k_out, q, k, positions, frequencies, interleaved: bool = False, first: int = 0,
+         factor: float = 1.0, stream=None):
+    """Rotary positions: rows q [T][n_q][d] to q_out and k [T][n_kv][d] to k_out
+    (bf16; strided over tokens and heads as views of one projection's output
+    are; an output may be its input, None makes it; k None: q alone), positions
+    int32 [T], the rotated dims first .. first + 2 * len(frequencies) - 1 as
+    halves or as interleaved pairs, cosine and sine times `factor`.  Returns
+    q_out, k_out."""
+    if q_out is None:
+        q_out = _made_for(stream, lambda: torch.empty(q.shape, dtype=q.dtype, device=q.device),
+                          result=True)
+    if k is not None and k_out is None:
+        k_out = _made_for(stream, lambda: torch.empty(k.shape, dtype=k.dtype, device=k.device),
+                          result=True)
+    s = (_tensor_side or _tensors()).rope(q_out, k_out, q, k, positions, frequencies,
+                                          bool(interleaved), first, factor, stream)
+    if s:
+        _check(s)
+    return q_out, k_out
+
+
+def rope_append(q_out, q, k, v, k_cache, v_cache, slots, positions, frequencies,
+                interleaved: bool = False, first: int = 0, factor: float = 1.0, stream=None):
+    """rope with K written into the paged bf16 cache, and V beside it, at
+    slots[t] = block * block size + slot (int64 [T]; negative: the token is left
+    out).  Returns q_out (None makes it)."""
+    if q_out is None:
+        q_out = _made_for(stream, lambda: torch.empty(q.shape, dtype=q.dtype, device=q.device),
+                          result=True)
+    s = (_tensor_side or _tensors()).rope_append(q_out, q, k, v, k_cache, v_cache, slots,
+                                                 positions, frequencies, bool(interleaved), first,
+                                                 factor, stream)
+    if s:
+        _check(s)
+    return q_out
+
+
+# ------------------------------------------------ block tables grown on the GPU
+def make_block_pool(num_blocks: int, device=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """(refs, free_bits) of a pool whose blocks are all free."""
+    if num_blocks < 1:
+        raise ValueError("num_blocks must be positive")
+    device = device if device is not None else torch.device("cuda")
+    bits = torch.full(((num_blocks + 31) // 32,), -1, dtype=torch.int32, device=device)
+    if num_blocks % 32:
+        bits[-1] = (1 << (num_blocks % 32)) - 1
+    return torch.zeros(num_blocks, dtype=torch.int32, device=device), bits
+
+
+def grow_tables(block_tables, context_lens, new_tokens, refs, free_bits, block_size: int,
+                positions, token_starts, slots, token_positions, copy_src, copy_dst, result,
+                stream=None) -> None:
+    """Add new_tokens[b] tokens to every row of block_tables [B][MB]: blocks
+    from the pool (refs, free_bits), lengths, and the step's positions [B],
+    token_starts [B + 1], slots and token_positions [N], copies [B] and result
+    [4] (int32, slots int64; see pgd_grow_tables)."""
+    s = (_tensor_side or _tensors()).grow(block_tables, context_lens, new_tokens, refs, free_bits,
+                                          block_size, positions, token_starts, slots,
+                                          token_positions, copy_src, copy_dst, result, stream)
+    if s:
+        _check(s)
+
+
+def trim_tables(block_tables, context_lens, keep_lens, refs, free_bits, block_size: int,
+                stream=None) -> None:
+    """Cut row b to keep_lens[b] tokens and give the blocks behind them back
+    (0: release the request)."""
+    s = (_tensor_side or _tensors()).trim(block_tables, context_lens, keep_lens, refs, free_bits,
+                                          block_size, stream)
+    if s:
+        _check(s)
+
+
 # ------------------------------------------------------ block-sparse attention
 def block_bounds(bounds, bound_scales, k_cache, block_tables, context_lens, positions=None,
                  max_tokens: Optional[int] = None, k_scales=None, stream=None) -> None:
@@ -926,14 +1161,19 @@ def _prepared_sparse(out, q, k_cache, v_cache, bounds, bound_scales, block_table
 
 
 def copy_blocks(k_cache, v_cache, src_ids, dst_ids, stream=None) -> None:
-    """Copy whole physical blocks src_ids[i] -> dst_ids[i] (device int32)."""
-    _need(k_cache, torch.bfloat16, "k_cache")
-    _need(v_cache, torch.bfloat16, "v_cache")
+    """Copy whole physical blocks src_ids[i] -> dst_ids[i] (device int32; a
+    pair -1, -1 is none) of bf16 pools, or of 4-bit ones (uint8)."""
+    fp4 = k_cache.dtype == torch.uint8
+    _need(k_cache, torch.uint8 if fp4 else torch.bfloat16, "k_cache")
+    _need(v_cache, torch.uint8 if fp4 else torch.bfloat16, "v_cache")
     _need(src_ids, torch.int32, "src_ids")
     _need(dst_ids, torch.int32, "dst_ids")
-    NB, n_kv, bs, d = _cache_dims(k_cache)
-    _check(lib().pgd_copy_blocks(_ptr(k_cache), _ptr(v_cache), _ptr(src_ids), _ptr(dst_ids),
-                                 src_ids.numel(), n_kv, d, bs, NB, _stream(stream)))
+    NB, n_kv, bs, d = _cache4_dims(k_cache) if fp4 else _cache_dims(k_cache)
+    if v_cache.shape != k_cache.shape or dst_ids.shape != src_ids.shape:
+        raise ValueError("k_cache and v_cache, src_ids and dst_ids must have one shape")
+    fn = lib().pgd_copy_blocks_fp4 if fp4 else lib().pgd_copy_blocks
+    _check(fn(_ptr(k_cache), _ptr(v_cache), _ptr(src_ids), _ptr(dst_ids), src_ids.numel(), n_kv,
+              d, bs, NB, _stream(stream)))
 
 
 def device_errors(clear: bool = True, stream=None) -> int:

@@ -1,5 +1,6 @@
-// tensors.cpp -- the tensor side of the binding's calls on the block-scaled
-// cache and on block selections: checks torch tensors against the types,
+// tensors.cpp -- the tensor side of the binding's calls on the block-scaled and
+// the 4-bit cache, on block selections, of rotary positions and of block tables
+// on the GPU: checks torch tensors against the types,
 // shapes and device that a call takes and hands their addresses to libpgd.
 //
 // These calls run for two to five microseconds on the GPU at a decode step's
@@ -22,6 +23,7 @@
 namespace {
 
 constexpr int64_t kDim = 128;
+constexpr int64_t kGroup4 = 1152;  // bytes of 16 tokens of a 4-bit tile
 
 struct Refused {};  // a Python exception is set
 
@@ -112,6 +114,10 @@ struct Args {
   // A contiguous tensor on the call's device: its address.
   void *place(const at::Tensor &t, const char *name) {
     if (!t.is_contiguous()) refuse(PyExc_ValueError, std::string(name) + " must be contiguous");
+    return address(t, name);
+  }
+  // A tensor on the call's device: its address.
+  void *address(const ::at::Tensor &t, const char *name) {
     if (!t.is_cuda()) refuse(PyExc_ValueError, std::string(name) + " must be on a CUDA device");
     if (dev == -2) dev = t.get_device();
     if (t.get_device() != dev)
@@ -170,6 +176,33 @@ PyObject *finish(bool pack, pgd_status (*fn)(P...), A... a) {
 const int32_t *i32(void *p) { return static_cast<const int32_t *>(p); }
 float *f32(void *p) { return static_cast<float *>(p); }
 
+// The tokens of a call over ranges: rows [N] and the most of a sequence.
+struct Ranges {
+  int64_t N, T;
+};
+Ranges ranges_of(const at::Tensor &rows, int64_t n_kv, int64_t B, PyObject *starts,
+                 PyObject *most) {
+  if (rows.dim() < 3 || rows.size(-2) != n_kv || rows.size(-1) != kDim)
+    refuse(PyExc_ValueError, "rows must end in [" + std::to_string(n_kv) + "][128], got " +
+                                 shape_text(rows.sizes()));
+  Ranges r;
+  r.N = n_kv ? rows.numel() / (n_kv * kDim) : 0;
+  if (starts == Py_None) {
+    if ((r.N && !B) || (B && r.N % B))
+      refuse(PyExc_ValueError,
+             std::to_string(r.N) + " rows for " + std::to_string(B) + " sequences");
+    r.T = B ? r.N / B : 0;
+    if (most != Py_None && integer(most, "max_tokens") != r.T)
+      refuse(PyExc_ValueError, "max_tokens is not the " + std::to_string(r.T) +
+                                   " tokens that every sequence has");
+  } else if (most == Py_None) {
+    refuse(PyExc_ValueError, "token_starts needs max_tokens, the most tokens of a sequence");
+  } else {
+    r.T = integer(most, "max_tokens");
+  }
+  return r;
+}
+
 // (is_read, k_rows, v_rows, k_cache, v_cache, k_scales, v_scales, tables,
 //  positions, starts or None, max_tokens or None, stream)
 PyObject *range_call(PyObject *const *a) {
@@ -182,24 +215,8 @@ PyObject *range_call(PyObject *const *a) {
   const int64_t NB = pool[0], n_kv = pool[1], rg = pool[2];
   const auto table = sizes(a[7], 2, "block_tables");
   const int64_t B = table[0], MB = table[1];
-  if (kr.dim() < 3 || kr.size(-2) != n_kv || kr.size(-1) != kDim)
-    refuse(PyExc_ValueError, "rows must end in [" + std::to_string(n_kv) + "][128], got " +
-                                 shape_text(kr.sizes()));
-  const int64_t N = n_kv ? kr.numel() / (n_kv * kDim) : 0;
-  int64_t T;
-  if (a[9] == Py_None) {
-    if ((N && !B) || (B && N % B))
-      refuse(PyExc_ValueError,
-             std::to_string(N) + " rows for " + std::to_string(B) + " sequences");
-    T = B ? N / B : 0;
-    if (a[10] != Py_None && integer(a[10], "max_tokens") != T)
-      refuse(PyExc_ValueError, "max_tokens is not the " + std::to_string(T) +
-                                   " tokens that every sequence has");
-  } else if (a[10] == Py_None) {
-    refuse(PyExc_ValueError, "token_starts needs max_tokens, the most tokens of a sequence");
-  } else {
-    T = integer(a[10], "max_tokens");
-  }
+  const Ranges r = ranges_of(kr, n_kv, B, a[9], a[10]);
+  const int64_t N = r.N, T = r.T;
   void *k = x.take(a[3], at::kByte, {NB, n_kv, rg, 8, 8, 16}, "k_cache");
   void *v = x.take(a[4], at::kByte, {NB, n_kv, rg, 8, 8, 16}, "v_cache");
   float *ks = f32(x.take(a[5], at::kFloat, {NB, n_kv}, "k_scales"));
@@ -357,6 +374,200 @@ PyObject *tiles_call(PyObject *const *a) {
                 splits, ws, (size_t)w.nbytes(), x.stream(a[17]));
 }
 
+// (is_read, k_rows, v_rows, k_cache, v_cache, tables, positions, starts or None,
+//  max_tokens or None, k_scale, v_scale, stream)
+PyObject *range4_call(PyObject *const *a) {
+  Args x;
+  const bool read = a[0] == Py_True;
+  const at::Tensor &kr = tensor(a[1], "k rows");
+  void *k_rows = x.take(a[1], at::kBFloat16, kr.sizes(), "k rows");
+  void *v_rows = x.take(a[2], at::kBFloat16, kr.sizes(), "v rows");
+  const auto pool = sizes(a[3], 4, "k_cache", at::kByte);
+  const int64_t NB = pool[0], n_kv = pool[1], ng = pool[2];
+  const auto table = sizes(a[5], 2, "block_tables");
+  const int64_t B = table[0], MB = table[1];
+  const Ranges r = ranges_of(kr, n_kv, B, a[7], a[8]);
+  void *k = x.take(a[3], at::kByte, {NB, n_kv, ng, kGroup4}, "k_cache");
+  void *v = x.take(a[4], at::kByte, {NB, n_kv, ng, kGroup4}, "v_cache");
+  const int32_t *tables = i32(x.take(a[5], at::kInt, {B, MB}, "block_tables"));
+  const int32_t *pos = i32(x.take(a[6], at::kInt, {B}, "positions"));
+  const int32_t *starts = i32(x.take_opt(a[7], at::kInt, {B + 1}, "token_starts"));
+  const int32_t b = int32(B, "B"), t = int32(r.T, "max_tokens"), n = int32(r.N, "rows"),
+                h = int32(n_kv, "n_kv"), bs = int32(ng * 16, "block size"), mb = int32(MB, "MB"),
+                nb = int32(NB, "NB");
+  const float k_scale = real(a[9]), v_scale = real(a[10]);
+  void *st = x.stream(a[11]);
+  if (read)
+    return finish(false, pgd_kv_read_fp4, k_rows, v_rows, k, v, tables, pos, starts, b, t, n, h,
+                  (int32_t)kDim, bs, mb, nb, k_scale, v_scale, st);
+  return finish(false, pgd_kv_append_fp4, k_rows, v_rows, k, v, tables, pos, starts, b, t, n, h,
+                (int32_t)kDim, bs, mb, nb, k_scale, v_scale, st);
+}
+
+// (out, q, k_new or None, v_new or None, k_cache, v_cache, tables, context_lens,
+//  scale, k_scale, v_scale, num_splits, workspace, stream, pack)
+PyObject *attention4_call(PyObject *const *a) {
+  Args x;
+  const auto pool = sizes(a[4], 4, "k_cache", at::kByte);
+  const int64_t NB = pool[0], n_kv = pool[1], ng = pool[2];
+  const auto qs = sizes(a[1], 3, "q");
+  const int64_t B = qs[0], n_q = qs[1], d = qs[2];
+  const int64_t MB = sizes(a[6], 2, "block_tables")[1];
+  void *q = x.take(a[1], at::kBFloat16, {B, n_q, d}, "q");
+  void *out = x.take(a[0], at::kBFloat16, {B, n_q, d}, "out");
+  const bool append = a[2] != Py_None;
+  void *kn = append ? x.take(a[2], at::kBFloat16, {B, n_kv, d}, "k_new") : nullptr;
+  void *vn = append ? x.take(a[3], at::kBFloat16, {B, n_kv, d}, "v_new") : nullptr;
+  void *k = x.take(a[4], at::kByte, {NB, n_kv, ng, kGroup4}, "k_cache");
+  void *v = x.take(a[5], at::kByte, {NB, n_kv, ng, kGroup4}, "v_cache");
+  const int32_t *tables = i32(x.take(a[6], at::kInt, {B, MB}, "block_tables"));
+  const int32_t *ctx = i32(x.take(a[7], at::kInt, {B}, "context_lens"));
+  const at::Tensor &w = tensor(a[12], "workspace");
+  void *ws = x.place(w, "workspace");
+  const float scale = real(a[8]), k_scale = real(a[9]), v_scale = real(a[10]);
+  const int32_t splits = (int32_t)integer(a[11], "num_splits");
+  const int32_t b = int32(B, "B"), nq = int32(n_q, "n_q"), h = int32(n_kv, "n_kv"),
+                dd = int32(d, "d"), bs = int32(ng * 16, "block size"), mb = int32(MB, "MB"),
+                nb = int32(NB, "NB");
+  void *st = x.stream(a[13]);
+  const bool pack = a[14] == Py_True;
+  if (append)
+    return finish(pack, pgd_append_decode_attention_fp4, out, q, kn, vn, k, v, tables, ctx, b, nq,
+                  h, dd, bs, mb, nb, scale, k_scale, v_scale, splits, ws, (size_t)w.nbytes(), st);
+  return finish(pack, pgd_paged_decode_attention_fp4, out, q, k, v, tables, ctx, b, nq, h, dd, bs,
+                mb, nb, scale, k_scale, v_scale, splits, ws, (size_t)w.nbytes(), st);
+}
+
+// Rows [T][heads][d] of bf16, strided over tokens and heads: address and
+// strides (those of a dimension of one element do not matter).
+void *rows_of(Args &x, PyObject *o, int64_t T, int64_t d, int64_t heads, const char *name,
+              int64_t *strides) {
+  const at::Tensor &t = tensor(o, name);
+  if (t.scalar_type() != at::kBFloat16)
+    refuse(PyExc_TypeError,
+           std::string(name) + " must be torch.bfloat16, got " + dtype_name(t.scalar_type()));
+  if (t.dim() != 3 || t.size(0) != T || t.size(2) != d || (heads >= 0 && t.size(1) != heads))
+    refuse(PyExc_ValueError, std::string(name) + " must be [" + std::to_string(T) + "][" +
+                                 (heads >= 0 ? std::to_string(heads) : "heads") + "][" +
+                                 std::to_string(d) + "], got " + shape_text(t.sizes()));
+  if (t.stride(2) != 1 && d != 1)
+    refuse(PyExc_ValueError, std::string(name) + " must be contiguous in its last dim");
+  strides[0] = t.size(0) > 1 ? t.stride(0) : 0;
+  strides[1] = t.size(1) > 1 ? t.stride(1) : 0;
+  return x.address(t, name);
+}
+// An output's elements must lie apart (a view made by expand() has one place
+// for several).
+void lie_apart(PyObject *o, const char *name) {
+  const at::Tensor &t = tensor(o, name);
+  if (t.numel() == 0) return;
+  const int64_t r = t.stride(0), h = t.stride(1), T = t.size(0), n = t.size(1), d = t.size(2);
+  const bool by_token = n == 1 || h >= d, heads_in_token = T == 1 || r >= (n - 1) * h + d,
+             by_head = T == 1 || r >= d, tokens_in_head = n == 1 || h >= (T - 1) * r + d;
+  if (!(by_token && heads_in_token) && !(by_head && tokens_in_head))
+    refuse(PyExc_ValueError, std::string(name) + " has rows that overlap");
+}
+
+// (q_out, k_out or None, q, k or None, positions, frequencies, interleaved,
+//  first, factor, stream)
+PyObject *rope_call(PyObject *const *a) {
+  Args x;
+  const auto qs = sizes(a[2], 3, "q", at::kBFloat16);
+  const int64_t T = qs[0], n_q = qs[1], d = qs[2];
+  int64_t strides[8] = {0, 0, 0, 0, 0, 0, 0, 0}, n_kv = 0;
+  void *q = rows_of(x, a[2], T, d, n_q, "q", strides + 4);
+  void *q_out = rows_of(x, a[0], T, d, n_q, "q_out", strides);
+  lie_apart(a[0], "q_out");
+  void *k = nullptr, *k_out = nullptr;
+  if (a[3] != Py_None) {
+    k = rows_of(x, a[3], T, d, -1, "k", strides + 6);
+    n_kv = tensor(a[3], "k").size(1);
+    k_out = rows_of(x, a[1], T, d, n_kv, "k_out", strides + 2);
+    lie_apart(a[1], "k_out");
+  } else if (a[1] != Py_None) {
+    refuse(PyExc_ValueError, "k_out without k");
+  }
+  const int32_t *pos = i32(x.take(a[4], at::kInt, {T}, "positions"));
+  const int64_t half = sizes(a[5], 1, "frequencies")[0];
+  const int64_t *freq =
+      static_cast<const int64_t *>(x.take(a[5], at::kLong, {half}, "frequencies"));
+  const int64_t *st = strides;
+  return finish(false, pgd_rope, q_out, k_out, q, k, pos, freq, int32(T, "T"), int32(n_q, "n_q"),
+                int32(n_kv, "n_kv"), int32(d, "d"), (int32_t)integer(a[7], "first"),
+                int32(2 * half, "rotary"), (int32_t)(a[6] == Py_True), real(a[8]), st,
+                x.stream(a[9]));
+}
+
+// (q_out, q, k, v, k_cache, v_cache, slots, positions, frequencies, interleaved,
+//  first, factor, stream)
+PyObject *rope_append_call(PyObject *const *a) {
+  Args x;
+  const auto qs = sizes(a[1], 3, "q", at::kBFloat16);
+  const int64_t T = qs[0], n_q = qs[1], d = qs[2];
+  const auto pool = sizes(a[4], 6, "k_cache", at::kBFloat16);
+  const int64_t NB = pool[0], n_kv = pool[1], rg = pool[2];
+  int64_t strides[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  void *q_out = rows_of(x, a[0], T, d, n_q, "q_out", strides);
+  lie_apart(a[0], "q_out");
+  void *q = rows_of(x, a[1], T, d, n_q, "q", strides + 2);
+  void *k = rows_of(x, a[2], T, d, n_kv, "k", strides + 4);
+  void *v = rows_of(x, a[3], T, d, n_kv, "v", strides + 6);
+  void *kc = x.take(a[4], at::kBFloat16, {NB, n_kv, rg, kDim / 8, 8, 8}, "k_cache");
+  void *vc = x.take(a[5], at::kBFloat16, {NB, n_kv, rg, kDim / 8, 8, 8}, "v_cache");
+  const int64_t *slots = static_cast<const int64_t *>(x.take(a[6], at::kLong, {T}, "slots"));
+  const int32_t *pos = i32(x.take(a[7], at::kInt, {T}, "positions"));
+  const int64_t half = sizes(a[8], 1, "frequencies")[0];
+  const int64_t *freq =
+      static_cast<const int64_t *>(x.take(a[8], at::kLong, {half}, "frequencies"));
+  const int64_t *st = strides;
+  return finish(false, pgd_rope_append, q_out, q, k, v, kc, vc, slots, pos, freq, int32(T, "T"),
+                int32(n_q, "n_q"), int32(n_kv, "n_kv"), int32(d, "d"), int32(rg * 8, "block size"),
+                int32(NB, "NB"), (int32_t)integer(a[10], "first"), int32(2 * half, "rotary"),
+                (int32_t)(a[9] == Py_True), real(a[11]), st, x.stream(a[12]));
+}
+
+int32_t *i32_out(void *p) { return static_cast<int32_t *>(p); }
+
+// (tables, context_lens, new_tokens, refs, free_bits, block_size, positions,
+//  token_starts, slots, token_positions, copy_src, copy_dst, result, stream)
+PyObject *grow_call(PyObject *const *a) {
+  Args x;
+  const auto table = sizes(a[0], 2, "block_tables");
+  const int64_t B = table[0], MB = table[1], NB = sizes(a[3], 1, "refs")[0];
+  const int64_t N = sizes(a[8], 1, "slots")[0];
+  int32_t *tables = i32_out(x.take(a[0], at::kInt, {B, MB}, "block_tables"));
+  int32_t *ctx = i32_out(x.take(a[1], at::kInt, {B}, "context_lens"));
+  const int32_t *more = i32(x.take(a[2], at::kInt, {B}, "new_tokens"));
+  int32_t *refs = i32_out(x.take(a[3], at::kInt, {NB}, "refs"));
+  int32_t *bits = i32_out(x.take(a[4], at::kInt, {(NB + 31) / 32}, "free_bits"));
+  int32_t *pos = i32_out(x.take(a[6], at::kInt, {B}, "positions"));
+  int32_t *starts = i32_out(x.take(a[7], at::kInt, {B + 1}, "token_starts"));
+  int64_t *slots = static_cast<int64_t *>(x.take(a[8], at::kLong, {N}, "slots"));
+  int32_t *places = i32_out(x.take(a[9], at::kInt, {N}, "token_positions"));
+  int32_t *src = i32_out(x.take(a[10], at::kInt, {B}, "copy_src"));
+  int32_t *dst = i32_out(x.take(a[11], at::kInt, {B}, "copy_dst"));
+  int32_t *result = i32_out(x.take(a[12], at::kInt, {4}, "result"));
+  return finish(false, pgd_grow_tables, tables, ctx, more, refs, bits, pos, starts, slots, places,
+                src, dst, result, int32(B, "B"), int32(N, "N"),
+                (int32_t)integer(a[5], "block_size"), int32(MB, "MB"), int32(NB, "NB"),
+                x.stream(a[13]));
+}
+
+// (tables, context_lens, keep_lens, refs, free_bits, block_size, stream)
+PyObject *trim_call(PyObject *const *a) {
+  Args x;
+  const auto table = sizes(a[0], 2, "block_tables");
+  const int64_t B = table[0], MB = table[1], NB = sizes(a[3], 1, "refs")[0];
+  int32_t *tables = i32_out(x.take(a[0], at::kInt, {B, MB}, "block_tables"));
+  int32_t *ctx = i32_out(x.take(a[1], at::kInt, {B}, "context_lens"));
+  const int32_t *keep = i32(x.take(a[2], at::kInt, {B}, "keep_lens"));
+  int32_t *refs = i32_out(x.take(a[3], at::kInt, {NB}, "refs"));
+  int32_t *bits = i32_out(x.take(a[4], at::kInt, {(NB + 31) / 32}, "free_bits"));
+  return finish(false, pgd_trim_tables, tables, ctx, keep, refs, bits, int32(B, "B"),
+                (int32_t)integer(a[5], "block_size"), int32(MB, "MB"), int32(NB, "NB"),
+                x.stream(a[6]));
+}
+
 // A call with its number of arguments, no C++ exception left to Python.
 template <PyObject *(*F)(PyObject *const *), Py_ssize_t N>
 PyObject *guarded(PyObject *, PyObject *const *args, Py_ssize_t n) {
@@ -380,7 +591,10 @@ PyObject *guarded(PyObject *, PyObject *const *args, Py_ssize_t n) {
 PyMethodDef methods[] = {
     PGD_METHOD("range", range_call, 12),   PGD_METHOD("attention", attention_call, 15),
     PGD_METHOD("bounds", bounds_call, 9),  PGD_METHOD("select", select_call, 11),
-    PGD_METHOD("tiles", tiles_call, 19),   {nullptr, nullptr, 0, nullptr},
+    PGD_METHOD("tiles", tiles_call, 19),   PGD_METHOD("range4", range4_call, 12),
+    PGD_METHOD("attention4", attention4_call, 15), PGD_METHOD("rope", rope_call, 10),
+    PGD_METHOD("rope_append", rope_append_call, 13), PGD_METHOD("grow", grow_call, 14),
+    PGD_METHOD("trim", trim_call, 7), {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_pgd_tensors", nullptr, -1, methods,
                       nullptr, nullptr, nullptr, nullptr};

@@ -14,8 +14,11 @@
 #include <tuple>
 #include <atomic>
 
+#include "block_tables.cuh"
+#include "kv_fp4.cuh"
 #include "kv_fp8b.cuh"
 #include "pgd_device.cuh"
+#include "rope.cuh"
 #include "short_attention.cuh"
 
 namespace pgd {
@@ -41,7 +44,7 @@ cudaError_t kv_append_launch(const void *k_new, const void *v_new, void *k_cache
                              int T, int n_kv, int bs, int MB, int NB, int32_t *err,
                              cudaStream_t stream);
 cudaError_t copy_blocks_launch(void *k_cache, void *v_cache, const int32_t *src_ids,
-                               const int32_t *dst_ids, int n, int n_kv, int bs, int NB,
+                               const int32_t *dst_ids, int n, int block_bytes, int NB,
                                int32_t *err, cudaStream_t stream);
 cudaError_t read_stream_launch(const void *src, size_t bytes, int mode, int32_t *err,
                                cudaStream_t stream);
@@ -1209,9 +1212,10 @@ pgd_status pgd_mla_step(void *out_h, const void *q_h, const void *c_new_h,
 }
 
 
-pgd_status pgd_copy_blocks(void *k_cache, void *v_cache, const int32_t *src_ids,
-                           const int32_t *dst_ids, int32_t n, int32_t n_kv, int32_t d,
-                           int32_t bs, int32_t NB, void *stream) {
+// Blocks of two pools copied, `token_bytes` a token and head in each.
+static pgd_status copy_blocks_call(void *k_cache, void *v_cache, const int32_t *src_ids,
+                                   const int32_t *dst_ids, int32_t n, int32_t n_kv, int32_t d,
+                                   int32_t bs, int32_t NB, int token_bytes, void *stream) {
   if (n < 0) return fail(PGD_ERR_INVALID_ARG, "n = %d", n);
   pgd_status s = check_cache_shape(n_kv, d, bs, 1, NB);
   if (s != PGD_OK) return s;
@@ -1219,13 +1223,31 @@ pgd_status pgd_copy_blocks(void *k_cache, void *v_cache, const int32_t *src_ids,
   if (!k_cache || !v_cache || !src_ids || !dst_ids) return fail(PGD_ERR_INVALID_ARG, "null pointer");
   if (!aligned(k_cache, 16) || !aligned(v_cache, 16))
     return fail(PGD_ERR_INVALID_ARG, "caches must be 16-byte aligned");
+  if ((long long)n_kv * bs * token_bytes > 0x7fffffffLL)
+    return fail(PGD_ERR_INVALID_ARG, "a block of n_kv * bs = %lld rows is too large",
+                (long long)n_kv * bs);
   int32_t *err = nullptr;
   s = error_word(&err);
   if (s != PGD_OK) return s;
-  cudaError_t e = copy_blocks_launch(k_cache, v_cache, src_ids, dst_ids, n, n_kv, bs, NB, err,
+  cudaError_t e = copy_blocks_launch(k_cache, v_cache, src_ids, dst_ids, n,
+                                     n_kv * bs * token_bytes, NB, err,
                                      static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "copy_blocks launch");
   return ok();
+}
+
+pgd_status pgd_copy_blocks(void *k_cache, void *v_cache, const int32_t *src_ids,
+                           const int32_t *dst_ids, int32_t n, int32_t n_kv, int32_t d,
+                           int32_t bs, int32_t NB, void *stream) {
+  return copy_blocks_call(k_cache, v_cache, src_ids, dst_ids, n, n_kv, d, bs, NB, kHeadDim * 2,
+                          stream);
+}
+
+pgd_status pgd_copy_blocks_fp4(void *k_cache, void *v_cache, const int32_t *src_ids,
+                               const int32_t *dst_ids, int32_t n, int32_t n_kv, int32_t d,
+                               int32_t bs, int32_t NB, void *stream) {
+  return copy_blocks_call(k_cache, v_cache, src_ids, dst_ids, n, n_kv, d, bs, NB,
+                          kGroupBytes4 / kGroupTokens4, stream);
 }
 
 pgd_status pgd_read_stream(const void *src, size_t bytes, int32_t mode, void *stream) {
@@ -1674,6 +1696,438 @@ pgd_status pgd_sparse_decode_attention(
   return selected_attention(out, q, k_cache, v_cache, k_scales, v_scales, tiles, tile_tokens, B,
                             n_q, n_kv, d, bs, NB, W, scale, num_splits, workspace,
                             workspace_bytes, B ? &sp : nullptr, static_cast<cudaStream_t>(stream));
+}
+
+// ------------------------------------------------------------ 4-bit cache
+// A call's scale: a power of two, so that nothing is rounded by it.
+static pgd_status check_pow2(float x, const char *name) {
+  int e = 0;
+  if (!(x > 0.f) || !isfinite(x) || frexpf(x, &e) != 0.5f || e - 1 < -32 || e - 1 > 32)
+    return fail(PGD_ERR_INVALID_ARG, "%s = %g is no power of two from 2^-32 to 2^32", name,
+                (double)x);
+  return PGD_OK;
+}
+
+static pgd_status check_scales4(float k_scale, float v_scale) {
+  const pgd_status s = check_pow2(k_scale, "k_scale");
+  return s != PGD_OK ? s : check_pow2(v_scale, "v_scale");
+}
+
+// Sizes of a write or a read-back: one warp per 16-token group, head and pool.
+static pgd_status check_ranges4(int32_t B, int32_t T, int32_t n_kv, int32_t d, int32_t bs,
+                                int32_t MB, int32_t NB) {
+  if (B < 0 || T < 0) return fail(PGD_ERR_INVALID_ARG, "B = %d, T = %d", B, T);
+  const pgd_status s = check_cache_shape(n_kv, d, bs, MB, NB);
+  if (s != PGD_OK) return s;
+  const long long groups = most_groups4(std::max(T, 1), bs, MB);
+  if (groups * n_kv > 0x7fffffffLL / 2 || B * groups > 0x7fffffffLL ||
+      B * groups * n_kv > 0x7fffffffLL)
+    return fail(PGD_ERR_INVALID_ARG, "B * T * n_kv too large");
+  return PGD_OK;
+}
+
+static pgd_status kv4_range_call(bool write, const void *k_rows, const void *v_rows,
+                                 const void *k_cache, const void *v_cache, const int32_t *tables,
+                                 const int32_t *positions, const int32_t *starts, int32_t B,
+                                 int32_t T, int32_t N, int32_t n_kv, int32_t d, int32_t bs,
+                                 int32_t MB, int32_t NB, float k_scale, float v_scale,
+                                 void *stream) {
+  pgd_status s = check_ranges4(B, T, n_kv, d, bs, MB, NB);
+  if (s != PGD_OK) return s;
+  if ((s = check_scales4(k_scale, v_scale)) != PGD_OK) return s;
+  if (N < 0 || (!starts && (long long)B * T != N))
+    return fail(PGD_ERR_INVALID_ARG, "N = %d rows (B * T = %lld)", N, (long long)B * T);
+  if (B == 0 || T == 0 || N == 0) return ok();
+  if (!k_rows || !v_rows || !k_cache || !v_cache || !tables || !positions)
+    return fail(PGD_ERR_INVALID_ARG, "null pointer");
+  if (!aligned(k_rows, 16) || !aligned(v_rows, 16) || !aligned(k_cache, 16) ||
+      !aligned(v_cache, 16))
+    return fail(PGD_ERR_INVALID_ARG, "rows and pools must be 16-byte aligned");
+  Kv4Params p = {};
+  p.k_new = static_cast<const __nv_bfloat16 *>(k_rows);
+  p.v_new = static_cast<const __nv_bfloat16 *>(v_rows);
+  p.k_out = static_cast<__nv_bfloat16 *>(const_cast<void *>(k_rows));
+  p.v_out = static_cast<__nv_bfloat16 *>(const_cast<void *>(v_rows));
+  p.k_cache = static_cast<unsigned char *>(const_cast<void *>(k_cache));
+  p.v_cache = static_cast<unsigned char *>(const_cast<void *>(v_cache));
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.tables = tables;
+  p.pos = positions;
+  p.starts = starts;
+  p.B = B;
+  p.T = T;
+  p.N = N;
+  p.n_kv = n_kv;
+  p.bs = bs;
+  p.MB = MB;
+  p.NB = NB;
+  if ((s = error_word(&p.err)) != PGD_OK) return s;
+  const cudaError_t e = write ? kv_append_fp4_launch(p, static_cast<cudaStream_t>(stream))
+                              : kv_read_fp4_launch(p, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, write ? "kv_append_fp4 launch" : "kv_read_fp4 launch");
+  return ok();
+}
+
+pgd_status pgd_kv_append_fp4(const void *k_new, const void *v_new, void *k_cache, void *v_cache,
+                             const int32_t *block_tables, const int32_t *positions,
+                             const int32_t *token_starts, int32_t B, int32_t T, int32_t N,
+                             int32_t n_kv, int32_t d, int32_t bs, int32_t MB, int32_t NB,
+                             float k_scale, float v_scale, void *stream) {
+  return kv4_range_call(true, k_new, v_new, k_cache, v_cache, block_tables, positions,
+                        token_starts, B, T, N, n_kv, d, bs, MB, NB, k_scale, v_scale, stream);
+}
+
+pgd_status pgd_kv_read_fp4(void *k_out, void *v_out, const void *k_cache, const void *v_cache,
+                           const int32_t *block_tables, const int32_t *positions,
+                           const int32_t *token_starts, int32_t B, int32_t T, int32_t N,
+                           int32_t n_kv, int32_t d, int32_t bs, int32_t MB, int32_t NB,
+                           float k_scale, float v_scale, void *stream) {
+  return kv4_range_call(false, k_out, v_out, k_cache, v_cache, block_tables, positions,
+                        token_starts, B, T, N, n_kv, d, bs, MB, NB, k_scale, v_scale, stream);
+}
+
+// The grid of a call: its parts, or a number that goes by the device alone.
+static long long fp4_grid(int32_t B, int32_t n_kv, int32_t num_splits, int sms) {
+  return num_splits > 0 ? (long long)num_splits * B * n_kv
+                        : attention_fp4_grid((long long)B * n_kv, sms);
+}
+
+size_t pgd_fp4_workspace_size(int32_t B, int32_t n_q, int32_t n_kv, int32_t d,
+                              int32_t num_splits) {
+  if (B < 0 || n_kv <= 0 || n_q <= 0 || n_q % n_kv || d != kHeadDim || num_splits < 0) return 0;
+  if ((long long)B * n_kv > kMaxBlockUnits) return 0;
+  return ws_layout(B, n_q, n_kv, fp4_grid(B, n_kv, num_splits, sm_count()), true).total;
+}
+
+static pgd_status attention_fp4_call(void *out, const void *q, const void *k_new,
+                                     const void *v_new, void *k_cache, void *v_cache,
+                                     const int32_t *tables, const int32_t *ctx, int32_t B,
+                                     int32_t n_q, int32_t n_kv, int32_t d, int32_t bs, int32_t MB,
+                                     int32_t NB, float scale, float k_scale, float v_scale,
+                                     int32_t num_splits, void *workspace, size_t workspace_bytes,
+                                     bool append, cudaStream_t stream) {
+  pgd_status s = check_attention_args(out, q, k_cache, v_cache, tables, ctx, B, n_q, n_kv, d, bs,
+                                      MB, NB, scale, num_splits);
+  if (s != PGD_OK) return s;
+  if ((s = check_scales4(k_scale, v_scale)) != PGD_OK) return s;
+  if (B == 0) return ok();
+  if (append) {
+    if (!k_new || !v_new) return fail(PGD_ERR_INVALID_ARG, "null pointer");
+    if (!aligned(k_new, 16) || !aligned(v_new, 16))
+      return fail(PGD_ERR_INVALID_ARG, "bf16 arrays must be 16-byte aligned");
+    if ((s = check_ranges4(B, 1, n_kv, d, bs, MB, NB)) != PGD_OK) return s;
+  }
+  // the line of 32-token steps is 32 bits wide, the workspace has kMaxBlockUnits counters
+  const long long units = (long long)B * n_kv;
+  if (units > kMaxBlockUnits)
+    return fail(PGD_ERR_UNSUPPORTED, "B * n_kv = %lld > %lld", units, kMaxBlockUnits);
+  if (units * (((long long)MB * bs + 31) / 32) >= (1LL << 30))
+    return fail(PGD_ERR_UNSUPPORTED, "B * n_kv * MB * bs >= 2^35");
+  if (!workspace) return fail(PGD_ERR_WORKSPACE, "workspace is NULL");
+  if (!aligned(workspace, kWsAlign)) return fail(PGD_ERR_WORKSPACE, "workspace not 256-aligned");
+  const long long grid = fp4_grid(B, n_kv, num_splits, sm_count());
+  const WsLayout L = ws_layout(B, n_q, n_kv, grid, true);
+  if (workspace_bytes < L.total)
+    return fail(PGD_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, L.total);
+  Attn4Params p = {};
+  if ((s = error_word(&p.a.err)) != PGD_OK) return s;
+  unsigned char *ws = static_cast<unsigned char *>(workspace);
+  p.a.out = static_cast<__nv_bfloat16 *>(out);
+  p.a.q = static_cast<const __nv_bfloat16 *>(q);
+  p.a.k_cache = static_cast<const unsigned char *>(k_cache);
+  p.a.v_cache = static_cast<const unsigned char *>(v_cache);
+  p.a.tables = tables;
+  p.a.ctx = ctx;
+  p.a.B = B;
+  p.a.n_q = n_q;
+  p.a.n_kv = n_kv;
+  p.a.MB = MB;
+  p.a.NB = NB;
+  p.a.qk_scale_log2 = (float)((double)scale * k_scale * 1.4426950408889634);  // log2(e)
+  p.a.counters = reinterpret_cast<int32_t *>(ws + L.counters);
+  p.a.part_ml = reinterpret_cast<float *>(ws + L.part_ml);
+  p.a.part_o = reinterpret_cast<float *>(ws + L.part_o);
+  p.a.auto_split = num_splits == 0 ? 1 : 0;
+  p.a.wait_late = append ? 1 : 0;  // the append writes only the cache
+  p.v_scale = v_scale;
+  if (append) {
+    Kv4Params ap = {};
+    ap.k_new = static_cast<const __nv_bfloat16 *>(k_new);
+    ap.v_new = static_cast<const __nv_bfloat16 *>(v_new);
+    ap.k_cache = static_cast<unsigned char *>(k_cache);
+    ap.v_cache = static_cast<unsigned char *>(v_cache);
+    ap.k_scale = k_scale;
+    ap.v_scale = v_scale;
+    ap.tables = tables;
+    ap.pos = ctx;
+    ap.pos_offset = -1;
+    ap.B = B;
+    ap.T = 1;
+    ap.N = B;
+    ap.n_kv = n_kv;
+    ap.bs = bs;
+    ap.MB = MB;
+    ap.NB = NB;
+    ap.err = p.a.err;
+    const cudaError_t e = kv_append_fp4_launch(ap, stream);
+    if (e != cudaSuccess) return cuda_fail(e, "kv_append_fp4 launch");
+  }
+  const cudaError_t e = attention_fp4_launch(p, n_q / n_kv, bs, (int)grid, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "4-bit attention launch");
+  return ok();
+}
+
+pgd_status pgd_paged_decode_attention_fp4(void *out, const void *q, const void *k_cache,
+                                          const void *v_cache, const int32_t *block_tables,
+                                          const int32_t *context_lens, int32_t B, int32_t n_q,
+                                          int32_t n_kv, int32_t d, int32_t bs, int32_t MB,
+                                          int32_t NB, float scale, float k_scale, float v_scale,
+                                          int32_t num_splits, void *workspace,
+                                          size_t workspace_bytes, void *stream) {
+  return attention_fp4_call(out, q, nullptr, nullptr, const_cast<void *>(k_cache),
+                            const_cast<void *>(v_cache), block_tables, context_lens, B, n_q, n_kv,
+                            d, bs, MB, NB, scale, k_scale, v_scale, num_splits, workspace,
+                            workspace_bytes, false, static_cast<cudaStream_t>(stream));
+}
+
+pgd_status pgd_append_decode_attention_fp4(
+    void *out, const void *q, const void *k_new, const void *v_new, void *k_cache, void *v_cache,
+    const int32_t *block_tables, const int32_t *context_lens, int32_t B, int32_t n_q,
+    int32_t n_kv, int32_t d, int32_t bs, int32_t MB, int32_t NB, float scale, float k_scale,
+    float v_scale, int32_t num_splits, void *workspace, size_t workspace_bytes, void *stream) {
+  return attention_fp4_call(out, q, k_new, v_new, k_cache, v_cache, block_tables, context_lens, B,
+                            n_q, n_kv, d, bs, MB, NB, scale, k_scale, v_scale, num_splits,
+                            workspace, workspace_bytes, true, static_cast<cudaStream_t>(stream));
+}
+
+// ------------------------------------------------------- rotary positions
+pgd_status pgd_rope_frequencies(int64_t *freq_h, int32_t rotary, double base, int32_t scaling,
+                                double factor, double original_context, double slow_turns,
+                                double fast_turns) {
+  if (!freq_h) return fail(PGD_ERR_INVALID_ARG, "null pointer");
+  if (rotary <= 0 || rotary % 2) return fail(PGD_ERR_INVALID_ARG, "rotary = %d dims", rotary);
+  if (scaling < PGD_ROPE_PLAIN || scaling > PGD_ROPE_RAMP_WAVELENGTH)
+    return fail(PGD_ERR_INVALID_ARG, "scaling %d", scaling);
+  if (!(base > 1.0) || !isfinite(base)) return fail(PGD_ERR_INVALID_ARG, "base = %g", base);
+  if (!(factor >= 1.0) || !isfinite(factor))
+    return fail(PGD_ERR_INVALID_ARG, "factor = %g", factor);
+  const bool ramp = scaling == PGD_ROPE_RAMP_DIM || scaling == PGD_ROPE_RAMP_WAVELENGTH;
+  if (ramp && (!(original_context > 0.0) || !isfinite(original_context) || !(slow_turns > 0.0) ||
+               !(fast_turns > slow_turns) || !isfinite(fast_turns)))
+    return fail(PGD_ERR_INVALID_ARG, "a ramp wants a context and 0 < slow_turns < fast_turns");
+  if (scaling == PGD_ROPE_BASE && rotary == 2)
+    return fail(PGD_ERR_INVALID_ARG, "one pair has no base to change");
+  const double two_pi = 6.283185307179586476925286766559;
+  if (scaling == PGD_ROPE_BASE) base *= pow(factor, (double)rotary / (rotary - 2));
+  const int pairs = rotary / 2;
+  // the pair (a real number) that makes `turns` turns in the original context
+  const auto pair_of = [&](double turns) {
+    return rotary * log(original_context / (turns * two_pi)) / (2.0 * log(base));
+  };
+  const double lo = ramp ? std::max(floor(pair_of(fast_turns)), 0.0) : 0.0;
+  double hi = ramp ? std::min(ceil(pair_of(slow_turns)), rotary - 1.0) : 0.0;
+  if (hi <= lo) hi = lo + 0.001;
+  for (int i = 0; i < pairs; ++i) {
+    double f = pow(base, -2.0 * i / rotary);
+    if (scaling == PGD_ROPE_LINEAR) f /= factor;
+    if (ramp) {
+      // kept: 1 for the fast pairs, 0 for the slow ones
+      double kept;
+      if (scaling == PGD_ROPE_RAMP_DIM)
+        kept = 1.0 - (i - lo) / (hi - lo);
+      else
+        kept = (original_context * f / two_pi - slow_turns) / (fast_turns - slow_turns);
+      kept = std::min(1.0, std::max(0.0, kept));
+      f = f * kept + f / factor * (1.0 - kept);
+    }
+    // turns a position, in units of 2^-64 (f <= 1: below 2^62)
+    freq_h[i] = (int64_t)llrint(ldexp(f / two_pi, 64));
+  }
+  return ok();
+}
+
+static pgd_status rope_call(RopeParams &p, int32_t d, cudaStream_t stream) {
+  if (p.T < 0) return fail(PGD_ERR_INVALID_ARG, "T = %d", p.T);
+  if (p.n_q < 0 || p.n_kv < 0 || (long long)p.n_q + 2LL * p.n_kv > 65536)
+    return fail(PGD_ERR_INVALID_ARG, "n_q = %d, n_kv = %d", p.n_q, p.n_kv);
+  if (d <= 0 || d % 16 || d > 2048)
+    return fail(PGD_ERR_UNSUPPORTED, "d = %d (a multiple of 16 up to 2048)", d);
+  if (p.rotary <= 0 || p.rotary % 16 || p.first < 0 || p.first % 8 ||
+      (long long)p.first + p.rotary > d)
+    return fail(PGD_ERR_UNSUPPORTED, "rotary dims %d .. + %d of %d (multiples of 8 and 16)",
+                p.first, p.rotary, d);
+  if (!isfinite(p.factor)) return fail(PGD_ERR_INVALID_ARG, "factor = %g", (double)p.factor);
+  if (p.T == 0 || p.n_q + p.n_kv == 0) return ok();
+  if (!p.positions || !p.freq) return fail(PGD_ERR_INVALID_ARG, "null pointer");
+  if (!aligned(p.positions, 4) || !aligned(p.freq, 8))
+    return fail(PGD_ERR_INVALID_ARG, "positions and frequencies must be aligned to their size");
+  p.d = d;
+  const struct {
+    const void *at;
+    long long row, head;
+    int heads;
+  } arrays[] = {{p.q, p.q_row, p.q_head, p.n_q},
+                {p.q_out, p.qo_row, p.qo_head, p.n_q},
+                {p.k, p.k_row, p.k_head, p.n_kv},
+                {p.k_cache ? p.k : p.k_out, p.k_cache ? p.k_row : p.ko_row,
+                 p.k_cache ? p.k_head : p.ko_head, p.n_kv},
+                {p.k_cache ? p.v : p.k, p.k_cache ? p.v_row : p.k_row,
+                 p.k_cache ? p.v_head : p.k_head, p.n_kv}};
+  for (const auto &a : arrays) {
+    if (a.heads == 0) continue;
+    if (!a.at) return fail(PGD_ERR_INVALID_ARG, "null pointer");
+    if (!aligned(a.at, 16) || a.row % 8 || a.head % 8 || a.row < 0 || a.head < 0)
+      return fail(PGD_ERR_INVALID_ARG,
+                  "rows must be 16-byte aligned: strides of 8 elements, %lld and %lld given",
+                  a.row, a.head);
+  }
+  pgd_status s = error_word(&p.err);
+  if (s != PGD_OK) return s;
+  const cudaError_t e = rope_launch(p, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "rope launch");
+  return ok();
+}
+
+pgd_status pgd_rope(void *q_out, void *k_out, const void *q, const void *k,
+                    const int32_t *positions, const int64_t *frequencies, int32_t T, int32_t n_q,
+                    int32_t n_kv, int32_t d, int32_t first, int32_t rotary, int32_t interleaved,
+                    float factor, const int64_t *strides, void *stream) {
+  RopeParams p = {};
+  p.q = static_cast<const __nv_bfloat16 *>(q);
+  p.k = static_cast<const __nv_bfloat16 *>(k);
+  p.q_out = static_cast<__nv_bfloat16 *>(q_out);
+  p.k_out = static_cast<__nv_bfloat16 *>(k_out);
+  p.positions = positions;
+  p.freq = frequencies;
+  p.T = T;
+  p.n_q = n_q;
+  p.n_kv = n_kv;
+  p.first = first;
+  p.rotary = rotary;
+  p.interleaved = interleaved ? 1 : 0;
+  p.factor = factor;
+  const long long qr = (long long)n_q * d, kr = (long long)n_kv * d;
+  const long long dense[8] = {qr, d, kr, d, qr, d, kr, d};
+  long long *const at[8] = {&p.qo_row, &p.qo_head, &p.ko_row, &p.ko_head,
+                            &p.q_row,  &p.q_head,  &p.k_row,  &p.k_head};
+  for (int i = 0; i < 8; ++i) *at[i] = strides ? strides[i] : dense[i];
+  return rope_call(p, d, static_cast<cudaStream_t>(stream));
+}
+
+pgd_status pgd_rope_append(void *q_out, const void *q, const void *k, const void *v, void *k_cache,
+                           void *v_cache, const int64_t *slots, const int32_t *positions,
+                           const int64_t *frequencies, int32_t T, int32_t n_q, int32_t n_kv,
+                           int32_t d, int32_t bs, int32_t NB, int32_t first, int32_t rotary,
+                           int32_t interleaved, float factor, const int64_t *strides,
+                           void *stream) {
+  pgd_status s = check_cache_shape(n_kv, d, bs, 1, NB);
+  if (s != PGD_OK) return s;
+  if (n_q < 0) return fail(PGD_ERR_INVALID_ARG, "n_q = %d", n_q);
+  if (T > 0) {
+    if (!k_cache || !v_cache || !slots) return fail(PGD_ERR_INVALID_ARG, "null pointer");
+    if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(slots, 8))
+      return fail(PGD_ERR_INVALID_ARG, "caches must be 16-byte aligned, slots 8-byte");
+  }
+  RopeParams p = {};
+  p.q = static_cast<const __nv_bfloat16 *>(q);
+  p.k = static_cast<const __nv_bfloat16 *>(k);
+  p.v = static_cast<const __nv_bfloat16 *>(v);
+  p.q_out = static_cast<__nv_bfloat16 *>(q_out);
+  p.k_cache = static_cast<unsigned char *>(k_cache);
+  p.v_cache = static_cast<unsigned char *>(v_cache);
+  p.slots = slots;
+  p.positions = positions;
+  p.freq = frequencies;
+  p.T = T;
+  p.n_q = n_q;
+  p.n_kv = n_kv;
+  p.bs = bs;
+  p.NB = NB;
+  p.first = first;
+  p.rotary = rotary;
+  p.interleaved = interleaved ? 1 : 0;
+  p.factor = factor;
+  const long long qr = (long long)n_q * d, kr = (long long)n_kv * d;
+  const long long dense[8] = {qr, d, qr, d, kr, d, kr, d};
+  long long *const at[8] = {&p.qo_row, &p.qo_head, &p.q_row, &p.q_head,
+                            &p.k_row,  &p.k_head,  &p.v_row, &p.v_head};
+  for (int i = 0; i < 8; ++i) *at[i] = strides ? strides[i] : dense[i];
+  return rope_call(p, d, static_cast<cudaStream_t>(stream));
+}
+
+// ------------------------------------------- block tables grown on the GPU
+static pgd_status check_tables(int32_t B, int32_t bs, int32_t MB, int32_t NB) {
+  if (B < 0) return fail(PGD_ERR_INVALID_ARG, "B = %d", B);
+  if (bs <= 0 || MB <= 0 || NB <= 0)
+    return fail(PGD_ERR_INVALID_ARG, "bs, MB and NB must be positive");
+  if ((long long)MB * bs > 0x7fffffffLL)
+    return fail(PGD_ERR_INVALID_ARG, "MB * bs overflows int32");
+  return PGD_OK;
+}
+
+pgd_status pgd_grow_tables(int32_t *block_tables, int32_t *context_lens,
+                           const int32_t *new_tokens, int32_t *refs, int32_t *free_bits,
+                           int32_t *positions, int32_t *token_starts, int64_t *slots,
+                           int32_t *token_positions, int32_t *copy_src, int32_t *copy_dst,
+                           int32_t *result, int32_t B, int32_t N, int32_t bs, int32_t MB,
+                           int32_t NB, void *stream) {
+  pgd_status s = check_tables(B, bs, MB, NB);
+  if (s != PGD_OK) return s;
+  if (N < 0) return fail(PGD_ERR_INVALID_ARG, "N = %d", N);
+  if (B > kMaxGrowRows) return fail(PGD_ERR_UNSUPPORTED, "B = %d > %d", B, kMaxGrowRows);
+  if (!token_starts || !result || !refs || !free_bits ||
+      (B && (!block_tables || !context_lens || !new_tokens || !positions || !copy_src ||
+             !copy_dst)) ||
+      (N && (!slots || !token_positions)))
+    return fail(PGD_ERR_INVALID_ARG, "null pointer");
+  if (!aligned(slots, 8)) return fail(PGD_ERR_INVALID_ARG, "slots must be 8-byte aligned");
+  GrowParams p = {};
+  p.tables = block_tables;
+  p.ctx = context_lens;
+  p.new_tokens = new_tokens;
+  p.refs = refs;
+  p.free_bits = reinterpret_cast<uint32_t *>(free_bits);
+  p.positions = positions;
+  p.starts = token_starts;
+  p.slots = slots;
+  p.token_positions = token_positions;
+  p.copy_src = copy_src;
+  p.copy_dst = copy_dst;
+  p.result = result;
+  p.B = B;
+  p.N = N;
+  p.bs = bs;
+  p.MB = MB;
+  p.NB = NB;
+  if ((s = error_word(&p.err)) != PGD_OK) return s;
+  const cudaError_t e = grow_tables_launch(p, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "grow_tables launch");
+  return ok();
+}
+
+pgd_status pgd_trim_tables(int32_t *block_tables, int32_t *context_lens,
+                           const int32_t *keep_lens, int32_t *refs, int32_t *free_bits, int32_t B,
+                           int32_t bs, int32_t MB, int32_t NB, void *stream) {
+  pgd_status s = check_tables(B, bs, MB, NB);
+  if (s != PGD_OK) return s;
+  if (B == 0) return ok();
+  if (!block_tables || !context_lens || !keep_lens || !refs || !free_bits)
+    return fail(PGD_ERR_INVALID_ARG, "null pointer");
+  TrimParams p = {};
+  p.tables = block_tables;
+  p.ctx = context_lens;
+  p.keep = keep_lens;
+  p.refs = refs;
+  p.free_bits = reinterpret_cast<uint32_t *>(free_bits);
+  p.B = B;
+  p.bs = bs;
+  p.MB = MB;
+  p.NB = NB;
+  if ((s = error_word(&p.err)) != PGD_OK) return s;
+  const cudaError_t e = trim_tables_launch(p, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "trim_tables launch");
+  return ok();
 }
 
 }  // extern "C"

@@ -155,6 +155,7 @@ copy_blocks_kernel(uint4 *__restrict__ k_cache, uint4 *__restrict__ v_cache,
                    int block_vecs, int NB, int32_t *err) {
   const int i = blockIdx.x;
   const int src = __ldg(src_ids + i), dst = __ldg(dst_ids + i);
+  if (src == -1 && dst == -1) return;  // a place without a pair
   if ((unsigned)src >= (unsigned)NB || (unsigned)dst >= (unsigned)NB) {
     if (threadIdx.x == 0 && blockIdx.y == 0) atomicOr(err, PGD_DEVERR_BAD_BLOCK_ID);
     return;
@@ -168,10 +169,10 @@ copy_blocks_kernel(uint4 *__restrict__ k_cache, uint4 *__restrict__ v_cache,
 }
 
 cudaError_t copy_blocks_launch(void *k_cache, void *v_cache, const int32_t *src_ids,
-                               const int32_t *dst_ids, int n, int n_kv, int bs, int NB,
+                               const int32_t *dst_ids, int n, int block_bytes, int NB,
                                int32_t *err, cudaStream_t stream) {
   if (n == 0) return cudaSuccess;
-  const int block_vecs = n_kv * bs * kHeadDim * 2 / 16;
+  const int block_vecs = block_bytes / 16;
   int chunks = (block_vecs + 255) / 256;
   if (chunks > 64) chunks = 64;
   dim3 grid(n, chunks);
