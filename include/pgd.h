@@ -714,7 +714,7 @@ pgd_status pgd_rope_append(void *q_out, const void *q, const void *k, const void
  * copies -1, so that the step's appends write nothing.  (2 also sets
  * PGD_DEVERR_BAD_POSITION.)  A row with a negative length or count, or more than
  * MB * bs tokens, sets PGD_DEVERR_BAD_CONTEXT, one whose last block's id is bad
- * PGD_DEVERR_BAD_BLOCK_ID; it gets no tokens.  B at most 16384.
+ * PGD_DEVERR_BAD_BLOCK_ID; it gets no tokens.  B at most 16384, N and NB below 2^30.
  *
  * pgd_trim_tables cuts row b to keep_lens[b] tokens (no change where it has no
  * more; 0 releases the request): entries behind them become -1, their blocks

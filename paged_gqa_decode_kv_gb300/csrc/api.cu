@@ -1787,17 +1787,26 @@ pgd_status pgd_kv_read_fp4(void *k_out, void *v_out, const void *k_cache, const 
                         token_starts, B, T, N, n_kv, d, bs, MB, NB, k_scale, v_scale, stream);
 }
 
-// The grid of a call: its parts, or a number that goes by the device alone.
-static long long fp4_grid(int32_t B, int32_t n_kv, int32_t num_splits, int sms) {
-  return num_splits > 0 ? (long long)num_splits * B * n_kv
-                        : attention_fp4_grid((long long)B * n_kv, sms);
+// The most CTAs of a call, one a part; tokens: MB * bs.
+static long long fp4_grid(int32_t B, int32_t n_kv, long long tokens, int32_t num_splits, int sms) {
+  const long long units = (long long)B * n_kv;
+  return num_splits > 0 ? num_splits * units : attention_fp4_grid(units, tokens, sms);
+}
+
+// A slot for every CTA (ws_layout adds the units).
+static WsLayout fp4_layout(int32_t B, int32_t n_q, int32_t n_kv, long long grid) {
+  return ws_layout(B, n_q, n_kv, grid - std::min(grid, (long long)B * n_kv), true);
 }
 
 size_t pgd_fp4_workspace_size(int32_t B, int32_t n_q, int32_t n_kv, int32_t d,
                               int32_t num_splits) {
   if (B < 0 || n_kv <= 0 || n_q <= 0 || n_q % n_kv || d != kHeadDim || num_splits < 0) return 0;
   if ((long long)B * n_kv > kMaxBlockUnits) return 0;
-  return ws_layout(B, n_q, n_kv, fp4_grid(B, n_kv, num_splits, sm_count()), true).total;
+  // (tables of any width: few short contexts take the larger grid)
+  const int sms = sm_count();
+  return fp4_layout(B, n_q, n_kv, std::max(fp4_grid(B, n_kv, 1LL << 31, num_splits, sms),
+                                           num_splits ? 0 : (long long)B * n_kv + 12LL * sms))
+      .total;
 }
 
 static pgd_status attention_fp4_call(void *out, const void *q, const void *k_new,
@@ -1826,8 +1835,8 @@ static pgd_status attention_fp4_call(void *out, const void *q, const void *k_new
     return fail(PGD_ERR_UNSUPPORTED, "B * n_kv * MB * bs >= 2^35");
   if (!workspace) return fail(PGD_ERR_WORKSPACE, "workspace is NULL");
   if (!aligned(workspace, kWsAlign)) return fail(PGD_ERR_WORKSPACE, "workspace not 256-aligned");
-  const long long grid = fp4_grid(B, n_kv, num_splits, sm_count());
-  const WsLayout L = ws_layout(B, n_q, n_kv, grid, true);
+  const long long grid = fp4_grid(B, n_kv, (long long)MB * bs, num_splits, sm_count());
+  const WsLayout L = fp4_layout(B, n_q, n_kv, grid);
   if (workspace_bytes < L.total)
     return fail(PGD_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, L.total);
   Attn4Params p = {};
@@ -1848,9 +1857,10 @@ static pgd_status attention_fp4_call(void *out, const void *q, const void *k_new
   p.a.counters = reinterpret_cast<int32_t *>(ws + L.counters);
   p.a.part_ml = reinterpret_cast<float *>(ws + L.part_ml);
   p.a.part_o = reinterpret_cast<float *>(ws + L.part_o);
-  p.a.auto_split = num_splits == 0 ? 1 : 0;
   p.a.wait_late = append ? 1 : 0;  // the append writes only the cache
+  p.a.wait_limit_ns = g_wait_limit_ns.load();
   p.v_scale = v_scale;
+  p.splits = num_splits;
   if (append) {
     Kv4Params ap = {};
     ap.k_new = static_cast<const __nv_bfloat16 *>(k_new);
@@ -1873,7 +1883,7 @@ static pgd_status attention_fp4_call(void *out, const void *q, const void *k_new
     const cudaError_t e = kv_append_fp4_launch(ap, stream);
     if (e != cudaSuccess) return cuda_fail(e, "kv_append_fp4 launch");
   }
-  const cudaError_t e = attention_fp4_launch(p, n_q / n_kv, bs, (int)grid, stream);
+  const cudaError_t e = attention_fp4_launch(p, n_q / n_kv, bs, (int)grid, sm_count(), stream);
   if (e != cudaSuccess) return cuda_fail(e, "4-bit attention launch");
   return ok();
 }
@@ -2076,6 +2086,8 @@ pgd_status pgd_grow_tables(int32_t *block_tables, int32_t *context_lens,
   if (s != PGD_OK) return s;
   if (N < 0) return fail(PGD_ERR_INVALID_ARG, "N = %d", N);
   if (B > kMaxGrowRows) return fail(PGD_ERR_UNSUPPORTED, "B = %d > %d", B, kMaxGrowRows);
+  if (N >= 1 << 30 || NB >= 1 << 30)
+    return fail(PGD_ERR_UNSUPPORTED, "N = %d, NB = %d (below 2^30)", N, NB);
   if (!token_starts || !result || !refs || !free_bits ||
       (B && (!block_tables || !context_lens || !new_tokens || !positions || !copy_src ||
              !copy_dst)) ||

@@ -25,17 +25,20 @@
 //
 // Copies.  Each warp has a ring of its own of 32-token steps, filled by
 // 16-byte asynchronous copies and waited for by that warp alone: no barrier
-// and no wait on another warp while a context is read.
+// and no wait on another warp while a context is read.  (Bulk copies of whole
+// tiles on barriers of the warp took 224 us where these took 213 on 64 ragged
+// contexts with eight heads.)
 //
-// Split.  The steps of all units (sequence, KV head) lie on one line, in that
-// order, cut into equal parts, one a CTA.  A cut within `snap` steps of a
-// unit's end moves there, so that units are not split for nothing.  A CTA's
-// warps take its steps of a unit in turn and merge their states in shared
-// memory; parts of a unit go through the workspace, merged by the CTA that
-// finishes last, in the order of the parts.
+// Split.  A unit (sequence, KV head) is cut into parts of nearly equal size, of
+// at most the total over a number of CTAs that goes by the SMs: one part a CTA,
+// four CTAs an SM side by side and the rest as those finish, so that one's start
+// and end lie beside another's stream.  A CTA's warps take its steps in turn and
+// merge their states in shared memory; parts of a unit go through the
+// workspace, merged by the CTA that finishes last, in the order of the parts.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 
 #include "kv_fp4.cuh"
@@ -48,6 +51,8 @@ constexpr int kStepBytes = 2 * 2 * kGroupBytes4;  // K and V of two groups
 constexpr int kStages = 3;
 constexpr int kHeads = 8;              // query heads a product takes
 constexpr int kMergeRow = kHeadDim + 4;  // floats between heads when states are merged
+constexpr int kLeastSteps = 8;         // steps of a part of an automatic split
+constexpr int kManySteps = 25;          // steps a warp from which three CTAs follow one another
 constexpr float kMoveLog2 = 8.f;       // move the reference when exceeded by 2^8
 constexpr float kUnitLog2 = 7.f;       // a weight of the reference is 2^7
 
@@ -56,13 +61,16 @@ constexpr int ring_bytes() {
   return W * kStages * kStepBytes;
 }
 template <int W>
-constexpr size_t smem_bytes(int B) {
-  return (size_t)ring_bytes<W>() + W * kHeads * 8 + 64 + (size_t)(B + 1) * 4;
+constexpr size_t smem_bytes() {
+  return (size_t)ring_bytes<W>() + W * kHeads * 8 + 16 + W * 4;
 }
 static_assert(kHeads * kMergeRow * 4 <= kStages * kStepBytes, "a warp's state fits its ring");
 
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+// 16 bytes, or zeros (bytes = 0); read once, so the first to leave L2.
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, uint32_t bytes,
+                                       uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst),
+               "l"(src), "r"(bytes), "l"(policy)
                : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -73,7 +81,7 @@ __device__ __forceinline__ void copies_wait() {
 
 __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                           uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -93,47 +101,156 @@ __device__ __forceinline__ uint32_t times(uint32_t a, __half2 s) {
   return half2_bits(__hmul2(bits_half2(a), s));
 }
 
-// The line of steps: sequence b's units begin at pre[b], n_kv of them with
-// (pre[b + 1] - pre[b]) / n_kv steps each.
-struct Line {
-  const int *pre;
-  int B, n_kv, total;
-};
-struct Unit {
-  int b, h, start, steps;  // start: on the line
-};
-// The unit of step x (0 <= x < total).
-__device__ __forceinline__ Unit unit_at(const Line &l, int x) {
-  int lo = 0, hi = l.B;  // pre[lo] <= x < pre[hi]
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (l.pre[mid] <= x) lo = mid; else hi = mid;
+// Steps of a sequence's units (0: a bad context).
+__device__ __forceinline__ int unit_steps(const AttnParams &a, int BS, int b, int &ctx) {
+  ctx = __ldg(a.ctx + b);
+  if (ctx < 1 || ctx > a.MB * BS) {
+    if (blockIdx.x == 0) atomicOr(a.err, PGD_DEVERR_BAD_CONTEXT);
+    return 0;
   }
-  Unit u;
-  u.b = lo;
-  u.steps = (l.pre[lo + 1] - l.pre[lo]) / l.n_kv;
-  u.h = (x - l.pre[lo]) / u.steps;
-  u.start = l.pre[lo] + u.h * u.steps;
-  return u;
+  return (ctx - 1) / kStepTokens + 1;
 }
 
-// Equal cuts: CTA c's part of the line before any moves.
-struct Cuts {
-  int n, q, r, snap;  // parts; r of them have q + 1 steps, the others q
-  __device__ __forceinline__ int at(int c) const { return c * q + min(c, r); }
-  // The least c with at(c) >= x.
-  __device__ __forceinline__ int reach(int x) const {
-    const int head = r * (q + 1);
-    return x <= head ? (x + q) / (q + 1) : r + (x - head + q - 1) / q;
-  }
+// Parts of a unit with `steps` steps: of at most `part` each, or a given number.
+__device__ __forceinline__ int parts_of(int steps, int part, int splits) {
+  return splits ? min(splits, steps) : (steps + part - 1) / part;
+}
+
+// What a CTA does: steps [i0, i1) of a unit, which is part `part` of `parts`.
+struct Part {
+  bool some;
+  int b, h, ctx, steps, part, parts;
+  int i0, i1;
+  int first;   // the CTA of (part 0, head 0) of this sequence
 };
-__device__ __forceinline__ int cut(const Line &l, const Cuts &k, int c) {
-  const int x = k.at(c);
-  if (x >= l.total) return l.total;
-  const Unit u = unit_at(l, x);
-  if (x - u.start <= k.snap) return u.start;
-  if (u.start + u.steps - x <= k.snap) return u.start + u.steps;
+
+__device__ __forceinline__ int inclusive_sum(int x, int lane) {
+#pragma unroll
+  for (int i = 1; i < 32; i <<= 1) {
+    const int y = __shfl_up_sync(kFullMask, x, i);
+    if (lane >= i) x += y;
+  }
   return x;
+}
+
+// Finds CTA blockIdx.x's part.  Called by every thread; `scratch` holds W ints.
+// Up to 32 sequences every warp finds it in its lanes, without a barrier; of
+// more a warp looks at a run.
+template <int W>
+__device__ __forceinline__ Part find_part(const Attn4Params &p, int BS, int *scratch) {
+  const AttnParams &a = p.a;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int runs = a.B <= 32 ? 1 : W, run = (a.B + 32 * runs - 1) / (32 * runs) * 32;
+  const int b0 = a.B <= 32 ? 0 : warp * run;
+  Part r;
+  r.some = false;
+  int ctx = 0, steps = 0;
+  int sum = 0;
+  for (int i = 0; i < run && b0 + i < a.B; i += 32) {
+    steps = b0 + i + lane < a.B ? unit_steps(a, BS, b0 + i + lane, ctx) : 0;
+    sum += __reduce_add_sync(kFullMask, steps);
+  }
+  int total = sum;
+  if (runs > 1) {
+    if (lane == 0) scratch[warp] = sum;
+    __syncthreads();
+    total = 0;
+#pragma unroll
+    for (int i = 0; i < W; ++i) total += scratch[i];
+    __syncthreads();
+  }
+  // Parts of at most `part` steps (total * n_kv < 2^30): as many as CTAs are
+  // resident at once, or where that leaves each with much to do three times as
+  // many.
+  const int all = total * a.n_kv;
+  int part;
+  if (all / (W * p.resident) >= kManySteps) {
+    part = (all - 1) / (3 * p.resident) + 1;
+  } else {
+    part = max(kLeastSteps, (all - 1) / p.resident + 1);
+    for (int tries = 0; tries < 4; ++tries) {
+      int count = 0;
+      for (int i = 0; i < run && b0 + i < a.B; i += 32) {
+        if (runs > 1) steps = b0 + i + lane < a.B ? unit_steps(a, BS, b0 + i + lane, ctx) : 0;
+        count += __reduce_add_sync(kFullMask, parts_of(steps, part, 0));
+      }
+      if (runs > 1) {
+        if (lane == 0) scratch[warp] = count;
+        __syncthreads();
+        count = 0;
+#pragma unroll
+        for (int i = 0; i < W; ++i) count += scratch[i];
+        __syncthreads();
+      }
+      count *= a.n_kv;
+      if (count <= p.resident || count <= a.B * a.n_kv) break;
+      part = max(part + 1, (int)((float)part * (float)count / (float)p.resident));
+    }
+  }
+  int before = 0;  // CTAs of the sequences before
+  if (runs > 1) {
+    int mine = 0;
+    for (int i = 0; i < run && b0 + i < a.B; i += 32) {
+      const int b = b0 + i + lane;
+      const int n = b < a.B ? unit_steps(a, BS, b, ctx) : 0;
+      mine += __reduce_add_sync(kFullMask, parts_of(n, part, p.splits));
+    }
+    if (lane == 0) scratch[warp] = mine;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < W; ++i)
+      if (i < warp) before += scratch[i];
+    __syncthreads();
+    before *= a.n_kv;
+  }
+  const int cta = blockIdx.x;
+  bool found = false;
+  int n = 0, at = 0;
+  for (int i = 0; i < run && b0 + i < a.B; i += 32) {
+    if (runs > 1) steps = b0 + i + lane < a.B ? unit_steps(a, BS, b0 + i + lane, ctx) : 0;
+    n = parts_of(steps, part, p.splits);
+    const int upto = before + inclusive_sum(n, lane) * a.n_kv;
+    at = upto - n * a.n_kv;
+    const uint32_t hit = __ballot_sync(kFullMask, n > 0 && at <= cta && cta < upto);
+    if (hit) {
+      const int l = __ffs(hit) - 1;
+      r.b = b0 + i + l;
+      r.ctx = __shfl_sync(kFullMask, ctx, l);
+      r.steps = __shfl_sync(kFullMask, steps, l);
+      r.parts = __shfl_sync(kFullMask, n, l);
+      r.first = __shfl_sync(kFullMask, at, l);
+      found = true;
+    }
+    before = __shfl_sync(kFullMask, upto, 31);
+  }
+  if (runs > 1) {  // one warp has found it, or none
+    __shared__ int got[6];
+    if (threadIdx.x == 0) got[5] = 0;
+    __syncthreads();
+    if (found && lane == 0) {
+      got[0] = r.b;
+      got[1] = r.ctx;
+      got[2] = r.steps;
+      got[3] = r.parts;
+      got[4] = r.first;
+      got[5] = 1;
+    }
+    __syncthreads();
+    r.b = got[0];
+    r.ctx = got[1];
+    r.steps = got[2];
+    r.parts = got[3];
+    r.first = got[4];
+    found = got[5];
+  }
+  if (!found) return r;
+  r.some = true;
+  r.part = (cta - r.first) / a.n_kv;
+  r.h = cta - r.first - r.part * a.n_kv;
+  const int q = r.steps / r.parts, left = r.steps - q * r.parts;
+  r.i0 = r.part * q + min(r.part, left);
+  r.i1 = r.i0 + q + (r.part < left ? 1 : 0);
+  return r;
 }
 
 template <int BS, int W>
@@ -142,13 +259,16 @@ struct Worker {
   int lane, g, t4, warp;
   unsigned char *ring;  // this warp's
   uint32_t ring_at;
+  uint64_t policy;
 
   // Fragments and state.
   uint32_t qf[16];
   float f0, f1;      // factors of the scores of heads 2 t4, 2 t4 + 1 (log2 domain)
-  float m0, m1;      // references
+  float m0, m1;      // references (log2 domain)
+  float limit0, limit1;  // products at which they move
   float l0, l1;      // this lane's part of the sums
   float o[8][4];     // dims 16 i + g (+ 8) of those two heads
+  uint32_t pf[2][2]; // weights of a step's tokens as operands
 
   __device__ __forceinline__ Worker(const Attn4Params &p_, unsigned char *smem) : p(p_) {
     lane = threadIdx.x & 31;
@@ -157,31 +277,30 @@ struct Worker {
     t4 = lane & 3;
     ring = smem + warp * kStages * kStepBytes;
     ring_at = smem_addr(ring);
+    policy = l2_policy_evict_first();
   }
 
-  // The query as operand registers: lane (g, t4) holds dims 32 t4 .. + 31 of
-  // head g, in the order in which K's codes lie.
-  __device__ __forceinline__ void load_query(int b, int h, int G) {
-    float x[32];
+  // The query's loads: lane (g, t4) holds dims 32 t4 .. + 31 of head g.
+  __device__ __forceinline__ void fetch_query(int b, int h, int G, uint4 (&v)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i] = make_uint4(0, 0, 0, 0);
+      if (g < G)
+        v[i] = __ldg(reinterpret_cast<const uint4 *>(
+                         p.a.q + ((size_t)b * p.a.n_q + (size_t)h * G + g) * kHeadDim + 32 * t4) +
+                     i);
+    }
+  }
+  // As operand registers, in the order in which K's codes lie; the state of a
+  // unit without tokens.
+  __device__ __forceinline__ void start(const uint4 (&v)[4]) {
     uint32_t top = 0;
-    if (g < G) {
-      const uint4 *src = reinterpret_cast<const uint4 *>(
-          p.a.q + ((size_t)b * p.a.n_q + (size_t)h * G + g) * kHeadDim + 32 * t4);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint4 v = __ldg(src + i);
-        float y[8];
-        unpack8(v, y);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[8 * i + j] = y[j];
-        top = __vmaxu2(top, v.x & 0x7fff7fffu);
-        top = __vmaxu2(top, v.y & 0x7fff7fffu);
-        top = __vmaxu2(top, v.z & 0x7fff7fffu);
-        top = __vmaxu2(top, v.w & 0x7fff7fffu);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 32; ++i) x[i] = 0.f;
+    for (int i = 0; i < 4; ++i) {
+      top = __vmaxu2(top, v[i].x & 0x7fff7fffu);
+      top = __vmaxu2(top, v[i].y & 0x7fff7fffu);
+      top = __vmaxu2(top, v[i].z & 0x7fff7fffu);
+      top = __vmaxu2(top, v[i].w & 0x7fff7fffu);
     }
     top = max(top & 0xffffu, top >> 16);
     top = max(top, __shfl_xor_sync(kFullMask, top, 1));
@@ -190,12 +309,18 @@ struct Worker {
     const int e = max((int)(top >> 7) - 127, -100);
     const float up = pow2f(14 - e);
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      qf[i] = half2_bits(__floats2half2_rn(x[2 * i] * up, x[2 * i + 1] * up));
-    const float back = p.a.qk_scale_log2 * pow2f(e - 14);
+    for (int i = 0; i < 4; ++i) {
+      float x[8];
+      unpack8(v[i], x);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        qf[4 * i + j] = half2_bits(__floats2half2_rn(x[2 * j] * up, x[2 * j + 1] * up));
+    }
+    // (never 0, which would make a masked score of minus infinity NaN)
+    const float back = fmaxf(p.a.qk_scale_log2 * pow2f(e - 14), 0x1p-126f);
     f0 = __shfl_sync(kFullMask, back, 8 * t4);
     f1 = __shfl_sync(kFullMask, back, 8 * t4 + 4);
-    m0 = m1 = __uint_as_float(0xff800000u);
+    m0 = m1 = limit0 = limit1 = __uint_as_float(0xff800000u);
     l0 = l1 = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -211,11 +336,11 @@ struct Worker {
       const unsigned char *k = p.a.k_cache + at, *v = p.a.v_cache + at;
       const uint32_t n = id0 >= 0 ? 16u : 0u;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) copy16(dst + j * 512, k + lane * 16 + j * 512, n);
+      for (int j = 0; j < 4; ++j) copy16(dst + j * 512, k + lane * 16 + j * 512, n, policy);
       // the fifth goes on from K (128 more bytes ... 144 pieces) to V
-      copy16(dst + 4 * 512, lane < 16 ? k + lane * 16 + 2048 : v + (lane - 16) * 16, n);
+      copy16(dst + 4 * 512, lane < 16 ? k + lane * 16 + 2048 : v + (lane - 16) * 16, n, policy);
 #pragma unroll
-      for (int j = 5; j < 9; ++j) copy16(dst + j * 512, v + (lane - 16) * 16 + (j - 4) * 512, n);
+      for (int j = 5; j < 9; ++j) copy16(dst + j * 512, v + (lane - 16) * 16 + (j - 4) * 512, n, policy);
     } else {
       const size_t a0 = ((size_t)max(id0, 0) * p.a.n_kv + h) * kGroupBytes4;
       const size_t a1 = ((size_t)max(id1, 0) * p.a.n_kv + h) * kGroupBytes4;
@@ -223,65 +348,78 @@ struct Worker {
       const unsigned char *k1 = p.a.k_cache + a1, *v1 = p.a.v_cache + a1;
       const uint32_t n0 = id0 >= 0 ? 16u : 0u, n1 = id1 >= 0 ? 16u : 0u;
       const int x = lane * 16;
-      copy16(dst, k0 + x, n0);
-      copy16(dst + 512, k0 + x + 512, n0);
-      copy16(dst + 1024, lane < 8 ? k0 + x + 1024 : k1 + (x - 128), lane < 8 ? n0 : n1);
-      copy16(dst + 1536, k1 + (x - 128) + 512, n1);
-      copy16(dst + 2048, lane < 16 ? k1 + (x - 128) + 1024 : v0 + (x - 256), lane < 16 ? n1 : n0);
-      copy16(dst + 2560, v0 + (x - 256) + 512, n0);
-      copy16(dst + 3072, lane < 24 ? v0 + (x - 256) + 1024 : v1 + (x - 384), lane < 24 ? n0 : n1);
-      copy16(dst + 3584, v1 + (x - 384) + 512, n1);
-      copy16(dst + 4096, v1 + (x - 384) + 1024, n1);
+      copy16(dst, k0 + x, n0, policy);
+      copy16(dst + 512, k0 + x + 512, n0, policy);
+      copy16(dst + 1024, lane < 8 ? k0 + x + 1024 : k1 + (x - 128), lane < 8 ? n0 : n1, policy);
+      copy16(dst + 1536, k1 + (x - 128) + 512, n1, policy);
+      copy16(dst + 2048, lane < 16 ? k1 + (x - 128) + 1024 : v0 + (x - 256), lane < 16 ? n1 : n0, policy);
+      copy16(dst + 2560, v0 + (x - 256) + 512, n0, policy);
+      copy16(dst + 3072, lane < 24 ? v0 + (x - 256) + 1024 : v1 + (x - 384), lane < 24 ? n0 : n1, policy);
+      copy16(dst + 3584, v1 + (x - 384) + 512, n1, policy);
+      copy16(dst + 4096, v1 + (x - 384) + 1024, n1, policy);
     }
   }
 
-  // One step of 32 tokens, `valid` of them (32 but at a context's end).
-  __device__ __forceinline__ void compute(int slot, int valid) {
-    unsigned char *st = ring + slot * kStepBytes;
-    if (valid < kStepTokens) {
-      // tokens behind the context: their V scales to zero (they may hold NaN)
-      for (int i = lane; i < kStepTokens * 8; i += 32) {
-        const int t = i >> 3, c = i & 7;
-        if (t >= valid)
-          st[2 * kGroupBytes4 + (t >> 4) * kGroupBytes4 + kGroupCodes4 + ((t & 15) >> 2) * 32 +
-             c * 4 + (t & 3)] = 0;
-      }
-      __syncwarp();
-    }
-    const int tok = 4 * (g >> 1) + (g & 1);  // row g of the product; row g + 8 is tok + 2
-    float s[2][4];
+  // Quarter w of the scores of a step, s += : both groups' 16 tokens by two of
+  // the eight steps over the dims.
+  struct Keys {
+    uint4 a[2], b[2];        // codes of token rows g and g + 8 of the product
+    __half2 sa[2], sb[2];    // their scales of this lane's 32 dims
+  };
+  __device__ __forceinline__ void load_keys(const unsigned char *st, Keys &x) {
+    const int tok = 4 * (g >> 1) + (g & 1);  // row g; row g + 8 is tok + 2
 #pragma unroll
     for (int sub = 0; sub < 2; ++sub) {
       const unsigned char *k = st + sub * kGroupBytes4;
-      const uint4 a = *reinterpret_cast<const uint4 *>(k + tok * 64 + t4 * 16);
-      const uint4 b = *reinterpret_cast<const uint4 *>(k + tok * 64 + 128 + t4 * 16);
-      const __half2 sa = e4m3x2_to_half2(
+      x.a[sub] = *reinterpret_cast<const uint4 *>(k + tok * 64 + t4 * 16);
+      x.b[sub] = *reinterpret_cast<const uint4 *>(k + tok * 64 + 128 + t4 * 16);
+      x.sa[sub] = e4m3x2_to_half2(
           *reinterpret_cast<const uint16_t *>(k + kGroupCodes4 + tok * 8 + 2 * t4));
-      const __half2 sb = e4m3x2_to_half2(
+      x.sb[sub] = e4m3x2_to_half2(
           *reinterpret_cast<const uint16_t *>(k + kGroupCodes4 + tok * 8 + 16 + 2 * t4));
-      const uint32_t wa[4] = {a.x, a.y, a.z, a.w}, wb[4] = {b.x, b.y, b.z, b.w};
-      s[sub][0] = s[sub][1] = s[sub][2] = s[sub][3] = 0.f;
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const __half2 fa = w < 2 ? __low2half2(sa) : __high2half2(sa);
-        const __half2 fb = w < 2 ? __low2half2(sb) : __high2half2(sb);
-        uint32_t x[4], y[4];
-        e2m1x8_to_half2x4(wa[w], x);
-        e2m1x8_to_half2x4(wb[w], y);
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          mma_16816(s[sub], times(x[2 * i], fa), times(y[2 * i], fb), times(x[2 * i + 1], fa),
-                    times(y[2 * i + 1], fb), qf[4 * w + 2 * i], qf[4 * w + 2 * i + 1]);
-      }
     }
+  }
+  template <int w>
+  __device__ __forceinline__ void scores(const Keys &k, float (&s)[2][4]) {
 #pragma unroll
     for (int sub = 0; sub < 2; ++sub) {
-      s[sub][0] *= f0;
-      s[sub][1] *= f1;
-      s[sub][2] *= f0;
-      s[sub][3] *= f1;
+      const uint32_t wa = w == 0 ? k.a[sub].x : w == 1 ? k.a[sub].y : w == 2 ? k.a[sub].z : k.a[sub].w;
+      const uint32_t wb = w == 0 ? k.b[sub].x : w == 1 ? k.b[sub].y : w == 2 ? k.b[sub].z : k.b[sub].w;
+      const __half2 fa = w < 2 ? __low2half2(k.sa[sub]) : __high2half2(k.sa[sub]);
+      const __half2 fb = w < 2 ? __low2half2(k.sb[sub]) : __high2half2(k.sb[sub]);
+      uint32_t x[4], y[4];
+      e2m1x8_to_half2x4(wa, x);
+      e2m1x8_to_half2x4(wb, y);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        mma_16816(s[sub], times(x[2 * i], fa), times(y[2 * i], fb), times(x[2 * i + 1], fa),
+                  times(y[2 * i + 1], fb), qf[4 * w + 2 * i], qf[4 * w + 2 * i + 1]);
     }
+  }
+
+  // Quarter w of the outputs of a step: 64 dims of 16 tokens.
+  template <int w>
+  __device__ __forceinline__ void outputs(const unsigned char *st) {
+    constexpr int sub = w >> 1, half = w & 1;
+    const unsigned char *v = st + sub * kGroupBytes4;
+    const uint4 a = *reinterpret_cast<const uint4 *>(v + half * 512 + lane * 16);
+    const uint4 c = *reinterpret_cast<const uint4 *>(v + kGroupCodes4 + t4 * 32 + half * 16);
+    const uint32_t wa[4] = {a.x, a.y, a.z, a.w}, wc[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __half2 s01 = e4m3x2_to_half2((uint16_t)wc[i]);
+      const __half2 s23 = e4m3x2_to_half2((uint16_t)(wc[i] >> 16));
+      uint32_t x[4];
+      e2m1x8_to_half2x4(wa[i], x);  // dim row g: tokens 0 1, 2 3; dim row g + 8
+      mma_16816(o[4 * half + i], times(x[0], s01), times(x[2], s01), times(x[1], s23),
+                times(x[3], s23), pf[sub][0], pf[sub][1]);
+    }
+  }
+
+  // Weights from the products of a step with `valid` tokens.
+  __device__ __forceinline__ void weights(float (&s)[2][4], int valid) {
     if (valid < kStepTokens) {
+      const int tok = 4 * (g >> 1) + (g & 1);
       const float none = __uint_as_float(0xff800000u);
 #pragma unroll
       for (int sub = 0; sub < 2; ++sub) {
@@ -291,16 +429,18 @@ struct Worker {
     }
     float x0 = fmaxf(fmaxf(s[0][0], s[0][2]), fmaxf(s[1][0], s[1][2]));
     float x1 = fmaxf(fmaxf(s[0][1], s[0][3]), fmaxf(s[1][1], s[1][3]));
-    if (__any_sync(kFullMask, x0 > m0 + kMoveLog2 || x1 > m1 + kMoveLog2)) {
+    if (__any_sync(kFullMask, x0 > limit0 || x1 > limit1)) {
 #pragma unroll
       for (int i = 4; i < 32; i <<= 1) {
         x0 = fmaxf(x0, __shfl_xor_sync(kFullMask, x0, i));
         x1 = fmaxf(x1, __shfl_xor_sync(kFullMask, x1, i));
       }
-      const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);
+      const float n0 = fmaxf(m0, x0 * f0), n1 = fmaxf(m1, x1 * f1);
       const float r0 = exp2_approx(m0 - n0), r1 = exp2_approx(m1 - n1);
       m0 = n0;
       m1 = n1;
+      limit0 = __fdividef(m0 + kMoveLog2, f0);
+      limit1 = __fdividef(m1 + kMoveLog2, f1);
       l0 *= r0;
       l1 *= r1;
 #pragma unroll
@@ -311,45 +451,37 @@ struct Worker {
         o[i][3] *= r1;
       }
     }
-    uint32_t pf[2][2];
     const float b0 = kUnitLog2 - m0, b1 = kUnitLog2 - m1;
 #pragma unroll
     for (int sub = 0; sub < 2; ++sub) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const float w0 = exp2_approx(s[sub][2 * i] + b0), w1 = exp2_approx(s[sub][2 * i + 1] + b1);
+        const float w0 = exp2_approx(fmaf(s[sub][2 * i], f0, b0)),
+                    w1 = exp2_approx(fmaf(s[sub][2 * i + 1], f1, b1));
         l0 += w0;
         l1 += w1;
         pf[sub][i] = transposed(half2_bits(__floats2half2_rn(w0, w1)));
       }
     }
-#pragma unroll
-    for (int sub = 0; sub < 2; ++sub) {
-      const unsigned char *v = st + (2 + sub) * kGroupBytes4;
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const uint4 a = *reinterpret_cast<const uint4 *>(v + half * 512 + lane * 16);
-        const uint4 c = *reinterpret_cast<const uint4 *>(v + kGroupCodes4 + t4 * 32 + half * 16);
-        const uint32_t wa[4] = {a.x, a.y, a.z, a.w}, wc[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const __half2 s01 = e4m3x2_to_half2((uint16_t)wc[i]);
-          const __half2 s23 = e4m3x2_to_half2((uint16_t)(wc[i] >> 16));
-          uint32_t x[4];
-          e2m1x8_to_half2x4(wa[i], x);  // dim row g: tokens 0 1, 2 3; dim row g + 8
-          mma_16816(o[4 * half + i], times(x[0], s01), times(x[2], s01), times(x[1], s23),
-                    times(x[3], s23), pf[sub][0], pf[sub][1]);
-        }
-      }
+  }
+
+  // The last step's tokens behind the context: their V scales to zero (they may
+  // hold NaN).
+  __device__ __forceinline__ void clear_scales(unsigned char *st, int valid) {
+    for (int i = lane; i < kStepTokens * 8; i += 32) {
+      const int t = i >> 3, c = i & 7;
+      if (t >= valid)
+        st[(t >> 4) * kGroupBytes4 + kGroupCodes4 + ((t & 15) >> 2) * 32 + c * 4 + (t & 3)] = 0;
     }
+    __syncwarp();
   }
 
   // Steps i0 + warp, + W, ... below i1 of one unit.
-  __device__ __forceinline__ void run(const Unit &u, int ctx, int i0, int i1) {
+  __device__ __forceinline__ void run(const Part &u, int G) {
     const int32_t *row = p.a.tables + (size_t)u.b * p.a.MB;
-    const int nblk = (ctx - 1) / BS + 1;
-    const int first = i0 + warp;
-    const int n = first < i1 ? (i1 - first + W - 1) / W : 0;
+    const int nblk = (u.ctx - 1) / BS + 1;
+    const int first = u.i0 + warp;
+    const int n = first < u.i1 ? (u.i1 - first + W - 1) / W : 0;
     int a0 = -1, a1 = -1;  // lane l: the ids of the warp's step 32 j + l
     auto ids = [&](int k0) {
       const int t = first + (k0 + lane) * W;
@@ -363,24 +495,42 @@ struct Worker {
         }
       }
     };
-    auto issue = [&](int k) {
+    auto issue = [&](int k, int slot) {
       if (k < n) {
         if ((k & 31) == 0) ids(k);
-        load_step(k % kStages, __shfl_sync(kFullMask, a0, k & 31),
+        load_step(slot, __shfl_sync(kFullMask, a0, k & 31),
                   BS == 32 ? -1 : __shfl_sync(kFullMask, a1, k & 31), u.h);
       }
       copies_commit();
     };
+    // the query's loads before the copies, which they would queue behind
+    uint4 q[4];
+    fetch_query(u.b, u.h, G, q);
 #pragma unroll
-    for (int k = 0; k < kStages - 1; ++k) issue(k);
+    for (int k = 0; k < kStages - 1; ++k) issue(k, k);
+    start(q);
     int slot = 0;
 #pragma unroll 1
     for (int k = 0; k < n; ++k) {
       copies_wait<kStages - 2>();
       __syncwarp();  // every lane's copies have landed, and step k - 1 is read
-      issue(k + kStages - 1);
-      compute(slot, min(kStepTokens, ctx - (first + k * W) * kStepTokens));
-      slot = slot == kStages - 1 ? 0 : slot + 1;
+      issue(k + kStages - 1, slot == 0 ? kStages - 1 : slot - 1);
+      const int valid = min(kStepTokens, u.ctx - (first + k * W) * kStepTokens);
+      unsigned char *st = ring + slot * kStepBytes;
+      if (valid < kStepTokens) clear_scales(st + 2 * kGroupBytes4, valid);
+      Keys x;
+      load_keys(st, x);
+      float s[2][4] = {};
+      scores<0>(x, s);
+      scores<1>(x, s);
+      scores<2>(x, s);
+      scores<3>(x, s);
+      weights(s, valid);
+      outputs<0>(st + 2 * kGroupBytes4);
+      outputs<1>(st + 2 * kGroupBytes4);
+      outputs<2>(st + 2 * kGroupBytes4);
+      outputs<3>(st + 2 * kGroupBytes4);
+      if (++slot == kStages) slot = 0;
     }
     copies_wait<0>();
   }
@@ -392,176 +542,180 @@ struct Worker {
   }
 };
 
+__device__ __forceinline__ void store_row(__nv_bfloat16 *at, float4 v, float f) {
+  const __nv_bfloat162 y0 = __floats2bfloat162_rn(v.x * f, v.y * f);
+  const __nv_bfloat162 y1 = __floats2bfloat162_rn(v.z * f, v.w * f);
+  *reinterpret_cast<uint2 *>(at) = make_uint2(*reinterpret_cast<const uint32_t *>(&y0),
+                                              *reinterpret_cast<const uint32_t *>(&y1));
+}
+
+// A unit's parts, slots s0, s0 + n_kv, ..., to its G rows at `out`: a head by a
+// warp, or by W / G of them that take the parts in turn.
+template <int W>
+__device__ __forceinline__ void merge_parts(const Attn4Params &p, int G, size_t s0, int parts,
+                                            __nv_bfloat16 *out, unsigned char *smem) {
+  const AttnParams &a = p.a;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int sets = G < W ? W / G : 1;
+  const int set = G < W ? warp / G : 0;  // (G is a power of two)
+  float4 *sum = reinterpret_cast<float4 *>(smem);               // [W][32]
+  float2 *states = reinterpret_cast<float2 *>(smem + W * 512);  // [W] (max, sum)
+  constexpr int kBatch = 8;  // parts' loads in flight
+  for (int h = G < W ? warp % G : warp; h < G; h += W) {
+    const float2 *ml = reinterpret_cast<const float2 *>(a.part_ml) + s0 * G + h;
+    const float4 *o = reinterpret_cast<const float4 *>(a.part_o) + (s0 * G + h) * 32 + lane;
+    float M = __uint_as_float(0xff800000u), L = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+    for (int i0 = set; i0 < parts; i0 += kBatch * sets) {
+      float2 s[kBatch];
+      float4 v[kBatch];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const int i = i0 + j * sets;
+        const size_t at = (size_t)i * a.n_kv * G;
+        s[j] = make_float2(__uint_as_float(0xff800000u), 0.f);
+        v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i < parts) {
+          s[j] = __ldcg(ml + at);
+          v[j] = __ldcg(o + at * 32);
+        }
+      }
+      float top = M;
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) top = fmaxf(top, s[j].x);
+      const float keep = exp2_approx(M - top);
+      M = top;
+      L *= keep;
+      acc.x *= keep;
+      acc.y *= keep;
+      acc.z *= keep;
+      acc.w *= keep;
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const float r = exp2_approx(s[j].x - M);
+        L += s[j].y * r;
+        acc.x += v[j].x * r;
+        acc.y += v[j].y * r;
+        acc.z += v[j].z * r;
+        acc.w += v[j].w * r;
+      }
+    }
+    if (sets == 1) {
+      store_row(out + (size_t)h * kHeadDim + 4 * lane, acc, p.v_scale / L);
+    } else {
+      sum[warp * 32 + lane] = acc;
+      if (lane == 0) states[warp] = make_float2(M, L);
+    }
+  }
+  if (sets == 1) return;
+  __syncthreads();
+  if (warp < G) {
+    float M = states[warp].x, L = 0.f;
+    for (int i = 1; i < sets; ++i) M = fmaxf(M, states[i * G + warp].x);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < sets; ++i) {
+      // (a set without parts has no weight)
+      const float2 s = states[i * G + warp];
+      const float r = exp2_approx(s.x - M);
+      const float4 v = sum[(i * G + warp) * 32 + lane];
+      L += s.y * r;
+      acc.x += v.x * r;
+      acc.y += v.y * r;
+      acc.z += v.z * r;
+      acc.w += v.w * r;
+    }
+    store_row(out + (size_t)warp * kHeadDim + 4 * lane, acc, p.v_scale / L);
+  }
+}
+
 template <int BS, int W>
 __global__ void __launch_bounds__(W * 32, W == 4 ? 4 : 1)
     attention_fp4_kernel(const Attn4Params p, int G) {
-  extern __shared__ __align__(16) unsigned char smem[];
-  float2 *ml = reinterpret_cast<float2 *>(smem + ring_bytes<W>());  // [W][8] (max, sum)
-  int *flag = reinterpret_cast<int *>(smem + ring_bytes<W>() + W * kHeads * 8);
-  int *pre = flag + 16;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  extern __shared__ __align__(128) unsigned char smem[];
+  float *refs = reinterpret_cast<float *>(smem + ring_bytes<W>());  // [W][8] warps' references
+  float *sums = refs + W * kHeads;                                  // [W][8] and sums
+  int *flag = reinterpret_cast<int *>(sums + W * kHeads);
+  const int tid = threadIdx.x, warp = tid >> 5;
   const AttnParams &a = p.a;
 
   if (!a.wait_late) pdl_wait();
   pdl_launch_dependents();
+  const Part u = find_part<W>(p, BS, flag + 4);
+  if (a.wait_late) pdl_wait();
+  if (!u.some) return;
+  Worker<BS, W> w(p, smem);
+  w.run(u, G);
 
-  // The line: steps of every sequence's units, summed by warp 0.
-  if (warp == 0) {
-    int sum = 0;
-    for (int b0 = 0; b0 < a.B; b0 += 32) {
-      const int b = b0 + lane;
-      int n = 0;
-      if (b < a.B) {
-        const int ctx = __ldg(a.ctx + b);
-        if (ctx < 1 || ctx > a.MB * BS) {
-          if (blockIdx.x == 0) atomicOr(a.err, PGD_DEVERR_BAD_CONTEXT);
-        } else {
-          n = ((ctx - 1) / kStepTokens + 1) * a.n_kv;
-        }
-      }
+  // ---- the warps' states, merged
+  float l0 = w.l0, l1 = w.l1;
 #pragma unroll
-      for (int i = 1; i < 32; i <<= 1) {
-        const int y = __shfl_up_sync(kFullMask, n, i);
-        if (lane >= i) n += y;
-      }
-      if (b < a.B) pre[b + 1] = sum + n;
-      sum += __shfl_sync(kFullMask, n, 31);
+  for (int i = 4; i < 32; i <<= 1) {
+    l0 += __shfl_xor_sync(kFullMask, l0, i);
+    l1 += __shfl_xor_sync(kFullMask, l1, i);
+  }
+  if (w.g == 0) *reinterpret_cast<float2 *>(refs + warp * kHeads + 2 * w.t4) = make_float2(w.m0, w.m1);
+  __syncthreads();  // the rings are done with, the references written
+  float M0 = w.m0, M1 = w.m1;
+#pragma unroll
+  for (int i = 0; i < W; ++i) {
+    const float2 m = *reinterpret_cast<const float2 *>(refs + i * kHeads + 2 * w.t4);
+    M0 = fmaxf(M0, m.x);
+    M1 = fmaxf(M1, m.y);
+  }
+  {
+    const float r0 = exp2_approx(w.m0 - M0), r1 = exp2_approx(w.m1 - M1);
+    if (w.g == 0)
+      *reinterpret_cast<float2 *>(sums + warp * kHeads + 2 * w.t4) = make_float2(l0 * r0, l1 * r1);
+    float *mine = reinterpret_cast<float *>(w.ring) + 2 * w.t4 * kMergeRow + w.g;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      mine[16 * i] = w.o[i][0] * r0;
+      mine[16 * i + kMergeRow] = w.o[i][1] * r1;
+      mine[16 * i + 8] = w.o[i][2] * r0;
+      mine[16 * i + 8 + kMergeRow] = w.o[i][3] * r1;
     }
-    if (lane == 0) pre[0] = 0;
   }
   __syncthreads();
-  const Line line = {pre, a.B, a.n_kv, pre[a.B]};
-  Cuts k;
-  k.n = max(1, min((int)gridDim.x, line.total / p.steps_per_cta));
-  k.q = line.total / k.n;
-  k.r = line.total % k.n;
-  k.snap = a.auto_split ? min(k.q >> 3, 2 * W) : 0;
-  const int cta = blockIdx.x;
-  if (a.wait_late) pdl_wait();
-  if (cta >= k.n || line.total == 0) return;
-
-  const int end = cut(line, k, cta + 1);
-  int x = cut(line, k, cta);
-  Worker<BS, W> w(p, smem);
-  while (x < end) {
-    const Unit u = unit_at(line, x);
-    const int i0 = x - u.start, i1 = min(u.steps, end - u.start);
-    x = u.start + i1;
-    const int ctx = __ldg(a.ctx + u.b);
-    w.load_query(u.b, u.h, G);
-    w.run(u, ctx, i0, i1);
-
-    // ---- the warps' states, merged
-    float l0 = w.l0, l1 = w.l1;
+  const bool whole = u.parts == 1;
+  const int unit = u.b * a.n_kv + u.h;
+  const size_t slot = blockIdx.x;
+  __nv_bfloat16 *out = a.out + ((size_t)u.b * a.n_q + (size_t)u.h * G) * kHeadDim;
+  // two dims of a head a thread
+  for (int i = 2 * tid; i < G * kHeadDim; i += 64 * W) {
+    const int h = i >> 7;
+    const float *src = reinterpret_cast<const float *>(smem) + h * kMergeRow + (i & 127);
+    float L = 0.f;
+    float2 acc = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int i = 4; i < 32; i <<= 1) {
-      l0 += __shfl_xor_sync(kFullMask, l0, i);
-      l1 += __shfl_xor_sync(kFullMask, l1, i);
+    for (int j = 0; j < W; ++j) {
+      const float2 v = *reinterpret_cast<const float2 *>(src + j * (kStages * kStepBytes / 4));
+      L += sums[j * kHeads + h];
+      acc.x += v.x;
+      acc.y += v.y;
     }
-    if (w.g == 0) {
-      ml[warp * kHeads + 2 * w.t4] = make_float2(w.m0, l0);
-      ml[warp * kHeads + 2 * w.t4 + 1] = make_float2(w.m1, l1);
-    }
-    __syncthreads();  // the rings are done with, the references written
-    float M0 = w.m0, M1 = w.m1;
+    if (whole) {
+      const float inv = p.v_scale / L;
+      *reinterpret_cast<__nv_bfloat162 *>(out + i) = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
+    } else {
+      *reinterpret_cast<float2 *>(a.part_o + slot * G * kHeadDim + i) = acc;
+      if ((i & 127) == 0) {
+        float M = refs[h];
 #pragma unroll
-    for (int i = 0; i < W; ++i) {
-      M0 = fmaxf(M0, ml[i * kHeads + 2 * w.t4].x);
-      M1 = fmaxf(M1, ml[i * kHeads + 2 * w.t4 + 1].x);
-    }
-    {
-      const float r0 = exp2_approx(w.m0 - M0), r1 = exp2_approx(w.m1 - M1);
-      float *mine = reinterpret_cast<float *>(w.ring) + 2 * w.t4 * kMergeRow + w.g;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        mine[16 * i] = w.o[i][0] * r0;
-        mine[16 * i + kMergeRow] = w.o[i][1] * r1;
-        mine[16 * i + 8] = w.o[i][2] * r0;
-        mine[16 * i + 8 + kMergeRow] = w.o[i][3] * r1;
+        for (int j = 1; j < W; ++j) M = fmaxf(M, refs[j * kHeads + h]);
+        *reinterpret_cast<float2 *>(a.part_ml + (slot * G + h) * 2) = make_float2(M, L);
       }
     }
-    __syncthreads();
-    const bool whole = i0 == 0 && i1 == u.steps;
-    const int unit = u.b * a.n_kv + u.h;
-    const size_t slot = (size_t)unit + cta;
-    for (int h = warp; h < G; h += W) {
-      float M = ml[h].x;
-#pragma unroll
-      for (int i = 1; i < W; ++i) M = fmaxf(M, ml[i * kHeads + h].x);
-      float L = 0.f;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int i = 0; i < W; ++i) {
-        const float2 s = ml[i * kHeads + h];
-        L += s.y * exp2_approx(s.x - M);
-        const float4 v = *reinterpret_cast<const float4 *>(
-            smem + i * kStages * kStepBytes + (h * kMergeRow + 4 * lane) * 4);
-        acc.x += v.x;
-        acc.y += v.y;
-        acc.z += v.z;
-        acc.w += v.w;
-      }
-      if (whole) {
-        const float inv = p.v_scale / L;
-        const __nv_bfloat162 y0 = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
-        const __nv_bfloat162 y1 = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
-        *reinterpret_cast<uint2 *>(a.out + ((size_t)u.b * a.n_q + (size_t)u.h * G + h) * kHeadDim +
-                                   4 * lane) =
-            make_uint2(*reinterpret_cast<const uint32_t *>(&y0),
-                       *reinterpret_cast<const uint32_t *>(&y1));
-      } else {
-        if (lane == 0) *reinterpret_cast<float2 *>(a.part_ml + (slot * G + h) * 2) = make_float2(M, L);
-        *reinterpret_cast<float4 *>(a.part_o + (slot * G + h) * kHeadDim + 4 * lane) = acc;
-      }
-    }
-    if (!whole) {
-      // the parts of this unit: those of the CTAs first .. last
-      const int c1 = k.reach(u.start + k.snap + 1);
-      const int c2 = k.reach(u.start + u.steps - k.snap) - 1;
-      const int first = c1 - 1, parts = c2 - first + 1;
-      __syncthreads();
-      if (tid == 0) {
-        const int seen = atomic_add_acq_rel_gpu(a.counters + unit, 1);
-        if (seen == parts - 1) a.counters[unit] = 0;
-        *flag = seen == parts - 1;
-      }
-      __syncthreads();
-      if (*flag) {
-        __threadfence();
-        const size_t s0 = (size_t)unit + first;
-        for (int h = warp; h < G; h += W) {
-          float M = __uint_as_float(0xff800000u);
-          for (int i = lane; i < parts; i += 32)
-            M = fmaxf(M, __ldcg(a.part_ml + ((s0 + i) * G + h) * 2));
-#pragma unroll
-          for (int i = 16; i; i >>= 1) M = fmaxf(M, __shfl_xor_sync(kFullMask, M, i));
-          float L = 0.f;
-          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-          for (int i = 0; i < parts; ++i) {
-            const float2 s = __ldcg(reinterpret_cast<const float2 *>(a.part_ml + ((s0 + i) * G + h) * 2));
-            const float4 v = __ldcg(reinterpret_cast<const float4 *>(
-                a.part_o + ((s0 + i) * G + h) * kHeadDim + 4 * lane));
-            const float r = exp2_approx(s.x - M);
-            L += s.y * r;
-            acc.x += v.x * r;
-            acc.y += v.y * r;
-            acc.z += v.z * r;
-            acc.w += v.w * r;
-          }
-          const float inv = p.v_scale / L;
-          const __nv_bfloat162 y0 = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
-          const __nv_bfloat162 y1 = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
-          *reinterpret_cast<uint2 *>(a.out +
-                                     ((size_t)u.b * a.n_q + (size_t)u.h * G + h) * kHeadDim +
-                                     4 * lane) =
-              make_uint2(*reinterpret_cast<const uint32_t *>(&y0),
-                         *reinterpret_cast<const uint32_t *>(&y1));
-        }
-      }
-    }
-    __syncthreads();  // rings, states and flag are free again
   }
+  if (whole) return;
+  __syncthreads();
+  if (tid == 0) {
+    const int seen = atomic_add_acq_rel_gpu(a.counters + unit, 1);
+    if (seen == u.parts - 1) a.counters[unit] = 0;
+    *flag = seen == u.parts - 1;
+  }
+  __syncthreads();
+  if (*flag) merge_parts<W>(p, G, (size_t)u.first + u.h, u.parts, out, smem);
 }
 
 template <int BS, int W>
@@ -574,7 +728,7 @@ cudaError_t launch_kernel(const Attn4Params &p, int G, int grid, cudaStream_t st
   auto kernel = attention_fp4_kernel<BS, W>;
   if (!set[dev].load()) {
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)smem_bytes<W>(PGD_MAX_BATCH));
+                             (int)smem_bytes<W>());
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
                                cudaSharedmemCarveoutMaxShared);
@@ -584,7 +738,7 @@ cudaError_t launch_kernel(const Attn4Params &p, int G, int grid, cudaStream_t st
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(W * 32);
-  cfg.dynamicSmemBytes = smem_bytes<W>(p.a.B);
+  cfg.dynamicSmemBytes = smem_bytes<W>();
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -593,16 +747,33 @@ cudaError_t launch_kernel(const Attn4Params &p, int G, int grid, cudaStream_t st
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, p, G);
 }
-static_assert(smem_bytes<4>(PGD_MAX_BATCH) <= 232448, "layout exceeds 227 KB");
 
 }  // namespace
 
-int attention_fp4_grid(long long units, int sms) { return 4 * sms; }
+// 4 warps a CTA, four CTAs an SM, or 16 and one: for long contexts of units
+// that are so few that small parts would be many to merge, or so many that most
+// SMs have one whole.
+static int warps_of(long long units, long long tokens, int sms) {
+  const long long steps = units * ((tokens - 1) / kStepTokens + 1);
+  return steps >= 64LL * sms && (units <= 16 || (units <= sms && 4 * units > 3 * sms)) ? 16 : 4;
+}
+static long long resident_ctas(int W, int sms) { return W == 16 ? sms : 4LL * sms; }
 
-cudaError_t attention_fp4_launch(const Attn4Params &p_in, int G, int bs, int grid,
+// The most CTAs of an automatic call on tables of MB * bs = tokens.
+long long attention_fp4_grid(long long units, long long tokens, int sms) {
+  const long long steps = (tokens - 1) / kStepTokens + 1;
+  const long long most = units * ((steps - 1) / kLeastSteps + 1);
+  return std::min(most, units + 3 * resident_ctas(warps_of(units, tokens, sms), sms));
+}
+
+cudaError_t attention_fp4_launch(const Attn4Params &p_in, int G, int bs, int grid, int sms,
                                  cudaStream_t stream) {
   Attn4Params p = p_in;
-  p.steps_per_cta = p.a.auto_split ? 4 : 1;
+  const int W = warps_of((long long)p.a.B * p.a.n_kv, (long long)p.a.MB * bs, sms);
+  p.resident = (int)resident_ctas(W, sms);
+  if (W == 16)
+    return bs == 16 ? launch_kernel<16, 16>(p, G, grid, stream)
+                    : launch_kernel<32, 16>(p, G, grid, stream);
   return bs == 16 ? launch_kernel<16, 4>(p, G, grid, stream)
                   : launch_kernel<32, 4>(p, G, grid, stream);
 }

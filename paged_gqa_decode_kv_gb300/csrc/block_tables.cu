@@ -8,15 +8,18 @@
 // outcome is a function of the state alone, whatever order blocks came back in.
 // Every new token gets its slot (block * bs + offset) and its position.
 //
-// One CTA does the sums and the tables (the rows and the pool's bits are a few
-// kilobytes to 128 KiB, and what bounds it is a chain of dependent loads); the
-// tokens' slots follow in the same CTA while they are few, else in a second
-// launch over all SMs, which finds a token's row by bisection of the starts.
-// Nothing changes when the blocks do not suffice.
+// The rows and the pool's bits are a few kilobytes to 128 KiB; what bounds a
+// step's call is a chain of dependent loads (length, last entry, its references)
+// and barriers.  So one CTA takes three sums (blocks, tokens, free bits) in one
+// scan and gives out blocks and slots from shared memory.  Admissions (many
+// tokens) and large pools take a cluster of eight CTAs that share
+// the blocks to write, and a second launch over all SMs for the
+// tokens' slots.  Nothing changes when the blocks do not suffice.
 //
-// trim: a warp a row gives back the blocks behind the tokens that it keeps.
+// trim: a CTA a row gives back the blocks behind the tokens that it keeps.
 // Counts fall by atomics whose order does not matter; the row that takes the
 // last reference sets the block's bit.
+#include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
 #include "block_tables.cuh"
@@ -24,57 +27,56 @@
 namespace pgd {
 namespace {
 
-constexpr int kGrowThreads = 1024;
-constexpr int kGrowWarps = kGrowThreads / 32;
-constexpr int kSlotThreads = 256;
-// Up to this many token places are written by the CTA that builds the tables.
-constexpr int kInlineTokens = 8192;
+namespace cg = cooperative_groups;
 
-// Inclusive sum over the CTA, and the total.
-template <typename T>
-__device__ __forceinline__ T block_scan(T x, T *warp_sums, T &total) {
+constexpr int kCluster = 8;
+constexpr int kSlotThreads = 256;
+// Up to this many token places, and blocks of a pool, one CTA does everything.
+constexpr int kInlineTokens = 8192;
+constexpr int kInlineBlocks = 1 << 18;
+constexpr int kWords = 4;     // of the pool's bits a thread looks at
+constexpr int kIds = 2048;   // new ids that it keeps in shared memory
+constexpr int kMost = 1 << 30;  // sums end here: more than any pool or call has
+
+__device__ __forceinline__ int capped(int a, int b) { return min(a + b, kMost); }  // a, b <= kMost
+
+// Inclusive sums of x over the CTA's NT threads, and the totals.
+template <int NT, int N>
+__device__ __forceinline__ void block_scan(int (&x)[N], int (*sums)[32], int (&total)[N]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
-  for (int i = 1; i < 32; i <<= 1) {
-    const T y = __shfl_up_sync(kFullMask, x, i);
-    if (lane >= i) x += y;
-  }
-  if (lane == 31) warp_sums[warp] = x;
-  __syncthreads();
-  T w = warp_sums[lane];
+  for (int i = 1; i < 32; i <<= 1)
 #pragma unroll
-  for (int i = 1; i < 32; i <<= 1) {
-    const T y = __shfl_up_sync(kFullMask, w, i);
-    if (lane >= i) w += y;
+    for (int j = 0; j < N; ++j) {
+      const int y = __shfl_up_sync(kFullMask, x[j], i);
+      if (lane >= i) x[j] = capped(x[j], y);
+    }
+  if (lane == 31)
+#pragma unroll
+    for (int j = 0; j < N; ++j) sums[j][warp] = x[j];
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    int w = lane < NT / 32 ? sums[j][lane] : 0;
+#pragma unroll
+    for (int i = 1; i < NT / 32; i <<= 1) {
+      const int y = __shfl_up_sync(kFullMask, w, i);
+      if (lane >= i) w = capped(w, y);
+    }
+    total[j] = __shfl_sync(kFullMask, w, NT / 32 - 1);
+    const int before = __shfl_sync(kFullMask, w, max(warp - 1, 0));
+    if (warp) x[j] = capped(x[j], before);
   }
-  total = __shfl_sync(kFullMask, w, 31);
-  if (warp) x += __shfl_sync(kFullMask, w, warp - 1);
-  __syncthreads();  // warp_sums is free again
-  return x;
 }
-static_assert(kGrowWarps == 32, "one lane a warp in block_scan");
 
-// The row of token n: the last whose start is at most n (starts[B] > n).
-__device__ __forceinline__ int row_of_token(const int32_t *starts, int B, int n) {
+// The last row whose start is at most n (starts[B] > n).
+__device__ __forceinline__ int row_of(const int32_t *starts, int B, int n) {
   int lo = 0, hi = B;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (starts[mid] <= n) lo = mid; else hi = mid;
   }
   return lo;
-}
-
-__device__ __forceinline__ void place_token(const GrowParams &p, const int32_t *starts, int n,
-                                            int total) {
-  long long slot = -1;
-  int pos = 0;
-  if (n < total) {
-    const int b = row_of_token(starts, p.B, n);
-    pos = p.positions[b] + (n - starts[b]);
-    slot = (long long)p.tables[(size_t)b * p.MB + pos / p.bs] * p.bs + pos % p.bs;
-  }
-  p.slots[n] = slot;
-  p.token_positions[n] = pos;
 }
 
 // Word w of the pool's bits; bits past the pool do not count.
@@ -84,150 +86,295 @@ __device__ __forceinline__ uint32_t free_word(const GrowParams &p, int w) {
   return left < 32 ? bits & ((1u << left) - 1u) : bits;
 }
 
-__global__ void __launch_bounds__(kGrowThreads) grow_tables_kernel(const GrowParams p) {
+// The place of set bit n (from 0) of a word that has more than n.
+__device__ __forceinline__ int nth_bit(uint32_t w, int n) {
+  int at = 0;
+#pragma unroll
+  for (int width = 16; width; width >>= 1) {
+    const int c = __popc(w & ((1u << width) - 1u));
+    if (n >= c) {
+      n -= c;
+      w >>= width;
+      at += width;
+    }
+  }
+  return at;
+}
+
+// One CTA of NT threads, or (C > 1) a cluster of C.
+template <int NT, int C>
+__global__ void __launch_bounds__(NT) grow_tables_kernel(const GrowParams p) {
   extern __shared__ int32_t rows[];
   int32_t *off = rows;                 // [B + 1] blocks taken by the rows before
-  int32_t *starts = rows + p.B + 1;    // [B + 1] tokens of the rows before
-  int32_t *col = starts + p.B + 1;     // [B] the first table entry that changes
-  __shared__ long long sums[kGrowWarps];
-  __shared__ int isums[kGrowWarps];
-  const int tid = threadIdx.x, words = (p.NB - 1) / 32 + 1;
+  int32_t *starts = off + p.B + 1;     // [B + 1] tokens of the rows before
+  int32_t *lens = starts + p.B + 1;    // [B] the length, its top bit: last block copied
+  int32_t *lasts = lens + p.B;         // [B] the last block (C = 1 and keep_lasts)
+  __shared__ int sums[3][32];
+  __shared__ int counts[C];            // free blocks of every CTA's share
+  __shared__ int ids[C == 1 ? kIds : 1];
+  __shared__ int upto[NT];             // a chunk of the pool: free blocks up to
+  __shared__ __align__(16) uint32_t chunk[NT][kWords];  // and with a thread's words
+  const int tid = threadIdx.x;
+  const int rank = C > 1 ? (int)blockIdx.x : 0;
+  const bool first = rank == 0;
+  const int words = (p.NB - 1) / 32 + 1;
+  const int row_per = (p.B + NT - 1) / NT;  // rows a thread, side by side
   pdl_wait();
   pdl_launch_dependents();
 
-  int mine = 0;
-  for (int w = tid; w < words; w += kGrowThreads) mine += __popc(free_word(p, w));
-
-  // What every row needs.
-  long long blocks = 0, tokens = 0;
-  for (int b0 = 0; b0 < p.B; b0 += kGrowThreads) {
-    const int b = b0 + tid;
-    int need = 0, add = 0, at = 0, src = -1, len = 0;
-    if (b < p.B) {
-      len = p.ctx[b];
-      add = p.new_tokens[b];
-      if (len < 0 || add < 0 || (long long)len + add > (long long)p.MB * p.bs) {
-        atomicOr(p.err, PGD_DEVERR_BAD_CONTEXT);
-        add = 0;
-      }
-      if (add > 0) {
-        at = (int)(((long long)len + p.bs - 1) / p.bs);
-        need = (int)(((long long)len + add + p.bs - 1) / p.bs) - at;
-        if (len % p.bs) {
-          const int last = p.tables[(size_t)b * p.MB + at - 1];
-          if ((unsigned)last >= (unsigned)p.NB) {
-            atomicOr(p.err, PGD_DEVERR_BAD_BLOCK_ID);
-            need = add = 0;
-          } else if (p.refs[last] > 1) {
-            src = last;
-            --at;
-            ++need;
-          }
+  int x[3] = {0, 0, 0};  // blocks needed, tokens, free blocks
+  uint32_t bits[kWords];  // of a chunk of the pool
+  if (C == 1) {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+      const int w = tid * kWords + i;
+      bits[i] = w < words ? free_word(p, w) : 0u;
+      x[2] += __popc(bits[i]);
+    }
+    for (int w = NT * kWords + tid; w < words; w += NT) x[2] += __popc(free_word(p, w));
+  } else {
+    for (int w = rank * NT + tid; w < words; w += C * NT)
+      x[2] = capped(x[2], __popc(free_word(p, w)));
+  }
+  const int b0 = tid * row_per;
+  for (int b = b0; b < min(p.B, b0 + row_per); ++b) {
+    int need = 0, src = -1, last = -1;
+    const int len = p.ctx[b];
+    int add = p.new_tokens[b];
+    if (len < 0 || add < 0 || (long long)len + add > (long long)p.MB * p.bs) {
+      if (first) atomicOr(p.err, PGD_DEVERR_BAD_CONTEXT);
+      add = 0;
+    }
+    if (add > 0) {
+      const int at = (int)(((long long)len + p.bs - 1) / p.bs);
+      need = (int)(((long long)len + add + p.bs - 1) / p.bs) - at;
+      if (len % p.bs) {
+        last = p.tables[(size_t)b * p.MB + at - 1];
+        if ((unsigned)last >= (unsigned)p.NB) {
+          if (first) atomicOr(p.err, PGD_DEVERR_BAD_BLOCK_ID);
+          need = add = 0;
+        } else if (p.refs[last] > 1) {
+          src = last;
+          ++need;
         }
       }
     }
-    long long n, m;
-    const long long e = block_scan<long long>(need, sums, n);
-    const long long f = block_scan<long long>(add, sums, m);
-    if (b < p.B) {
-      // (beyond int32 only where the call is refused below)
-      off[b] = (int)(blocks + e - need);
-      starts[b] = (int)(tokens + f - add);
-      col[b] = at;
+    off[b] = need;
+    starts[b] = add;
+    lens[b] = len & 0x7fffffff;
+    if (src >= 0) lens[b] |= (int)0x80000000;
+    if (p.keep_lasts) lasts[b] = last;
+    if (first) {
       p.positions[b] = len;
       p.copy_src[b] = src;
       p.copy_dst[b] = -1;
     }
-    blocks += n;
-    tokens += m;
+    x[0] = capped(x[0], need);
+    x[1] = capped(x[1], min(add, kMost));
   }
-  int free_blocks;
-  block_scan<int>(mine, isums, free_blocks);
-  const bool fits = tokens <= p.N, done = fits && blocks <= free_blocks;
-  if (tid == 0) {
+  const int mine[3] = {x[0], x[1], x[2]};
+  int total[3];
+  block_scan<NT, 3>(x, sums, total);
+  int free_blocks = total[2];
+  if constexpr (C > 1) {
+    // every CTA learns what the others counted; none changes anything before
+    cg::cluster_group cluster = cg::this_cluster();
+    if (tid < C) *cluster.map_shared_rank(counts + rank, tid) = total[2];
+    cluster.sync();
+    free_blocks = 0;
+#pragma unroll
+    for (int i = 0; i < C; ++i) free_blocks = capped(free_blocks, counts[i]);
+  }
+  const int need = total[0], tokens = total[1];
+  const bool fits = tokens <= p.N, done = fits && need <= free_blocks;
+  if (first && tid == 0) {
     p.result[0] = done ? 0 : fits ? 1 : 2;
-    p.result[1] = done ? (int)blocks : 0;
-    p.result[2] = done || !fits ? 0 : (int)min(blocks - free_blocks, 0x7fffffffLL);
-    p.result[3] = done ? (int)tokens : 0;
+    p.result[1] = done ? need : 0;
+    p.result[2] = done || !fits ? 0 : need - free_blocks;
+    p.result[3] = done ? tokens : 0;
   }
   if (!done) {
+    if (!first) return;
     if (tid == 0 && !fits) atomicOr(p.err, PGD_DEVERR_BAD_POSITION);
-    for (int b = tid; b <= p.B; b += kGrowThreads) {
+    __syncthreads();
+    for (int b = tid; b <= p.B; b += NT) {
       p.starts[b] = 0;
       if (b < p.B) p.copy_src[b] = -1;
     }
-    if (p.N <= kInlineTokens)
-      for (int n = tid; n < p.N; n += kGrowThreads) {
+    if (C == 1)
+      for (int n = tid; n < p.N; n += NT) {
         p.slots[n] = -1;
         p.token_positions[n] = 0;
       }
     return;
   }
-  const int need = (int)blocks, total = (int)tokens;
-  if (tid == 0) {
-    off[p.B] = need;
-    starts[p.B] = total;
-  }
-  __syncthreads();
-
-  // The lowest free ids, in the order of the rows.
-  int before = 0;
-  for (int w0 = 0; before < need; w0 += kGrowThreads) {
-    const int w = w0 + tid;
-    const uint32_t bits = w < words ? free_word(p, w) : 0u;
-    int n;
-    int i = before + block_scan<int>(__popc(bits), isums, n) - __popc(bits);
-    before += n;
-    if (bits && i < need) {
-      int b = row_of_token(off, p.B, i);
-      uint32_t left = bits;
-      while (left && i < need) {
-        while (off[b + 1] <= i) ++b;
-        const int id = w * 32 + __ffs(left) - 1;
-        left &= left - 1;
-        const int k = i - off[b];
-        p.tables[(size_t)b * p.MB + col[b] + k] = id;
-        p.refs[id] = 1;
-        if (k == 0 && p.copy_src[b] >= 0) p.copy_dst[b] = id;
-        ++i;
-      }
-      p.free_bits[w] = left;
+  {  // counts to sums of the rows before
+    int o = x[0] - mine[0], t = x[1] - mine[1];
+    for (int b = b0; b < min(p.B, b0 + row_per); ++b) {
+      const int n = off[b], m = starts[b];
+      off[b] = o;
+      starts[b] = t;
+      o += n;
+      t += m;
+    }
+    if (tid == 0) {
+      off[p.B] = need;
+      starts[p.B] = tokens;
     }
   }
   __syncthreads();
-  for (int b = tid; b <= p.B; b += kGrowThreads) {
+
+  // The lowest free ids, in the order of the rows, by chunks of the pool that
+  // every CTA sums for itself: the i-th free block of a chunk is found by
+  // bisection, so that neighbouring threads write neighbouring entries and the
+  // CTAs take equal shares wherever in the pool the free blocks lie.
+  int before = 0;
+  for (int c0 = 0; c0 < words && before < need; c0 += NT * kWords) {
+    int n[1] = {0}, all[1] = {total[2]};
+    if (C > 1 || c0 > 0)
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) {
+        const int w = c0 + tid * kWords + i;
+        bits[i] = w < words ? free_word(p, w) : 0u;
+      }
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) n[0] += __popc(bits[i]);
+    const int had = n[0];
+    if (C > 1 || words > NT * kWords) {
+      __syncthreads();  // (the last chunk is done with)
+      block_scan<NT, 1>(n, sums, all);
+    } else {
+      n[0] = x[2];  // the one chunk there is: summed above
+    }
+    upto[tid] = n[0];
+    *reinterpret_cast<uint4 *>(chunk[tid]) = make_uint4(bits[0], bits[1], bits[2], bits[3]);
+    if constexpr (C > 1)
+      cg::this_cluster().sync();  // every CTA has read the chunk's bits
+    else
+      __syncthreads();
+    for (int k = rank * NT + tid; k < min(all[0], need - before); k += C * NT) {
+      int lo = 0, hi = NT - 1;  // the first thread with upto > k
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (upto[mid] > k) hi = mid; else lo = mid + 1;
+      }
+      int left = k - (lo ? upto[lo - 1] : 0), word = 0;
+#pragma unroll
+      for (int i = 0; i < kWords - 1; ++i) {
+        const int m = __popc(chunk[lo][i]);
+        if (word == i && left >= m) {
+          left -= m;
+          ++word;
+        }
+      }
+      const int id = (c0 + lo * kWords + word) * 32 + nth_bit(chunk[lo][word], left);
+      const int i = before + k, b = row_of(off, p.B, i), at = i - off[b];
+      const int len = lens[b] & 0x7fffffff;
+      const bool copied = lens[b] < 0;
+      const int col = (int)(((long long)len + p.bs - 1) / p.bs) - (copied ? 1 : 0);
+      p.tables[(size_t)b * p.MB + col + at] = id;
+      p.refs[id] = 1;
+      if (C == 1 && i < kIds) ids[i] = id;
+      if (at == 0 && copied) p.copy_dst[b] = id;
+    }
+    // the bits of what was taken: the lowest of this thread's
+    int taken = min(had, need - before - (n[0] - had));
+    if (taken > 0 && tid % C == rank)
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) {
+        const int m = __popc(bits[i]), t = min(m, taken);
+        if (t <= 0) continue;
+        taken -= t;
+        const uint32_t kept = t == m ? 0u : bits[i] & ~((1u << nth_bit(bits[i], t)) - 1u);
+        p.free_bits[c0 + tid * kWords + i] = kept;
+      }
+    before += all[0];
+  }
+  if constexpr (C > 1) {
+    cg::this_cluster().sync();
+    if (!first) return;
+  } else {
+    __syncthreads();
+  }
+  for (int b = tid; b <= p.B; b += NT) {
     p.starts[b] = starts[b];
     if (b == p.B) break;
-    p.ctx[b] = p.positions[b] + (starts[b + 1] - starts[b]);
-    const int src = p.copy_src[b];
-    if (src >= 0 && atomicSub(p.refs + src, 1) == 1)
-      atomicOr(p.free_bits + (src >> 5), 1u << (src & 31));
+    if (starts[b + 1] > starts[b])
+      p.ctx[b] = (lens[b] & 0x7fffffff) + (starts[b + 1] - starts[b]);
+    if (lens[b] < 0) {
+      const int src = p.copy_src[b];
+      if (src >= 0 && atomicSub(p.refs + src, 1) == 1)
+        atomicOr(p.free_bits + (src >> 5), 1u << (src & 31));
+    }
   }
-  if (p.N <= kInlineTokens)
-    for (int n = tid; n < p.N; n += kGrowThreads) place_token(p, starts, n, total);
+  if constexpr (C == 1)
+    for (int n = tid; n < p.N; n += NT) {
+      long long slot = -1;
+      int pos = 0;
+      if (n < tokens) {
+        const int b = row_of(starts, p.B, n), len = lens[b] & 0x7fffffff;
+        const int col = (int)(((long long)len + p.bs - 1) / p.bs) - (lens[b] < 0 ? 1 : 0);
+        pos = len + (n - starts[b]);
+        const int j = pos / p.bs, i = off[b] + j - col;
+        int id;
+        if (j >= col && i < kIds)
+          id = ids[i];
+        else if (j < col && p.keep_lasts)
+          id = lasts[b];
+        else
+          id = p.tables[(size_t)b * p.MB + j];
+        slot = (long long)id * p.bs + (pos - j * p.bs);
+      }
+      p.slots[n] = slot;
+      p.token_positions[n] = pos;
+    }
 }
 
+// Slots of many tokens: a warp takes 32 times kRun in a row and finds the first
+// one's row of the table; the others walk on from there.
+constexpr int kRun = 4;
 __global__ void __launch_bounds__(kSlotThreads) place_tokens_kernel(const GrowParams p) {
   pdl_wait();
   pdl_launch_dependents();
-  const int n = blockIdx.x * kSlotThreads + threadIdx.x;
-  if (n < p.N) place_token(p, p.starts, n, p.result[3]);
+  const int n0 = (blockIdx.x * (kSlotThreads / 32) + (threadIdx.x >> 5)) * 32 * kRun;
+  if (n0 >= p.N) return;
+  const int total = p.result[3];
+  int b = n0 < total ? row_of(p.starts, p.B, n0) : 0;
+  int j[kRun], at[kRun], entry[kRun];
+#pragma unroll
+  for (int i = 0; i < kRun; ++i) {
+    const int n = n0 + 32 * i + (threadIdx.x & 31);
+    j[i] = -1;
+    at[i] = 0;
+    if (n < total) {
+      while (p.starts[b + 1] <= n) ++b;
+      at[i] = p.positions[b] + (n - p.starts[b]);
+      j[i] = at[i] / p.bs;
+      entry[i] = p.tables[(size_t)b * p.MB + j[i]];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kRun; ++i) {
+    const int n = n0 + 32 * i + (threadIdx.x & 31);
+    if (n >= p.N) break;
+    p.slots[n] = j[i] < 0 ? -1 : (long long)entry[i] * p.bs + (at[i] - j[i] * p.bs);
+    p.token_positions[n] = at[i];
+  }
 }
 
 __global__ void __launch_bounds__(128) trim_tables_kernel(const TrimParams p) {
   pdl_wait();
   pdl_launch_dependents();
-  const int b = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (b >= p.B) return;
+  const int b = blockIdx.x;
   const int len = p.ctx[b], keep = __ldg(p.keep + b);
   if (len < 0 || (long long)len > (long long)p.MB * p.bs || keep < 0) {
-    if (lane == 0) atomicOr(p.err, PGD_DEVERR_BAD_CONTEXT);
+    if (threadIdx.x == 0) atomicOr(p.err, PGD_DEVERR_BAD_CONTEXT);
     return;
   }
   if (keep >= len) return;
   int32_t *row = p.tables + (size_t)b * p.MB;
   const int j1 = (int)(((long long)len + p.bs - 1) / p.bs);
-  for (int j = (int)(((long long)keep + p.bs - 1) / p.bs) + lane; j < j1; j += 32) {
+  for (int j = (int)(((long long)keep + p.bs - 1) / p.bs) + threadIdx.x; j < j1; j += 128) {
     const int id = row[j];
     row[j] = -1;
     if ((unsigned)id >= (unsigned)p.NB) {
@@ -242,46 +389,53 @@ __global__ void __launch_bounds__(128) trim_tables_kernel(const TrimParams p) {
       atomicOr(p.err, PGD_DEVERR_BAD_BLOCK_ID);
     }
   }
-  __syncwarp();
-  if (lane == 0) p.ctx[b] = keep;
+  __syncthreads();  // every thread has read the length
+  if (threadIdx.x == 0) p.ctx[b] = keep;
 }
 
 template <typename... P, typename... A>
-cudaError_t launch(void (*kernel)(P...), int grid, int threads, size_t smem, cudaStream_t stream,
-                   A... args) {
+cudaError_t launch(void (*kernel)(P...), int grid, int threads, size_t smem, int cluster,
+                   cudaStream_t stream, A... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 }  // namespace
 
-cudaError_t grow_tables_launch(const GrowParams &p, cudaStream_t stream) {
-  const size_t smem = ((size_t)p.B * 3 + 2) * sizeof(int32_t);
-  if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(
-        grow_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-        (int)(((size_t)kMaxGrowRows * 3 + 2) * sizeof(int32_t)));
+cudaError_t grow_tables_launch(const GrowParams &p_in, cudaStream_t stream) {
+  GrowParams p = p_in;
+  const bool one = p.N <= kInlineTokens && p.NB <= kInlineBlocks;
+  p.keep_lasts = one && p.B <= 8192 ? 1 : 0;
+  const size_t smem = ((size_t)p.B * (p.keep_lasts ? 4 : 3) + 2) * sizeof(int32_t);
+  auto kernel = one ? grow_tables_kernel<512, 1> : grow_tables_kernel<1024, kCluster>;
+  if (smem > 16 * 1024) {  // (more than 48 KB with the static part)
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)(((size_t)kMaxGrowRows * 3 + 2) * sizeof(int32_t)));
     if (e != cudaSuccess) return e;
   }
-  cudaError_t e = launch(grow_tables_kernel, 1, kGrowThreads, smem, stream, p);
-  if (e == cudaSuccess && p.N > kInlineTokens)
-    e = launch(place_tokens_kernel, (int)(((long long)p.N + kSlotThreads - 1) / kSlotThreads),
-               kSlotThreads, 0, stream, p);
-  return e;
+  if (one) return launch(kernel, 1, 512, smem, 1, stream, p);
+  const cudaError_t e = launch(kernel, kCluster, 1024, smem, kCluster, stream, p);
+  if (e != cudaSuccess || p.N == 0) return e;
+  return launch(place_tokens_kernel, (int)(((long long)p.N + kSlotThreads * kRun - 1) / (kSlotThreads * kRun)), kSlotThreads,
+                0, 1, stream, p);
 }
 
 cudaError_t trim_tables_launch(const TrimParams &p, cudaStream_t stream) {
   if (p.B == 0) return cudaSuccess;
-  return launch(trim_tables_kernel, (p.B + 3) / 4, 128, 0, stream, p);
+  return launch(trim_tables_kernel, p.B, 128, 0, 1, stream, p);
 }
 
 }  // namespace pgd

@@ -19,6 +19,7 @@ struct GrowParams {
   int32_t *copy_src, *copy_dst;  // [B]
   int32_t *result;               // [4]
   int B, N, bs, MB, NB;
+  int keep_lasts;                // the launch's: room for the rows' last blocks
   int32_t *err;
 };
 constexpr int kMaxGrowRows = 16384;  // three int32 a row in shared memory

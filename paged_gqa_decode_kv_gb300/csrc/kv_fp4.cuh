@@ -88,10 +88,11 @@ cudaError_t kv_read_fp4_launch(const Kv4Params &p, cudaStream_t stream);
 struct Attn4Params {
   AttnParams a;
   float v_scale;
-  int steps_per_cta;  // an automatic split gives no CTA fewer steps than this
+  int splits;       // parts of a unit, or 0: automatic,
+  int resident;     // ... for this many CTAs at once
 };
-int attention_fp4_grid(long long units, int sms);
-cudaError_t attention_fp4_launch(const Attn4Params &p, int G, int bs, int grid,
+long long attention_fp4_grid(long long units, long long tokens, int sms);
+cudaError_t attention_fp4_launch(const Attn4Params &p, int G, int bs, int grid, int sms,
                                  cudaStream_t stream);
 
 }  // namespace pgd
