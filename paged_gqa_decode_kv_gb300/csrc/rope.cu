@@ -9,15 +9,19 @@
 // Angles.  In fp32 position * f loses the place in the circle as positions
 // grow (2^-24 of 10^6 radians is 0.06).  Frequencies come as 64-bit fractions
 // of a turn, so that position * f wraps modulo 2^64 to the fraction itself:
-// one integer product, exact, for any int32 position.  Its upper 32 bits go to
-// sincospi.
+// one integer product, exact, for any int32 position.  What is left is within
+// half a turn, where the fast sine and cosine are off by 2^-21: 2^12 times less
+// than the rounding to bf16 that follows.
 //
-// Bound by memory: every row read and written once.  A CTA takes 1 or 4 tokens;
-// its threads find one (token, pair) angle each, and then stay with 16 dims of
-// a head (8 pairs, whose cosines and sines they load once) for every head in
-// turn, two 16-byte vectors a head, four heads' loads in flight.
+// Bound by memory: every row read and written once.  A thread takes 16 dims (8
+// pairs) of one token, finds their cosines and sines itself and stays with them
+// for head after head, two 16-byte vectors a head, four heads' loads in flight:
+// no barrier, and nothing shared.  Few tokens' heads are spread over several
+// threads.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+
+#include <algorithm>
 
 #include "rope.cuh"
 
@@ -27,189 +31,172 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kInFlight = 4;  // heads
 
-// A head's row of one token: where from, where to (16-byte vectors).
-struct Row {
-  const uint4 *src;
-  uint4 *dst;
-  int step;  // vectors between the row's 16-byte vectors at dst (8 in a tile)
-  bool rotated, there;
-};
-
-template <bool APPEND>
-__device__ __forceinline__ Row row_of(const RopeParams &p, int t, int head, long long slot) {
-  Row r;
-  r.step = 1;
-  r.there = true;
-  r.rotated = true;
-  if (head < p.n_q) {
-    r.src = reinterpret_cast<const uint4 *>(p.q + t * p.q_row + head * p.q_head);
-    r.dst = reinterpret_cast<uint4 *>(p.q_out + t * p.qo_row + head * p.qo_head);
-    return r;
-  }
-  int g = head - p.n_q;
-  const bool is_v = g >= p.n_kv;
-  if (!APPEND) {
-    r.there = !is_v;
-    r.src = reinterpret_cast<const uint4 *>(p.k + t * p.k_row + g * p.k_head);
-    r.dst = reinterpret_cast<uint4 *>(p.k_out + t * p.ko_row + g * p.ko_head);
-    return r;
-  }
-  if (is_v) g -= p.n_kv;
-  r.there = g < p.n_kv;
-  r.rotated = !is_v;
-  r.src = is_v ? reinterpret_cast<const uint4 *>(p.v + t * p.v_row + g * p.v_head)
-               : reinterpret_cast<const uint4 *>(p.k + t * p.k_row + g * p.k_head);
-  // 16-byte vector v of slot s: core matrix (s / 8, v), row s % 8
-  const long long blk = slot / p.bs;
-  const int s = (int)(slot % p.bs);
-  r.dst = reinterpret_cast<uint4 *>(is_v ? p.v_cache : p.k_cache) +
-          (blk * p.n_kv + g) * (long long)(p.bs * 16) + (s >> 3) * 128 + (s & 7);
-  r.step = 8;
-  return r;
-}
-
 __device__ __forceinline__ uint32_t pack(float a, float b) {
   const __nv_bfloat162 z = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t *>(&z);
 }
 
-// TT tokens a CTA; blockDim (columns of 16 dims, heads at a time).
-template <bool APPEND, int TT>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
-  extern __shared__ __align__(16) float2 turn[];  // [TT][rotary / 2] (cos, sin)
-  pdl_wait();
-  pdl_launch_dependents();
-  const int tid = threadIdx.y * blockDim.x + threadIdx.x, n = blockDim.x * blockDim.y;
-  const int pairs = p.rotary >> 1, t0 = blockIdx.x * TT;
-  for (int i = tid; i < TT * pairs; i += n) {
-    const int t = t0 + i / pairs, f = i % pairs;
-    if (t < p.T) {
-      const uint64_t part = (uint64_t)(int64_t)__ldg(p.positions + t) *
-                            (uint64_t)__ldg(p.freq + f);
-      const float half_turns = (float)(int32_t)(uint32_t)(part >> 32) * 0x1p-31f;
-      float s, c;
-      sincospif(half_turns, &s, &c);
-      turn[i] = make_float2(c * p.factor, s * p.factor);
+// Cosines and sines of a thread's pairs; where its vectors lie in a row.
+struct Pairs {
+  float c[8], s[8];
+  int v0, v1;
+  bool rotary;
+};
+
+template <bool INTERLEAVED>
+__device__ __forceinline__ void turn(const Pairs &r, uint4 &a, uint4 &b) {
+  float y[8], z[8];
+  unpack8(a, y);
+  unpack8(b, z);
+  if (INTERLEAVED) {
+#pragma unroll
+    for (int k = 0; k < 8; k += 2) {
+      const float u = y[k], w = y[k + 1], e = z[k], f = z[k + 1];
+      y[k] = u * r.c[k / 2] - w * r.s[k / 2];
+      y[k + 1] = w * r.c[k / 2] + u * r.s[k / 2];
+      z[k] = e * r.c[4 + k / 2] - f * r.s[4 + k / 2];
+      z[k + 1] = f * r.c[4 + k / 2] + e * r.s[4 + k / 2];
     }
-  }
-  __syncthreads();
-  // This thread's 16 dims: column x of the rotary part, or of what is copied.
-  const int cols = p.rotary >> 4, x = threadIdx.x;
-  const bool rotary = x < cols;
-  int v0, v1;  // its two vectors of a row
-  if (rotary) {
-    v0 = (p.first >> 3) + (p.interleaved ? 2 * x : x);
-    v1 = (p.first >> 3) + (p.interleaved ? 2 * x + 1 : x + cols);
   } else {
-    // the vectors outside the rotary part, two at a time
-    const int i = 2 * (x - cols), lead = p.first >> 3;
-    v0 = i < lead ? i : i + 2 * cols;
-    v1 = i + 1 < lead ? i + 1 : i + 1 + 2 * cols;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float u = y[k], w = z[k];
+      y[k] = u * r.c[k] - w * r.s[k];
+      z[k] = w * r.c[k] + u * r.s[k];
+    }
   }
-  const int heads = p.n_q + (APPEND ? 2 : 1) * p.n_kv;
+  a = make_uint4(pack(y[0], y[1]), pack(y[2], y[3]), pack(y[4], y[5]), pack(y[6], y[7]));
+  b = make_uint4(pack(z[0], z[1]), pack(z[2], z[3]), pack(z[4], z[5]), pack(z[6], z[7]));
+}
+
+// n heads' rows from src to dst (16-byte vectors; `from` and `to` between
+// heads, `step` between a row's vectors at dst).
+template <bool INTERLEAVED>
+__device__ __forceinline__ void rows(const Pairs &r, bool rotated, const uint4 *src, long long from,
+                                     uint4 *dst, long long to, int step, int n) {
+  if (!r.rotary && src == dst && from == to) return;  // in place: there already
+  const int w0 = r.v0 * step, w1 = r.v1 * step;
 #pragma unroll 1
-  for (int j = 0; j < TT; ++j) {
-    const int t = t0 + j;
-    if (t >= p.T) break;
-    long long slot = 0;
-    if (APPEND) {
-      slot = __ldg(p.slots + t);
-      if (slot < 0) continue;
-      if (slot >= (long long)p.NB * p.bs) {
-        if (tid == 0) atomicOr(p.err, PGD_DEVERR_BAD_POSITION);
-        continue;
-      }
-    }
-    float c[8], s[8];
-    if (rotary) {
-      const float4 *at = reinterpret_cast<const float4 *>(turn + j * pairs + 8 * x);
+  for (int h = 0; h < n; h += kInFlight) {
+    uint4 a[kInFlight], b[kInFlight];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float4 y = at[i];
-        c[2 * i] = y.x;
-        s[2 * i] = y.y;
-        c[2 * i + 1] = y.z;
-        s[2 * i + 1] = y.w;
-      }
-    }
-#pragma unroll 1
-    for (int h0 = threadIdx.y; h0 < heads; h0 += kInFlight * blockDim.y) {
-      uint4 a[kInFlight], b[kInFlight];
-      Row r[kInFlight];
-#pragma unroll
-      for (int i = 0; i < kInFlight; ++i) {
-        const int h = h0 + i * blockDim.y;
-        r[i] = row_of<APPEND>(p, t, h, slot);
-        if (h >= heads) r[i].there = false;
-        // (in place, what is not rotated is there already)
-        if (!rotary && r[i].src == r[i].dst) r[i].there = false;
-        if (r[i].there) {
-          a[i] = r[i].src[v0];
-          b[i] = r[i].src[v1];
-        }
+    for (int i = 0; i < kInFlight; ++i)
+      if (h + i < n) {
+        a[i] = __ldcs(src + i * from + r.v0);
+        b[i] = __ldcs(src + i * from + r.v1);
       }
 #pragma unroll
-      for (int i = 0; i < kInFlight; ++i) {
-        if (!r[i].there) continue;
-        if (rotary && r[i].rotated) {
-          float y[8], z[8];
-          unpack8(a[i], y);
-          unpack8(b[i], z);
-          if (p.interleaved) {
-#pragma unroll
-            for (int k = 0; k < 8; k += 2) {
-              const float u = y[k], w = y[k + 1], e = z[k], f = z[k + 1];
-              y[k] = u * c[k / 2] - w * s[k / 2];
-              y[k + 1] = w * c[k / 2] + u * s[k / 2];
-              z[k] = e * c[4 + k / 2] - f * s[4 + k / 2];
-              z[k + 1] = f * c[4 + k / 2] + e * s[4 + k / 2];
-            }
-          } else {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const float u = y[k], w = z[k];
-              y[k] = u * c[k] - w * s[k];
-              z[k] = w * c[k] + u * s[k];
-            }
-          }
-          a[i] = make_uint4(pack(y[0], y[1]), pack(y[2], y[3]), pack(y[4], y[5]),
-                            pack(y[6], y[7]));
-          b[i] = make_uint4(pack(z[0], z[1]), pack(z[2], z[3]), pack(z[4], z[5]),
-                            pack(z[6], z[7]));
-        }
-        r[i].dst[v0 * r[i].step] = a[i];
-        r[i].dst[v1 * r[i].step] = b[i];
+    for (int i = 0; i < kInFlight; ++i)
+      if (h + i < n) {
+        if (r.rotary && rotated) turn<INTERLEAVED>(r, a[i], b[i]);
+        dst[i * to + w0] = a[i];
+        dst[i * to + w1] = b[i];
       }
-    }
+    src += kInFlight * from;
+    dst += kInFlight * to;
   }
 }
 
-template <bool APPEND, int TT>
+// Threads (columns of 16 dims, tokens); blockIdx.y: `share` heads of a token's.
+template <bool APPEND, bool INTERLEAVED>
+__global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p, int share) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const long long t = (long long)blockIdx.x * blockDim.y + threadIdx.y;
+  if (t >= p.T) return;
+  long long slot = 0;
+  if (APPEND) {
+    slot = __ldg(p.slots + t);
+    if (slot < 0) return;
+    if (slot >= (long long)p.NB * p.bs) {
+      if (threadIdx.x == 0 && blockIdx.y == 0) atomicOr(p.err, PGD_DEVERR_BAD_POSITION);
+      return;
+    }
+  }
+  const int cols = p.rotary >> 4, x = threadIdx.x, lead = p.first >> 3;
+  Pairs r;
+  r.rotary = x < cols;
+  if (r.rotary) {
+    r.v0 = lead + (INTERLEAVED ? 2 * x : x);
+    r.v1 = lead + (INTERLEAVED ? 2 * x + 1 : x + cols);
+    const uint64_t pos = (uint64_t)(int64_t)__ldg(p.positions + t);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint64_t part = pos * (uint64_t)__ldg(p.freq + 8 * x + i);
+      const float half_turns = (float)(int32_t)(uint32_t)(part >> 32) * 0x1p-31f;
+      float s, c;
+      __sincosf(half_turns * 3.14159265358979f, &s, &c);
+      r.c[i] = c * p.factor;
+      r.s[i] = s * p.factor;
+    }
+  } else {
+    // the vectors outside the rotary part, two at a time
+    const int i = 2 * (x - cols);
+    r.v0 = i < lead ? i : i + 2 * cols;
+    r.v1 = i + 1 < lead ? i + 1 : i + 1 + 2 * cols;
+  }
+  // heads [h0, h1) of q's, then k's, then (appended) v's
+  const int h0 = blockIdx.y * share;
+  const int h1 = min(h0 + share, p.n_q + (APPEND ? 2 : 1) * p.n_kv);
+  if (h0 < p.n_q)
+    rows<INTERLEAVED>(r, true, reinterpret_cast<const uint4 *>(p.q + t * p.q_row + h0 * p.q_head),
+                      p.q_head >> 3,
+                      reinterpret_cast<uint4 *>(p.q_out + t * p.qo_row + h0 * p.qo_head),
+                      p.qo_head >> 3, 1, min(h1, p.n_q) - h0);
+  const int k0 = max(h0 - p.n_q, 0), k1 = min(h1 - p.n_q, p.n_kv);
+  if (!APPEND) {
+    if (k0 < k1)
+      rows<INTERLEAVED>(r, true, reinterpret_cast<const uint4 *>(p.k + t * p.k_row + k0 * p.k_head),
+                        p.k_head >> 3,
+                        reinterpret_cast<uint4 *>(p.k_out + t * p.ko_row + k0 * p.ko_head),
+                        p.ko_head >> 3, 1, k1 - k0);
+    return;
+  }
+  // 16-byte vector v of slot s of a tile: core matrix (s / 8, v), row s % 8
+  const long long blk = slot / p.bs;
+  const int s = (int)(slot - blk * p.bs);
+  const long long tile = p.bs * 16LL, at = (s >> 3) * 128 + (s & 7);
+  if (k0 < k1)
+    rows<INTERLEAVED>(r, true, reinterpret_cast<const uint4 *>(p.k + t * p.k_row + k0 * p.k_head),
+                      p.k_head >> 3,
+                      reinterpret_cast<uint4 *>(p.k_cache) + (blk * p.n_kv + k0) * tile + at, tile,
+                      8, k1 - k0);
+  const int v0 = max(h0 - p.n_q - p.n_kv, 0), v1 = h1 - p.n_q - p.n_kv;
+  if (v0 < v1)
+    rows<INTERLEAVED>(r, false, reinterpret_cast<const uint4 *>(p.v + t * p.v_row + v0 * p.v_head),
+                      p.v_head >> 3,
+                      reinterpret_cast<uint4 *>(p.v_cache) + (blk * p.n_kv + v0) * tile + at, tile,
+                      8, v1 - v0);
+}
+
+template <bool APPEND, bool INTERLEAVED>
 cudaError_t launch(const RopeParams &p, cudaStream_t stream) {
-  const int cols = p.d >> 4;
-  const int heads = p.n_q + (APPEND ? 2 : 1) * p.n_kv;
-  int y = kThreads / cols;
-  if (y > heads) y = heads;
+  const int cols = p.d >> 4, heads = p.n_q + (APPEND ? 2 : 1) * p.n_kv;
+  const int y = std::max(1, std::min(kThreads / cols, p.T));
+  const long long tiles = ((long long)p.T + y - 1) / y;
+  // every token's heads in one thread a column where that fills the GPU (about
+  // 1000 threads an SM), else in shares of kInFlight heads and more
+  const long long want = std::max(1LL, 152LL * 1024 / (tiles * y * cols));
+  const int share = (int)std::max<long long>(kInFlight, (heads + want - 1) / want);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((p.T + TT - 1) / TT));
+  cfg.gridDim = dim3((unsigned)tiles, (unsigned)((heads + share - 1) / share));
   cfg.blockDim = dim3((unsigned)cols, (unsigned)y);
-  cfg.dynamicSmemBytes = (size_t)TT * (p.rotary >> 1) * sizeof(float2);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, rope_kernel<APPEND, TT>, p);
+  return cudaLaunchKernelEx(&cfg, rope_kernel<APPEND, INTERLEAVED>, p, share);
 }
 
 }  // namespace
 
 cudaError_t rope_launch(const RopeParams &p, cudaStream_t stream) {
   if (p.T == 0) return cudaSuccess;
-  const bool many = p.T > 1024;
-  if (p.k_cache) return many ? launch<true, 4>(p, stream) : launch<true, 1>(p, stream);
-  return many ? launch<false, 4>(p, stream) : launch<false, 1>(p, stream);
+  if (p.k_cache)
+    return p.interleaved ? launch<true, true>(p, stream) : launch<true, false>(p, stream);
+  return p.interleaved ? launch<false, true>(p, stream) : launch<false, false>(p, stream);
 }
 
 }  // namespace pgd

@@ -173,9 +173,10 @@ def turned(x, positions, freq, first, interleaved, factor):
     """Rows [T][heads][d] (64 bits) with rotary dims turned, and the bound of a bf16 result's error.
 
     freq: the 2^-64 turns of every pair, taken modulo a turn in whole numbers.  The kernel's fraction
-    of a turn is cut to 32 bits and rounded to fp32's 24 (2^-26 of a turn: 2^-23 radians), its sine and
-    cosine are off by 2^-22, and three roundings of 2^-24 follow, so each of the two products by at
-    most 2^-20 of |x| factor; then bf16: 2^-8 of the result."""
+    of a turn is cut to 32 bits and rounded to fp32's 24, as is its angle (2^-22 radians), its sine
+    and cosine are off by 2^-21.2, and three roundings of 2^-24 follow, so each of the two products by
+    at most 2^-20 of |x| factor (2^-22 + 2^-21.2 + 3 * 2^-24 < 2^-20); then bf16: 2^-8 of the
+    result."""
     half = len(freq)
     turn = np.array([[((int(p) * int(f)) % (1 << 64)) / 2.0 ** 64 for f in freq]
                      for p in positions]).reshape(len(positions), half)
