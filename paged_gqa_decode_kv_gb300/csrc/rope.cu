@@ -28,7 +28,7 @@
 namespace pgd {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kInFlight = 4;  // heads
 
 __device__ __forceinline__ uint32_t pack(float a, float b) {
@@ -40,8 +40,22 @@ __device__ __forceinline__ uint32_t pack(float a, float b) {
 struct Pairs {
   float c[8], s[8];
   int v0, v1;
-  bool rotary;
+  bool rotary, known;  // known: c and s are found
 };
+
+// The angles of pairs 8 x .. 8 x + 7 of a token.
+__device__ __forceinline__ void find_angles(const RopeParams &p, long long t, int x, Pairs &r) {
+  const uint64_t pos = (uint64_t)(int64_t)__ldg(p.positions + t);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint64_t part = pos * (uint64_t)__ldg(p.freq + 8 * x + i);
+    const float half_turns = (float)(int32_t)(uint32_t)(part >> 32) * 0x1p-31f;
+    float s, c;
+    __sincosf(half_turns * 3.14159265358979f, &s, &c);
+    r.c[i] = c * p.factor;
+    r.s[i] = s * p.factor;
+  }
+}
 
 template <bool INTERLEAVED>
 __device__ __forceinline__ void turn(const Pairs &r, uint4 &a, uint4 &b) {
@@ -72,8 +86,9 @@ __device__ __forceinline__ void turn(const Pairs &r, uint4 &a, uint4 &b) {
 // n heads' rows from src to dst (16-byte vectors; `from` and `to` between
 // heads, `step` between a row's vectors at dst).
 template <bool INTERLEAVED>
-__device__ __forceinline__ void rows(const Pairs &r, bool rotated, const uint4 *src, long long from,
-                                     uint4 *dst, long long to, int step, int n) {
+__device__ __forceinline__ void rows(const RopeParams &p, long long t, Pairs &r, bool rotated,
+                                     const uint4 *src, long long from, uint4 *dst, long long to,
+                                     int step, int n) {
   if (!r.rotary && src == dst && from == to) return;  // in place: there already
   const int w0 = r.v0 * step, w1 = r.v1 * step;
 #pragma unroll 1
@@ -85,6 +100,10 @@ __device__ __forceinline__ void rows(const Pairs &r, bool rotated, const uint4 *
         a[i] = __ldcs(src + i * from + r.v0);
         b[i] = __ldcs(src + i * from + r.v1);
       }
+    if (r.rotary && !r.known) {  // (beside the first loads)
+      find_angles(p, t, threadIdx.x, r);
+      r.known = true;
+    }
 #pragma unroll
     for (int i = 0; i < kInFlight; ++i)
       if (h + i < n) {
@@ -115,20 +134,11 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p, int 
   }
   const int cols = p.rotary >> 4, x = threadIdx.x, lead = p.first >> 3;
   Pairs r;
+  r.known = false;
   r.rotary = x < cols;
   if (r.rotary) {
     r.v0 = lead + (INTERLEAVED ? 2 * x : x);
     r.v1 = lead + (INTERLEAVED ? 2 * x + 1 : x + cols);
-    const uint64_t pos = (uint64_t)(int64_t)__ldg(p.positions + t);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint64_t part = pos * (uint64_t)__ldg(p.freq + 8 * x + i);
-      const float half_turns = (float)(int32_t)(uint32_t)(part >> 32) * 0x1p-31f;
-      float s, c;
-      __sincosf(half_turns * 3.14159265358979f, &s, &c);
-      r.c[i] = c * p.factor;
-      r.s[i] = s * p.factor;
-    }
   } else {
     // the vectors outside the rotary part, two at a time
     const int i = 2 * (x - cols);
@@ -139,14 +149,14 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p, int 
   const int h0 = blockIdx.y * share;
   const int h1 = min(h0 + share, p.n_q + (APPEND ? 2 : 1) * p.n_kv);
   if (h0 < p.n_q)
-    rows<INTERLEAVED>(r, true, reinterpret_cast<const uint4 *>(p.q + t * p.q_row + h0 * p.q_head),
+    rows<INTERLEAVED>(p, t, r, true, reinterpret_cast<const uint4 *>(p.q + t * p.q_row + h0 * p.q_head),
                       p.q_head >> 3,
                       reinterpret_cast<uint4 *>(p.q_out + t * p.qo_row + h0 * p.qo_head),
                       p.qo_head >> 3, 1, min(h1, p.n_q) - h0);
   const int k0 = max(h0 - p.n_q, 0), k1 = min(h1 - p.n_q, p.n_kv);
   if (!APPEND) {
     if (k0 < k1)
-      rows<INTERLEAVED>(r, true, reinterpret_cast<const uint4 *>(p.k + t * p.k_row + k0 * p.k_head),
+      rows<INTERLEAVED>(p, t, r, true, reinterpret_cast<const uint4 *>(p.k + t * p.k_row + k0 * p.k_head),
                         p.k_head >> 3,
                         reinterpret_cast<uint4 *>(p.k_out + t * p.ko_row + k0 * p.ko_head),
                         p.ko_head >> 3, 1, k1 - k0);
@@ -157,13 +167,13 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p, int 
   const int s = (int)(slot - blk * p.bs);
   const long long tile = p.bs * 16LL, at = (s >> 3) * 128 + (s & 7);
   if (k0 < k1)
-    rows<INTERLEAVED>(r, true, reinterpret_cast<const uint4 *>(p.k + t * p.k_row + k0 * p.k_head),
+    rows<INTERLEAVED>(p, t, r, true, reinterpret_cast<const uint4 *>(p.k + t * p.k_row + k0 * p.k_head),
                       p.k_head >> 3,
                       reinterpret_cast<uint4 *>(p.k_cache) + (blk * p.n_kv + k0) * tile + at, tile,
                       8, k1 - k0);
   const int v0 = max(h0 - p.n_q - p.n_kv, 0), v1 = h1 - p.n_q - p.n_kv;
   if (v0 < v1)
-    rows<INTERLEAVED>(r, false, reinterpret_cast<const uint4 *>(p.v + t * p.v_row + v0 * p.v_head),
+    rows<INTERLEAVED>(p, t, r, false, reinterpret_cast<const uint4 *>(p.v + t * p.v_row + v0 * p.v_head),
                       p.v_head >> 3,
                       reinterpret_cast<uint4 *>(p.v_cache) + (blk * p.n_kv + v0) * tile + at, tile,
                       8, v1 - v0);
@@ -175,9 +185,9 @@ cudaError_t launch(const RopeParams &p, cudaStream_t stream) {
   const int y = std::max(1, std::min(kThreads / cols, p.T));
   const long long tiles = ((long long)p.T + y - 1) / y;
   // every token's heads in one thread a column where that fills the GPU (about
-  // 1000 threads an SM), else in shares of kInFlight heads and more
+  // 1000 threads an SM), else in as many shares as do
   const long long want = std::max(1LL, 152LL * 1024 / (tiles * y * cols));
-  const int share = (int)std::max<long long>(kInFlight, (heads + want - 1) / want);
+  const int share = (int)std::max<long long>(1, (heads + want - 1) / want);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)tiles, (unsigned)((heads + share - 1) / share));
   cfg.blockDim = dim3((unsigned)cols, (unsigned)y);
