@@ -62,15 +62,14 @@ constexpr int ring_bytes() {
 }
 template <int W>
 constexpr size_t smem_bytes() {
-  return (size_t)ring_bytes<W>() + W * kHeads * 8 + 16 + W * 4;
+  return (size_t)ring_bytes<W>() + W * kHeads * 8 + 16;
 }
 static_assert(kHeads * kMergeRow * 4 <= kStages * kStepBytes, "a warp's state fits its ring");
 
-// 16 bytes, or zeros (bytes = 0); read once, so the first to leave L2.
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, uint32_t bytes,
-                                       uint64_t policy) {
-  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst),
-               "l"(src), "r"(bytes), "l"(policy)
+// 16 bytes; read once, so the first to leave L2.
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "l"(policy)
                : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -111,18 +110,39 @@ __device__ __forceinline__ int unit_steps(const AttnParams &a, int BS, int b, in
   return (ctx - 1) / kStepTokens + 1;
 }
 
-// Parts of a unit with `steps` steps: of at most `part` each, or a given number.
-__device__ __forceinline__ int parts_of(int steps, int part, int splits) {
-  return splits ? min(splits, steps) : (steps + part - 1) / part;
-}
-
-// What a CTA does: steps [i0, i1) of a unit, which is part `part` of `parts`.
+// What a CTA does: steps [i0, i1) of a unit, which is one of its `parts` parts.
 struct Part {
   bool some;
-  int b, h, ctx, steps, part, parts;
+  int b, h, ctx, steps, parts;
   int i0, i1;
   int first;   // the CTA of (part 0, head 0) of this sequence
 };
+
+// How units are cut: into parts of at most `size` steps (to a millionth: every
+// CTA computes the same, and never more than ceil(steps / size)), or into a given
+// number.
+struct Cut {
+  int splits;
+  float inverse;  // of the size, and 2^-20 less
+  __device__ __forceinline__ int parts(int steps) const {
+    if (splits) return min(splits, steps);
+    return steps ? max(1, (int)ceilf((float)steps * inverse)) : 0;
+  }
+};
+// The sizes to try, the smaller first, for `all` steps.  With as many parts as
+// CTAs are resident at once; if rounding makes them more, with so many less that
+// it cannot; three times as many where a CTA has much to do.
+template <int W>
+__device__ __forceinline__ void choose_cuts(const Attn4Params &p, int all, Cut &one, Cut &two) {
+  one.splits = two.splits = p.splits;
+  const float x = (float)all;
+  float size = ceilf(x * p.inv_resident), other = ceilf(x * p.inv_spare);
+  if (size >= (float)(W * kManySteps)) size = other = ceilf(size * (1.f / 3.f));
+  size = fmaxf(size, (float)kLeastSteps);
+  other = fmaxf(other, (float)kLeastSteps);
+  one.inverse = __frcp_rn(size) * (1.f - 0x1p-20f);
+  two.inverse = __frcp_rn(other) * (1.f - 0x1p-20f);
+}
 
 __device__ __forceinline__ int inclusive_sum(int x, int lane) {
 #pragma unroll
@@ -133,123 +153,105 @@ __device__ __forceinline__ int inclusive_sum(int x, int lane) {
   return x;
 }
 
-// Finds CTA blockIdx.x's part.  Called by every thread; `scratch` holds W ints.
-// Up to 32 sequences every warp finds it in its lanes, without a barrier; of
-// more a warp looks at a run.
+// Finds CTA blockIdx.x's part.  Called by every thread.  Up to 32 sequences
+// every warp finds it in its lanes, without a barrier; of more a thread looks at
+// a run.
 template <int W>
-__device__ __forceinline__ Part find_part(const Attn4Params &p, int BS, int *scratch) {
+__device__ __forceinline__ Part find_part(const Attn4Params &p, int BS) {
+  __shared__ int sums[3][W], got[6];
   const AttnParams &a = p.a;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int runs = a.B <= 32 ? 1 : W, run = (a.B + 32 * runs - 1) / (32 * runs) * 32;
-  const int b0 = a.B <= 32 ? 0 : warp * run;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, cta = blockIdx.x;
   Part r;
-  r.some = false;
-  int ctx = 0, steps = 0;
-  int sum = 0;
-  for (int i = 0; i < run && b0 + i < a.B; i += 32) {
-    steps = b0 + i + lane < a.B ? unit_steps(a, BS, b0 + i + lane, ctx) : 0;
-    sum += __reduce_add_sync(kFullMask, steps);
-  }
-  int total = sum;
-  if (runs > 1) {
-    if (lane == 0) scratch[warp] = sum;
-    __syncthreads();
-    total = 0;
-#pragma unroll
-    for (int i = 0; i < W; ++i) total += scratch[i];
-    __syncthreads();
-  }
-  // Parts of at most `part` steps (total * n_kv < 2^30): as many as CTAs are
-  // resident at once, or where that leaves each with much to do three times as
-  // many.
-  const int all = total * a.n_kv;
-  int part;
-  if (all / (W * p.resident) >= kManySteps) {
-    part = (all - 1) / (3 * p.resident) + 1;
+  Cut one, two;
+  if (a.B <= 32) {
+    int ctx = 0, steps = 0;
+    if (lane < a.B) steps = unit_steps(a, BS, lane, ctx);
+    choose_cuts<W>(p, __reduce_add_sync(kFullMask, steps) * a.n_kv, one, two);
+    int n = one.parts(steps);
+    if (!p.splits && __reduce_add_sync(kFullMask, n) * a.n_kv > p.resident) n = two.parts(steps);
+    const int upto = inclusive_sum(n, lane) * a.n_kv, at = upto - n * a.n_kv;
+    const uint32_t hit = __ballot_sync(kFullMask, at <= cta && cta < upto);
+    r.some = hit != 0;
+    if (!hit) return r;
+    r.b = __ffs(hit) - 1;
+    r.ctx = __shfl_sync(kFullMask, ctx, r.b);
+    r.steps = __shfl_sync(kFullMask, steps, r.b);
+    r.parts = __shfl_sync(kFullMask, n, r.b);
+    r.first = __shfl_sync(kFullMask, at, r.b);
   } else {
-    part = max(kLeastSteps, (all - 1) / p.resident + 1);
-    for (int tries = 0; tries < 4; ++tries) {
-      int count = 0;
-      for (int i = 0; i < run && b0 + i < a.B; i += 32) {
-        if (runs > 1) steps = b0 + i + lane < a.B ? unit_steps(a, BS, b0 + i + lane, ctx) : 0;
-        count += __reduce_add_sync(kFullMask, parts_of(steps, part, 0));
-      }
-      if (runs > 1) {
-        if (lane == 0) scratch[warp] = count;
-        __syncthreads();
-        count = 0;
-#pragma unroll
-        for (int i = 0; i < W; ++i) count += scratch[i];
-        __syncthreads();
-      }
-      count *= a.n_kv;
-      if (count <= p.resident || count <= a.B * a.n_kv) break;
-      part = max(part + 1, (int)((float)part * (float)count / (float)p.resident));
-    }
-  }
-  int before = 0;  // CTAs of the sequences before
-  if (runs > 1) {
-    int mine = 0;
-    for (int i = 0; i < run && b0 + i < a.B; i += 32) {
-      const int b = b0 + i + lane;
-      const int n = b < a.B ? unit_steps(a, BS, b, ctx) : 0;
-      mine += __reduce_add_sync(kFullMask, parts_of(n, part, p.splits));
-    }
-    if (lane == 0) scratch[warp] = mine;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < W; ++i)
-      if (i < warp) before += scratch[i];
-    __syncthreads();
-    before *= a.n_kv;
-  }
-  const int cta = blockIdx.x;
-  bool found = false;
-  int n = 0, at = 0;
-  for (int i = 0; i < run && b0 + i < a.B; i += 32) {
-    if (runs > 1) steps = b0 + i + lane < a.B ? unit_steps(a, BS, b0 + i + lane, ctx) : 0;
-    n = parts_of(steps, part, p.splits);
-    const int upto = before + inclusive_sum(n, lane) * a.n_kv;
-    at = upto - n * a.n_kv;
-    const uint32_t hit = __ballot_sync(kFullMask, n > 0 && at <= cta && cta < upto);
-    if (hit) {
-      const int l = __ffs(hit) - 1;
-      r.b = b0 + i + l;
-      r.ctx = __shfl_sync(kFullMask, ctx, l);
-      r.steps = __shfl_sync(kFullMask, steps, l);
-      r.parts = __shfl_sync(kFullMask, n, l);
-      r.first = __shfl_sync(kFullMask, at, l);
-      found = true;
-    }
-    before = __shfl_sync(kFullMask, upto, 31);
-  }
-  if (runs > 1) {  // one warp has found it, or none
-    __shared__ int got[6];
+    const int run = (a.B + 32 * W - 1) / (32 * W);
+    const int b0 = threadIdx.x * run, b1 = min(a.B, b0 + run);
+    int ctx, sum = 0;
+    for (int b = b0; b < b1; ++b) sum += unit_steps(a, BS, b, ctx);
+    sum = __reduce_add_sync(kFullMask, sum);
+    if (lane == 0) sums[0][warp] = sum;
     if (threadIdx.x == 0) got[5] = 0;
     __syncthreads();
-    if (found && lane == 0) {
-      got[0] = r.b;
-      got[1] = r.ctx;
-      got[2] = r.steps;
-      got[3] = r.parts;
-      got[4] = r.first;
-      got[5] = 1;
+    int all = 0;
+#pragma unroll
+    for (int i = 0; i < W; ++i) all += sums[0][i];
+    choose_cuts<W>(p, all * a.n_kv, one, two);
+    int n1 = 0, n2 = 0;
+    for (int b = b0; b < b1; ++b) {
+      const int steps = unit_steps(a, BS, b, ctx);
+      n1 += one.parts(steps);
+      n2 += two.parts(steps);
+    }
+    const int u1 = inclusive_sum(n1, lane), u2 = inclusive_sum(n2, lane);
+    if (lane == 31) {
+      sums[1][warp] = u1;
+      sums[2][warp] = u2;
     }
     __syncthreads();
+    int before1 = 0, before2 = 0, all1 = 0;
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      all1 += sums[1][i];
+      if (i < warp) {
+        before1 += sums[1][i];
+        before2 += sums[2][i];
+      }
+    }
+    const bool first = p.splits || all1 * a.n_kv <= p.resident;
+    int upto = (first ? before1 + u1 : before2 + u2) * a.n_kv;
+    int at = upto - (first ? n1 : n2) * a.n_kv;
+    if (at <= cta && cta < upto)  // (one thread at most)
+      for (int b = b0; b < b1; ++b) {
+        const int steps = unit_steps(a, BS, b, ctx);
+        const int n = first ? one.parts(steps) : two.parts(steps);
+        upto = at + n * a.n_kv;
+        if (cta < upto) {
+          got[0] = b;
+          got[1] = ctx;
+          got[2] = steps;
+          got[3] = n;
+          got[4] = at;
+          got[5] = 1;
+          break;
+        }
+        at = upto;
+      }
+    __syncthreads();
+    r.some = got[5];
+    if (!r.some) return r;
     r.b = got[0];
     r.ctx = got[1];
     r.steps = got[2];
     r.parts = got[3];
     r.first = got[4];
-    found = got[5];
   }
-  if (!found) return r;
-  r.some = true;
-  r.part = (cta - r.first) / a.n_kv;
-  r.h = cta - r.first - r.part * a.n_kv;
-  const int q = r.steps / r.parts, left = r.steps - q * r.parts;
-  r.i0 = r.part * q + min(r.part, left);
-  r.i1 = r.i0 + q + (r.part < left ? 1 : 0);
+  int part = 0;
+  r.h = cta - r.first;
+  if (r.parts > 1) {
+    part = r.h / a.n_kv;
+    r.h -= part * a.n_kv;
+    const int q = r.steps / r.parts, left = r.steps - q * r.parts;
+    r.i0 = part * q + min(part, left);
+    r.i1 = r.i0 + q + (part < left ? 1 : 0);
+  } else {
+    r.i0 = 0;
+    r.i1 = r.steps;
+  }
   return r;
 }
 
@@ -258,8 +260,9 @@ struct Worker {
   const Attn4Params &p;
   int lane, g, t4, warp;
   unsigned char *ring;  // this warp's
-  uint32_t ring_at;
+  uint32_t ring_at, rest_at;  // as shared addresses: its start, this lane's last piece
   uint64_t policy;
+  const unsigned char *from_k, *from_v;  // the head's tile of block 0, this lane's first piece
 
   // Fragments and state.
   uint32_t qf[16];
@@ -277,6 +280,7 @@ struct Worker {
     t4 = lane & 3;
     ring = smem + warp * kStages * kStepBytes;
     ring_at = smem_addr(ring);
+    rest_at = ring_at + (lane >> 3) * kGroupBytes4 + 1024 + (lane & 7) * 16;
     policy = l2_policy_evict_first();
   }
 
@@ -328,36 +332,23 @@ struct Worker {
       for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
   }
 
-  // Starts the copies of a step from its blocks' ids (-1: nothing, zeros).
-  __device__ __forceinline__ void load_step(int slot, int id0, int id1, int h) {
+  // Starts the copies of a step from its blocks' ids: of each of its four groups
+  // (72 pieces of 16 bytes) two pieces a lane, and the last eight of all in one.
+  __device__ __forceinline__ void load_step(int slot, int id0, int id1) {
     const uint32_t dst = ring_at + slot * kStepBytes + lane * 16;
-    if constexpr (BS == 32) {
-      const size_t at = ((size_t)max(id0, 0) * p.a.n_kv + h) * (2 * kGroupBytes4);
-      const unsigned char *k = p.a.k_cache + at, *v = p.a.v_cache + at;
-      const uint32_t n = id0 >= 0 ? 16u : 0u;
+    const uint32_t block = (uint32_t)p.a.n_kv * (BS / kGroupTokens4 * kGroupBytes4);
+    const unsigned char *src[4];
+    src[0] = from_k + (uint64_t)(uint32_t)id0 * block;
+    src[2] = from_v + (uint64_t)(uint32_t)id0 * block;
+    src[1] = BS == 32 ? src[0] + kGroupBytes4 : from_k + (uint64_t)(uint32_t)id1 * block;
+    src[3] = BS == 32 ? src[2] + kGroupBytes4 : from_v + (uint64_t)(uint32_t)id1 * block;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) copy16(dst + j * 512, k + lane * 16 + j * 512, n, policy);
-      // the fifth goes on from K (128 more bytes ... 144 pieces) to V
-      copy16(dst + 4 * 512, lane < 16 ? k + lane * 16 + 2048 : v + (lane - 16) * 16, n, policy);
-#pragma unroll
-      for (int j = 5; j < 9; ++j) copy16(dst + j * 512, v + (lane - 16) * 16 + (j - 4) * 512, n, policy);
-    } else {
-      const size_t a0 = ((size_t)max(id0, 0) * p.a.n_kv + h) * kGroupBytes4;
-      const size_t a1 = ((size_t)max(id1, 0) * p.a.n_kv + h) * kGroupBytes4;
-      const unsigned char *k0 = p.a.k_cache + a0, *v0 = p.a.v_cache + a0;
-      const unsigned char *k1 = p.a.k_cache + a1, *v1 = p.a.v_cache + a1;
-      const uint32_t n0 = id0 >= 0 ? 16u : 0u, n1 = id1 >= 0 ? 16u : 0u;
-      const int x = lane * 16;
-      copy16(dst, k0 + x, n0, policy);
-      copy16(dst + 512, k0 + x + 512, n0, policy);
-      copy16(dst + 1024, lane < 8 ? k0 + x + 1024 : k1 + (x - 128), lane < 8 ? n0 : n1, policy);
-      copy16(dst + 1536, k1 + (x - 128) + 512, n1, policy);
-      copy16(dst + 2048, lane < 16 ? k1 + (x - 128) + 1024 : v0 + (x - 256), lane < 16 ? n1 : n0, policy);
-      copy16(dst + 2560, v0 + (x - 256) + 512, n0, policy);
-      copy16(dst + 3072, lane < 24 ? v0 + (x - 256) + 1024 : v1 + (x - 384), lane < 24 ? n0 : n1, policy);
-      copy16(dst + 3584, v1 + (x - 384) + 512, n1, policy);
-      copy16(dst + 4096, v1 + (x - 384) + 1024, n1, policy);
+    for (int i = 0; i < 4; ++i) {
+      copy16(dst + i * kGroupBytes4, src[i], policy);
+      copy16(dst + i * kGroupBytes4 + 512, src[i] + 512, policy);
     }
+    const unsigned char *mine = lane < 16 ? (lane < 8 ? src[0] : src[1]) : (lane < 24 ? src[2] : src[3]);
+    copy16(rest_at + slot * kStepBytes, mine + 1024 - (lane & 24) * 16, policy);
   }
 
   // Quarter w of the scores of a step, s += : both groups' 16 tokens by two of
@@ -397,22 +388,45 @@ struct Worker {
     }
   }
 
+  // V's scales as halves, each converted once: lane l those of tokens 4 (l / 8)
+  // .. + 3 and group l % 8 of the 16, for all lanes that hold these tokens.  They
+  // take the place of K's codes, which have been read.  Tokens behind the context
+  // get zeros (they may hold NaN).
+  __device__ __forceinline__ void spread_scales(unsigned char *st, int valid) const {
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      uint32_t x = *reinterpret_cast<const uint32_t *>(st + (2 + i) * kGroupBytes4 + kGroupCodes4 +
+                                                       lane * 4);
+      if (valid < kStepTokens) {
+        const int left = valid - 16 * i - 4 * (lane >> 3);  // tokens of this lane's four
+        x = left <= 0 ? 0u : left < 4 ? x & ((1u << (8 * left)) - 1u) : x;
+      }
+      *reinterpret_cast<uint2 *>(st + i * 256 + lane * 8) =
+          make_uint2(half2_bits(e4m3x2_to_half2((uint16_t)x)),
+                     half2_bits(e4m3x2_to_half2((uint16_t)(x >> 16))));
+    }
+    __syncwarp();
+  }
+
   // Quarter w of the outputs of a step: 64 dims of 16 tokens.
   template <int w>
   __device__ __forceinline__ void outputs(const unsigned char *st) {
     constexpr int sub = w >> 1, half = w & 1;
-    const unsigned char *v = st + sub * kGroupBytes4;
-    const uint4 a = *reinterpret_cast<const uint4 *>(v + half * 512 + lane * 16);
-    const uint4 c = *reinterpret_cast<const uint4 *>(v + kGroupCodes4 + t4 * 32 + half * 16);
-    const uint32_t wa[4] = {a.x, a.y, a.z, a.w}, wc[4] = {c.x, c.y, c.z, c.w};
+    const uint4 a = *reinterpret_cast<const uint4 *>(st + (2 + sub) * kGroupBytes4 + half * 512 +
+                                                     lane * 16);
+    const uint32_t wa[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __half2 s01 = e4m3x2_to_half2((uint16_t)wc[i]);
-      const __half2 s23 = e4m3x2_to_half2((uint16_t)(wc[i] >> 16));
-      uint32_t x[4];
-      e2m1x8_to_half2x4(wa[i], x);  // dim row g: tokens 0 1, 2 3; dim row g + 8
-      mma_16816(o[4 * half + i], times(x[0], s01), times(x[2], s01), times(x[1], s23),
-                times(x[3], s23), pf[sub][0], pf[sub][1]);
+    for (int j = 0; j < 2; ++j) {
+      const uint4 c = *reinterpret_cast<const uint4 *>(st + sub * 256 + t4 * 64 + half * 32 + j * 16);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const __half2 s01 = bits_half2(i ? c.z : c.x), s23 = bits_half2(i ? c.w : c.y);
+        uint32_t x[4];
+        e2m1x8_to_half2x4(wa[2 * j + i], x);  // dim row g: tokens 0 1, 2 3; dim row g + 8
+        mma_16816(o[4 * half + 2 * j + i], times(x[0], s01), times(x[2], s01), times(x[1], s23),
+                  times(x[3], s23), pf[sub][0], pf[sub][1]);
+      }
     }
   }
 
@@ -465,27 +479,21 @@ struct Worker {
     }
   }
 
-  // The last step's tokens behind the context: their V scales to zero (they may
-  // hold NaN).
-  __device__ __forceinline__ void clear_scales(unsigned char *st, int valid) {
-    for (int i = lane; i < kStepTokens * 8; i += 32) {
-      const int t = i >> 3, c = i & 7;
-      if (t >= valid)
-        st[(t >> 4) * kGroupBytes4 + kGroupCodes4 + ((t & 15) >> 2) * 32 + c * 4 + (t & 3)] = 0;
-    }
-    __syncwarp();
-  }
-
   // Steps i0 + warp, + W, ... below i1 of one unit.
   __device__ __forceinline__ void run(const Part &u, int G) {
     const int32_t *row = p.a.tables + (size_t)u.b * p.a.MB;
     const int nblk = (u.ctx - 1) / BS + 1;
     const int first = u.i0 + warp;
     const int n = first < u.i1 ? (u.i1 - first + W - 1) / W : 0;
-    int a0 = -1, a1 = -1;  // lane l: the ids of the warp's step 32 j + l
+    const size_t head = (size_t)u.h * (BS / kGroupTokens4 * kGroupBytes4) + lane * 16;
+    from_k = p.a.k_cache + head;
+    from_v = p.a.v_cache + head;
+    // lane l: the ids of the warp's step 32 j + l; a bad id (flagged) and a block
+    // that the context does not reach (its tokens are masked) read block 0
+    int a0 = 0, a1 = 0;
     auto ids = [&](int k0) {
       const int t = first + (k0 + lane) * W;
-      a0 = a1 = -1;
+      a0 = a1 = 0;
       if (k0 + lane < n) {
         if constexpr (BS == 32) {
           a0 = check(__ldg(row + t));
@@ -499,7 +507,7 @@ struct Worker {
       if (k < n) {
         if ((k & 31) == 0) ids(k);
         load_step(slot, __shfl_sync(kFullMask, a0, k & 31),
-                  BS == 32 ? -1 : __shfl_sync(kFullMask, a1, k & 31), u.h);
+                  BS == 32 ? 0 : __shfl_sync(kFullMask, a1, k & 31));
       }
       copies_commit();
     };
@@ -517,19 +525,19 @@ struct Worker {
       issue(k + kStages - 1, slot == 0 ? kStages - 1 : slot - 1);
       const int valid = min(kStepTokens, u.ctx - (first + k * W) * kStepTokens);
       unsigned char *st = ring + slot * kStepBytes;
-      if (valid < kStepTokens) clear_scales(st + 2 * kGroupBytes4, valid);
       Keys x;
       load_keys(st, x);
+      spread_scales(st, valid);
       float s[2][4] = {};
       scores<0>(x, s);
       scores<1>(x, s);
       scores<2>(x, s);
       scores<3>(x, s);
       weights(s, valid);
-      outputs<0>(st + 2 * kGroupBytes4);
-      outputs<1>(st + 2 * kGroupBytes4);
-      outputs<2>(st + 2 * kGroupBytes4);
-      outputs<3>(st + 2 * kGroupBytes4);
+      outputs<0>(st);
+      outputs<1>(st);
+      outputs<2>(st);
+      outputs<3>(st);
       if (++slot == kStages) slot = 0;
     }
     copies_wait<0>();
@@ -538,7 +546,7 @@ struct Worker {
   __device__ __forceinline__ int check(int id) {
     if ((unsigned)id < (unsigned)p.a.NB) return id;
     atomicOr(p.a.err, PGD_DEVERR_BAD_BLOCK_ID);
-    return -1;
+    return 0;
   }
 };
 
@@ -641,7 +649,7 @@ __global__ void __launch_bounds__(W * 32, W == 4 ? 4 : 1)
 
   if (!a.wait_late) pdl_wait();
   pdl_launch_dependents();
-  const Part u = find_part<W>(p, BS, flag + 4);
+  const Part u = find_part<W>(p, BS);
   if (a.wait_late) pdl_wait();
   if (!u.some) return;
   Worker<BS, W> w(p, smem);
@@ -770,7 +778,12 @@ cudaError_t attention_fp4_launch(const Attn4Params &p_in, int G, int bs, int gri
                                  cudaStream_t stream) {
   Attn4Params p = p_in;
   const int W = warps_of((long long)p.a.B * p.a.n_kv, (long long)p.a.MB * bs, sms);
+  const long long units = (long long)p.a.B * p.a.n_kv;
   p.resident = (int)resident_ctas(W, sms);
+  p.inv_resident = 1.f / (float)p.resident;
+  // ceil(steps / size) over the units is at most all / size + units; more units
+  // than that stay whole
+  p.inv_spare = units < p.resident ? 1.f / (float)(p.resident - units) : 1.f;
   if (W == 16)
     return bs == 16 ? launch_kernel<16, 16>(p, G, grid, stream)
                     : launch_kernel<32, 16>(p, G, grid, stream);

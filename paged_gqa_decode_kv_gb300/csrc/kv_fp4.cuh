@@ -88,8 +88,10 @@ cudaError_t kv_read_fp4_launch(const Kv4Params &p, cudaStream_t stream);
 struct Attn4Params {
   AttnParams a;
   float v_scale;
-  int splits;       // parts of a unit, or 0: automatic,
-  int resident;     // ... for this many CTAs at once
+  int splits;          // parts of a unit, or 0: automatic,
+  int resident;        // ... for this many CTAs at once
+  float inv_resident;  // 1 / resident
+  float inv_spare;     // 1 / (resident - units), or 1
 };
 long long attention_fp4_grid(long long units, long long tokens, int sms);
 cudaError_t attention_fp4_launch(const Attn4Params &p, int G, int bs, int grid, int sms,
