@@ -51,7 +51,6 @@ constexpr int kStepBytes = 2 * 2 * kGroupBytes4;  // K and V of two groups
 constexpr int kStages = 3;
 constexpr int kHeads = 8;              // query heads a product takes
 constexpr int kMergeRow = kHeadDim + 4;  // floats between heads when states are merged
-constexpr int kLeastSteps = 8;         // steps of a part of an automatic split
 constexpr int kManySteps = 25;          // steps a warp from which three CTAs follow one another
 constexpr float kMoveLog2 = 8.f;       // move the reference when exceeded by 2^8
 constexpr float kUnitLog2 = 7.f;       // a weight of the reference is 2^7
@@ -138,8 +137,8 @@ __device__ __forceinline__ void choose_cuts(const Attn4Params &p, int all, Cut &
   const float x = (float)all;
   float size = ceilf(x * p.inv_resident), other = ceilf(x * p.inv_spare);
   if (size >= (float)(W * kManySteps)) size = other = ceilf(size * (1.f / 3.f));
-  size = fmaxf(size, (float)kLeastSteps);
-  other = fmaxf(other, (float)kLeastSteps);
+  size = fmaxf(size, (float)p.least_steps);
+  other = fmaxf(other, (float)p.least_steps);
   one.inverse = __frcp_rn(size) * (1.f - 0x1p-20f);
   two.inverse = __frcp_rn(other) * (1.f - 0x1p-20f);
 }
@@ -767,10 +766,18 @@ static int warps_of(long long units, long long tokens, int sms) {
 }
 static long long resident_ctas(int W, int sms) { return W == 16 ? sms : 4LL * sms; }
 
+// Steps of a part at least: a step a warp where all CTAs together are few, else
+// two, as more parts take longer to merge (one context of 512 tokens: 5.0 us with
+// 4 steps, 5.6 with 8; of 4096: 7.6 and 6.4).
+static int least_steps(long long units, long long tokens, int sms) {
+  const long long steps = (tokens - 1) / kStepTokens + 1;
+  return units * ((steps - 1) / 8 + 1) <= sms / 2 ? 4 : 8;
+}
+
 // The most CTAs of an automatic call on tables of MB * bs = tokens.
 long long attention_fp4_grid(long long units, long long tokens, int sms) {
   const long long steps = (tokens - 1) / kStepTokens + 1;
-  const long long most = units * ((steps - 1) / kLeastSteps + 1);
+  const long long most = units * ((steps - 1) / least_steps(units, tokens, sms) + 1);
   return std::min(most, units + 3 * resident_ctas(warps_of(units, tokens, sms), sms));
 }
 
@@ -780,6 +787,7 @@ cudaError_t attention_fp4_launch(const Attn4Params &p_in, int G, int bs, int gri
   const int W = warps_of((long long)p.a.B * p.a.n_kv, (long long)p.a.MB * bs, sms);
   const long long units = (long long)p.a.B * p.a.n_kv;
   p.resident = (int)resident_ctas(W, sms);
+  p.least_steps = least_steps(units, (long long)p.a.MB * bs, sms);
   p.inv_resident = 1.f / (float)p.resident;
   // ceil(steps / size) over the units is at most all / size + units; more units
   // than that stay whole

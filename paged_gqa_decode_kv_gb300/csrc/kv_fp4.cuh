@@ -89,7 +89,8 @@ struct Attn4Params {
   AttnParams a;
   float v_scale;
   int splits;          // parts of a unit, or 0: automatic,
-  int resident;        // ... for this many CTAs at once
+  int resident;        // ... for this many CTAs at once,
+  int least_steps;     // ... of so many steps at least
   float inv_resident;  // 1 / resident
   float inv_spare;     // 1 / (resident - units), or 1
 };
