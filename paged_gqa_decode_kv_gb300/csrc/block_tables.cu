@@ -69,6 +69,12 @@ __device__ __forceinline__ void block_scan(int (&x)[N], int (*sums)[32], int (&t
   }
 }
 
+// x / bs, rounded down and up (x >= 0): block sizes are powers of two as a rule.
+__device__ __forceinline__ int blocks_down(int x, int bs, int lg) { return lg >= 0 ? x >> lg : x / bs; }
+__device__ __forceinline__ int blocks_up(long long x, int bs, int lg) {
+  return (int)(lg >= 0 ? (x + bs - 1) >> lg : (x + bs - 1) / bs);
+}
+
 // The last row whose start is at most n (starts[B] > n).
 __device__ __forceinline__ int row_of(const int32_t *starts, int B, int n) {
   int lo = 0, hi = B;
@@ -146,9 +152,9 @@ __global__ void __launch_bounds__(NT) grow_tables_kernel(const GrowParams p) {
       add = 0;
     }
     if (add > 0) {
-      const int at = (int)(((long long)len + p.bs - 1) / p.bs);
-      need = (int)(((long long)len + add + p.bs - 1) / p.bs) - at;
-      if (len % p.bs) {
+      const int at = blocks_up(len, p.bs, p.lg_bs);
+      need = blocks_up((long long)len + add, p.bs, p.lg_bs) - at;
+      if (len != at * (long long)p.bs) {
         last = p.tables[(size_t)b * p.MB + at - 1];
         if ((unsigned)last >= (unsigned)p.NB) {
           if (first) atomicOr(p.err, PGD_DEVERR_BAD_BLOCK_ID);
@@ -222,6 +228,11 @@ __global__ void __launch_bounds__(NT) grow_tables_kernel(const GrowParams p) {
       starts[p.B] = tokens;
     }
   }
+  // (the first chunk of one CTA is summed already)
+  if (C == 1 && words <= NT * kWords) {
+    upto[tid] = x[2];
+    *reinterpret_cast<uint4 *>(chunk[tid]) = make_uint4(bits[0], bits[1], bits[2], bits[3]);
+  }
   __syncthreads();
 
   // The lowest free ids, in the order of the rows, by chunks of the pool that
@@ -243,15 +254,15 @@ __global__ void __launch_bounds__(NT) grow_tables_kernel(const GrowParams p) {
     if (C > 1 || words > NT * kWords) {
       __syncthreads();  // (the last chunk is done with)
       block_scan<NT, 1>(n, sums, all);
+      upto[tid] = n[0];
+      *reinterpret_cast<uint4 *>(chunk[tid]) = make_uint4(bits[0], bits[1], bits[2], bits[3]);
+      if constexpr (C > 1)
+        cg::this_cluster().sync();  // every CTA has read the chunk's bits
+      else
+        __syncthreads();
     } else {
-      n[0] = x[2];  // the one chunk there is: summed above
+      n[0] = x[2];
     }
-    upto[tid] = n[0];
-    *reinterpret_cast<uint4 *>(chunk[tid]) = make_uint4(bits[0], bits[1], bits[2], bits[3]);
-    if constexpr (C > 1)
-      cg::this_cluster().sync();  // every CTA has read the chunk's bits
-    else
-      __syncthreads();
     for (int k = rank * NT + tid; k < min(all[0], need - before); k += C * NT) {
       int lo = 0, hi = NT - 1;  // the first thread with upto > k
       while (lo < hi) {
@@ -271,7 +282,7 @@ __global__ void __launch_bounds__(NT) grow_tables_kernel(const GrowParams p) {
       const int i = before + k, b = row_of(off, p.B, i), at = i - off[b];
       const int len = lens[b] & 0x7fffffff;
       const bool copied = lens[b] < 0;
-      const int col = (int)(((long long)len + p.bs - 1) / p.bs) - (copied ? 1 : 0);
+      const int col = blocks_up(len, p.bs, p.lg_bs) - (copied ? 1 : 0);
       p.tables[(size_t)b * p.MB + col + at] = id;
       p.refs[id] = 1;
       if (C == 1 && i < kIds) ids[i] = id;
@@ -313,9 +324,9 @@ __global__ void __launch_bounds__(NT) grow_tables_kernel(const GrowParams p) {
       int pos = 0;
       if (n < tokens) {
         const int b = row_of(starts, p.B, n), len = lens[b] & 0x7fffffff;
-        const int col = (int)(((long long)len + p.bs - 1) / p.bs) - (lens[b] < 0 ? 1 : 0);
+        const int col = blocks_up(len, p.bs, p.lg_bs) - (lens[b] < 0 ? 1 : 0);
         pos = len + (n - starts[b]);
-        const int j = pos / p.bs, i = off[b] + j - col;
+        const int j = blocks_down(pos, p.bs, p.lg_bs), i = off[b] + j - col;
         int id;
         if (j >= col && i < kIds)
           id = ids[i];
@@ -349,7 +360,7 @@ __global__ void __launch_bounds__(kSlotThreads) place_tokens_kernel(const GrowPa
     if (n < total) {
       while (p.starts[b + 1] <= n) ++b;
       at[i] = p.positions[b] + (n - p.starts[b]);
-      j[i] = at[i] / p.bs;
+      j[i] = blocks_down(at[i], p.bs, p.lg_bs);
       entry[i] = p.tables[(size_t)b * p.MB + j[i]];
     }
   }
@@ -418,6 +429,7 @@ cudaError_t grow_tables_launch(const GrowParams &p_in, cudaStream_t stream) {
   GrowParams p = p_in;
   const bool one = p.N <= kInlineTokens && p.NB <= kInlineBlocks;
   p.keep_lasts = one && p.B <= 8192 ? 1 : 0;
+  p.lg_bs = (p.bs & (p.bs - 1)) ? -1 : __builtin_ctz((unsigned)p.bs);
   const size_t smem = ((size_t)p.B * (p.keep_lasts ? 4 : 3) + 2) * sizeof(int32_t);
   auto kernel = one ? grow_tables_kernel<512, 1> : grow_tables_kernel<1024, kCluster>;
   if (smem > 16 * 1024) {  // (more than 48 KB with the static part)

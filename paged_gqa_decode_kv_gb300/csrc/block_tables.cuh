@@ -19,7 +19,8 @@ struct GrowParams {
   int32_t *copy_src, *copy_dst;  // [B]
   int32_t *result;               // [4]
   int B, N, bs, MB, NB;
-  int keep_lasts;                // the launch's: room for the rows' last blocks
+  // the launch's: log2(bs), or -1; room for the rows' last blocks
+  int lg_bs, keep_lasts;
   int32_t *err;
 };
 constexpr int kMaxGrowRows = 16384;  // three int32 a row in shared memory
