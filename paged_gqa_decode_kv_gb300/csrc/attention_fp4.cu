@@ -55,6 +55,9 @@ constexpr int kManySteps = 25;          // steps a warp from which three CTAs fo
 constexpr float kMoveLog2 = 8.f;       // move the reference when exceeded by 2^8
 constexpr float kUnitLog2 = 7.f;       // a weight of the reference is 2^7
 
+// CTAs an SM: 16 warps with a ring each, as many as shared memory holds.
+template <int W>
+constexpr int kResident = W == 1 ? 15 : W == 2 ? 7 : 16 / W;
 template <int W>
 constexpr int ring_bytes() {
   return W * kStages * kStepBytes;
@@ -136,7 +139,7 @@ __device__ __forceinline__ void choose_cuts(const Attn4Params &p, int all, Cut &
   one.splits = two.splits = p.splits;
   const float x = (float)all;
   float size = ceilf(x * p.inv_resident), other = ceilf(x * p.inv_spare);
-  if (size >= (float)(W * kManySteps)) size = other = ceilf(size * (1.f / 3.f));
+  if (p.uneven && size >= (float)(W * kManySteps)) size = other = ceilf(size * (1.f / 3.f));
   size = fmaxf(size, (float)p.least_steps);
   other = fmaxf(other, (float)p.least_steps);
   one.inverse = __frcp_rn(size) * (1.f - 0x1p-20f);
@@ -637,7 +640,7 @@ __device__ __forceinline__ void merge_parts(const Attn4Params &p, int G, size_t 
 }
 
 template <int BS, int W>
-__global__ void __launch_bounds__(W * 32, W == 4 ? 4 : 1)
+__global__ void __launch_bounds__(W * 32, kResident<W>)
     attention_fp4_kernel(const Attn4Params p, int G) {
   extern __shared__ __align__(128) unsigned char smem[];
   float *refs = reinterpret_cast<float *>(smem + ring_bytes<W>());  // [W][8] warps' references
@@ -757,14 +760,20 @@ cudaError_t launch_kernel(const Attn4Params &p, int G, int grid, cudaStream_t st
 
 }  // namespace
 
-// 4 warps a CTA, four CTAs an SM, or 16 and one: for long contexts of units
-// that are so few that small parts would be many to merge, or so many that most
-// SMs have one whole.
+// 4 warps a CTA, four CTAs an SM, or 16 and one.  16 for long contexts of so few
+// units that smaller parts are many to merge (one context of 131072 tokens, 8
+// units: 30.8 us, with 4 warps 35; but 4096: 7.4 and 6.4), and where most SMs have
+// one whole unit that is not too long for the SMs without one to matter (16 x
+// 8192, 128 units: 30.1 and 32.1; x 32768: 119 and 107).
+// 32 units of 32768 tokens: 32 and 29.7; 64 of 37 thousand: 79 and 59.
 static int warps_of(long long units, long long tokens, int sms) {
   const long long steps = units * ((tokens - 1) / kStepTokens + 1);
-  return steps >= 64LL * sms && (units <= 16 || (units <= sms && 4 * units > 3 * sms)) ? 16 : 4;
+  if (units <= 16) return steps >= 20LL * sms ? 16 : 4;
+  return steps >= 64LL * sms && steps < 400LL * sms && units <= sms && 4 * units > 3 * sms ? 16 : 4;
 }
-static long long resident_ctas(int W, int sms) { return W == 16 ? sms : 4LL * sms; }
+static long long resident_ctas(int W, int sms) {
+  return (W == 16 ? kResident<16> : kResident<4>) * (long long)sms;
+}
 
 // Steps of a part at least: a step a warp where all CTAs together are few, else
 // two, as more parts take longer to merge (one context of 512 tokens: 5.0 us with
@@ -789,6 +798,7 @@ cudaError_t attention_fp4_launch(const Attn4Params &p_in, int G, int bs, int gri
   p.resident = (int)resident_ctas(W, sms);
   p.least_steps = least_steps(units, (long long)p.a.MB * bs, sms);
   p.inv_resident = 1.f / (float)p.resident;
+  p.uneven = 8 * units > p.resident;
   // ceil(steps / size) over the units is at most all / size + units; more units
   // than that stay whole
   p.inv_spare = units < p.resident ? 1.f / (float)(p.resident - units) : 1.f;

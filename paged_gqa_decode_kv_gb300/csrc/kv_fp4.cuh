@@ -91,6 +91,7 @@ struct Attn4Params {
   int splits;          // parts of a unit, or 0: automatic,
   int resident;        // ... for this many CTAs at once,
   int least_steps;     // ... of so many steps at least
+  int uneven;          // the units are so many that parts of one size do not fill these CTAs
   float inv_resident;  // 1 / resident
   float inv_spare;     // 1 / (resident - units), or 1
 };
