@@ -61,13 +61,14 @@ struct Group {
 __device__ __forceinline__ Group find_group(const Kv4Params &p, uint32_t groups, uint32_t run) {
   Group it;
   it.r0 = it.r1 = 0;
-  const long long id = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const long long warp = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
   const bool lane0 = (threadIdx.x & 31) == 0;
   const uint32_t items = 2 * (uint32_t)p.n_kv, runs = (items + run - 1) / run;
-  const long long per_b = (long long)groups * runs;
-  if (id >= per_b * p.B) return it;
+  const uint32_t per_b = groups * runs;  // (the host bounds B * groups * items by 2^32)
+  if (warp >= (long long)per_b * p.B) return it;
+  const uint32_t id = (uint32_t)warp;
   const int b = (int)(id / per_b);
-  const uint32_t rest = (uint32_t)(id - b * per_b), jrel = rest / runs;
+  const uint32_t rest = id - (uint32_t)b * per_b, jrel = rest / runs;
   const uint32_t r0 = (rest - jrel * runs) * run;
   const TokenRange t = token_range(p.starts, b, p.T, p.N);
   const bool first = jrel == 0 && r0 == 0 && lane0;
@@ -146,6 +147,19 @@ __device__ __forceinline__ void append_group(const Kv4Params &p, const Group &it
                              (size_t)head * (p.bs / kGroupTokens4) * kGroupBytes4;
   // (a power of two: its inverse is exact)
   const float inv_scale = __frcp_rn(is_v ? p.v_scale : p.k_scale);
+  // V's words that keep nibbles: lane * 16 holds dims of row lane / 4, tokens 4 t4 ..
+  const int t4 = lane & 3;
+  uint32_t keep = 0;
+  uint4 old[2];
+  if (is_v) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (4 * t4 + u < it.t0 || 4 * t4 + u >= it.t1) keep |= 0x000f000fu << (4 * u);
+    if (keep != 0 && keep != 0xffffffffu) {
+      old[0] = *reinterpret_cast<const uint4 *>(dst + lane * 16);
+      old[1] = *reinterpret_cast<const uint4 *>(dst + 512 + lane * 16);
+    }
+  }
   uint4 x[4][2];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -159,6 +173,7 @@ __device__ __forceinline__ void append_group(const Kv4Params &p, const Group &it
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int t = 4 * i + r;
+    if (4 * i + 3 < it.t0 || 4 * i >= it.t1) continue;  // (none of these four)
     uint32_t sc;
     const uint2 codes = quantise16(x[i], inv_scale, sc);
     const bool there = t >= it.t0 && t < it.t1;
@@ -176,23 +191,16 @@ __device__ __forceinline__ void append_group(const Kv4Params &p, const Group &it
   }
   if (!is_v) return;
   __syncwarp();
-  const int t4 = lane & 3;  // lane * 16: dims of row lane / 4, tokens 4 t4 ..
-  uint32_t keep = 0;  // nibbles of a word that stay as they are
-#pragma unroll
-  for (int u = 0; u < 4; ++u)
-    if (4 * t4 + u < it.t0 || 4 * t4 + u >= it.t1) keep |= 0xfu << (4 * u);
-  if (keep == 0xffffu) return;
-  keep |= keep << 16;
+  if (keep == 0xffffffffu) return;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     uint4 o = *reinterpret_cast<const uint4 *>(smem + image_at(h * 512 + lane * 16));
     uint4 *at = reinterpret_cast<uint4 *>(dst + h * 512 + lane * 16);
     if (keep) {
-      const uint4 old = *at;
-      o.x = (o.x & ~keep) | (old.x & keep);
-      o.y = (o.y & ~keep) | (old.y & keep);
-      o.z = (o.z & ~keep) | (old.z & keep);
-      o.w = (o.w & ~keep) | (old.w & keep);
+      o.x = (o.x & ~keep) | (old[h].x & keep);
+      o.y = (o.y & ~keep) | (old[h].y & keep);
+      o.z = (o.z & ~keep) | (old[h].z & keep);
+      o.w = (o.w & ~keep) | (old[h].w & keep);
     }
     *at = o;
   }
