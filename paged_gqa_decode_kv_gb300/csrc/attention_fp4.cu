@@ -51,6 +51,10 @@ constexpr int kStepBytes = 2 * 2 * kGroupBytes4;  // K and V of two groups
 constexpr int kStages = 3;
 constexpr int kHeads = 8;              // query heads a product takes
 constexpr int kMergeRow = kHeadDim + 4;  // floats between heads when states are merged
+// Units of no more steps than this are not cut: a part's way through the workspace
+// takes longer than three steps of a warp (4 contexts of 217 tokens: 3.9 us whole,
+// 5.8 in two parts).
+constexpr int kWholeSteps = 12;
 constexpr int kManySteps = 25;          // steps a warp from which three CTAs follow one another
 constexpr float kMoveLog2 = 8.f;       // move the reference when exceeded by 2^8
 constexpr float kUnitLog2 = 7.f;       // a weight of the reference is 2^7
@@ -128,7 +132,8 @@ struct Cut {
   float inverse;  // of the size, and 2^-20 less
   __device__ __forceinline__ int parts(int steps) const {
     if (splits) return min(splits, steps);
-    return steps ? max(1, (int)ceilf((float)steps * inverse)) : 0;
+    if (steps <= kWholeSteps) return steps > 0 ? 1 : 0;
+    return max(1, (int)ceilf((float)steps * inverse));
   }
 };
 // The sizes to try, the smaller first, for `all` steps.  With as many parts as
@@ -155,32 +160,71 @@ __device__ __forceinline__ int inclusive_sum(int x, int lane) {
   return x;
 }
 
-// Finds CTA blockIdx.x's part.  Called by every thread.  Up to 32 sequences
-// every warp finds it in its lanes, without a barrier; of more a thread looks at
-// a run.
+// The sequence of CTA blockIdx.x's part, found by every warp for itself: a lane
+// looks at R sequences.  False: there is none.
+template <int R, int W>
+__device__ __forceinline__ bool find_in_lanes(const Attn4Params &p, int BS, Part &r) {
+  const AttnParams &a = p.a;
+  const int lane = threadIdx.x & 31, cta = blockIdx.x;
+  int ctx[R], steps[R], n[R], sum = 0;
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    ctx[i] = steps[i] = 0;
+    if (lane * R + i < a.B) steps[i] = unit_steps(a, BS, lane * R + i, ctx[i]);
+    sum += steps[i];
+  }
+  Cut one, two;
+  choose_cuts<W>(p, __reduce_add_sync(kFullMask, sum) * a.n_kv, one, two);
+  int mine = 0;
+#pragma unroll
+  for (int i = 0; i < R; ++i) mine += n[i] = one.parts(steps[i]);
+  if (!p.splits && __reduce_add_sync(kFullMask, mine) * a.n_kv > p.resident) {
+    mine = 0;
+#pragma unroll
+    for (int i = 0; i < R; ++i) mine += n[i] = two.parts(steps[i]);
+  }
+  const int upto = inclusive_sum(mine, lane) * a.n_kv;
+  int at = upto - mine * a.n_kv;
+  const uint32_t hit = __ballot_sync(kFullMask, at <= cta && cta < upto);
+  if (!hit) return false;
+  const int from = __ffs(hit) - 1;
+  // (which of the lane's R it is matters in that lane alone)
+  int pick = 0;
+#pragma unroll
+  for (int i = 0; i + 1 < R; ++i)
+    if (pick == i && cta >= at + n[i] * a.n_kv) {
+      at += n[i] * a.n_kv;
+      ++pick;
+    }
+#pragma unroll
+  for (int i = 1; i < R; ++i)
+    if (pick == i) {
+      ctx[0] = ctx[i];
+      steps[0] = steps[i];
+      n[0] = n[i];
+    }
+  r.b = from * R + __shfl_sync(kFullMask, pick, from);
+  r.ctx = __shfl_sync(kFullMask, ctx[0], from);
+  r.steps = __shfl_sync(kFullMask, steps[0], from);
+  r.parts = __shfl_sync(kFullMask, n[0], from);
+  r.first = __shfl_sync(kFullMask, at, from);
+  return true;
+}
+
+// Finds CTA blockIdx.x's part.  Called by every thread: up to 128 sequences are
+// looked at by every warp in its lanes, without a barrier; more by all threads, a
+// run each.
 template <int W>
 __device__ __forceinline__ Part find_part(const Attn4Params &p, int BS) {
   __shared__ int sums[3][W], got[6];
   const AttnParams &a = p.a;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, cta = blockIdx.x;
   Part r;
-  Cut one, two;
-  if (a.B <= 32) {
-    int ctx = 0, steps = 0;
-    if (lane < a.B) steps = unit_steps(a, BS, lane, ctx);
-    choose_cuts<W>(p, __reduce_add_sync(kFullMask, steps) * a.n_kv, one, two);
-    int n = one.parts(steps);
-    if (!p.splits && __reduce_add_sync(kFullMask, n) * a.n_kv > p.resident) n = two.parts(steps);
-    const int upto = inclusive_sum(n, lane) * a.n_kv, at = upto - n * a.n_kv;
-    const uint32_t hit = __ballot_sync(kFullMask, at <= cta && cta < upto);
-    r.some = hit != 0;
-    if (!hit) return r;
-    r.b = __ffs(hit) - 1;
-    r.ctx = __shfl_sync(kFullMask, ctx, r.b);
-    r.steps = __shfl_sync(kFullMask, steps, r.b);
-    r.parts = __shfl_sync(kFullMask, n, r.b);
-    r.first = __shfl_sync(kFullMask, at, r.b);
+  if (a.B <= 128) {
+    r.some = a.B <= 32 ? find_in_lanes<1, W>(p, BS, r) : find_in_lanes<4, W>(p, BS, r);
+    if (!r.some) return r;
   } else {
+    Cut one, two;
     const int run = (a.B + 32 * W - 1) / (32 * W);
     const int b0 = threadIdx.x * run, b1 = min(a.B, b0 + run);
     int ctx, sum = 0;
