@@ -35,12 +35,16 @@
 // and end lie beside another's stream.  A CTA's warps take its steps in turn and
 // merge their states in shared memory; parts of a unit go through the
 // workspace, merged by the CTA that finishes last, in the order of the parts.
+// Few units of long contexts take CTAs of 16 warps and one an SM: fewer parts to
+// merge.  Few units of short contexts take a cluster of CTAs each, whose states
+// go from shared memory to shared memory.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
 #include <atomic>
 
+#include "cluster.cuh"
 #include "kv_fp4.cuh"
 
 namespace pgd {
@@ -52,7 +56,7 @@ constexpr int kStages = 3;
 constexpr int kHeads = 8;              // query heads a product takes
 constexpr int kMergeRow = kHeadDim + 4;  // floats between heads when states are merged
 // Units of no more steps than this are not cut: a part's way through the workspace
-// takes longer than three steps of a warp (4 contexts of 217 tokens: 3.9 us whole,
+// takes longer than three steps of a warp (4 contexts of 217 tokens: 4.1 us whole,
 // 5.8 in two parts).
 constexpr int kWholeSteps = 12;
 constexpr int kManySteps = 25;          // steps a warp from which three CTAs follow one another
@@ -107,10 +111,10 @@ __device__ __forceinline__ uint32_t times(uint32_t a, __half2 s) {
 }
 
 // Steps of a sequence's units (0: a bad context).
-__device__ __forceinline__ int unit_steps(const AttnParams &a, int BS, int b, int &ctx) {
+__device__ __forceinline__ int unit_steps(const AttnParams &a, int BS, int b, int &ctx, bool tell) {
   ctx = __ldg(a.ctx + b);
   if (ctx < 1 || ctx > a.MB * BS) {
-    if (blockIdx.x == 0) atomicOr(a.err, PGD_DEVERR_BAD_CONTEXT);
+    if (tell) atomicOr(a.err, PGD_DEVERR_BAD_CONTEXT);
     return 0;
   }
   return (ctx - 1) / kStepTokens + 1;
@@ -170,7 +174,7 @@ __device__ __forceinline__ bool find_in_lanes(const Attn4Params &p, int BS, Part
 #pragma unroll
   for (int i = 0; i < R; ++i) {
     ctx[i] = steps[i] = 0;
-    if (lane * R + i < a.B) steps[i] = unit_steps(a, BS, lane * R + i, ctx[i]);
+    if (lane * R + i < a.B) steps[i] = unit_steps(a, BS, lane * R + i, ctx[i], cta == 0);
     sum += steps[i];
   }
   Cut one, two;
@@ -228,7 +232,7 @@ __device__ __forceinline__ Part find_part(const Attn4Params &p, int BS) {
     const int run = (a.B + 32 * W - 1) / (32 * W);
     const int b0 = threadIdx.x * run, b1 = min(a.B, b0 + run);
     int ctx, sum = 0;
-    for (int b = b0; b < b1; ++b) sum += unit_steps(a, BS, b, ctx);
+    for (int b = b0; b < b1; ++b) sum += unit_steps(a, BS, b, ctx, cta == 0);
     sum = __reduce_add_sync(kFullMask, sum);
     if (lane == 0) sums[0][warp] = sum;
     if (threadIdx.x == 0) got[5] = 0;
@@ -239,7 +243,7 @@ __device__ __forceinline__ Part find_part(const Attn4Params &p, int BS) {
     choose_cuts<W>(p, all * a.n_kv, one, two);
     int n1 = 0, n2 = 0;
     for (int b = b0; b < b1; ++b) {
-      const int steps = unit_steps(a, BS, b, ctx);
+      const int steps = unit_steps(a, BS, b, ctx, cta == 0);
       n1 += one.parts(steps);
       n2 += two.parts(steps);
     }
@@ -263,7 +267,7 @@ __device__ __forceinline__ Part find_part(const Attn4Params &p, int BS) {
     int at = upto - (first ? n1 : n2) * a.n_kv;
     if (at <= cta && cta < upto)  // (one thread at most)
       for (int b = b0; b < b1; ++b) {
-        const int steps = unit_steps(a, BS, b, ctx);
+        const int steps = unit_steps(a, BS, b, ctx, cta == 0);
         const int n = first ? one.parts(steps) : two.parts(steps);
         upto = at + n * a.n_kv;
         if (cta < upto) {
@@ -596,6 +600,68 @@ struct Worker {
   }
 };
 
+// The states of a CTA's warps on one reference a head, in their rings.
+template <int W>
+struct Sums {
+  const float *refs, *totals;  // [W][8]
+  __device__ __forceinline__ float reference(int h) const {
+    float M = refs[h];
+#pragma unroll
+    for (int j = 1; j < W; ++j) M = fmaxf(M, refs[j * kHeads + h]);
+    return M;
+  }
+  // Outputs i, i + 1 of [G][128] (i even), and their head's sum.
+  __device__ __forceinline__ float2 dims(const unsigned char *smem, int i, float &total) const {
+    const float *src = reinterpret_cast<const float *>(smem) + (i >> 7) * kMergeRow + (i & 127);
+    float2 acc = make_float2(0.f, 0.f);
+    total = 0.f;
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+      const float2 v = *reinterpret_cast<const float2 *>(src + j * (kStages * kStepBytes / 4));
+      total += totals[j * kHeads + (i >> 7)];
+      acc.x += v.x;
+      acc.y += v.y;
+    }
+    return acc;
+  }
+};
+
+// Called by every thread; refs: [2][W][8] floats.
+template <int BS, int W>
+__device__ __forceinline__ Sums<W> merge_warps(const Worker<BS, W> &w, float *refs) {
+  float *totals = refs + W * kHeads;
+  float l0 = w.l0, l1 = w.l1;
+#pragma unroll
+  for (int i = 4; i < 32; i <<= 1) {
+    l0 += __shfl_xor_sync(kFullMask, l0, i);
+    l1 += __shfl_xor_sync(kFullMask, l1, i);
+  }
+  const int mine_at = w.warp * kHeads + 2 * w.t4;
+  if (w.g == 0) *reinterpret_cast<float2 *>(refs + mine_at) = make_float2(w.m0, w.m1);
+  __syncthreads();  // the rings are done with, the references written
+  float M0 = w.m0, M1 = w.m1;
+#pragma unroll
+  for (int i = 0; i < W; ++i) {
+    const float2 m = *reinterpret_cast<const float2 *>(refs + i * kHeads + 2 * w.t4);
+    M0 = fmaxf(M0, m.x);
+    M1 = fmaxf(M1, m.y);
+  }
+  const float none = __uint_as_float(0xff800000u);  // (a warp without steps has no weight)
+  const float r0 = w.m0 == none ? 0.f : exp2_approx(w.m0 - M0);
+  const float r1 = w.m1 == none ? 0.f : exp2_approx(w.m1 - M1);
+  if (w.g == 0) *reinterpret_cast<float2 *>(totals + mine_at) = make_float2(l0 * r0, l1 * r1);
+  float *mine = reinterpret_cast<float *>(w.ring) + 2 * w.t4 * kMergeRow + w.g;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    mine[16 * i] = w.o[i][0] * r0;
+    mine[16 * i + kMergeRow] = w.o[i][1] * r1;
+    mine[16 * i + 8] = w.o[i][2] * r0;
+    mine[16 * i + 8 + kMergeRow] = w.o[i][3] * r1;
+  }
+  __syncthreads();
+  return {refs, totals};
+}
+
 __device__ __forceinline__ void store_row(__nv_bfloat16 *at, float4 v, float f) {
   const __nv_bfloat162 y0 = __floats2bfloat162_rn(v.x * f, v.y * f);
   const __nv_bfloat162 y1 = __floats2bfloat162_rn(v.z * f, v.w * f);
@@ -688,9 +754,8 @@ __global__ void __launch_bounds__(W * 32, kResident<W>)
     attention_fp4_kernel(const Attn4Params p, int G) {
   extern __shared__ __align__(128) unsigned char smem[];
   float *refs = reinterpret_cast<float *>(smem + ring_bytes<W>());  // [W][8] warps' references
-  float *sums = refs + W * kHeads;                                  // [W][8] and sums
-  int *flag = reinterpret_cast<int *>(sums + W * kHeads);
-  const int tid = threadIdx.x, warp = tid >> 5;
+  int *flag = reinterpret_cast<int *>(refs + 2 * W * kHeads);
+  const int tid = threadIdx.x;
   const AttnParams &a = p.a;
 
   if (!a.wait_late) pdl_wait();
@@ -701,36 +766,7 @@ __global__ void __launch_bounds__(W * 32, kResident<W>)
   Worker<BS, W> w(p, smem);
   w.run(u, G);
 
-  // ---- the warps' states, merged
-  float l0 = w.l0, l1 = w.l1;
-#pragma unroll
-  for (int i = 4; i < 32; i <<= 1) {
-    l0 += __shfl_xor_sync(kFullMask, l0, i);
-    l1 += __shfl_xor_sync(kFullMask, l1, i);
-  }
-  if (w.g == 0) *reinterpret_cast<float2 *>(refs + warp * kHeads + 2 * w.t4) = make_float2(w.m0, w.m1);
-  __syncthreads();  // the rings are done with, the references written
-  float M0 = w.m0, M1 = w.m1;
-#pragma unroll
-  for (int i = 0; i < W; ++i) {
-    const float2 m = *reinterpret_cast<const float2 *>(refs + i * kHeads + 2 * w.t4);
-    M0 = fmaxf(M0, m.x);
-    M1 = fmaxf(M1, m.y);
-  }
-  {
-    const float r0 = exp2_approx(w.m0 - M0), r1 = exp2_approx(w.m1 - M1);
-    if (w.g == 0)
-      *reinterpret_cast<float2 *>(sums + warp * kHeads + 2 * w.t4) = make_float2(l0 * r0, l1 * r1);
-    float *mine = reinterpret_cast<float *>(w.ring) + 2 * w.t4 * kMergeRow + w.g;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      mine[16 * i] = w.o[i][0] * r0;
-      mine[16 * i + kMergeRow] = w.o[i][1] * r1;
-      mine[16 * i + 8] = w.o[i][2] * r0;
-      mine[16 * i + 8 + kMergeRow] = w.o[i][3] * r1;
-    }
-  }
-  __syncthreads();
+  const Sums<W> sums = merge_warps(w, refs);
   const bool whole = u.parts == 1;
   const int unit = u.b * a.n_kv + u.h;
   const size_t slot = blockIdx.x;
@@ -738,25 +774,15 @@ __global__ void __launch_bounds__(W * 32, kResident<W>)
   // two dims of a head a thread
   for (int i = 2 * tid; i < G * kHeadDim; i += 64 * W) {
     const int h = i >> 7;
-    const float *src = reinterpret_cast<const float *>(smem) + h * kMergeRow + (i & 127);
-    float L = 0.f;
-    float2 acc = make_float2(0.f, 0.f);
-#pragma unroll
-    for (int j = 0; j < W; ++j) {
-      const float2 v = *reinterpret_cast<const float2 *>(src + j * (kStages * kStepBytes / 4));
-      L += sums[j * kHeads + h];
-      acc.x += v.x;
-      acc.y += v.y;
-    }
+    float L;
+    const float2 acc = sums.dims(smem, i, L);
     if (whole) {
       const float inv = p.v_scale / L;
       *reinterpret_cast<__nv_bfloat162 *>(out + i) = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
     } else {
       *reinterpret_cast<float2 *>(a.part_o + slot * G * kHeadDim + i) = acc;
       if ((i & 127) == 0) {
-        float M = refs[h];
-#pragma unroll
-        for (int j = 1; j < W; ++j) M = fmaxf(M, refs[j * kHeads + h]);
+        const float M = sums.reference(h);
         *reinterpret_cast<float2 *>(a.part_ml + (slot * G + h) * 2) = make_float2(M, L);
       }
     }
@@ -770,6 +796,84 @@ __global__ void __launch_bounds__(W * 32, kResident<W>)
   }
   __syncthreads();
   if (*flag) merge_parts<W>(p, G, (size_t)u.first + u.h, u.parts, out, smem);
+}
+
+// Short contexts of few units: a cluster of CL CTAs a unit, each with an equal
+// share of its steps.  Which unit and steps a CTA has follows from its place and
+// one length, and the states go to the cluster's CTAs on their barriers, each CTA
+// merging 128 / CL dims: no scan of the lengths, nothing through the workspace.
+// (One context of 512 tokens: 3.3 us, through the workspace 5.1; of 2048: 4.0 and
+// 5.8.)
+constexpr int kClusterWarps = 4;
+
+template <int BS, int CL>
+__global__ void __launch_bounds__(kClusterWarps * 32)
+    attention_fp4_cluster_kernel(const Attn4Params p, int G) {
+  constexpr int W = kClusterWarps, kDims = kHeadDim / CL;
+  extern __shared__ __align__(128) unsigned char smem[];
+  float *refs = reinterpret_cast<float *>(smem + ring_bytes<W>());  // [2][W][8]
+  __shared__ __align__(16) float in_o[CL][kHeads][kDims];
+  __shared__ __align__(16) float2 in_ml[CL][kHeads];
+  __shared__ __align__(8) uint64_t arrived;
+  const AttnParams &a = p.a;
+  const int tid = threadIdx.x, rank = blockIdx.x % CL, unit = blockIdx.x / CL;
+  if (tid == 0) {
+    mbar_init(&arrived, 1);
+    mbar_init_fence();
+    mbar_arrive_expect_tx(&arrived, (uint32_t)(CL * G * (kDims * 4 + 8)));
+  }
+  // (every CTA of the cluster has its barrier: waited for before the first store)
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  if (!a.wait_late) pdl_wait();
+  pdl_launch_dependents();
+  Part u;
+  u.b = unit / a.n_kv;
+  u.h = unit - u.b * a.n_kv;
+  u.steps = unit_steps(a, BS, u.b, u.ctx, rank == 0 && u.h == 0);
+  u.i0 = u.steps * rank / CL;
+  u.i1 = u.steps * (rank + 1) / CL;
+  if (a.wait_late) pdl_wait();
+  if (u.steps == 0) {  // (a bad context: the whole cluster leaves)
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    return;
+  }
+  Worker<BS, W> w(p, smem);
+  w.run(u, G);
+  const Sums<W> sums = merge_warps(w, refs);
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  for (int i = 2 * tid; i < G * kHeadDim; i += 64 * W) {
+    const int h = i >> 7, to = (i & 127) / kDims, d = i % kDims;
+    float L;
+    const float2 acc = sums.dims(smem, i, L);
+    send8(&in_o[rank][h][d], &arrived, (uint32_t)to, __float_as_uint(acc.x),
+          __float_as_uint(acc.y));
+    if (d == 0)
+      send8(&in_ml[rank][h], &arrived, (uint32_t)to, __float_as_uint(sums.reference(h)),
+            __float_as_uint(L));
+  }
+  if (tid >= G * kDims) return;
+  if (!wait_for_peers(&arrived, 0)) {
+    atomicOr(a.err, PGD_DEVERR_TIMEOUT);
+    wait_to_leave();
+    return;
+  }
+  for (int i = tid; i < G * kDims; i += 32 * W) {
+    const int h = i / kDims, d = i % kDims;
+    float M = in_ml[0][h].x;
+#pragma unroll
+    for (int k = 1; k < CL; ++k) M = fmaxf(M, in_ml[k][h].x);
+    float num = 0.f, L = 0.f;
+#pragma unroll
+    for (int k = 0; k < CL; ++k) {
+      // (a CTA without steps has no weight)
+      const float x = in_ml[k][h].x;
+      const float r = x == __uint_as_float(0xff800000u) ? 0.f : exp2_approx(x - M);
+      num = fmaf(r, in_o[k][h][d], num);
+      L = fmaf(r, in_ml[k][h].y, L);
+    }
+    a.out[((size_t)u.b * a.n_q + (size_t)u.h * G + h) * kHeadDim + rank * kDims + d] =
+        __float2bfloat16_rn(num * (p.v_scale / L));
+  }
 }
 
 template <int BS, int W>
@@ -802,7 +906,55 @@ cudaError_t launch_kernel(const Attn4Params &p, int G, int grid, cudaStream_t st
   return cudaLaunchKernelEx(&cfg, kernel, p, G);
 }
 
+template <int BS, int CL>
+cudaError_t launch_cluster(const Attn4Params &p, int G, cudaStream_t stream) {
+  static std::atomic<bool> set[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  auto kernel = attention_fp4_cluster_kernel<BS, CL>;
+  constexpr size_t smem = ring_bytes<kClusterWarps>() + 2 * kClusterWarps * kHeads * 4;
+  if (!set[dev].load()) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e == cudaSuccess && CL > 8)
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    set[dev].store(true);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(p.a.B * p.a.n_kv * CL));
+  cfg.blockDim = dim3(kClusterWarps * 32);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = CL;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, p, G);
+}
+
 }  // namespace
+
+// CTAs a cluster for units whose tables hold `tokens`, or 0: parts through the
+// workspace.  Equal shares of short contexts are worth more than parts of equal
+// size as long as all clusters run at once and are small (us, cluster / workspace):
+//   16 CTAs  8 x 8192: 7.0 / 8.7, 1 x 4096: 5.0 / 6.5 (8 CTAs: 5.4); 8 x 16384: 11.0 / 9.6;
+//   8 CTAs   1 x 512: 3.2 / 5.1, 32 x 1024: 5.2 / 6.8, 32 x 4096: 9.1 / 11.9,
+//            32 x 8192: 14.0 / 16.2; 32 x 256: 4.5 / 4.2; 64 x 2048: 10.8 / 9.0;
+//   4 CTAs   100 x 1000: 6.3 / 9.4, 64 x 512: 4.6 / 5.8, 64 x 2048: 8.2 / 9.1;
+//            64 x 128: 3.8 / 3.4, 112 x 2300: 15.9 / 14.0, 136 x 1000: 11.9 / 10.9.
+static int cluster_of(long long units, long long tokens, int sms) {
+  if (tokens > 8192) return 0;
+  if (16 * units <= sms && tokens > 1024) return 16;
+  if (4 * units <= sms) return 8;
+  if (4 * units <= 3 * sms && tokens > 384 && units * tokens <= 1 << 17) return 4;
+  return 0;
+}
 
 // 4 warps a CTA, four CTAs an SM, or 16 and one.  16 for long contexts of so few
 // units that smaller parts are many to merge (one context of 131072 tokens, 8
@@ -837,10 +989,17 @@ long long attention_fp4_grid(long long units, long long tokens, int sms) {
 cudaError_t attention_fp4_launch(const Attn4Params &p_in, int G, int bs, int grid, int sms,
                                  cudaStream_t stream) {
   Attn4Params p = p_in;
-  const int W = warps_of((long long)p.a.B * p.a.n_kv, (long long)p.a.MB * bs, sms);
-  const long long units = (long long)p.a.B * p.a.n_kv;
+  const long long units = (long long)p.a.B * p.a.n_kv, tokens = (long long)p.a.MB * bs;
+  const int CL = p.splits ? 0 : cluster_of(units, tokens, sms);
+  if (CL == 16)
+    return bs == 16 ? launch_cluster<16, 16>(p, G, stream) : launch_cluster<32, 16>(p, G, stream);
+  if (CL == 8)
+    return bs == 16 ? launch_cluster<16, 8>(p, G, stream) : launch_cluster<32, 8>(p, G, stream);
+  if (CL == 4)
+    return bs == 16 ? launch_cluster<16, 4>(p, G, stream) : launch_cluster<32, 4>(p, G, stream);
+  const int W = warps_of(units, tokens, sms);
   p.resident = (int)resident_ctas(W, sms);
-  p.least_steps = least_steps(units, (long long)p.a.MB * bs, sms);
+  p.least_steps = least_steps(units, tokens, sms);
   p.inv_resident = 1.f / (float)p.resident;
   p.uneven = 8 * units > p.resident;
   // ceil(steps / size) over the units is at most all / size + units; more units

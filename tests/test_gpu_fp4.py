@@ -227,6 +227,164 @@ def test_attention(case, num_splits):
     assert not ws.view(torch.int32)[:65536].any()  # (the counters)
 
 
+def _over_few_blocks(ctx, n_kv, bs, blocks=64, seed=3):
+    """A cache whose sequences read the same few blocks, each from a place of its own, over and over."""
+    c = fp4.Cache([blocks * bs], n_kv, bs, seed=seed)
+    r = np.random.default_rng(seed)
+    MB = -(-max(ctx) // bs)
+    held = c.tables[0, :blocks]
+    c.tables = np.stack([held[(np.arange(MB) + r.integers(blocks)) % blocks] for _ in ctx])
+    c.ctx = list(ctx)
+    return c
+
+
+PATHS = [  # (n_q, n_kv, bs, sequences, shortest, longest context)
+    (8, 1, 16, 1, 1025, 1025), (18, 9, 32, 1, 8192, 8192), (3, 3, 16, 3, 1, 2000),   # clusters of 16
+    (2, 2, 32, 19, 1, 40), (16, 2, 16, 19, 1, 900), (8, 1, 32, 30, 1, 5000),         # of 8
+    (8, 8, 16, 1, 1024, 1024), (20, 5, 16, 4, 129, 129),
+    (3, 3, 32, 13, 385, 500), (48, 6, 16, 19, 1, 600), (8, 2, 32, 40, 1, 1500),     # of 4
+    (40, 10, 16, 4, 30, 384), (24, 6, 16, 20, 1, 390),                               # and beside them
+    (8, 2, 16, 33, 1, 900), (4, 1, 32, 128, 1, 700), (4, 1, 16, 129, 1, 700),        # many sequences
+    (4, 2, 16, 700, 1, 90), (1, 1, 32, 2048, 1, 70),
+    (8, 1, 16, 1, 98000, 98000), (8, 4, 32, 2, 30000, 40000),                        # 16 warps
+    (16, 8, 16, 15, 1500, 2700), (19, 19, 32, 8, 2500, 2600),                        # and whole units
+    (32, 4, 16, 20, 20000, 46000), (10, 10, 32, 31, 20000, 21000),                    # three waves
+]
+
+
+@pytest.mark.parametrize("case", PATHS, ids=str)
+def test_attention_of_every_size(case):
+    n_q, n_kv, bs, B, lo, hi = case
+    ctx = np.random.default_rng(n_q + B).integers(lo, hi + 1, B)
+    ctx[B // 2] = hi
+    ctx[B // 3] = lo if B > 1 else hi
+    c = _over_few_blocks(ctx.tolist(), n_kv, bs)
+    k, v, tables, lens = c.cuda()
+    q = bsc.make_query(B, n_q)
+    ws = pgd.make_fp4_workspace(B, n_q, n_kv)
+    out = [torch.full((B, n_q, 128), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    for x in out:
+        pgd.paged_decode_attention_fp4(x, q.cuda(), k, v, tables, lens, SCALE, workspace=ws,
+                                       **fp4.scales_kw(c))
+    assert torch.equal(*out)
+    assert not ws.view(torch.int32)[:65536].any()  # (the counters)
+    x = bsc.f64(out[0])
+    some = sorted({0, B // 3, B // 2, B - 1} | set(range(0, B, max(1, B // 20)) if hi < 3000 else []))
+    for b in some:
+        n = int(ctx[b])
+        want, tol = fp4.bound(bsc.f64(q[b]), c.rows(0, b, n), c.rows(1, b, n), SCALE)
+        err = np.abs(x[b] - want) / tol
+        assert np.isfinite(err).all() and err.max() <= 1, (b, n, err.max())
+
+
+@pytest.mark.parametrize("ctx", [[5, 3000], [700, 40, 1]], ids=str)
+def test_a_table_much_wider_than_its_contexts(ctx):
+    """Also contexts beside a table of more entries, none of which is read (they hold no ids)."""
+    for G in (1, 4, 8):
+        c = fp4.Cache(ctx, 2, 16, seed=4 + G)
+        k, v, tables, lens = c.cuda()
+        wide = torch.full((len(ctx), 9000), 2 ** 31 - 1, dtype=torch.int32, device="cuda")
+        wide[:, :tables.shape[1]] = torch.where(tables < 0, wide[:, :tables.shape[1]], tables)
+        q = bsc.make_query(len(ctx), 2 * G)
+        want, tol = fp4.bounds_of(c, q, SCALE)
+        for t in (wide, wide[:, :tables.shape[1]].contiguous()):
+            for splits in (0, 2, 300):
+                got = pgd.paged_decode_attention_fp4(None, q.cuda(), k, v, t, lens, SCALE,
+                                                     num_splits=splits, **fp4.scales_kw(c))
+                assert (np.abs(bsc.f64(got) - want) <= tol).all()
+
+
+@pytest.mark.parametrize("ctx,MB", [([33, 200], 13), ([1500, 33], 94), ([33, 700, 200], 1200)], ids=str)
+@pytest.mark.parametrize("what", ["k", "v", "q"])
+def test_nan_stays_with_its_head_and_dims(ctx, MB, what):
+    """A NaN scale of the last token of head 1 (alone in its step), or a NaN or infinity of a query,
+    reaches what the formula says and no more."""
+    G, n_kv = 2, 3
+    c = fp4.Cache(ctx, n_kv, 16, seed=6)
+    q = bsc.make_query(len(ctx), G * n_kv)
+    b = ctx.index(33)
+    hit = np.zeros((len(ctx), G * n_kv, 128), bool)
+    if what == "q":
+        q[b, 1, 9], q[b, 4, 77] = float("nan"), float("inf")
+        hit[b, 1] = hit[b, 4] = True
+    else:
+        i = "kv".index(what)
+        c.scales[i][c.tables[b, 2], 1, 0, 3] = 0x7F
+        if what == "k":
+            hit[b, 2:4] = True
+        else:
+            hit[b, 2:4, 48:64] = True
+    k, v, tables, lens = c.cuda()
+    t = torch.full((len(ctx), MB), -1, dtype=torch.int32, device="cuda")
+    t[:, :tables.shape[1]] = tables
+    with np.errstate(invalid="ignore"):
+        want, tol = fp4.bounds_of(c, q, SCALE)
+    for splits in (0, 1, 2):
+        x = bsc.f64(pgd.paged_decode_attention_fp4(None, q.cuda(), k, v, t, lens, SCALE,
+                                                   num_splits=splits, **fp4.scales_kw(c)))
+        assert np.isnan(x[hit]).all()
+        assert (np.abs(x - want) <= tol)[~hit].all()
+
+
+@pytest.mark.parametrize("MB", [60, 900])
+def test_captured_and_on_two_streams(MB):
+    """Captured calls of two shapes on two streams at once, replayed over new contents and lengths."""
+    sides = []
+    for n_kv, ctx in [(1, [400, 900]), (6, [30, 800, 1, 64, 950, 333, 17])]:
+        c = fp4.Cache(ctx, n_kv, 16, seed=n_kv)
+        k, v, tables, lens = c.cuda()
+        t = torch.full((len(ctx), MB), -1, dtype=torch.int32, device="cuda")
+        t[:, :tables.shape[1]] = tables
+        q = bsc.make_query(len(ctx), 4 * n_kv)
+        stream = torch.cuda.Stream()
+        qd, out = q.cuda(), torch.zeros(q.shape, dtype=torch.bfloat16, device="cuda")
+        ws = pgd.make_fp4_workspace(len(ctx), 4 * n_kv, n_kv)
+        call = lambda a=(out, qd, k, v, t, lens, SCALE), w=ws, kw=fp4.scales_kw(c): (  # noqa: E731
+            pgd.paged_decode_attention_fp4(*a, workspace=w, **kw))
+        torch.cuda.synchronize()
+        with torch.cuda.stream(stream):
+            call()
+            graph = torch.cuda.CUDAGraph()
+            stream.synchronize()
+            with torch.cuda.graph(graph, stream=stream):
+                call()
+                call()
+        sides.append((c, q, qd, lens, out, stream, graph))
+    for turn in range(3):
+        for c, q, qd, lens, out, stream, graph in sides:
+            out.fill_(3.0)
+            if turn:
+                q.copy_(bsc.make_query(*q.shape[:2], std=0.5 * turn))
+                qd.copy_(q)
+                c.ctx = [max(1, n - 5) for n in c.ctx]
+                lens.copy_(torch.tensor(c.ctx, dtype=torch.int32))
+        torch.cuda.synchronize()
+        for _ in range(5):
+            for *_, stream, graph in sides:
+                with torch.cuda.stream(stream):
+                    graph.replay()
+        torch.cuda.synchronize()
+        for c, q, qd, lens, out, stream, graph in sides:
+            want, tol = fp4.bounds_of(c, q, SCALE)
+            assert (np.abs(bsc.f64(out) - want) <= tol).all()
+
+
+@pytest.mark.parametrize("n_kv,ctx", [(1, [1100]), (8, [900, 1]), (5, [500] * 20), (8, [40, 7] * 40)],
+                         ids=str)
+def test_append_then_attend_of_every_size(n_kv, ctx):
+    c = fp4.Cache(ctx, n_kv, 16, seed=n_kv)
+    k, v, tables, lens = c.cuda()
+    B = len(ctx)
+    new = [_rows(B, n_kv, 40 + i) for i in range(2)]
+    q = bsc.make_query(B, 2 * n_kv)
+    got = pgd.append_decode_attention_fp4(None, q.cuda(), new[0].cuda(), new[1].cuda(), k, v, tables,
+                                          lens, SCALE, **fp4.scales_kw(c))
+    c.append(*new, [n - 1 for n in ctx], list(range(B + 1)))
+    _same(c, k, v)
+    want, tol = fp4.bounds_of(c, q, SCALE)
+    assert (np.abs(bsc.f64(got) - want) <= tol).all()
+
+
 @pytest.mark.parametrize("std", [1e-30, 2.0 ** -60, 40.0])
 def test_queries_of_any_size(std):
     """Scores next to zero, and scores whose softmax is one token's."""
