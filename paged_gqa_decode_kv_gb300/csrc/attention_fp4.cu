@@ -36,8 +36,8 @@
 // merge their states in shared memory; parts of a unit go through the
 // workspace, merged by the CTA that finishes last, in the order of the parts.
 // Few units of long contexts take CTAs of 16 warps and one an SM: fewer parts to
-// merge.  Few units of short contexts take a cluster of CTAs each, whose states
-// go from shared memory to shared memory.
+// merge.  Where tables are short a unit has a CTA or a cluster of its own
+// (shape_of).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -798,18 +798,15 @@ __global__ void __launch_bounds__(W * 32, kResident<W>)
   if (*flag) merge_parts<W>(p, G, (size_t)u.first + u.h, u.parts, out, smem);
 }
 
-// Short contexts of few units: a cluster of CL CTAs a unit, each with an equal
-// share of its steps.  Which unit and steps a CTA has follows from its place and
-// one length, and the states go to the cluster's CTAs on their barriers, each CTA
-// merging 128 / CL dims: no scan of the lengths, nothing through the workspace.
-// (One context of 512 tokens: 3.3 us, through the workspace 5.1; of 2048: 4.0 and
-// 5.8.)
-constexpr int kClusterWarps = 4;
-
-template <int BS, int CL>
-__global__ void __launch_bounds__(kClusterWarps * 32)
-    attention_fp4_cluster_kernel(const Attn4Params p, int G) {
-  constexpr int W = kClusterWarps, kDims = kHeadDim / CL;
+// Units with CTAs of their own: a cluster of CL, each with an equal share of the
+// unit's steps, or one of W warps.  Which unit and steps a CTA has follows from its
+// place and one length: no scan of the lengths, nothing through the workspace.  The
+// states of a cluster go to its CTAs' shared memory on their barriers, each CTA
+// merging 128 / CL dims.
+template <int BS, int CL, int W>
+__global__ void __launch_bounds__(W * 32)
+    attention_fp4_unit_kernel(const Attn4Params p, int G) {
+  constexpr int kDims = kHeadDim / CL;
   extern __shared__ __align__(128) unsigned char smem[];
   float *refs = reinterpret_cast<float *>(smem + ring_bytes<W>());  // [2][W][8]
   __shared__ __align__(16) float in_o[CL][kHeads][kDims];
@@ -817,13 +814,13 @@ __global__ void __launch_bounds__(kClusterWarps * 32)
   __shared__ __align__(8) uint64_t arrived;
   const AttnParams &a = p.a;
   const int tid = threadIdx.x, rank = blockIdx.x % CL, unit = blockIdx.x / CL;
-  if (tid == 0) {
+  if (CL > 1 && tid == 0) {
     mbar_init(&arrived, 1);
     mbar_init_fence();
     mbar_arrive_expect_tx(&arrived, (uint32_t)(CL * G * (kDims * 4 + 8)));
   }
   // (every CTA of the cluster has its barrier: waited for before the first store)
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  if (CL > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   if (!a.wait_late) pdl_wait();
   pdl_launch_dependents();
   Part u;
@@ -834,12 +831,22 @@ __global__ void __launch_bounds__(kClusterWarps * 32)
   u.i1 = u.steps * (rank + 1) / CL;
   if (a.wait_late) pdl_wait();
   if (u.steps == 0) {  // (a bad context: the whole cluster leaves)
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (CL > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     return;
   }
   Worker<BS, W> w(p, smem);
   w.run(u, G);
   const Sums<W> sums = merge_warps(w, refs);
+  __nv_bfloat16 *out = a.out + ((size_t)u.b * a.n_q + (size_t)u.h * G) * kHeadDim;
+  if constexpr (CL == 1) {
+    for (int i = 2 * tid; i < G * kHeadDim; i += 64 * W) {
+      float L;
+      const float2 acc = sums.dims(smem, i, L);
+      const float f = p.v_scale / L;
+      *reinterpret_cast<__nv_bfloat162 *>(out + i) = __floats2bfloat162_rn(acc.x * f, acc.y * f);
+    }
+    return;
+  }
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   for (int i = 2 * tid; i < G * kHeadDim; i += 64 * W) {
     const int h = i >> 7, to = (i & 127) / kDims, d = i % kDims;
@@ -871,8 +878,7 @@ __global__ void __launch_bounds__(kClusterWarps * 32)
       num = fmaf(r, in_o[k][h][d], num);
       L = fmaf(r, in_ml[k][h].y, L);
     }
-    a.out[((size_t)u.b * a.n_q + (size_t)u.h * G + h) * kHeadDim + rank * kDims + d] =
-        __float2bfloat16_rn(num * (p.v_scale / L));
+    out[h * kHeadDim + rank * kDims + d] = __float2bfloat16_rn(num * (p.v_scale / L));
   }
 }
 
@@ -906,15 +912,15 @@ cudaError_t launch_kernel(const Attn4Params &p, int G, int grid, cudaStream_t st
   return cudaLaunchKernelEx(&cfg, kernel, p, G);
 }
 
-template <int BS, int CL>
-cudaError_t launch_cluster(const Attn4Params &p, int G, cudaStream_t stream) {
+template <int BS, int CL, int W>
+cudaError_t launch_units_of(const Attn4Params &p, int G, cudaStream_t stream) {
   static std::atomic<bool> set[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  auto kernel = attention_fp4_cluster_kernel<BS, CL>;
-  constexpr size_t smem = ring_bytes<kClusterWarps>() + 2 * kClusterWarps * kHeads * 4;
+  auto kernel = attention_fp4_unit_kernel<BS, CL, W>;
+  constexpr size_t smem = ring_bytes<W>() + 2 * W * kHeads * 4;
   if (!set[dev].load()) {
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e == cudaSuccess && CL > 8)
@@ -924,7 +930,7 @@ cudaError_t launch_cluster(const Attn4Params &p, int G, cudaStream_t stream) {
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(p.a.B * p.a.n_kv * CL));
-  cfg.blockDim = dim3(kClusterWarps * 32);
+  cfg.blockDim = dim3(W * 32);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
@@ -934,38 +940,56 @@ cudaError_t launch_cluster(const Attn4Params &p, int G, cudaStream_t stream) {
   attr[1].val.clusterDim.x = CL;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
+  cfg.numAttrs = CL > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, p, G);
+}
+
+template <int CL, int W>
+cudaError_t launch_units(const Attn4Params &p, int G, int bs, cudaStream_t stream) {
+  return bs == 16 ? launch_units_of<16, CL, W>(p, G, stream)
+                  : launch_units_of<32, CL, W>(p, G, stream);
 }
 
 }  // namespace
 
-// CTAs a cluster for units whose tables hold `tokens`, or 0: parts through the
-// workspace.  Equal shares of short contexts are worth more than parts of equal
-// size as long as all clusters run at once and are small (us, cluster / workspace):
+// Which units get CTAs of their own, by the tokens that the tables hold, or none
+// (0): parts through the workspace.  Equal shares of short contexts are worth more
+// than parts of equal size while all clusters run at once and are small (us,
+// clusters / workspace):
 //   16 CTAs  8 x 8192: 7.0 / 8.7, 1 x 4096: 5.0 / 6.5 (8 CTAs: 5.4); 8 x 16384: 11.0 / 9.6;
 //   8 CTAs   1 x 512: 3.2 / 5.1, 32 x 1024: 5.2 / 6.8, 32 x 4096: 9.1 / 11.9,
 //            32 x 8192: 14.0 / 16.2; 32 x 256: 4.5 / 4.2; 64 x 2048: 10.8 / 9.0;
 //   4 CTAs   100 x 1000: 6.3 / 9.4, 64 x 512: 4.6 / 5.8, 64 x 2048: 8.2 / 9.1;
 //            64 x 128: 3.8 / 3.4, 112 x 2300: 15.9 / 14.0, 136 x 1000: 11.9 / 10.9.
-static int cluster_of(long long units, long long tokens, int sms) {
-  if (tokens > 8192) return 0;
-  if (16 * units <= sms && tokens > 1024) return 16;
-  if (4 * units <= sms) return 8;
-  if (4 * units <= 3 * sms && tokens > 384 && units * tokens <= 1 << 17) return 4;
-  return 0;
+// Where units are enough for the SMs, a CTA each takes less than parts of equal size
+// as long as the longest context is not far from the mean (whole / workspace):
+//   16 warps  136 x 500-1000: 7.8 / 10.9, 112 x 4096: 16.9 / 18.7, 152 x 1-4000: 15.9 / 15.4;
+//             76 x 1-2500: 11.1 / 9.7, 100 x 1-3000: 12.7 / 11.1, 136 x 1-8000: 25.8 / 22.3;
+//   8 warps   256 x 200-1000: 9.7 / 12.5, 304 x 2000-4000: 28.2 / 37.3; 256 x 1-4000: 26.8 / 23.8;
+//   4 warps   696 x 125-991: 16.3 / 18.6, 1024 x 1-2000: 36.7 / 39.4, 2048 x 1-2000: 60 / 71,
+//             64 x 128: 2.9 / 3.4 (16 warps 3.8); 512 x 1-8000: 82 / 63.
+struct Shape {
+  int ctas, warps;  // CTAs a unit, warps a CTA
+};
+static Shape shape_of(long long units, long long tokens, int splits, int sms) {
+  if (splits > 1) return {0, 0};
+  if (splits == 0 && tokens <= 8192) {
+    if (16 * units <= sms && tokens > 1024) return {16, 4};
+    if (4 * units <= sms) return {8, 4};
+    if (4 * units <= 3 * sms && tokens > 384 && units * tokens <= 1 << 17) return {4, 4};
+  }
+  if (splits == 0 && tokens > (3 * units > 2 * sms ? 4096 : 384)) return {0, 0};
+  return {1, tokens <= 384 || units > 2 * sms ? 4 : units > sms ? 8 : 16};
 }
 
-// 4 warps a CTA, four CTAs an SM, or 16 and one.  16 for long contexts of so few
+// 4 warps a CTA, four CTAs an SM, or 16 and one: 16 for long contexts of so few
 // units that smaller parts are many to merge (one context of 131072 tokens, 8
-// units: 30.8 us, with 4 warps 35; but 4096: 7.4 and 6.4), and where most SMs have
-// one whole unit that is not too long for the SMs without one to matter (16 x
-// 8192, 128 units: 30.1 and 32.1; x 32768: 119 and 107).
-// 32 units of 32768 tokens: 32 and 29.7; 64 of 37 thousand: 79 and 59.
+// units: 30.8 us, with 4 warps 35; but 4096: 7.4 and 6.4; 32 units of 32768
+// tokens: 32 and 29.7).  A CTA of 16 warps a unit was 6 % faster for 128 units of
+// 8192 tokens each (30.0 and 31.9), but 36 where 21.5 do for 1 to 8192 tokens.
 static int warps_of(long long units, long long tokens, int sms) {
   const long long steps = units * ((tokens - 1) / kStepTokens + 1);
-  if (units <= 16) return steps >= 20LL * sms ? 16 : 4;
-  return steps >= 64LL * sms && steps < 400LL * sms && units <= sms && 4 * units > 3 * sms ? 16 : 4;
+  return units <= 16 && steps >= 20LL * sms ? 16 : 4;
 }
 static long long resident_ctas(int W, int sms) {
   return (W == 16 ? kResident<16> : kResident<4>) * (long long)sms;
@@ -990,13 +1014,14 @@ cudaError_t attention_fp4_launch(const Attn4Params &p_in, int G, int bs, int gri
                                  cudaStream_t stream) {
   Attn4Params p = p_in;
   const long long units = (long long)p.a.B * p.a.n_kv, tokens = (long long)p.a.MB * bs;
-  const int CL = p.splits ? 0 : cluster_of(units, tokens, sms);
-  if (CL == 16)
-    return bs == 16 ? launch_cluster<16, 16>(p, G, stream) : launch_cluster<32, 16>(p, G, stream);
-  if (CL == 8)
-    return bs == 16 ? launch_cluster<16, 8>(p, G, stream) : launch_cluster<32, 8>(p, G, stream);
-  if (CL == 4)
-    return bs == 16 ? launch_cluster<16, 4>(p, G, stream) : launch_cluster<32, 4>(p, G, stream);
+  switch (const Shape x = shape_of(units, tokens, p.splits, sms); 100 * x.ctas + x.warps) {
+    case 1604: return launch_units<16, 4>(p, G, bs, stream);
+    case 804: return launch_units<8, 4>(p, G, bs, stream);
+    case 404: return launch_units<4, 4>(p, G, bs, stream);
+    case 116: return launch_units<1, 16>(p, G, bs, stream);
+    case 108: return launch_units<1, 8>(p, G, bs, stream);
+    case 104: return launch_units<1, 4>(p, G, bs, stream);
+  }
   const int W = warps_of(units, tokens, sms);
   p.resident = (int)resident_ctas(W, sms);
   p.least_steps = least_steps(units, tokens, sms);

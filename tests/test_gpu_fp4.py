@@ -239,16 +239,21 @@ def _over_few_blocks(ctx, n_kv, bs, blocks=64, seed=3):
 
 
 PATHS = [  # (n_q, n_kv, bs, sequences, shortest, longest context)
-    (8, 1, 16, 1, 1025, 1025), (18, 9, 32, 1, 8192, 8192), (3, 3, 16, 3, 1, 2000),   # clusters of 16
-    (2, 2, 32, 19, 1, 40), (16, 2, 16, 19, 1, 900), (8, 1, 32, 30, 1, 5000),         # of 8
+    # clusters of 16, of 8, of 4
+    (8, 1, 16, 1, 1025, 1025), (18, 9, 32, 1, 8192, 8192), (3, 3, 16, 3, 1, 2000),
+    (2, 2, 32, 19, 1, 40), (16, 2, 16, 19, 1, 900), (8, 1, 32, 30, 1, 5000),
     (8, 8, 16, 1, 1024, 1024), (20, 5, 16, 4, 129, 129),
-    (3, 3, 32, 13, 385, 500), (48, 6, 16, 19, 1, 600), (8, 2, 32, 40, 1, 1500),     # of 4
-    (40, 10, 16, 4, 30, 384), (24, 6, 16, 20, 1, 390),                               # and beside them
-    (8, 2, 16, 33, 1, 900), (4, 1, 32, 128, 1, 700), (4, 1, 16, 129, 1, 700),        # many sequences
-    (4, 2, 16, 700, 1, 90), (1, 1, 32, 2048, 1, 70),
-    (8, 1, 16, 1, 98000, 98000), (8, 4, 32, 2, 30000, 40000),                        # 16 warps
-    (16, 8, 16, 15, 1500, 2700), (19, 19, 32, 8, 2500, 2600),                        # and whole units
-    (32, 4, 16, 20, 20000, 46000), (10, 10, 32, 31, 20000, 21000),                    # three waves
+    (3, 3, 32, 13, 385, 500), (48, 6, 16, 19, 1, 600), (8, 2, 32, 40, 1, 1500),
+    # whole units of 4, 8 and 16 warps
+    (40, 10, 16, 4, 30, 384), (24, 6, 16, 20, 1, 380), (4, 2, 16, 700, 1, 90),
+    (1, 1, 32, 2048, 1, 70), (8, 8, 32, 40, 1, 4000),
+    (8, 8, 16, 30, 1, 2000), (16, 2, 32, 100, 1, 700), (4, 1, 16, 300, 1, 500),
+    (16, 8, 16, 15, 1500, 2700), (19, 19, 32, 8, 2500, 2600),
+    # parts through the workspace: few sequences, up to 128, more; 16 warps; three waves
+    (24, 6, 16, 12, 1, 4000), (8, 2, 16, 33, 1, 8300), (4, 1, 32, 128, 1, 5000),
+    (4, 1, 16, 129, 1, 5000), (4, 2, 16, 700, 1, 4200), (1, 1, 32, 2048, 1, 4200),
+    (8, 1, 16, 1, 98000, 98000), (8, 4, 32, 2, 30000, 40000),
+    (32, 4, 16, 20, 20000, 46000), (10, 10, 32, 31, 20000, 21000),
 ]
 
 
@@ -262,19 +267,21 @@ def test_attention_of_every_size(case):
     k, v, tables, lens = c.cuda()
     q = bsc.make_query(B, n_q)
     ws = pgd.make_fp4_workspace(B, n_q, n_kv)
-    out = [torch.full((B, n_q, 128), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
-    for x in out:
+    out = [torch.full((B, n_q, 128), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(3)]
+    for x in out[:2]:
         pgd.paged_decode_attention_fp4(x, q.cuda(), k, v, tables, lens, SCALE, workspace=ws,
                                        **fp4.scales_kw(c))
-    assert torch.equal(*out)
+    assert torch.equal(*out[:2])
     assert not ws.view(torch.int32)[:65536].any()  # (the counters)
-    x = bsc.f64(out[0])
-    some = sorted({0, B // 3, B // 2, B - 1} | set(range(0, B, max(1, B // 20)) if hi < 3000 else []))
-    for b in some:
+    pgd.paged_decode_attention_fp4(out[2], q.cuda(), k, v, tables, lens, SCALE, num_splits=1,
+                                   **fp4.scales_kw(c))
+    some = {0, B // 3, B // 2, B - 1} | set(range(0, B, max(1, B // (20 if hi < 3000 else 6))))
+    for b in sorted(some):
         n = int(ctx[b])
         want, tol = fp4.bound(bsc.f64(q[b]), c.rows(0, b, n), c.rows(1, b, n), SCALE)
-        err = np.abs(x[b] - want) / tol
-        assert np.isfinite(err).all() and err.max() <= 1, (b, n, err.max())
+        for x in (out[0], out[2]):
+            err = np.abs(bsc.f64(x[b]) - want) / tol
+            assert np.isfinite(err).all() and err.max() <= 1, (b, n, err.max())
 
 
 @pytest.mark.parametrize("ctx", [[5, 3000], [700, 40, 1]], ids=str)
