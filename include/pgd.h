@@ -656,7 +656,7 @@ pgd_status pgd_append_decode_attention_fp4(
  * q, k in that order (heads of one projection's output lie side by side).  An
  * output may be its input (same address and strides); no other overlap.
  * d a multiple of 16 up to 2048, first of 8, rotary of 16, strides of 8, rows
- * 16-byte aligned.
+ * 16-byte aligned; n_q + 2 n_kv at most 65535.
  *
  * pgd_rope_append: the same with K written into the paged bf16 cache and V copied
  * beside it (d = 128): token t at slots[t] = block * bs + slot (device int64 [T],

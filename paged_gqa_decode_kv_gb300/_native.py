@@ -1163,13 +1163,13 @@ def _prepared_sparse(out, q, k_cache, v_cache, bounds, bound_scales, block_table
 def copy_blocks(k_cache, v_cache, src_ids, dst_ids, stream=None) -> None:
     """Copy whole physical blocks src_ids[i] -> dst_ids[i] (device int32; a
     pair -1, -1 is none) of bf16 pools, or of 4-bit ones (uint8)."""
-    fp4 = k_cache.dtype == torch.uint8
+    fp4 = getattr(k_cache, "dtype", None) == torch.uint8
     _need(k_cache, torch.uint8 if fp4 else torch.bfloat16, "k_cache")
     _need(v_cache, torch.uint8 if fp4 else torch.bfloat16, "v_cache")
     _need(src_ids, torch.int32, "src_ids")
     _need(dst_ids, torch.int32, "dst_ids")
     NB, n_kv, bs, d = _cache4_dims(k_cache) if fp4 else _cache_dims(k_cache)
-    if v_cache.shape != k_cache.shape or dst_ids.shape != src_ids.shape:
+    if fp4 and (v_cache.shape != k_cache.shape or dst_ids.shape != src_ids.shape):
         raise ValueError("k_cache and v_cache, src_ids and dst_ids must have one shape")
     fn = lib().pgd_copy_blocks_fp4 if fp4 else lib().pgd_copy_blocks
     _check(fn(_ptr(k_cache), _ptr(v_cache), _ptr(src_ids), _ptr(dst_ids), src_ids.numel(), n_kv,

@@ -1820,6 +1820,10 @@ static pgd_status attention_fp4_call(void *out, const void *q, const void *k_new
                                       MB, NB, scale, num_splits);
   if (s != PGD_OK) return s;
   if ((s = check_scales4(k_scale, v_scale)) != PGD_OK) return s;
+  const float qk_scale_log2 = (float)((double)scale * k_scale * 1.4426950408889634);  // log2(e)
+  if (!isfinite(qk_scale_log2))
+    return fail(PGD_ERR_INVALID_ARG, "scale = %g times k_scale = %g", (double)scale,
+                (double)k_scale);
   if (B == 0) return ok();
   if (append) {
     if (!k_new || !v_new) return fail(PGD_ERR_INVALID_ARG, "null pointer");
@@ -1853,7 +1857,7 @@ static pgd_status attention_fp4_call(void *out, const void *q, const void *k_new
   p.a.n_kv = n_kv;
   p.a.MB = MB;
   p.a.NB = NB;
-  p.a.qk_scale_log2 = (float)((double)scale * k_scale * 1.4426950408889634);  // log2(e)
+  p.a.qk_scale_log2 = qk_scale_log2;
   p.a.counters = reinterpret_cast<int32_t *>(ws + L.counters);
   p.a.part_ml = reinterpret_cast<float *>(ws + L.part_ml);
   p.a.part_o = reinterpret_cast<float *>(ws + L.part_o);
@@ -1959,8 +1963,9 @@ pgd_status pgd_rope_frequencies(int64_t *freq_h, int32_t rotary, double base, in
 
 static pgd_status rope_call(RopeParams &p, int32_t d, cudaStream_t stream) {
   if (p.T < 0) return fail(PGD_ERR_INVALID_ARG, "T = %d", p.T);
-  if (p.n_q < 0 || p.n_kv < 0 || (long long)p.n_q + 2LL * p.n_kv > 65536)
-    return fail(PGD_ERR_INVALID_ARG, "n_q = %d, n_kv = %d", p.n_q, p.n_kv);
+  if (p.n_q < 0 || p.n_kv < 0 || (long long)p.n_q + 2LL * p.n_kv > 65535)
+    return fail(PGD_ERR_INVALID_ARG, "n_q = %d, n_kv = %d (n_q + 2 n_kv at most 65535)", p.n_q,
+                p.n_kv);
   if (d <= 0 || d % 16 || d > 2048)
     return fail(PGD_ERR_UNSUPPORTED, "d = %d (a multiple of 16 up to 2048)", d);
   if (p.rotary <= 0 || p.rotary % 16 || p.first < 0 || p.first % 8 ||

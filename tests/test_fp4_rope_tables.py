@@ -173,6 +173,7 @@ def _attend(L, append=False, **kw):
     (dict(n_q=6, n_kv=4), INVALID), (dict(n_q=32, n_kv=2), UNSUPPORTED),
     (dict(n_q=6, n_kv=2), UNSUPPORTED), (dict(d=64), UNSUPPORTED), (dict(bs=24), UNSUPPORTED),
     (dict(scale=0.0), INVALID), (dict(scale=float("inf")), INVALID), (dict(splits=-1), INVALID),
+    (dict(scale=1e38, ks=2.0 ** 32), INVALID),
     (dict(ks=1.5), INVALID), (dict(vs=0.0), INVALID), (dict(ws=None), WORKSPACE),
     (dict(ws=P + 16), WORKSPACE), (dict(wb=1000), WORKSPACE),
     (dict(B=2048, n_q=64, n_kv=64), UNSUPPORTED),
@@ -207,6 +208,7 @@ def _rope(L, **kw):
     (dict(k=P + 2), INVALID), (dict(pos=None), INVALID), (dict(f=None), INVALID),
     (dict(f=P + 4), INVALID), (dict(T=-1), INVALID), (dict(n_q=-1), INVALID),
     (dict(n_kv=-1), INVALID), (dict(n_q=70000), INVALID), (dict(d=72), UNSUPPORTED),
+    (dict(n_q=65532, n_kv=2), INVALID),
     (dict(d=0), UNSUPPORTED), (dict(d=4096), UNSUPPORTED), (dict(rotary=24), UNSUPPORTED),
     (dict(rotary=0), UNSUPPORTED), (dict(rotary=144), UNSUPPORTED), (dict(first=4), UNSUPPORTED),
     (dict(first=-8), UNSUPPORTED), (dict(first=72), UNSUPPORTED),

@@ -129,6 +129,29 @@ def test_shared_blocks_are_copied_on_growth_and_freed_at_the_last_reference():
     dev.grow([16, 16, 16, 16, 0])
 
 
+@pytest.mark.parametrize("N", [5000, 9000])
+def test_many_shared_blocks(N):
+    """300 rows, every third sharing all blocks of the row before, the last partly filled or not;
+    with few tokens and with many (the other kernel)."""
+    B, MB, NB, bs = 300, 9, 4000, 16
+    host, r = _state(B, MB, NB, bs, seed=9, most=90)
+    for b in range(2, B, 3):
+        old = -(-host.ctx[b] // bs)
+        for j in range(old):
+            host.refs[host.tables[b][j]] -= 1
+        host.ctx[b] = host.ctx[b - 1]
+        host.tables[b] = list(host.tables[b - 1])
+        for j in range(-(-host.ctx[b] // bs)):
+            host.refs[host.tables[b][j]] += 1
+    dev = Device(host, MB, N)
+    for step in range(4):
+        got = dev.grow([int(x) for x in r.integers(0, 1 + min(16, N // B), B)])
+        assert got["result"][0] == 0
+        assert sum(x >= 0 for x in got["copy_src"]) > (20 if step == 0 else -1)
+        dev.trim([int(max(0, n - x)) for n, x in zip(host.ctx, r.integers(-2, 20, B))])
+    dev.trim([0] * B)
+
+
 def test_too_few_blocks_or_too_many_tokens_change_nothing():
     host, _ = _state(4, 8, 30, 16, seed=1, most=30, used=1.0)  # no block free
     dev = Device(host, 8, 90)
