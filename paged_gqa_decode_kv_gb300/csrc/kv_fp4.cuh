@@ -93,7 +93,6 @@ struct Attn4Params {
   int least_steps;     // ... of so many steps at least
   int uneven;          // the units are so many that parts of one size do not fill these CTAs
   float inv_resident;  // 1 / resident
-  float inv_spare;     // 1 / (resident - units), or 1
 };
 long long attention_fp4_grid(long long units, long long tokens, int sms);
 cudaError_t attention_fp4_launch(const Attn4Params &p, int G, int bs, int grid, int sms,
