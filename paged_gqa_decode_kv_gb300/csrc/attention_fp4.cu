@@ -142,12 +142,12 @@ struct Cut {
 };
 // The sizes to try, the smallest first, for `all` steps, and the most parts that
 // there should be: as many as CTAs are resident at once, or three times as many
-// where a CTA has much to do.  Rounding makes them more by half a part a unit where
-// lengths differ, by one at most: the sizes are for as many parts, half the units
-// less and all the units less (which is never more than there should be, and which
-// three waves can do without, as they can without either where units are many: 1024
-// of 1 to 8000 tokens 114.3, with half of them less 116.5).  64 contexts of 128 to 32768 tokens with 512 units:
-// 203.9 us with the first size alone, 200.3; 16 x 32768: 107.7 and 103.6.
+// where a CTA has much to do.  Rounding makes them more, by half a part a unit where
+// lengths differ, by one at most: the next sizes are for half the units fewer and
+// for all the units fewer, which is never too many.  (64 contexts of 128 to 32768
+// tokens, 512 units: 203.9 us with the first size alone, 200.4; 16 x 32768: 107.7
+// and 103.6.)  Three waves of very many units keep the first: 1024 of 1 to 8000
+// tokens 114.3, with half of them fewer 116.5.
 constexpr int kSizes = 3;
 template <int W>
 __device__ __forceinline__ Cut choose_cut(const Attn4Params &p, int all, int k, int &limit) {
