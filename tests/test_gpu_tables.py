@@ -212,6 +212,28 @@ def test_trim_of_bad_and_unheld_blocks():
     dev.trim([0, 0], flags=BAD_ID)
 
 
+@pytest.mark.parametrize("n", [8, 9, 40, 511, 513, 1200])
+def test_trim_of_many_blocks(n):
+    """n blocks of a row and as many that two rows share, a bad id and one without references among
+    them; cut in two goes, the rest afterwards."""
+    host, _ = _state(3, 1300, 6000, 16, seed=n, most=0, used=0.3)
+    dev = Device(host, 1300, 50000)
+    dev.grow([16 * n, 16 * n, 0])
+    host.tables[2][:n], host.ctx[2] = host.tables[1][:n], 16 * n
+    for i in host.tables[1][:n]:
+        host.refs[i] += 1
+    host.tables[0][n - 3] = 6000
+    unheld = next(i for i, r in enumerate(host.refs) if r == 0)
+    host.tables[0][n // 2] = unheld
+    dev.tables.copy_(_i32(host.tables))
+    dev.ctx.copy_(_i32(host.ctx))
+    dev.refs.copy_(_i32(host.refs))
+    dev.trim([5, 16 * n - 40, 3], flags=BAD_ID)
+    dev.trim([0, 17, 0])
+    dev.grow([100, 0, 16 * n])
+    dev.trim([0, 0, 0])
+
+
 @pytest.mark.parametrize("N", [0, 5, 9000])
 def test_no_rows(N):
     host = fp4.Tables([], [], [0] * 40, 16)
