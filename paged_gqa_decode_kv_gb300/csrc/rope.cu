@@ -17,7 +17,9 @@
 // pairs) of one token, finds their cosines and sines itself and stays with them
 // for head after head, two 16-byte vectors a head, four heads' loads in flight:
 // no barrier, and nothing shared.  Few tokens' heads are spread over several
-// threads.
+// threads.  (A kernel of its own for K and V whose stores were whole lines of the
+// tiles, 8 tokens by 4 columns a warp, read its rows in pieces and was slower: 138
+// against 129 us for 32 thousand tokens of 48 heads.)
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -30,6 +32,12 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kInFlight = 4;  // heads
+// Heads of a thread where tokens are many.  To rows 16 (43 thousand tokens of 40
+// heads: 157.8 us, eight 164, all 159.8), into the cache eight (32 thousand tokens of
+// 48: 128.8 at slots side by side, 16 134.0; 188.9 at slots anywhere, where every
+// 16 bytes are a sector of their own, 16 219.2).
+template <bool APPEND>
+constexpr int kManyHeads = APPEND ? 8 : 16;
 
 __device__ __forceinline__ uint32_t pack(float a, float b) {
   const __nv_bfloat162 z = __floats2bfloat162_rn(a, b);
@@ -100,14 +108,14 @@ __device__ __forceinline__ void rows(const RopeParams &p, long long t, Pairs &r,
         a[i] = __ldcs(src + i * from + r.v0);
         b[i] = __ldcs(src + i * from + r.v1);
       }
-    if (r.rotary && !r.known) {  // (beside the first loads)
+    if (rotated && r.rotary && !r.known) {  // (beside the first loads)
       find_angles(p, t, threadIdx.x, r);
       r.known = true;
     }
 #pragma unroll
     for (int i = 0; i < kInFlight; ++i)
       if (h + i < n) {
-        if (r.rotary && rotated) turn<INTERLEAVED>(r, a[i], b[i]);
+        if (rotated && r.rotary) turn<INTERLEAVED>(r, a[i], b[i]);
         dst[i * to + w0] = a[i];
         dst[i * to + w1] = b[i];
       }
@@ -149,14 +157,16 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p, int 
   const int h0 = blockIdx.y * share;
   const int h1 = min(h0 + share, p.n_q + (APPEND ? 2 : 1) * p.n_kv);
   if (h0 < p.n_q)
-    rows<INTERLEAVED>(p, t, r, true, reinterpret_cast<const uint4 *>(p.q + t * p.q_row + h0 * p.q_head),
+    rows<INTERLEAVED>(p, t, r, true,
+                      reinterpret_cast<const uint4 *>(p.q + t * p.q_row + h0 * p.q_head),
                       p.q_head >> 3,
                       reinterpret_cast<uint4 *>(p.q_out + t * p.qo_row + h0 * p.qo_head),
                       p.qo_head >> 3, 1, min(h1, p.n_q) - h0);
   const int k0 = max(h0 - p.n_q, 0), k1 = min(h1 - p.n_q, p.n_kv);
   if (!APPEND) {
     if (k0 < k1)
-      rows<INTERLEAVED>(p, t, r, true, reinterpret_cast<const uint4 *>(p.k + t * p.k_row + k0 * p.k_head),
+      rows<INTERLEAVED>(p, t, r, true,
+                        reinterpret_cast<const uint4 *>(p.k + t * p.k_row + k0 * p.k_head),
                         p.k_head >> 3,
                         reinterpret_cast<uint4 *>(p.k_out + t * p.ko_row + k0 * p.ko_head),
                         p.ko_head >> 3, 1, k1 - k0);
@@ -167,13 +177,15 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p, int 
   const int s = (int)(slot - blk * p.bs);
   const long long tile = p.bs * 16LL, at = (s >> 3) * 128 + (s & 7);
   if (k0 < k1)
-    rows<INTERLEAVED>(p, t, r, true, reinterpret_cast<const uint4 *>(p.k + t * p.k_row + k0 * p.k_head),
+    rows<INTERLEAVED>(p, t, r, true,
+                      reinterpret_cast<const uint4 *>(p.k + t * p.k_row + k0 * p.k_head),
                       p.k_head >> 3,
                       reinterpret_cast<uint4 *>(p.k_cache) + (blk * p.n_kv + k0) * tile + at, tile,
                       8, k1 - k0);
   const int v0 = max(h0 - p.n_q - p.n_kv, 0), v1 = h1 - p.n_q - p.n_kv;
   if (v0 < v1)
-    rows<INTERLEAVED>(p, t, r, false, reinterpret_cast<const uint4 *>(p.v + t * p.v_row + v0 * p.v_head),
+    rows<INTERLEAVED>(p, t, r, false,
+                      reinterpret_cast<const uint4 *>(p.v + t * p.v_row + v0 * p.v_head),
                       p.v_head >> 3,
                       reinterpret_cast<uint4 *>(p.v_cache) + (blk * p.n_kv + v0) * tile + at, tile,
                       8, v1 - v0);
@@ -183,11 +195,14 @@ template <bool APPEND, bool INTERLEAVED>
 cudaError_t launch(const RopeParams &p, cudaStream_t stream) {
   const int cols = p.d >> 4, heads = p.n_q + (APPEND ? 2 : 1) * p.n_kv;
   const int y = std::max(1, std::min(kThreads / cols, p.T));
-  const long long tiles = ((long long)p.T + y - 1) / y;
-  // every token's heads in one thread a column where that fills the GPU (about
-  // 1000 threads an SM), else in as many shares as do
-  const long long want = std::max(1LL, 152LL * 1024 / (tiles * y * cols));
-  const int share = (int)std::max<long long>(1, (heads + want - 1) / want);
+  const long long tiles = ((long long)p.T + y - 1) / y, threads = tiles * y * cols;
+  // kManyHeads a thread where that makes four times the threads that are resident at
+  // once, else as many threads as twice those (15 thousand tokens of 90 heads to rows:
+  // 107 us, every thread all of them 112; 600 tokens of 72: 5.4 and, 16 a thread, 8.4)
+  const long long want = std::max(1LL, (152LL * 1024 + threads - 1) / threads);
+  constexpr int kMany = kManyHeads<APPEND>;
+  const int share =
+      threads * heads / kMany >= 152LL * 512 * 4 ? kMany : (int)((heads + want - 1) / want);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)tiles, (unsigned)((heads + share - 1) / share));
   cfg.blockDim = dim3((unsigned)cols, (unsigned)y);

@@ -165,6 +165,41 @@ def test_append_is_rope_and_kv_append():
         assert torch.equal(a.view(torch.int16), b.view(torch.int16))
 
 
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("scattered", [False, True])
+def test_many_tokens_are_few_at_a_time(interleaved, scattered):
+    """Calls that give a thread a share of many tokens' heads, against the same tokens 50 at a time;
+    padding among them."""
+    T, n_q, n_kv, bs = 9600, 62, 5, 32
+    g = torch.Generator(device="cuda").manual_seed(3)
+    qkv = torch.randn(T, n_q + 2 * n_kv, 128, generator=g, device="cuda").to(torch.bfloat16)
+    q, k, v = qkv.split([n_q, n_kv, n_kv], 1)
+    places = torch.randint(0, 2 ** 31 - 1, (T,), generator=g, device="cuda").to(torch.int32)
+    freq = pgd.rope_frequencies(96, 5000.0)
+    NB = T // bs + 2
+    slots = (torch.randperm(NB * bs, generator=g, device="cuda")[:T] if scattered else
+             torch.arange(T, device="cuda") + 5)
+    slots[::7] = -1
+    got = []
+    for step in (T, 50):
+        q_out, k_out = (torch.full((T, n, 128), 3.0, dtype=torch.bfloat16, device="cuda")
+                        for n in (n_q, n_kv))
+        q_app = torch.full_like(q_out, 3.0)
+        kc, vc = (torch.zeros(NB, n_kv, bs // 8, 16, 8, 8, dtype=torch.bfloat16, device="cuda")
+                  for _ in range(2))
+        for i in range(0, T, step):
+            at = slice(i, i + step)
+            pgd.rope(q_out[at], k_out[at], q[at], k[at], places[at], freq, interleaved, first=16)
+            pgd.rope_append(q_app[at], q[at], k[at], v[at], kc, vc, slots[at], places[at], freq,
+                            interleaved, first=16)
+        got.append((q_out, k_out, q_app, kc, vc))
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+    left_out = slots < 0
+    assert (got[0][2][left_out] == 3.0).all()
+    assert torch.equal(got[0][2][~left_out], got[0][0][~left_out])
+
+
 def test_append_flags_slots_past_the_pool():
     k_cache = torch.zeros(3, 2, 2, 16, 8, 8, dtype=torch.bfloat16, device="cuda")
     v_cache = torch.zeros_like(k_cache)
