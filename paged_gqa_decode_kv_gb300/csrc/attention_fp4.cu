@@ -59,7 +59,12 @@ constexpr int kMergeRow = kHeadDim + 4;  // floats between heads when states are
 // takes longer than three steps of a warp (4 contexts of 217 tokens: 4.1 us whole,
 // 5.8 in two parts).
 constexpr int kWholeSteps = 12;
-constexpr int kManySteps = 25;          // steps a warp from which three CTAs follow one another
+// Steps a warp from which three CTAs follow one another: fewer where the units are so
+// many that one wave cannot be cut evenly (512 units of 1 to 8000 tokens: 60 us, from
+// 40 steps 87; but 256 of 8192: 64 and 58), and none up to a unit for every fourth
+// CTA (80 of 1 to 80000: 87, in one wave 78; 128 of 1 to 60000: 101 and 97, of 32768
+// all: 103 and 105; but 256 of 1 to 40000: 111 and 150).
+constexpr int kManySteps = 40, kManyUnits = 25;
 constexpr float kMoveLog2 = 8.f;       // move the reference when exceeded by 2^8
 constexpr float kUnitLog2 = 7.f;       // a weight of the reference is 2^7
 
@@ -145,8 +150,8 @@ struct Cut {
 // where a CTA has much to do.  Rounding makes them more, by half a part a unit where
 // lengths differ, by one at most: the next sizes are for half the units fewer and
 // for all the units fewer, which is never too many.  (64 contexts of 128 to 32768
-// tokens, 512 units: 203.9 us with the first size alone, 200.4; 16 x 32768: 107.7
-// and 103.6.)  Three waves of very many units keep the first: 1024 of 1 to 8000
+// tokens, 512 units: 203.9 us with the first size alone, 200.4; 256 of 1 to 8000: 39.1
+// and 33.0.)  Three waves of very many units keep the first: 1024 of 1 to 8000
 // tokens 114.3, with half of them fewer 116.5.
 constexpr int kSizes = 3;
 template <int W>
@@ -155,7 +160,7 @@ __device__ __forceinline__ Cut choose_cut(const Attn4Params &p, int all, int k, 
   const int units = p.a.B * p.a.n_kv;
   limit = p.resident;
   float size = ceilf(x * p.inv_resident);
-  const bool waves = p.uneven && size >= (float)(W * kManySteps);
+  const bool waves = p.uneven && size >= (float)(W * (2 * units > limit ? kManyUnits : kManySteps));
   if (waves) {
     limit *= 3;
     size = ceilf(size * (1.f / 3.f));
@@ -1034,7 +1039,7 @@ cudaError_t attention_fp4_launch(const Attn4Params &p_in, int G, int bs, int gri
   p.resident = (int)resident_ctas(W, sms);
   p.least_steps = least_steps(units, tokens, sms);
   p.inv_resident = 1.f / (float)p.resident;
-  p.uneven = 8 * units > p.resident;
+  p.uneven = 4 * units > p.resident;
   if (W == 16)
     return bs == 16 ? launch_kernel<16, 16>(p, G, grid, stream)
                     : launch_kernel<32, 16>(p, G, grid, stream);

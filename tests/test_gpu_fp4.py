@@ -254,6 +254,7 @@ PATHS = [  # (n_q, n_kv, bs, sequences, shortest, longest context)
     (4, 1, 16, 129, 1, 5000), (4, 2, 16, 700, 1, 4200), (1, 1, 32, 2048, 1, 4200),
     (8, 1, 16, 1, 98000, 98000), (8, 4, 32, 2, 30000, 40000),
     (32, 4, 16, 20, 20000, 46000), (10, 10, 32, 31, 20000, 21000), (8, 8, 16, 128, 1, 20000),
+    (8, 8, 16, 24, 15000, 40000),
 ]
 
 
