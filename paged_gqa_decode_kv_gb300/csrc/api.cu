@@ -1802,11 +1802,8 @@ size_t pgd_fp4_workspace_size(int32_t B, int32_t n_q, int32_t n_kv, int32_t d,
                               int32_t num_splits) {
   if (B < 0 || n_kv <= 0 || n_q <= 0 || n_q % n_kv || d != kHeadDim || num_splits < 0) return 0;
   if ((long long)B * n_kv > kMaxBlockUnits) return 0;
-  // (tables of any width: few short contexts take the larger grid)
-  const int sms = sm_count();
-  return fp4_layout(B, n_q, n_kv, std::max(fp4_grid(B, n_kv, 1LL << 31, num_splits, sms),
-                                           num_splits ? 0 : (long long)B * n_kv + 12LL * sms))
-      .total;
+  // (tables of any width)
+  return fp4_layout(B, n_q, n_kv, fp4_grid(B, n_kv, 1LL << 31, num_splits, sm_count())).total;
 }
 
 static pgd_status attention_fp4_call(void *out, const void *q, const void *k_new,

@@ -969,7 +969,9 @@ cudaError_t launch_units(const Attn4Params &p, int G, int bs, cudaStream_t strea
 // (0): parts through the workspace.  Equal shares of short contexts are worth more
 // than parts of equal size while all clusters run at once and are small (us,
 // clusters / workspace):
-//   16 CTAs  8 x 8192: 7.0 / 8.7, 1 x 4096: 5.0 / 6.5 (8 CTAs: 5.4); 8 x 16384: 11.0 / 9.6;
+//   16 CTAs  8 x 8192: 7.0 / 8.7, 8 x 4096: 5.0 / 6.5 (8 CTAs: 5.4); 8 x 16384: 11.0 / 9.6;
+//            of 16 warps 1 x 16384: 7.6 / 9.9, 4 x 32768: 11.1 / 12.8, 6 x 16384: 7.2 / 9.3;
+//            8 x 16384: 13.8 / 9.6 (not all at once), 1 x 65536: 16.4 / 13.2;
 //   8 CTAs   1 x 512: 3.2 / 5.1, 32 x 1024: 5.2 / 6.8, 32 x 4096: 9.1 / 11.9,
 //            32 x 8192: 14.0 / 16.2; 32 x 256: 4.5 / 4.2; 64 x 2048: 10.8 / 9.0;
 //   4 CTAs   100 x 1000: 6.3 / 9.4, 64 x 512: 4.6 / 5.8, 64 x 2048: 8.2 / 9.1;
@@ -986,6 +988,7 @@ struct Shape {
 };
 static Shape shape_of(long long units, long long tokens, int splits, int sms) {
   if (splits > 1) return {0, 0};
+  if (splits == 0 && units <= 6 && tokens > 8192 && tokens <= 32768) return {16, 16};
   if (splits == 0 && tokens <= 8192) {
     if (16 * units <= sms && tokens > 1024) return {16, 4};
     if (4 * units <= sms) return {8, 4};
@@ -995,32 +998,26 @@ static Shape shape_of(long long units, long long tokens, int splits, int sms) {
   return {1, tokens <= 384 || units > 2 * sms ? 4 : units > sms ? 8 : 16};
 }
 
-// 4 warps a CTA, four CTAs an SM, or 16 and one: 16 for long contexts of so few
-// units that smaller parts are many to merge (one context of 131072 tokens, 8
-// units: 30.8 us, with 4 warps 35; but 4096: 7.4 and 6.4; 32 units of 32768
-// tokens: 32 and 29.7).  A CTA of 16 warps a unit was 6 % faster for 128 units of
-// 8192 tokens each (30.0 and 31.9), but 36 where 21.5 do for 1 to 8192 tokens.
-static int warps_of(long long units, long long tokens, int sms) {
-  const long long steps = units * ((tokens - 1) / kStepTokens + 1);
-  return units <= 16 && steps >= 20LL * sms ? 16 : 4;
-}
+// 4 warps a CTA, four CTAs an SM, or 16 and one: 16 for so few units that smaller
+// parts are many to merge (one context of 131072 tokens, 8 units: 30.8 us, with 4
+// warps 35; 1 unit of 65536: 16.2 and 37.9; but 32 units of 32768: 32 and 29.7).  A
+// CTA of 16 warps a unit was 6 % faster for 128 units of 8192 tokens each (30.0 and
+// 31.9), but 36 where 21.5 do for 1 to 8192 tokens.
+static int warps_of(long long units) { return units <= 16 ? 16 : 4; }
 static long long resident_ctas(int W, int sms) {
   return (W == 16 ? kResident<16> : kResident<4>) * (long long)sms;
 }
 
-// Steps of a part at least: a step a warp where all CTAs together are few, else
-// two, as more parts take longer to merge (one context of 512 tokens: 5.0 us with
-// 4 steps, 5.6 with 8; of 4096: 7.6 and 6.4).
-static int least_steps(long long units, long long tokens, int sms) {
-  const long long steps = (tokens - 1) / kStepTokens + 1;
-  return units * ((steps - 1) / 8 + 1) <= sms / 2 ? 4 : 8;
-}
+// Steps of a part at least: two a warp.  Where so few units have all the CTAs more
+// parts take longer to merge than they save (1 unit of 65536 tokens: 13.2 us, 16.2
+// with 8 steps; but 8 of 1000 to 20000: 9.7 and 9.1).
+static int least_steps(long long units) { return units <= 4 ? 32 : 8; }
 
 // The most CTAs of an automatic call on tables of MB * bs = tokens.
 long long attention_fp4_grid(long long units, long long tokens, int sms) {
   const long long steps = (tokens - 1) / kStepTokens + 1;
-  const long long most = units * ((steps - 1) / least_steps(units, tokens, sms) + 1);
-  return std::min(most, units + 3 * resident_ctas(warps_of(units, tokens, sms), sms));
+  const long long most = units * ((steps - 1) / least_steps(units) + 1);
+  return std::min(most, units + 3 * resident_ctas(warps_of(units), sms));
 }
 
 cudaError_t attention_fp4_launch(const Attn4Params &p_in, int G, int bs, int grid, int sms,
@@ -1029,15 +1026,16 @@ cudaError_t attention_fp4_launch(const Attn4Params &p_in, int G, int bs, int gri
   const long long units = (long long)p.a.B * p.a.n_kv, tokens = (long long)p.a.MB * bs;
   switch (const Shape x = shape_of(units, tokens, p.splits, sms); 100 * x.ctas + x.warps) {
     case 1604: return launch_units<16, 4>(p, G, bs, stream);
+    case 1616: return launch_units<16, 16>(p, G, bs, stream);
     case 804: return launch_units<8, 4>(p, G, bs, stream);
     case 404: return launch_units<4, 4>(p, G, bs, stream);
     case 116: return launch_units<1, 16>(p, G, bs, stream);
     case 108: return launch_units<1, 8>(p, G, bs, stream);
     case 104: return launch_units<1, 4>(p, G, bs, stream);
   }
-  const int W = warps_of(units, tokens, sms);
+  const int W = warps_of(units);
   p.resident = (int)resident_ctas(W, sms);
-  p.least_steps = least_steps(units, tokens, sms);
+  p.least_steps = least_steps(units);
   p.inv_resident = 1.f / (float)p.resident;
   p.uneven = 4 * units > p.resident;
   if (W == 16)
