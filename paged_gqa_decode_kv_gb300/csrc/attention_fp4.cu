@@ -980,7 +980,8 @@ cudaError_t launch_units(const Attn4Params &p, int G, int bs, cudaStream_t strea
 // as long as the longest context is not far from the mean (whole / workspace):
 //   16 warps  136 x 500-1000: 7.8 / 10.9, 112 x 4096: 16.9 / 18.7, 152 x 1-4000: 15.9 / 15.4;
 //             76 x 1-2500: 11.1 / 9.7, 100 x 1-3000: 12.7 / 11.1, 136 x 1-8000: 25.8 / 22.3;
-//   8 warps   256 x 200-1000: 9.7 / 12.5, 304 x 2000-4000: 28.2 / 37.3; 256 x 1-4000: 26.8 / 23.8;
+//   8 warps   256 x 200-1000: 9.7 / 12.5, 304 x 1-2000: 16.0 / 18.5; 256 x 1-4000: 26.9 / 21.4,
+//             304 x 2000-4000: 27.7 / 30.4;
 //   4 warps   696 x 125-991: 16.3 / 18.6, 1024 x 1-2000: 36.7 / 39.4, 2048 x 1-2000: 60 / 71,
 //             64 x 128: 2.9 / 3.4 (16 warps 3.8); 512 x 1-8000: 82 / 63.
 struct Shape {
@@ -994,7 +995,8 @@ static Shape shape_of(long long units, long long tokens, int splits, int sms) {
     if (4 * units <= sms) return {8, 4};
     if (4 * units <= 3 * sms && tokens > 384 && units * tokens <= 1 << 17) return {4, 4};
   }
-  if (splits == 0 && tokens > (3 * units > 2 * sms ? 4096 : 384)) return {0, 0};
+  const int most = 3 * units <= 2 * sms ? 384 : units > sms && units <= 2 * sms ? 2048 : 4096;
+  if (splits == 0 && tokens > most) return {0, 0};
   return {1, tokens <= 384 || units > 2 * sms ? 4 : units > sms ? 8 : 16};
 }
 

@@ -255,6 +255,7 @@ PATHS = [  # (n_q, n_kv, bs, sequences, shortest, longest context)
     (8, 1, 16, 1, 98000, 98000), (8, 4, 32, 2, 30000, 40000),
     (32, 4, 16, 20, 20000, 46000), (10, 10, 32, 31, 20000, 21000), (8, 8, 16, 128, 1, 20000),
     (8, 8, 16, 24, 15000, 40000),
+    (4, 4, 16, 60, 1, 3500),
     # clusters of 16 CTAs of 16 warps, and few units through the workspace
     (8, 1, 16, 1, 20000, 20000), (4, 2, 32, 2, 1, 30000), (16, 4, 16, 1, 32768, 32768),
     (8, 1, 16, 1, 60000, 60000), (2, 2, 32, 2, 100, 90000), (6, 6, 16, 1, 9000, 9000),
