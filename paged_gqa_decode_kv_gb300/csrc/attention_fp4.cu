@@ -57,8 +57,9 @@ constexpr int kHeads = 8;              // query heads a product takes
 constexpr int kMergeRow = kHeadDim + 4;  // floats between heads when states are merged
 // Units of no more steps than this are not cut: a part's way through the workspace
 // takes longer than three steps of a warp (4 contexts of 217 tokens: 4.1 us whole,
-// 5.8 in two parts).
-constexpr int kWholeSteps = 12;
+// 5.8 in two parts; a step a warp of 16: 512 tokens of a wide table 5.4, 6.7 in two).
+template <int W>
+constexpr int kWholeSteps = W == 16 ? 16 : 12;
 // Steps a warp from which three CTAs follow one another: fewer where the units are so
 // many that one wave cannot be cut evenly (512 units of 1 to 8000 tokens: 60 us, from
 // 40 steps 87; but 256 of 8192: 64 and 58), and none up to a unit for every fourth
@@ -136,12 +137,13 @@ struct Part {
 // How units are cut: into parts of at most `size` steps (to a millionth: every
 // CTA computes the same, and never more than ceil(steps / size)), or into a given
 // number.
+template <int W>
 struct Cut {
   int splits;
   float inverse;  // of the size, and 2^-20 less
   __device__ __forceinline__ int parts(int steps) const {
     if (splits) return min(splits, steps);
-    if (steps <= kWholeSteps) return steps > 0 ? 1 : 0;
+    if (steps <= kWholeSteps<W>) return steps > 0 ? 1 : 0;
     return max(1, (int)ceilf((float)steps * inverse));
   }
 };
@@ -155,7 +157,7 @@ struct Cut {
 // tokens 114.3, with half of them fewer 116.5.
 constexpr int kSizes = 3;
 template <int W>
-__device__ __forceinline__ Cut choose_cut(const Attn4Params &p, int all, int k, int &limit) {
+__device__ __forceinline__ Cut<W> choose_cut(const Attn4Params &p, int all, int k, int &limit) {
   const float x = (float)all;
   const int units = p.a.B * p.a.n_kv;
   limit = p.resident;
@@ -199,7 +201,7 @@ __device__ __forceinline__ bool find_in_lanes(const Attn4Params &p, int BS, Part
   int mine, limit;
 #pragma unroll 1
   for (int k = 0; k < kSizes; ++k) {
-    const Cut cut = choose_cut<W>(p, all, k, limit);
+    const Cut<W> cut = choose_cut<W>(p, all, k, limit);
     mine = 0;
 #pragma unroll
     for (int i = 0; i < R; ++i) mine += n[i] = cut.parts(steps[i]);
@@ -257,7 +259,7 @@ __device__ __forceinline__ Part find_part(const Attn4Params &p, int BS) {
     int all = 0;
 #pragma unroll
     for (int i = 0; i < W; ++i) all += sums[0][i];
-    Cut cut;
+    Cut<W> cut;
     int at, end, limit;
 #pragma unroll 1
     for (int k = 0; k < kSizes; ++k) {
