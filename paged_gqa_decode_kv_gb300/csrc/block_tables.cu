@@ -396,8 +396,7 @@ __global__ void __launch_bounds__(kTrimThreads) trim_tables_kernel(const TrimPar
   __syncthreads();  // every thread has read the length
   if (threadIdx.x == 0) p.ctx[b] = keep;
   int32_t *row = p.tables + (size_t)b * p.MB;
-  const int j1 = (int)(((long long)len + p.bs - 1) / p.bs);
-  const int j0 = (int)(((long long)keep + p.bs - 1) / p.bs);
+  const int j0 = blocks_up(keep, p.bs, p.lg_bs), j1 = blocks_up(len, p.bs, p.lg_bs);
   if (j1 - j0 <= kFewBlocks) {
     const int j = j0 + threadIdx.x;
     if (j >= j1) return;
@@ -468,11 +467,14 @@ cudaError_t launch(void (*kernel)(P...), int grid, int threads, size_t smem, int
 
 }  // namespace
 
+// -1: no power of two.
+static int log2_of(int bs) { return (bs & (bs - 1)) ? -1 : __builtin_ctz((unsigned)bs); }
+
 cudaError_t grow_tables_launch(const GrowParams &p_in, cudaStream_t stream) {
   GrowParams p = p_in;
   const bool one = p.N <= kInlineTokens && p.NB <= kInlineBlocks;
   p.keep_lasts = one && p.B <= 8192 ? 1 : 0;
-  p.lg_bs = (p.bs & (p.bs - 1)) ? -1 : __builtin_ctz((unsigned)p.bs);
+  p.lg_bs = log2_of(p.bs);
   const size_t smem = ((size_t)p.B * (p.keep_lasts ? 4 : 3) + 2) * sizeof(int32_t);
   auto kernel = one ? grow_tables_kernel<512, 1> : grow_tables_kernel<kClusterThreads, kCluster>;
   if (!one) {
@@ -493,8 +495,10 @@ cudaError_t grow_tables_launch(const GrowParams &p_in, cudaStream_t stream) {
   return launch(place_tokens_kernel, (int)((p.N + per - 1) / per), kSlotThreads, 0, 1, stream, p);
 }
 
-cudaError_t trim_tables_launch(const TrimParams &p, cudaStream_t stream) {
+cudaError_t trim_tables_launch(const TrimParams &p_in, cudaStream_t stream) {
+  TrimParams p = p_in;
   if (p.B == 0) return cudaSuccess;
+  p.lg_bs = log2_of(p.bs);
   return launch(trim_tables_kernel, p.B, kTrimThreads, 0, 1, stream, p);
 }
 

@@ -33,6 +33,7 @@ struct TrimParams {
   int32_t *refs;        // [NB]
   uint32_t *free_bits;  // [(NB + 31) / 32]
   int B, bs, MB, NB;
+  int lg_bs;            // set by the launch
   int32_t *err;
 };
 cudaError_t trim_tables_launch(const TrimParams &p, cudaStream_t stream);

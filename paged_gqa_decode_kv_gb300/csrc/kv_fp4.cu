@@ -65,18 +65,20 @@ struct Group {
   size_t at;       // byte of the group in head 0's tile
 };
 
-__device__ __forceinline__ Group find_group(const Kv4Params &p, uint32_t groups, uint32_t run) {
+__device__ __forceinline__ Group find_group(const Kv4Params &p, uint32_t groups, uint32_t run,
+                                            uint32_t runs) {
   Group it;
   it.r0 = it.r1 = 0;
   const long long warp = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
   const bool lane0 = (threadIdx.x & 31) == 0;
-  const uint32_t items = 2 * (uint32_t)p.n_kv, runs = (items + run - 1) / run;
+  const uint32_t items = 2 * (uint32_t)p.n_kv;
   const uint32_t per_b = groups * runs;  // (the host bounds B * groups * items by 2^32)
   if (warp >= (long long)per_b * p.B) return it;
   const uint32_t id = (uint32_t)warp;
   const int b = (int)(id / per_b);
-  const uint32_t rest = id - (uint32_t)b * per_b, jrel = rest / runs;
+  const uint32_t rest = id - (uint32_t)b * per_b, jrel = groups == 1 ? 0 : rest / runs;
   const uint32_t r0 = (rest - jrel * runs) * run;
+  const int pos = __ldg(p.pos + b);  // (beside the starts)
   const TokenRange t = token_range(p.starts, b, p.T, p.N);
   const bool first = jrel == 0 && r0 == 0 && lane0;
   if (t.bad) {
@@ -84,14 +86,16 @@ __device__ __forceinline__ Group find_group(const Kv4Params &p, uint32_t groups,
     return it;
   }
   if (t.count == 0) return it;
-  const long long p0 = (long long)__ldg(p.pos + b) + p.pos_offset, p1 = p0 + t.count;
+  const long long p0 = (long long)pos + p.pos_offset, p1 = p0 + t.count;
   if (p0 < 0 || p1 > (long long)p.MB * p.bs) {
     if (first) atomicOr(p.err, PGD_DEVERR_BAD_POSITION);
     return it;
   }
   const long long base = (p0 / kGroupTokens4 + jrel) * kGroupTokens4;
   if (base >= p1) return it;
-  const int blk = __ldg(p.tables + (size_t)b * p.MB + base / p.bs);
+  // (blocks of 16 or 32)
+  const int lg_bs = p.bs == 32 ? 5 : 4, in_tile = p.bs / kGroupTokens4;
+  const int blk = __ldg(p.tables + (size_t)b * p.MB + (base >> lg_bs));
   if ((unsigned)blk >= (unsigned)p.NB) {
     if (r0 == 0 && lane0) atomicOr(p.err, PGD_DEVERR_BAD_BLOCK_ID);
     return it;
@@ -99,8 +103,8 @@ __device__ __forceinline__ Group find_group(const Kv4Params &p, uint32_t groups,
   it.t0 = (int)max(0ll, p0 - base);
   it.t1 = (int)min((long long)kGroupTokens4, p1 - base);
   it.row0 = t.row + (base + it.t0 - p0);
-  const int in_tile = p.bs / kGroupTokens4;
-  it.at = ((size_t)blk * p.n_kv * in_tile + (size_t)(base % p.bs) / kGroupTokens4) * kGroupBytes4;
+  it.at = ((size_t)blk * p.n_kv * in_tile + ((size_t)base & (p.bs - 1)) / kGroupTokens4) *
+          kGroupBytes4;
   it.r0 = (int)r0;
   it.r1 = (int)min(items, r0 + run);
   return it;
@@ -288,11 +292,11 @@ __device__ __forceinline__ void read_group(const Kv4Params &p, const Group &it, 
 
 template <bool WRITE>
 __global__ void __launch_bounds__(kWarps * 32, WRITE ? 6 : 8)
-    ranges_fp4_kernel(const Kv4Params p, uint32_t groups, uint32_t run) {
+    ranges_fp4_kernel(const Kv4Params p, uint32_t groups, uint32_t run, uint32_t runs) {
   __shared__ __align__(16) unsigned char smem[kWarps][kImage];
   pdl_wait();
   pdl_launch_dependents();
-  const Group it = find_group(p, groups, run);
+  const Group it = find_group(p, groups, run, runs);
 #pragma unroll 1
   for (int r = it.r0; r < it.r1; ++r) {
     if constexpr (WRITE)
@@ -311,7 +315,8 @@ cudaError_t launch(const Kv4Params &p, cudaStream_t stream) {
   // one item a warp for few, several of many, which share the chain of loads
   // that finds the group
   const uint32_t run = p.B * groups * items > 16384 ? kRun<WRITE> : 1;
-  const long long grid = (p.B * groups * ((items + run - 1) / run) + kWarps - 1) / kWarps;
+  const uint32_t runs = (items + run - 1) / run;
+  const long long grid = (p.B * groups * runs + kWarps - 1) / kWarps;
   if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
@@ -322,7 +327,7 @@ cudaError_t launch(const Kv4Params &p, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, ranges_fp4_kernel<WRITE>, p, (uint32_t)groups, run);
+  return cudaLaunchKernelEx(&cfg, ranges_fp4_kernel<WRITE>, p, (uint32_t)groups, run, runs);
 }
 
 }  // namespace

@@ -173,8 +173,9 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p, int 
     return;
   }
   // 16-byte vector v of slot s of a tile: core matrix (s / 8, v), row s % 8
-  const long long blk = slot / p.bs;
-  const int s = (int)(slot - blk * p.bs);
+  const int lg_bs = p.bs == 32 ? 5 : 4;  // (blocks of 16 or 32)
+  const long long blk = slot >> lg_bs;
+  const int s = (int)slot & (p.bs - 1);
   const long long tile = p.bs * 16LL, at = (s >> 3) * 128 + (s & 7);
   if (k0 < k1)
     rows<INTERLEAVED>(p, t, r, true,
