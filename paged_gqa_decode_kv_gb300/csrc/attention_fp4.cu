@@ -828,7 +828,7 @@ __global__ void __launch_bounds__(W * 32)
   __shared__ __align__(16) float2 in_ml[CL][kHeads];
   __shared__ __align__(8) uint64_t arrived;
   const AttnParams &a = p.a;
-  const int tid = threadIdx.x, rank = blockIdx.x % CL, unit = blockIdx.x / CL;
+  const int tid = threadIdx.x, rank = blockIdx.x % CL;
   if (CL > 1 && tid == 0) {
     mbar_init(&arrived, 1);
     mbar_init_fence();
@@ -839,8 +839,8 @@ __global__ void __launch_bounds__(W * 32)
   if (!a.wait_late) pdl_wait();
   pdl_launch_dependents();
   Part u;
-  u.b = unit / a.n_kv;
-  u.h = unit - u.b * a.n_kv;
+  u.b = blockIdx.y;
+  u.h = blockIdx.x / CL;
   u.steps = unit_steps(a, BS, u.b, u.ctx, rank == 0 && u.h == 0);
   u.i0 = u.steps * rank / CL;
   u.i1 = u.steps * (rank + 1) / CL;
@@ -944,7 +944,7 @@ cudaError_t launch_units_of(const Attn4Params &p, int G, cudaStream_t stream) {
     set[dev].store(true);
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(p.a.B * p.a.n_kv * CL));
+  cfg.gridDim = dim3((unsigned)(p.a.n_kv * CL), (unsigned)p.a.B);
   cfg.blockDim = dim3(W * 32);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
