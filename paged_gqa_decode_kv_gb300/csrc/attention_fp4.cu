@@ -985,7 +985,10 @@ cudaError_t launch_units(const Attn4Params &p, int G, int bs, cudaStream_t strea
 //   8 warps   256 x 200-1000: 9.7 / 12.5, 304 x 1-2000: 16.0 / 18.5; 256 x 1-4000: 26.9 / 21.4,
 //             304 x 2000-4000: 27.7 / 30.4;
 //   4 warps   696 x 125-991: 16.3 / 18.6, 1024 x 1-2000: 36.7 / 39.4, 2048 x 1-2000: 60 / 71,
-//             64 x 128: 2.9 / 3.4 (16 warps 3.8); 512 x 1-8000: 82 / 63.
+//             64 x 128: 2.9 / 3.4 (16 warps 3.8); 512 x 1-8000: 82 / 63;
+//   2 warps (or 4)  1024 x 100-300: 11.6 (12.4), 4096 x 1-64: 14.9 (22.1); 512 x 100-200:
+//             6.1 (5.8), 1024 x 100-600: 17.8 (16.7);
+//   1 warp (or 2)   4096 x 1-64: 11.8 (14.9), 1024 x 1-20: 3.9 (4.8); 1024 x 30-100: 6.9 (6.6).
 struct Shape {
   int ctas, warps;  // CTAs a unit, warps a CTA
 };
@@ -999,7 +1002,8 @@ static Shape shape_of(long long units, long long tokens, int splits, int sms) {
   }
   const int most = 3 * units <= 2 * sms ? 384 : units > sms && units <= 2 * sms ? 2048 : 4096;
   if (splits == 0 && tokens > most) return {0, 0};
-  return {1, tokens <= 384 || units > 2 * sms ? 4 : units > sms ? 8 : 16};
+  if (tokens <= 384) return {1, units <= 4 * sms ? 4 : tokens <= 64 ? 1 : 2};
+  return {1, units > 2 * sms ? 4 : units > sms ? 8 : 16};
 }
 
 // 4 warps a CTA, four CTAs an SM, or 16 and one: 16 for so few units that smaller
@@ -1036,6 +1040,8 @@ cudaError_t attention_fp4_launch(const Attn4Params &p_in, int G, int bs, int gri
     case 116: return launch_units<1, 16>(p, G, bs, stream);
     case 108: return launch_units<1, 8>(p, G, bs, stream);
     case 104: return launch_units<1, 4>(p, G, bs, stream);
+    case 102: return launch_units<1, 2>(p, G, bs, stream);
+    case 101: return launch_units<1, 1>(p, G, bs, stream);
   }
   const int W = warps_of(units);
   p.resident = (int)resident_ctas(W, sms);

@@ -245,7 +245,8 @@ PATHS = [  # (n_q, n_kv, bs, sequences, shortest, longest context)
     (8, 8, 16, 1, 1024, 1024), (20, 5, 16, 4, 129, 129),
     (3, 3, 32, 13, 385, 500), (48, 6, 16, 19, 1, 600), (8, 2, 32, 40, 1, 1500),
     # whole units of 4, 8 and 16 warps
-    (40, 10, 16, 4, 30, 384), (24, 6, 16, 20, 1, 380), (4, 2, 16, 700, 1, 90),
+    (40, 10, 16, 4, 30, 384), (24, 6, 16, 20, 1, 380), (4, 2, 16, 700, 1, 90), (32, 8, 32, 90, 1, 384),
+    (8, 8, 16, 80, 1, 30),
     (1, 1, 32, 2048, 1, 70), (8, 8, 32, 40, 1, 4000),
     (8, 8, 16, 30, 1, 2000), (16, 2, 32, 100, 1, 700), (4, 1, 16, 300, 1, 500),
     (16, 8, 16, 15, 1500, 2700), (19, 19, 32, 8, 2500, 2600),
