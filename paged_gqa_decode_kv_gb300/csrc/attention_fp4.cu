@@ -71,7 +71,7 @@ constexpr float kUnitLog2 = 7.f;       // a weight of the reference is 2^7
 
 // CTAs an SM: 16 warps with a ring each, as many as shared memory holds.
 template <int W>
-constexpr int kResident = W == 1 ? 15 : W == 2 ? 7 : 16 / W;
+constexpr int kResident = 16 / W;
 template <int W>
 constexpr int ring_bytes() {
   return W * kStages * kStepBytes;
