@@ -130,6 +130,9 @@ __global__ void __launch_bounds__(NT) grow_tables_kernel(const GrowParams p) {
   const bool first = rank == 0;
   const int words = (p.NB - 1) / 32 + 1;
   const int row_per = (p.B + NT - 1) / NT;  // rows a thread, side by side
+  // (every CTA of the cluster has started: waited for before the first store into
+  // another's shared memory)
+  if constexpr (C > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   pdl_wait();
   pdl_launch_dependents();
 
@@ -189,6 +192,7 @@ __global__ void __launch_bounds__(NT) grow_tables_kernel(const GrowParams p) {
   int free_blocks = total[2];
   if constexpr (C > 1) {
     // every CTA learns what the others counted; none changes anything before
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     cg::cluster_group cluster = cg::this_cluster();
     if (tid < C) *cluster.map_shared_rank(counts + rank, tid) = total[2];
     cluster.sync();
