@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(NT) grow_tables_kernel(const GrowParams p) {
         const int b = row_of(starts, p.B, n), len = lens[b] & 0x7fffffff;
         const int col = blocks_up(len, p.bs, p.lg_bs) - (lens[b] < 0 ? 1 : 0);
         pos = len + (n - starts[b]);
-        const int j = blocks_down(pos, p.bs, p.lg_bs), i = off[b] + j - col;
+        const int j = blocks_down(pos, p.bs, p.lg_bs), i = off[b] + (j - col);
         int id;
         if (j >= col && i < kIds)
           id = ids[i];
@@ -400,9 +400,11 @@ __global__ void __launch_bounds__(kTrimThreads) trim_tables_kernel(const TrimPar
   __syncthreads();  // every thread has read the length
   if (threadIdx.x == 0) p.ctx[b] = keep;
   int32_t *row = p.tables + (size_t)b * p.MB;
-  const int j0 = blocks_up(keep, p.bs, p.lg_bs), j1 = blocks_up(len, p.bs, p.lg_bs);
+  // (unsigned: a row may have 2^31 - 1 blocks, of one token, and a place behind the last wraps)
+  const uint32_t j0 = (uint32_t)blocks_up(keep, p.bs, p.lg_bs),
+                 j1 = (uint32_t)blocks_up(len, p.bs, p.lg_bs);
   if (j1 - j0 <= kFewBlocks) {
-    const int j = j0 + threadIdx.x;
+    const uint32_t j = j0 + threadIdx.x;
     if (j >= j1) return;
     const int id = row[j];
     row[j] = -1;
@@ -416,16 +418,16 @@ __global__ void __launch_bounds__(kTrimThreads) trim_tables_kernel(const TrimPar
     atomicOr(p.err, PGD_DEVERR_BAD_BLOCK_ID);
     return;
   }
-  for (int at = j0; at < j1; at += kTrimThreads * kTrimRun) {
+  for (uint32_t at = j0; at < j1; at += kTrimThreads * kTrimRun) {
     int id[kTrimRun], had[kTrimRun];
 #pragma unroll
     for (int i = 0; i < kTrimRun; ++i) {
-      const int j = at + i * kTrimThreads + threadIdx.x;
+      const uint32_t j = at + i * kTrimThreads + threadIdx.x;
       id[i] = j < j1 ? row[j] : 0;
     }
 #pragma unroll
     for (int i = 0; i < kTrimRun; ++i) {
-      const int j = at + i * kTrimThreads + threadIdx.x;
+      const uint32_t j = at + i * kTrimThreads + threadIdx.x;
       had[i] = 2;
       if (j >= j1) continue;
       row[j] = -1;
