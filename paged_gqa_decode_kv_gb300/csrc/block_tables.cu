@@ -43,7 +43,10 @@ constexpr int kWords = 4;     // of the pool's bits a thread looks at
 constexpr int kIds = 2048;   // new ids that it keeps in shared memory
 constexpr int kMost = 1 << 30;  // sums end here: more than any pool or call has
 
-__device__ __forceinline__ int capped(int a, int b) { return min(a + b, kMost); }  // a, b <= kMost
+// a, b from 0 to kMost (twice kMost is 2^31: added without a sign).
+__device__ __forceinline__ int capped(int a, int b) {
+  return (int)min((uint32_t)a + (uint32_t)b, (uint32_t)kMost);
+}
 
 // Inclusive sums of x over the CTA's NT threads, and the totals.
 template <int NT, int N>
@@ -183,7 +186,7 @@ __global__ void __launch_bounds__(NT) grow_tables_kernel(const GrowParams p) {
       p.copy_src[b] = src;
       p.copy_dst[b] = -1;
     }
-    x[0] = capped(x[0], need);
+    x[0] = capped(x[0], min(need, kMost));
     x[1] = capped(x[1], min(add, kMost));
   }
   const int mine[3] = {x[0], x[1], x[2]};

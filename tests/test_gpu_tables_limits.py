@@ -3,6 +3,7 @@ import pytest
 import torch
 
 import paged_gqa_decode_kv_gb300 as pgd
+from paged_gqa_decode_kv_gb300 import _native
 
 pytestmark = pytest.mark.gpu
 
@@ -44,3 +45,27 @@ def test_a_row_of_the_most_blocks(cut):
     assert ctx.tolist() == [MB - cut]
     assert not refs.any() and torch.equal(bits, all_free)
     assert int(tables.max()) == -1 == int(tables.min())
+
+
+@pytest.mark.parametrize("rows", [2, 3, 4, 31, 700])
+@pytest.mark.parametrize("N", [16, 9000])  # one CTA, a cluster
+@pytest.mark.parametrize("free", [True, False])
+def test_sums_of_new_tokens_past_32_bits(rows, N, free):
+    """Rows that each fit their table and together make 2^31 tokens and more: refused as too many, whether
+    blocks are there or not, and nothing changes."""
+    bs, NB = 2 ** 30, 1000
+    tables = torch.full((rows, 1), -1, dtype=torch.int32, device="cuda")
+    ctx = _i32([0] * rows)
+    refs, bits = pgd.make_block_pool(NB)
+    if not free:
+        refs.fill_(1)
+        bits.zero_()
+    before = [x.clone() for x in (tables, ctx, refs, bits)]
+    out = _outputs(rows, N)
+    pgd.grow_tables(tables, ctx, _i32([bs] * rows), refs, bits, bs, *out)
+    assert pgd.device_errors(clear=True) == _native.DEVERR_BAD_POSITION
+    assert out[6].tolist() == [2, 0, 0, 0]
+    for a, b in zip(before, (tables, ctx, refs, bits)):
+        assert torch.equal(a, b)
+    assert not out[0].any() and not out[1].any() and (out[2] == -1).all() and not out[3].any()
+    assert (out[4] == -1).all()
