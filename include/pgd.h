@@ -900,8 +900,11 @@ pgd_status pgd_read_stream(const void *src, size_t bytes, int32_t mode, void *st
  * (4e9 ns); pgd_set_wait_limit_ns sets it, process-wide, for the launches
  * made after the call (0 restores 4 s) -- a short limit makes the waits run
  * out on purpose, which is what a test of that exit path needs; nothing else
- * should change it.  Thread-safe; pgd_wait_limit_ns returns the value in
- * force.  No counterpart on the pages. */
+ * should change it.  It also limits the wait of the 4-bit attention's clusters
+ * for their other CTAs' states (below 1 us: what is not there at once is late;
+ * the CTA leaves when it has landed); the clusters of the block selection and
+ * of block-scaled short contexts keep 4 s.  Thread-safe; pgd_wait_limit_ns
+ * returns the value in force.  No counterpart on the pages. */
 void pgd_set_wait_limit_ns(uint64_t ns);
 uint64_t pgd_wait_limit_ns(void);
 

@@ -1859,7 +1859,7 @@ static pgd_status attention_fp4_call(void *out, const void *q, const void *k_new
   p.a.part_ml = reinterpret_cast<float *>(ws + L.part_ml);
   p.a.part_o = reinterpret_cast<float *>(ws + L.part_o);
   p.a.wait_late = append ? 1 : 0;  // the append writes only the cache
-  p.a.wait_limit_ns = g_wait_limit_ns.load();
+  p.a.wait_limit_ns = pgd_wait_limit_ns();
   p.v_scale = v_scale;
   p.splits = num_splits;
   if (append) {

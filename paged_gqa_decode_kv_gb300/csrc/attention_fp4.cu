@@ -874,11 +874,7 @@ __global__ void __launch_bounds__(W * 32)
             __float_as_uint(L));
   }
   if (tid >= G * kDims) return;
-  if (!wait_for_peers(&arrived, 0)) {
-    atomicOr(a.err, PGD_DEVERR_TIMEOUT);
-    wait_to_leave();
-    return;
-  }
+  if (!peers_in_time(&arrived, 0, a.wait_limit_ns)) return leave_late(&arrived, 0, a.err);
   for (int i = tid; i < G * kDims; i += 32 * W) {
     const int h = i / kDims, d = i % kDims;
     float M = in_ml[0][h].x;

@@ -34,10 +34,11 @@ __device__ __forceinline__ void send8(const void *local, const uint64_t *bar, ui
       : "memory");
 }
 
-// Wait for a phase of a barrier that peers' stores complete, at most
-// kWaitLimitNs (every CTA of the cluster sends before it waits, so the limit
-// is never met); the stores are visible behind it.
-__device__ __forceinline__ bool wait_for_peers(uint64_t *bar, uint32_t parity) {
+// Wait for a phase of a barrier that peers' stores complete, at most limit_ns
+// (every CTA of the cluster sends before it waits, so kWaitLimitNs is never
+// met); the stores are visible behind it.
+__device__ __forceinline__ bool wait_for_peers(uint64_t *bar, uint32_t parity,
+                                               uint64_t limit_ns = kWaitLimitNs) {
   uint64_t t0 = 0;
   for (uint32_t i = 0;; ++i) {
     uint32_t done;
@@ -52,7 +53,7 @@ __device__ __forceinline__ bool wait_for_peers(uint64_t *bar, uint32_t parity) {
     if ((i & 31u) == 0) {
       const uint64_t t = global_timer_ns();
       if (t0 == 0) t0 = t;
-      if (t - t0 > kWaitLimitNs) return false;
+      if (t - t0 > limit_ns) return false;
     }
   }
 }
@@ -61,6 +62,31 @@ __device__ __forceinline__ bool wait_for_peers(uint64_t *bar, uint32_t parity) {
 // left, so that no peer stores into the memory of a CTA that has gone.
 __device__ __forceinline__ void wait_to_leave() {
   asm volatile("barrier.cluster.arrive.relaxed;\n\tbarrier.cluster.wait;" ::: "memory");
+}
+
+// The wait with a launch's own limit.  Under one below 1 us (a test of the exit) what
+// is not there already is late: the first poll would suspend the thread for longer
+// than the peers' way here.
+__device__ __forceinline__ bool peers_in_time(uint64_t *bar, uint32_t parity, uint64_t limit_ns) {
+  if (limit_ns < 1000ull) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+    return done != 0;
+  }
+  return wait_for_peers(bar, parity, limit_ns);
+}
+
+// Behind a wait that gave up: the CTA leaves when what is on its way to it has
+// landed.
+static __device__ __noinline__ void leave_late(uint64_t *bar, uint32_t parity, int32_t *err) {
+  atomicOr(err, PGD_DEVERR_TIMEOUT);
+  if (!wait_for_peers(bar, parity)) wait_to_leave();
 }
 
 }  // namespace pgd
