@@ -1996,7 +1996,7 @@ static pgd_status rope_call(RopeParams &p, int32_t d, cudaStream_t stream) {
   }
   pgd_status s = error_word(&p.err);
   if (s != PGD_OK) return s;
-  const cudaError_t e = rope_launch(p, stream);
+  const cudaError_t e = rope_launch(p, sm_count(), stream);
   if (e != cudaSuccess) return cuda_fail(e, "rope launch");
   return ok();
 }

@@ -193,17 +193,17 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p, int 
 }
 
 template <bool APPEND, bool INTERLEAVED>
-cudaError_t launch(const RopeParams &p, cudaStream_t stream) {
+cudaError_t launch(const RopeParams &p, int sms, cudaStream_t stream) {
   const int cols = p.d >> 4, heads = p.n_q + (APPEND ? 2 : 1) * p.n_kv;
   const int y = std::max(1, std::min(kThreads / cols, p.T));
   const long long tiles = ((long long)p.T + y - 1) / y, threads = tiles * y * cols;
   // kManyHeads a thread where that makes four times the threads that are resident at
   // once, else as many threads as twice those (15 thousand tokens of 90 heads to rows:
   // 107 us, every thread all of them 112; 600 tokens of 72: 5.4 and, 16 a thread, 8.4)
-  const long long want = std::max(1LL, (152LL * 1024 + threads - 1) / threads);
+  const long long want = std::max(1LL, (sms * 1024LL + threads - 1) / threads);
   constexpr int kMany = kManyHeads<APPEND>;
   const int share =
-      threads * heads / kMany >= 152LL * 512 * 4 ? kMany : (int)((heads + want - 1) / want);
+      threads * heads / kMany >= sms * 512LL * 4 ? kMany : (int)((heads + want - 1) / want);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)tiles, (unsigned)((heads + share - 1) / share));
   cfg.blockDim = dim3((unsigned)cols, (unsigned)y);
@@ -218,11 +218,11 @@ cudaError_t launch(const RopeParams &p, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t rope_launch(const RopeParams &p, cudaStream_t stream) {
+cudaError_t rope_launch(const RopeParams &p, int sms, cudaStream_t stream) {
   if (p.T == 0) return cudaSuccess;
   if (p.k_cache)
-    return p.interleaved ? launch<true, true>(p, stream) : launch<true, false>(p, stream);
-  return p.interleaved ? launch<false, true>(p, stream) : launch<false, false>(p, stream);
+    return p.interleaved ? launch<true, true>(p, sms, stream) : launch<true, false>(p, sms, stream);
+  return p.interleaved ? launch<false, true>(p, sms, stream) : launch<false, false>(p, sms, stream);
 }
 
 }  // namespace pgd

@@ -19,6 +19,7 @@ struct RopeParams {
   float factor;                        // of cosine and sine
   int32_t *err;
 };
-cudaError_t rope_launch(const RopeParams &p, cudaStream_t stream);
+// sms: the device's.
+cudaError_t rope_launch(const RopeParams &p, int sms, cudaStream_t stream);
 
 }  // namespace pgd
