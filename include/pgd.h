@@ -685,7 +685,7 @@ pgd_status pgd_rope_append(void *q_out, const void *q, const void *k, const void
 /* ---------------------------------------------------------------------- */
 /* block tables grown and cut on the GPU                                   */
 /* ---------------------------------------------------------------------- */
-/* The host allocator's work (below) for a batch at once, on device state, so
+/* Work like the host allocator's (below) for a batch at once, on device state, so
  * that a captured step can grow its own tables ("Module 10", sections "Mapping
  * logical positions to physical blocks" and "Share only identical state"; "Ch.
  * 6", 6.4).  State, all device memory: block_tables int32 [B][MB], context_lens
@@ -700,7 +700,11 @@ pgd_status pgd_rope_append(void *q_out, const void *q, const void *k, const void
  * (copy_src[b], copy_dst[b]: the pair to copy before anything is written,
  * pgd_copy_blocks or pgd_copy_blocks_fp4 with n = B; -1, -1 where there is
  * none).  Rows that share such a block each take a copy, the last of them too;
- * a block that loses its last reference so is free for later calls.  Blocks are
+ * a block that loses its last reference so is free for later calls.  (All rows
+ * are asked before any reference falls.  pgd_alloc_append_slot asks at each
+ * row's turn, so that of n owners the last keeps the block: it makes n - 1
+ * copies where this makes n, and may find blocks enough where this is short of
+ * one.)  Blocks are
  * given out in the order of the rows, the lowest free ids first.  Outputs:
  *   positions[b]        the row's length before (int32 [B])
  *   context_lens[b]     its new length
@@ -709,7 +713,8 @@ pgd_status pgd_rope_append(void *q_out, const void *q, const void *k, const void
  *                       of new token n, rows in order; -1 and 0 from the last
  *                       new token to N
  *   result[0..3]        0 done, 1 too few free blocks, 2 more than N new
- *                       tokens; blocks taken; blocks that were missing; tokens
+ *                       tokens; blocks taken; blocks that were missing (sums
+ *                       end at 2^30); tokens
  * Where result[0] is not 0 nothing changes: token_starts are 0, slots -1,
  * copies -1, so that the step's appends write nothing.  (2 also sets
  * PGD_DEVERR_BAD_POSITION.)  A row with a negative length or count, or more than

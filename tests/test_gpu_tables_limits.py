@@ -69,3 +69,34 @@ def test_sums_of_new_tokens_past_32_bits(rows, N, free):
         assert torch.equal(a, b)
     assert not out[0].any() and not out[1].any() and (out[2] == -1).all() and not out[3].any()
     assert (out[4] == -1).all()
+
+
+@pytest.mark.parametrize("free", [2, 3])
+def test_the_last_owner_of_a_shared_block_copies_too(free):
+    """Three rows of one partly filled block, a token more each: the host allocator, which asks at each
+    row's turn, makes two copies; grow_tables makes three, or reports the block that it misses."""
+    bs, MB, NB = 16, 2, 1 + free
+    host = pgd.BlockAllocator(NB)
+    rows = [[-1] * MB for _ in range(3)]
+    for pos in range(5):
+        host.append_slot(rows[0], pos, bs)
+    for b in (1, 2):
+        host.fork(rows[0], 5, bs, rows[b])
+    shared = rows[0][0]
+    refs, bits = pgd.make_block_pool(NB)
+    tables = _i32([[0, -1]] * 3)
+    refs[0] = 3
+    bits[0] &= ~1
+    ctx, out = _i32([5] * 3), _outputs(3, 4)
+    before = [x.clone() for x in (tables, ctx, refs, bits)]
+    copies = [host.append_slot(row, 5, bs) for row in rows]
+    assert [src for src, _ in copies] == [shared, shared, -1] and host.num_free == free - 2
+    pgd.grow_tables(tables, ctx, _i32([1] * 3), refs, bits, bs, *out)
+    if free == 2:
+        assert out[6].tolist() == [1, 0, 1, 0]
+        for a, b in zip(before, (tables, ctx, refs, bits)):
+            assert torch.equal(a, b)
+    else:
+        assert out[6].tolist() == [0, 3, 0, 3] and out[4].tolist() == [0] * 3
+        assert out[5].tolist() == [1, 2, 3] and tables[:, 0].tolist() == [1, 2, 3]
+        assert refs.tolist() == [0, 1, 1, 1] and int(bits) == 1 and ctx.tolist() == [6] * 3
