@@ -971,7 +971,8 @@ cudaError_t launch_units(const Attn4Params &p, int G, int bs, cudaStream_t strea
 //            of 16 warps 1 x 16384: 7.6 / 9.9, 4 x 32768: 11.1 / 12.8, 6 x 16384: 7.2 / 9.3;
 //            8 x 16384: 13.8 / 9.6 (not all at once), 1 x 65536: 16.4 / 13.2;
 //   8 CTAs   1 x 512: 3.2 / 5.1, 32 x 1024: 5.2 / 6.8, 32 x 4096: 9.1 / 11.9,
-//            32 x 8192: 14.0 / 16.2; 32 x 256: 4.5 / 4.2; 64 x 2048: 10.8 / 9.0;
+//            32 x 8192: 14.0 / 16.2; 64 x 2048: 10.8 / 9.0; and where the rule takes the
+//            slower one, 32 x 256: 4.5 / 4.2;
 //   4 CTAs   100 x 1000: 6.3 / 9.4, 64 x 512: 4.6 / 5.8, 64 x 2048: 8.2 / 9.1;
 //            64 x 128: 3.8 / 3.4, 112 x 2300: 15.9 / 14.0, 136 x 1000: 11.9 / 10.9.
 // Where units are enough for the SMs, a CTA each takes less than parts of equal size

@@ -110,9 +110,11 @@ __device__ __forceinline__ Group find_group(const Kv4Params &p, uint32_t groups,
   return it;
 }
 
-// Two quotients to a multiple of 2^-12 (|x * inv| stays below 8 but where x is an
-// infinity or its scale has saturated), by paired instructions: issue slots are what
-// the write is short of.
+// Two quotients to a multiple of 2^-12, by paired instructions: issue slots are what
+// the write is short of.  |x * inv| stays below 9 but where x is an infinity or its
+// scale has saturated (a wanted scale just below 1.5 * 2^-9 becomes 2^-9, the smallest
+// there is), so that the sum lies in [2^11, 2^12), whose numbers are 2^-12 apart; past
+// it the code is 6 whatever the rounding.
 __device__ __forceinline__ float2 quotients(float2 x, float inv) {
   constexpr float kCut = 0x1.8p11f;
   asm("{\n\t.reg .b64 a, b, c;\n\t"
