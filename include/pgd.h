@@ -585,7 +585,8 @@ pgd_status pgd_append_decode_attention_fp8b(
  * pgd_paged_decode_attention_fp4, pgd_append_decode_attention_fp4: the calls of
  * those names over this cache -- same definition on the values that it stands
  * for, same arguments, checks and errors.  The append is pgd_kv_append_fp4 of
- * one token at context_lens[b] - 1.  The query must be finite.  B * n_kv at most
+ * one token at context_lens[b] - 1.  The query must be finite, and scores within
+ * fp32's range: 2^19 * scale * k_scale * max |q| below 2^127.  B * n_kv at most
  * 65536, B * n_kv * MB * bs below 2^35.  Arithmetic: q.k^T and p.v on f16
  * operands with fp32 accumulation -- K, V and the query exact (a query's element
  * to 2^-39 of its largest), a probability to 2^-11 of itself and 2^-32 of the

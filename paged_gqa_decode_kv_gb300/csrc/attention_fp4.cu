@@ -331,8 +331,8 @@ struct Worker {
 
   // Fragments and state.
   uint32_t qf[16];
-  float f0, f1;      // factors of the scores of heads 2 t4, 2 t4 + 1 (log2 domain)
-  float m0, m1;      // references (log2 domain)
+  float f0, f1;      // factors of the products of heads 2 t4, 2 t4 + 1 (scores in log2)
+  float m0, m1;      // references, as products
   float limit0, limit1;  // products at which they move
   float l0, l1;      // this lane's part of the sums
   float o[8][4];     // dims 16 i + g (+ 8) of those two heads
@@ -385,8 +385,9 @@ struct Worker {
       for (int j = 0; j < 4; ++j)
         qf[4 * i + j] = half2_bits(__floats2half2_rn(x[2 * j] * up, x[2 * j + 1] * up));
     }
-    // (never 0, which would make a masked score of minus infinity NaN)
-    const float back = fmaxf(p.a.qk_scale_log2 * pow2f(e - 14), 0x1p-126f);
+    // (never 0, which would make a masked score of minus infinity NaN, nor infinite,
+    // which would a distance of 0)
+    const float back = fminf(fmaxf(p.a.qk_scale_log2 * pow2f(e - 14), 0x1p-126f), 0x1p127f);
     f0 = __shfl_sync(kFullMask, back, 8 * t4);
     f1 = __shfl_sync(kFullMask, back, 8 * t4 + 4);
     m0 = m1 = limit0 = limit1 = __uint_as_float(0xff800000u);
@@ -514,12 +515,13 @@ struct Worker {
         x0 = fmaxf(x0, __shfl_xor_sync(kFullMask, x0, i));
         x1 = fmaxf(x1, __shfl_xor_sync(kFullMask, x1, i));
       }
-      const float n0 = fmaxf(m0, x0 * f0), n1 = fmaxf(m1, x1 * f1);
-      const float r0 = exp2_approx(m0 - n0), r1 = exp2_approx(m1 - n1);
+      const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);
+      const float r0 = exp2_approx((m0 - n0) * f0), r1 = exp2_approx((m1 - n1) * f1);
       m0 = n0;
       m1 = n1;
-      limit0 = __fdividef(m0 + kMoveLog2, f0);
-      limit1 = __fdividef(m1 + kMoveLog2, f1);
+      // (rounded down: no weight is above 2^15)
+      limit0 = __fadd_rd(m0, __fdividef(kMoveLog2, f0));
+      limit1 = __fadd_rd(m1, __fdividef(kMoveLog2, f1));
       l0 *= r0;
       l1 *= r1;
 #pragma unroll
@@ -530,13 +532,14 @@ struct Worker {
         o[i][3] *= r1;
       }
     }
-    const float b0 = kUnitLog2 - m0, b1 = kUnitLog2 - m1;
+    // The distance to the reference before the factor: the score of a large product
+    // less that of the reference would keep nothing but their roundings.
 #pragma unroll
     for (int sub = 0; sub < 2; ++sub) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const float w0 = exp2_approx(fmaf(s[sub][2 * i], f0, b0)),
-                    w1 = exp2_approx(fmaf(s[sub][2 * i + 1], f1, b1));
+        const float w0 = exp2_approx(fmaf(s[sub][2 * i] - m0, f0, kUnitLog2)),
+                    w1 = exp2_approx(fmaf(s[sub][2 * i + 1] - m1, f1, kUnitLog2));
         l0 += w0;
         l1 += w1;
         pf[sub][i] = transposed(half2_bits(__floats2half2_rn(w0, w1)));
@@ -652,9 +655,11 @@ __device__ __forceinline__ Sums<W> merge_warps(const Worker<BS, W> &w, float *re
     l1 += __shfl_xor_sync(kFullMask, l1, i);
   }
   const int mine_at = w.warp * kHeads + 2 * w.t4;
-  if (w.g == 0) *reinterpret_cast<float2 *>(refs + mine_at) = make_float2(w.m0, w.m1);
+  // (in log2 from here on)
+  const float m0 = w.m0 * w.f0, m1 = w.m1 * w.f1;
+  if (w.g == 0) *reinterpret_cast<float2 *>(refs + mine_at) = make_float2(m0, m1);
   __syncthreads();  // the rings are done with, the references written
-  float M0 = w.m0, M1 = w.m1;
+  float M0 = m0, M1 = m1;
 #pragma unroll
   for (int i = 0; i < W; ++i) {
     const float2 m = *reinterpret_cast<const float2 *>(refs + i * kHeads + 2 * w.t4);
@@ -662,8 +667,8 @@ __device__ __forceinline__ Sums<W> merge_warps(const Worker<BS, W> &w, float *re
     M1 = fmaxf(M1, m.y);
   }
   const float none = __uint_as_float(0xff800000u);  // (a warp without steps has no weight)
-  const float r0 = w.m0 == none ? 0.f : exp2_approx(w.m0 - M0);
-  const float r1 = w.m1 == none ? 0.f : exp2_approx(w.m1 - M1);
+  const float r0 = m0 == none ? 0.f : exp2_approx(m0 - M0);
+  const float r1 = m1 == none ? 0.f : exp2_approx(m1 - M1);
   if (w.g == 0) *reinterpret_cast<float2 *>(totals + mine_at) = make_float2(l0 * r0, l1 * r1);
   float *mine = reinterpret_cast<float *>(w.ring) + 2 * w.t4 * kMergeRow + w.g;
 #pragma unroll
